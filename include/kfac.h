@@ -409,6 +409,139 @@ kfac_status kfac_diag_factors_static(const void* a, int64_t lda, const void* g, 
                                      int in_dtype, double scale, float* g_new, float* a_new,
                                      cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators between the linear layers of a transformer block: what turns the
+ * projections' outputs into the next layer's input a, and the next layer's
+ * gradient into this layer's output gradient g.  They take no handle; the
+ * conventions at the top of this file hold (caller-owned device pointers, no
+ * device allocation, work enqueued on the given stream of the current device,
+ * argument errors returned before any launch).  Activations are 3-D per batch
+ * entry: [batch, length, heads, head_dim] addressed by three strides in
+ * elements (batch, row, head), the channels of a head contiguous, so that any
+ * order of the first three axes, packed q/k/v buffers and padded rows pass
+ * without a copy.  An input stride may be 0 (one tensor for every batch entry
+ * or head); an output's may not where its axis is longer than one.  A call
+ * without outputs (a size of 0) returns KFAC_OK and enqueues nothing; no keys
+ * (len_kv 0) or no queries is the empty sum. */
+
+typedef struct {
+  int dtype;                /* kfac_dtype of q, k and the outputs                */
+  int batch, length;        /* tokens: batch x length                            */
+  int heads, kv_heads;      /* of q and of k; either may be 0 (that tensor NULL) */
+  int head_dim;             /* <= 65536                                          */
+  int rotary_dim;           /* even, 2 <= rotary_dim <= head_dim                 */
+  int interleaved;          /* 0: pairs (i, i + rotary_dim/2); 1: (2i, 2i + 1)   */
+  int inverse;              /* 1: the transposed rotation (the backward pass)    */
+  int64_t table_rows;
+  int64_t position_offset;  /* position of row 0 when positions is NULL          */
+  int64_t position_stride;  /* elements of positions between batch entries       */
+  int64_t q_stride[3], k_stride[3], out_q_stride[3], out_k_stride[3];
+} kfac_rope_desc;
+
+/* Rotary positions: pair (x0, x1) of channel pair i of every head of q and k,
+ * at position t, becomes
+ *   (x0 c - x1 s, x0 s + x1 c),  c = table[t][i], s = table[t][rotary_dim/2 + i]
+ * (inverse: -s, the gradient with respect to the input for the same table);
+ * channels from rotary_dim on are copied.  table: fp32 [table_rows x
+ * rotary_dim], e.g. of kfac_rope_table.  positions: int32, the position of
+ * (b, row) at positions[b * position_stride + row] (stride 0: shared), or NULL
+ * for position_offset + row.  A position outside [0, table_rows) gives NaN in
+ * that token's rotated channels.  out_q may be q and out_k may be k with the
+ * same strides (in place); other overlaps are not allowed. */
+kfac_status kfac_rope(const kfac_rope_desc* desc, const void* q, const void* k,
+                      const float* table, const int* positions, void* out_q, void* out_k,
+                      cudaStream_t stream);
+
+/* How the angles of a rotary table are stretched over a longer context.  With
+ * f_i = base^(-2i/R), R = rotary_dim:
+ *   PLAIN  f_i
+ *   LINEAR f_i / factor (positions interpolated)
+ *   NTK    base replaced by base * factor^(R/(R-2))
+ *   YARN   f_i (1 - r_i) + (f_i / factor) r_i, r_i rising from 0 for pairs that
+ *          turn 32 times within original_length to 1 for those that turn once,
+ *          and table entries scaled by 0.1 ln(factor) + 1 */
+typedef enum {
+  KFAC_ROPE_PLAIN = 0,
+  KFAC_ROPE_LINEAR = 1,
+  KFAC_ROPE_NTK = 2,
+  KFAC_ROPE_YARN = 3
+} kfac_rope_scaling;
+
+/* table[t][i] = cos(t f_i), table[t][R/2 + i] = sin(t f_i) for t < rows, the
+ * angles in 64 bits.  base > 1; factor >= 1 (not read for PLAIN);
+ * original_length >= 1 (read for YARN). */
+kfac_status kfac_rope_table(float* table, int64_t rows, int rotary_dim, double base, int scaling,
+                            double factor, double original_length, cudaStream_t stream);
+
+/* Dropout with the residual added, from a counter-based generator:
+ *   out_i = residual_i + (u_i >= floor(p 2^32) ? x_i / (1 - p) : 0),
+ * i the row-major index of [rows x cols], u_i word i mod 4 of Philox4x32-10
+ * (Salmon et al., SC 2011) with counter words (i/4 low, i/4 high, offset low,
+ * offset high) and key words (seed low, seed high).  residual may be NULL
+ * (none).  The mask is a function of (seed, offset, i) alone and is never
+ * stored: the gradient with respect to x is the same call on the output
+ * gradient with the same p, seed and offset and no residual (the residual's
+ * gradient is the output gradient itself).  0 <= p <= 1; p = 1 drops
+ * everything.  A dropped x is not read into the result (Inf and NaN there do
+ * not reach out).  out may be x or residual. */
+kfac_status kfac_dropout(int dtype, const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                         void* out, int64_t ldo, int64_t rows, int64_t cols, double p,
+                         uint64_t seed, uint64_t offset, cudaStream_t stream);
+
+typedef struct {
+  int dtype;                 /* kfac_dtype of every tensor but lse               */
+  int batch, len_q, len_kv;  /* queries and keys per batch entry                 */
+  int heads, kv_heads;       /* kv_heads divides heads; query head h reads key
+                                head h / (heads / kv_heads)                      */
+  int head_dim;              /* 1..128                                           */
+  float scale;               /* of q k^T; 0: 1/sqrt(head_dim)                    */
+  int64_t q_stride[3], k_stride[3], v_stride[3], out_stride[3];
+} kfac_attention_desc;
+
+typedef struct {
+  int64_t dout_stride[3], dq_stride[3], dk_stride[3], dv_stride[3];
+} kfac_attention_grad_desc;
+
+/* Bytes of workspace that kfac_cross_attention (backward = 0) or it and
+ * kfac_cross_attention_backward (backward = 1) need on the current device for
+ * these sizes (a 256-byte multiple; may be 0).  The workspace holds nothing
+ * between calls; calls that share one must be ordered. */
+kfac_status kfac_cross_attention_workspace_size(const kfac_attention_desc* desc, int backward,
+                                                size_t* bytes);
+
+/* Attention of len_q queries to the len_kv states of an encoder:
+ *   S = scale q k^T over the permitted keys,  out = softmax(S) v,
+ *   lse = log sum exp S.
+ * A key j of batch entry b is permitted when j < kv_len[b] (kv_len NULL: all;
+ * values are clamped to [0, len_kv]) and key_mask[b * len_kv + j] != 0
+ * (key_mask NULL: all).  Whatever stands in the k and v of a key that is not
+ * permitted, Inf and NaN included, does not reach the outputs.  A query with
+ * no permitted key gives out = 0 and lse = -infinity.
+ * q [batch, len_q, heads, head_dim]; k, v [batch, len_kv, kv_heads, head_dim];
+ * out as q; lse: fp32 [batch, heads, len_q] contiguous (NULL: not wanted).
+ * Scores, softmax statistics and sums are fp32; bf16 inputs enter the tensor
+ * cores as they are and the probabilities as bf16 (fp32 inputs: fp32
+ * throughout).  workspace: 256-byte aligned, at least the size above. */
+kfac_status kfac_cross_attention(const kfac_attention_desc* desc, const void* q, const void* k,
+                                 const void* v, const int* kv_len, const uint8_t* key_mask,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/* Its gradients, from the forward call's out and lse and the output gradient:
+ *   P = exp(S - lse), delta = sum_d dout out, dP = dout v^T,
+ *   dv = P^T dout, dS = P (dP - delta), dq = scale dS k, dk = scale dS^T q,
+ * dk and dv summed over the query heads that share a key head.  Keys that are
+ * not permitted get zero gradients; a query without permitted keys gets and
+ * gives none.  dout as out, dq as q, dk as k, dv as v (written, not
+ * accumulated).  No atomics: the same inputs give the same bits. */
+kfac_status kfac_cross_attention_backward(const kfac_attention_desc* desc,
+                                          const kfac_attention_grad_desc* grads, const void* dout,
+                                          const void* q, const void* k, const void* v,
+                                          const void* out, const float* lse, const int* kv_len,
+                                          const uint8_t* key_mask, void* dq, void* dk, void* dv,
+                                          void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream);
+
 /* Diagnostics: number of kernels this library has launched in this process. */
 unsigned long long kfac_launch_count(void);
 

@@ -19,14 +19,32 @@ from ._lib import (LIB, KFAC_KRON, KFAC_DIAG, KFAC_F32, KFAC_BF16, KFAC_MATH_3XT
                    KFAC_MATH_BF16, KFAC_EMA_INIT_ZERO, KFAC_EMA_INIT_FIRST, KFAC_STATE_A,
                    KFAC_STATE_G, KFAC_STATE_AINV, KFAC_STATE_GINV, KFAC_STATE_MOMENTUM,
                    KFAC_STATE_GDIAG, KFAC_STATE_ADIAG, LayerDesc, HParams, Conv2dGeom, KfacError,
-                   status_string, launch_count)
+                   status_string, launch_count, KFAC_ROPE_PLAIN, KFAC_ROPE_LINEAR,
+                   KFAC_ROPE_NTK, KFAC_ROPE_YARN)
+
+# the operators of _block.py, loaded with torch at their first use: the rest of the package
+# imports without torch
+_BLOCK = ("rope", "rope_table", "dropout", "dropout_backward", "cross_attention",
+          "cross_attention_backward", "cross_attention_workspace")
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import _block
+        for n in _BLOCK:
+            globals()[n] = getattr(_block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 __all__ = ["Kfac", "diag_factors_static", "conv2d_geom", "LayerDesc", "HParams", "Conv2dGeom",
            "KfacError", "status_string", "launch_count",
            "KFAC_KRON", "KFAC_DIAG", "KFAC_F32", "KFAC_BF16", "KFAC_MATH_3XTF32",
            "KFAC_MATH_BF16", "KFAC_EMA_INIT_ZERO", "KFAC_EMA_INIT_FIRST", "KFAC_FACTOR_A",
            "KFAC_IKFAC_OFF", "KFAC_IKFAC_TF32", "KFAC_IKFAC_BF16",
-           "KFAC_FACTOR_G", "LIB"]
+           "KFAC_FACTOR_G", "LIB",
+           *_BLOCK,
+           "KFAC_ROPE_PLAIN", "KFAC_ROPE_LINEAR", "KFAC_ROPE_NTK", "KFAC_ROPE_YARN"]
 
 
 def _ptr(t) -> Optional[int]:

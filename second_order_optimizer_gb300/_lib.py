@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkfac.so")
@@ -20,6 +21,7 @@ KFAC_MATH_3XTF32, KFAC_MATH_BF16 = 0, 1
 KFAC_EMA_INIT_ZERO, KFAC_EMA_INIT_FIRST = 0, 1
 KFAC_IKFAC_OFF, KFAC_IKFAC_TF32, KFAC_IKFAC_BF16 = 0, 1, 2
 KFAC_FACTOR_A, KFAC_FACTOR_G = 1, 2
+KFAC_ROPE_PLAIN, KFAC_ROPE_LINEAR, KFAC_ROPE_NTK, KFAC_ROPE_YARN = range(4)
 (KFAC_STATE_A, KFAC_STATE_G, KFAC_STATE_AINV, KFAC_STATE_GINV, KFAC_STATE_MOMENTUM,
  KFAC_STATE_GDIAG, KFAC_STATE_ADIAG) = range(7)
 
@@ -58,6 +60,13 @@ class KfacError(RuntimeError):
 _vp, _i, _i64, _d, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
 _pLD, _pHP = ctypes.POINTER(LayerDesc), ctypes.POINTER(HParams)
 _pCG = ctypes.POINTER(Conv2dGeom)
+_u64 = ctypes.c_uint64
+# kfac_rope_desc, kfac_attention_desc and kfac_attention_grad_desc, packed with the
+# C compiler's alignment; a call passes the bytes where it takes the descriptor
+# (building a ctypes.Structure costs several times the rest of a small call)
+ROPE_DESC = struct.Struct("@9i15q")
+ATTENTION_DESC = struct.Struct("@7if12q")
+ATTENTION_GRAD_DESC = struct.Struct("@12q")
 
 # (name, restype, argtypes): one line per entry point of include/kfac.h
 SIGNATURES = [
@@ -90,6 +99,13 @@ SIGNATURES = [
     ("kfac_last_cuda_error", ctypes.c_char_p, []),
     ("kfac_diag_factors_static", _i, [_vp, _i64, _vp, _i64, _i64, _i, _i, _i, _i, _d, _vp, _vp,
                                       _vp]),
+    ("kfac_rope", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("kfac_rope_table", _i, [_vp, _i64, _i, _d, _i, _d, _d, _vp]),
+    ("kfac_dropout", _i, [_i, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _d, _u64, _u64, _vp]),
+    ("kfac_cross_attention_workspace_size", _i, [_vp, _i, ctypes.POINTER(_sz)]),
+    ("kfac_cross_attention", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_cross_attention_backward", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _sz, _vp]),
 ]
 
 for _name, _res, _args in SIGNATURES:

@@ -1,0 +1,45 @@
+// Shared by the cross-attention translation units.
+#pragma once
+#include "kfac_internal.cuh"
+
+namespace kfac {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// One call's tensors.  Strides are (batch, row, head) in elements.  rows = group *
+// len_q: the query rows that read one key head, query head (r / len_q) of the group
+// and query r % len_q for row r.
+struct Args {
+  const void *q, *k, *v, *o, *dout;
+  void *out, *dq, *dk, *dv;
+  float* lse;                       // forward: written when not null
+  const float* lse_in;              // backward
+  float* delta;                     // backward: [batch][heads][len_q]
+  const int* kv_len;
+  const uint8_t* key_mask;
+  int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
+  int batch, len_q, len_kv, heads, kv_heads, group, dim, rows;
+  float scale;
+  int splits;                       // parts of the key axis (1: outputs written directly)
+  float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised
+  float* part_lse;                  // [splits][batch][kv_heads][rows]
+};
+
+// Permitted keys of batch entry b end here.
+__device__ __forceinline__ int key_count(const Args& a, int b) {
+  return a.kv_len ? min(max(__ldg(a.kv_len + b), 0), a.len_kv) : a.len_kv;
+}
+__device__ __forceinline__ bool key_ok(const Args& a, int b, int len, int key) {
+  return key < len && (!a.key_mask || __ldg(a.key_mask + (int64_t)b * a.len_kv + key) != 0);
+}
+// Offset of packed row r of key head hk.
+__device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[3], int b, int hk,
+                                              int r) {
+  const int g = r / a.len_q, i = r - g * a.len_q;
+  return b * s[0] + i * s[1] + (int64_t)(hk * a.group + g) * s[2];
+}
+
+}  // namespace attn
+}  // namespace kfac

@@ -1,0 +1,660 @@
+// Cross attention: argument checks, the choice of kernels, and the kernels on the
+// CUDA cores (fp32 inputs, and bf16 ones whose rows the tensor-memory accelerator
+// cannot address).
+//
+//   S = scale q k^T,  P = softmax over the permitted keys,  out = P v
+//   dV = P^T dO,  dS = P (dO v^T - delta),  dQ = scale dS k,  dK = scale dS^T q,
+//   delta = sum_d dO out.
+// One pass over the keys with a running maximum m and sum l per row: a tile's
+// probabilities are exp(S - m), and what was summed so far is rescaled by
+// exp(m_old - m) when the maximum grows.
+//
+// Query heads that share a key head are packed into one row axis (heads of the
+// group x queries), so a tile of keys is loaded once for all of them.  Keys that
+// are not permitted enter shared memory as zeros and their scores as -infinity:
+// what stands there in memory never meets a product.
+#include "attn.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+namespace kfac {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 256;   // 16 x 16: rows x (keys or channels)
+constexpr int BK = 64;          // keys per tile
+constexpr int PP = BK + 4;      // pitch of a probability row (floats; 16-byte rows)
+
+template <int BQ, int DP> struct SimtCfg {
+  static constexpr int DPP = DP + 4;   // row pitch: float4 reads of 8 rows hit 32 banks
+  static constexpr int RT = BQ / 16;   // rows per thread
+  static constexpr int CV = DP / 64;   // float4 of channels per thread
+  static constexpr size_t FWD = sizeof(float) * (BQ * DPP + 2 * BK * DPP + BQ * PP) + 4 * BK;
+  static constexpr size_t BWD = sizeof(float) * (2 * BQ * DPP + 2 * BK * DPP + 2 * BQ * PP + 2 * BQ) + 4 * BK;
+};
+
+// rows x dim of global memory -> shared [n][DP + 4] fp32, zeros past dim and where
+// `ok` is false.
+template <typename T, int DP, typename Off>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int n, int dim, Off off) {
+  for (int e = threadIdx.x; e < n * DP; e += kThreads) {
+    const int r = e / DP, d = e % DP;
+    const int64_t o = off(r);
+    dst[r * (DP + 4) + d] = (o >= 0 && d < dim) ? to_f32<T>(src[o + d]) : 0.f;
+  }
+}
+
+__device__ __forceinline__ float half_max(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float half_sum(float v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// acc[i][j] = sum_d x[row i][d] y[key j][d], rows ty * RT + i, keys tx + 16 j
+template <int RT, int DP>
+__device__ __forceinline__ void dots(const float* x, const float* y, int ty, int tx,
+                                     float (&acc)[RT][4]) {
+  constexpr int DPP = DP + 4;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 xr[RT], yr[4];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) xr[i] = *reinterpret_cast<const float4*>(x + (ty * RT + i) * DPP + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) yr[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * DPP + d);
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fmaf(xr[i].x, yr[j].x, acc[i][j]);
+        acc[i][j] = fmaf(xr[i].y, yr[j].y, acc[i][j]);
+        acc[i][j] = fmaf(xr[i].z, yr[j].z, acc[i][j]);
+        acc[i][j] = fmaf(xr[i].w, yr[j].w, acc[i][j]);
+      }
+  }
+}
+
+// o[i][c] += sum_key p[row i][key] y[key][4 tx + 64 c ..]
+template <int RT, int CV, int DP>
+__device__ __forceinline__ void add_rows(const float* p, const float* y, int ty, int tx,
+                                         float4 (&o)[RT][CV]) {
+  constexpr int DPP = DP + 4;
+#pragma unroll 4
+  for (int k = 0; k < BK; k += 4) {
+    float4 pr[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(p + (ty * RT + i) * PP + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+      for (int c = 0; c < CV; ++c) {
+        const float4 yv = *reinterpret_cast<const float4*>(y + (k + kk) * DPP + 4 * tx + 64 * c);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
+          o[i][c].x = fmaf(w, yv.x, o[i][c].x);
+          o[i][c].y = fmaf(w, yv.y, o[i][c].y);
+          o[i][c].z = fmaf(w, yv.z, o[i][c].z);
+          o[i][c].w = fmaf(w, yv.w, o[i][c].w);
+        }
+      }
+  }
+}
+
+// o[i][c] += sum_row p[row][key ty * 4 + i] y[row][4 tx + 64 c ..]
+template <int BQ, int CV, int DP>
+__device__ __forceinline__ void add_cols(const float* p, const float* y, int ty, int tx,
+                                         float4 (&o)[4][CV]) {
+  constexpr int DPP = DP + 4;
+#pragma unroll 4
+  for (int r = 0; r < BQ; ++r) {
+    const float4 w = *reinterpret_cast<const float4*>(p + r * PP + ty * 4);
+#pragma unroll
+    for (int c = 0; c < CV; ++c) {
+      const float4 yv = *reinterpret_cast<const float4*>(y + r * DPP + 4 * tx + 64 * c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float wi = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+        o[i][c].x = fmaf(wi, yv.x, o[i][c].x);
+        o[i][c].y = fmaf(wi, yv.y, o[i][c].y);
+        o[i][c].z = fmaf(wi, yv.z, o[i][c].z);
+        o[i][c].w = fmaf(wi, yv.w, o[i][c].w);
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, int d, int dim, float4 v, float f) {
+  if (d < dim) dst[d] = (T)(v.x * f);
+  if (d + 1 < dim) dst[d + 1] = (T)(v.y * f);
+  if (d + 2 < dim) dst[d + 2] = (T)(v.z * f);
+  if (d + 3 < dim) dst[d + 3] = (T)(v.w * f);
+}
+
+// grid: (row tiles x splits, kv_heads, batch)
+template <typename T, int BQ, int DP>
+__global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_constant__ Args a) {
+  using C = SimtCfg<BQ, DP>;
+  constexpr int RT = C::RT, CV = C::CV, DPP = C::DPP;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + BQ * DPP;
+  float* Vs = Ks + BK * DPP;
+  float* Ps = Vs + BK * DPP;
+  int* oks = reinterpret_cast<int*>(Ps + BQ * PP);
+  pdl_wait();
+  pdl_trigger();
+  const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+  const int hk = blockIdx.y, b = blockIdx.z, r0 = tile * BQ;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int len = key_count(a, b);
+  const int tiles = (len + BK - 1) / BK;
+  const int t0 = (int)((int64_t)tiles * split / a.splits);
+  const int t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
+  load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, [&](int r) -> int64_t {
+    return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
+  });
+  float m[RT], l[RT];
+  float4 o[RT][CV];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < CV; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  const float c2 = a.scale * kLog2e;
+  for (int t = t0; t < t1; ++t) {
+    __syncthreads();
+    if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
+    __syncthreads();
+    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, [&](int r) -> int64_t {
+      return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
+    });
+    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, [&](int r) -> int64_t {
+      return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
+    });
+    __syncthreads();
+    float s[RT][4];
+    dots<RT, DP>(Qs, Ks, ty, tx, s);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = oks[tx + 16 * j] ? s[i][j] * c2 : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+      const float mn = fmaxf(m[i], half_max(top));
+      const float base = mn == -INFINITY ? 0.f : mn;   // nothing permitted so far
+      const float f = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        Ps[(ty * RT + i) * PP + tx + 16 * j] = p;
+      }
+      l[i] = l[i] * f + half_sum(sum);
+      m[i] = mn;
+#pragma unroll
+      for (int c = 0; c < CV; ++c) {
+        o[i][c].x *= f;
+        o[i][c].y *= f;
+        o[i][c].z *= f;
+        o[i][c].w *= f;
+      }
+    }
+    __syncwarp();   // a row's probabilities come from its own half warp
+    add_rows<RT, CV, DP>(Ps, Vs, ty, tx, o);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + ty * RT + i;
+    if (r >= a.rows) continue;
+    const float inv = l[i] > 0.f ? 1.f / l[i] : (l[i] == 0.f ? 0.f : l[i]);
+    const float lse = l[i] == 0.f ? -INFINITY : m[i] * kLn2 + logf(l[i]);
+    if (a.splits == 1) {
+      T* dst = static_cast<T*>(a.out) + row_offset(a, a.os, b, hk, r);
+#pragma unroll
+      for (int c = 0; c < CV; ++c) store4(dst, 4 * tx + 64 * c, a.dim, o[i][c], inv);
+      if (a.lse && tx == 0) a.lse[((int64_t)b * a.kv_heads + hk) * a.rows + r] = lse;
+    } else {
+      const int64_t at = (((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.rows + r;
+#pragma unroll
+      for (int c = 0; c < CV; ++c) store4(a.part_o + at * a.dim, 4 * tx + 64 * c, a.dim, o[i][c], inv);
+      if (tx == 0) a.part_lse[at] = lse;
+    }
+  }
+}
+
+// Joins the parts of the key axis: out = sum_s w_s o_s, w_s = exp(lse_s - lse).  One
+// warp per row.  [batch][kv_heads][rows] is [batch][heads][len_q], lse's layout.
+template <typename T>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n = (int64_t)a.batch * a.kv_heads * a.rows;
+  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= n) return;
+  const int r = (int)(row % a.rows), hk = (int)(row / a.rows % a.kv_heads);
+  const int b = (int)(row / a.rows / a.kv_heads);
+  float top = -INFINITY;
+  for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * n + row]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = top == -INFINITY ? 0.f : top;
+  float total = 0.f;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s = 0; s < a.splits; ++s) {
+    const float w = exp2f((a.part_lse[s * n + row] - base) * kLog2e);
+    total += w;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int d = lane + 32 * c;
+      if (d < a.dim) acc[c] = fmaf(w, a.part_o[(s * n + row) * a.dim + d], acc[c]);
+    }
+  }
+  const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+  T* dst = static_cast<T*>(a.out) + row_offset(a, a.os, b, hk, r);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    if (lane + 32 * c < a.dim) dst[lane + 32 * c] = (T)(acc[c] * inv);
+  if (a.lse && lane == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
+}
+
+// delta[b][h][i] = sum_d dout out, in fp32.  One warp per row.
+template <typename T>
+__global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
+  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= n) return;
+  const int i = (int)(row % a.len_q);
+  const int64_t bh = row / a.len_q;
+  const int h = (int)(bh % a.heads), b = (int)(bh / a.heads);
+  const T* o = static_cast<const T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
+  const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + i * a.dos[1] + h * a.dos[2];
+  float s = 0.f;
+  for (int d = lane; d < a.dim; d += 32) s = fmaf(to_f32<T>(o[d]), to_f32<T>(g[d]), s);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (lane == 0) a.delta[row] = s;
+}
+
+// P and dS of one tile (64 rows x 64 keys) into Ps (null: not wanted) and Ss.
+template <int DP>
+__device__ __forceinline__ void grad_tile(const float* Qs, const float* Os, const float* Ks,
+                                          const float* Vs, const float* lse2, const float* delta,
+                                          const int* oks, float c2, int ty, int tx, float* Ps,
+                                          float* Ss) {
+  float s[4][4], dp[4][4];
+  dots<4, DP>(Qs, Ks, ty, tx, s);
+  dots<4, DP>(Os, Vs, ty, tx, dp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty * 4 + i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool ok = oks[tx + 16 * j] != 0;
+      const float p = ok ? exp2f(fmaf(s[i][j], c2, -lse2[r])) : 0.f;
+      if (Ps) Ps[r * PP + tx + 16 * j] = p;
+      Ss[r * PP + tx + 16 * j] = ok ? p * (dp[i][j] - delta[r]) : 0.f;
+    }
+  }
+}
+
+// grid: (key tiles + row tiles, kv_heads, batch); the first a.splits = key tiles of x
+// produce dK and dV, the others dQ: no sums across blocks, so no atomics.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads) simt_backward_kernel(const __grid_constant__ Args a) {
+  using C = SimtCfg<64, DP>;
+  constexpr int CV = C::CV, DPP = C::DPP, BQ = 64;
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Os = Qs + BQ * DPP;
+  float* Ks = Os + BQ * DPP;
+  float* Vs = Ks + BK * DPP;
+  float* Ps = Vs + BK * DPP;
+  float* Ss = Ps + BQ * PP;
+  float* lse2 = Ss + BQ * PP;
+  float* delta = lse2 + BQ;
+  int* oks = reinterpret_cast<int*>(delta + BQ);
+  pdl_wait();
+  pdl_trigger();
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int len = key_count(a, b);
+  const int key_tiles = (a.len_kv + BK - 1) / BK;
+  const float c2 = a.scale * kLog2e;
+  const float* lse_row = a.lse_in + ((int64_t)b * a.kv_heads + hk) * a.rows;
+  const float* delta_row = a.delta + ((int64_t)b * a.kv_heads + hk) * a.rows;
+  auto load_keys = [&](int t) {
+    if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
+    __syncthreads();
+    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, [&](int r) -> int64_t {
+      return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
+    });
+    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, [&](int r) -> int64_t {
+      return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
+    });
+  };
+  auto load_rows = [&](int r0) {
+    load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, [&](int r) -> int64_t {
+      return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
+    });
+    load_tile<T, DP>(Os, static_cast<const T*>(a.dout), BQ, a.dim, [&](int r) -> int64_t {
+      return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
+    });
+    if (threadIdx.x < BQ) {
+      const int r = r0 + threadIdx.x;
+      // past the rows, or a row without keys: P = exp(S - inf) = 0
+      const float z = r < a.rows ? lse_row[r] * kLog2e : INFINITY;
+      lse2[threadIdx.x] = z == -INFINITY ? INFINITY : z;
+      delta[threadIdx.x] = r < a.rows ? delta_row[r] : 0.f;
+    }
+  };
+  if ((int)blockIdx.x < key_tiles) {   // ------------------------------ dK, dV
+    const int t = blockIdx.x;
+    float4 dk[4][CV], dv[4][CV];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < CV; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    load_keys(t);
+    if (t * BK < len)
+      for (int r0 = 0; r0 < a.rows; r0 += BQ) {
+        __syncthreads();
+        load_rows(r0);
+        __syncthreads();
+        grad_tile<DP>(Qs, Os, Ks, Vs, lse2, delta, oks, c2, ty, tx, Ps, Ss);
+        __syncthreads();
+        add_cols<BQ, CV, DP>(Ps, Os, ty, tx, dv);
+        add_cols<BQ, CV, DP>(Ss, Qs, ty, tx, dk);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int key = t * BK + ty * 4 + i;
+      if (key >= a.len_kv) continue;
+      T* pk = static_cast<T*>(a.dk) + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2];
+      T* pv = static_cast<T*>(a.dv) + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2];
+#pragma unroll
+      for (int c = 0; c < CV; ++c) {
+        store4(pk, 4 * tx + 64 * c, a.dim, dk[i][c], a.scale);
+        store4(pv, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
+      }
+    }
+    return;
+  }
+  // ---------------------------------------------------------------------- dQ
+  const int r0 = ((int)blockIdx.x - key_tiles) * BQ;
+  float4 dq[4][CV];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < CV; ++c) dq[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  load_rows(r0);
+  for (int t = 0; t * BK < len; ++t) {
+    __syncthreads();
+    load_keys(t);
+    __syncthreads();
+    grad_tile<DP>(Qs, Os, Ks, Vs, lse2, delta, oks, c2, ty, tx, nullptr, Ss);
+    __syncwarp();
+    add_rows<4, CV, DP>(Ss, Ks, ty, tx, dq);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty * 4 + i;
+    if (r >= a.rows) continue;
+    T* p = static_cast<T*>(a.dq) + row_offset(a, a.dqs, b, hk, r);
+#pragma unroll
+    for (int c = 0; c < CV; ++c) store4(p, 4 * tx + 64 * c, a.dim, dq[i][c], a.scale);
+  }
+}
+
+template <typename K>
+bool allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+         cudaSuccess;
+}
+
+template <typename T, int BQ, int DP>
+kfac_status launch_simt_forward(const Args& a, cudaStream_t st) {
+  using C = SimtCfg<BQ, DP>;
+  static const bool ok = allow_smem(simt_forward_kernel<T, BQ, DP>, C::FWD);
+  if (!ok) return KFAC_ERR_CUDA;
+  const dim3 grid((unsigned)(cdiv(a.rows, BQ) * a.splits), a.kv_heads, a.batch);
+  launch_pdl(simt_forward_kernel<T, BQ, DP>, grid, dim3(kThreads), C::FWD, st, a);
+  count_launch();
+  return check_launch();
+}
+
+template <typename T>
+kfac_status launch_combine(const Args& a, cudaStream_t st) {
+  const int64_t n = (int64_t)a.batch * a.kv_heads * a.rows;
+  launch_pdl(combine_kernel<T>, dim3((unsigned)cdiv(n, 4)), dim3(128), 0, st, a);
+  count_launch();
+  return check_launch();
+}
+
+template <typename T>
+kfac_status simt_forward(const Args& a, cudaStream_t st) {
+  kfac_status e;
+  if (a.rows <= 16)
+    e = a.dim <= 64 ? launch_simt_forward<T, 16, 64>(a, st) : launch_simt_forward<T, 16, 128>(a, st);
+  else
+    e = a.dim <= 64 ? launch_simt_forward<T, 64, 64>(a, st) : launch_simt_forward<T, 64, 128>(a, st);
+  if (e == KFAC_OK && a.splits > 1) e = launch_combine<T>(a, st);
+  return e;
+}
+
+template <typename T, int DP>
+kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
+  using C = SimtCfg<64, DP>;
+  static const bool ok = allow_smem(simt_backward_kernel<T, DP>, C::BWD);
+  if (!ok) return KFAC_ERR_CUDA;
+  const dim3 grid((unsigned)(cdiv(a.len_kv, BK) + cdiv(a.rows, 64)), a.kv_heads, a.batch);
+  launch_pdl(simt_backward_kernel<T, DP>, grid, dim3(kThreads), C::BWD, st, a);
+  count_launch();
+  return check_launch();
+}
+
+template <typename T>
+kfac_status simt_backward(const Args& a, cudaStream_t st) {
+  const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
+  if (n > 0) {
+    launch_pdl(delta_kernel<T>, dim3((unsigned)cdiv(n, 8)), dim3(256), 0, st, a);
+    count_launch();
+    if (kfac_status e = check_launch()) return e;
+  }
+  return a.dim <= 64 ? launch_simt_backward<T, 64>(a, st) : launch_simt_backward<T, 128>(a, st);
+}
+
+// Parts of the key axis for `ctas` blocks without a split: enough for two blocks per
+// SM, no part shorter than a tile of keys.
+int pick_splits(int64_t ctas, int len_kv) {
+  const int64_t want = cdiv(2 * num_sms(), std::max<int64_t>(ctas, 1));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, cdiv(len_kv, BK), 64}));
+}
+
+int forward_splits(const kfac_attention_desc& d) {
+  const int rows = d.heads / d.kv_heads * d.len_q;
+  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, d.len_kv);
+}
+
+bool valid_desc(const kfac_attention_desc* d) {
+  if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16)) return false;
+  if (d->batch < 0 || d->len_q < 0 || d->len_kv < 0 || d->heads < 1 || d->kv_heads < 1) return false;
+  if (d->heads % d->kv_heads || d->heads > 65535 || d->kv_heads > 65535 || d->batch > 65535)
+    return false;
+  if (d->head_dim < 1) return false;
+  if (!std::isfinite(d->scale) || d->scale < 0.f) return false;
+  // packed rows, tiles and rows of the statistics are counted in 32 bits
+  if ((int64_t)d->heads * std::max(d->len_q, 1) > (int64_t(1) << 30) || d->len_kv > (1 << 30))
+    return false;
+  if ((int64_t)d->batch * d->heads * d->len_q > (int64_t(1) << 31)) return false;
+  return true;
+}
+
+size_t part_bytes(const kfac_attention_desc& d, int splits) {
+  return splits > 1 ? align_up((size_t)splits * d.batch * d.heads * d.len_q * (d.head_dim + 1) *
+                               sizeof(float))
+                    : 0;
+}
+
+size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
+  const size_t fwd = part_bytes(d, forward_splits(d));
+  const size_t bwd = backward ? align_up((size_t)d.batch * d.heads * d.len_q * sizeof(float)) : 0;
+  return std::max(fwd, bwd);
+}
+
+struct Tensor {
+  const void* p;
+  const int64_t* s;
+  int64_t rows, heads;
+  bool output;
+};
+
+bool valid_tensor(const kfac_attention_desc& d, const Tensor& t) {
+  const size_t es = d.dtype == KFAC_BF16 ? 2 : 4;
+  const int64_t n[3] = {d.batch, t.rows, t.heads};
+  if (d.batch == 0 || t.rows == 0) return true;   // nothing there to read or write
+  if (!t.p || (uintptr_t)t.p % es) return false;
+  for (int i = 0; i < 3; ++i) {
+    if (t.s[i] < 0) return false;
+    // an output's rows may not overlap; an input's axis may be broadcast
+    if (t.output && n[i] > 1 && t.s[i] < d.head_dim) return false;
+  }
+  return true;
+}
+
+void fill(Args& a, const kfac_attention_desc& d) {
+  a.batch = d.batch;
+  a.len_q = d.len_q;
+  a.len_kv = d.len_kv;
+  a.heads = d.heads;
+  a.kv_heads = d.kv_heads;
+  a.group = d.heads / d.kv_heads;
+  a.dim = d.head_dim;
+  a.rows = a.group * d.len_q;
+  a.scale = d.scale > 0.f ? d.scale : (float)(1.0 / std::sqrt((double)d.head_dim));
+  for (int i = 0; i < 3; ++i) {
+    a.qs[i] = d.q_stride[i];
+    a.ks[i] = d.k_stride[i];
+    a.vs[i] = d.v_stride[i];
+    a.os[i] = d.out_stride[i];
+  }
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace kfac
+
+using namespace kfac;
+using namespace kfac::attn;
+
+extern "C" {
+
+kfac_status kfac_cross_attention_workspace_size(const kfac_attention_desc* d, int backward,
+                                                size_t* bytes) {
+  if (!valid_desc(d) || !bytes || (backward != 0 && backward != 1)) return KFAC_ERR_INVALID_ARG;
+  if (d->head_dim > 128) return KFAC_ERR_UNSUPPORTED;
+  *bytes = workspace_bytes_for(*d, backward != 0);
+  return KFAC_OK;
+}
+
+kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, const void* k,
+                                 const void* v, const int* kv_len, const uint8_t* key_mask,
+                                 void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                 cudaStream_t stream) {
+  if (!valid_desc(d)) return KFAC_ERR_INVALID_ARG;
+  if (d->head_dim > 128) return KFAC_ERR_UNSUPPORTED;
+  const Tensor ts[] = {{q, d->q_stride, d->len_q, d->heads, false},
+                       {k, d->k_stride, d->len_kv, d->kv_heads, false},
+                       {v, d->v_stride, d->len_kv, d->kv_heads, false},
+                       {out, d->out_stride, d->len_q, d->heads, true}};
+  for (const Tensor& t : ts)
+    if (!valid_tensor(*d, t)) return KFAC_ERR_INVALID_ARG;
+  if ((uintptr_t)kv_len % 4 || (uintptr_t)lse % 4) return KFAC_ERR_INVALID_ARG;
+  const size_t need = workspace_bytes_for(*d, false);
+  if (need && (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need))
+    return KFAC_ERR_WORKSPACE;
+  if (d->batch == 0 || d->len_q == 0) return KFAC_OK;
+  Args a{};
+  fill(a, *d);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.lse = lse;
+  a.kv_len = kv_len;
+  a.key_mask = key_mask;
+  a.splits = forward_splits(*d);
+  a.part_o = static_cast<float*>(workspace);
+  a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
+  return d->dtype == KFAC_BF16 ? simt_forward<__nv_bfloat16>(a, stream) : simt_forward<float>(a, stream);
+}
+
+kfac_status kfac_cross_attention_backward(const kfac_attention_desc* d,
+                                          const kfac_attention_grad_desc* g, const void* dout,
+                                          const void* q, const void* k, const void* v,
+                                          const void* out, const float* lse, const int* kv_len,
+                                          const uint8_t* key_mask, void* dq, void* dk, void* dv,
+                                          void* workspace, size_t workspace_bytes,
+                                          cudaStream_t stream) {
+  if (!valid_desc(d) || !g) return KFAC_ERR_INVALID_ARG;
+  if (d->head_dim > 128) return KFAC_ERR_UNSUPPORTED;
+  const Tensor ts[] = {{q, d->q_stride, d->len_q, d->heads, false},
+                       {k, d->k_stride, d->len_kv, d->kv_heads, false},
+                       {v, d->v_stride, d->len_kv, d->kv_heads, false},
+                       {out, d->out_stride, d->len_q, d->heads, false},
+                       {dout, g->dout_stride, d->len_q, d->heads, false},
+                       {dq, g->dq_stride, d->len_q, d->heads, true},
+                       {dk, g->dk_stride, d->len_kv, d->kv_heads, true},
+                       {dv, g->dv_stride, d->len_kv, d->kv_heads, true}};
+  for (const Tensor& t : ts)
+    if (!valid_tensor(*d, t)) return KFAC_ERR_INVALID_ARG;
+  if ((d->batch && d->len_q && !lse) || (uintptr_t)kv_len % 4 || (uintptr_t)lse % 4)
+    return KFAC_ERR_INVALID_ARG;
+  const size_t need = workspace_bytes_for(*d, true);
+  if (need && (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need))
+    return KFAC_ERR_WORKSPACE;
+  if (d->batch == 0 || (d->len_q == 0 && d->len_kv == 0)) return KFAC_OK;
+  Args a{};
+  fill(a, *d);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = out;
+  a.dout = dout;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.lse_in = lse;
+  a.kv_len = kv_len;
+  a.key_mask = key_mask;
+  a.delta = static_cast<float*>(workspace);
+  for (int i = 0; i < 3; ++i) {
+    a.dos[i] = g->dout_stride[i];
+    a.dqs[i] = g->dq_stride[i];
+    a.dks[i] = g->dk_stride[i];
+    a.dvs[i] = g->dv_stride[i];
+  }
+  return d->dtype == KFAC_BF16 ? simt_backward<__nv_bfloat16>(a, stream) : simt_backward<float>(a, stream);
+}
+
+}  // extern "C"

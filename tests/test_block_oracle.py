@@ -1,0 +1,218 @@
+"""CPU checks of the block operators: the float64 reference against what its definitions fix
+(known generator outputs, rotations, differences of the loss), and every refusal of the entry
+points that needs no GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from oracle import block_oracle as B
+
+
+# ------------------------------------------------------------------------------- the oracle
+
+def test_philox_known_answers():
+    """The published test vectors of Philox4x32-10 (zeros, ones, digits of pi)."""
+    f = 0xFFFFFFFF
+    cases = [((0, 0, 0, 0), (0, 0), (0x6627e8d5, 0xe169c58d, 0xbc57ac4c, 0x9b00dbd8)),
+             ((f, f, f, f), (f, f), (0x408f276d, 0x41c83b0e, 0xa20bc7c6, 0x6d5451fd)),
+             ((0x243f6a88, 0x85a308d3, 0x13198a2e, 0x03707344), (0xa4093822, 0x299f31d0),
+              (0xd16cfe09, 0x94fdcceb, 0x5001e420, 0x24126ea1))]
+    for ctr, key, want in cases:
+        assert tuple(B.philox4x32(ctr, key)) == want
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25, 1.0])
+def test_dropout_keeps_its_share_and_its_mean(p):
+    x = np.ones(20000)
+    y = B.dropout(x, p, 7, 3)
+    kept = (y != 0).mean()
+    assert abs(kept - (1 - p)) <= 4 * np.sqrt(0.25 / x.size)
+    if p < 1:
+        assert np.allclose(y[y != 0], 1 / (1 - p))
+    assert np.array_equal(B.dropout(x, p, 7, 3), y)
+    if 0 < p < 1:
+        assert not np.array_equal(B.dropout(x, p, 7, 4), y)
+        assert not np.array_equal(B.dropout(x, p, 8, 3), y)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rope_turns_pairs_and_its_inverse_turns_them_back(interleaved):
+    rng = np.random.default_rng(0)
+    x = rng.standard_normal((2, 5, 3, 12))
+    table = B.rope_table(40, 8)
+    pos = rng.integers(0, 40, (2, 5))
+    y = B.rope(x, table, pos, interleaved)
+    assert np.allclose(B.rope(y, table, pos, interleaved, inverse=True), x)
+    assert np.array_equal(y[..., 8:], x[..., 8:])
+    assert np.allclose((y ** 2).sum(-1), (x ** 2).sum(-1))
+    # scores depend on the distance of two positions alone
+    q, k = x[:1, :1, :1], x[:1, 1:2, :1]
+    at = lambda t: np.array([[t]])
+    dots = [(B.rope(q, table, at(a), interleaved) * B.rope(k, table, at(c), interleaved)).sum()
+            for a, c in ((3, 7), (30, 34))]
+    assert abs(dots[0] - dots[1]) <= 1e-12 * max(1, abs(dots[0]))
+
+
+def test_rope_scalings_at_their_limits():
+    plain, _ = B.rope_frequencies(64)
+    for scaling in ("linear", "ntk", "yarn"):
+        f, mag = B.rope_frequencies(64, scaling=scaling, factor=1.0, original_length=4096)
+        assert np.allclose(f, plain) and mag == 1.0
+    f, mag = B.rope_frequencies(64, scaling="ntk", factor=8.0)
+    assert np.isclose(f[0], plain[0]) and np.isclose(f[-1], plain[-1] / 8)
+    f, mag = B.rope_frequencies(64, scaling="yarn", factor=8.0, original_length=4096)
+    assert np.isclose(f[0], plain[0]) and np.isclose(f[-1], plain[-1] / 8) and mag > 1
+    assert np.all(np.diff(f) < 0)
+
+
+def test_attention_gradients_are_differences_of_the_loss():
+    rng = np.random.default_rng(1)
+    q, k, v = (rng.standard_normal(s) for s in ((2, 3, 4, 5), (2, 6, 2, 5), (2, 6, 2, 5)))
+    g = rng.standard_normal(q.shape)
+    ok = B.permitted(2, 6, kv_len=[4, 6], key_mask=rng.random((2, 6)) < 0.7)
+    ok[1, 0] = True
+    dq, dk, dv = B.cross_attention_backward(g, q, k, v, ok)
+    loss = lambda: (B.cross_attention(q, k, v, ok)[0] * g).sum()
+    for x, dx in ((q, dq), (k, dk), (v, dv)):
+        for _ in range(12):
+            i = tuple(rng.integers(0, n) for n in x.shape)
+            keep, h = x[i], 1e-5
+            x[i] = keep + h
+            up = loss()
+            x[i] = keep - h
+            down = loss()
+            x[i] = keep
+            # central difference: h^2 truncation and 1e-16 / h rounding, both about 1e-10
+            assert abs((up - down) / (2 * h) - dx[i]) <= 1e-8
+
+
+def test_attention_without_permitted_keys_is_zero():
+    q, k, v = np.ones((1, 2, 2, 4)), np.full((1, 3, 1, 4), np.nan), np.full((1, 3, 1, 4), np.inf)
+    ok = B.permitted(1, 3, kv_len=[0])
+    out, lse = B.cross_attention(q, k, v, ok)
+    assert (out == 0).all() and np.isneginf(lse).all()
+    assert all((t == 0).all() for t in B.cross_attention_backward(q, q, k, v, ok))
+
+
+# ------------------------------------------------------------- refusals (nothing is launched)
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build()
+    import second_order_optimizer_gb300._lib as L
+    return L
+
+
+A, W, U = 1, 2, 7   # KFAC_ERR_INVALID_ARG, KFAC_ERR_WORKSPACE, KFAC_ERR_UNSUPPORTED
+P = 0x10000         # an aligned address that is never read
+
+
+def _rope(lib, q=P, k=P, table=P, pos=None, oq=2 * P, ok=2 * P, **kw):
+    d = dict(dtype=1, batch=2, length=4, heads=2, kv_heads=1, head_dim=16, rotary_dim=8,
+             interleaved=0, inverse=0, table_rows=64, position_offset=0, position_stride=4,
+             qs=(128, 32, 16), ks=(64, 16, 16), oqs=(128, 32, 16), oks=(64, 16, 16))
+    d.update(kw)
+    s = [d.pop(n) for n in ("qs", "ks", "oqs", "oks")]
+    desc = lib.ROPE_DESC.pack(*d.values(), *(x for t in s for x in t))
+    return lib.LIB.kfac_rope(desc, q, k, table, pos, oq, ok, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(batch=-1), dict(head_dim=0), dict(rotary_dim=7), dict(rotary_dim=0),
+    dict(rotary_dim=18), dict(interleaved=2), dict(inverse=-1), dict(table_rows=0),
+    dict(position_offset=-1), dict(position_offset=61), dict(q=None), dict(ok=None), dict(k=P + 1),
+    dict(table=None), dict(table=P + 2), dict(pos=P + 2), dict(qs=(-1, 32, 16)),
+    dict(oqs=(128, 8, 16)),                       # output rows overlap
+    dict(oqs=(0, 32, 16)),                        # an output broadcast over the batch
+    dict(oq=P, oqs=(256, 32, 16))])               # in place with other strides
+def test_rope_refuses(lib, kw):
+    assert _rope(lib, **kw) == A
+
+
+def test_rope_table_refuses(lib):
+    f = lambda rows=4, r=8, base=1e4, scaling=0, factor=1.0, n=1.0, t=P: lib.LIB.kfac_rope_table(
+        t, rows, r, base, scaling, factor, n, None)
+    assert [f(t=None), f(rows=-1), f(r=3), f(r=0), f(base=1.0), f(base=float("nan")),
+            f(scaling=4), f(scaling=-1), f(scaling=1, factor=0.5),
+            f(scaling=3, factor=2.0, n=0.0), f(scaling=2, factor=2.0, r=2)] == [A] * 11
+    assert f(rows=0) == 0
+
+
+def test_dropout_refuses(lib):
+    f = lambda dt=0, x=P, ldx=8, r=None, ldr=8, o=P, ldo=8, rows=3, cols=8, p=0.5: (
+        lib.LIB.kfac_dropout(dt, x, ldx, r, ldr, o, ldo, rows, cols, p, 1, 0, None))
+    assert [f(dt=2), f(x=None), f(o=None), f(x=P + 2), f(r=P + 1), f(ldx=7), f(ldo=0),
+            f(r=P, ldr=4), f(rows=-1), f(cols=-1), f(p=-0.1), f(p=1.5), f(p=float("nan"))] == [A] * 13
+    assert f(rows=0) == 0 and f(cols=0, x=None) == 0
+
+
+def _desc(lib, **kw):
+    d = dict(dtype=1, batch=2, len_q=4, len_kv=6, heads=4, kv_heads=2, head_dim=16, scale=0.0,
+             qs=(256, 64, 16), ks=(192, 32, 16), vs=(192, 32, 16), os=(256, 64, 16))
+    d.update(kw)
+    s = [d.pop(n) for n in ("qs", "ks", "vs", "os")]
+    return lib.ATTENTION_DESC.pack(*d.values(), *(x for t in s for x in t))
+
+
+BAD_DESC = [dict(dtype=3), dict(batch=-1), dict(len_q=-1), dict(len_kv=-1), dict(heads=0),
+            dict(kv_heads=3), dict(kv_heads=0), dict(head_dim=0), dict(scale=-1.0),
+            dict(scale=float("nan")), dict(scale=float("inf"))]
+
+
+@pytest.mark.parametrize("kw", BAD_DESC)
+def test_attention_refuses_bad_descriptors(lib, kw):
+    n = ctypes.c_size_t(0)
+    d, g = _desc(lib, **kw), lib.ATTENTION_GRAD_DESC.pack(*([1024] * 12))
+    assert lib.LIB.kfac_cross_attention_workspace_size(d, 0, ctypes.byref(n)) == A
+    assert lib.LIB.kfac_cross_attention(d, P, P, P, None, None, P, P, P, 1 << 30, None) == A
+    assert lib.LIB.kfac_cross_attention_backward(d, g, P, P, P, P, P, P, None, None, P, P, P, P,
+                                                 1 << 30, None) == A
+
+
+def test_attention_refuses(lib):
+    fwd = lambda d=None, q=P, k=P, v=P, n=None, m=None, o=P, lse=P, ws=P, nb=1 << 30: (
+        lib.LIB.kfac_cross_attention(d or _desc(lib), q, k, v, n, m, o, lse, ws, nb, None))
+    assert [fwd(q=None), fwd(k=None), fwd(v=P + 1), fwd(o=None), fwd(n=P + 2), fwd(lse=P + 2),
+            fwd(_desc(lib, os=(256, 8, 16))), fwd(_desc(lib, os=(0, 64, 16))),
+            fwd(_desc(lib, ks=(192, -32, 16)))] == [A] * 9
+    assert fwd(_desc(lib, head_dim=129, qs=(4096, 1024, 256), os=(4096, 1024, 256))) == U
+    assert fwd(_desc(lib, batch=0)) == 0 and fwd(_desc(lib, len_q=0)) == 0
+    grads = lambda **kw: lib.ATTENTION_GRAD_DESC.pack(*(x for n, s in (
+        ("dout", (256, 64, 16)), ("dq", (256, 64, 16)), ("dk", (192, 32, 16)),
+        ("dv", (192, 32, 16))) for x in kw.get(n, s)))
+    bwd = lambda d=None, g=None, do=P, lse=P, dq=P, dk=P, dv=P, ws=P, nb=1 << 30: (
+        lib.LIB.kfac_cross_attention_backward(d or _desc(lib), g or grads(), do, P, P, P, P, lse,
+                                              None, None, dq, dk, dv, ws, nb, None))
+    assert [bwd(do=None), bwd(lse=None), bwd(lse=P + 1), bwd(dq=None), bwd(dk=P + 1),
+            bwd(dv=None), bwd(g=grads(dk=(0, 32, 16))), bwd(g=grads(dq=(256, 64, 8)))] == [A] * 8
+    assert lib.LIB.kfac_cross_attention_backward(_desc(lib), None, P, P, P, P, P, P, None, None,
+                                                 P, P, P, P, 1 << 30, None) == A
+    assert [bwd(ws=None), bwd(ws=P + 16), bwd(nb=16)] == [W] * 3
+
+
+def test_attention_workspace_is_what_the_backward_pass_needs(lib):
+    n = ctypes.c_size_t(0)
+    d = _desc(lib)
+    assert lib.LIB.kfac_cross_attention_workspace_size(d, 1, ctypes.byref(n)) == 0
+    assert n.value % 256 == 0 and n.value >= 2 * 4 * 4 * 4   # one fp32 statistic per query row
+    assert lib.LIB.kfac_cross_attention_workspace_size(d, 2, ctypes.byref(n)) == A
+    assert lib.LIB.kfac_cross_attention_workspace_size(d, 0, None) == A
+    assert lib.LIB.kfac_cross_attention_workspace_size(None, 0, ctypes.byref(n)) == A
+
+
+def test_python_refuses_cpu_tensors_and_wrong_types(lib):
+    torch = pytest.importorskip("torch")
+    import second_order_optimizer_gb300 as K
+    x = torch.zeros(2, 3, 4, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.rope(x, None, torch.zeros(3, 8))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        K.dropout(x.double(), 0.5, 1)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.dropout(x, 0.5, 1)
+    with pytest.raises(ValueError, match="64-bit"):
+        K.dropout(x, 0.5, -1)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.cross_attention(x, x, x)
