@@ -25,7 +25,7 @@ from ._lib import (LIB, KFAC_KRON, KFAC_DIAG, KFAC_F32, KFAC_BF16, KFAC_MATH_3XT
 # the operators of _block.py, loaded with torch at their first use: the rest of the package
 # imports without torch
 _BLOCK = ("rope", "rope_table", "dropout", "dropout_backward", "cross_attention",
-          "cross_attention_backward", "cross_attention_workspace")
+          "cross_attention_backward", "cross_attention_workspace", "operator_status")
 
 
 def __getattr__(name):

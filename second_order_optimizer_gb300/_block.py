@@ -315,3 +315,10 @@ def cross_attention_backward(dout, q, k, v, out, lse, kv_len=None, key_mask=None
             "kfac_cross_attention_backward")
     _used_on(stream, q.device, *made)
     return dq, dk, dv
+
+
+def operator_status():
+    """kfac_operator_status: synchronises; (code, info) of the first device error of these
+    operators since the last call (code 0: none)."""
+    info = ctypes.c_int(0)
+    return LIB.kfac_operator_status(ctypes.byref(info)), info.value

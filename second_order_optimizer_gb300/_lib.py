@@ -106,6 +106,7 @@ SIGNATURES = [
     ("kfac_cross_attention", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     ("kfac_cross_attention_backward", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_operator_status", _i, [ctypes.POINTER(_i)]),
 ]
 
 for _name, _res, _args in SIGNATURES:

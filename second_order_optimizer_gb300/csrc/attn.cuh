@@ -41,5 +41,9 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
   return b * s[0] + i * s[1] + (int64_t)(hk * a.group + g) * s[2];
 }
 
+// Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
+bool tc_forward_ok(const Args& a);
+kfac_status tc_forward(const Args& a, cudaStream_t st);
+
 }  // namespace attn
 }  // namespace kfac

@@ -484,16 +484,22 @@ kfac_status simt_backward(const Args& a, cudaStream_t st) {
   return a.dim <= 64 ? launch_simt_backward<T, 64>(a, st) : launch_simt_backward<T, 128>(a, st);
 }
 
-// Parts of the key axis for `ctas` blocks without a split: enough for two blocks per
-// SM, no part shorter than a tile of keys.
-int pick_splits(int64_t ctas, int len_kv) {
-  const int64_t want = cdiv(2 * num_sms(), std::max<int64_t>(ctas, 1));
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, cdiv(len_kv, BK), 64}));
+// Parts of the key axis for `ctas` blocks of the unsplit product: enough for `per_sm`
+// blocks per SM, no part shorter than a tile of `tile` keys.
+int pick_splits(int64_t ctas, int per_sm, int len_kv, int tile) {
+  const int64_t want = per_sm * num_sms() / std::max<int64_t>(ctas, 1);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, cdiv(len_kv, tile), 64}));
 }
 
-int forward_splits(const kfac_attention_desc& d) {
+int simt_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
-  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, d.len_kv);
+  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, 2, d.len_kv, BK);
+}
+int tc_splits(const kfac_attention_desc& d) {
+  return pick_splits((int64_t)cdiv(d.len_q, 256) * d.heads * d.batch, 1, d.len_kv, 128);
+}
+bool tc_sizes(const kfac_attention_desc& d) {
+  return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q > 16;
 }
 
 bool valid_desc(const kfac_attention_desc* d) {
@@ -517,7 +523,7 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 }
 
 size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
-  const size_t fwd = part_bytes(d, forward_splits(d));
+  const size_t fwd = part_bytes(d, std::max(simt_splits(d), tc_sizes(d) ? tc_splits(d) : 1));
   const size_t bwd = backward ? align_up((size_t)d.batch * d.heads * d.len_q * sizeof(float)) : 0;
   return std::max(fwd, bwd);
 }
@@ -603,9 +609,15 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
   a.lse = lse;
   a.kv_len = kv_len;
   a.key_mask = key_mask;
-  a.splits = forward_splits(*d);
+  const bool tc = tc_sizes(*d) && tc_forward_ok(a);
+  a.splits = tc ? tc_splits(*d) : simt_splits(*d);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
+  if (tc) {
+    kfac_status e = tc_forward(a, stream);
+    if (e == KFAC_OK && a.splits > 1) e = launch_combine<__nv_bfloat16>(a, stream);
+    return e;
+  }
   return d->dtype == KFAC_BF16 ? simt_forward<__nv_bfloat16>(a, stream) : simt_forward<float>(a, stream);
 }
 

@@ -44,6 +44,12 @@ def _close(got, ref, tol):
     assert (bad <= 0).all(), (np.unravel_index(bad.argmax(), bad.shape), bad.max())
 
 
+@pytest.fixture(autouse=True)
+def no_device_error():
+    yield
+    assert K.operator_status() == (0, 0)
+
+
 # --------------------------------------------------------------------------------------- rope
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
