@@ -44,6 +44,8 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
 bool tc_forward_ok(const Args& a);
 kfac_status tc_forward(const Args& a, cudaStream_t st);
+bool tc_backward_ok(const Args& a);
+kfac_status tc_backward(const Args& a, cudaStream_t st);   // a.delta already written
 
 }  // namespace attn
 }  // namespace kfac

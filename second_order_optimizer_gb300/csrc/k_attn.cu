@@ -474,13 +474,14 @@ kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
 }
 
 template <typename T>
-kfac_status simt_backward(const Args& a, cudaStream_t st) {
+kfac_status backward(const Args& a, cudaStream_t st) {
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
   if (n > 0) {
     launch_pdl(delta_kernel<T>, dim3((unsigned)cdiv(n, 8)), dim3(256), 0, st, a);
     count_launch();
     if (kfac_status e = check_launch()) return e;
   }
+  if (sizeof(T) == 2 && tc_backward_ok(a)) return tc_backward(a, st);
   return a.dim <= 64 ? launch_simt_backward<T, 64>(a, st) : launch_simt_backward<T, 128>(a, st);
 }
 
@@ -666,7 +667,7 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* d,
     a.dks[i] = g->dk_stride[i];
     a.dvs[i] = g->dv_stride[i];
   }
-  return d->dtype == KFAC_BF16 ? simt_backward<__nv_bfloat16>(a, stream) : simt_backward<float>(a, stream);
+  return d->dtype == KFAC_BF16 ? backward<__nv_bfloat16>(a, stream) : backward<float>(a, stream);
 }
 
 }  // extern "C"

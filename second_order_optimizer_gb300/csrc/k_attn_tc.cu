@@ -124,7 +124,7 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t half
 template <int NC> struct FwdCfg {
   static constexpr int TILE = NC * kChunk;
   static constexpr int STAGES = NC == 1 ? 3 : 2;
-  static constexpr size_t SMEM = 1024 + (size_t)(2 + 2 * STAGES) * TILE + 256;
+  static constexpr size_t SMEM = (size_t)(2 + 2 * STAGES) * TILE + 256;
 };
 constexpr float kGrow = 8.f;
 
@@ -135,8 +135,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
                   const MapMul xq, const MapMul xk, const MapMul xv) {
   using C = FwdCfg<NC>;
   constexpr int ST = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t smem[];   // the 128-byte swizzle's period
   uint8_t* Qs = smem;
   uint8_t* Ks = Qs + 2 * C::TILE;
   uint8_t* Vs = Ks + ST * C::TILE;
@@ -378,6 +377,431 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------------ backward
+//
+// One launch, two kinds of blocks, each recomputing S and dO V^T for its tiles: seven
+// products in all instead of the five that one pass would take, but every output has
+// one block that sums it in TMEM in a fixed order - no atomics, no fp32 dQ in memory,
+// and the query heads that share a key head are summed where they are produced.
+//
+// dK/dV block: 128 keys, all query tiles of the group's heads.  One TMEM lane per key:
+//   S^T = K Q^T, dP^T = V dO^T          (TMEM columns 0.., 128..)
+//   P^T = exp(S^T - lse) over S^T;      dV += P^T dO    (columns 256..)
+//   dS^T = P^T (dP^T - delta) over dP^T; dK += dS^T Q   (columns 256 + 64 NC..)
+// The issuing order dP(i), dV(i), S(i+1), dK(i) lets P(i+1) run under dK(i) and
+// dP(i+1), and dS(i) under dV(i) and S(i+1).
+//
+// dQ block: 128 queries of one head, all tiles of permitted keys.  One lane per query:
+//   S = Q K^T (two buffers, columns 0.. and 128..), dP = dO V^T (256..)
+//   dS = P (dP - delta) over dP; dQ += dS K (384..)
+// Issuing order S(j+1), dQ(j), dP(j+1).
+//
+// Two groups of four warps share a tile's columns, 64 each.
+template <int NC> struct BwdCfg {
+  static constexpr int TILE = NC * kChunk;
+  static constexpr int STATS = 2 * 2 * BT * 4;   // two stages of 128 lse and 128 delta
+  static constexpr size_t SMEM = (size_t)7 * TILE + STATS + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory of one block");
+};
+
+__device__ __forceinline__ void store_row(const uint32_t (&o)[32], __nv_bfloat16* dst, int c, int dim,
+                                          float f, bool zero) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    if (c + i < dim) {
+      uint32_t u[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        u[k] = zero ? 0u : pack_bf16(__uint_as_float(o[i + 2 * k]) * f, __uint_as_float(o[i + 2 * k + 1]) * f);
+      *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+}
+
+struct BwdMaps {
+  CUtensorMap q, k, v, g;
+  MapMul xq, xk, xv, xg;
+};
+
+template <int NC>
+__device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint8_t* smem,
+                                          uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
+  using C = BwdCfg<NC>;
+  uint8_t *Ks = smem, *Vs = Ks + C::TILE, *Qs = Vs + C::TILE, *Gs = Qs + 3 * C::TILE;
+  float* stats = reinterpret_cast<float*>(Gs + 2 * C::TILE);   // [2][lse 128, delta 128]
+  uint64_t *kv_full = bars, *q_full = bars + 1, *q_empty = bars + 4, *g_full = bars + 7,
+           *g_empty = bars + 9, *s_full = bars + 11, *dp_full = bars + 12, *p_ready = bars + 13,
+           *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int k0 = (int)blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
+  const int len = key_count(a, b);
+  const int qtiles = (a.len_q + BT - 1) / BT;
+  const int n = k0 < len ? a.group * qtiles : 0;
+  const int ksteps = (a.dim + 15) / 16;
+  auto give_up = [&](int info) {
+    *abort_flag = 1;
+    if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
+  };
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
+      tc::mbar_expect_tx(kv_full, 2 * C::TILE);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        tc::tma_load_4d(Ks + c * kChunk, &mp.k, kv_full, 64 * c, k0, hk * mp.xk.head, b * mp.xk.batch);
+        tc::tma_load_4d(Vs + c * kChunk, &mp.v, kv_full, 64 * c, k0, hk * mp.xv.head, b * mp.xv.batch);
+      }
+      int i = 0;
+      for (; i < n; ++i) {
+        const int h = hk * a.group + i / qtiles, row = i % qtiles * BT;
+        const int sq = i % 3, sg = i % 2;
+        if (!tc::mbar_wait(&q_empty[sq], ((uint32_t)(i / 3) & 1u) ^ 1u, abort_flag)) break;
+        load_chunks<NC>(Qs + sq * C::TILE, &mp.q, &q_full[sq], row, h * mp.xq.head, b * mp.xq.batch);
+        if (!tc::mbar_wait(&g_empty[sg], ((uint32_t)(i / 2) & 1u) ^ 1u, abort_flag)) break;
+        load_chunks<NC>(Gs + sg * C::TILE, &mp.g, &g_full[sg], row, h * mp.xg.head, b * mp.xg.batch);
+      }
+      if (i < n) {   // winding down: let the copies in flight land
+        give_up(111);
+        int never = 0;
+        for (int s = 0; s < 3; ++s) tc::mbar_wait(&q_full[s], (uint32_t)(i / 3) & 1u, &never, 1 << 20);
+        for (int s = 0; s < 2; ++s) tc::mbar_wait(&g_full[s], (uint32_t)(i / 2) & 1u, &never, 1 << 20);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {  // ------------------------------------------- MMA issuer
+      const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        if (!ok) give_up(112);
+        tc::tc_fence_after();
+        return ok;
+      };
+      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
+      if (ok) {
+        mma_scores(tmem, Ks, Qs, ksteps);
+        tc::umma_commit(s_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int sq = i % 3, sg = i % 2, s1 = (i + 1) % 3;
+        const uint32_t ph = (uint32_t)i & 1u;
+        if (!(ok = wait(&g_full[sg], (uint32_t)(i / 2) & 1u))) break;
+        mma_scores(tmem + 128, Vs, Gs + sg * C::TILE, ksteps);
+        tc::umma_commit(dp_full);
+        if (!(ok = wait(p_ready, ph))) break;
+        mma_values(tmem + 256, tmem, 64, Gs + sg * C::TILE, idesc, i > 0);
+        tc::umma_commit(&g_empty[sg]);
+        if (i + 1 < n) {
+          if (!(ok = wait(&q_full[s1], (uint32_t)((i + 1) / 3) & 1u))) break;
+          mma_scores(tmem, Ks, Qs + s1 * C::TILE, ksteps);
+          tc::umma_commit(s_full);
+        }
+        if (!(ok = wait(ds_ready, ph))) break;
+        mma_values(tmem + 256 + 64 * NC, tmem + 128, 64, Qs + sq * C::TILE, idesc, i > 0);
+        tc::umma_commit(&q_empty[sq]);
+      }
+      if (ok) tc::umma_commit(done);
+    }
+  } else if (warp == 2) {  // ---------------------------------------------- row statistics
+    for (int i = 0; i < n; ++i) {
+      const int h = hk * a.group + i / qtiles, row = i % qtiles * BT, s = i % 2;
+      if (!__all_sync(kFull, tc::mbar_wait(&st_empty[s], ((uint32_t)(i / 2) & 1u) ^ 1u, abort_flag))) {
+        give_up(113);
+        break;
+      }
+      const int64_t at = ((int64_t)b * a.heads + h) * a.len_q + row;
+      float* dst = stats + s * 2 * BT;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int r = 32 * c + lane;
+        const bool in = row + r < a.len_q;
+        // past the queries, or a query without keys: P = exp(S - inf) = 0
+        float z = in ? __ldg(a.lse_in + at + r) * kLog2e : INFINITY;
+        dst[r] = z == -INFINITY ? INFINITY : z;
+        dst[BT + r] = in ? a.delta[at + r] : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&st_full[s]);
+    }
+  } else if (warp >= 4) {  // ----------------------------------------------- P^T and dS^T
+    const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
+    const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
+    const uint32_t ts = tmem + lanes + 64 * half, td = ts + 128;
+    const int key = k0 + 32 * (warp % 4) + lane;
+    const bool mine = key_ok(a, b, len, key);
+    const float c2 = a.scale * kLog2e;
+    bool ok = true;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t ph = (uint32_t)i & 1u;
+      const int s = i % 2;
+      const float4* lse = reinterpret_cast<const float4*>(stats + s * 2 * BT + 64 * half);
+      const float4* delta = lse + BT / 4;
+      ok = __all_sync(kFull, tc::mbar_wait(&st_full[s], (uint32_t)(i / 2) & 1u, abort_flag) &&
+                                 tc::mbar_wait(s_full, ph, abort_flag));
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint32_t r[2][32];
+      tc::tmem_ld32_issue(ts, r[0]);
+      tc::tmem_ld32_issue(ts + 32, r[1]);
+      tc::tmem_ld_wait();
+      tc::tmem_ld_use(r[0]);
+      tc::tmem_ld_use(r[1]);
+      float p[64];
+      uint32_t u[32];
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 z = lse[c];
+        const float zz[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = ex2(fmaf(__uint_as_float(r[c / 8][c % 8 * 4 + e]), c2, -zz[e]));
+          p[4 * c + e] = mine ? x : 0.f;
+        }
+        u[2 * c] = pack_bf16(p[4 * c], p[4 * c + 1]);
+        u[2 * c + 1] = pack_bf16(p[4 * c + 2], p[4 * c + 3]);
+      }
+      tc::tmem_st32(ts, u);
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(p_ready);
+      ok = __all_sync(kFull, tc::mbar_wait(dp_full, ph, abort_flag));
+      if (!ok) break;
+      tc::tc_fence_after();
+      tc::tmem_ld32_issue(td, r[0]);
+      tc::tmem_ld32_issue(td + 32, r[1]);
+      tc::tmem_ld_wait();
+      tc::tmem_ld_use(r[0]);
+      tc::tmem_ld_use(r[1]);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) {
+        const float4 z = delta[c];
+        const float zz[4] = {z.x, z.y, z.z, z.w};
+        float d[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          d[e] = mine ? p[4 * c + e] * (__uint_as_float(r[c / 8][c % 8 * 4 + e]) - zz[e]) : 0.f;
+        u[2 * c] = pack_bf16(d[0], d[1]);
+        u[2 * c + 1] = pack_bf16(d[2], d[3]);
+      }
+      tc::tmem_st32(td, u);
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&st_empty[s]);
+        tc::mbar_arrive(ds_ready);
+      }
+    }
+    if (n > 0 && ok) ok = __all_sync(kFull, tc::mbar_wait(done, 0, abort_flag));
+    if (!ok) give_up(114);
+    tc::tc_fence_after();
+    // dV by the first group, dK by the second
+    const int64_t* st = half ? a.dks : a.dvs;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + b * st[0] + key * st[1] + hk * st[2];
+    const float f = !ok ? kNaN : half ? a.scale : 1.f;
+    for (int c = 0; c < a.dim; c += 32) {
+      uint32_t o[32];
+      if (n > 0) {
+        tc::tmem_ld32_issue(tmem + lanes + 256 + 64 * NC * half + c, o);
+        tc::tmem_ld_wait();
+        tc::tmem_ld_use(o);
+      }
+      if (key < a.len_kv) store_row(o, dst, c, a.dim, f, n == 0 || !mine);
+    }
+    tc::tc_fence_before();
+  }
+}
+
+template <int NC>
+__device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int tile, uint8_t* smem,
+                                         uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
+  using C = BwdCfg<NC>;
+  uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
+  uint64_t *qg_full = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7,
+           *v_empty = bars + 9, *dp_full = bars + 12, *ds_ready = bars + 14, *s_full = bars + 15,
+           *done = bars + 19;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int qtiles = (a.len_q + BT - 1) / BT;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int h = hk * a.group + tile / qtiles, q0 = tile % qtiles * BT;
+  const int len = key_count(a, b);
+  const int n = (len + BT - 1) / BT;
+  const int ksteps = (a.dim + 15) / 16;
+  auto give_up = [&](int info) {
+    *abort_flag = 1;
+    if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
+  };
+  if (warp == 0) {
+    if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
+      tc::mbar_expect_tx(qg_full, 2 * C::TILE);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        tc::tma_load_4d(Qs + c * kChunk, &mp.q, qg_full, 64 * c, q0, h * mp.xq.head, b * mp.xq.batch);
+        tc::tma_load_4d(Gs + c * kChunk, &mp.g, qg_full, 64 * c, q0, h * mp.xg.head, b * mp.xg.batch);
+      }
+      int j = 0;
+      for (; j < n; ++j) {
+        const int sk = j % 3, sv = j % 2;
+        if (!tc::mbar_wait(&k_empty[sk], ((uint32_t)(j / 3) & 1u) ^ 1u, abort_flag)) break;
+        load_chunks<NC>(Ks + sk * C::TILE, &mp.k, &k_full[sk], j * BT, hk * mp.xk.head, b * mp.xk.batch);
+        if (!tc::mbar_wait(&v_empty[sv], ((uint32_t)(j / 2) & 1u) ^ 1u, abort_flag)) break;
+        load_chunks<NC>(Vs + sv * C::TILE, &mp.v, &v_full[sv], j * BT, hk * mp.xv.head, b * mp.xv.batch);
+      }
+      if (j < n) {   // winding down: let the copies in flight land
+        give_up(121);
+        int never = 0;
+        for (int s = 0; s < 3; ++s) tc::mbar_wait(&k_full[s], (uint32_t)(j / 3) & 1u, &never, 1 << 20);
+        for (int s = 0; s < 2; ++s) tc::mbar_wait(&v_full[s], (uint32_t)(j / 2) & 1u, &never, 1 << 20);
+      }
+    }
+  } else if (warp == 1) {  // ----------------------------------------------- MMA issuer
+    const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
+      if (!ok) give_up(122);
+      tc::tc_fence_after();
+      return ok;
+    };
+    // S(j); keys that are not permitted become zero rows: dS = 0 there, and 0 x NaN
+    auto scores = [&](int j) {
+      const int s = j % 3;
+      if (!wait(&k_full[s], (uint32_t)(j / 3) & 1u)) return false;
+      uint32_t w[4];
+      key_words(a, b, len, j * BT, w);
+      if (!all_ok(w)) zero_rows<NC>(Ks + s * C::TILE, w);
+      if (lane == 0) {
+        mma_scores(tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
+        tc::umma_commit(&s_full[j % 2]);
+      }
+      return true;
+    };
+    auto grads = [&](int j) {
+      const int s = j % 2;
+      if (!wait(&v_full[s], (uint32_t)(j / 2) & 1u)) return false;
+      if (lane == 0) {
+        mma_scores(tmem + 256, Gs, Vs + s * C::TILE, ksteps);
+        tc::umma_commit(dp_full);
+        tc::umma_commit(&v_empty[s]);
+      }
+      return true;
+    };
+    bool ok = n > 0 && wait(qg_full, 0) && scores(0) && grads(0);
+    for (int j = 0; j < n && ok; ++j) {
+      if (j + 1 < n) ok = scores(j + 1);
+      ok = ok && wait(ds_ready, (uint32_t)j & 1u);
+      if (ok && lane == 0) {
+        mma_values(tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
+        tc::umma_commit(&k_empty[j % 3]);
+        if (j + 1 == n) tc::umma_commit(done);
+      }
+      __syncwarp();
+      if (ok && j + 1 < n) ok = grads(j + 1);
+    }
+  } else if (warp >= 4) {  // -------------------------------------------------------- dS
+    const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
+    const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
+    const uint32_t td = tmem + lanes + 256 + 64 * half;
+    const int q = q0 + 32 * (warp % 4) + lane;
+    const int64_t row = ((int64_t)b * a.heads + h) * a.len_q + q;
+    const bool in = q < a.len_q;
+    float lse = in ? __ldg(a.lse_in + row) * kLog2e : INFINITY;
+    if (lse == -INFINITY) lse = INFINITY;   // no permitted key: P = 0
+    const float delta = in ? a.delta[row] : 0.f;
+    const float c2 = a.scale * kLog2e;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      uint32_t w[4];
+      key_words(a, b, len, j * BT, w);
+      ok = __all_sync(kFull, tc::mbar_wait(&s_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag));
+      if (!ok) break;
+      tc::tc_fence_after();
+      const uint32_t ts = tmem + lanes + 128 * (j % 2) + 64 * half;
+      uint32_t r[2][32];
+      tc::tmem_ld32_issue(ts, r[0]);
+      tc::tmem_ld32_issue(ts + 32, r[1]);
+      tc::tmem_ld_wait();
+      tc::tmem_ld_use(r[0]);
+      tc::tmem_ld_use(r[1]);
+      float p[64];
+#pragma unroll
+      for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(r[c / 32][c % 32]), c2, -lse));
+      ok = __all_sync(kFull, tc::mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag));
+      if (!ok) break;
+      tc::tc_fence_after();
+      tc::tmem_ld32_issue(td, r[0]);
+      tc::tmem_ld32_issue(td + 32, r[1]);
+      tc::tmem_ld_wait();
+      tc::tmem_ld_use(r[0]);
+      tc::tmem_ld_use(r[1]);
+#pragma unroll
+      for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(r[c / 32][c % 32]) - delta;
+      if (!all_ok(w)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+          if (!((half ? w[2 + c / 32] : w[c / 32]) >> (c % 32) & 1u)) p[c] = 0.f;
+      }
+      uint32_t u[32];
+#pragma unroll
+      for (int c = 0; c < 32; ++c) u[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+      tc::tmem_st32(td, u);
+      tc::tmem_st_wait();
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(ds_ready);
+    }
+    if (n > 0 && ok) ok = __all_sync(kFull, tc::mbar_wait(done, 0, abort_flag));
+    if (!ok) give_up(124);
+    tc::tc_fence_after();
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + b * a.dqs[0] + q * a.dqs[1] + h * a.dqs[2];
+    for (int c = 32 * half; c < a.dim; c += 64) {   // the groups take 32 channels in turn
+      uint32_t o[32];
+      if (n > 0) {
+        tc::tmem_ld32_issue(tmem + lanes + 384 + c, o);
+        tc::tmem_ld_wait();
+        tc::tmem_ld_use(o);
+      }
+      if (in) store_row(o, dst, c, a.dim, ok ? a.scale : kNaN, n == 0);
+    }
+    tc::tc_fence_before();
+  }
+}
+
+// grid: (key tiles + group x query tiles, kv_heads, batch)
+template <int NC>
+__global__ void __launch_bounds__(kTcThreads, 1)
+tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMaps mp) {
+  using C = BwdCfg<NC>;
+  extern __shared__ __align__(1024) uint8_t smem[];   // the 128-byte swizzle's period
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE + C::STATS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x / 32;
+  const int key_tiles = (a.len_kv + BT - 1) / BT;
+  const bool dkv = (int)blockIdx.x < key_tiles;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 20; ++i) {
+      // 13: p_ready, 14: ds_ready (one arrival per warp of the two groups);
+      // 17, 18: the dK/dV role's st_empty (the same)
+      const bool warps = i == 13 || i == 14 || i == 17 || i == 18;
+      tc::mbar_init(&bars[i], warps ? 8 : 1);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  if (dkv) dkv_block<NC>(a, mp, smem, bars, abort_flag, tmem);
+  else dq_block<NC>(a, mp, (int)blockIdx.x - key_tiles, smem, bars, abort_flag, tmem);
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+}
+
 // ------------------------------------------------------------------------ tensor maps
 
 // [batch, rows, heads, dim] as a 4-D map (channels, rows, heads, batch), boxes of 128
@@ -426,6 +850,24 @@ kfac_status launch_tc_forward(const Args& a, cudaStream_t st) {
   return check_launch();
 }
 
+template <int NC>
+kfac_status launch_tc_backward(const Args& a, cudaStream_t st) {
+  using C = BwdCfg<NC>;
+  static const bool ok = cudaFuncSetAttribute(tc_backward_kernel<NC>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)C::SMEM) == cudaSuccess;
+  BwdMaps m;
+  if (!ok || !make_map(&m.q, &m.xq, a.q, a.qs, a.dim, a.len_q, a.heads, a.batch) ||
+      !make_map(&m.k, &m.xk, a.k, a.ks, a.dim, a.len_kv, a.kv_heads, a.batch) ||
+      !make_map(&m.v, &m.xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch) ||
+      !make_map(&m.g, &m.xg, a.dout, a.dos, a.dim, a.len_q, a.heads, a.batch))
+    return KFAC_ERR_CUDA;
+  const dim3 grid((unsigned)(cdiv(a.len_kv, BT) + a.group * cdiv(a.len_q, BT)), a.kv_heads, a.batch);
+  launch_pdl(tc_backward_kernel<NC>, grid, dim3(kTcThreads), C::SMEM, st, a, m);
+  count_launch();
+  return check_launch();
+}
+
 }  // namespace
 
 bool tc_forward_ok(const Args& a) {
@@ -437,6 +879,21 @@ bool tc_forward_ok(const Args& a) {
 
 kfac_status tc_forward(const Args& a, cudaStream_t st) {
   return a.dim <= 64 ? launch_tc_forward<1>(a, st) : launch_tc_forward<2>(a, st);
+}
+
+bool tc_backward_ok(const Args& a) {
+  return a.dim % 8 == 0 && a.len_q > 0 && a.len_kv > 0 &&
+         rows_ok(a.q, a.qs, a.len_q, a.heads, a.batch) &&
+         rows_ok(a.k, a.ks, a.len_kv, a.kv_heads, a.batch) &&
+         rows_ok(a.v, a.vs, a.len_kv, a.kv_heads, a.batch) &&
+         rows_ok(a.dout, a.dos, a.len_q, a.heads, a.batch) &&
+         rows_ok(a.dq, a.dqs, a.len_q, a.heads, a.batch) &&
+         rows_ok(a.dk, a.dks, a.len_kv, a.kv_heads, a.batch) &&
+         rows_ok(a.dv, a.dvs, a.len_kv, a.kv_heads, a.batch);
+}
+
+kfac_status tc_backward(const Args& a, cudaStream_t st) {
+  return a.dim <= 64 ? launch_tc_backward<1>(a, st) : launch_tc_backward<2>(a, st);
 }
 
 }  // namespace attn
