@@ -23,6 +23,7 @@ struct Args {
   int batch, len_q, len_kv, heads, kv_heads, group, dim, rows;
   float scale;
   int splits;                       // parts of the key axis (1: outputs written directly)
+  int part_keys;                    // token kernel: keys per part
   float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised
   float* part_lse;                  // [splits][batch][kv_heads][rows]
 };
@@ -40,6 +41,10 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
   const int g = r / a.len_q, i = r - g * a.len_q;
   return b * s[0] + i * s[1] + (int64_t)(hk * a.group + g) * s[2];
 }
+
+// Few query rows (bf16, rows that tc_forward_ok accepts).
+constexpr int kTokenWarps = 4;
+kfac_status token_forward(const Args& a, cudaStream_t st);
 
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
 bool tc_forward_ok(const Args& a);

@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ar
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   for (int s = 0; s < a.splits; ++s) {
     const float w = exp2f((a.part_lse[s * n + row] - base) * kLog2e);
+    if (w == 0.f) continue;   // an empty part, or one far below the others
     total += w;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -499,8 +500,24 @@ int simt_splits(const kfac_attention_desc& d) {
 int tc_splits(const kfac_attention_desc& d) {
   return pick_splits((int64_t)cdiv(d.len_q, 256) * d.heads * d.batch, 1, d.len_kv, 128);
 }
-bool tc_sizes(const kfac_attention_desc& d) {
-  return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q > 16;
+// The form of the forward pass for bf16 rows that TMA and 16-byte loads can address.
+// Few rows: the token kernel reads k and v once per 16 rows, while the tensor-core
+// kernel spends two tiles of 128 rows on them.
+constexpr int kTokenRows = 64;
+bool token_sizes(const kfac_attention_desc& d) {
+  return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q <= kTokenRows;
+}
+// Keys per part: about 8 blocks per SM over the full length (ragged lengths then
+// balance), at least one step of every warp.
+int token_part_keys(const kfac_attention_desc& d) {
+  const int64_t ctas = cdiv((int64_t)d.heads / d.kv_heads * d.len_q, 16) * d.kv_heads * d.batch;
+  const int64_t parts = std::max<int64_t>(1, 8 * num_sms() / std::max<int64_t>(ctas, 1));
+  const int step = 16 * kTokenWarps;
+  const int64_t keys = std::max<int64_t>(cdiv(d.len_kv, parts), cdiv(d.len_kv, 256));
+  return (int)std::max<int64_t>(step, cdiv(keys, step) * step);
+}
+int token_splits(const kfac_attention_desc& d) {
+  return (int)std::max<int64_t>(1, cdiv(d.len_kv, token_part_keys(d)));
 }
 
 bool valid_desc(const kfac_attention_desc* d) {
@@ -524,7 +541,9 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 }
 
 size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
-  const size_t fwd = part_bytes(d, std::max(simt_splits(d), tc_sizes(d) ? tc_splits(d) : 1));
+  int splits = simt_splits(d);   // whichever form the tensors' layouts allow
+  if (d.dtype == KFAC_BF16) splits = std::max(splits, token_sizes(d) ? token_splits(d) : tc_splits(d));
+  const size_t fwd = part_bytes(d, splits);
   const size_t bwd = backward ? align_up((size_t)d.batch * d.heads * d.len_q * sizeof(float)) : 0;
   return std::max(fwd, bwd);
 }
@@ -610,12 +629,13 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
   a.lse = lse;
   a.kv_len = kv_len;
   a.key_mask = key_mask;
-  const bool tc = tc_sizes(*d) && tc_forward_ok(a);
-  a.splits = tc ? tc_splits(*d) : simt_splits(*d);
+  const bool tc = d->dtype == KFAC_BF16 && tc_forward_ok(a), token = tc && token_sizes(*d);
+  a.splits = token ? token_splits(*d) : tc ? tc_splits(*d) : simt_splits(*d);
+  a.part_keys = token_part_keys(*d);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
   if (tc) {
-    kfac_status e = tc_forward(a, stream);
+    kfac_status e = token ? token_forward(a, stream) : tc_forward(a, stream);
     if (e == KFAC_OK && a.splits > 1) e = launch_combine<__nv_bfloat16>(a, stream);
     return e;
   }
