@@ -26,6 +26,9 @@ namespace {
 
 constexpr int kTcThreads = 384;
 constexpr int BT = 128;                    // rows of every tile
+// Registers per thread: 384 x 168 at launch; the score warps hold whole rows of S.
+constexpr int kRegsLaunch = 168, kRegsOther = 72, kRegsRow = 216;
+static_assert(128 * kRegsOther + 256 * kRegsRow <= kTcThreads * kRegsLaunch, "register shares");
 constexpr int kChunk = BT * 128;           // bytes of a 128-row, 64-channel chunk
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNaN = __builtin_nanf("");
@@ -46,15 +49,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&p);
 }
 
-// Bit i of w[c]: key key0 + 32 c + i is permitted.  Called by whole warps.
-__device__ __forceinline__ void key_words(const Args& a, int b, int len, int key0,
-                                          uint32_t (&w)[4]) {
-  const int lane = threadIdx.x % 32;
+// Bit i of w[c]: key key0 + 32 c + i is below len.
+__device__ __forceinline__ void len_words(int len, int key0, uint32_t (&w)[4]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int n = len - (key0 + 32 * c);
     w[c] = n >= 32 ? kFull : n <= 0 ? 0u : (1u << n) - 1u;
-    if (a.key_mask) w[c] &= __ballot_sync(kFull, key_ok(a, b, len, key0 + 32 * c + lane));
   }
 }
 __device__ __forceinline__ bool all_ok(const uint32_t (&w)[4]) {
@@ -62,23 +62,46 @@ __device__ __forceinline__ bool all_ok(const uint32_t (&w)[4]) {
 }
 
 // Rows of a [128 x 64 NC] tile whose key is not permitted become zero: 0 x Inf or NaN
-// in a product over keys would reach every row.  One warp; visible to the tensor
-// cores afterwards.
+// in a product over keys would reach every row.  One warp, one row per lane (starting
+// at different 16-byte columns: no bank is written twice at once); visible to the
+// tensor cores afterwards.
 template <int NC>
 __device__ __forceinline__ void zero_rows(uint8_t* tile, const uint32_t (&w)[4]) {
   const int lane = threadIdx.x % 32;
-  // lane = 16-byte column (8 per chunk row) x 4 rows at a time
-#pragma unroll 1
-  for (int r = lane / 8; r < BT; r += 4) {
-    if (w[r / 32] >> (r % 32) & 1u) continue;
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-      *reinterpret_cast<uint4*>(tile + c * kChunk + r * 128 + (lane % 8) * 16) = make_uint4(0, 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (!(w[i] >> lane & 1u)) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4*>(tile + c * kChunk + (32 * i + lane) * 128 + (k + lane) % 8 * 16) =
+              make_uint4(0, 0, 0, 0);
+    }
   tc::fence_proxy_async();
   __syncwarp();
 }
 
+// The same warp's walk over a block's key tiles: the words of tile `key0` (the mask's
+// bytes of the next tile are already on their way), published to the score warps.
+struct MaskWalk {
+  uint8_t next[4];
+  __device__ __forceinline__ void fetch(const Args& a, int b, int len, int key0) {
+    if (!a.key_mask) return;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int key = key0 + 32 * c + (int)(threadIdx.x % 32);
+      next[c] = key < len ? __ldg(a.key_mask + (int64_t)b * a.len_kv + key) : (uint8_t)0;
+    }
+  }
+  __device__ __forceinline__ void words(const Args& a, int len, int key0, uint32_t (&w)[4]) const {
+    len_words(len, key0, w);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (a.key_mask) w[c] &= __ballot_sync(kFull, next[c] != 0);
+    }
+  }
+};
 template <int NC>
 __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, uint64_t* bar,
                                             int row, int head, int batch) {
@@ -124,7 +147,7 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t half
 template <int NC> struct FwdCfg {
   static constexpr int TILE = NC * kChunk;
   static constexpr int STAGES = NC == 1 ? 3 : 2;
-  static constexpr size_t SMEM = (size_t)(2 + 2 * STAGES) * TILE + 256;
+  static constexpr size_t SMEM = (size_t)(2 + 2 * STAGES) * TILE + 512;
 };
 constexpr float kGrow = 8.f;
 
@@ -141,10 +164,11 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   uint8_t* Vs = Ks + ST * C::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(Vs + ST * C::TILE);
   uint64_t *q_full = bars, *k_full = q_full + 2, *k_empty = k_full + ST, *v_full = k_empty + ST,
-           *v_empty = v_full + ST, *s_full = v_empty + ST, *p_ready = s_full + 2,
-           *o_full = p_ready + 2;
+           *v_empty = v_full + ST, *v_ready = v_empty + ST, *w_full = v_ready + ST,
+           *s_full = w_full + ST, *p_ready = s_full + 2, *o_full = p_ready + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint4* words = reinterpret_cast<uint4*>(tmem_slot + 4);   // [ST] permitted keys of a tile
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
@@ -158,6 +182,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       tc::mbar_init(&k_empty[s], 1);
       tc::mbar_init(&v_full[s], 1);
       tc::mbar_init(&v_empty[s], 1);
+      tc::mbar_init(&v_ready[s], 1);
+      tc::mbar_init(&w_full[s], 1);
     }
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -187,6 +213,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
   };
 
+  if (warp < 4) {
+  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // -------------------------------------- TMA producer
       tc::tma_prefetch_desc(&mq);
@@ -233,12 +261,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     for (int j = 0; j < n && ok; ++j) {
       const int s = j % ST, s1 = (j + 1) % ST;
       for (int t = 0; t < nt && ok; ++t) {
-        if (t == 0) {
-          ok = wait(&v_full[s], (uint32_t)(j / ST) & 1u);
-          uint32_t w[4];
-          key_words(a, b, len, (t0 + j) * BT, w);
-          if (ok && !all_ok(w)) zero_rows<NC>(Vs + s * C::TILE, w);
-        }
+        if (t == 0) ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u);
         ok = ok && wait(&p_ready[t], (uint32_t)j & 1u);
         if (ok && lane == 0) {
           mma_values(tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
@@ -256,7 +279,33 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         __syncwarp();
       }
     }
-  } else if (warp >= 4 && (warp - 4) / 4 < nt) {  // -------------- softmax, epilogue
+  } else if (warp == 2) {  // ------------------------------------------- key mask
+    MaskWalk mask;
+    mask.fetch(a, b, len, t0 * BT);
+    for (int j = 0; j < n; ++j) {
+      const int s = j % ST, key0 = (t0 + j) * BT;
+      const uint32_t ph = (uint32_t)(j / ST) & 1u;
+      uint32_t w[4];
+      mask.words(a, len, key0, w);
+      mask.fetch(a, b, len, key0 + BT);
+      // the slot's last tile has been multiplied, so its words have been read
+      bool ok = tc::mbar_wait(&v_empty[s], ph ^ 1, abort_flag);
+      if (ok && lane == 0) {
+        words[s] = make_uint4(w[0], w[1], w[2], w[3]);
+        tc::mbar_arrive(&w_full[s]);
+      }
+      ok = __all_sync(kFull, ok && tc::mbar_wait(&v_full[s], ph, abort_flag));
+      if (!ok) {
+        give_up(104);
+        break;
+      }
+      if (!all_ok(w)) zero_rows<NC>(Vs + s * C::TILE, w);
+      if (lane == 0) tc::mbar_arrive(&v_ready[s]);
+    }
+  }
+  } else {
+  tc::regs_inc<kRegsRow>();
+  if ((warp - 4) / 4 < nt) {  // ---------------------------------- softmax, epilogue
     const int t = (warp - 4) / 4;
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
     const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 64 * NC * t + lanes;
@@ -264,11 +313,18 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n && ok; ++j) {
-      uint32_t w[4];
-      key_words(a, b, len, (t0 + j) * BT, w);
-      ok = __all_sync(kFull, tc::mbar_wait(&s_full[t], (uint32_t)j & 1u, abort_flag));
+      ok = __all_sync(kFull, tc::mbar_wait(&s_full[t], (uint32_t)j & 1u, abort_flag) &&
+                                 (!a.key_mask || tc::mbar_wait(&w_full[j % ST], (uint32_t)(j / ST) & 1u,
+                                                               abort_flag)));
       if (!ok) break;
       tc::tc_fence_after();
+      uint32_t w[4];
+      if (a.key_mask) {
+        const uint4 u = words[j % ST];
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      } else {
+        len_words(len, (t0 + j) * BT, w);
+      }
       uint32_t r[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::tmem_ld32_issue(ts + 32 * c, r[c]);
@@ -373,6 +429,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     }
     tc::tc_fence_before();
   }
+  }
   __syncthreads();
   if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
@@ -397,10 +454,11 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 // Issuing order S(j+1), dQ(j), dP(j+1).
 //
 // Two groups of four warps share a tile's columns, 64 each.
+constexpr int kBwdBars = 26;   // then the TMEM slot and abort flag, then the mask words
 template <int NC> struct BwdCfg {
   static constexpr int TILE = NC * kChunk;
   static constexpr int STATS = 2 * 2 * BT * 4;   // two stages of 128 lse and 128 delta
-  static constexpr size_t SMEM = (size_t)7 * TILE + STATS + 256;
+  static constexpr size_t SMEM = (size_t)7 * TILE + STATS + 512;
   static_assert(SMEM <= 227 * 1024, "shared memory of one block");
 };
 
@@ -441,6 +499,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
     *abort_flag = 1;
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
   };
+  if (warp < 4) {
+  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
       tc::mbar_expect_tx(kv_full, 2 * C::TILE);
@@ -520,7 +580,9 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&st_full[s]);
     }
-  } else if (warp >= 4) {  // ----------------------------------------------- P^T and dS^T
+  }
+  } else {  // ----------------------------------------------- P^T and dS^T
+    tc::regs_inc<kRegsRow>();
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
     const uint32_t ts = tmem + lanes + 64 * half, td = ts + 128;
@@ -617,7 +679,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
   uint64_t *qg_full = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7,
            *v_empty = bars + 9, *dp_full = bars + 12, *ds_ready = bars + 14, *s_full = bars + 15,
-           *done = bars + 19;
+           *done = bars + 19, *k_ready = bars + 20, *w_full = bars + 23;
+  uint4* words = reinterpret_cast<uint4*>(bars + 28);   // [3] permitted keys of a tile
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int hk = blockIdx.y, b = blockIdx.z;
@@ -629,6 +692,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     *abort_flag = 1;
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
   };
+  if (warp < 4) {
+  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
       tc::mbar_expect_tx(qg_full, 2 * C::TILE);
@@ -660,13 +725,9 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       tc::tc_fence_after();
       return ok;
     };
-    // S(j); keys that are not permitted become zero rows: dS = 0 there, and 0 x NaN
     auto scores = [&](int j) {
       const int s = j % 3;
-      if (!wait(&k_full[s], (uint32_t)(j / 3) & 1u)) return false;
-      uint32_t w[4];
-      key_words(a, b, len, j * BT, w);
-      if (!all_ok(w)) zero_rows<NC>(Ks + s * C::TILE, w);
+      if (!wait(&k_ready[s], (uint32_t)(j / 3) & 1u)) return false;
       if (lane == 0) {
         mma_scores(tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
         tc::umma_commit(&s_full[j % 2]);
@@ -695,7 +756,33 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       __syncwarp();
       if (ok && j + 1 < n) ok = grads(j + 1);
     }
-  } else if (warp >= 4) {  // -------------------------------------------------------- dS
+  } else if (warp == 2) {  // ----------------------------------------------- key mask
+    // K's rows of keys that are not permitted become zero: dS is 0 there, and 0 x NaN
+    // would reach dQ
+    MaskWalk mask;
+    mask.fetch(a, b, len, 0);
+    for (int j = 0; j < n; ++j) {
+      const int s = j % 3;
+      uint32_t w[4];
+      mask.words(a, len, j * BT, w);
+      mask.fetch(a, b, len, j * BT + BT);
+      // the slot's last tile has been multiplied, so its words have been read
+      bool ok = tc::mbar_wait(&k_empty[s], ((uint32_t)(j / 3) & 1u) ^ 1u, abort_flag);
+      if (ok && lane == 0) {
+        words[s] = make_uint4(w[0], w[1], w[2], w[3]);
+        tc::mbar_arrive(&w_full[s]);
+      }
+      ok = __all_sync(kFull, ok && tc::mbar_wait(&k_full[s], (uint32_t)(j / 3) & 1u, abort_flag));
+      if (!ok) {
+        give_up(123);
+        break;
+      }
+      if (!all_ok(w)) zero_rows<NC>(Ks + s * C::TILE, w);
+      if (lane == 0) tc::mbar_arrive(&k_ready[s]);
+    }
+  }
+  } else {  // -------------------------------------------------------- dS
+    tc::regs_inc<kRegsRow>();
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
     const uint32_t td = tmem + lanes + 256 + 64 * half;
@@ -708,11 +795,18 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     const float c2 = a.scale * kLog2e;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      uint32_t w[4];
-      key_words(a, b, len, j * BT, w);
-      ok = __all_sync(kFull, tc::mbar_wait(&s_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag));
+      ok = __all_sync(kFull, tc::mbar_wait(&s_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag) &&
+                                 (!a.key_mask || tc::mbar_wait(&w_full[j % 3], (uint32_t)(j / 3) & 1u,
+                                                               abort_flag)));
       if (!ok) break;
       tc::tc_fence_after();
+      uint32_t w[4];
+      if (a.key_mask) {
+        const uint4 u = words[j % 3];
+        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+      } else {
+        len_words(len, j * BT, w);
+      }
       const uint32_t ts = tmem + lanes + 128 * (j % 2) + 64 * half;
       uint32_t r[2][32];
       tc::tmem_ld32_issue(ts, r[0]);
@@ -771,13 +865,13 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   using C = BwdCfg<NC>;
   extern __shared__ __align__(1024) uint8_t smem[];   // the 128-byte swizzle's period
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE + C::STATS);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 20);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBwdBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x / 32;
   const int key_tiles = (a.len_kv + BT - 1) / BT;
   const bool dkv = (int)blockIdx.x < key_tiles;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 20; ++i) {
+    for (int i = 0; i < kBwdBars; ++i) {
       // 13: p_ready, 14: ds_ready (one arrival per warp of the two groups);
       // 17, 18: the dK/dV role's st_empty (the same)
       const bool warps = i == 13 || i == 14 || i == 17 || i == 18;
