@@ -115,23 +115,22 @@ __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, 
 __device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* a, const uint8_t* b,
                                            int ksteps) {
   constexpr uint32_t idesc = tc::make_idesc(1, 128, 128);
-  const uint32_t sa = tc::smem_u32(a), sb = tc::smem_u32(b);
-#pragma unroll 1
-  for (int kk = 0; kk < ksteps; ++kk) {
-    const uint32_t off = (uint32_t)(kk / 4 * kChunk + kk % 4 * 32);
-    tc::umma_f16(d, tc::sdesc_kmajor_sw128(sa + off), tc::sdesc_kmajor_sw128(sb + off), idesc,
-                 kk > 0);
+  const uint64_t da = tc::sdesc_kmajor_sw128(tc::smem_u32(a)), db = tc::sdesc_kmajor_sw128(tc::smem_u32(b));
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {   // addresses in the descriptors count 16 bytes
+    const uint64_t off = (uint64_t)((kk / 4 * kChunk + kk % 4 * 32) >> 4);
+    if (kk < ksteps) tc::umma_f16(d, da + off, db + off, idesc, kk > 0);
   }
 }
 // D[128 x n] (+)= A[128 x 128] (TMEM, bf16; its second 64 columns of k start `half`
 // TMEM columns after the first) . B, B the [128 x n] tile (rows = k).
 __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t half, const uint8_t* b,
                                            uint32_t idesc, bool accumulate) {
-  const uint32_t sb = tc::smem_u32(b);
+  const uint64_t db = tc::sdesc_mnmajor_sw128(tc::smem_u32(b), kChunk);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    tc::umma_f16_ts(d, a + (kk < 4 ? 0u : half) + (uint32_t)(kk % 4) * 8,
-                    tc::sdesc_mnmajor_sw128(sb + kk * 2048, kChunk), idesc, accumulate || kk > 0);
+  for (int kk = 0; kk < 8; ++kk)   // 16 k: two groups of eight 128-byte rows
+    tc::umma_f16_ts(d, a + (kk < 4 ? 0u : half) + (uint32_t)(kk % 4) * 8, db + (kk * 2048 >> 4),
+                    idesc, accumulate || kk > 0);
 }
 
 // ------------------------------------------------------------------------- forward
@@ -241,42 +240,37 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         }
       }
     }
-  } else if (warp == 1) {  // ------------------------------------------- MMA issuer
-    const uint32_t idesc_o = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
-      if (!ok) give_up(102);
-      tc::tc_fence_after();
-      return ok;
-    };
-    bool ok = n > 0 && wait(&k_full[0], 0);
-    for (int t = 0; t < nt && ok; ++t) {
-      ok = wait(&q_full[t], 0);
-      if (ok && lane == 0) {
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {  // ---------------------------------------- MMA issuer
+      const uint32_t idesc_o = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        if (!ok) give_up(102);
+        tc::tc_fence_after();
+        return ok;
+      };
+      bool ok = wait(&k_full[0], 0);
+      for (int t = 0; t < nt && ok; ++t) {
+        if (!(ok = wait(&q_full[t], 0))) break;
         mma_scores(tmem + 128 * t, Qs + t * C::TILE, Ks, ksteps);
         tc::umma_commit(&s_full[t]);
         if (t == nt - 1) tc::umma_commit(&k_empty[0]);
       }
-    }
-    for (int j = 0; j < n && ok; ++j) {
-      const int s = j % ST, s1 = (j + 1) % ST;
-      for (int t = 0; t < nt && ok; ++t) {
-        if (t == 0) ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u);
-        ok = ok && wait(&p_ready[t], (uint32_t)j & 1u);
-        if (ok && lane == 0) {
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j % ST, s1 = (j + 1) % ST;
+        if (!(ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u))) break;
+        for (int t = 0; t < nt; ++t) {
+          if (!(ok = wait(&p_ready[t], (uint32_t)j & 1u))) break;
           mma_values(tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
           if (t == nt - 1) tc::umma_commit(&v_empty[s]);
           if (j == n - 1) tc::umma_commit(&o_full[t]);
-        }
-        if (j + 1 < n && ok) {
-          if (t == 0) ok = wait(&k_full[s1], (uint32_t)((j + 1) / ST) & 1u);
-          if (ok && lane == 0) {
+          if (j + 1 < n) {
+            if (t == 0 && !(ok = wait(&k_full[s1], (uint32_t)((j + 1) / ST) & 1u))) break;
             mma_scores(tmem + 128 * t, Qs + t * C::TILE, Ks + s1 * C::TILE, ksteps);
             tc::umma_commit(&s_full[t]);
             if (t == nt - 1) tc::umma_commit(&k_empty[s1]);
           }
         }
-        __syncwarp();
       }
     }
   } else if (warp == 2) {  // ------------------------------------------- key mask
@@ -717,44 +711,39 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         for (int s = 0; s < 2; ++s) tc::mbar_wait(&v_full[s], (uint32_t)(j / 2) & 1u, &never, 1 << 20);
       }
     }
-  } else if (warp == 1) {  // ----------------------------------------------- MMA issuer
-    const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
-      if (!ok) give_up(122);
-      tc::tc_fence_after();
-      return ok;
-    };
-    auto scores = [&](int j) {
-      const int s = j % 3;
-      if (!wait(&k_ready[s], (uint32_t)(j / 3) & 1u)) return false;
-      if (lane == 0) {
+  } else if (warp == 1) {
+    if (lane == 0 && n > 0) {  // ------------------------------------------- MMA issuer
+      const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        if (!ok) give_up(122);
+        tc::tc_fence_after();
+        return ok;
+      };
+      auto scores = [&](int j) {
+        const int s = j % 3;
+        if (!wait(&k_ready[s], (uint32_t)(j / 3) & 1u)) return false;
         mma_scores(tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
         tc::umma_commit(&s_full[j % 2]);
-      }
-      return true;
-    };
-    auto grads = [&](int j) {
-      const int s = j % 2;
-      if (!wait(&v_full[s], (uint32_t)(j / 2) & 1u)) return false;
-      if (lane == 0) {
+        return true;
+      };
+      auto grads = [&](int j) {
+        const int s = j % 2;
+        if (!wait(&v_full[s], (uint32_t)(j / 2) & 1u)) return false;
         mma_scores(tmem + 256, Gs, Vs + s * C::TILE, ksteps);
         tc::umma_commit(dp_full);
         tc::umma_commit(&v_empty[s]);
-      }
-      return true;
-    };
-    bool ok = n > 0 && wait(qg_full, 0) && scores(0) && grads(0);
-    for (int j = 0; j < n && ok; ++j) {
-      if (j + 1 < n) ok = scores(j + 1);
-      ok = ok && wait(ds_ready, (uint32_t)j & 1u);
-      if (ok && lane == 0) {
+        return true;
+      };
+      bool ok = wait(qg_full, 0) && scores(0) && grads(0);
+      for (int j = 0; j < n && ok; ++j) {
+        if (j + 1 < n && !(ok = scores(j + 1))) break;
+        if (!(ok = wait(ds_ready, (uint32_t)j & 1u))) break;
         mma_values(tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
         tc::umma_commit(&k_empty[j % 3]);
         if (j + 1 == n) tc::umma_commit(done);
+        else ok = grads(j + 1);
       }
-      __syncwarp();
-      if (ok && j + 1 < n) ok = grads(j + 1);
     }
   } else if (warp == 2) {  // ----------------------------------------------- key mask
     // K's rows of keys that are not permitted become zero: dS is 0 there, and 0 x NaN
