@@ -112,24 +112,24 @@ __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, 
 
 // D[128 x 128] = A[128 x dim] . B[128 x dim]^T, both tiles in shared memory, channels
 // contiguous.
-__device__ __forceinline__ void mma_scores(uint32_t d, const uint8_t* a, const uint8_t* b,
+__device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, const uint8_t* a, const uint8_t* b,
                                            int ksteps) {
   constexpr uint32_t idesc = tc::make_idesc(1, 128, 128);
   const uint64_t da = tc::sdesc_kmajor_sw128(tc::smem_u32(a)), db = tc::sdesc_kmajor_sw128(tc::smem_u32(b));
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk) {   // addresses in the descriptors count 16 bytes
     const uint64_t off = (uint64_t)((kk / 4 * kChunk + kk % 4 * 32) >> 4);
-    if (kk < ksteps) tc::umma_f16(d, da + off, db + off, idesc, kk > 0);
+    if (kk < ksteps) tc::umma_f16_by(leader, d, da + off, db + off, idesc, kk > 0);
   }
 }
 // D[128 x n] (+)= A[128 x 128] (TMEM, bf16; its second 64 columns of k start `half`
 // TMEM columns after the first) . B, B the [128 x n] tile (rows = k).
-__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint32_t half, const uint8_t* b,
+__device__ __forceinline__ void mma_values(uint32_t leader, uint32_t d, uint32_t a, uint32_t half, const uint8_t* b,
                                            uint32_t idesc, bool accumulate) {
   const uint64_t db = tc::sdesc_mnmajor_sw128(tc::smem_u32(b), kChunk);
 #pragma unroll
   for (int kk = 0; kk < 8; ++kk)   // 16 k: two groups of eight 128-byte rows
-    tc::umma_f16_ts(d, a + (kk < 4 ? 0u : half) + (uint32_t)(kk % 4) * 8, db + (kk * 2048 >> 4),
+    tc::umma_f16_ts_by(leader, d, a + (kk < 4 ? 0u : half) + (uint32_t)(kk % 4) * 8, db + (kk * 2048 >> 4),
                     idesc, accumulate || kk > 0);
 }
 
@@ -168,7 +168,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint4* words = reinterpret_cast<uint4*>(tmem_slot + 4);   // [ST] permitted keys of a tile
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(&q_full[t], 1);
@@ -194,7 +194,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
 
@@ -202,7 +202,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int q0 = (int)(blockIdx.x / a.splits) * 2 * BT, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / a.group;
   const int nt = q0 + BT < a.len_q ? 2 : 1;
-  const int len = key_count(a, b);
+  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int tiles = (len + BT - 1) / BT;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int n = (int)((int64_t)tiles * (split + 1) / a.splits) - t0;
@@ -241,10 +241,11 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {  // ---------------------------------------- MMA issuer
+    if (n > 0) {  // ----------------------------------------------------- MMA issuer
+      const uint32_t leader = tc::elect_leader();
       const uint32_t idesc_o = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(102);
         tc::tc_fence_after();
         return ok;
@@ -252,23 +253,23 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       bool ok = wait(&k_full[0], 0);
       for (int t = 0; t < nt && ok; ++t) {
         if (!(ok = wait(&q_full[t], 0))) break;
-        mma_scores(tmem + 128 * t, Qs + t * C::TILE, Ks, ksteps);
-        tc::umma_commit(&s_full[t]);
-        if (t == nt - 1) tc::umma_commit(&k_empty[0]);
+        mma_scores(leader, tmem + 128 * t, Qs + t * C::TILE, Ks, ksteps);
+        tc::umma_commit_by(leader, &s_full[t]);
+        if (t == nt - 1) tc::umma_commit_by(leader, &k_empty[0]);
       }
       for (int j = 0; j < n && ok; ++j) {
         const int s = j % ST, s1 = (j + 1) % ST;
         if (!(ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u))) break;
         for (int t = 0; t < nt; ++t) {
           if (!(ok = wait(&p_ready[t], (uint32_t)j & 1u))) break;
-          mma_values(tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
-          if (t == nt - 1) tc::umma_commit(&v_empty[s]);
-          if (j == n - 1) tc::umma_commit(&o_full[t]);
+          mma_values(leader, tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
+          if (t == nt - 1) tc::umma_commit_by(leader, &v_empty[s]);
+          if (j == n - 1) tc::umma_commit_by(leader, &o_full[t]);
           if (j + 1 < n) {
             if (t == 0 && !(ok = wait(&k_full[s1], (uint32_t)((j + 1) / ST) & 1u))) break;
-            mma_scores(tmem + 128 * t, Qs + t * C::TILE, Ks + s1 * C::TILE, ksteps);
-            tc::umma_commit(&s_full[t]);
-            if (t == nt - 1) tc::umma_commit(&k_empty[s1]);
+            mma_scores(leader, tmem + 128 * t, Qs + t * C::TILE, Ks + s1 * C::TILE, ksteps);
+            tc::umma_commit_by(leader, &s_full[t]);
+            if (t == nt - 1) tc::umma_commit_by(leader, &k_empty[s1]);
           }
         }
       }
@@ -483,9 +484,9 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
   uint64_t *kv_full = bars, *q_full = bars + 1, *q_empty = bars + 4, *g_full = bars + 7,
            *g_empty = bars + 9, *s_full = bars + 11, *dp_full = bars + 12, *p_ready = bars + 13,
            *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int k0 = (int)blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
-  const int len = key_count(a, b);
+  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int n = k0 < len ? a.group * qtiles : 0;
   const int ksteps = (a.dim + 15) / 16;
@@ -520,38 +521,39 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {  // ------------------------------------------- MMA issuer
+    if (n > 0) {  // ------------------------------------------------------- MMA issuer
+      const uint32_t leader = tc::elect_leader();
       const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(112);
         tc::tc_fence_after();
         return ok;
       };
       bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
       if (ok) {
-        mma_scores(tmem, Ks, Qs, ksteps);
-        tc::umma_commit(s_full);
+        mma_scores(leader, tmem, Ks, Qs, ksteps);
+        tc::umma_commit_by(leader, s_full);
       }
       for (int i = 0; i < n && ok; ++i) {
         const int sq = i % 3, sg = i % 2, s1 = (i + 1) % 3;
         const uint32_t ph = (uint32_t)i & 1u;
         if (!(ok = wait(&g_full[sg], (uint32_t)(i / 2) & 1u))) break;
-        mma_scores(tmem + 128, Vs, Gs + sg * C::TILE, ksteps);
-        tc::umma_commit(dp_full);
+        mma_scores(leader, tmem + 128, Vs, Gs + sg * C::TILE, ksteps);
+        tc::umma_commit_by(leader, dp_full);
         if (!(ok = wait(p_ready, ph))) break;
-        mma_values(tmem + 256, tmem, 64, Gs + sg * C::TILE, idesc, i > 0);
-        tc::umma_commit(&g_empty[sg]);
+        mma_values(leader, tmem + 256, tmem, 64, Gs + sg * C::TILE, idesc, i > 0);
+        tc::umma_commit_by(leader, &g_empty[sg]);
         if (i + 1 < n) {
           if (!(ok = wait(&q_full[s1], (uint32_t)((i + 1) / 3) & 1u))) break;
-          mma_scores(tmem, Ks, Qs + s1 * C::TILE, ksteps);
-          tc::umma_commit(s_full);
+          mma_scores(leader, tmem, Ks, Qs + s1 * C::TILE, ksteps);
+          tc::umma_commit_by(leader, s_full);
         }
         if (!(ok = wait(ds_ready, ph))) break;
-        mma_values(tmem + 256 + 64 * NC, tmem + 128, 64, Qs + sq * C::TILE, idesc, i > 0);
-        tc::umma_commit(&q_empty[sq]);
+        mma_values(leader, tmem + 256 + 64 * NC, tmem + 128, 64, Qs + sq * C::TILE, idesc, i > 0);
+        tc::umma_commit_by(leader, &q_empty[sq]);
       }
-      if (ok) tc::umma_commit(done);
+      if (ok) tc::umma_commit_by(leader, done);
     }
   } else if (warp == 2) {  // ---------------------------------------------- row statistics
     for (int i = 0; i < n; ++i) {
@@ -675,11 +677,11 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
            *v_empty = bars + 9, *dp_full = bars + 12, *ds_ready = bars + 14, *s_full = bars + 15,
            *done = bars + 19, *k_ready = bars + 20, *w_full = bars + 23;
   uint4* words = reinterpret_cast<uint4*>(bars + 28);   // [3] permitted keys of a tile
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int h = hk * a.group + tile / qtiles, q0 = tile % qtiles * BT;
-  const int len = key_count(a, b);
+  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int n = (len + BT - 1) / BT;
   const int ksteps = (a.dim + 15) / 16;
   auto give_up = [&](int info) {
@@ -712,10 +714,11 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && n > 0) {  // ------------------------------------------- MMA issuer
+    if (n > 0) {  // ------------------------------------------------------- MMA issuer
+      const uint32_t leader = tc::elect_leader();
       const uint32_t idesc = tc::make_idesc(1, 128, ksteps * 16) | tc::kIdescMnB;
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = tc::mbar_wait(bar, parity, abort_flag);
+        const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(122);
         tc::tc_fence_after();
         return ok;
@@ -723,25 +726,25 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       auto scores = [&](int j) {
         const int s = j % 3;
         if (!wait(&k_ready[s], (uint32_t)(j / 3) & 1u)) return false;
-        mma_scores(tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
-        tc::umma_commit(&s_full[j % 2]);
+        mma_scores(leader, tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
+        tc::umma_commit_by(leader, &s_full[j % 2]);
         return true;
       };
       auto grads = [&](int j) {
         const int s = j % 2;
         if (!wait(&v_full[s], (uint32_t)(j / 2) & 1u)) return false;
-        mma_scores(tmem + 256, Gs, Vs + s * C::TILE, ksteps);
-        tc::umma_commit(dp_full);
-        tc::umma_commit(&v_empty[s]);
+        mma_scores(leader, tmem + 256, Gs, Vs + s * C::TILE, ksteps);
+        tc::umma_commit_by(leader, dp_full);
+        tc::umma_commit_by(leader, &v_empty[s]);
         return true;
       };
       bool ok = wait(qg_full, 0) && scores(0) && grads(0);
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n && !(ok = scores(j + 1))) break;
         if (!(ok = wait(ds_ready, (uint32_t)j & 1u))) break;
-        mma_values(tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
-        tc::umma_commit(&k_empty[j % 3]);
-        if (j + 1 == n) tc::umma_commit(done);
+        mma_values(leader, tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
+        tc::umma_commit_by(leader, &k_empty[j % 3]);
+        if (j + 1 == n) tc::umma_commit_by(leader, done);
         else ok = grads(j + 1);
       }
     }
@@ -856,7 +859,7 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 7 * C::TILE + C::STATS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBwdBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const int warp = threadIdx.x / 32;
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0);
   const int key_tiles = (a.len_kv + BT - 1) / BT;
   const bool dkv = (int)blockIdx.x < key_tiles;
   if (threadIdx.x == 0) {
@@ -876,7 +879,7 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
   if (dkv) dkv_block<NC>(a, mp, smem, bars, abort_flag, tmem);
