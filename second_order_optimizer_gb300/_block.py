@@ -13,7 +13,6 @@ tensors allocated here are marked as used on it.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -22,8 +21,12 @@ from ._lib import (LIB, KFAC_F32, KFAC_BF16, KFAC_ROPE_PLAIN, ROPE_DESC, ATTENTI
                    ATTENTION_GRAD_DESC, KfacError)
 
 _DTYPE = {torch.float32: KFAC_F32, torch.bfloat16: KFAC_BF16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_here = contextlib.nullcontext()
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_MAX64 = (1 << 64) - 1
+
+# The checks below are spelled out call by call rather than looped over: a call of a few rows
+# takes the GPU two microseconds, and each attribute of a tensor costs about 0.1.
 
 
 def _check(code: int, what: str):
@@ -32,57 +35,59 @@ def _check(code: int, what: str):
 
 
 def _dtype(t, what):
-    try:
-        return _DTYPE[t.dtype]
-    except KeyError:
-        raise ValueError(f"{what}: float32 or bfloat16 tensors, not {t.dtype}") from None
+    dt = _DTYPE.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"{what}: float32 or bfloat16 tensors, not {t.dtype}")
+    return dt
 
 
-def _same(what, ref, **tensors):
-    """Every tensor on ref's CUDA device."""
-    if not ref.is_cuda:
+def _device(t, what):
+    """The index of t's CUDA device."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{what}: CUDA tensors (there is no CPU implementation)")
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"{what}: {name} is on {t.device}, not {ref.device}")
+    return dev
 
 
-def _heads(what, name, t, dtype, shape):
-    """t: [batch, length, heads, head_dim] of this type and shape, channels contiguous."""
-    if t.dtype != dtype or t.shape != shape:
+def _elsewhere(what, name, t, dev):
+    raise ValueError(f"{what}: {name} is on {t.device}, not cuda:{dev}")
+
+
+def _heads(what, name, t, dtype, shape, dev):
+    """Strides of t: [batch, length, heads, head_dim] of this type, shape and device, channels
+    contiguous."""
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: {name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
+    if t.get_device() != dev:
+        _elsewhere(what, name, t, dev)
     s = t.stride()
     if s[3] != 1 and shape[3] > 1:
         raise ValueError(f"{what}: {name}'s channels are not contiguous (stride {s[3]})")
     return s
 
 
-def _on(device):
-    """The library works on the current device: make it the tensors'."""
-    return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream(stream, device):
+def _call(f, what, dev, stream, *args):
+    """f(*args, stream) on the tensors' device (the library works on the current one)."""
     if stream is None:
-        if _raw_stream is not None:
-            return _raw_stream(device.index)
-        return torch.cuda.current_stream(device).cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        s = _raw_stream(dev)
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev == _current_device():
+        code = f(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, s)
+    if code != 0:
+        raise KfacError(code, what)
 
 
-def _used_on(stream, device, *made):
+def _used_on(stream, dev, *made):
     """Tensors allocated here belong to torch's current stream: tell its allocator where else
     they are used."""
-    if stream is None:
-        return
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
     for t in made:
         if t is not None:
             t.record_stream(s)
-
-
-def _p(t):
-    return None if t is None else t.data_ptr()
 
 
 # --------------------------------------------------------------------------- rotary positions
@@ -97,14 +102,13 @@ def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, scaling: int =
     if out is None:
         dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         out = made = torch.empty(rows, rotary_dim, device=dev)
-    _same("rope_table", out)
+    dev = _device(out, "rope_table")
     if out.dtype != torch.float32 or out.shape != (rows, rotary_dim) or not out.is_contiguous():
         raise ValueError("rope_table: out is float32 [rows, rotary_dim], contiguous")
-    with _on(out.device):
-        _check(LIB.kfac_rope_table(out.data_ptr(), rows, rotary_dim, float(base), scaling,
-                                   float(factor), float(original_length),
-                                   _stream(stream, out.device)), "kfac_rope_table")
-    _used_on(stream, out.device, made)
+    _call(LIB.kfac_rope_table, "kfac_rope_table", dev, stream, out.data_ptr(), rows, rotary_dim,
+          float(base), scaling, float(factor), float(original_length))
+    if stream is not None:
+        _used_on(stream, dev, made)
     return out
 
 
@@ -116,84 +120,94 @@ def rope(q, k, table, positions=None, position_offset: int = 0, interleaved: boo
     inverse=True is the backward pass (gradients of the outputs in, of the inputs out).
     out_q=q, out_k=k work in place."""
     ref = q if q is not None else k
-    if ref is None or ref.dim() != 4:
-        raise ValueError("rope: q or k [batch, length, heads, head_dim]")
-    _same("rope", ref, k=k, table=table, positions=positions, out_q=out_q, out_k=out_k)
-    dt = _dtype(ref, "rope")
+    if ref is None or ref.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("rope: q and k are [batch, length, heads, head_dim]")
+    dt, dtype, dev = _dtype(ref, "rope"), ref.dtype, _device(ref, "rope")
     b, n, _, d = ref.shape
-    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+    if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("rope: table is float32 [rows, rotary_dim], contiguous")
-    made = [None, None]
-    strides, heads = [], []
-    for i, (name, x, y) in enumerate((("q", q, out_q), ("k", k, out_k))):
-        if x is None:
-            strides.append(((0, 0, 0, 0), (0, 0, 0, 0)))
-            heads.append(0)
-            continue
-        h = x.shape[2] if x.dim() == 4 else 0
-        shape = (b, n, h, d)
-        sx = _heads("rope", name, x, ref.dtype, shape)
-        if y is None:
-            y = made[i] = torch.empty(shape, dtype=x.dtype, device=x.device)
-            if i == 0:
-                out_q = y
-            else:
-                out_k = y
-        strides.append((sx, _heads("rope", "out_" + name, y, ref.dtype, shape)))
-        heads.append(h)
-    ps = 0
+    if table.get_device() != dev:
+        _elsewhere("rope", "table", table, dev)
+    made_q = made_k = None
+    h = kv = 0
+    qs = ks = oqs = oks = (0, 0, 0, 0)
+    if q is not None:
+        shape = q.shape
+        h = shape[2]
+        qs = _heads("rope", "q", q, dtype, shape, dev)
+        if out_q is None:
+            out_q = made_q = torch.empty(shape, dtype=dtype, device=q.device)
+        oqs = _heads("rope", "out_q", out_q, dtype, shape, dev)
+    if k is not None:
+        kv = k.shape[2]
+        shape = (b, n, kv, d)
+        ks = _heads("rope", "k", k, dtype, shape, dev)
+        if out_k is None:
+            out_k = made_k = torch.empty(shape, dtype=dtype, device=k.device)
+        oks = _heads("rope", "out_k", out_k, dtype, shape, dev)
+    ps, pp = 0, None
     if positions is not None:
-        if positions.dtype != torch.int32 or positions.shape not in ((b, n), (n,)) or (
+        if positions.dtype is not torch.int32 or positions.shape not in ((b, n), (n,)) or (
                 n > 1 and positions.stride(-1) != 1):
             raise ValueError("rope: positions is int32 [batch, length] or [length], rows contiguous")
-        ps = positions.stride(0) if positions.dim() == 2 else 0
-    (qs, oq), (ks, ok) = strides
-    desc = ROPE_DESC.pack(dt, b, n, heads[0], heads[1], d, table.shape[1], bool(interleaved),
-                          bool(inverse), table.shape[0], position_offset, ps, qs[0], qs[1], qs[2],
-                          ks[0], ks[1], ks[2], oq[0], oq[1], oq[2], ok[0], ok[1], ok[2])
-    with _on(ref.device):
-        _check(LIB.kfac_rope(desc, _p(q), _p(k), table.data_ptr(), _p(positions),
-                             None if q is None else out_q.data_ptr(),
-                             None if k is None else out_k.data_ptr(), _stream(stream, ref.device)),
-               "kfac_rope")
-    _used_on(stream, ref.device, *made)
+        if positions.get_device() != dev:
+            _elsewhere("rope", "positions", positions, dev)
+        ps, pp = positions.stride(0) if positions.dim() == 2 else 0, positions.data_ptr()
+    rows, rotary = table.shape
+    desc = ROPE_DESC.pack(dt, b, n, h, kv, d, rotary, bool(interleaved), bool(inverse), rows,
+                          position_offset, ps, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], oqs[0],
+                          oqs[1], oqs[2], oks[0], oks[1], oks[2])
+    _call(LIB.kfac_rope, "kfac_rope", dev, stream, desc, None if q is None else q.data_ptr(),
+          None if k is None else k.data_ptr(), table.data_ptr(), pp,
+          None if q is None else out_q.data_ptr(), None if k is None else out_k.data_ptr())
+    if stream is not None:
+        _used_on(stream, dev, made_q, made_k)
     return (None if q is None else out_q), (None if k is None else out_k)
 
 
 # ------------------------------------------------------------------------------------ dropout
 
-def _rows(what, name, t, like):
-    """(leading dimension) of a tensor read as [rows, cols] with contiguous columns."""
-    if t.shape != like.shape or t.dtype != like.dtype:
-        raise ValueError(f"{what}: {name} is {t.dtype} {tuple(t.shape)}, not {like.dtype} "
-                         f"{tuple(like.shape)}")
-    if t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1):
-        return t.stride(0)
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: {name} is contiguous, or 2-D with contiguous rows")
-    return t.shape[-1] if t.dim() else 1
+def _ld(name, t):
+    """Leading dimension of a 2-D tensor with contiguous rows."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"dropout: {name} is contiguous, or 2-D with contiguous rows")
+    return t.stride(0)
+
+
+def _like(name, t, x, shape, dev):
+    if t.shape != shape or t.dtype is not x.dtype:
+        raise ValueError(f"dropout: {name} is {t.dtype} {tuple(t.shape)}, not {x.dtype} {tuple(shape)}")
+    if t.get_device() != dev:
+        _elsewhere("dropout", name, t, dev)
 
 
 def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, stream=None):
     """kfac_dropout: residual + dropout(x) (residual may be None) with the mask of (seed, offset);
     returns out.  x: contiguous of any shape, or 2-D with contiguous rows.  Each use within a
     step takes an offset (or seed) of its own; the backward pass takes the same one."""
-    dt = _dtype(x, "dropout")
-    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+    if not (0 <= seed <= _MAX64 and 0 <= offset <= _MAX64):
         raise ValueError("dropout: seed and offset are 64-bit counts")
-    _same("dropout", x, residual=residual, out=out)
-    made = None
+    dt, shape, dev = _dtype(x, "dropout"), x.shape, _device(x, "dropout")
+    made, rp = None, None
     if out is None:
-        out = made = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    ldx, ldo = _rows("dropout", "x", x, x), _rows("dropout", "out", out, x)
-    ldr = _rows("dropout", "residual", residual, x) if residual is not None else 0
-    cols = x.shape[-1] if x.dim() else 1
-    rows = x.numel() // cols if cols else 0
-    with _on(x.device):
-        _check(LIB.kfac_dropout(dt, x.data_ptr(), ldx, _p(residual), ldr, out.data_ptr(), ldo,
-                                rows, cols, p, seed, offset, _stream(stream, x.device)),
-               "kfac_dropout")
-    _used_on(stream, x.device, made)
+        out = made = torch.empty(shape, dtype=x.dtype, device=x.device)
+    else:
+        _like("out", out, x, shape, dev)
+    flat = x.is_contiguous() and out.is_contiguous()
+    if residual is not None:
+        _like("residual", residual, x, shape, dev)
+        rp, flat = residual.data_ptr(), flat and residual.is_contiguous()
+    if flat:   # the row-major index is the address
+        rows, cols = 1, x.numel()
+        ldx = ldr = ldo = cols
+    else:
+        ldx, ldo = _ld("x", x), _ld("out", out)
+        ldr = _ld("residual", residual) if residual is not None else 0
+        rows, cols = shape
+    _call(LIB.kfac_dropout, "kfac_dropout", dev, stream, dt, x.data_ptr(), ldx, rp, ldr,
+          out.data_ptr(), ldo, rows, cols, p, seed, offset)
+    if stream is not None:
+        _used_on(stream, dev, made)
     return out
 
 
@@ -205,34 +219,57 @@ def dropout_backward(dout, p: float, seed: int, offset: int = 0, out=None, strea
 
 # ---------------------------------------------------------------------------- cross attention
 
-def _attention(what, q, k, v, out, scale):
-    """Descriptor bytes of these tensors."""
+def _attention(what, q, k, v, out, scale, dev):
+    """Descriptor bytes of these tensors (v and out None: laid out as k and q)."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"{what}: q [batch, len_q, heads, head_dim], k [batch, len_kv, kv_heads, "
                          f"head_dim]")
-    b, nq, h, d = q.shape
-    nk, kv = k.shape[1], k.shape[2]
-    qs = _heads(what, "q", q, q.dtype, q.shape)
-    ks = _heads(what, "k", k, q.dtype, (b, nk, kv, d))
-    vs = _heads(what, "v", v, q.dtype, (b, nk, kv, d)) if v is not None else ks
-    os = _heads(what, "out", out, q.dtype, q.shape) if out is not None else qs
+    dtype, shape = q.dtype, q.shape
+    b, nq, h, d = shape
+    _, nk, kv, _ = k.shape
+    keys = (b, nk, kv, d)
+    qs = q.stride()
+    if qs[3] != 1 and d > 1:
+        raise ValueError(f"{what}: q's channels are not contiguous (stride {qs[3]})")
+    ks = _heads(what, "k", k, dtype, keys, dev)
+    vs = _heads(what, "v", v, dtype, keys, dev) if v is not None else ks
+    os = _heads(what, "out", out, dtype, shape, dev) if out is not None else qs
     return ATTENTION_DESC.pack(_dtype(q, what), b, nq, nk, h, kv, d,
                                0.0 if scale is None else scale, qs[0], qs[1], qs[2], ks[0], ks[1],
                                ks[2], vs[0], vs[1], vs[2], os[0], os[1], os[2])
 
 
-def _keys(what, kv_len, key_mask, k):
-    if kv_len is not None and (kv_len.dtype != torch.int32 or kv_len.shape != (k.shape[0],)
-                               or not kv_len.is_contiguous()):
-        raise ValueError(f"{what}: kv_len is int32 [batch], contiguous")
-    if key_mask is not None and (key_mask.dtype not in (torch.uint8, torch.bool)
-                                 or key_mask.shape != k.shape[:2] or not key_mask.is_contiguous()):
-        raise ValueError(f"{what}: key_mask is uint8 or bool [batch, len_kv], contiguous")
+def _keys(what, kv_len, key_mask, k, dev):
+    """Addresses of kv_len and key_mask, checked."""
+    lp = mp = None
+    if kv_len is not None:
+        if kv_len.dtype is not torch.int32 or kv_len.shape != k.shape[:1] or (
+                not kv_len.is_contiguous()):
+            raise ValueError(f"{what}: kv_len is int32 [batch], contiguous")
+        if kv_len.get_device() != dev:
+            _elsewhere(what, "kv_len", kv_len, dev)
+        lp = kv_len.data_ptr()
+    if key_mask is not None:
+        if key_mask.dtype not in (torch.uint8, torch.bool) or key_mask.shape != k.shape[:2] or (
+                not key_mask.is_contiguous()):
+            raise ValueError(f"{what}: key_mask is uint8 or bool [batch, len_kv], contiguous")
+        if key_mask.get_device() != dev:
+            _elsewhere(what, "key_mask", key_mask, dev)
+        mp = key_mask.data_ptr()
+    return lp, mp
 
 
-def _workspace_bytes(desc, backward, device):
+def _stats(what, lse, q, dev):
+    if lse.dtype is not torch.float32 or lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or (
+            not lse.is_contiguous()):
+        raise ValueError(f"{what}: lse is float32 [batch, heads, len_q], contiguous")
+    if lse.get_device() != dev:
+        _elsewhere(what, "lse", lse, dev)
+
+
+def _workspace_bytes(desc, backward, dev):
     nbytes = ctypes.c_size_t(0)
-    with _on(device):
+    with torch.cuda.device(dev):   # the plan depends on the device's SM count
         _check(LIB.kfac_cross_attention_workspace_size(desc, int(backward), ctypes.byref(nbytes)),
                "kfac_cross_attention_workspace_size")
     return nbytes.value
@@ -241,9 +278,9 @@ def _workspace_bytes(desc, backward, device):
 def cross_attention_workspace(q, k, backward: bool = False):
     """A workspace tensor for cross_attention (backward=True: and cross_attention_backward) of
     tensors like these, to be kept and passed to the calls."""
-    _same("cross_attention_workspace", q, k=k)
-    desc = _attention("cross_attention_workspace", q, k, None, None, None)
-    n = _workspace_bytes(desc, backward, q.device)
+    what = "cross_attention_workspace"
+    dev = _device(q, what)
+    n = _workspace_bytes(_attention(what, q, k, None, None, None, dev), backward, dev)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
 
 
@@ -254,28 +291,27 @@ def cross_attention(q, k, v, kv_len=None, key_mask=None, scale=None, out=None, l
     [batch] and key_mask uint8 or bool [batch, len_kv] say which keys are permitted (None: all);
     scale None: 1/sqrt(head_dim).  lse: float32 [batch, heads, len_q], kept for the backward
     pass."""
-    _same("cross_attention", q, k=k, v=v, kv_len=kv_len, key_mask=key_mask, out=out, lse=lse,
-          workspace=workspace)
-    made = [None, None, None]
+    what = "cross_attention"
+    dev = _device(q, what)
+    made_o = made_l = made_w = None
     if out is None:
-        out = made[0] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    desc = _attention("cross_attention", q, k, v, out, scale)
-    _keys("cross_attention", kv_len, key_mask, k)
-    stats = (q.shape[0], q.shape[2], q.shape[1])
+        out = made_o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    desc = _attention(what, q, k, v, out, scale, dev)
+    lp, mp = _keys(what, kv_len, key_mask, k, dev)
     if lse is None:
-        lse = made[1] = torch.empty(stats, device=q.device)
-    elif lse.dtype != torch.float32 or lse.shape != stats or not lse.is_contiguous():
-        raise ValueError("cross_attention: lse is float32 [batch, heads, len_q], contiguous")
+        lse = made_l = torch.empty(q.shape[0], q.shape[2], q.shape[1], device=q.device)
+    else:
+        _stats(what, lse, q, dev)
     if workspace is None:
-        workspace = made[2] = torch.empty(_workspace_bytes(desc, False, q.device),
-                                          dtype=torch.uint8, device=q.device)
-    with _on(q.device):
-        _check(LIB.kfac_cross_attention(desc, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                        _p(kv_len), _p(key_mask), out.data_ptr(), lse.data_ptr(),
-                                        workspace.data_ptr(),
-                                        workspace.numel() * workspace.element_size(),
-                                        _stream(stream, q.device)), "kfac_cross_attention")
-    _used_on(stream, q.device, *made)
+        workspace = made_w = torch.empty(_workspace_bytes(desc, False, dev), dtype=torch.uint8,
+                                         device=q.device)
+    elif workspace.get_device() != dev:
+        _elsewhere(what, "workspace", workspace, dev)
+    _call(LIB.kfac_cross_attention, "kfac_cross_attention", dev, stream, desc, q.data_ptr(),
+          k.data_ptr(), v.data_ptr(), lp, mp, out.data_ptr(), lse.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)
+    if stream is not None:
+        _used_on(stream, dev, made_o, made_l, made_w)
     return out, lse
 
 
@@ -285,35 +321,35 @@ def cross_attention_backward(dout, q, k, v, out, lse, kv_len=None, key_mask=None
     gradient dout of its output, from its inputs and its out and lse; dk and dv of a key head
     sum over the query heads that share it."""
     what = "cross_attention_backward"
-    _same(what, q, dout=dout, k=k, v=v, out=out, lse=lse, kv_len=kv_len, key_mask=key_mask,
-          dq=dq, dk=dk, dv=dv, workspace=workspace)
-    desc = _attention(what, q, k, v, out, scale)
-    _keys(what, kv_len, key_mask, k)
-    if lse.dtype != torch.float32 or lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or (
-            not lse.is_contiguous()):
-        raise ValueError(f"{what}: lse is float32 [batch, heads, len_q], contiguous")
+    dev = _device(q, what)
+    desc = _attention(what, q, k, v, out, scale, dev)
+    lp, mp = _keys(what, kv_len, key_mask, k, dev)
+    _stats(what, lse, q, dev)
+    dtype, shape, keys = q.dtype, q.shape, k.shape
     made = [None] * 4
     if dq is None:
-        dq = made[0] = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        dq = made[0] = torch.empty(shape, dtype=dtype, device=q.device)
     if dk is None:
-        dk = made[1] = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        dk = made[1] = torch.empty(keys, dtype=dtype, device=q.device)
     if dv is None:
-        dv = made[2] = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    grads = ATTENTION_GRAD_DESC.pack(*_heads(what, "dout", dout, q.dtype, q.shape)[:3],
-                                     *_heads(what, "dq", dq, q.dtype, q.shape)[:3],
-                                     *_heads(what, "dk", dk, q.dtype, k.shape)[:3],
-                                     *_heads(what, "dv", dv, q.dtype, k.shape)[:3])
+        dv = made[2] = torch.empty(keys, dtype=dtype, device=q.device)
+    gs = _heads(what, "dout", dout, dtype, shape, dev)
+    qs = _heads(what, "dq", dq, dtype, shape, dev)
+    ks = _heads(what, "dk", dk, dtype, keys, dev)
+    vs = _heads(what, "dv", dv, dtype, keys, dev)
+    grads = ATTENTION_GRAD_DESC.pack(gs[0], gs[1], gs[2], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
+                                     vs[0], vs[1], vs[2])
     if workspace is None:
-        workspace = made[3] = torch.empty(_workspace_bytes(desc, True, q.device),
-                                          dtype=torch.uint8, device=q.device)
-    with _on(q.device):
-        _check(LIB.kfac_cross_attention_backward(
-            desc, grads, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            out.data_ptr(), lse.data_ptr(), _p(kv_len), _p(key_mask), dq.data_ptr(),
-            dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream(stream, q.device)),
-            "kfac_cross_attention_backward")
-    _used_on(stream, q.device, *made)
+        workspace = made[3] = torch.empty(_workspace_bytes(desc, True, dev), dtype=torch.uint8,
+                                          device=q.device)
+    elif workspace.get_device() != dev:
+        _elsewhere(what, "workspace", workspace, dev)
+    _call(LIB.kfac_cross_attention_backward, "kfac_cross_attention_backward", dev, stream, desc,
+          grads, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), lp, mp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+          workspace.data_ptr(), workspace.nbytes)
+    if stream is not None:
+        _used_on(stream, dev, *made)
     return dq, dk, dv
 
 
