@@ -22,8 +22,9 @@ struct Args {
   int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
   int batch, len_q, len_kv, heads, kv_heads, group, dim, rows;
   float scale;
+  bool vec;                         // CUDA-core kernels: fp32 rows of whole 16 bytes
   int splits;                       // parts of the key axis (1: outputs written directly)
-  int part_keys;                    // token kernel: keys per part
+  int part_keys;                    // token kernel, more parts than a cluster: keys per part
   float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised
   float* part_lse;                  // [splits][batch][kv_heads][rows]
 };
@@ -44,6 +45,7 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
 
 // Few query rows (bf16, rows that tc_forward_ok accepts).
 constexpr int kTokenWarps = 4;
+constexpr int kTokenCluster = 8;    // parts that one cluster joins
 kfac_status token_forward(const Args& a, cudaStream_t st);
 
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.

@@ -35,13 +35,31 @@ template <int BQ, int DP> struct SimtCfg {
 };
 
 // rows x dim of global memory -> shared [n][DP + 4] fp32, zeros past dim and where
-// `ok` is false.
+// `off` gives none (negative).  16 threads per row, four channels at a time: one
+// offset per row and thread, and 16-byte loads where the rows allow (vec).
 template <typename T, int DP, typename Off>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int n, int dim, Off off) {
-  for (int e = threadIdx.x; e < n * DP; e += kThreads) {
-    const int r = e / DP, d = e % DP;
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int n, int dim, bool vec, Off off) {
+  const int c0 = threadIdx.x % 16;
+#pragma unroll 4
+  for (int r = threadIdx.x / 16; r < n; r += kThreads / 16) {
     const int64_t o = off(r);
-    dst[r * (DP + 4) + d] = (o >= 0 && d < dim) ? to_f32<T>(src[o + d]) : 0.f;
+    const T* p = src + o;
+#pragma unroll
+    for (int c = c0; c < DP / 4; c += 16) {
+      const int d = 4 * c;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (o >= 0 && d < dim) {
+        if (sizeof(T) == 4 && vec) {
+          v = *reinterpret_cast<const float4*>(p + d);
+        } else {
+          v.x = to_f32<T>(p[d]);
+          if (d + 1 < dim) v.y = to_f32<T>(p[d + 1]);
+          if (d + 2 < dim) v.z = to_f32<T>(p[d + 2]);
+          if (d + 3 < dim) v.w = to_f32<T>(p[d + 3]);
+        }
+      }
+      *reinterpret_cast<float4*>(dst + r * (DP + 4) + d) = v;
+    }
   }
 }
 
@@ -162,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_con
   const int tiles = (len + BK - 1) / BK;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
-  load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, [&](int r) -> int64_t {
+  load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, a.vec, [&](int r) -> int64_t {
     return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
   });
   float m[RT], l[RT];
@@ -179,10 +197,10 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_con
     __syncthreads();
     if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
     __syncthreads();
-    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, a.vec, [&](int r) -> int64_t {
       return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
     });
-    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, a.vec, [&](int r) -> int64_t {
       return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
     });
     __syncthreads();
@@ -347,18 +365,18 @@ __global__ void __launch_bounds__(kThreads) simt_backward_kernel(const __grid_co
   auto load_keys = [&](int t) {
     if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
     __syncthreads();
-    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, a.vec, [&](int r) -> int64_t {
       return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
     });
-    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, a.vec, [&](int r) -> int64_t {
       return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
     });
   };
   auto load_rows = [&](int r0) {
-    load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, a.vec, [&](int r) -> int64_t {
       return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
     });
-    load_tile<T, DP>(Os, static_cast<const T*>(a.dout), BQ, a.dim, [&](int r) -> int64_t {
+    load_tile<T, DP>(Os, static_cast<const T*>(a.dout), BQ, a.dim, a.vec, [&](int r) -> int64_t {
       return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
     });
     if (threadIdx.x < BQ) {
@@ -452,8 +470,17 @@ kfac_status launch_combine(const Args& a, cudaStream_t st) {
   return check_launch();
 }
 
+// fp32 rows that start at multiples of 16 bytes and hold whole ones.
+bool vec_rows(const void* p, const int64_t* s, int rows, int heads, int batch, int dim) {
+  return dim % 4 == 0 && (uintptr_t)p % 16 == 0 && (batch <= 1 || s[0] % 4 == 0) &&
+         (rows <= 1 || s[1] % 4 == 0) && (heads <= 1 || s[2] % 4 == 0);
+}
+
 template <typename T>
-kfac_status simt_forward(const Args& a, cudaStream_t st) {
+kfac_status simt_forward(Args a, cudaStream_t st) {
+  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim) &&
+          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim) &&
+          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim);
   kfac_status e;
   if (a.rows <= 16)
     e = a.dim <= 64 ? launch_simt_forward<T, 16, 64>(a, st) : launch_simt_forward<T, 16, 128>(a, st);
@@ -475,7 +502,11 @@ kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
 }
 
 template <typename T>
-kfac_status backward(const Args& a, cudaStream_t st) {
+kfac_status backward(Args a, cudaStream_t st) {
+  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim) &&
+          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim) &&
+          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim) &&
+          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim);
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
   if (n > 0) {
     launch_pdl(delta_kernel<T>, dim3((unsigned)cdiv(n, 8)), dim3(256), 0, st, a);
@@ -507,17 +538,24 @@ constexpr int kTokenRows = 64;
 bool token_sizes(const kfac_attention_desc& d) {
   return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q <= kTokenRows;
 }
-// Keys per part: about 8 blocks per SM over the full length (ragged lengths then
-// balance), at least one step of every warp.
-int token_part_keys(const kfac_attention_desc& d) {
-  const int64_t ctas = cdiv((int64_t)d.heads / d.kv_heads * d.len_q, 16) * d.kv_heads * d.batch;
-  const int64_t parts = std::max<int64_t>(1, 8 * num_sms() / std::max<int64_t>(ctas, 1));
+// Parts of the key axis for the token kernel: as many blocks as are resident at once
+// (two per SM) - no more for equal lengths, where a second wave of a few blocks costs as
+// much as a whole one, and at least as many for ragged ones, which a part more evens out
+// (32 x 8192 keys on 4 key heads: 85 us in 2 parts and 116 us in 3; ragged, 81 and 67).
+// Each warp has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a
+// cluster, more are fixed lengths.
+int token_splits(const kfac_attention_desc& d, bool ragged, int* part_keys) {
+  const int64_t ctas = std::max<int64_t>(
+      1, cdiv((int64_t)d.heads / d.kv_heads * d.len_q, 16) * d.kv_heads * d.batch);
   const int step = 16 * kTokenWarps;
-  const int64_t keys = std::max<int64_t>(cdiv(d.len_kv, parts), cdiv(d.len_kv, 256));
-  return (int)std::max<int64_t>(step, cdiv(keys, step) * step);
-}
-int token_splits(const kfac_attention_desc& d) {
-  return (int)std::max<int64_t>(1, cdiv(d.len_kv, token_part_keys(d)));
+  const int64_t most = std::max<int64_t>(1, cdiv(d.len_kv, step)), slots = 2 * num_sms();
+  int64_t parts = std::min<int64_t>(most, ragged ? cdiv(slots, ctas) : std::max<int64_t>(1, slots / ctas));
+  *part_keys = d.len_kv;
+  if (parts > kTokenCluster) {
+    *part_keys = (int)(cdiv(cdiv(d.len_kv, parts), step) * step);
+    parts = cdiv(d.len_kv, *part_keys);
+  }
+  return (int)parts;
 }
 
 bool valid_desc(const kfac_attention_desc* d) {
@@ -541,8 +579,9 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 }
 
 size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
-  int splits = simt_splits(d);   // whichever form the tensors' layouts allow
-  if (d.dtype == KFAC_BF16) splits = std::max(splits, token_sizes(d) ? token_splits(d) : tc_splits(d));
+  int splits = simt_splits(d), keys;   // whichever form the tensors' layouts allow
+  if (d.dtype == KFAC_BF16)
+    splits = std::max(splits, token_sizes(d) ? token_splits(d, true, &keys) : tc_splits(d));
   const size_t fwd = part_bytes(d, splits);
   const size_t bwd = backward ? align_up((size_t)d.batch * d.heads * d.len_q * sizeof(float)) : 0;
   return std::max(fwd, bwd);
@@ -630,13 +669,13 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
   a.kv_len = kv_len;
   a.key_mask = key_mask;
   const bool tc = d->dtype == KFAC_BF16 && tc_forward_ok(a), token = tc && token_sizes(*d);
-  a.splits = token ? token_splits(*d) : tc ? tc_splits(*d) : simt_splits(*d);
-  a.part_keys = token_part_keys(*d);
+  a.splits = token ? token_splits(*d, kv_len != nullptr, &a.part_keys) : tc ? tc_splits(*d) : simt_splits(*d);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
   if (tc) {
     kfac_status e = token ? token_forward(a, stream) : tc_forward(a, stream);
-    if (e == KFAC_OK && a.splits > 1) e = launch_combine<__nv_bfloat16>(a, stream);
+    const bool joined = token && a.splits <= kTokenCluster;
+    if (e == KFAC_OK && a.splits > 1 && !joined) e = launch_combine<__nv_bfloat16>(a, stream);
     return e;
   }
   return d->dtype == KFAC_BF16 ? simt_forward<__nv_bfloat16>(a, stream) : simt_forward<float>(a, stream);

@@ -1,26 +1,27 @@
 // Cross attention of few query rows (bf16): single new tokens against long encoder
 // states.  rows = heads of a group x queries, 16 of them per block.
 //
-// Bound by memory: k and v are read once, at about 4 flop per byte and row.  A warp
-// takes 16 keys at a time straight from memory into the fragments of mma.sync
-// m16n8k16 - no shared memory, no barriers in the loop.  The order of channels within
-// a product is free as long as both operands agree, and so is the order of keys in
-// P V, so every lane loads whole 16-byte pieces:
-//   k: lane (g, t) = (lane / 4, lane % 4) takes key g (and 8 + g), channels
-//      32 c + 8 t .. + 7: two k-steps of S = q k^T;
-//   v: keys 2t, 2t + 1, 8 + 2t, 8 + 2t + 1 (the columns of S this lane holds),
-//      channels 64 c + 8 g .. + 7; pairs of keys interleave into eight n-tiles of P V.
-// P enters as two bf16 parts (high and remainder): the second product costs nothing
-// here and keeps P exact to 2^-17.
-// Blocks take fixed lengths of the key axis (many more than fit at once, so that
-// ragged lengths balance); parts are joined by the combine kernel.
+// Bound by memory: k and v are read once, at 2 flop per byte and row.  Each warp walks
+// 16 keys at a time through a ring of its own in shared memory (16-byte cp.async, two
+// steps ahead, no block-wide barrier): S = q k^T and O += P v by mma.sync m16n8k16 on
+// fragments that ldmatrix reads, rows swizzled so that eight rows of one 16-byte
+// column hit all banks.  Keys that are not permitted are filled with zeros, their
+// scores are -infinity.  P enters as two bf16 parts (high and remainder): the second
+// product costs nothing here and keeps P exact to 2^-17.
+//
+// The key axis is split.  Up to 8 parts are the blocks of one cluster, each taking its
+// share of the sequence's own length; they exchange maxima, sums and outputs through
+// distributed shared memory and the call is one launch.  More parts (few sequences,
+// long states) are fixed lengths of the axis, joined by the combine kernel.
 #include "attn.cuh"
+#include "tc_prims.cuh"
 
 namespace kfac {
 namespace attn {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kStages = 3;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -30,18 +31,30 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void ldm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldm4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 // (hi, lo) bf16 pairs of two fp32 values
 __device__ __forceinline__ void split2(float x, float y, uint32_t* hi, uint32_t* lo) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   const __nv_bfloat162 l = __floats2bfloat162_rn(x - __bfloat162float(h.x), y - __bfloat162float(h.y));
   *hi = *reinterpret_cast<const uint32_t*>(&h);
   *lo = *reinterpret_cast<const uint32_t*>(&l);
-}
-__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
-  uint4 v;   // read once: keep it out of L1
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
 }
 __device__ __forceinline__ float quad_max(float v) {
   v = fmaxf(v, __shfl_xor_sync(kFull, v, 1));
@@ -52,94 +65,129 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor_sync(kFull, v, 2);
 }
 
-// DC: 32-channel pieces (dim <= 32 DC), VC: 64-channel pieces.
-// grid: (16-row tiles x parts, kv_heads, batch); part s: keys [s, s + 1) x part_keys
-template <int DC>
+template <int DC> struct TokenCfg {            // dim <= 32 DC
+  static constexpr int CH = 4 * DC;            // 16-byte pieces per row
+  static constexpr int ROW = 64 * DC;          // bytes
+  static constexpr int TILE = 16 * ROW;        // 16 keys of k or of v
+  static constexpr int RING = kStages * 2 * TILE;   // per warp
+  static constexpr int OP = 32 * DC + 4;       // pitch of an output row (floats)
+  static constexpr size_t JOIN = sizeof(float) * (kTokenWarps + 1) * (16 * OP + 32);
+  static constexpr size_t SMEM = (size_t)kTokenWarps * RING > JOIN ? (size_t)kTokenWarps * RING : JOIN;
+  __device__ static uint32_t at(int row, int chunk) {
+    return (uint32_t)(row * ROW + ((chunk ^ (DC % 2 ? row >> 1 & 3 : row & 7)) << 4));
+  }
+};
+
+// grid: (16-row tiles x parts, kv_heads, batch).  kCluster: a tile's parts are one
+// cluster and share the sequence's length; otherwise part s takes keys
+// [s, s + 1) x part_keys.
+template <int DC, bool kCluster>
 __global__ void __launch_bounds__(kTokenWarps * 32)
 token_kernel(const __grid_constant__ Args a) {
-  constexpr int VC = (DC + 1) / 2;
-  __shared__ float so[kTokenWarps][16][32 * DC + 4];
-  __shared__ float sm[kTokenWarps][16], sl[kTokenWarps][16];
+  using C = TokenCfg<DC>;
+  extern __shared__ __align__(1024) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int split = (int)(blockIdx.x % a.splits), r0 = (int)(blockIdx.x / a.splits) * 16;
   const int hk = blockIdx.y, b = blockIdx.z;
   const int len = key_count(a, b);
-  const int first = split * a.part_keys, last = min(len, first + a.part_keys);
+  int first, last;
+  if (kCluster) {
+    const int blocks = (len + 15) / 16;
+    first = (int)((int64_t)blocks * split / a.splits) * 16;
+    last = min(len, (int)((int64_t)blocks * (split + 1) / a.splits) * 16);
+  } else {
+    first = split * a.part_keys;
+    last = min(len, first + a.part_keys);
+  }
   const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k) + b * a.ks[0] + hk * a.ks[2];
   const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + b * a.vs[0] + hk * a.vs[2];
+  const uint8_t* mp = a.key_mask ? a.key_mask + (int64_t)b * a.len_kv : nullptr;
+  const uint32_t ring = tc::smem_u32(smem) + warp * C::RING;
+  const int begin = first + 16 * warp, step = 16 * kTokenWarps;
 
-  uint4 kr[2][DC], vr[4][VC];
-  bool ok[4];
-  auto load_k = [&](int key0) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int c = 0; c < DC; ++c) {
-        const int key = key0 + 8 * i + g, d = 32 * c + 8 * t;
-        kr[i][c] = make_uint4(0, 0, 0, 0);
-        if (key < last && d < a.dim) kr[i][c] = load16(kp + key * a.ks[1] + d);
-      }
+  // permitted keys among the 16 from key0 (bit i), given this lane's mask byte
+  auto word = [&](int key0, uint8_t byte) {
+    const int n = last - key0;
+    const uint32_t w = n >= 16 ? 0xffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    return mp ? w & __ballot_sync(kFull, byte != 0) : w;
   };
-  auto load_v = [&](int key0) {
+  auto mask_byte = [&](int key0) -> uint8_t {
+    const int key = key0 + lane;
+    return mp && lane < 16 && key < last ? __ldg(mp + key) : (uint8_t)0;
+  };
+  auto fetch = [&](int key0, int stage, uint32_t w) {
+    const uint32_t ks = ring + stage * 2 * C::TILE, vs = ks + C::TILE;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = key0 + (i / 2) * 8 + 2 * t + i % 2;
-      ok[i] = key < last && (!a.key_mask || __ldg(a.key_mask + (int64_t)b * a.len_kv + key) != 0);
-#pragma unroll
-      for (int c = 0; c < VC; ++c) {
-        const int d = 64 * c + 8 * g;
-        vr[i][c] = make_uint4(0, 0, 0, 0);   // not permitted: whatever is there stays out
-        if (ok[i] && d < a.dim) vr[i][c] = load16(vp + key * a.vs[1] + d);
-      }
+    for (int i = 0; i < 2 * DC; ++i) {
+      const int e = lane + 32 * i, row = e / C::CH, c = e % C::CH;
+      const bool real = (w >> row & 1u) && 8 * c < a.dim;
+      copy16(ks + C::at(row, c), real ? kp + (key0 + row) * a.ks[1] + 8 * c : kp, real);
+      copy16(vs + C::at(row, c), real ? vp + (key0 + row) * a.vs[1] + 8 * c : vp, real);
     }
   };
 
-  int key0 = first + 16 * warp;
-  if (key0 < last) load_k(key0);
+  uint32_t words[kStages];
+#pragma unroll
+  for (int s = 0; s + 1 < kStages; ++s) {
+    const int key0 = begin + s * step;
+    words[s] = word(key0, mask_byte(key0));
+    if (key0 < last) fetch(key0, s, words[s]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  uint8_t byte = mask_byte(begin + (kStages - 1) * step);
+
   // rows g and g + 8 of q, as A fragments
-  uint4 qr[2][DC];
+  uint32_t qr[2 * DC][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = r0 + 8 * i + g;
     const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) +
                               (r < a.rows ? row_offset(a, a.qs, b, hk, r) : 0);
 #pragma unroll
-    for (int c = 0; c < DC; ++c) {
-      qr[i][c] = make_uint4(0, 0, 0, 0);
-      if (r < a.rows && 32 * c + 8 * t < a.dim)
-        qr[i][c] = *reinterpret_cast<const uint4*>(qp + 32 * c + 8 * t);
-    }
+    for (int kk = 0; kk < 2 * DC; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int d = 16 * kk + 8 * e + 2 * t;
+        qr[kk][2 * e + i] = r < a.rows && d < a.dim ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
+      }
   }
-  if (key0 < last) load_v(key0);
   const float c2 = a.scale * kLog2e;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[VC][8][4];
+  float o[C::CH][4];
 #pragma unroll
-  for (int c = 0; c < VC; ++c)
+  for (int c = 0; c < C::CH; ++c)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[c][j][e] = 0.f;
+    for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
 
-  for (; key0 < last; key0 += 16 * kTokenWarps) {
-    const int next = key0 + 16 * kTokenWarps;
+  int stage = 0;
+  for (int key0 = begin; key0 < last; key0 += step) {
+    // the stage that the previous step has read takes the keys two steps ahead
+    const int ahead = key0 + (kStages - 1) * step;
+    words[kStages - 1] = word(ahead, byte);
+    byte = mask_byte(ahead + step);
+    __syncwarp();
+    if (ahead < last) fetch(ahead, stage == 0 ? kStages - 1 : stage - 1, words[kStages - 1]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    __syncwarp();
+    const uint32_t ks = ring + stage * 2 * C::TILE, vs = ks + C::TILE, w = words[0];
     float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int c = 0; c < DC; ++c)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mma16816(s[i], qr[0][c].x, qr[1][c].x, qr[0][c].y, qr[1][c].y, kr[i][c].x, kr[i][c].y);
-        mma16816(s[i], qr[0][c].z, qr[1][c].z, qr[0][c].w, qr[1][c].w, kr[i][c].z, kr[i][c].w);
-      }
-    if (next < last) load_k(next);
+    for (int kk = 0; kk < 2 * DC; ++kk) {
+      uint32_t f[4];
+      ldm4(ks + C::at((lane / 16) * 8 + lane % 8, 2 * kk + lane / 8 % 2), f);
+      mma16816(s[0], qr[kk][0], qr[kk][1], qr[kk][2], qr[kk][3], f[0], f[1]);
+      mma16816(s[1], qr[kk][0], qr[kk][1], qr[kk][2], qr[kk][3], f[2], f[3]);
+    }
     // rows g (e = 0, 1) and g + 8 (e = 2, 3); columns 8 i + 2 t + e % 2
-    float mn[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = ok[2 * i + e % 2] ? s[i][e] * c2 : -INFINITY;
+      for (int e = 0; e < 4; ++e)
+        s[i][e] = w >> (8 * i + 2 * t + e % 2) & 1u ? s[i][e] * c2 : -INFINITY;
+    float mn[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       mn[h] = fmaxf(m[h], quad_max(fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]),
@@ -151,12 +199,10 @@ token_kernel(const __grid_constant__ Args a) {
         m[h] = mn[h];
         l[h] *= f;
 #pragma unroll
-        for (int c = 0; c < VC; ++c)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[c][j][2 * h] *= f;
-            o[c][j][2 * h + 1] *= f;
-          }
+        for (int c = 0; c < C::CH; ++c) {
+          o[c][2 * h] *= f;
+          o[c][2 * h + 1] *= f;
+        }
       }
     }
     uint32_t hi[4], lo[4];   // A fragments: (row g, tile 0), (g + 8, 0), (g, 1), (g + 8, 1)
@@ -170,52 +216,50 @@ token_kernel(const __grid_constant__ Args a) {
         split2(x, y, &hi[2 * i + h], &lo[2 * i + h]);
       }
 #pragma unroll
-    for (int c = 0; c < VC; ++c) {
-      const uint32_t w[4][4] = {{vr[0][c].x, vr[0][c].y, vr[0][c].z, vr[0][c].w},
-                                {vr[1][c].x, vr[1][c].y, vr[1][c].z, vr[1][c].w},
-                                {vr[2][c].x, vr[2][c].y, vr[2][c].z, vr[2][c].w},
-                                {vr[3][c].x, vr[3][c].y, vr[3][c].z, vr[3][c].w}};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = j % 2 ? 0x7632u : 0x5410u;
-        const uint32_t b0 = __byte_perm(w[0][j / 2], w[1][j / 2], sel);
-        const uint32_t b1 = __byte_perm(w[2][j / 2], w[3][j / 2], sel);
-        mma16816(o[c][j], hi[0], hi[1], hi[2], hi[3], b0, b1);
-        mma16816(o[c][j], lo[0], lo[1], lo[2], lo[3], b0, b1);
-      }
+    for (int c = 0; c < C::CH; c += 2) {
+      uint32_t f[4];
+      ldm4_t(vs + C::at(lane / 8 % 2 * 8 + lane % 8, c + lane / 16), f);
+      mma16816(o[c], hi[0], hi[1], hi[2], hi[3], f[0], f[1]);
+      mma16816(o[c + 1], hi[0], hi[1], hi[2], hi[3], f[2], f[3]);
+      mma16816(o[c], lo[0], lo[1], lo[2], lo[3], f[0], f[1]);
+      mma16816(o[c + 1], lo[0], lo[1], lo[2], lo[3], f[2], f[3]);
     }
-    if (next < last) load_v(next);
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) words[i] = words[i + 1];
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 
-  // join the warps: each row's largest maximum, sums rescaled to it
+  // join the warps (the rings are free): each row's largest maximum, sums and outputs
+  // rescaled to it, left in part [kTokenWarps]
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  constexpr int PART = 16 * C::OP + 32;   // floats: rows, then 16 maxima and 16 sums
+  float* parts = reinterpret_cast<float*>(smem);
+  float* mine = parts + warp * PART;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] = quad_sum(l[h]);
     if (t == 0) {
-      sm[warp][g + 8 * h] = m[h];
-      sl[warp][g + 8 * h] = l[h];
+      mine[16 * C::OP + g + 8 * h] = m[h];
+      mine[16 * C::OP + 16 + g + 8 * h] = l[h];
     }
 #pragma unroll
-    for (int c = 0; c < VC; ++c)
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int d = 64 * c + 8 * (2 * t + e) + j;
-          if (d < 32 * DC) so[warp][g + 8 * h][d] = o[c][j][2 * h + e];
-        }
+    for (int c = 0; c < C::CH; ++c)
+      *reinterpret_cast<float2*>(mine + (g + 8 * h) * C::OP + 8 * c + 2 * t) =
+          make_float2(o[c][2 * h], o[c][2 * h + 1]);
   }
   __syncthreads();
   const int rows = min(16, a.rows - r0);
+  float* all = parts + kTokenWarps * PART;
   for (int r = warp; r < rows; r += kTokenWarps) {
     float top = -INFINITY, total = 0.f, f[kTokenWarps];
 #pragma unroll
-    for (int w = 0; w < kTokenWarps; ++w) top = fmaxf(top, sm[w][r]);
+    for (int w = 0; w < kTokenWarps; ++w) top = fmaxf(top, parts[w * PART + 16 * C::OP + r]);
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
     for (int w = 0; w < kTokenWarps; ++w) {
-      f[w] = exp2f(sm[w][r] - base);
-      total += f[w] * sl[w][r];
+      f[w] = exp2f(parts[w * PART + 16 * C::OP + r] - base);
+      total += f[w] * parts[w * PART + 16 * C::OP + 16 + r];
     }
     const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
     const float lse = total == 0.f ? -INFINITY : (base + log2f(total)) * kLn2;
@@ -225,27 +269,105 @@ token_kernel(const __grid_constant__ Args a) {
     for (int d = lane; d < a.dim; d += 32) {
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kTokenWarps; ++w) v = fmaf(f[w], so[w][r][d], v);
-      if (a.splits == 1) dst[d] = __float2bfloat16_rn(v * inv);
+      for (int w = 0; w < kTokenWarps; ++w) v = fmaf(f[w], parts[w * PART + r * C::OP + d], v);
+      if (kCluster) all[r * C::OP + d] = v;
+      else if (a.splits == 1) dst[d] = __float2bfloat16_rn(v * inv);
       else a.part_o[part * a.dim + d] = v * inv;
     }
     if (lane == 0) {
-      if (a.splits > 1) a.part_lse[part] = lse;
-      else if (a.lse) a.lse[row] = lse;
+      if (kCluster) {
+        all[16 * C::OP + r] = top;
+        all[16 * C::OP + 16 + r] = total;
+      } else if (a.splits > 1) {
+        a.part_lse[part] = lse;
+      } else if (a.lse) {
+        a.lse[row] = lse;
+      }
     }
   }
+  if (kCluster) {   // the parts' blocks share out the rows
+    tc::cluster_sync();
+    for (int r = split + a.splits * warp; r < rows; r += a.splits * kTokenWarps) {
+      const uint32_t stat = tc::smem_u32(all + 16 * C::OP + r);
+      float pm = -INFINITY, pl = 0.f;   // lane s: part s
+      if (lane < a.splits) {
+        uint32_t addr;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(stat), "r"(lane));
+        pm = ld_cluster(addr);
+        pl = ld_cluster(addr + 64);
+      }
+      float top = pm;
+#pragma unroll
+      for (int i = 4; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+      top = __shfl_sync(kFull, top, 0);
+      const float base = top == -INFINITY ? 0.f : top;
+      const float f = lane < a.splits ? exp2f(pm - base) : 0.f;
+      float total = f * pl;
+#pragma unroll
+      for (int i = 4; i; i >>= 1) total += __shfl_xor_sync(kFull, total, i);
+      total = __shfl_sync(kFull, total, 0);
+      const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+      float v[DC];
+#pragma unroll
+      for (int c = 0; c < DC; ++c) v[c] = 0.f;
+      for (int s = 0; s < a.splits; ++s) {
+        uint32_t addr;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(addr) : "r"(tc::smem_u32(all + r * C::OP + lane)), "r"(s));
+        const float w = __shfl_sync(kFull, f, s);
+#pragma unroll
+        for (int c = 0; c < DC; ++c)
+          if (32 * c + lane < a.dim) v[c] = fmaf(w, ld_cluster(addr + 128 * c), v[c]);
+      }
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row_offset(a, a.os, b, hk, r0 + r);
+#pragma unroll
+      for (int c = 0; c < DC; ++c)
+        if (32 * c + lane < a.dim) dst[32 * c + lane] = __float2bfloat16_rn(v[c] * inv);
+      if (a.lse && lane == 0)
+        a.lse[((int64_t)b * a.kv_heads + hk) * a.rows + r0 + r] =
+            total == 0.f ? -INFINITY : (base + log2f(total)) * kLn2;
+    }
+    tc::cluster_sync();   // no block leaves while its part is being read
+  }
+}
+
+template <int DC, bool kCluster>
+kfac_status launch_token(const Args& a, cudaStream_t st) {
+  using C = TokenCfg<DC>;
+  static const bool ok = cudaFuncSetAttribute(token_kernel<DC, kCluster>,
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              (int)C::SMEM) == cudaSuccess;
+  if (!ok) return KFAC_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(cdiv(a.rows, 16) * a.splits), a.kv_heads, a.batch);
+  cfg.blockDim = dim3(kTokenWarps * 32);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = a.splits;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = kCluster ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, token_kernel<DC, kCluster>, a);
+  count_launch();
+  return check_launch();
+}
+template <int DC>
+kfac_status dispatch_token(const Args& a, cudaStream_t st) {
+  return a.splits > 1 && a.splits <= kTokenCluster ? launch_token<DC, true>(a, st)
+                                                   : launch_token<DC, false>(a, st);
 }
 
 }  // namespace
 
 kfac_status token_forward(const Args& a, cudaStream_t st) {
-  const dim3 grid((unsigned)(cdiv(a.rows, 16) * a.splits), a.kv_heads, a.batch), block(kTokenWarps * 32);
-  if (a.dim <= 32) launch_pdl(token_kernel<1>, grid, block, 0, st, a);
-  else if (a.dim <= 64) launch_pdl(token_kernel<2>, grid, block, 0, st, a);
-  else if (a.dim <= 96) launch_pdl(token_kernel<3>, grid, block, 0, st, a);
-  else launch_pdl(token_kernel<4>, grid, block, 0, st, a);
-  count_launch();
-  return check_launch();
+  if (a.dim <= 32) return dispatch_token<1>(a, st);
+  if (a.dim <= 64) return dispatch_token<2>(a, st);
+  if (a.dim <= 96) return dispatch_token<3>(a, st);
+  return dispatch_token<4>(a, st);
 }
 
 }  // namespace attn

@@ -285,6 +285,15 @@ def test_attention(dtype, keys, b, nq, nk, h, kv, d):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys", ["all", "len", "mask"])
+@pytest.mark.parametrize("b,nq,nk,h,kv,d", [(1, 1, 4097, 1, 1, 64), (2, 5, 2500, 8, 2, 96),
+                                            (1, 40, 1999, 1, 1, 128), (40, 1, 700, 8, 8, 32)])
+def test_attention_few_rows_many_parts(dtype, keys, b, nq, nk, h, kv, d):
+    """Parts of the key axis: one, a cluster's, more than a cluster's."""
+    _check_attention(*_inputs(dtype, b, nq, nk, h, kv, d, keys), backward=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_without_queries_or_keys(dtype):
     q, k, v, g, *_ = _inputs(dtype, 2, 5, 7, 2, 2, 64, "all")
     out, lse = K.cross_attention(q, k[:, :0], v[:, :0])
