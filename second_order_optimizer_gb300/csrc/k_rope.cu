@@ -7,10 +7,12 @@
 //   copied (nothing to do in place).
 //
 // Bound by memory: 3 flop per loaded element.  One launch serves q and k.  A thread
-// keeps the cosines and sines of its VEC pairs in registers and applies them to up
-// to kHeads heads of its token, so a table row is read once per kHeads heads (from
-// L1/L2) and several 16-byte loads are in flight per thread.  VEC is the widest
-// vector (up to 16 bytes) that every address, stride and size allows.
+// keeps the cosines and sines of its VEC pairs in registers and applies them to
+// kHeads = 2 heads of its token: four 16-byte loads in flight at 64 registers.  VEC
+// is the widest vector (up to 16 bytes) that every address, stride and size allows.
+// 16384 tokens, 16 + 16 heads of 128 bf16 (269 MB): 48 us, 5.6 TB/s.  Heads per thread,
+// same case: 1: 52 us, 2: 49 us, 4: 66 us (registers leave too few blocks), 8: 101 us;
+// 128 threads a block, not 256: 48 us.
 // Arithmetic in fp32 whatever the type, one rounding at the store.
 #include "kfac_internal.cuh"
 
@@ -19,8 +21,8 @@
 namespace kfac {
 namespace {
 
-constexpr int kHeads = 4;        // heads per thread
-constexpr int kRopeThreads = 256;
+constexpr int kHeads = 2;        // heads per thread
+constexpr int kRopeThreads = 128;
 
 struct RopeArgs {
   const void* x[2];              // q, k
@@ -104,11 +106,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   const int64_t pos = a.positions ? (int64_t)a.positions[b * a.pos_stride + row] : a.offset + row;
   float cs[VEC], sn[VEC];
   if (pos >= 0 && pos < a.table_rows) {
+    constexpr int TV = VEC < 4 ? VEC : 4;   // 16-byte table loads where VEC covers them
+    using TVec = Vec<float, TV>;
     const float* t = a.table + pos * a.rotary + VEC * chunk;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-      cs[i] = __ldg(t + i);
-      sn[i] = __ldg(t + half + i) * a.sign;
+    for (int i = 0; i < VEC; i += TV) {
+      const TVec c = *reinterpret_cast<const TVec*>(t + i), s = *reinterpret_cast<const TVec*>(t + half + i);
+#pragma unroll
+      for (int e = 0; e < TV; ++e) {
+        cs[i + e] = c.v[e];
+        sn[i + e] = s.v[e] * a.sign;
+      }
     }
   } else {   // outside the table: no value to give
 #pragma unroll
@@ -187,6 +195,7 @@ bool vec_ok(const RopeArgs& a, int es, int vec, bool inter) {
   // vectors start at multiples of vec in each half (half layout) or in the rotated
   // part (interleaved, 2 vec per chunk), and at multiples of vec behind it
   if (a.rotary % (2 * vec) || a.dim % vec) return false;
+  if ((uintptr_t)a.table % (sizeof(float) * (vec < 4 ? vec : 4))) return false;
   (void)inter;
   const size_t bytes = (size_t)es * vec;
   for (int w = 0; w < 2; ++w) {
