@@ -22,7 +22,7 @@ struct Args {
   int64_t qs[3], ks[3], vs[3], os[3], dos[3], dqs[3], dks[3], dvs[3];
   int batch, len_q, len_kv, heads, kv_heads, group, dim, rows;
   float scale;
-  bool vec;                         // CUDA-core kernels: fp32 rows of whole 16 bytes
+  bool vec;                         // CUDA-core kernels: rows of whole 16-byte pieces
   int splits;                       // parts of the key axis (1: outputs written directly)
   int part_keys;                    // token kernel, more parts than a cluster: keys per part
   float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised

@@ -294,25 +294,37 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ar
   if (a.lse && lane == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
 }
 
-// delta[b][h][i] = sum_d dout out, in fp32.  One warp per row.
-template <typename T>
+// delta[b][h][i] = sum_d dout out, in fp32.  L lanes per row (L divides 32), each taking
+// pieces of 16 bytes (vec) or one channel at a time.
+template <typename T, int L>
 __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Args a) {
   pdl_wait();
   pdl_trigger();
+  constexpr int V = 16 / (int)sizeof(T);
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
-  const int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= n) return;
-  const int i = (int)(row % a.len_q);
-  const int64_t bh = row / a.len_q;
-  const int h = (int)(bh % a.heads), b = (int)(bh / a.heads);
-  const T* o = static_cast<const T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
-  const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + i * a.dos[1] + h * a.dos[2];
+  const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int lane = threadIdx.x % L;
   float s = 0.f;
-  for (int d = lane; d < a.dim; d += 32) s = fmaf(to_f32<T>(o[d]), to_f32<T>(g[d]), s);
+  if (row < n) {
+    const int i = (int)(row % a.len_q);
+    const int64_t bh = row / a.len_q;
+    const int h = (int)(bh % a.heads), b = (int)(bh / a.heads);
+    const T* o = static_cast<const T*>(a.o) + b * a.os[0] + i * a.os[1] + h * a.os[2];
+    const T* g = static_cast<const T*>(a.dout) + b * a.dos[0] + i * a.dos[1] + h * a.dos[2];
+    if (a.vec) {
+      struct alignas(16) P { T v[V]; };
+      for (int d = V * lane; d < a.dim; d += V * L) {
+        const P x = *reinterpret_cast<const P*>(o + d), y = *reinterpret_cast<const P*>(g + d);
 #pragma unroll
-  for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  if (lane == 0) a.delta[row] = s;
+        for (int e = 0; e < V; ++e) s = fmaf(to_f32<T>(x.v[e]), to_f32<T>(y.v[e]), s);
+      }
+    } else {
+      for (int d = lane; d < a.dim; d += L) s = fmaf(to_f32<T>(o[d]), to_f32<T>(g[d]), s);
+    }
+  }
+#pragma unroll
+  for (int k = L / 2; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+  if (lane == 0 && row < n) a.delta[row] = s;
 }
 
 // P and dS of one tile (64 rows x 64 keys) into Ps (null: not wanted) and Ss.
@@ -470,17 +482,17 @@ kfac_status launch_combine(const Args& a, cudaStream_t st) {
   return check_launch();
 }
 
-// fp32 rows that start at multiples of 16 bytes and hold whole ones.
-bool vec_rows(const void* p, const int64_t* s, int rows, int heads, int batch, int dim) {
-  return dim % 4 == 0 && (uintptr_t)p % 16 == 0 && (batch <= 1 || s[0] % 4 == 0) &&
-         (rows <= 1 || s[1] % 4 == 0) && (heads <= 1 || s[2] % 4 == 0);
+// Rows that start at multiples of 16 bytes (v elements) and hold whole ones.
+bool vec_rows(const void* p, const int64_t* s, int rows, int heads, int batch, int dim, int v) {
+  return dim % v == 0 && (uintptr_t)p % 16 == 0 && (batch <= 1 || s[0] % v == 0) &&
+         (rows <= 1 || s[1] % v == 0) && (heads <= 1 || s[2] % v == 0);
 }
 
 template <typename T>
 kfac_status simt_forward(Args a, cudaStream_t st) {
-  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim) &&
-          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim) &&
-          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim);
+  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
+          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
+          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   kfac_status e;
   if (a.rows <= 16)
     e = a.dim <= 64 ? launch_simt_forward<T, 16, 64>(a, st) : launch_simt_forward<T, 16, 128>(a, st);
@@ -503,17 +515,20 @@ kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
 
 template <typename T>
 kfac_status backward(Args a, cudaStream_t st) {
-  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim) &&
-          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim) &&
-          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim) &&
-          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim);
+  constexpr int V = 16 / (int)sizeof(T);
+  a.vec = vec_rows(a.o, a.os, a.len_q, a.heads, a.batch, a.dim, V) &&
+          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, V);
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
   if (n > 0) {
-    launch_pdl(delta_kernel<T>, dim3((unsigned)cdiv(n, 8)), dim3(256), 0, st, a);
+    launch_pdl(delta_kernel<T, 8>, dim3((unsigned)cdiv(n, 32)), dim3(256), 0, st, a);
     count_launch();
     if (kfac_status e = check_launch()) return e;
   }
   if (sizeof(T) == 2 && tc_backward_ok(a)) return tc_backward(a, st);
+  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
+          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
+          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
+          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   return a.dim <= 64 ? launch_simt_backward<T, 64>(a, st) : launch_simt_backward<T, 128>(a, st);
 }
 

@@ -44,6 +44,36 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Two fp32 operations in one instruction, on pairs of registers.
+struct F2 { uint64_t v; };
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ F2 f2(uint32_t x, uint32_t y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(x), "r"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack(F2 a, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&p);
@@ -356,7 +386,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         }
       }
       const float base = m == -INFINITY ? 0.f : m * c2;   // nothing permitted so far
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const F2 cc2 = f2(c2, c2), nb2 = f2(-base, -base);
+      F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t p[32];
@@ -365,15 +396,18 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
             const int c = 2 * half + cc;
-            const float x = ex2(fmaf(__uint_as_float(r[c][i]), c2, -base));
-            const float y = ex2(fmaf(__uint_as_float(r[c][i + 1]), c2, -base));
-            sum[i % 4] += x;
-            sum[i % 4 + 1] += y;
+            float x, y;
+            unpack(fma2(f2(r[c][i], r[c][i + 1]), cc2, nb2), &x, &y);
+            x = ex2(x);
+            y = ex2(y);
+            sum[i / 2 % 2] = add2(sum[i / 2 % 2], f2(x, y));
             p[16 * cc + i / 2] = pack_bf16(x, y);
           }
         tc::tmem_st32(ts + 32 * half, p);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float l0, l1;
+      unpack(add2(sum[0], sum[1]), &l0, &l1);
+      l += l0 + l1;
       tc::tmem_st_wait();
       tc::tc_fence_before();
       __syncwarp();
@@ -476,16 +510,17 @@ struct BwdMaps {
 };
 
 template <int NC>
-__device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint8_t* smem,
+__device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int tile, int hk, int b, uint8_t* smem,
                                           uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
   using C = BwdCfg<NC>;
   uint8_t *Ks = smem, *Vs = Ks + C::TILE, *Qs = Vs + C::TILE, *Gs = Qs + 3 * C::TILE;
   float* stats = reinterpret_cast<float*>(Gs + 2 * C::TILE);   // [2][lse 128, delta 128]
   uint64_t *kv_full = bars, *q_full = bars + 1, *q_empty = bars + 4, *g_full = bars + 7,
            *g_empty = bars + 9, *s_full = bars + 11, *dp_full = bars + 12, *p_ready = bars + 13,
-           *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19;
+           *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19,
+           *kv_ready = bars + 20;
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-  const int k0 = (int)blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
+  const int k0 = tile * BT;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int n = k0 < len ? a.group * qtiles : 0;
@@ -530,7 +565,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
         tc::tc_fence_after();
         return ok;
       };
-      bool ok = wait(kv_full, 0) && wait(&q_full[0], 0);
+      bool ok = wait(kv_ready, 0) && wait(&q_full[0], 0);
       if (ok) {
         mma_scores(leader, tmem, Ks, Qs, ksteps);
         tc::umma_commit_by(leader, s_full);
@@ -555,7 +590,24 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       }
       if (ok) tc::umma_commit_by(leader, done);
     }
-  } else if (warp == 2) {  // ---------------------------------------------- row statistics
+  } else if (warp == 2) {  // ------------------------- keys not permitted, row statistics
+    // Their rows of K and V become zero, so that whatever stands there cannot make an
+    // exception of its lane; the lane's own results are dropped at the end.
+    if (n > 0) {
+      uint32_t w[4];
+      MaskWalk mask;
+      mask.fetch(a, b, len, k0);
+      mask.words(a, len, k0, w);
+      if (__all_sync(kFull, tc::mbar_wait(kv_full, 0, abort_flag))) {
+        if (!all_ok(w)) {
+          zero_rows<NC>(Ks, w);
+          zero_rows<NC>(Vs, w);
+        }
+        if (lane == 0) tc::mbar_arrive(kv_ready);
+      } else {
+        give_up(113);
+      }
+    }
     for (int i = 0; i < n; ++i) {
       const int h = hk * a.group + i / qtiles, row = i % qtiles * BT, s = i % 2;
       if (!__all_sync(kFull, tc::mbar_wait(&st_empty[s], ((uint32_t)(i / 2) & 1u) ^ 1u, abort_flag))) {
@@ -568,10 +620,10 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       for (int c = 0; c < 4; ++c) {
         const int r = 32 * c + lane;
         const bool in = row + r < a.len_q;
-        // past the queries, or a query without keys: P = exp(S - inf) = 0
-        float z = in ? __ldg(a.lse_in + at + r) * kLog2e : INFINITY;
-        dst[r] = z == -INFINITY ? INFINITY : z;
-        dst[BT + r] = in ? a.delta[at + r] : 0.f;
+        // negated; past the queries, or a query without keys: P = exp(S - inf) = 0
+        const float z = in ? -__ldg(a.lse_in + at + r) * kLog2e : -INFINITY;
+        dst[r] = z == INFINITY ? -INFINITY : z;
+        dst[BT + r] = in ? -a.delta[at + r] : 0.f;
       }
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&st_full[s]);
@@ -585,6 +637,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
     const int key = k0 + 32 * (warp % 4) + lane;
     const bool mine = key_ok(a, b, len, key);
     const float c2 = a.scale * kLog2e;
+    const F2 cc2 = f2(c2, c2);
     bool ok = true;
     for (int i = 0; i < n; ++i) {
       const uint32_t ph = (uint32_t)i & 1u;
@@ -601,19 +654,22 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       tc::tmem_ld_wait();
       tc::tmem_ld_use(r[0]);
       tc::tmem_ld_use(r[1]);
-      float p[64];
+      F2 p[32];
       uint32_t u[32];
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 z = lse[c];
-        const float zz[4] = {z.x, z.y, z.z, z.w};
+      for (int c = 0; c < 32; c += 2) {
+        const float4 z = lse[c / 2];   // negated
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = ex2(fmaf(__uint_as_float(r[c / 8][c % 8 * 4 + e]), c2, -zz[e]));
-          p[4 * c + e] = mine ? x : 0.f;
+        for (int e = 0; e < 2; ++e) {
+          const int i2 = 2 * (c + e);
+          float x, y;
+          unpack(fma2(f2(r[i2 / 32][i2 % 32], r[i2 / 32][i2 % 32 + 1]), cc2, e ? f2(z.z, z.w) : f2(z.x, z.y)),
+                 &x, &y);
+          x = ex2(x);
+          y = ex2(y);
+          p[c + e] = f2(x, y);
+          u[c + e] = pack_bf16(x, y);
         }
-        u[2 * c] = pack_bf16(p[4 * c], p[4 * c + 1]);
-        u[2 * c + 1] = pack_bf16(p[4 * c + 2], p[4 * c + 3]);
       }
       tc::tmem_st32(ts, u);
       tc::tmem_st_wait();
@@ -629,15 +685,16 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
       tc::tmem_ld_use(r[0]);
       tc::tmem_ld_use(r[1]);
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const float4 z = delta[c];
-        const float zz[4] = {z.x, z.y, z.z, z.w};
-        float d[4];
+      for (int c = 0; c < 32; c += 2) {
+        const float4 z = delta[c / 2];   // negated
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          d[e] = mine ? p[4 * c + e] * (__uint_as_float(r[c / 8][c % 8 * 4 + e]) - zz[e]) : 0.f;
-        u[2 * c] = pack_bf16(d[0], d[1]);
-        u[2 * c + 1] = pack_bf16(d[2], d[3]);
+        for (int e = 0; e < 2; ++e) {
+          const int i2 = 2 * (c + e);
+          float x, y;
+          unpack(mul2(p[c + e], add2(f2(r[i2 / 32][i2 % 32], r[i2 / 32][i2 % 32 + 1]),
+                                     e ? f2(z.z, z.w) : f2(z.x, z.y))), &x, &y);
+          u[c + e] = pack_bf16(x, y);
+        }
       }
       tc::tmem_st32(td, u);
       tc::tmem_st_wait();
@@ -669,7 +726,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, uint
 }
 
 template <int NC>
-__device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int tile, uint8_t* smem,
+__device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int tile, int hk, int b, uint8_t* smem,
                                          uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
   using C = BwdCfg<NC>;
   uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
@@ -679,7 +736,6 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   uint4* words = reinterpret_cast<uint4*>(bars + 28);   // [3] permitted keys of a tile
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
-  const int hk = blockIdx.y, b = blockIdx.z;
   const int h = hk * a.group + tile / qtiles, q0 = tile % qtiles * BT;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int n = (len + BT - 1) / BT;
@@ -785,6 +841,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     if (lse == -INFINITY) lse = INFINITY;   // no permitted key: P = 0
     const float delta = in ? a.delta[row] : 0.f;
     const float c2 = a.scale * kLog2e;
+    const F2 cc2 = f2(c2, c2), nl2 = f2(-lse, -lse), nd2 = f2(-delta, -delta);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       ok = __all_sync(kFull, tc::mbar_wait(&s_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag) &&
@@ -806,9 +863,13 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       tc::tmem_ld_wait();
       tc::tmem_ld_use(r[0]);
       tc::tmem_ld_use(r[1]);
-      float p[64];
+      F2 p[32];
 #pragma unroll
-      for (int c = 0; c < 64; ++c) p[c] = ex2(fmaf(__uint_as_float(r[c / 32][c % 32]), c2, -lse));
+      for (int c = 0; c < 32; ++c) {
+        float x, y;
+        unpack(fma2(f2(r[c / 16][2 * c % 32], r[c / 16][2 * c % 32 + 1]), cc2, nl2), &x, &y);
+        p[c] = f2(ex2(x), ex2(y));
+      }
       ok = __all_sync(kFull, tc::mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag));
       if (!ok) break;
       tc::tc_fence_after();
@@ -817,16 +878,20 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       tc::tmem_ld_wait();
       tc::tmem_ld_use(r[0]);
       tc::tmem_ld_use(r[1]);
-#pragma unroll
-      for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(r[c / 32][c % 32]) - delta;
-      if (!all_ok(w)) {
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (!((half ? w[2 + c / 32] : w[c / 32]) >> (c % 32) & 1u)) p[c] = 0.f;
-      }
       uint32_t u[32];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) u[c] = pack_bf16(p[2 * c], p[2 * c + 1]);
+      for (int c = 0; c < 32; ++c) {
+        float x, y;
+        unpack(mul2(p[c], add2(f2(r[c / 16][2 * c % 32], r[c / 16][2 * c % 32 + 1]), nd2)), &x, &y);
+        u[c] = pack_bf16(x, y);
+      }
+      if (!all_ok(w)) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const uint32_t bits = (half ? w[2 + c / 16] : w[c / 16]) >> (2 * c % 32);
+          u[c] &= (bits & 1u ? 0xffffu : 0u) | (bits & 2u ? 0xffff0000u : 0u);
+        }
+      }
       tc::tmem_st32(td, u);
       tc::tmem_st_wait();
       tc::tc_fence_before();
@@ -850,7 +915,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   }
 }
 
-// grid: (key tiles + group x query tiles, kv_heads, batch)
+// grid: every dK/dV block, then every dQ block: the longer ones start first.
 template <int NC>
 __global__ void __launch_bounds__(kTcThreads, 1)
 tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMaps mp) {
@@ -860,8 +925,11 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBwdBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0);
-  const int key_tiles = (a.len_kv + BT - 1) / BT;
-  const bool dkv = (int)blockIdx.x < key_tiles;
+  const int key_tiles = (a.len_kv + BT - 1) / BT, q_tiles = a.group * ((a.len_q + BT - 1) / BT);
+  const int pairs = a.kv_heads * a.batch;
+  const bool dkv = (int)blockIdx.x < key_tiles * pairs;
+  const int id = dkv ? (int)blockIdx.x : (int)blockIdx.x - key_tiles * pairs;
+  const int tile = id % (dkv ? key_tiles : q_tiles), pair = id / (dkv ? key_tiles : q_tiles);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBwdBars; ++i) {
       // 13: p_ready, 14: ds_ready (one arrival per warp of the two groups);
@@ -882,8 +950,8 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
-  if (dkv) dkv_block<NC>(a, mp, smem, bars, abort_flag, tmem);
-  else dq_block<NC>(a, mp, (int)blockIdx.x - key_tiles, smem, bars, abort_flag, tmem);
+  if (dkv) dkv_block<NC>(a, mp, tile, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
+  else dq_block<NC>(a, mp, tile, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
   __syncthreads();
   if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
@@ -948,7 +1016,9 @@ kfac_status launch_tc_backward(const Args& a, cudaStream_t st) {
       !make_map(&m.v, &m.xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&m.g, &m.xg, a.dout, a.dos, a.dim, a.len_q, a.heads, a.batch))
     return KFAC_ERR_CUDA;
-  const dim3 grid((unsigned)(cdiv(a.len_kv, BT) + a.group * cdiv(a.len_q, BT)), a.kv_heads, a.batch);
+  const int64_t blocks = (cdiv(a.len_kv, BT) + a.group * cdiv(a.len_q, BT)) * a.kv_heads * a.batch;
+  if (blocks > INT32_MAX) return KFAC_ERR_INVALID_ARG;
+  const dim3 grid((unsigned)blocks);
   launch_pdl(tc_backward_kernel<NC>, grid, dim3(kTcThreads), C::SMEM, st, a, m);
   count_launch();
   return check_launch();
