@@ -44,6 +44,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Two fp32 operations in one instruction, on pairs of registers.
 struct F2 { uint64_t v; };
 __device__ __forceinline__ F2 f2(float x, float y) {
@@ -277,7 +282,6 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(102);
-        tc::tc_fence_after();
         return ok;
       };
       bool ok = wait(&k_full[0], 0);
@@ -292,6 +296,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         if (!(ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u))) break;
         for (int t = 0; t < nt; ++t) {
           if (!(ok = wait(&p_ready[t], (uint32_t)j & 1u))) break;
+          tc::tc_fence_after();
           mma_values(leader, tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
           if (t == nt - 1) tc::umma_commit_by(leader, &v_empty[s]);
           if (j == n - 1) tc::umma_commit_by(leader, &o_full[t]);
@@ -365,9 +370,10 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       }
       float top[4] = {m, m, m, m};
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
+      for (int i = 0; i < 32; i += 2)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) top[c] = fmaxf(top[c], __uint_as_float(r[c][i]));
+        for (int c = 0; c < 4; ++c)
+          top[c] = max3(top[c], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
       const float grown = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
       if (j == 0) {
         m = grown;
@@ -562,7 +568,6 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(112);
-        tc::tc_fence_after();
         return ok;
       };
       bool ok = wait(kv_ready, 0) && wait(&q_full[0], 0);
@@ -577,6 +582,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         mma_scores(leader, tmem + 128, Vs, Gs + sg * C::TILE, ksteps);
         tc::umma_commit_by(leader, dp_full);
         if (!(ok = wait(p_ready, ph))) break;
+        tc::tc_fence_after();
         mma_values(leader, tmem + 256, tmem, 64, Gs + sg * C::TILE, idesc, i > 0);
         tc::umma_commit_by(leader, &g_empty[sg]);
         if (i + 1 < n) {
@@ -585,6 +591,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
           tc::umma_commit_by(leader, s_full);
         }
         if (!(ok = wait(ds_ready, ph))) break;
+        tc::tc_fence_after();
         mma_values(leader, tmem + 256 + 64 * NC, tmem + 128, 64, Qs + sq * C::TILE, idesc, i > 0);
         tc::umma_commit_by(leader, &q_empty[sq]);
       }
@@ -776,7 +783,6 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool ok = __all_sync(kFull, tc::mbar_wait(bar, parity, abort_flag));
         if (!ok) give_up(122);
-        tc::tc_fence_after();
         return ok;
       };
       auto scores = [&](int j) {
@@ -798,6 +804,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n && !(ok = scores(j + 1))) break;
         if (!(ok = wait(ds_ready, (uint32_t)j & 1u))) break;
+        tc::tc_fence_after();
         mma_values(leader, tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
         tc::umma_commit_by(leader, &k_empty[j % 3]);
         if (j + 1 == n) tc::umma_commit_by(leader, done);
