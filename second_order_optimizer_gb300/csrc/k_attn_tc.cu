@@ -26,8 +26,11 @@ namespace {
 
 constexpr int kTcThreads = 384;
 constexpr int BT = 128;                    // rows of every tile
-// Registers per thread: 384 x 168 at launch; the score warps hold whole rows of S.
-constexpr int kRegsLaunch = 168, kRegsOther = 72, kRegsRow = 216;
+// Registers per thread: 384 x 168 at launch.  The forward kernel's score warps hold rows
+// of 128 scores, the others 16 descriptors of an unrolled product (a spill in the
+// issuing warp costs an L2 latency: shared memory leaves L1 no room).  The backward
+// kernel's rows of 64 fit the launch's share.
+constexpr int kRegsLaunch = 168, kRegsOther = 104, kRegsRow = 200;
 static_assert(128 * kRegsOther + 256 * kRegsRow <= kTcThreads * kRegsLaunch, "register shares");
 constexpr int kChunk = BT * 128;           // bytes of a 128-row, 64-channel chunk
 constexpr uint32_t kFull = 0xffffffffu;
@@ -536,7 +539,6 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
   };
   if (warp < 4) {
-  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
       tc::mbar_expect_tx(kv_full, 2 * C::TILE);
@@ -637,7 +639,6 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     }
   }
   } else {  // ----------------------------------------------- P^T and dS^T
-    tc::regs_inc<kRegsRow>();
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
     const uint32_t ts = tmem + lanes + 64 * half, td = ts + 128;
@@ -752,7 +753,6 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
   };
   if (warp < 4) {
-  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // ----------------------------------------- TMA producer
       tc::mbar_expect_tx(qg_full, 2 * C::TILE);
@@ -837,7 +837,6 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     }
   }
   } else {  // -------------------------------------------------------- dS
-    tc::regs_inc<kRegsRow>();
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
     const uint32_t td = tmem + lanes + 256 + 64 * half;
