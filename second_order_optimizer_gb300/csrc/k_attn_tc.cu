@@ -26,12 +26,6 @@ namespace {
 
 constexpr int kTcThreads = 384;
 constexpr int BT = 128;                    // rows of every tile
-// Registers per thread: 384 x 168 at launch.  The forward kernel's score warps hold rows
-// of 128 scores, the others 16 descriptors of an unrolled product (a spill in the
-// issuing warp costs an L2 latency: shared memory leaves L1 no room).  The backward
-// kernel's rows of 64 fit the launch's share.
-constexpr int kRegsLaunch = 168, kRegsOther = 104, kRegsRow = 200;
-static_assert(128 * kRegsOther + 256 * kRegsRow <= kTcThreads * kRegsLaunch, "register shares");
 constexpr int kChunk = BT * 128;           // bytes of a 128-row, 64-channel chunk
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr float kNaN = __builtin_nanf("");
@@ -160,16 +154,17 @@ __device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, const ui
     if (kk < ksteps) tc::umma_f16_by(leader, d, da + off, db + off, idesc, kk > 0);
   }
 }
-// D[128 x n] (+)= A[128 x 128] (TMEM, bf16; its second 64 columns of k start `half`
-// TMEM columns after the first) . B, B the [128 x n] tile (rows = k).
-__device__ __forceinline__ void mma_values(uint32_t leader, uint32_t d, uint32_t a, uint32_t half, const uint8_t* b,
+// D[128 x n] (+)= A[128 x 64] (TMEM, bf16) . B, 64 rows (k) of n channels in shared
+// memory.
+__device__ __forceinline__ void mma_values(uint32_t leader, uint32_t d, uint32_t a, const uint8_t* b,
                                            uint32_t idesc, bool accumulate) {
   const uint64_t db = tc::sdesc_mnmajor_sw128(tc::smem_u32(b), kChunk);
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)   // 16 k: two groups of eight 128-byte rows
-    tc::umma_f16_ts_by(leader, d, a + (kk < 4 ? 0u : half) + (uint32_t)(kk % 4) * 8, db + (kk * 2048 >> 4),
-                    idesc, accumulate || kk > 0);
+  for (int kk = 0; kk < 4; ++kk)   // 16 k: two groups of eight 128-byte rows
+    tc::umma_f16_ts_by(leader, d, a + (uint32_t)kk * 8, db + (kk * 2048 >> 4), idesc,
+                       accumulate || kk > 0);
 }
+constexpr int kHalf = 64 * 128;   // bytes from a tile's row 0 to its row 64
 
 // ------------------------------------------------------------------------- forward
 //
@@ -177,16 +172,21 @@ __device__ __forceinline__ void mma_values(uint32_t leader, uint32_t d, uint32_t
 //   S_t = Q_t K^T          128 x 128 x dim, TMEM columns [128 t, 128 t + 128)
 //   P_t = exp(S_t - m_t)   one thread per row: no shuffles for the maximum or the sum
 //   O_t += P_t V           128 x dim x 128, TMEM columns [256 + 64 NC t, ...)
-// Two tiles so that one's exponentials run under the other's products.  m_t is the
-// row's reference maximum: it moves (and O_t, l_t are rescaled) only when the true
-// maximum has grown past it by more than 2^8, which changes no result (P <= 2^8 fits
-// bf16 as well as P <= 1) and leaves the rescaling out of almost every tile.
+// Two tiles so that one's exponentials run under the other's products.  The chain of a
+// tile - S, exponentials, P V, S - is what bounds the kernel, so it is kept short: P is
+// handed over in halves of 64 keys, and a half's exponentials do not wait for its
+// maximum.  They are taken against the row's reference maximum m_t so far; only when
+// the half's own maximum, found alongside, has grown past it are they taken again and
+// O_t, l_t rescaled: by more than 2^8 in a tile's first half, where O_t is at rest,
+// 2^90 in its second, where the products of the first must first end.  A reference
+// that lags changes no result: P and the sums are floating point (P <= 2^90, sums of
+// at most 2^30 of them).
 template <int NC> struct FwdCfg {
   static constexpr int TILE = NC * kChunk;
   static constexpr int STAGES = NC == 1 ? 3 : 2;
   static constexpr size_t SMEM = (size_t)(2 + 2 * STAGES) * TILE + 512;
 };
-constexpr float kGrow = 8.f;
+constexpr float kGrow0 = 8.f, kGrow1 = 90.f;
 
 template <int NC>
 __global__ void __launch_bounds__(kTcThreads, 1)
@@ -202,7 +202,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   uint64_t* bars = reinterpret_cast<uint64_t*>(Vs + ST * C::TILE);
   uint64_t *q_full = bars, *k_full = q_full + 2, *k_empty = k_full + ST, *v_full = k_empty + ST,
            *v_empty = v_full + ST, *v_ready = v_empty + ST, *w_full = v_ready + ST,
-           *s_full = w_full + ST, *p_ready = s_full + 2, *o_full = p_ready + 2;
+           *s_full = w_full + ST, *p_ready = s_full + 2 /* [2 t + half] */, *half_done = p_ready + 4,
+           *o_full = half_done + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint4* words = reinterpret_cast<uint4*>(tmem_slot + 4);   // [ST] permitted keys of a tile
@@ -211,7 +212,9 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     for (int t = 0; t < 2; ++t) {
       tc::mbar_init(&q_full[t], 1);
       tc::mbar_init(&s_full[t], 1);
-      tc::mbar_init(&p_ready[t], 4);
+      tc::mbar_init(&p_ready[2 * t], 4);
+      tc::mbar_init(&p_ready[2 * t + 1], 4);
+      tc::mbar_init(&half_done[t], 1);
       tc::mbar_init(&o_full[t], 1);
     }
     for (int s = 0; s < ST; ++s) {
@@ -251,7 +254,6 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   };
 
   if (warp < 4) {
-  tc::regs_dec<kRegsOther>();
   if (warp == 0) {
     if (lane == 0 && n > 0) {  // -------------------------------------- TMA producer
       tc::tma_prefetch_desc(&mq);
@@ -298,9 +300,14 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         const int s = j % ST, s1 = (j + 1) % ST;
         if (!(ok = wait(&v_ready[s], (uint32_t)(j / ST) & 1u))) break;
         for (int t = 0; t < nt; ++t) {
-          if (!(ok = wait(&p_ready[t], (uint32_t)j & 1u))) break;
-          tc::tc_fence_after();
-          mma_values(leader, tmem + 256 + 64 * NC * t, tmem + 128 * t, 32, Vs + s * C::TILE, idesc_o, j > 0);
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = wait(&p_ready[2 * t + half], (uint32_t)j & 1u))) break;
+            tc::tc_fence_after();
+            mma_values(leader, tmem + 256 + 64 * NC * t, tmem + 128 * t + 32 * half,
+                       Vs + s * C::TILE + half * kHalf, idesc_o, j > 0 || half > 0);
+            if (half == 0) tc::umma_commit_by(leader, &half_done[t]);
+          }
+          if (!ok) break;
           if (t == nt - 1) tc::umma_commit_by(leader, &v_empty[s]);
           if (j == n - 1) tc::umma_commit_by(leader, &o_full[t]);
           if (j + 1 < n) {
@@ -337,7 +344,6 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     }
   }
   } else {
-  tc::regs_inc<kRegsRow>();
   if ((warp - 4) / 4 < nt) {  // ---------------------------------- softmax, epilogue
     const int t = (warp - 4) / 4;
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
@@ -358,69 +364,75 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       } else {
         len_words(len, (t0 + j) * BT, w);
       }
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc::tmem_ld32_issue(ts + 32 * c, r[c]);
-      tc::tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tc::tmem_ld_use(r[c]);
-      if (!all_ok(w)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(w[c] >> i & 1u)) r[c][i] = 0xff800000u;   // -infinity
-      }
-      float top[4] = {m, m, m, m};
-#pragma unroll
-      for (int i = 0; i < 32; i += 2)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          top[c] = max3(top[c], __uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1]));
-      const float grown = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-      if (j == 0) {
-        m = grown;
-      } else if (__any_sync(kFull, (grown - m) * c2 > kGrow)) {
-        const float f = grown == m ? 1.f : ex2((m - grown) * c2);
-        m = grown;
-        l *= f;
-        for (int c = 0; c < ksteps * 16; c += 32) {
-          uint32_t o[32];
-          tc::tmem_ld32_issue(to + c, o);
-          tc::tmem_ld_wait();
-          tc::tmem_ld_use(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-          tc::tmem_st32(to + c, o);
-        }
-      }
-      const float base = m == -INFINITY ? 0.f : m * c2;   // nothing permitted so far
-      const F2 cc2 = f2(c2, c2), nb2 = f2(-base, -base);
-      F2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
+        uint32_t r[2][32];
+        auto load = [&]() {
+          tc::tmem_ld32_issue(ts + 64 * half, r[0]);
+          tc::tmem_ld32_issue(ts + 64 * half + 32, r[1]);
+          tc::tmem_ld_wait();
+          tc::tmem_ld_use(r[0]);
+          tc::tmem_ld_use(r[1]);
+          if ((w[2 * half] & w[2 * half + 1]) != kFull) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(w[2 * half + c] >> e & 1u)) r[c][e] = 0xff800000u;   // -infinity
+          }
+        };
         uint32_t p[32];
+        F2 sum[2];
+        float top[4];
+        auto exponentials = [&]() {
+          const float base = m == -INFINITY ? 0.f : m * c2;   // nothing permitted so far
+          const F2 cc2 = f2(c2, c2), nb2 = f2(-base, -base);
+          sum[0] = sum[1] = f2(0.f, 0.f);
+          top[0] = top[1] = top[2] = top[3] = m;
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc)
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const int c = 2 * half + cc;
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t u = r[e / 16][2 * e % 32], v = r[e / 16][2 * e % 32 + 1];
             float x, y;
-            unpack(fma2(f2(r[c][i], r[c][i + 1]), cc2, nb2), &x, &y);
+            unpack(fma2(f2(u, v), cc2, nb2), &x, &y);
+            top[e % 4] = max3(top[e % 4], __uint_as_float(u), __uint_as_float(v));
             x = ex2(x);
             y = ex2(y);
-            sum[i / 2 % 2] = add2(sum[i / 2 % 2], f2(x, y));
-            p[16 * cc + i / 2] = pack_bf16(x, y);
+            sum[e % 2] = add2(sum[e % 2], f2(x, y));
+            p[e] = pack_bf16(x, y);
           }
+        };
+        load();
+        exponentials();
+        const float grown = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        // (m = -infinity: any key counts as growth)
+        if (__any_sync(kFull, (grown - m) * c2 > (half ? kGrow1 : kGrow0))) {
+          if (half == 1) ok = __all_sync(kFull, tc::mbar_wait(&half_done[t], (uint32_t)j & 1u, abort_flag));
+          if (!ok) break;
+          tc::tc_fence_after();
+          const float f = grown == m ? 1.f : ex2((m - grown) * c2);
+          m = grown;
+          l *= f;
+          for (int c = 0; c < ksteps * 16 && j + half > 0; c += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32_issue(to + c, o);
+            tc::tmem_ld_wait();
+            tc::tmem_ld_use(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tc::tmem_st32(to + c, o);
+          }
+          load();
+          exponentials();
+        }
         tc::tmem_st32(ts + 32 * half, p);
+        float l0, l1;
+        unpack(add2(sum[0], sum[1]), &l0, &l1);
+        l += l0 + l1;
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&p_ready[2 * t + half]);
       }
-      float l0, l1;
-      unpack(add2(sum[0], sum[1]), &l0, &l1);
-      l += l0 + l1;
-      tc::tmem_st_wait();
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&p_ready[t]);
     }
     if (n > 0 && ok) ok = __all_sync(kFull, tc::mbar_wait(&o_full[t], 0, abort_flag));
     if (!ok) give_up(103);
@@ -585,7 +597,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         tc::umma_commit_by(leader, dp_full);
         if (!(ok = wait(p_ready, ph))) break;
         tc::tc_fence_after();
-        mma_values(leader, tmem + 256, tmem, 64, Gs + sg * C::TILE, idesc, i > 0);
+        for (int u = 0; u < 2; ++u)
+          mma_values(leader, tmem + 256, tmem + 64 * u, Gs + sg * C::TILE + u * kHalf, idesc, i > 0 || u > 0);
         tc::umma_commit_by(leader, &g_empty[sg]);
         if (i + 1 < n) {
           if (!(ok = wait(&q_full[s1], (uint32_t)((i + 1) / 3) & 1u))) break;
@@ -594,7 +607,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         }
         if (!(ok = wait(ds_ready, ph))) break;
         tc::tc_fence_after();
-        mma_values(leader, tmem + 256 + 64 * NC, tmem + 128, 64, Qs + sq * C::TILE, idesc, i > 0);
+        for (int u = 0; u < 2; ++u)
+          mma_values(leader, tmem + 256 + 64 * NC, tmem + 128 + 64 * u, Qs + sq * C::TILE + u * kHalf, idesc, i > 0 || u > 0);
         tc::umma_commit_by(leader, &q_empty[sq]);
       }
       if (ok) tc::umma_commit_by(leader, done);
@@ -805,7 +819,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         if (j + 1 < n && !(ok = scores(j + 1))) break;
         if (!(ok = wait(ds_ready, (uint32_t)j & 1u))) break;
         tc::tc_fence_after();
-        mma_values(leader, tmem + 384, tmem + 256, 64, Ks + j % 3 * C::TILE, idesc, j > 0);
+        for (int u = 0; u < 2; ++u)
+          mma_values(leader, tmem + 384, tmem + 256 + 64 * u, Ks + j % 3 * C::TILE + u * kHalf, idesc, j > 0 || u > 0);
         tc::umma_commit_by(leader, &k_empty[j % 3]);
         if (j + 1 == n) tc::umma_commit_by(leader, done);
         else ok = grads(j + 1);

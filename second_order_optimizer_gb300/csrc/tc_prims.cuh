@@ -410,16 +410,6 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// Registers of a warpgroup (four consecutive warps, all of them): given back to or
-// taken from what the block was launched with.  The shares of all warpgroups add up
-// to at most the launch's total, or the increase waits forever.
-template <int N> __device__ __forceinline__ void regs_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N> __device__ __forceinline__ void regs_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Round fp32 to the nearest TF32 (10 explicit mantissa bits), kept in fp32 format.
 __device__ __forceinline__ float to_tf32(float x) {
   uint32_t r;
