@@ -27,6 +27,11 @@ struct Args {
   int part_keys;                    // token kernel, more parts than a cluster: keys per part
   float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised
   float* part_lse;                  // [splits][batch][kv_heads][rows]
+  // backward: parts of the query rows for dK and dV, of the keys for dQ (1: outputs
+  // written directly), and their fp32 sums, unscaled
+  int dkv_splits, dq_splits;
+  float *part_dk, *part_dv;         // [dkv_splits][batch][kv_heads][len_kv][dim]
+  float* part_dq;                   // [dq_splits][batch][kv_heads][rows][dim]
 };
 
 // Permitted keys of batch entry b end here.

@@ -17,35 +17,44 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace kfac {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 256;   // 16 x 16: rows x (keys or channels)
-constexpr int BK = 64;          // keys per tile
-constexpr int PP = BK + 4;      // pitch of a probability row (floats; 16-byte rows)
-
-template <int BQ, int DP> struct SimtCfg {
+constexpr int kSimtRows = 32;   // query rows of a forward block
+// A block owns BO rows (queries, or keys for dK and dV) and streams tiles of BS rows of
+// the other side past them.  Threads form a grid of BO / RT x 16; thread (ty, tx) holds
+// own rows ty RT .. and streamed rows tx + 16 j of a score tile, and channels 4 tx +
+// 64 c of a result.  A row's scores belong to one half warp: only the loads of a tile
+// need the block's barrier.
+// Bound by the FMA pipe at large sizes (8 16-byte shared loads per 64 FMAs), by the
+// latency of a block's chain of tiles at small ones: hence small blocks (BO = 32, 128
+// threads), several per SM.
+template <int BO_, int RT_, int BS_, int DP_> struct Simt {
+  static constexpr int BO = BO_, RT = RT_, BS = BS_, DP = DP_;
+  static constexpr int THREADS = BO / RT * 16;
   static constexpr int DPP = DP + 4;   // row pitch: float4 reads of 8 rows hit 32 banks
-  static constexpr int RT = BQ / 16;   // rows per thread
+  static constexpr int PP = BS + 4;    // pitch of a probability row
   static constexpr int CV = DP / 64;   // float4 of channels per thread
-  static constexpr size_t FWD = sizeof(float) * (BQ * DPP + 2 * BK * DPP + BQ * PP) + 4 * BK;
-  static constexpr size_t BWD = sizeof(float) * (2 * BQ * DPP + 2 * BK * DPP + 2 * BQ * PP + 2 * BQ) + 4 * BK;
+  static constexpr int CT = BS / 16;   // streamed rows per thread
+  static constexpr size_t FWD = sizeof(float) * (BO * DPP + 2 * BS * DPP + BO * PP) + 4 * BS;
+  static constexpr size_t BWD = sizeof(float) * (2 * BO * DPP + 2 * BS * DPP + 2 * BO * PP + 2 * BS) + 4 * BS;
 };
 
-// rows x dim of global memory -> shared [n][DP + 4] fp32, zeros past dim and where
+// n rows x dim of global memory -> shared [n][DP + 4] fp32, zeros past dim and where
 // `off` gives none (negative).  16 threads per row, four channels at a time: one
 // offset per row and thread, and 16-byte loads where the rows allow (vec).
-template <typename T, int DP, typename Off>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int n, int dim, bool vec, Off off) {
+template <typename T, typename C, int N, typename Off>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, bool vec, Off off) {
   const int c0 = threadIdx.x % 16;
 #pragma unroll 4
-  for (int r = threadIdx.x / 16; r < n; r += kThreads / 16) {
+  for (int r = threadIdx.x / 16; r < N; r += C::THREADS / 16) {
     const int64_t o = off(r);
     const T* p = src + o;
 #pragma unroll
-    for (int c = c0; c < DP / 4; c += 16) {
+    for (int c = c0; c < C::DP / 4; c += 16) {
       const int d = 4 * c;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (o >= 0 && d < dim) {
@@ -58,9 +67,24 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int n, int d
           if (d + 3 < dim) v.w = to_f32<T>(p[d + 3]);
         }
       }
-      *reinterpret_cast<float4*>(dst + r * (DP + 4) + d) = v;
+      *reinterpret_cast<float4*>(dst + r * C::DPP + d) = v;
     }
   }
+}
+// BS (or BO) keys from key0 of k and v, zeros where a key is not permitted; oks[r] says
+// whether it is.
+template <typename T, typename C, int N>
+__device__ __forceinline__ void load_keys(const Args& a, float* Ks, float* Vs, int* oks, int b, int hk,
+                                          int len, int key0) {
+  const int64_t kb = b * a.ks[0] + hk * a.ks[2], vb = b * a.vs[0] + hk * a.vs[2];
+  load_tile<T, C, N>(Ks, static_cast<const T*>(a.k), a.dim, a.vec, [&](int r) -> int64_t {
+    const bool ok = key_ok(a, b, len, key0 + r);
+    if (threadIdx.x % 16 == 0) oks[r] = ok;
+    return ok ? kb + (int64_t)(key0 + r) * a.ks[1] : -1;
+  });
+  load_tile<T, C, N>(Vs, static_cast<const T*>(a.v), a.dim, a.vec, [&](int r) -> int64_t {
+    return key_ok(a, b, len, key0 + r) ? vb + (int64_t)(key0 + r) * a.vs[1] : -1;
+  });
 }
 
 __device__ __forceinline__ float half_max(float v) {
@@ -74,26 +98,26 @@ __device__ __forceinline__ float half_sum(float v) {
   return v;
 }
 
-// acc[i][j] = sum_d x[row i][d] y[key j][d], rows ty * RT + i, keys tx + 16 j
-template <int RT, int DP>
+// acc[i][j] = sum_d x[ty RT + i][d] y[tx + 16 j][d]
+template <typename C>
 __device__ __forceinline__ void dots(const float* x, const float* y, int ty, int tx,
-                                     float (&acc)[RT][4]) {
-  constexpr int DPP = DP + 4;
+                                     float (&acc)[C::RT][C::CT]) {
+  constexpr int RT = C::RT, CT = C::CT, DPP = C::DPP;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < CT; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
-  for (int d = 0; d < DP; d += 4) {
-    float4 xr[RT], yr[4];
+  for (int d = 0; d < C::DP; d += 4) {
+    float4 xr[RT], yr[CT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) xr[i] = *reinterpret_cast<const float4*>(x + (ty * RT + i) * DPP + d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) yr[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * DPP + d);
+    for (int j = 0; j < CT; ++j) yr[j] = *reinterpret_cast<const float4*>(y + (tx + 16 * j) * DPP + d);
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < CT; ++j) {
         acc[i][j] = fmaf(xr[i].x, yr[j].x, acc[i][j]);
         acc[i][j] = fmaf(xr[i].y, yr[j].y, acc[i][j]);
         acc[i][j] = fmaf(xr[i].z, yr[j].z, acc[i][j]);
@@ -102,21 +126,21 @@ __device__ __forceinline__ void dots(const float* x, const float* y, int ty, int
   }
 }
 
-// o[i][c] += sum_key p[row i][key] y[key][4 tx + 64 c ..]
-template <int RT, int CV, int DP>
+// o[i][c] += sum_k p[ty RT + i][k] y[k][4 tx + 64 c ..]
+template <typename C>
 __device__ __forceinline__ void add_rows(const float* p, const float* y, int ty, int tx,
-                                         float4 (&o)[RT][CV]) {
-  constexpr int DPP = DP + 4;
+                                         float4 (&o)[C::RT][C::CV]) {
+  constexpr int RT = C::RT;
 #pragma unroll 4
-  for (int k = 0; k < BK; k += 4) {
+  for (int k = 0; k < C::BS; k += 4) {
     float4 pr[RT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(p + (ty * RT + i) * PP + k);
+    for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(p + (ty * RT + i) * C::PP + k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-      for (int c = 0; c < CV; ++c) {
-        const float4 yv = *reinterpret_cast<const float4*>(y + (k + kk) * DPP + 4 * tx + 64 * c);
+      for (int c = 0; c < C::CV; ++c) {
+        const float4 yv = *reinterpret_cast<const float4*>(y + (k + kk) * C::DPP + 4 * tx + 64 * c);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           const float w = kk == 0 ? pr[i].x : kk == 1 ? pr[i].y : kk == 2 ? pr[i].z : pr[i].w;
@@ -128,28 +152,12 @@ __device__ __forceinline__ void add_rows(const float* p, const float* y, int ty,
       }
   }
 }
-
-// o[i][c] += sum_row p[row][key ty * 4 + i] y[row][4 tx + 64 c ..]
-template <int BQ, int CV, int DP>
-__device__ __forceinline__ void add_cols(const float* p, const float* y, int ty, int tx,
-                                         float4 (&o)[4][CV]) {
-  constexpr int DPP = DP + 4;
-#pragma unroll 4
-  for (int r = 0; r < BQ; ++r) {
-    const float4 w = *reinterpret_cast<const float4*>(p + r * PP + ty * 4);
+template <typename C>
+__device__ __forceinline__ void clear(float4 (&o)[C::RT][C::CV]) {
 #pragma unroll
-    for (int c = 0; c < CV; ++c) {
-      const float4 yv = *reinterpret_cast<const float4*>(y + r * DPP + 4 * tx + 64 * c);
+  for (int i = 0; i < C::RT; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float wi = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-        o[i][c].x = fmaf(wi, yv.x, o[i][c].x);
-        o[i][c].y = fmaf(wi, yv.y, o[i][c].y);
-        o[i][c].z = fmaf(wi, yv.z, o[i][c].z);
-        o[i][c].w = fmaf(wi, yv.w, o[i][c].w);
-      }
-    }
-  }
+    for (int c = 0; c < C::CV; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 template <typename T>
@@ -161,56 +169,47 @@ __device__ __forceinline__ void store4(T* dst, int d, int dim, float4 v, float f
 }
 
 // grid: (row tiles x splits, kv_heads, batch)
-template <typename T, int BQ, int DP>
-__global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_constant__ Args a) {
-  using C = SimtCfg<BQ, DP>;
-  constexpr int RT = C::RT, CV = C::CV, DPP = C::DPP;
+template <typename T, typename C>
+__global__ void __launch_bounds__(C::THREADS) simt_forward_kernel(const __grid_constant__ Args a) {
+  constexpr int RT = C::RT, CV = C::CV, CT = C::CT, BO = C::BO, BS = C::BS;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
-  float* Ks = Qs + BQ * DPP;
-  float* Vs = Ks + BK * DPP;
-  float* Ps = Vs + BK * DPP;
-  int* oks = reinterpret_cast<int*>(Ps + BQ * PP);
+  float* Ks = Qs + BO * C::DPP;
+  float* Vs = Ks + BS * C::DPP;
+  float* Ps = Vs + BS * C::DPP;
+  int* oks = reinterpret_cast<int*>(Ps + BO * C::PP);
   pdl_wait();
   pdl_trigger();
   const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
-  const int hk = blockIdx.y, b = blockIdx.z, r0 = tile * BQ;
+  const int hk = blockIdx.y, b = blockIdx.z, r0 = tile * BO;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int len = key_count(a, b);
-  const int tiles = (len + BK - 1) / BK;
+  const int tiles = (len + BS - 1) / BS;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int t1 = (int)((int64_t)tiles * (split + 1) / a.splits);
-  load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, a.vec, [&](int r) -> int64_t {
+  load_tile<T, C, BO>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, [&](int r) -> int64_t {
     return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
   });
   float m[RT], l[RT];
   float4 o[RT][CV];
+  clear<C>(o);
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < CV; ++c) o[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   const float c2 = a.scale * kLog2e;
   for (int t = t0; t < t1; ++t) {
     __syncthreads();
-    if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
+    load_keys<T, C, BS>(a, Ks, Vs, oks, b, hk, len, t * BS);
     __syncthreads();
-    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, a.vec, [&](int r) -> int64_t {
-      return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
-    });
-    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, a.vec, [&](int r) -> int64_t {
-      return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
-    });
-    __syncthreads();
-    float s[RT][4];
-    dots<RT, DP>(Qs, Ks, ty, tx, s);
+    float s[RT][CT];
+    dots<C>(Qs, Ks, ty, tx, s);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       float top = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < CT; ++j) {
         s[i][j] = oks[tx + 16 * j] ? s[i][j] * c2 : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
@@ -219,10 +218,10 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_con
       const float f = exp2f(m[i] - base);
       float sum = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < CT; ++j) {
         const float p = exp2f(s[i][j] - base);
         sum += p;
-        Ps[(ty * RT + i) * PP + tx + 16 * j] = p;
+        Ps[(ty * RT + i) * C::PP + tx + 16 * j] = p;
       }
       l[i] = l[i] * f + half_sum(sum);
       m[i] = mn;
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) simt_forward_kernel(const __grid_con
       }
     }
     __syncwarp();   // a row's probabilities come from its own half warp
-    add_rows<RT, CV, DP>(Ps, Vs, ty, tx, o);
+    add_rows<C>(Ps, Vs, ty, tx, o);
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
@@ -327,133 +326,187 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Args
   if (lane == 0 && row < n) a.delta[row] = s;
 }
 
-// P and dS of one tile (64 rows x 64 keys) into Ps (null: not wanted) and Ss.
-template <int DP>
-__device__ __forceinline__ void grad_tile(const float* Qs, const float* Os, const float* Ks,
-                                          const float* Vs, const float* lse2, const float* delta,
-                                          const int* oks, float c2, int ty, int tx, float* Ps,
-                                          float* Ss) {
-  float s[4][4], dp[4][4];
-  dots<4, DP>(Qs, Ks, ty, tx, s);
-  dots<4, DP>(Os, Vs, ty, tx, dp);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty * 4 + i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool ok = oks[tx + 16 * j] != 0;
-      const float p = ok ? exp2f(fmaf(s[i][j], c2, -lse2[r])) : 0.f;
-      if (Ps) Ps[r * PP + tx + 16 * j] = p;
-      Ss[r * PP + tx + 16 * j] = ok ? p * (dp[i][j] - delta[r]) : 0.f;
-    }
-  }
-}
-
-// grid: (key tiles + row tiles, kv_heads, batch); the first a.splits = key tiles of x
-// produce dK and dV, the others dQ: no sums across blocks, so no atomics.
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) simt_backward_kernel(const __grid_constant__ Args a) {
-  using C = SimtCfg<64, DP>;
-  constexpr int CV = C::CV, DPP = C::DPP, BQ = 64;
+// grid: (key tiles x dkv_splits + row tiles x dq_splits, kv_heads, batch); the first
+// produce dK and dV (own rows: keys; streamed: queries), the others dQ (the reverse).
+template <typename T, typename C>
+__global__ void __launch_bounds__(C::THREADS) simt_backward_kernel(const __grid_constant__ Args a) {
+  constexpr int RT = C::RT, CV = C::CV, CT = C::CT, BO = C::BO, BS = C::BS;
   extern __shared__ __align__(16) float sm[];
-  float* Qs = sm;
-  float* Os = Qs + BQ * DPP;
-  float* Ks = Os + BQ * DPP;
-  float* Vs = Ks + BK * DPP;
-  float* Ps = Vs + BK * DPP;
-  float* Ss = Ps + BQ * PP;
-  float* lse2 = Ss + BQ * PP;
-  float* delta = lse2 + BQ;
-  int* oks = reinterpret_cast<int*>(delta + BQ);
+  float* X0 = sm;                    // own: K or Q
+  float* X1 = X0 + BO * C::DPP;      //      V or dO
+  float* Y0 = X1 + BO * C::DPP;      // streamed: Q or K
+  float* Y1 = Y0 + BS * C::DPP;      //           dO or V
+  float* Ps = Y1 + BS * C::DPP;
+  float* Ss = Ps + BO * C::PP;
+  float* stats = Ss + BO * C::PP;    // dK/dV: lse and delta of the streamed queries
+  int* oks = reinterpret_cast<int*>(stats + 2 * BS);   // of the keys, own or streamed
   pdl_wait();
   pdl_trigger();
   const int hk = blockIdx.y, b = blockIdx.z;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int len = key_count(a, b);
-  const int key_tiles = (a.len_kv + BK - 1) / BK;
+  const int dkv_blocks = (a.len_kv + BO - 1) / BO * a.dkv_splits;
   const float c2 = a.scale * kLog2e;
   const float* lse_row = a.lse_in + ((int64_t)b * a.kv_heads + hk) * a.rows;
   const float* delta_row = a.delta + ((int64_t)b * a.kv_heads + hk) * a.rows;
-  auto load_keys = [&](int t) {
-    if (threadIdx.x < BK) oks[threadIdx.x] = key_ok(a, b, len, t * BK + threadIdx.x);
-    __syncthreads();
-    load_tile<T, DP>(Ks, static_cast<const T*>(a.k), BK, a.dim, a.vec, [&](int r) -> int64_t {
-      return oks[r] ? b * a.ks[0] + (int64_t)(t * BK + r) * a.ks[1] + hk * a.ks[2] : -1;
-    });
-    load_tile<T, DP>(Vs, static_cast<const T*>(a.v), BK, a.dim, a.vec, [&](int r) -> int64_t {
-      return oks[r] ? b * a.vs[0] + (int64_t)(t * BK + r) * a.vs[1] + hk * a.vs[2] : -1;
-    });
+  // past the rows, or a row without keys: P = exp(S - inf) = 0
+  auto lse2 = [&](int r) {
+    const float z = r < a.rows ? lse_row[r] * kLog2e : INFINITY;
+    return z == -INFINITY ? INFINITY : z;
   };
-  auto load_rows = [&](int r0) {
-    load_tile<T, DP>(Qs, static_cast<const T*>(a.q), BQ, a.dim, a.vec, [&](int r) -> int64_t {
+  auto load_queries = [&](float* Qs, float* Os, int r0, auto tag) {
+    constexpr int N = decltype(tag)::value;
+    load_tile<T, C, N>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, [&](int r) -> int64_t {
       return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
     });
-    load_tile<T, DP>(Os, static_cast<const T*>(a.dout), BQ, a.dim, a.vec, [&](int r) -> int64_t {
+    load_tile<T, C, N>(Os, static_cast<const T*>(a.dout), a.dim, a.vec, [&](int r) -> int64_t {
       return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
     });
-    if (threadIdx.x < BQ) {
-      const int r = r0 + threadIdx.x;
-      // past the rows, or a row without keys: P = exp(S - inf) = 0
-      const float z = r < a.rows ? lse_row[r] * kLog2e : INFINITY;
-      lse2[threadIdx.x] = z == -INFINITY ? INFINITY : z;
-      delta[threadIdx.x] = r < a.rows ? delta_row[r] : 0.f;
-    }
   };
-  if ((int)blockIdx.x < key_tiles) {   // ------------------------------ dK, dV
-    const int t = blockIdx.x;
-    float4 dk[4][CV], dv[4][CV];
+  float s[RT][CT], dp[RT][CT];
+  if ((int)blockIdx.x < dkv_blocks) {   // ----------------------------- dK, dV
+    const int k0 = (int)blockIdx.x / a.dkv_splits * BO, split = (int)blockIdx.x % a.dkv_splits;
+    const int steps = (a.rows + BS - 1) / BS;
+    const int s0 = (int)((int64_t)steps * split / a.dkv_splits);
+    const int s1 = (int)((int64_t)steps * (split + 1) / a.dkv_splits);
+    float4 dk[RT][CV], dv[RT][CV];
+    clear<C>(dk);
+    clear<C>(dv);
+    if (k0 < len) {
+      load_keys<T, C, BO>(a, X0, X1, oks, b, hk, len, k0);
+      __syncthreads();
+      for (int r0 = s0 * BS; r0 < s1 * BS; r0 += BS) {
+        __syncthreads();
+        load_queries(Y0, Y1, r0, std::integral_constant<int, BS>());
+        for (int r = threadIdx.x; r < BS; r += C::THREADS) {
+          stats[r] = lse2(r0 + r);
+          stats[BS + r] = r0 + r < a.rows ? delta_row[r0 + r] : 0.f;
+        }
+        __syncthreads();
+        dots<C>(X0, Y0, ty, tx, s);
+        dots<C>(X1, Y1, ty, tx, dp);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
-      for (int c = 0; c < CV; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    load_keys(t);
-    if (t * BK < len)
-      for (int r0 = 0; r0 < a.rows; r0 += BQ) {
-        __syncthreads();
-        load_rows(r0);
-        __syncthreads();
-        grad_tile<DP>(Qs, Os, Ks, Vs, lse2, delta, oks, c2, ty, tx, Ps, Ss);
-        __syncthreads();
-        add_cols<BQ, CV, DP>(Ps, Os, ty, tx, dv);
-        add_cols<BQ, CV, DP>(Ss, Qs, ty, tx, dk);
+          for (int j = 0; j < CT; ++j) {
+            const int at = (ty * RT + i) * C::PP + tx + 16 * j;
+            // (a key that is not permitted gives zero rows of K and V; its own results
+            // are dropped below)
+            const float p = exp2f(fmaf(s[i][j], c2, -stats[tx + 16 * j]));
+            Ps[at] = p;
+            Ss[at] = p * (dp[i][j] - stats[BS + tx + 16 * j]);
+          }
+        __syncwarp();
+        add_rows<C>(Ps, Y1, ty, tx, dv);
+        add_rows<C>(Ss, Y0, ty, tx, dk);
       }
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = t * BK + ty * 4 + i;
+    for (int i = 0; i < RT; ++i) {
+      const int key = k0 + ty * RT + i;
       if (key >= a.len_kv) continue;
+      if (k0 >= len || !oks[ty * RT + i])
+#pragma unroll
+        for (int c = 0; c < CV; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
       T* pk = static_cast<T*>(a.dk) + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2];
       T* pv = static_cast<T*>(a.dv) + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2];
+      const int64_t part = ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.len_kv + key) * a.dim;
 #pragma unroll
       for (int c = 0; c < CV; ++c) {
-        store4(pk, 4 * tx + 64 * c, a.dim, dk[i][c], a.scale);
-        store4(pv, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
+        if (a.dkv_splits == 1) {
+          store4(pk, 4 * tx + 64 * c, a.dim, dk[i][c], a.scale);
+          store4(pv, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
+        } else {
+          store4(a.part_dk + part, 4 * tx + 64 * c, a.dim, dk[i][c], 1.f);
+          store4(a.part_dv + part, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
+        }
       }
     }
     return;
   }
   // ---------------------------------------------------------------------- dQ
-  const int r0 = ((int)blockIdx.x - key_tiles) * BQ;
-  float4 dq[4][CV];
+  const int id = (int)blockIdx.x - dkv_blocks;
+  const int r0 = id / a.dq_splits * BO, split = id % a.dq_splits;
+  const int steps = (len + BS - 1) / BS;
+  const int s0 = (int)((int64_t)steps * split / a.dq_splits);
+  const int s1 = (int)((int64_t)steps * (split + 1) / a.dq_splits);
+  float4 dq[RT][CV];
+  clear<C>(dq);
+  load_queries(X0, X1, r0, std::integral_constant<int, BO>());
+  float lse[RT], delta[RT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + ty * RT + i;
+    lse[i] = lse2(r);
+    delta[i] = r < a.rows ? delta_row[r] : 0.f;
+  }
+  for (int k0 = s0 * BS; k0 < s1 * BS; k0 += BS) {
+    __syncthreads();
+    load_keys<T, C, BS>(a, Y0, Y1, oks, b, hk, len, k0);
+    __syncthreads();
+    dots<C>(X0, Y0, ty, tx, s);
+    dots<C>(X1, Y1, ty, tx, dp);
 #pragma unroll
-    for (int c = 0; c < CV; ++c) dq[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  load_rows(r0);
-  for (int t = 0; t * BK < len; ++t) {
-    __syncthreads();
-    load_keys(t);
-    __syncthreads();
-    grad_tile<DP>(Qs, Os, Ks, Vs, lse2, delta, oks, c2, ty, tx, nullptr, Ss);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < CT; ++j)
+        Ss[(ty * RT + i) * C::PP + tx + 16 * j] =
+            oks[tx + 16 * j] ? exp2f(fmaf(s[i][j], c2, -lse[i])) * (dp[i][j] - delta[i]) : 0.f;
     __syncwarp();
-    add_rows<4, CV, DP>(Ss, Ks, ty, tx, dq);
+    add_rows<C>(Ss, Y0, ty, tx, dq);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = r0 + ty * 4 + i;
+  for (int i = 0; i < RT; ++i) {
+    const int r = r0 + ty * RT + i;
     if (r >= a.rows) continue;
     T* p = static_cast<T*>(a.dq) + row_offset(a, a.dqs, b, hk, r);
+    const int64_t part = ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.rows + r) * a.dim;
 #pragma unroll
-    for (int c = 0; c < CV; ++c) store4(p, 4 * tx + 64 * c, a.dim, dq[i][c], a.scale);
+    for (int c = 0; c < CV; ++c) {
+      if (a.dq_splits == 1) store4(p, 4 * tx + 64 * c, a.dim, dq[i][c], a.scale);
+      else store4(a.part_dq + part, 4 * tx + 64 * c, a.dim, dq[i][c], 1.f);
+    }
+  }
+}
+
+// Sums the parts of the gradients that have several, in their order.  One warp per row:
+// dQ's rows first (when it has parts), then dK's and dV's.
+template <typename T>
+__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ Args a) {
+  pdl_wait();
+  pdl_trigger();
+  const int64_t nq = a.dq_splits > 1 ? (int64_t)a.batch * a.kv_heads * a.rows : 0;
+  const int64_t nk = a.dkv_splits > 1 ? (int64_t)a.batch * a.kv_heads * a.len_kv : 0;
+  int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= nq + 2 * nk) return;
+  const float* src;
+  T* dst;
+  int64_t n;
+  int splits;
+  float f = a.scale;
+  if (row < nq) {
+    src = a.part_dq;
+    n = nq;
+    splits = a.dq_splits;
+    const int r = (int)(row % a.rows);
+    const int64_t bh = row / a.rows;
+    dst = static_cast<T*>(a.dq) + row_offset(a, a.dqs, (int)(bh / a.kv_heads), (int)(bh % a.kv_heads), r);
+  } else {
+    row -= nq;
+    const bool v = row >= nk;
+    if (v) row -= nk, f = 1.f;
+    src = v ? a.part_dv : a.part_dk;
+    n = nk;
+    splits = a.dkv_splits;
+    const int64_t key = row % a.len_kv, bh = row / a.len_kv;
+    const int64_t(&st)[3] = v ? a.dvs : a.dks;
+    dst = static_cast<T*>(v ? a.dv : a.dk) + bh / a.kv_heads * st[0] + key * st[1] + bh % a.kv_heads * st[2];
+  }
+  for (int d = lane; d < a.dim; d += 32) {
+    float s = 0.f;
+    for (int i = 0; i < splits; ++i) s += src[(i * n + row) * a.dim + d];
+    dst[d] = (T)(s * f);
   }
 }
 
@@ -463,13 +516,12 @@ bool allow_smem(K kern, size_t bytes) {
          cudaSuccess;
 }
 
-template <typename T, int BQ, int DP>
+template <typename T, typename C>
 kfac_status launch_simt_forward(const Args& a, cudaStream_t st) {
-  using C = SimtCfg<BQ, DP>;
-  static const bool ok = allow_smem(simt_forward_kernel<T, BQ, DP>, C::FWD);
+  static const bool ok = allow_smem(simt_forward_kernel<T, C>, C::FWD);
   if (!ok) return KFAC_ERR_CUDA;
-  const dim3 grid((unsigned)(cdiv(a.rows, BQ) * a.splits), a.kv_heads, a.batch);
-  launch_pdl(simt_forward_kernel<T, BQ, DP>, grid, dim3(kThreads), C::FWD, st, a);
+  const dim3 grid((unsigned)(cdiv(a.rows, C::BO) * a.splits), a.kv_heads, a.batch);
+  launch_pdl(simt_forward_kernel<T, C>, grid, dim3(C::THREADS), C::FWD, st, a);
   count_launch();
   return check_launch();
 }
@@ -495,20 +547,22 @@ kfac_status simt_forward(Args a, cudaStream_t st) {
           vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   kfac_status e;
   if (a.rows <= 16)
-    e = a.dim <= 64 ? launch_simt_forward<T, 16, 64>(a, st) : launch_simt_forward<T, 16, 128>(a, st);
+    e = a.dim <= 64 ? launch_simt_forward<T, Simt<16, 1, 64, 64>>(a, st)
+                    : launch_simt_forward<T, Simt<16, 1, 64, 128>>(a, st);
   else
-    e = a.dim <= 64 ? launch_simt_forward<T, 64, 64>(a, st) : launch_simt_forward<T, 64, 128>(a, st);
+    e = a.dim <= 64 ? launch_simt_forward<T, Simt<kSimtRows, 4, 64, 64>>(a, st)
+                    : launch_simt_forward<T, Simt<kSimtRows, 4, 64, 128>>(a, st);
   if (e == KFAC_OK && a.splits > 1) e = launch_combine<T>(a, st);
   return e;
 }
 
-template <typename T, int DP>
+template <typename T, typename C>
 kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
-  using C = SimtCfg<64, DP>;
-  static const bool ok = allow_smem(simt_backward_kernel<T, DP>, C::BWD);
+  static const bool ok = allow_smem(simt_backward_kernel<T, C>, C::BWD);
   if (!ok) return KFAC_ERR_CUDA;
-  const dim3 grid((unsigned)(cdiv(a.len_kv, BK) + cdiv(a.rows, 64)), a.kv_heads, a.batch);
-  launch_pdl(simt_backward_kernel<T, DP>, grid, dim3(kThreads), C::BWD, st, a);
+  const dim3 grid((unsigned)(cdiv(a.len_kv, C::BO) * a.dkv_splits + cdiv(a.rows, C::BO) * a.dq_splits),
+                  a.kv_heads, a.batch);
+  launch_pdl(simt_backward_kernel<T, C>, grid, dim3(C::THREADS), C::BWD, st, a);
   count_launch();
   return check_launch();
 }
@@ -524,12 +578,23 @@ kfac_status backward(Args a, cudaStream_t st) {
     count_launch();
     if (kfac_status e = check_launch()) return e;
   }
-  if (sizeof(T) == 2 && tc_backward_ok(a)) return tc_backward(a, st);
-  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
-          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
-          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
-          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
-  return a.dim <= 64 ? launch_simt_backward<T, 64>(a, st) : launch_simt_backward<T, 128>(a, st);
+  kfac_status e;
+  if (sizeof(T) == 2 && tc_backward_ok(a)) {
+    e = tc_backward(a, st);
+  } else {
+    a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
+            vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
+            vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
+            vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
+    e = a.dim <= 64 ? launch_simt_backward<T, Simt<32, 4, 64, 64>>(a, st)
+                    : launch_simt_backward<T, Simt<32, 4, 32, 128>>(a, st);
+  }
+  const int64_t sums = (a.dq_splits > 1 ? n : 0) +
+                       (a.dkv_splits > 1 ? 2 * (int64_t)a.batch * a.kv_heads * a.len_kv : 0);
+  if (e != KFAC_OK || sums == 0) return e;
+  launch_pdl(sum_parts_kernel<T>, dim3((unsigned)cdiv(sums, 8)), dim3(256), 0, st, a);
+  count_launch();
+  return check_launch();
 }
 
 // Parts of the key axis for `ctas` blocks of the unsplit product: enough for `per_sm`
@@ -541,7 +606,7 @@ int pick_splits(int64_t ctas, int per_sm, int len_kv, int tile) {
 
 int simt_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
-  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, 2, d.len_kv, BK);
+  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : kSimtRows) * d.kv_heads * d.batch, 3, d.len_kv, 64);
 }
 int tc_splits(const kfac_attention_desc& d) {
   return pick_splits((int64_t)cdiv(d.len_q, 256) * d.heads * d.batch, 1, d.len_kv, 128);
@@ -593,13 +658,52 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
                     : 0;
 }
 
+// Parts of the backward pass's loops.  A dK/dV block walks the group's query tiles (four
+// products a step), a dQ block the key tiles (three).  Where one block's walk is longer
+// than an SM's share of the whole work, it is split, into pieces of at least four
+// steps; the sums then take a launch more.
+void backward_splits(const kfac_attention_desc& d, int rows_tile, int keys_tile, int per_sm, Args* a) {
+  const int64_t group = d.heads / d.kv_heads;
+  const int64_t qt = d.dtype == KFAC_BF16 ? group * cdiv(d.len_q, rows_tile) : cdiv(group * d.len_q, rows_tile);
+  const int64_t kt = cdiv(d.len_kv, keys_tile);
+  const int64_t share = std::max<int64_t>(1, 7 * qt * kt * d.kv_heads * d.batch / (per_sm * num_sms()));
+  auto parts = [&](int64_t steps, int64_t weight) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(steps * weight, share), steps / 4, 32}));
+  };
+  a->dkv_splits = parts(qt, 4);
+  a->dq_splits = parts(kt, 3);
+}
+
+void backward_splits(const kfac_attention_desc& d, Args& a) {
+  // (bf16 layouts that fall back to the CUDA cores keep the tensor cores' parts)
+  if (d.dtype == KFAC_BF16) backward_splits(d, 128, 128, 1, &a);
+  else backward_splits(d, 64, d.head_dim <= 64 ? 64 : 32, 3, &a);
+}
+// Bytes of the backward pass's workspace; places its pieces at `ws`.
+size_t backward_bytes(const kfac_attention_desc& d, Args& a, char* ws) {
+  size_t at = 0;
+  auto take = [&](size_t floats) {
+    float* p = reinterpret_cast<float*>(ws + at);
+    at += align_up(floats * sizeof(float));
+    return p;
+  };
+  const size_t q = (size_t)d.batch * d.heads * d.len_q, k = (size_t)d.batch * d.kv_heads * d.len_kv;
+  a.delta = take(q);
+  a.part_dq = a.dq_splits > 1 ? take(a.dq_splits * q * d.head_dim) : nullptr;
+  a.part_dk = a.dkv_splits > 1 ? take(a.dkv_splits * k * d.head_dim) : nullptr;
+  a.part_dv = a.dkv_splits > 1 ? take(a.dkv_splits * k * d.head_dim) : nullptr;
+  return at;
+}
+
 size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
   int splits = simt_splits(d), keys;   // whichever form the tensors' layouts allow
   if (d.dtype == KFAC_BF16)
     splits = std::max(splits, token_sizes(d) ? token_splits(d, true, &keys) : tc_splits(d));
   const size_t fwd = part_bytes(d, splits);
-  const size_t bwd = backward ? align_up((size_t)d.batch * d.heads * d.len_q * sizeof(float)) : 0;
-  return std::max(fwd, bwd);
+  if (!backward) return fwd;
+  Args a{};
+  backward_splits(d, a);
+  return std::max(fwd, backward_bytes(d, a, nullptr));
 }
 
 struct Tensor {
@@ -734,7 +838,8 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* d,
   a.lse_in = lse;
   a.kv_len = kv_len;
   a.key_mask = key_mask;
-  a.delta = static_cast<float*>(workspace);
+  backward_splits(*d, a);
+  backward_bytes(*d, a, static_cast<char*>(workspace));
   for (int i = 0; i < 3; ++i) {
     a.dos[i] = g->dout_stride[i];
     a.dqs[i] = g->dq_stride[i];

@@ -525,13 +525,27 @@ __device__ __forceinline__ void store_row(const uint32_t (&o)[32], __nv_bfloat16
     }
 }
 
+// The same to a part's fp32 sums.
+__device__ __forceinline__ void store_part(const uint32_t (&o)[32], float* dst, int c, int dim,
+                                           bool ok, bool zero) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    if (c + i < dim) {
+      float4 v = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]),
+                             __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+      if (zero) v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (!ok) v = make_float4(kNaN, kNaN, kNaN, kNaN);
+      *reinterpret_cast<float4*>(dst + c + i) = v;
+    }
+}
+
 struct BwdMaps {
   CUtensorMap q, k, v, g;
   MapMul xq, xk, xv, xg;
 };
 
 template <int NC>
-__device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int tile, int hk, int b, uint8_t* smem,
+__device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int tile, int split, int hk, int b, uint8_t* smem,
                                           uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
   using C = BwdCfg<NC>;
   uint8_t *Ks = smem, *Vs = Ks + C::TILE, *Qs = Vs + C::TILE, *Gs = Qs + 3 * C::TILE;
@@ -544,7 +558,10 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   const int k0 = tile * BT;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int qtiles = (a.len_q + BT - 1) / BT;
-  const int n = k0 < len ? a.group * qtiles : 0;
+  // this part of the group's query tiles
+  const int steps = k0 < len ? a.group * qtiles : 0;
+  const int first = (int)((int64_t)steps * split / a.dkv_splits);
+  const int n = (int)((int64_t)steps * (split + 1) / a.dkv_splits) - first;
   const int ksteps = (a.dim + 15) / 16;
   auto give_up = [&](int info) {
     *abort_flag = 1;
@@ -561,7 +578,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
       }
       int i = 0;
       for (; i < n; ++i) {
-        const int h = hk * a.group + i / qtiles, row = i % qtiles * BT;
+        const int h = hk * a.group + (first + i) / qtiles, row = (first + i) % qtiles * BT;
         const int sq = i % 3, sg = i % 2;
         if (!tc::mbar_wait(&q_empty[sq], ((uint32_t)(i / 3) & 1u) ^ 1u, abort_flag)) break;
         load_chunks<NC>(Qs + sq * C::TILE, &mp.q, &q_full[sq], row, h * mp.xq.head, b * mp.xq.batch);
@@ -632,7 +649,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
       }
     }
     for (int i = 0; i < n; ++i) {
-      const int h = hk * a.group + i / qtiles, row = i % qtiles * BT, s = i % 2;
+      const int h = hk * a.group + (first + i) / qtiles, row = (first + i) % qtiles * BT, s = i % 2;
       if (!__all_sync(kFull, tc::mbar_wait(&st_empty[s], ((uint32_t)(i / 2) & 1u) ^ 1u, abort_flag))) {
         give_up(113);
         break;
@@ -734,6 +751,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     const int64_t* st = half ? a.dks : a.dvs;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + b * st[0] + key * st[1] + hk * st[2];
     const float f = !ok ? kNaN : half ? a.scale : 1.f;
+    float* part = (half ? a.part_dk : a.part_dv) +
+                  ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.len_kv + key) * a.dim;
     for (int c = 0; c < a.dim; c += 32) {
       uint32_t o[32];
       if (n > 0) {
@@ -741,14 +760,16 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         tc::tmem_ld_wait();
         tc::tmem_ld_use(o);
       }
-      if (key < a.len_kv) store_row(o, dst, c, a.dim, f, n == 0 || !mine);
+      if (key >= a.len_kv) continue;
+      if (a.dkv_splits == 1) store_row(o, dst, c, a.dim, f, n == 0 || !mine);
+      else store_part(o, part, c, a.dim, ok, n == 0 || !mine);
     }
     tc::tc_fence_before();
   }
 }
 
 template <int NC>
-__device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int tile, int hk, int b, uint8_t* smem,
+__device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int tile, int split, int hk, int b, uint8_t* smem,
                                          uint64_t* bars, volatile int* abort_flag, uint32_t tmem) {
   using C = BwdCfg<NC>;
   uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
@@ -760,7 +781,10 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int h = hk * a.group + tile / qtiles, q0 = tile % qtiles * BT;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
-  const int n = (len + BT - 1) / BT;
+  // this part of the key tiles
+  const int tiles = (len + BT - 1) / BT;
+  const int first = (int)((int64_t)tiles * split / a.dq_splits);
+  const int n = (int)((int64_t)tiles * (split + 1) / a.dq_splits) - first;
   const int ksteps = (a.dim + 15) / 16;
   auto give_up = [&](int info) {
     *abort_flag = 1;
@@ -779,9 +803,9 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       for (; j < n; ++j) {
         const int sk = j % 3, sv = j % 2;
         if (!tc::mbar_wait(&k_empty[sk], ((uint32_t)(j / 3) & 1u) ^ 1u, abort_flag)) break;
-        load_chunks<NC>(Ks + sk * C::TILE, &mp.k, &k_full[sk], j * BT, hk * mp.xk.head, b * mp.xk.batch);
+        load_chunks<NC>(Ks + sk * C::TILE, &mp.k, &k_full[sk], (first + j) * BT, hk * mp.xk.head, b * mp.xk.batch);
         if (!tc::mbar_wait(&v_empty[sv], ((uint32_t)(j / 2) & 1u) ^ 1u, abort_flag)) break;
-        load_chunks<NC>(Vs + sv * C::TILE, &mp.v, &v_full[sv], j * BT, hk * mp.xv.head, b * mp.xv.batch);
+        load_chunks<NC>(Vs + sv * C::TILE, &mp.v, &v_full[sv], (first + j) * BT, hk * mp.xv.head, b * mp.xv.batch);
       }
       if (j < n) {   // winding down: let the copies in flight land
         give_up(121);
@@ -830,12 +854,12 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     // K's rows of keys that are not permitted become zero: dS is 0 there, and 0 x NaN
     // would reach dQ
     MaskWalk mask;
-    mask.fetch(a, b, len, 0);
+    mask.fetch(a, b, len, first * BT);
     for (int j = 0; j < n; ++j) {
       const int s = j % 3;
       uint32_t w[4];
-      mask.words(a, len, j * BT, w);
-      mask.fetch(a, b, len, j * BT + BT);
+      mask.words(a, len, (first + j) * BT, w);
+      mask.fetch(a, b, len, (first + j + 1) * BT);
       // the slot's last tile has been multiplied, so its words have been read
       bool ok = tc::mbar_wait(&k_empty[s], ((uint32_t)(j / 3) & 1u) ^ 1u, abort_flag);
       if (ok && lane == 0) {
@@ -875,7 +899,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         const uint4 u = words[j % 3];
         w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
       } else {
-        len_words(len, j * BT, w);
+        len_words(len, (first + j) * BT, w);
       }
       const uint32_t ts = tmem + lanes + 128 * (j % 2) + 64 * half;
       uint32_t r[2][32];
@@ -923,6 +947,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     if (!ok) give_up(124);
     tc::tc_fence_after();
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + b * a.dqs[0] + q * a.dqs[1] + h * a.dqs[2];
+    float* part = a.part_dq + ((int64_t)split * a.batch * a.heads * a.len_q + row) * a.dim;
     for (int c = 32 * half; c < a.dim; c += 64) {   // the groups take 32 channels in turn
       uint32_t o[32];
       if (n > 0) {
@@ -930,7 +955,9 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         tc::tmem_ld_wait();
         tc::tmem_ld_use(o);
       }
-      if (in) store_row(o, dst, c, a.dim, ok ? a.scale : kNaN, n == 0);
+      if (!in) continue;
+      if (a.dq_splits == 1) store_row(o, dst, c, a.dim, ok ? a.scale : kNaN, n == 0);
+      else store_part(o, part, c, a.dim, ok, n == 0);
     }
     tc::tc_fence_before();
   }
@@ -947,10 +974,11 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0);
   const int key_tiles = (a.len_kv + BT - 1) / BT, q_tiles = a.group * ((a.len_q + BT - 1) / BT);
-  const int pairs = a.kv_heads * a.batch;
-  const bool dkv = (int)blockIdx.x < key_tiles * pairs;
-  const int id = dkv ? (int)blockIdx.x : (int)blockIdx.x - key_tiles * pairs;
-  const int tile = id % (dkv ? key_tiles : q_tiles), pair = id / (dkv ? key_tiles : q_tiles);
+  const int dkv_blocks = key_tiles * a.dkv_splits * a.kv_heads * a.batch;
+  const bool dkv = (int)blockIdx.x < dkv_blocks;
+  const int id = dkv ? (int)blockIdx.x : (int)blockIdx.x - dkv_blocks;
+  const int tiles = dkv ? key_tiles : q_tiles, splits = dkv ? a.dkv_splits : a.dq_splits;
+  const int tile = id % tiles, split = id / tiles % splits, pair = id / tiles / splits;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBwdBars; ++i) {
       // 13: p_ready, 14: ds_ready (one arrival per warp of the two groups);
@@ -971,8 +999,8 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   const uint32_t tmem = __shfl_sync(kFull, *tmem_slot, 0);
   pdl_wait();
   pdl_trigger();
-  if (dkv) dkv_block<NC>(a, mp, tile, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
-  else dq_block<NC>(a, mp, tile, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
+  if (dkv) dkv_block<NC>(a, mp, tile, split, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
+  else dq_block<NC>(a, mp, tile, split, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
   __syncthreads();
   if (warp == 1) tc::tmem_dealloc(tmem, 512);
 }
@@ -1037,7 +1065,8 @@ kfac_status launch_tc_backward(const Args& a, cudaStream_t st) {
       !make_map(&m.v, &m.xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&m.g, &m.xg, a.dout, a.dos, a.dim, a.len_q, a.heads, a.batch))
     return KFAC_ERR_CUDA;
-  const int64_t blocks = (cdiv(a.len_kv, BT) + a.group * cdiv(a.len_q, BT)) * a.kv_heads * a.batch;
+  const int64_t blocks = (cdiv(a.len_kv, BT) * a.dkv_splits + a.group * cdiv(a.len_q, BT) * a.dq_splits) *
+                         a.kv_heads * a.batch;
   if (blocks > INT32_MAX) return KFAC_ERR_INVALID_ARG;
   const dim3 grid((unsigned)blocks);
   launch_pdl(tc_backward_kernel<NC>, grid, dim3(kTcThreads), C::SMEM, st, a, m);

@@ -294,6 +294,15 @@ def test_attention_few_rows_many_parts(dtype, keys, b, nq, nk, h, kv, d):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("keys", ["all", "both"])
+@pytest.mark.parametrize("b,nq,nk,h,kv,d", [(1, 20, 3100, 2, 1, 64), (1, 2500, 40, 2, 1, 128),
+                                            (2, 700, 1100, 2, 1, 72), (1, 1, 2000, 3, 3, 33)])
+def test_attention_gradients_in_parts(dtype, keys, b, nq, nk, h, kv, d):
+    """Few blocks with long walks: the sums of dQ, or of dK and dV, come in parts."""
+    _check_attention(*_inputs(dtype, b, nq, nk, h, kv, d, keys))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_without_queries_or_keys(dtype):
     q, k, v, g, *_ = _inputs(dtype, 2, 5, 7, 2, 2, 64, "all")
     out, lse = K.cross_attention(q, k[:, :0], v[:, :0])
