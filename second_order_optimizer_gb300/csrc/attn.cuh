@@ -53,6 +53,10 @@ constexpr int kTokenWarps = 4;
 constexpr int kTokenCluster = 8;    // parts that one cluster joins
 kfac_status token_forward(const Args& a, cudaStream_t st);
 
+// fp32 arithmetic: forward of more than 16 rows, and backward (a.delta already written).
+template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st);
+template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st);
+
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
 bool tc_forward_ok(const Args& a);
 kfac_status tc_forward(const Args& a, cudaStream_t st);

@@ -23,24 +23,19 @@ namespace kfac {
 namespace attn {
 namespace {
 
-constexpr int kSimtRows = 32;   // query rows of a forward block
-// A block owns BO rows (queries, or keys for dK and dV) and streams tiles of BS rows of
-// the other side past them.  Threads form a grid of BO / RT x 16; thread (ty, tx) holds
-// own rows ty RT .. and streamed rows tx + 16 j of a score tile, and channels 4 tx +
-// 64 c of a result.  A row's scores belong to one half warp: only the loads of a tile
-// need the block's barrier.
-// Bound by the FMA pipe at large sizes (8 16-byte shared loads per 64 FMAs), by the
-// latency of a block's chain of tiles at small ones: hence small blocks (BO = 32, 128
-// threads), several per SM.
-template <int BO_, int RT_, int BS_, int DP_> struct Simt {
-  static constexpr int BO = BO_, RT = RT_, BS = BS_, DP = DP_;
+// The forward kernel for few rows that the token kernel cannot take (fp32, or rows that
+// are not whole 16 bytes), on the FMA pipe: a block of 16 x 16 threads owns 16 query rows
+// and streams tiles of 64 keys past them; thread (ty, tx) holds row ty, keys tx + 16 j of
+// a score tile and channels 4 tx + 64 c of the result.  Bound by reading k and v: the key
+// axis is split over as many blocks as fit.
+template <int DP_> struct Few {
+  static constexpr int BO = 16, RT = 1, BS = 64, DP = DP_;
   static constexpr int THREADS = BO / RT * 16;
   static constexpr int DPP = DP + 4;   // row pitch: float4 reads of 8 rows hit 32 banks
   static constexpr int PP = BS + 4;    // pitch of a probability row
   static constexpr int CV = DP / 64;   // float4 of channels per thread
-  static constexpr int CT = BS / 16;   // streamed rows per thread
-  static constexpr size_t FWD = sizeof(float) * (BO * DPP + 2 * BS * DPP + BO * PP) + 4 * BS;
-  static constexpr size_t BWD = sizeof(float) * (2 * BO * DPP + 2 * BS * DPP + 2 * BO * PP + 2 * BS) + 4 * BS;
+  static constexpr int CT = BS / 16;   // keys per thread
+  static constexpr size_t SMEM = sizeof(float) * (BO * DPP + 2 * BS * DPP + BO * PP) + 4 * BS;
 };
 
 // n rows x dim of global memory -> shared [n][DP + 4] fp32, zeros past dim and where
@@ -71,7 +66,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, boo
     }
   }
 }
-// BS (or BO) keys from key0 of k and v, zeros where a key is not permitted; oks[r] says
+// N keys from key0 of k and v, zeros where a key is not permitted; oks[r] says
 // whether it is.
 template <typename T, typename C, int N>
 __device__ __forceinline__ void load_keys(const Args& a, float* Ks, float* Vs, int* oks, int b, int hk,
@@ -170,7 +165,7 @@ __device__ __forceinline__ void store4(T* dst, int d, int dim, float4 v, float f
 
 // grid: (row tiles x splits, kv_heads, batch)
 template <typename T, typename C>
-__global__ void __launch_bounds__(C::THREADS) simt_forward_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(C::THREADS) few_rows_kernel(const __grid_constant__ Args a) {
   constexpr int RT = C::RT, CV = C::CV, CT = C::CT, BO = C::BO, BS = C::BS;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
@@ -256,18 +251,17 @@ __global__ void __launch_bounds__(C::THREADS) simt_forward_kernel(const __grid_c
   }
 }
 
-// Joins the parts of the key axis: out = sum_s w_s o_s, w_s = exp(lse_s - lse).  One
-// warp per row.  [batch][kv_heads][rows] is [batch][heads][len_q], lse's layout.
+// Joins the parts of the key axis: out = sum_s w_s o_s, w_s = exp(lse_s - lse).  One block
+// of four warps per row, a quarter of the parts each (the sums of a quarter in order, then
+// the quarters in order).  [batch][kv_heads][rows] is [batch][heads][len_q], lse's layout.
 template <typename T>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Args a) {
+  __shared__ float acc_s[4][128], total_s[4];
   pdl_wait();
   pdl_trigger();
   const int64_t n = (int64_t)a.batch * a.kv_heads * a.rows;
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= n) return;
-  const int r = (int)(row % a.rows), hk = (int)(row / a.rows % a.kv_heads);
-  const int b = (int)(row / a.rows / a.kv_heads);
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   float top = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) top = fmaxf(top, a.part_lse[s * n + row]);
 #pragma unroll
@@ -275,9 +269,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ar
   const float base = top == -INFINITY ? 0.f : top;
   float total = 0.f;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+  for (int s = warp; s < a.splits; s += 4) {
     const float w = exp2f((a.part_lse[s * n + row] - base) * kLog2e);
-    if (w == 0.f) continue;   // an empty part, or one far below the others
     total += w;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -285,12 +279,18 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Ar
       if (d < a.dim) acc[c] = fmaf(w, a.part_o[(s * n + row) * a.dim + d], acc[c]);
     }
   }
-  const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
-  T* dst = static_cast<T*>(a.out) + row_offset(a, a.os, b, hk, r);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    if (lane + 32 * c < a.dim) dst[lane + 32 * c] = (T)(acc[c] * inv);
-  if (a.lse && lane == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
+  for (int c = 0; c < 4; ++c) acc_s[warp][lane + 32 * c] = acc[c];
+  if (lane == 0) total_s[warp] = total;
+  __syncthreads();
+  total = (total_s[0] + total_s[1]) + (total_s[2] + total_s[3]);
+  const float inv = total > 0.f ? 1.f / total : (total == 0.f ? 0.f : total);
+  const int r = (int)(row % a.rows), hk = (int)(row / a.rows % a.kv_heads);
+  const int b = (int)(row / a.rows / a.kv_heads), d = threadIdx.x;
+  if (d < a.dim)
+    static_cast<T*>(a.out)[row_offset(a, a.os, b, hk, r) + d] =
+        (T)(((acc_s[0][d] + acc_s[1][d]) + (acc_s[2][d] + acc_s[3][d])) * inv);
+  if (a.lse && d == 0) a.lse[row] = total == 0.f ? -INFINITY : base + logf(total);
 }
 
 // delta[b][h][i] = sum_d dout out, in fp32.  L lanes per row (L divides 32), each taking
@@ -324,149 +324,6 @@ __global__ void __launch_bounds__(256) delta_kernel(const __grid_constant__ Args
 #pragma unroll
   for (int k = L / 2; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
   if (lane == 0 && row < n) a.delta[row] = s;
-}
-
-// grid: (key tiles x dkv_splits + row tiles x dq_splits, kv_heads, batch); the first
-// produce dK and dV (own rows: keys; streamed: queries), the others dQ (the reverse).
-template <typename T, typename C>
-__global__ void __launch_bounds__(C::THREADS) simt_backward_kernel(const __grid_constant__ Args a) {
-  constexpr int RT = C::RT, CV = C::CV, CT = C::CT, BO = C::BO, BS = C::BS;
-  extern __shared__ __align__(16) float sm[];
-  float* X0 = sm;                    // own: K or Q
-  float* X1 = X0 + BO * C::DPP;      //      V or dO
-  float* Y0 = X1 + BO * C::DPP;      // streamed: Q or K
-  float* Y1 = Y0 + BS * C::DPP;      //           dO or V
-  float* Ps = Y1 + BS * C::DPP;
-  float* Ss = Ps + BO * C::PP;
-  float* stats = Ss + BO * C::PP;    // dK/dV: lse and delta of the streamed queries
-  int* oks = reinterpret_cast<int*>(stats + 2 * BS);   // of the keys, own or streamed
-  pdl_wait();
-  pdl_trigger();
-  const int hk = blockIdx.y, b = blockIdx.z;
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int len = key_count(a, b);
-  const int dkv_blocks = (a.len_kv + BO - 1) / BO * a.dkv_splits;
-  const float c2 = a.scale * kLog2e;
-  const float* lse_row = a.lse_in + ((int64_t)b * a.kv_heads + hk) * a.rows;
-  const float* delta_row = a.delta + ((int64_t)b * a.kv_heads + hk) * a.rows;
-  // past the rows, or a row without keys: P = exp(S - inf) = 0
-  auto lse2 = [&](int r) {
-    const float z = r < a.rows ? lse_row[r] * kLog2e : INFINITY;
-    return z == -INFINITY ? INFINITY : z;
-  };
-  auto load_queries = [&](float* Qs, float* Os, int r0, auto tag) {
-    constexpr int N = decltype(tag)::value;
-    load_tile<T, C, N>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, [&](int r) -> int64_t {
-      return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
-    });
-    load_tile<T, C, N>(Os, static_cast<const T*>(a.dout), a.dim, a.vec, [&](int r) -> int64_t {
-      return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
-    });
-  };
-  float s[RT][CT], dp[RT][CT];
-  if ((int)blockIdx.x < dkv_blocks) {   // ----------------------------- dK, dV
-    const int k0 = (int)blockIdx.x / a.dkv_splits * BO, split = (int)blockIdx.x % a.dkv_splits;
-    const int steps = (a.rows + BS - 1) / BS;
-    const int s0 = (int)((int64_t)steps * split / a.dkv_splits);
-    const int s1 = (int)((int64_t)steps * (split + 1) / a.dkv_splits);
-    float4 dk[RT][CV], dv[RT][CV];
-    clear<C>(dk);
-    clear<C>(dv);
-    if (k0 < len) {
-      load_keys<T, C, BO>(a, X0, X1, oks, b, hk, len, k0);
-      __syncthreads();
-      for (int r0 = s0 * BS; r0 < s1 * BS; r0 += BS) {
-        __syncthreads();
-        load_queries(Y0, Y1, r0, std::integral_constant<int, BS>());
-        for (int r = threadIdx.x; r < BS; r += C::THREADS) {
-          stats[r] = lse2(r0 + r);
-          stats[BS + r] = r0 + r < a.rows ? delta_row[r0 + r] : 0.f;
-        }
-        __syncthreads();
-        dots<C>(X0, Y0, ty, tx, s);
-        dots<C>(X1, Y1, ty, tx, dp);
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-#pragma unroll
-          for (int j = 0; j < CT; ++j) {
-            const int at = (ty * RT + i) * C::PP + tx + 16 * j;
-            // (a key that is not permitted gives zero rows of K and V; its own results
-            // are dropped below)
-            const float p = exp2f(fmaf(s[i][j], c2, -stats[tx + 16 * j]));
-            Ps[at] = p;
-            Ss[at] = p * (dp[i][j] - stats[BS + tx + 16 * j]);
-          }
-        __syncwarp();
-        add_rows<C>(Ps, Y1, ty, tx, dv);
-        add_rows<C>(Ss, Y0, ty, tx, dk);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int key = k0 + ty * RT + i;
-      if (key >= a.len_kv) continue;
-      if (k0 >= len || !oks[ty * RT + i])
-#pragma unroll
-        for (int c = 0; c < CV; ++c) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-      T* pk = static_cast<T*>(a.dk) + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2];
-      T* pv = static_cast<T*>(a.dv) + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2];
-      const int64_t part = ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.len_kv + key) * a.dim;
-#pragma unroll
-      for (int c = 0; c < CV; ++c) {
-        if (a.dkv_splits == 1) {
-          store4(pk, 4 * tx + 64 * c, a.dim, dk[i][c], a.scale);
-          store4(pv, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
-        } else {
-          store4(a.part_dk + part, 4 * tx + 64 * c, a.dim, dk[i][c], 1.f);
-          store4(a.part_dv + part, 4 * tx + 64 * c, a.dim, dv[i][c], 1.f);
-        }
-      }
-    }
-    return;
-  }
-  // ---------------------------------------------------------------------- dQ
-  const int id = (int)blockIdx.x - dkv_blocks;
-  const int r0 = id / a.dq_splits * BO, split = id % a.dq_splits;
-  const int steps = (len + BS - 1) / BS;
-  const int s0 = (int)((int64_t)steps * split / a.dq_splits);
-  const int s1 = (int)((int64_t)steps * (split + 1) / a.dq_splits);
-  float4 dq[RT][CV];
-  clear<C>(dq);
-  load_queries(X0, X1, r0, std::integral_constant<int, BO>());
-  float lse[RT], delta[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = r0 + ty * RT + i;
-    lse[i] = lse2(r);
-    delta[i] = r < a.rows ? delta_row[r] : 0.f;
-  }
-  for (int k0 = s0 * BS; k0 < s1 * BS; k0 += BS) {
-    __syncthreads();
-    load_keys<T, C, BS>(a, Y0, Y1, oks, b, hk, len, k0);
-    __syncthreads();
-    dots<C>(X0, Y0, ty, tx, s);
-    dots<C>(X1, Y1, ty, tx, dp);
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < CT; ++j)
-        Ss[(ty * RT + i) * C::PP + tx + 16 * j] =
-            oks[tx + 16 * j] ? exp2f(fmaf(s[i][j], c2, -lse[i])) * (dp[i][j] - delta[i]) : 0.f;
-    __syncwarp();
-    add_rows<C>(Ss, Y0, ty, tx, dq);
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    const int r = r0 + ty * RT + i;
-    if (r >= a.rows) continue;
-    T* p = static_cast<T*>(a.dq) + row_offset(a, a.dqs, b, hk, r);
-    const int64_t part = ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.rows + r) * a.dim;
-#pragma unroll
-    for (int c = 0; c < CV; ++c) {
-      if (a.dq_splits == 1) store4(p, 4 * tx + 64 * c, a.dim, dq[i][c], a.scale);
-      else store4(a.part_dq + part, 4 * tx + 64 * c, a.dim, dq[i][c], 1.f);
-    }
-  }
 }
 
 // Sums the parts of the gradients that have several, in their order.  One warp per row:
@@ -517,11 +374,11 @@ bool allow_smem(K kern, size_t bytes) {
 }
 
 template <typename T, typename C>
-kfac_status launch_simt_forward(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(simt_forward_kernel<T, C>, C::FWD);
+kfac_status launch_few_rows(const Args& a, cudaStream_t st) {
+  static const bool ok = allow_smem(few_rows_kernel<T, C>, C::SMEM);
   if (!ok) return KFAC_ERR_CUDA;
   const dim3 grid((unsigned)(cdiv(a.rows, C::BO) * a.splits), a.kv_heads, a.batch);
-  launch_pdl(simt_forward_kernel<T, C>, grid, dim3(C::THREADS), C::FWD, st, a);
+  launch_pdl(few_rows_kernel<T, C>, grid, dim3(C::THREADS), C::SMEM, st, a);
   count_launch();
   return check_launch();
 }
@@ -529,7 +386,7 @@ kfac_status launch_simt_forward(const Args& a, cudaStream_t st) {
 template <typename T>
 kfac_status launch_combine(const Args& a, cudaStream_t st) {
   const int64_t n = (int64_t)a.batch * a.kv_heads * a.rows;
-  launch_pdl(combine_kernel<T>, dim3((unsigned)cdiv(n, 4)), dim3(128), 0, st, a);
+  launch_pdl(combine_kernel<T>, dim3((unsigned)n), dim3(128), 0, st, a);
   count_launch();
   return check_launch();
 }
@@ -541,30 +398,18 @@ bool vec_rows(const void* p, const int64_t* s, int rows, int heads, int batch, i
 }
 
 template <typename T>
-kfac_status simt_forward(Args a, cudaStream_t st) {
+kfac_status plain_forward(Args a, cudaStream_t st) {
   a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
           vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
           vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   kfac_status e;
   if (a.rows <= 16)
-    e = a.dim <= 64 ? launch_simt_forward<T, Simt<16, 1, 64, 64>>(a, st)
-                    : launch_simt_forward<T, Simt<16, 1, 64, 128>>(a, st);
+    e = a.dim <= 64 ? launch_few_rows<T, Few<64>>(a, st)
+                    : launch_few_rows<T, Few<128>>(a, st);
   else
-    e = a.dim <= 64 ? launch_simt_forward<T, Simt<kSimtRows, 4, 64, 64>>(a, st)
-                    : launch_simt_forward<T, Simt<kSimtRows, 4, 64, 128>>(a, st);
+    e = f32_forward<T>(a, st);
   if (e == KFAC_OK && a.splits > 1) e = launch_combine<T>(a, st);
   return e;
-}
-
-template <typename T, typename C>
-kfac_status launch_simt_backward(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(simt_backward_kernel<T, C>, C::BWD);
-  if (!ok) return KFAC_ERR_CUDA;
-  const dim3 grid((unsigned)(cdiv(a.len_kv, C::BO) * a.dkv_splits + cdiv(a.rows, C::BO) * a.dq_splits),
-                  a.kv_heads, a.batch);
-  launch_pdl(simt_backward_kernel<T, C>, grid, dim3(C::THREADS), C::BWD, st, a);
-  count_launch();
-  return check_launch();
 }
 
 template <typename T>
@@ -586,8 +431,7 @@ kfac_status backward(Args a, cudaStream_t st) {
             vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
             vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
             vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
-    e = a.dim <= 64 ? launch_simt_backward<T, Simt<32, 4, 64, 64>>(a, st)
-                    : launch_simt_backward<T, Simt<32, 4, 32, 128>>(a, st);
+    e = f32_backward<T>(a, st);
   }
   const int64_t sums = (a.dq_splits > 1 ? n : 0) +
                        (a.dkv_splits > 1 ? 2 * (int64_t)a.batch * a.kv_heads * a.len_kv : 0);
@@ -604,9 +448,9 @@ int pick_splits(int64_t ctas, int per_sm, int len_kv, int tile) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, cdiv(len_kv, tile), 64}));
 }
 
-int simt_splits(const kfac_attention_desc& d) {
+int plain_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
-  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : kSimtRows) * d.kv_heads * d.batch, 3, d.len_kv, 64);
+  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, 3, d.len_kv, 64);
 }
 int tc_splits(const kfac_attention_desc& d) {
   return pick_splits((int64_t)cdiv(d.len_q, 256) * d.heads * d.batch, 1, d.len_kv, 128);
@@ -658,26 +502,24 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
                     : 0;
 }
 
-// Parts of the backward pass's loops.  A dK/dV block walks the group's query tiles (four
-// products a step), a dQ block the key tiles (three).  Where one block's walk is longer
-// than an SM's share of the whole work, it is split, into pieces of at least four
-// steps; the sums then take a launch more.
-void backward_splits(const kfac_attention_desc& d, int rows_tile, int keys_tile, int per_sm, Args* a) {
+// Parts of the backward pass's loops.  A dK/dV block owns `own` keys and walks the group's
+// queries in steps (four products each), a dQ block owns as many queries and walks the
+// keys (three).  Where one block's walk is longer than its share of the whole work, it is
+// split, into pieces of at least four steps; the sums then take a launch more.
+// (bf16 layouts that the tensor-core kernels cannot take keep their parts.)
+void backward_splits(const kfac_attention_desc& d, Args& a) {
+  const bool bf16 = d.dtype == KFAC_BF16;
+  const int own = bf16 ? 128 : 64, step = bf16 ? 128 : 32, per_sm = bf16 ? 1 : 2;
   const int64_t group = d.heads / d.kv_heads;
-  const int64_t qt = d.dtype == KFAC_BF16 ? group * cdiv(d.len_q, rows_tile) : cdiv(group * d.len_q, rows_tile);
-  const int64_t kt = cdiv(d.len_kv, keys_tile);
-  const int64_t share = std::max<int64_t>(1, 7 * qt * kt * d.kv_heads * d.batch / (per_sm * num_sms()));
+  const int64_t rows = group * d.len_q, blocks_q = bf16 ? group * cdiv(d.len_q, own) : cdiv(rows, own);
+  const int64_t steps_q = bf16 ? blocks_q : cdiv(rows, step), steps_k = cdiv(d.len_kv, step);
+  const int64_t work = (4 * cdiv(d.len_kv, own) * steps_q + 3 * blocks_q * steps_k) * d.kv_heads * d.batch;
+  const int64_t share = std::max<int64_t>(1, work / (per_sm * num_sms()));
   auto parts = [&](int64_t steps, int64_t weight) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(steps * weight, share), steps / 4, 32}));
   };
-  a->dkv_splits = parts(qt, 4);
-  a->dq_splits = parts(kt, 3);
-}
-
-void backward_splits(const kfac_attention_desc& d, Args& a) {
-  // (bf16 layouts that fall back to the CUDA cores keep the tensor cores' parts)
-  if (d.dtype == KFAC_BF16) backward_splits(d, 128, 128, 1, &a);
-  else backward_splits(d, 64, d.head_dim <= 64 ? 64 : 32, 3, &a);
+  a.dkv_splits = parts(steps_q, 4);
+  a.dq_splits = parts(steps_k, 3);
 }
 // Bytes of the backward pass's workspace; places its pieces at `ws`.
 size_t backward_bytes(const kfac_attention_desc& d, Args& a, char* ws) {
@@ -696,7 +538,7 @@ size_t backward_bytes(const kfac_attention_desc& d, Args& a, char* ws) {
 }
 
 size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
-  int splits = simt_splits(d), keys;   // whichever form the tensors' layouts allow
+  int splits = plain_splits(d), keys;   // whichever form the tensors' layouts allow
   if (d.dtype == KFAC_BF16)
     splits = std::max(splits, token_sizes(d) ? token_splits(d, true, &keys) : tc_splits(d));
   const size_t fwd = part_bytes(d, splits);
@@ -788,7 +630,7 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
   a.kv_len = kv_len;
   a.key_mask = key_mask;
   const bool tc = d->dtype == KFAC_BF16 && tc_forward_ok(a), token = tc && token_sizes(*d);
-  a.splits = token ? token_splits(*d, kv_len != nullptr, &a.part_keys) : tc ? tc_splits(*d) : simt_splits(*d);
+  a.splits = token ? token_splits(*d, kv_len != nullptr, &a.part_keys) : tc ? tc_splits(*d) : plain_splits(*d);
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
   if (tc) {
@@ -797,7 +639,7 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
     if (e == KFAC_OK && a.splits > 1 && !joined) e = launch_combine<__nv_bfloat16>(a, stream);
     return e;
   }
-  return d->dtype == KFAC_BF16 ? simt_forward<__nv_bfloat16>(a, stream) : simt_forward<float>(a, stream);
+  return d->dtype == KFAC_BF16 ? plain_forward<__nv_bfloat16>(a, stream) : plain_forward<float>(a, stream);
 }
 
 kfac_status kfac_cross_attention_backward(const kfac_attention_desc* d,

@@ -1,0 +1,487 @@
+// Cross attention of fp32 inputs (and of bf16 rows that the tensor-memory accelerator
+// cannot address): forward for more than 16 query rows, and the backward pass.
+//
+// Products run on the tensor cores with fp32 accuracy.  Each operand v enters as its
+// TF32 rounding h and the remainder r = v - h (exact in fp32); x y = h h' + (h r' + r h'),
+// three mma.sync m16n8k8 products, the dropped r r' about 2^-22 of the whole.  h h' and
+// the small cross terms have accumulators of their own, and no accumulator outlives a
+// tile: the tensor cores' additions round towards zero, and what is summed over tiles is
+// summed in fp32 registers.  (On the FMA pipe the same tiles were bound by shared-memory
+// reads, 8 16-byte loads per 64 FMAs: 25 TFLOP/s.)
+//
+// A block owns 64 rows (queries, or keys for dK and dV), 16 per warp, and streams tiles
+// of BS rows of the other side past them.  The scores of a warp's rows stay in its
+// registers: the columns that a lane holds of S are the k slots that it supplies to the
+// next product, once keys are taken in that order (slot t of eight: key 2t, slot t + 4:
+// key 2t + 1).  Shared rows have a pitch of 4 mod 32 floats, for which both kinds of
+// 16-byte reads are free of bank conflicts: rows of a score product (lane (g, t): row g,
+// channels 8t + 4j of 32) and rows of a value product (row 2t or 2t + 1, channels 4g).
+#include "attn.cuh"
+#include "tc_prims.cuh"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace kfac {
+namespace attn {
+namespace {
+
+constexpr int kRows = 64;        // own rows of a block
+constexpr int kF32Threads = 128;
+constexpr uint32_t kAll = 0xffffffffu;
+
+template <int BS_, int DP_> struct Cfg {
+  static constexpr int BS = BS_, DP = DP_, DPP = DP + 4;
+  static constexpr int NT = BS / 8;    // 8-column tiles of a score row
+  static constexpr int NB = DP / 32;   // 32-channel blocks
+  static constexpr int TILE = BS * DPP;   // floats of a streamed tile's part
+  static constexpr size_t FWD = sizeof(float) * (kRows * DPP + 4 * TILE) + 4 * BS;
+  static constexpr size_t BWD = sizeof(float) * (2 * kRows * DPP + 4 * TILE) + 4 * (2 * BS + kRows);
+};
+
+// v = h + r: h rounded to TF32's 11 bits (half away from zero, by integer addition), r
+// exact.  An infinite v has r = NaN here ...
+struct Split { uint32_t h, r; };
+__device__ __forceinline__ Split split(float v) {
+  const uint32_t h = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
+  return {h, __float_as_uint(v - __uint_as_float(h))};
+}
+// ... and 0 here, where the infinity would otherwise be lost: in streamed tiles.
+__device__ __forceinline__ Split split_inf(float v) {
+  Split s = split(v);
+  if ((s.h & 0x7fffffffu) == 0x7f800000u) s.r = 0u;
+  return s;
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma3(float (&hi)[4], float (&lo)[4], const Split (&a)[4], Split b0,
+                                     Split b1) {
+  mma_tf32(lo, a[0].r, a[1].r, a[2].r, a[3].r, b0.h, b1.h);
+  mma_tf32(lo, a[0].h, a[1].h, a[2].h, a[3].h, b0.r, b1.r);
+  mma_tf32(hi, a[0].h, a[1].h, a[2].h, a[3].h, b0.h, b1.h);
+}
+__device__ __forceinline__ float comp(const float4& v, int e) {
+  return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+}
+
+// s[nt] = 16 own rows (x) . 8 streamed rows (y: h parts, then r parts)^T, summed over the
+// channels.
+template <typename C>
+__device__ __forceinline__ void scores(const float* x, const float* y, float (&s)[C::NT][4]) {
+  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  float lo[C::NT][4];
+#pragma unroll
+  for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] = lo[n][e] = 0.f;
+#pragma unroll 2
+  for (int bj = 0; bj < 2 * C::NB; ++bj) {
+    const int d = 32 * (bj / 2) + 8 * t + 4 * (bj % 2);
+    const float4 x0 = *reinterpret_cast<const float4*>(x + g * C::DPP + d);
+    const float4 x1 = *reinterpret_cast<const float4*>(x + (g + 8) * C::DPP + d);
+    Split a[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      a[h][0] = split(comp(x0, 2 * h));
+      a[h][1] = split(comp(x1, 2 * h));
+      a[h][2] = split(comp(x0, 2 * h + 1));
+      a[h][3] = split(comp(x1, 2 * h + 1));
+    }
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+      const uint4 yh = *reinterpret_cast<const uint4*>(y + (8 * n + g) * C::DPP + d);
+      const uint4 yr = *reinterpret_cast<const uint4*>(y + C::TILE + (8 * n + g) * C::DPP + d);
+      mma3(s[n], lo[n], a[0], {yh.x, yr.x}, {yh.y, yr.y});
+      mma3(s[n], lo[n], a[1], {yh.z, yr.z}, {yh.w, yr.w});
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[n][e] += lo[n][e];
+}
+
+// o += p (16 own rows x BS, as scores() leaves them) . y (BS streamed rows, in parts).
+// Lane (g, t) holds, of rows g (elements 0, 1) and g + 8 (2, 3), channels 32 b + 8 t + e in
+// o[4 b + e][0 or 2] and 32 b + 8 t + 4 + e in o[4 b + e][1 or 3].
+template <typename C>
+__device__ __forceinline__ void add_values(const float (&p)[C::NT][4], const float* y,
+                                           float (&o)[4 * C::NB][4]) {
+  const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  Split a[C::NT][4];
+#pragma unroll
+  for (int n = 0; n < C::NT; ++n) {
+    a[n][0] = split(p[n][0]);
+    a[n][1] = split(p[n][2]);
+    a[n][2] = split(p[n][1]);
+    a[n][3] = split(p[n][3]);
+  }
+#pragma unroll
+  for (int blk = 0; blk < C::NB; ++blk) {
+    float hi[4][4], lo[4][4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hi[e][k] = lo[e][k] = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+      const float* row = y + (8 * n + 2 * t) * C::DPP + 32 * blk + 4 * g;
+      const uint4 h0 = *reinterpret_cast<const uint4*>(row), h1 = *reinterpret_cast<const uint4*>(row + C::DPP);
+      const uint4 r0 = *reinterpret_cast<const uint4*>(row + C::TILE),
+                  r1 = *reinterpret_cast<const uint4*>(row + C::TILE + C::DPP);
+      mma3(hi[0], lo[0], a[n], {h0.x, r0.x}, {h1.x, r1.x});
+      mma3(hi[1], lo[1], a[n], {h0.y, r0.y}, {h1.y, r1.y});
+      mma3(hi[2], lo[2], a[n], {h0.z, r0.z}, {h1.z, r1.z});
+      mma3(hi[3], lo[3], a[n], {h0.w, r0.w}, {h1.w, r1.w});
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[4 * blk + e][k] += hi[e][k] + lo[e][k];
+  }
+}
+
+// N rows x dim of global memory -> shared, zeros past dim and where `off` gives none
+// (negative).  16 threads per row, four channels at a time.  kParts: as h parts, and r
+// parts TILE floats behind.
+template <typename T, typename C, int N, bool kParts, typename Off>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, bool vec, Off off) {
+  const int c0 = threadIdx.x % 16;
+#pragma unroll 4
+  for (int r = threadIdx.x / 16; r < N; r += kF32Threads / 16) {
+    const int64_t o = off(r);
+    const T* p = src + o;
+#pragma unroll
+    for (int c = c0; c < C::DP / 4; c += 16) {
+      const int d = 4 * c;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (o >= 0 && d < dim) {
+        if (sizeof(T) == 4 && vec) {
+          v = *reinterpret_cast<const float4*>(p + d);
+        } else {
+          v.x = to_f32<T>(p[d]);
+          if (d + 1 < dim) v.y = to_f32<T>(p[d + 1]);
+          if (d + 2 < dim) v.z = to_f32<T>(p[d + 2]);
+          if (d + 3 < dim) v.w = to_f32<T>(p[d + 3]);
+        }
+      }
+      if (kParts) {
+        const Split s[4] = {split_inf(v.x), split_inf(v.y), split_inf(v.z), split_inf(v.w)};
+        *reinterpret_cast<uint4*>(dst + r * C::DPP + d) = make_uint4(s[0].h, s[1].h, s[2].h, s[3].h);
+        *reinterpret_cast<uint4*>(dst + C::TILE + r * C::DPP + d) = make_uint4(s[0].r, s[1].r, s[2].r, s[3].r);
+      } else {
+        *reinterpret_cast<float4*>(dst + r * C::DPP + d) = v;
+      }
+    }
+  }
+}
+// N keys from key0 of k and v, zeros where a key is not permitted; oks[r]: whether it is.
+template <typename T, typename C, int N, bool kParts>
+__device__ __forceinline__ void load_keys(const Args& a, float* Ks, float* Vs, int* oks, int b, int hk,
+                                          int len, int key0) {
+  const int64_t kb = b * a.ks[0] + hk * a.ks[2], vb = b * a.vs[0] + hk * a.vs[2];
+  load_tile<T, C, N, kParts>(Ks, static_cast<const T*>(a.k), a.dim, a.vec, [&](int r) -> int64_t {
+    const bool ok = key_ok(a, b, len, key0 + r);
+    if (threadIdx.x % 16 == 0) oks[r] = ok;
+    return ok ? kb + (int64_t)(key0 + r) * a.ks[1] : -1;
+  });
+  load_tile<T, C, N, kParts>(Vs, static_cast<const T*>(a.v), a.dim, a.vec, [&](int r) -> int64_t {
+    return key_ok(a, b, len, key0 + r) ? vb + (int64_t)(key0 + r) * a.vs[1] : -1;
+  });
+}
+template <typename T, typename C, int N, bool kParts>
+__device__ __forceinline__ void load_queries(const Args& a, float* Qs, float* Os, int b, int hk, int r0) {
+  load_tile<T, C, N, kParts>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, [&](int r) -> int64_t {
+    return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
+  });
+  if (Os)
+    load_tile<T, C, N, kParts>(Os, static_cast<const T*>(a.dout), a.dim, a.vec, [&](int r) -> int64_t {
+      return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
+    });
+}
+
+// One of a lane's two rows (h = 0: g, 1: g + 8) of a result, to a row of T's or of fp32 parts.
+template <typename C, typename T>
+__device__ __forceinline__ void store_result(T* dst, const float (&o)[4 * C::NB][4], int h, int dim,
+                                             float f) {
+  const int t = threadIdx.x % 4;
+#pragma unroll
+  for (int b = 0; b < C::NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = 32 * b + 8 * t + 4 * i + e;
+        if (d < dim) dst[d] = (T)(o[4 * b + e][2 * h + i] * f);
+      }
+}
+template <typename C>
+__device__ __forceinline__ void clear(float (&o)[4 * C::NB][4]) {
+#pragma unroll
+  for (int i = 0; i < 4 * C::NB; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(kAll, v, 1));
+  return fmaxf(v, __shfl_xor_sync(kAll, v, 2));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+  v += __shfl_xor_sync(kAll, v, 1);
+  return v + __shfl_xor_sync(kAll, v, 2);
+}
+
+// grid: (row tiles x splits, kv_heads, batch)
+template <typename T, typename C>
+__global__ void __launch_bounds__(kF32Threads) f32_forward_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(16) float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + kRows * C::DPP;
+  float* Vs = Ks + 2 * C::TILE;
+  int* oks = reinterpret_cast<int*>(Vs + 2 * C::TILE);
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int split_id = blockIdx.x % a.splits, r0 = (int)(blockIdx.x / a.splits) * kRows;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int len = key_count(a, b);
+  const int tiles = (len + C::BS - 1) / C::BS;
+  const int t0 = (int)((int64_t)tiles * split_id / a.splits);
+  const int t1 = (int)((int64_t)tiles * (split_id + 1) / a.splits);
+  load_queries<T, C, kRows, false>(a, Qs, nullptr, b, hk, r0);
+  const bool active = r0 + 16 * warp < a.rows;   // a warp without rows only loads
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[4 * C::NB][4];
+  clear<C>(o);
+  const float c2 = a.scale * kLog2e;
+  for (int tile = t0; tile < t1; ++tile) {
+    __syncthreads();
+    load_keys<T, C, C::BS, true>(a, Ks, Vs, oks, b, hk, len, tile * C::BS);
+    __syncthreads();
+    if (!active) continue;
+    float s[C::NT][4];
+    scores<C>(Qs + 16 * warp * C::DPP, Ks, s);
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[n][e] = oks[8 * n + 2 * t + e % 2] ? s[n][e] * c2 : -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float top = m[h];
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n) top = fmaxf(top, fmaxf(s[n][2 * h], s[n][2 * h + 1]));
+      top = quad_max(top);
+      const float base = top == -INFINITY ? 0.f : top;   // nothing permitted so far
+      const float f = exp2f(m[h] - base);
+      m[h] = top;
+      float sum = 0.f;
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int e = 2 * h; e < 2 * h + 2; ++e) {
+          s[n][e] = exp2f(s[n][e] - base);
+          sum += s[n][e];
+        }
+      l[h] = l[h] * f + sum;   // of this lane's columns
+#pragma unroll
+      for (int i = 0; i < 4 * C::NB; ++i) {
+        o[i][2 * h] *= f;
+        o[i][2 * h + 1] *= f;
+      }
+    }
+    add_values<C>(s, Vs, o);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] = quad_sum(l[h]);
+    const int r = r0 + 16 * warp + g + 8 * h;
+    if (r >= a.rows) continue;
+    const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == 0.f ? 0.f : l[h]);
+    const float lse = l[h] == 0.f ? -INFINITY : m[h] * kLn2 + logf(l[h]);
+    const int64_t row = ((int64_t)b * a.kv_heads + hk) * a.rows + r;
+    const int64_t at = (int64_t)split_id * a.batch * a.kv_heads * a.rows + row;
+    if (a.splits == 1) {
+      store_result<C>(static_cast<T*>(a.out) + row_offset(a, a.os, b, hk, r), o, h, a.dim, inv);
+      if (a.lse && t == 0) a.lse[row] = lse;
+    } else {
+      store_result<C>(a.part_o + at * a.dim, o, h, a.dim, inv);
+      if (t == 0) a.part_lse[at] = lse;
+    }
+  }
+}
+
+// grid: (key tiles x dkv_splits + row tiles x dq_splits, kv_heads, batch); the first
+// produce dK and dV (own rows: keys; streamed: queries), the others dQ (the reverse).
+template <typename T, typename C>
+__global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(16) float sm[];
+  float* X0 = sm;                        // own: K or Q
+  float* X1 = X0 + kRows * C::DPP;       //      V or dO
+  float* Y0 = X1 + kRows * C::DPP;       // streamed: Q or K
+  float* Y1 = Y0 + 2 * C::TILE;          //           dO or V
+  float* stats = Y1 + 2 * C::TILE;       // dK/dV: lse and delta of the streamed queries
+  int* oks = reinterpret_cast<int*>(stats + 2 * C::BS);   // of the keys, own or streamed
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int len = key_count(a, b);
+  const int dkv_blocks = (a.len_kv + kRows - 1) / kRows * a.dkv_splits;
+  const float c2 = a.scale * kLog2e;
+  const float* lse_row = a.lse_in + ((int64_t)b * a.kv_heads + hk) * a.rows;
+  const float* delta_row = a.delta + ((int64_t)b * a.kv_heads + hk) * a.rows;
+  // past the rows, or a row without keys: P = exp(S - inf) = 0
+  auto lse2 = [&](int r) {
+    const float z = r < a.rows ? lse_row[r] * kLog2e : INFINITY;
+    return z == -INFINITY ? INFINITY : z;
+  };
+  const float *x0 = X0 + 16 * warp * C::DPP, *x1 = X1 + 16 * warp * C::DPP;
+  float p[C::NT][4], ds[C::NT][4];
+  if ((int)blockIdx.x < dkv_blocks) {   // ----------------------------- dK, dV
+    const int k0 = (int)blockIdx.x / a.dkv_splits * kRows, part = (int)blockIdx.x % a.dkv_splits;
+    const int steps = (a.rows + C::BS - 1) / C::BS;
+    const int s0 = (int)((int64_t)steps * part / a.dkv_splits);
+    const int s1 = (int)((int64_t)steps * (part + 1) / a.dkv_splits);
+    float dk[4 * C::NB][4], dv[4 * C::NB][4];
+    clear<C>(dk);
+    clear<C>(dv);
+    if (k0 < len) {
+      load_keys<T, C, kRows, false>(a, X0, X1, oks, b, hk, len, k0);
+      __syncthreads();
+      for (int r0 = s0 * C::BS; r0 < s1 * C::BS; r0 += C::BS) {
+        __syncthreads();
+        load_queries<T, C, C::BS, true>(a, Y0, Y1, b, hk, r0);
+        for (int r = threadIdx.x; r < C::BS; r += kF32Threads) {
+          stats[r] = lse2(r0 + r);
+          stats[C::BS + r] = r0 + r < a.rows ? delta_row[r0 + r] : 0.f;
+        }
+        __syncthreads();
+        if (k0 + 16 * warp >= len) continue;
+        scores<C>(x0, Y0, p);
+        scores<C>(x1, Y1, ds);
+        // (a key that is not permitted has zero rows of K and V; its results are dropped
+        // below)
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int q = 8 * n + 2 * t + e % 2;
+            p[n][e] = exp2f(fmaf(p[n][e], c2, -stats[q]));
+            ds[n][e] = p[n][e] * (ds[n][e] - stats[C::BS + q]);
+          }
+        add_values<C>(p, Y1, dv);
+        add_values<C>(ds, Y0, dk);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int own = 16 * warp + g + 8 * h, key = k0 + own;
+      if (key >= a.len_kv) continue;
+      if (k0 >= len || !oks[own])
+#pragma unroll
+        for (int i = 0; i < 4 * C::NB; ++i)
+#pragma unroll
+          for (int e = 2 * h; e < 2 * h + 2; ++e) dk[i][e] = dv[i][e] = 0.f;
+      if (a.dkv_splits == 1) {
+        store_result<C>(static_cast<T*>(a.dk) + b * a.dks[0] + key * a.dks[1] + hk * a.dks[2], dk, h, a.dim, a.scale);
+        store_result<C>(static_cast<T*>(a.dv) + b * a.dvs[0] + key * a.dvs[1] + hk * a.dvs[2], dv, h, a.dim, 1.f);
+      } else {
+        const int64_t at = ((((int64_t)part * a.batch + b) * a.kv_heads + hk) * a.len_kv + key) * a.dim;
+        store_result<C>(a.part_dk + at, dk, h, a.dim, 1.f);
+        store_result<C>(a.part_dv + at, dv, h, a.dim, 1.f);
+      }
+    }
+    return;
+  }
+  // ---------------------------------------------------------------------- dQ
+  const int id = (int)blockIdx.x - dkv_blocks;
+  const int r0 = id / a.dq_splits * kRows, part = id % a.dq_splits;
+  const int steps = (len + C::BS - 1) / C::BS;
+  const int s0 = (int)((int64_t)steps * part / a.dq_splits);
+  const int s1 = (int)((int64_t)steps * (part + 1) / a.dq_splits);
+  float dq[4 * C::NB][4];
+  clear<C>(dq);
+  load_queries<T, C, kRows, false>(a, X0, X1, b, hk, r0);
+  const bool active = r0 + 16 * warp < a.rows;
+  float lse[2], delta[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + 16 * warp + g + 8 * h;
+    lse[h] = lse2(r);
+    delta[h] = r < a.rows ? delta_row[r] : 0.f;
+  }
+  for (int k0 = s0 * C::BS; k0 < s1 * C::BS; k0 += C::BS) {
+    __syncthreads();
+    load_keys<T, C, C::BS, true>(a, Y0, Y1, oks, b, hk, len, k0);
+    __syncthreads();
+    if (!active) continue;
+    scores<C>(x0, Y0, p);
+    scores<C>(x1, Y1, ds);
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        ds[n][e] = oks[8 * n + 2 * t + e % 2]
+                       ? exp2f(fmaf(p[n][e], c2, -lse[e / 2])) * (ds[n][e] - delta[e / 2])
+                       : 0.f;
+    add_values<C>(ds, Y0, dq);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + 16 * warp + g + 8 * h;
+    if (r >= a.rows) continue;
+    if (a.dq_splits == 1) {
+      store_result<C>(static_cast<T*>(a.dq) + row_offset(a, a.dqs, b, hk, r), dq, h, a.dim, a.scale);
+    } else {
+      const int64_t at = ((((int64_t)part * a.batch + b) * a.kv_heads + hk) * a.rows + r) * a.dim;
+      store_result<C>(a.part_dq + at, dq, h, a.dim, 1.f);
+    }
+  }
+}
+
+template <typename K>
+bool allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+         cudaSuccess;
+}
+template <typename T, typename C>
+kfac_status launch_forward(const Args& a, cudaStream_t st) {
+  static const bool ok = allow_smem(f32_forward_kernel<T, C>, C::FWD);
+  if (!ok) return KFAC_ERR_CUDA;
+  const dim3 grid((unsigned)(cdiv(a.rows, kRows) * a.splits), a.kv_heads, a.batch);
+  launch_pdl(f32_forward_kernel<T, C>, grid, dim3(kF32Threads), C::FWD, st, a);
+  count_launch();
+  return check_launch();
+}
+template <typename T, typename C>
+kfac_status launch_backward(const Args& a, cudaStream_t st) {
+  static const bool ok = allow_smem(f32_backward_kernel<T, C>, C::BWD);
+  if (!ok) return KFAC_ERR_CUDA;
+  const dim3 grid((unsigned)(cdiv(a.len_kv, kRows) * a.dkv_splits + cdiv(a.rows, kRows) * a.dq_splits),
+                  a.kv_heads, a.batch);
+  launch_pdl(f32_backward_kernel<T, C>, grid, dim3(kF32Threads), C::BWD, st, a);
+  count_launch();
+  return check_launch();
+}
+
+}  // namespace
+
+template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st) {
+  return a.dim <= 64 ? launch_forward<T, Cfg<32, 64>>(a, st) : launch_forward<T, Cfg<32, 128>>(a, st);
+}
+template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st) {
+  return a.dim <= 64 ? launch_backward<T, Cfg<32, 64>>(a, st) : launch_backward<T, Cfg<16, 128>>(a, st);
+}
+template kfac_status f32_forward<float>(const Args&, cudaStream_t);
+template kfac_status f32_forward<__nv_bfloat16>(const Args&, cudaStream_t);
+template kfac_status f32_backward<float>(const Args&, cudaStream_t);
+template kfac_status f32_backward<__nv_bfloat16>(const Args&, cudaStream_t);
+
+}  // namespace attn
+}  // namespace kfac
