@@ -30,12 +30,17 @@ constexpr int kRows = 64;        // own rows of a block
 constexpr int kF32Threads = 128;
 constexpr uint32_t kAll = 0xffffffffu;
 
-template <int BS_, int DP_> struct Cfg {
+// STAGED: the forward kernel's next tile is on its way while the present one is multiplied
+// (where shared memory allows it beside three blocks per SM; the backward kernel has no
+// registers for it).
+template <int BS_, int DP_, bool STAGED_ = false> struct Cfg {
+  static constexpr bool STAGED = STAGED_;
   static constexpr int BS = BS_, DP = DP_, DPP = DP + 4;
   static constexpr int NT = BS / 8;    // 8-column tiles of a score row
   static constexpr int NB = DP / 32;   // 32-channel blocks
   static constexpr int TILE = BS * DPP;   // floats of a streamed tile's part
-  static constexpr size_t FWD = sizeof(float) * (kRows * DPP + 4 * TILE) + 4 * BS;
+  static constexpr int STAGE = STAGED ? 2 * BS * DP : 0;   // floats
+  static constexpr size_t FWD = sizeof(float) * (kRows * DPP + 4 * TILE + STAGE) + 4 * BS;
   static constexpr size_t BWD = sizeof(float) * (2 * kRows * DPP + 4 * TILE) + 4 * (2 * BS + kRows);
 };
 
@@ -147,11 +152,32 @@ __device__ __forceinline__ void add_values(const float (&p)[C::NT][4], const flo
   }
 }
 
+// The next step's BS rows of one streamed tensor, on their way to `stage` (fp32 rows of
+// whole 16 bytes only): each thread copies the pieces that it will take from there itself
+// in load_tile, so only its own copies have to have landed.
+template <typename C, typename Off>
+__device__ __forceinline__ void stage_tile(float* stage, const float* src, int dim, Off off) {
+  const int c0 = threadIdx.x % 16;
+#pragma unroll
+  for (int r = threadIdx.x / 16; r < C::BS; r += kF32Threads / 16) {
+    const int64_t o = off(r);
+#pragma unroll
+    for (int c = c0; c < C::DP / 4; c += 16) {
+      const bool real = o >= 0 && 4 * c < dim;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       tc::smem_u32(stage + r * C::DP + 4 * c)),
+                   "l"(reinterpret_cast<uint64_t>(real ? src + o + 4 * c : src)), "r"(real ? 16 : 0)
+                   : "memory");
+    }
+  }
+}
+
 // N rows x dim of global memory -> shared, zeros past dim and where `off` gives none
 // (negative).  16 threads per row, four channels at a time.  kParts: as h parts, and r
 // parts TILE floats behind.
 template <typename T, typename C, int N, bool kParts, typename Off>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, bool vec, Off off) {
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, bool vec,
+                                          const float* stage, Off off) {
   const int c0 = threadIdx.x % 16;
 #pragma unroll 4
   for (int r = threadIdx.x / 16; r < N; r += kF32Threads / 16) {
@@ -161,7 +187,9 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, boo
     for (int c = c0; c < C::DP / 4; c += 16) {
       const int d = 4 * c;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (o >= 0 && d < dim) {
+      if (kParts && stage) {
+        v = *reinterpret_cast<const float4*>(stage + r * C::DP + d);
+      } else if (o >= 0 && d < dim) {
         if (sizeof(T) == 4 && vec) {
           v = *reinterpret_cast<const float4*>(p + d);
         } else {
@@ -181,30 +209,49 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, boo
     }
   }
 }
+// A block's source of keys: offsets of row r of the tile at key0, negative where the key is
+// not permitted.
+struct Keys {
+  const Args& a;
+  int b, len;
+  int64_t kb, vb;
+  __device__ Keys(const Args& a_, int b_, int hk, int len_)
+      : a(a_), b(b_), len(len_), kb(b_ * a_.ks[0] + hk * a_.ks[2]), vb(b_ * a_.vs[0] + hk * a_.vs[2]) {}
+  __device__ __forceinline__ int64_t k(int key) const { return key_ok(a, b, len, key) ? kb + (int64_t)key * a.ks[1] : -1; }
+  __device__ __forceinline__ int64_t v(int key) const { return key_ok(a, b, len, key) ? vb + (int64_t)key * a.vs[1] : -1; }
+};
 // N keys from key0 of k and v, zeros where a key is not permitted; oks[r]: whether it is.
 template <typename T, typename C, int N, bool kParts>
-__device__ __forceinline__ void load_keys(const Args& a, float* Ks, float* Vs, int* oks, int b, int hk,
-                                          int len, int key0) {
-  const int64_t kb = b * a.ks[0] + hk * a.ks[2], vb = b * a.vs[0] + hk * a.vs[2];
-  load_tile<T, C, N, kParts>(Ks, static_cast<const T*>(a.k), a.dim, a.vec, [&](int r) -> int64_t {
-    const bool ok = key_ok(a, b, len, key0 + r);
-    if (threadIdx.x % 16 == 0) oks[r] = ok;
-    return ok ? kb + (int64_t)(key0 + r) * a.ks[1] : -1;
+__device__ __forceinline__ void load_keys(const Keys& src, float* Ks, float* Vs, int* oks, int key0,
+                                          const float* stage) {
+  const Args& a = src.a;
+  load_tile<T, C, N, kParts>(Ks, static_cast<const T*>(a.k), a.dim, a.vec, stage, [&](int r) -> int64_t {
+    const int64_t o = src.k(key0 + r);
+    if (threadIdx.x % 16 == 0) oks[r] = o >= 0;
+    return o;
   });
-  load_tile<T, C, N, kParts>(Vs, static_cast<const T*>(a.v), a.dim, a.vec, [&](int r) -> int64_t {
-    return key_ok(a, b, len, key0 + r) ? vb + (int64_t)(key0 + r) * a.vs[1] : -1;
-  });
+  load_tile<T, C, N, kParts>(Vs, static_cast<const T*>(a.v), a.dim, a.vec,
+                             stage ? stage + C::BS * C::DP : nullptr,
+                             [&](int r) -> int64_t { return src.v(key0 + r); });
 }
+template <typename C>
+__device__ __forceinline__ void stage_keys(const Keys& src, float* stage, int key0) {
+  const Args& a = src.a;
+  stage_tile<C>(stage, static_cast<const float*>(a.k), a.dim, [&](int r) { return src.k(key0 + r); });
+  stage_tile<C>(stage + C::BS * C::DP, static_cast<const float*>(a.v), a.dim, [&](int r) { return src.v(key0 + r); });
+}
+// The same of q and dO (rows of key head hk).
 template <typename T, typename C, int N, bool kParts>
 __device__ __forceinline__ void load_queries(const Args& a, float* Qs, float* Os, int b, int hk, int r0) {
-  load_tile<T, C, N, kParts>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, [&](int r) -> int64_t {
+  load_tile<T, C, N, kParts>(Qs, static_cast<const T*>(a.q), a.dim, a.vec, nullptr, [&](int r) -> int64_t {
     return r0 + r < a.rows ? row_offset(a, a.qs, b, hk, r0 + r) : -1;
   });
   if (Os)
-    load_tile<T, C, N, kParts>(Os, static_cast<const T*>(a.dout), a.dim, a.vec, [&](int r) -> int64_t {
+    load_tile<T, C, N, kParts>(Os, static_cast<const T*>(a.dout), a.dim, a.vec, nullptr, [&](int r) -> int64_t {
       return r0 + r < a.rows ? row_offset(a, a.dos, b, hk, r0 + r) : -1;
     });
 }
+__device__ __forceinline__ void staged() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // One of a lane's two rows (h = 0: g, 1: g + 8) of a result, to a row of T's or of fp32 parts.
 template <typename C, typename T>
@@ -244,7 +291,8 @@ __global__ void __launch_bounds__(kF32Threads) f32_forward_kernel(const __grid_c
   float* Qs = sm;
   float* Ks = Qs + kRows * C::DPP;
   float* Vs = Ks + 2 * C::TILE;
-  int* oks = reinterpret_cast<int*>(Vs + 2 * C::TILE);
+  float* buf = Vs + 2 * C::TILE;
+  int* oks = reinterpret_cast<int*>(buf + C::STAGE);
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -254,6 +302,9 @@ __global__ void __launch_bounds__(kF32Threads) f32_forward_kernel(const __grid_c
   const int tiles = (len + C::BS - 1) / C::BS;
   const int t0 = (int)((int64_t)tiles * split_id / a.splits);
   const int t1 = (int)((int64_t)tiles * (split_id + 1) / a.splits);
+  const Keys keys(a, b, hk, len);
+  const float* stage = C::STAGED && sizeof(T) == 4 && a.vec ? buf : nullptr;
+  if (stage && t0 < t1) stage_keys<C>(keys, buf, t0 * C::BS);
   load_queries<T, C, kRows, false>(a, Qs, nullptr, b, hk, r0);
   const bool active = r0 + 16 * warp < a.rows;   // a warp without rows only loads
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -262,7 +313,9 @@ __global__ void __launch_bounds__(kF32Threads) f32_forward_kernel(const __grid_c
   const float c2 = a.scale * kLog2e;
   for (int tile = t0; tile < t1; ++tile) {
     __syncthreads();
-    load_keys<T, C, C::BS, true>(a, Ks, Vs, oks, b, hk, len, tile * C::BS);
+    if (stage) staged();
+    load_keys<T, C, C::BS, true>(keys, Ks, Vs, oks, tile * C::BS, stage);
+    if (stage && tile + 1 < t1) stage_keys<C>(keys, buf, (tile + 1) * C::BS);
     __syncthreads();
     if (!active) continue;
     float s[C::NT][4];
@@ -343,6 +396,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
   };
   const float *x0 = X0 + 16 * warp * C::DPP, *x1 = X1 + 16 * warp * C::DPP;
   float p[C::NT][4], ds[C::NT][4];
+  const Keys keys(a, b, hk, len);
   if ((int)blockIdx.x < dkv_blocks) {   // ----------------------------- dK, dV
     const int k0 = (int)blockIdx.x / a.dkv_splits * kRows, part = (int)blockIdx.x % a.dkv_splits;
     const int steps = (a.rows + C::BS - 1) / C::BS;
@@ -352,7 +406,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
     clear<C>(dk);
     clear<C>(dv);
     if (k0 < len) {
-      load_keys<T, C, kRows, false>(a, X0, X1, oks, b, hk, len, k0);
+      load_keys<T, C, kRows, false>(keys, X0, X1, oks, k0, nullptr);
       __syncthreads();
       for (int r0 = s0 * C::BS; r0 < s1 * C::BS; r0 += C::BS) {
         __syncthreads();
@@ -418,7 +472,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
   }
   for (int k0 = s0 * C::BS; k0 < s1 * C::BS; k0 += C::BS) {
     __syncthreads();
-    load_keys<T, C, C::BS, true>(a, Y0, Y1, oks, b, hk, len, k0);
+    load_keys<T, C, C::BS, true>(keys, Y0, Y1, oks, k0, nullptr);
     __syncthreads();
     if (!active) continue;
     scores<C>(x0, Y0, p);
@@ -473,9 +527,11 @@ kfac_status launch_backward(const Args& a, cudaStream_t st) {
 }  // namespace
 
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st) {
-  return a.dim <= 64 ? launch_forward<T, Cfg<32, 64>>(a, st) : launch_forward<T, Cfg<32, 128>>(a, st);
+  if (a.dim <= 32) return launch_forward<T, Cfg<64, 32, true>>(a, st);
+  return a.dim <= 64 ? launch_forward<T, Cfg<32, 64, true>>(a, st) : launch_forward<T, Cfg<32, 128>>(a, st);
 }
 template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st) {
+  if (a.dim <= 32) return launch_backward<T, Cfg<32, 32>>(a, st);
   return a.dim <= 64 ? launch_backward<T, Cfg<32, 64>>(a, st) : launch_backward<T, Cfg<16, 128>>(a, st);
 }
 template kfac_status f32_forward<float>(const Args&, cudaStream_t);
