@@ -68,10 +68,8 @@ def _heads(what, name, t, dtype, shape, dev):
 
 def _call(f, what, dev, stream, *args):
     """f(*args, stream) on the tensors' device (the library works on the current one)."""
-    if stream is None:
-        s = _raw_stream(dev)
-    else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
+    s = _raw_stream(dev) if stream is None else (
+        stream if isinstance(stream, int) else stream.cuda_stream)
     if dev == _current_device():
         code = f(*args, s)
     else:
@@ -132,19 +130,26 @@ def rope(q, k, table, positions=None, position_offset: int = 0, interleaved: boo
     h = kv = 0
     qs = ks = oqs = oks = (0, 0, 0, 0)
     if q is not None:
-        shape = q.shape
+        shape, qs = q.shape, q.stride()
         h = shape[2]
-        qs = _heads("rope", "q", q, dtype, shape, dev)
         if out_q is None:
             out_q = made_q = torch.empty(shape, dtype=dtype, device=q.device)
-        oqs = _heads("rope", "out_q", out_q, dtype, shape, dev)
+        oqs = out_q.stride()
+        if out_q.shape != shape or out_q.dtype is not dtype or out_q.get_device() != dev or (
+                d > 1 and (qs[3] != 1 or oqs[3] != 1)):
+            _heads("rope", "q", q, dtype, shape, dev)
+            _heads("rope", "out_q", out_q, dtype, shape, dev)
     if k is not None:
-        kv = k.shape[2]
-        shape = (b, n, kv, d)
-        ks = _heads("rope", "k", k, dtype, shape, dev)
+        shape, ks = k.shape, k.stride()
+        kb, kn, kv, kd = shape
         if out_k is None:
             out_k = made_k = torch.empty(shape, dtype=dtype, device=k.device)
-        oks = _heads("rope", "out_k", out_k, dtype, shape, dev)
+        oks = out_k.stride()
+        if kb != b or kn != n or kd != d or k.dtype is not dtype or k.get_device() != dev or (
+                out_k.shape != shape or out_k.dtype is not dtype or out_k.get_device() != dev) or (
+                d > 1 and (ks[3] != 1 or oks[3] != 1)):
+            _heads("rope", "k", k, dtype, (b, n, kv, d), dev)
+            _heads("rope", "out_k", out_k, dtype, (b, n, kv, d), dev)
     ps, pp = 0, None
     if positions is not None:
         if positions.dtype is not torch.int32 or positions.shape not in ((b, n), (n,)) or (
@@ -224,14 +229,14 @@ def _attention(what, q, k, v, out, scale, dev):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError(f"{what}: q [batch, len_q, heads, head_dim], k [batch, len_kv, kv_heads, "
                          f"head_dim]")
-    dtype, shape = q.dtype, q.shape
+    dtype, shape, keys = q.dtype, q.shape, k.shape
     b, nq, h, d = shape
-    _, nk, kv, _ = k.shape
-    keys = (b, nk, kv, d)
-    qs = q.stride()
-    if qs[3] != 1 and d > 1:
-        raise ValueError(f"{what}: q's channels are not contiguous (stride {qs[3]})")
-    ks = _heads(what, "k", k, dtype, keys, dev)
+    kb, nk, kv, kd = keys
+    qs, ks = q.stride(), k.stride()
+    if kb != b or kd != d or k.dtype is not dtype or k.get_device() != dev or (
+            d > 1 and (ks[3] != 1 or qs[3] != 1)):
+        _heads(what, "q", q, dtype, shape, dev)
+        _heads(what, "k", k, dtype, (b, nk, kv, d), dev)
     vs = _heads(what, "v", v, dtype, keys, dev) if v is not None else ks
     os = _heads(what, "out", out, dtype, shape, dev) if out is not None else qs
     return ATTENTION_DESC.pack(_dtype(q, what), b, nq, nk, h, kv, d,

@@ -50,6 +50,7 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
 
 // Few query rows (bf16, rows that tc_forward_ok accepts).
 constexpr int kTokenWarps = 4;
+constexpr int kTokenPerSm = 3;      // resident blocks per SM
 constexpr int kTokenCluster = 8;    // parts that one cluster joins
 kfac_status token_forward(const Args& a, cudaStream_t st);
 

@@ -462,17 +462,17 @@ constexpr int kTokenRows = 64;
 bool token_sizes(const kfac_attention_desc& d) {
   return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q <= kTokenRows;
 }
-// Parts of the key axis for the token kernel: as many blocks as are resident at once
-// (two per SM) - no more for equal lengths, where a second wave of a few blocks costs as
-// much as a whole one, and at least as many for ragged ones, which a part more evens out
-// (32 x 8192 keys on 4 key heads: 85 us in 2 parts and 116 us in 3; ragged, 81 and 67).
-// Each warp has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a
-// cluster, more are fixed lengths.
+// Parts of the key axis for the token kernel: as many blocks as are resident at once - no
+// more for equal lengths, where a second wave of a few blocks costs as much as a whole
+// one, and at least as many for ragged ones, which a part more evens out (32 x 8192 keys
+// on 4 key heads x 128: 84 us in 3 parts and 113 us in 4; ragged, 72 and 61).  Each warp
+// has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a cluster,
+// more are fixed lengths.
 int token_splits(const kfac_attention_desc& d, bool ragged, int* part_keys) {
   const int64_t ctas = std::max<int64_t>(
       1, cdiv((int64_t)d.heads / d.kv_heads * d.len_q, 16) * d.kv_heads * d.batch);
   const int step = 16 * kTokenWarps;
-  const int64_t most = std::max<int64_t>(1, cdiv(d.len_kv, step)), slots = 2 * num_sms();
+  const int64_t most = std::max<int64_t>(1, cdiv(d.len_kv, step)), slots = kTokenPerSm * num_sms();
   int64_t parts = std::min<int64_t>(most, ragged ? cdiv(slots, ctas) : std::max<int64_t>(1, slots / ctas));
   *part_keys = d.len_kv;
   if (parts > kTokenCluster) {

@@ -2,8 +2,9 @@
 // states.  rows = heads of a group x queries, 16 of them per block.
 //
 // Bound by memory: k and v are read once, at 2 flop per byte and row.  Each warp walks
-// 16 keys at a time through a ring of its own in shared memory (16-byte cp.async, two
-// steps ahead, no block-wide barrier): S = q k^T and O += P v by mma.sync m16n8k16 on
+// 16 keys at a time through a ring of its own in shared memory (16-byte cp.async, one
+// step ahead, no block-wide barrier; 128 channels: 65 KB a block, three blocks per SM -
+// two steps ahead and two blocks took 67 us where this takes 61): S = q k^T and O += P v by mma.sync m16n8k16 on
 // fragments that ldmatrix reads, rows swizzled so that eight rows of one 16-byte
 // column hit all banks.  Keys that are not permitted are filled with zeros, their
 // scores are -infinity.  P enters as two bf16 parts (high and remainder): the second
@@ -21,7 +22,7 @@ namespace attn {
 namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -82,7 +83,7 @@ template <int DC> struct TokenCfg {            // dim <= 32 DC
 // cluster and share the sequence's length; otherwise part s takes keys
 // [s, s + 1) x part_keys.
 template <int DC, bool kCluster>
-__global__ void __launch_bounds__(kTokenWarps * 32)
+__global__ void __launch_bounds__(kTokenWarps * 32, kTokenPerSm)
 token_kernel(const __grid_constant__ Args a) {
   using C = TokenCfg<DC>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -163,7 +164,7 @@ token_kernel(const __grid_constant__ Args a) {
 
   int stage = 0;
   for (int key0 = begin; key0 < last; key0 += step) {
-    // the stage that the previous step has read takes the keys two steps ahead
+    // the stage that the previous step has read takes the keys kStages - 1 steps ahead
     const int ahead = key0 + (kStages - 1) * step;
     words[kStages - 1] = word(ahead, byte);
     byte = mask_byte(ahead + step);
