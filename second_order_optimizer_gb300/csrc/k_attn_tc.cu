@@ -499,9 +499,11 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 // dP(i+1), and dS(i) under dV(i) and S(i+1).
 //
 // dQ block: 128 queries of one head, all tiles of permitted keys.  One lane per query:
-//   S = Q K^T (two buffers, columns 0.. and 128..), dP = dO V^T (256..)
+//   S = Q K^T (columns 0..), dP = dO V^T (two buffers, 128.. and 256..)
 //   dS = P (dP - delta) over dP; dQ += dS K (384..)
-// Issuing order S(j+1), dQ(j), dP(j+1).
+// Issuing order S(j+1), dP(j+1), dQ(j): S is free once it has been read, so both operands
+// of dS(j+1) are there when dS(j) is done.  (With two buffers of S and one of dP, dP(j+1)
+// waited for dQ(j): 2870 cycles a step; three products of 128 x 128 x 128 take 1536.)
 //
 // Two groups of four warps share a tile's columns, 64 each.
 constexpr int kBwdBars = 26;   // then the TMEM slot and abort flag, then the mask words
@@ -774,8 +776,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   using C = BwdCfg<NC>;
   uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
   uint64_t *qg_full = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7,
-           *v_empty = bars + 9, *dp_full = bars + 12, *ds_ready = bars + 14, *s_full = bars + 15,
-           *done = bars + 19, *k_ready = bars + 20, *w_full = bars + 23;
+           *v_empty = bars + 9, *dp_full = bars + 11, *s_read = bars + 13, *ds_ready = bars + 14,
+           *s_full = bars + 15, *done = bars + 19, *k_ready = bars + 20, *w_full = bars + 23;
   uint4* words = reinterpret_cast<uint4*>(bars + 28);   // [3] permitted keys of a tile
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
@@ -826,28 +828,32 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       auto scores = [&](int j) {
         const int s = j % 3;
         if (!wait(&k_ready[s], (uint32_t)(j / 3) & 1u)) return false;
-        mma_scores(leader, tmem + 128 * (j % 2), Qs, Ks + s * C::TILE, ksteps);
-        tc::umma_commit_by(leader, &s_full[j % 2]);
+        mma_scores(leader, tmem, Qs, Ks + s * C::TILE, ksteps);
+        tc::umma_commit_by(leader, s_full);
         return true;
       };
       auto grads = [&](int j) {
         const int s = j % 2;
         if (!wait(&v_full[s], (uint32_t)(j / 2) & 1u)) return false;
-        mma_scores(leader, tmem + 256, Gs, Vs + s * C::TILE, ksteps);
-        tc::umma_commit_by(leader, dp_full);
+        mma_scores(leader, tmem + 128 + 128 * (j % 2), Gs, Vs + s * C::TILE, ksteps);
+        tc::umma_commit_by(leader, &dp_full[j % 2]);
         tc::umma_commit_by(leader, &v_empty[s]);
         return true;
       };
       bool ok = wait(qg_full, 0) && scores(0) && grads(0);
       for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n && !(ok = scores(j + 1))) break;
+        if (j + 1 < n) {   // S has been read; dS(j - 1), in dP's other buffer, multiplied
+          if (!(ok = wait(s_read, (uint32_t)j & 1u))) break;
+          tc::tc_fence_after();
+          if (!(ok = scores(j + 1) && grads(j + 1))) break;
+        }
         if (!(ok = wait(ds_ready, (uint32_t)j & 1u))) break;
         tc::tc_fence_after();
         for (int u = 0; u < 2; ++u)
-          mma_values(leader, tmem + 384, tmem + 256 + 64 * u, Ks + j % 3 * C::TILE + u * kHalf, idesc, j > 0 || u > 0);
+          mma_values(leader, tmem + 384, tmem + 128 + 128 * (j % 2) + 64 * u, Ks + j % 3 * C::TILE + u * kHalf,
+                     idesc, j > 0 || u > 0);
         tc::umma_commit_by(leader, &k_empty[j % 3]);
         if (j + 1 == n) tc::umma_commit_by(leader, done);
-        else ok = grads(j + 1);
       }
     }
   } else if (warp == 2) {  // ----------------------------------------------- key mask
@@ -878,7 +884,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   } else {  // -------------------------------------------------------- dS
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-    const uint32_t td = tmem + lanes + 256 + 64 * half;
+    const uint32_t ts = tmem + lanes + 64 * half;
     const int q = q0 + 32 * (warp % 4) + lane;
     const int64_t row = ((int64_t)b * a.heads + h) * a.len_q + q;
     const bool in = q < a.len_q;
@@ -889,7 +895,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     const F2 cc2 = f2(c2, c2), nl2 = f2(-lse, -lse), nd2 = f2(-delta, -delta);
     bool ok = true;
     for (int j = 0; j < n; ++j) {
-      ok = __all_sync(kFull, tc::mbar_wait(&s_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag) &&
+      ok = __all_sync(kFull, tc::mbar_wait(s_full, (uint32_t)j & 1u, abort_flag) &&
                                  (!a.key_mask || tc::mbar_wait(&w_full[j % 3], (uint32_t)(j / 3) & 1u,
                                                                abort_flag)));
       if (!ok) break;
@@ -901,13 +907,16 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
       } else {
         len_words(len, (first + j) * BT, w);
       }
-      const uint32_t ts = tmem + lanes + 128 * (j % 2) + 64 * half;
+      const uint32_t td = ts + 128 + 128 * (j % 2);
       uint32_t r[2][32];
       tc::tmem_ld32_issue(ts, r[0]);
       tc::tmem_ld32_issue(ts + 32, r[1]);
       tc::tmem_ld_wait();
       tc::tmem_ld_use(r[0]);
       tc::tmem_ld_use(r[1]);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(s_read);
       F2 p[32];
 #pragma unroll
       for (int c = 0; c < 32; ++c) {
@@ -915,7 +924,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         unpack(fma2(f2(r[c / 16][2 * c % 32], r[c / 16][2 * c % 32 + 1]), cc2, nl2), &x, &y);
         p[c] = f2(ex2(x), ex2(y));
       }
-      ok = __all_sync(kFull, tc::mbar_wait(dp_full, (uint32_t)j & 1u, abort_flag));
+      ok = __all_sync(kFull, tc::mbar_wait(&dp_full[j % 2], (uint32_t)(j / 2) & 1u, abort_flag));
       if (!ok) break;
       tc::tc_fence_after();
       tc::tmem_ld32_issue(td, r[0]);
@@ -981,7 +990,7 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   const int tile = id % tiles, split = id / tiles % splits, pair = id / tiles / splits;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBwdBars; ++i) {
-      // 13: p_ready, 14: ds_ready (one arrival per warp of the two groups);
+      // 13: p_ready or s_read, 14: ds_ready (one arrival per warp of the two groups);
       // 17, 18: the dK/dV role's st_empty (the same)
       const bool warps = i == 13 || i == 14 || i == 17 || i == 18;
       tc::mbar_init(&bars[i], warps ? 8 : 1);
