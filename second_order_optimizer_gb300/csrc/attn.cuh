@@ -61,6 +61,7 @@ template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st);
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
 bool tc_forward_ok(const Args& a);
 kfac_status tc_forward(const Args& a, cudaStream_t st);
+int tc_forward_tiles(int dim, int len_q, int len_kv);   // of 128 queries per block: 1 or 2
 bool tc_backward_ok(const Args& a);
 kfac_status tc_backward(const Args& a, cudaStream_t st);   // a.delta already written
 

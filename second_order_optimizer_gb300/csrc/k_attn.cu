@@ -452,8 +452,11 @@ int plain_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
   return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, 3, d.len_kv, 64);
 }
+// (a part of fewer than 512 keys costs more to join than it saves: 2 x 300 queries, 300
+// keys, 8 heads x 64: 10 us unsplit, 15 us in three parts)
 int tc_splits(const kfac_attention_desc& d) {
-  return pick_splits((int64_t)cdiv(d.len_q, 256) * d.heads * d.batch, 1, d.len_kv, 128);
+  const int tiles = tc_forward_tiles(d.head_dim, d.len_q, d.len_kv);
+  return pick_splits((int64_t)cdiv(d.len_q, 128 * tiles) * d.heads * d.batch, tiles == 1 ? 2 : 1, d.len_kv, 512);
 }
 // The form of the forward pass for bf16 rows that TMA and 16-byte loads can address.
 // Few rows: the token kernel reads k and v once per 16 rows, while the tensor-core

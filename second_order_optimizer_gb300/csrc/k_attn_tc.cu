@@ -168,36 +168,41 @@ constexpr int kHalf = 64 * 128;   // bytes from a tile's row 0 to its row 64
 
 // ------------------------------------------------------------------------- forward
 //
-// A block takes two tiles of 128 queries of one head against the keys of its part:
+// A block takes NT tiles of 128 queries of one head against the keys of its part:
 //   S_t = Q_t K^T          128 x 128 x dim, TMEM columns [128 t, 128 t + 128)
 //   P_t = exp(S_t - m_t)   one thread per row: no shuffles for the maximum or the sum
-//   O_t += P_t V           128 x dim x 128, TMEM columns [256 + 64 NC t, ...)
-// Two tiles so that one's exponentials run under the other's products.  The chain of a
-// tile - S, exponentials, P V, S - is what bounds the kernel, so it is kept short: P is
-// handed over in halves of 64 keys, and a half's exponentials do not wait for its
-// maximum.  They are taken against the row's reference maximum m_t so far; only when
-// the half's own maximum, found alongside, has grown past it are they taken again and
-// O_t, l_t rescaled: by more than 2^8 in a tile's first half, where O_t is at rest,
-// 2^90 in its second, where the products of the first must first end.  A reference
-// that lags changes no result: P and the sums are floating point (P <= 2^90, sums of
-// at most 2^30 of them).
-template <int NC> struct FwdCfg {
+//   O_t += P_t V           128 x dim x 128, TMEM columns [128 NT + 64 NC t, ...)
+// Two tiles (or two blocks of one) per SM, so that one's exponentials run under the
+// other's products.  The chain of a tile - S, exponentials, P V, S - is what bounds the
+// kernel, so it is kept short: P is handed over in halves of 64 keys, and a half's
+// exponentials do not wait for its maximum.  They are taken against the row's reference
+// maximum m_t so far; only when the half's own maximum, found alongside, has grown past it
+// are they taken again and O_t, l_t rescaled: by more than 2^8 in a tile's first half,
+// where O_t is at rest, 2^90 in its second, where the products of the first must first
+// end.  A reference that lags changes no result: P and the sums are floating point
+// (P <= 2^90, sums of at most 2^30 of them).
+// Measured on 8 x 2048 queries, 4096 keys (half of them permitted), 16 heads x 128: 208 us,
+// 1480 TFLOP/s.  What was tried and cost more: S in two buffers of 64 keys (272 us: twice the
+// hand-overs), two groups of warps per tile (232 us).
+template <int NC, int NT> struct FwdCfg {
   static constexpr int TILE = NC * kChunk;
-  static constexpr int STAGES = NC == 1 ? 3 : 2;
-  static constexpr size_t SMEM = (size_t)(2 + 2 * STAGES) * TILE + 512;
+  static constexpr int THREADS = 128 + 128 * NT;
+  static constexpr int STAGES = (NC == 1 ? 3 : 2) - (NT == 1 ? 1 : 0);
+  static constexpr int TMEM = 256 * NT, OCOL = 128 * NT;   // columns, and where O starts
+  static constexpr size_t SMEM = (size_t)(NT + 2 * STAGES) * TILE + 512;
 };
 constexpr float kGrow0 = 8.f, kGrow1 = 90.f;
 
-template <int NC>
-__global__ void __launch_bounds__(kTcThreads, 1)
+template <int NC, int NT>
+__global__ void __launch_bounds__(FwdCfg<NC, NT>::THREADS, 3 - NT)
 tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap mq,
                   const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const MapMul xq, const MapMul xk, const MapMul xv) {
-  using C = FwdCfg<NC>;
+  using C = FwdCfg<NC, NT>;
   constexpr int ST = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];   // the 128-byte swizzle's period
   uint8_t* Qs = smem;
-  uint8_t* Ks = Qs + 2 * C::TILE;
+  uint8_t* Ks = Qs + NT * C::TILE;
   uint8_t* Vs = Ks + ST * C::TILE;
   uint64_t* bars = reinterpret_cast<uint64_t*>(Vs + ST * C::TILE);
   uint64_t *q_full = bars, *k_full = q_full + 2, *k_empty = k_full + ST, *v_full = k_empty + ST,
@@ -229,7 +234,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
     tc::fence_mbar_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_alloc(tmem_slot, C::TMEM);
     tc::tmem_relinquish();
   }
   tc::tc_fence_before();
@@ -240,9 +245,9 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   pdl_trigger();
 
   const int split = (int)(blockIdx.x % a.splits);
-  const int q0 = (int)(blockIdx.x / a.splits) * 2 * BT, h = blockIdx.y, b = blockIdx.z;
+  const int q0 = (int)(blockIdx.x / a.splits) * NT * BT, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / a.group;
-  const int nt = q0 + BT < a.len_q ? 2 : 1;
+  const int nt = NT == 2 && q0 + BT < a.len_q ? 2 : 1;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
   const int tiles = (len + BT - 1) / BT;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
@@ -303,7 +308,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
           for (int half = 0; half < 2; ++half) {
             if (!(ok = wait(&p_ready[2 * t + half], (uint32_t)j & 1u))) break;
             tc::tc_fence_after();
-            mma_values(leader, tmem + 256 + 64 * NC * t, tmem + 128 * t + 32 * half,
+            mma_values(leader, tmem + C::OCOL + 64 * NC * t, tmem + 128 * t + 32 * half,
                        Vs + s * C::TILE + half * kHalf, idesc_o, j > 0 || half > 0);
             if (half == 0) tc::umma_commit_by(leader, &half_done[t]);
           }
@@ -347,7 +352,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   if ((warp - 4) / 4 < nt) {  // ---------------------------------- softmax, epilogue
     const int t = (warp - 4) / 4;
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-    const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 64 * NC * t + lanes;
+    const uint32_t ts = tmem + 128 * t + lanes, to = tmem + C::OCOL + 64 * NC * t + lanes;
     const float c2 = a.scale * kLog2e;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -481,7 +486,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   }
   }
   __syncthreads();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc(tmem, C::TMEM);
 }
 
 // ------------------------------------------------------------------------ backward
@@ -1044,10 +1049,10 @@ bool rows_ok(const void* p, const int64_t* s, int rows, int heads, int batch) {
   return rows <= 1 || s[1] > 0;
 }
 
-template <int NC>
+template <int NC, int NT>
 kfac_status launch_tc_forward(const Args& a, cudaStream_t st) {
-  using C = FwdCfg<NC>;
-  static const bool ok = cudaFuncSetAttribute(tc_forward_kernel<NC>,
+  using C = FwdCfg<NC, NT>;
+  static const bool ok = cudaFuncSetAttribute(tc_forward_kernel<NC, NT>,
                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               (int)C::SMEM) == cudaSuccess;
   CUtensorMap mq, mk, mv;
@@ -1056,8 +1061,8 @@ kfac_status launch_tc_forward(const Args& a, cudaStream_t st) {
       !make_map(&mk, &xk, a.k, a.ks, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&mv, &xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch))
     return KFAC_ERR_CUDA;
-  const dim3 grid((unsigned)(cdiv(a.len_q, 2 * BT) * a.splits), a.heads, a.batch);
-  launch_pdl(tc_forward_kernel<NC>, grid, dim3(kTcThreads), C::SMEM, st, a, mq, mk, mv, xq, xk, xv);
+  const dim3 grid((unsigned)(cdiv(a.len_q, NT * BT) * a.splits), a.heads, a.batch);
+  launch_pdl(tc_forward_kernel<NC, NT>, grid, dim3(C::THREADS), C::SMEM, st, a, mq, mk, mv, xq, xk, xv);
   count_launch();
   return check_launch();
 }
@@ -1092,8 +1097,20 @@ bool tc_forward_ok(const Args& a) {
          rows_ok(a.out, a.os, a.len_q, a.heads, a.batch);
 }
 
+// Query tiles per block.  One (two blocks per SM) up to 64 channels, where the
+// exponentials bound the kernel and two independent blocks hide each other's chains (2 x
+// 2432 queries, 4096 keys, 16 heads x 64: 88 us, with two tiles 121 us), and where a block's
+// walk is short and its set-up and end weigh (14 x 316 queries, 35 keys, 32 heads x 128: 35 us
+// against 42 us).  Two where the products bound it and share each tile of keys (8 x 2048
+// queries, 4096 keys, 16 heads x 128: 220 us against 241 us).
+int tc_forward_tiles(int dim, int len_q, int len_kv) {
+  return dim <= 64 || len_q <= BT || len_kv <= 2 * BT ? 1 : 2;
+}
+
 kfac_status tc_forward(const Args& a, cudaStream_t st) {
-  return a.dim <= 64 ? launch_tc_forward<1>(a, st) : launch_tc_forward<2>(a, st);
+  if (a.dim <= 64) return launch_tc_forward<1, 1>(a, st);
+  return tc_forward_tiles(a.dim, a.len_q, a.len_kv) == 1 ? launch_tc_forward<2, 1>(a, st)
+                                                         : launch_tc_forward<2, 2>(a, st);
 }
 
 bool tc_backward_ok(const Args& a) {
