@@ -502,6 +502,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 //   dS^T = P^T (dP^T - delta) over dP^T; dK += dS^T Q   (columns 256 + 64 NC..)
 // The issuing order dP(i), dV(i), S(i+1), dK(i) lets P(i+1) run under dK(i) and
 // dP(i+1), and dS(i) under dV(i) and S(i+1).
+// With 64 channels, where the exponentials are the longer part, there is room for a second
+// S: dP(i), S(i+1), dV(i), dK(i) - the score warps never wait for S.
 //
 // dQ block: 128 queries of one head, all tiles of permitted keys.  One lane per query:
 //   S = Q K^T (columns 0..), dP = dO V^T (two buffers, 128.. and 256..)
@@ -558,9 +560,13 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   uint8_t *Ks = smem, *Vs = Ks + C::TILE, *Qs = Vs + C::TILE, *Gs = Qs + 3 * C::TILE;
   float* stats = reinterpret_cast<float*>(Gs + 2 * C::TILE);   // [2][lse 128, delta 128]
   uint64_t *kv_full = bars, *q_full = bars + 1, *q_empty = bars + 4, *g_full = bars + 7,
-           *g_empty = bars + 9, *s_full = bars + 11, *dp_full = bars + 12, *p_ready = bars + 13,
+           *g_empty = bars + 9, *dp_full = bars + 12, *p_ready = bars + 13,
            *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19,
            *kv_ready = bars + 20;
+  // S^T of step i: one buffer, or with 64 channels two (the second behind dK)
+  auto s_full = [&](int i) { return NC == 1 && i % 2 ? bars + 21 : bars + 11; };
+  auto s_phase = [&](int i) { return (uint32_t)(NC == 1 ? i / 2 : i) & 1u; };
+  auto s_at = [&](int i) { return tmem + (NC == 1 && i % 2 ? 384u : 0u); };
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int k0 = tile * BT;
   const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
@@ -610,8 +616,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
       };
       bool ok = wait(kv_ready, 0) && wait(&q_full[0], 0);
       if (ok) {
-        mma_scores(leader, tmem, Ks, Qs, ksteps);
-        tc::umma_commit_by(leader, s_full);
+        mma_scores(leader, s_at(0), Ks, Qs, ksteps);
+        tc::umma_commit_by(leader, s_full(0));
       }
       for (int i = 0; i < n && ok; ++i) {
         const int sq = i % 3, sg = i % 2, s1 = (i + 1) % 3;
@@ -619,16 +625,20 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         if (!(ok = wait(&g_full[sg], (uint32_t)(i / 2) & 1u))) break;
         mma_scores(leader, tmem + 128, Vs, Gs + sg * C::TILE, ksteps);
         tc::umma_commit_by(leader, dp_full);
+        auto next_scores = [&]() {
+          if (i + 1 == n) return true;
+          if (!wait(&q_full[s1], (uint32_t)((i + 1) / 3) & 1u)) return false;
+          mma_scores(leader, s_at(i + 1), Ks, Qs + s1 * C::TILE, ksteps);
+          tc::umma_commit_by(leader, s_full(i + 1));
+          return true;
+        };
+        if (NC == 1 && !(ok = next_scores())) break;
         if (!(ok = wait(p_ready, ph))) break;
         tc::tc_fence_after();
         for (int u = 0; u < 2; ++u)
-          mma_values(leader, tmem + 256, tmem + 64 * u, Gs + sg * C::TILE + u * kHalf, idesc, i > 0 || u > 0);
+          mma_values(leader, tmem + 256, s_at(i) + 64 * u, Gs + sg * C::TILE + u * kHalf, idesc, i > 0 || u > 0);
         tc::umma_commit_by(leader, &g_empty[sg]);
-        if (i + 1 < n) {
-          if (!(ok = wait(&q_full[s1], (uint32_t)((i + 1) / 3) & 1u))) break;
-          mma_scores(leader, tmem, Ks, Qs + s1 * C::TILE, ksteps);
-          tc::umma_commit_by(leader, s_full);
-        }
+        if (NC == 2 && !(ok = next_scores())) break;
         if (!(ok = wait(ds_ready, ph))) break;
         tc::tc_fence_after();
         for (int u = 0; u < 2; ++u)
@@ -679,7 +689,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   } else {  // ----------------------------------------------- P^T and dS^T
     const int half = (warp - 4) / 4;   // columns [64 half, 64 half + 64)
     const uint32_t lanes = (uint32_t)(warp % 4) * 32 << 16;
-    const uint32_t ts = tmem + lanes + 64 * half, td = ts + 128;
+    const uint32_t td = tmem + lanes + 128 + 64 * half;
     const int key = k0 + 32 * (warp % 4) + lane;
     const bool mine = key_ok(a, b, len, key);
     const float c2 = a.scale * kLog2e;
@@ -691,9 +701,10 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
       const float4* lse = reinterpret_cast<const float4*>(stats + s * 2 * BT + 64 * half);
       const float4* delta = lse + BT / 4;
       ok = __all_sync(kFull, tc::mbar_wait(&st_full[s], (uint32_t)(i / 2) & 1u, abort_flag) &&
-                                 tc::mbar_wait(s_full, ph, abort_flag));
+                                 tc::mbar_wait(s_full(i), s_phase(i), abort_flag));
       if (!ok) break;
       tc::tc_fence_after();
+      const uint32_t ts = s_at(i) + lanes + 64 * half;
       uint32_t r[2][32];
       tc::tmem_ld32_issue(ts, r[0]);
       tc::tmem_ld32_issue(ts + 32, r[1]);
