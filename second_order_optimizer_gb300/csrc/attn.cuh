@@ -53,10 +53,16 @@ constexpr int kTokenWarps = 4;
 constexpr int kTokenPerSm = 3;      // resident blocks per SM
 constexpr int kTokenCluster = 8;    // parts that one cluster joins
 kfac_status token_forward(const Args& a, cudaStream_t st);
+// delta from P dP, of batch entries with at most kExactKeys permitted keys alone (bf16, the
+// tensors of tc_backward_ok).
+constexpr int kExactKeys = 128;
+kfac_status delta_keys(const Args& a, cudaStream_t st);
 
 // fp32 arithmetic: forward of more than 16 rows, and backward (a.delta already written).
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st);
 template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st);
+// delta = sum_j P_j dP_j whatever the number of keys (bf16 inputs, whose out is rounded).
+kfac_status f32_delta(const Args& a, cudaStream_t st);
 
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.
 bool tc_forward_ok(const Args& a);

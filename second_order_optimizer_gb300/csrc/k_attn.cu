@@ -413,18 +413,34 @@ kfac_status plain_forward(Args a, cudaStream_t st) {
 }
 
 template <typename T>
-kfac_status backward(Args a, cudaStream_t st) {
+kfac_status launch_delta(Args a, cudaStream_t st) {
   constexpr int V = 16 / (int)sizeof(T);
+  const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
   a.vec = vec_rows(a.o, a.os, a.len_q, a.heads, a.batch, a.dim, V) &&
           vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, V);
+  launch_pdl(delta_kernel<T, 8>, dim3((unsigned)cdiv(n, 32)), dim3(256), 0, st, a);
+  count_launch();
+  return check_launch();
+}
+
+template <typename T>
+kfac_status backward(Args a, cudaStream_t st) {
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
+  const bool bf16 = sizeof(T) == 2, tc = bf16 && tc_backward_ok(a);
   if (n > 0) {
-    launch_pdl(delta_kernel<T, 8>, dim3((unsigned)cdiv(n, 32)), dim3(256), 0, st, a);
-    count_launch();
-    if (kfac_status e = check_launch()) return e;
+    // bf16: out is rounded, and with few keys delta has to be better than that
+    kfac_status e = KFAC_OK;
+    if (bf16 && !tc) {
+      e = f32_delta(a, st);
+    } else {
+      const bool all_few = tc && a.len_kv <= kExactKeys;
+      if (!all_few) e = launch_delta<T>(a, st);
+      if (e == KFAC_OK && tc && (all_few || a.kv_len || a.key_mask)) e = delta_keys(a, st);
+    }
+    if (e != KFAC_OK) return e;
   }
   kfac_status e;
-  if (sizeof(T) == 2 && tc_backward_ok(a)) {
+  if (tc) {
     e = tc_backward(a, st);
   } else {
     a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&

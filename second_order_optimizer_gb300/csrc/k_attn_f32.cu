@@ -499,6 +499,53 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
   }
 }
 
+// delta of bf16 inputs (sum_d dout out would carry out's rounding into every dS): the first
+// half of a dQ block.  grid: (row tiles, kv_heads, batch)
+template <typename T, typename C>
+__global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_constant__ Args a) {
+  extern __shared__ __align__(16) float sm[];
+  float* X0 = sm;
+  float* X1 = X0 + kRows * C::DPP;
+  float* Y0 = X1 + kRows * C::DPP;
+  float* Y1 = Y0 + 2 * C::TILE;
+  int* oks = reinterpret_cast<int*>(Y1 + 2 * C::TILE);
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int hk = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * kRows;
+  const int len = key_count(a, b);
+  const float c2 = a.scale * kLog2e;
+  const int64_t row0 = ((int64_t)b * a.kv_heads + hk) * a.rows;
+  load_queries<T, C, kRows, false>(a, X0, X1, b, hk, r0);
+  float lse2[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = r0 + 16 * warp + g + 8 * h;
+    lse2[h] = r < a.rows ? a.lse_in[row0 + r] * kLog2e : INFINITY;
+  }
+  const Keys keys(a, b, hk, len);
+  for (int k0 = 0; k0 < len; k0 += C::BS) {
+    __syncthreads();
+    load_keys<T, C, C::BS, true>(keys, Y0, Y1, oks, k0, nullptr);
+    __syncthreads();
+    float p[C::NT][4], dp[C::NT][4];
+    scores<C>(X0 + 16 * warp * C::DPP, Y0, p);
+    scores<C>(X1 + 16 * warp * C::DPP, Y1, dp);
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (oks[8 * n + 2 * t + e % 2])
+          sum[e / 2] = fmaf(exp2f(fmaf(p[n][e], c2, -lse2[e / 2])), dp[n][e], sum[e / 2]);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float d = quad_sum(sum[h]);
+    const int r = r0 + 16 * warp + g + 8 * h;
+    if (t == 0 && r < a.rows) a.delta[row0 + r] = d;
+  }
+}
+
 template <typename K>
 bool allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
@@ -524,6 +571,16 @@ kfac_status launch_backward(const Args& a, cudaStream_t st) {
   return check_launch();
 }
 
+template <typename C>
+kfac_status launch_delta(const Args& a, cudaStream_t st) {
+  static const bool ok = allow_smem(f32_delta_kernel<__nv_bfloat16, C>, C::BWD);
+  if (!ok) return KFAC_ERR_CUDA;
+  launch_pdl(f32_delta_kernel<__nv_bfloat16, C>, dim3((unsigned)cdiv(a.rows, kRows), a.kv_heads, a.batch),
+             dim3(kF32Threads), C::BWD, st, a);
+  count_launch();
+  return check_launch();
+}
+
 }  // namespace
 
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st) {
@@ -533,6 +590,9 @@ template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st) {
 template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st) {
   if (a.dim <= 32) return launch_backward<T, Cfg<32, 32>>(a, st);
   return a.dim <= 64 ? launch_backward<T, Cfg<32, 64>>(a, st) : launch_backward<T, Cfg<16, 128>>(a, st);
+}
+kfac_status f32_delta(const Args& a, cudaStream_t st) {
+  return a.dim <= 64 ? launch_delta<Cfg<32, 64>>(a, st) : launch_delta<Cfg<16, 128>>(a, st);
 }
 template kfac_status f32_forward<float>(const Args&, cudaStream_t);
 template kfac_status f32_forward<__nv_bfloat16>(const Args&, cudaStream_t);

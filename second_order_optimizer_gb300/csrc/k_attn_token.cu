@@ -332,6 +332,107 @@ token_kernel(const __grid_constant__ Args a) {
   }
 }
 
+// delta of the backward pass where batch entries have few permitted keys, a block per 64
+// packed query rows.  delta = sum_d dout out takes out as it was rounded to bf16; its
+// error of 2^-9 |dout out| goes into every dS of the row, and where few keys share the
+// row's weight that is not small beside dS = P (dP - delta) itself (one key: dS is 0, and
+// the error all that remains).  It falls with the square root of the number of keys: for
+// up to kExactKeys of them delta is taken here, as sum_j P_j dP_j from q, k, v, dout and lse
+// (two products more); for more of them it stays as delta_kernel took it from out.
+template <int DC>
+__global__ void __launch_bounds__(128) delta_keys_kernel(const __grid_constant__ Args a) {
+  using C = TokenCfg<DC>;
+  __shared__ __align__(1024) uint8_t kt[32 * C::ROW];
+  __shared__ __align__(1024) uint8_t vt[32 * C::ROW];
+  __shared__ int permitted;
+  if (threadIdx.x == 0) permitted = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  const int hk = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * 64 + 16 * warp;
+  const int len = key_count(a, b);
+  const int64_t row0 = ((int64_t)b * a.kv_heads + hk) * a.rows;
+  int count = len;
+  if (a.key_mask && len > kExactKeys) {
+    count = 0;   // no further than the answer needs
+    for (int key0 = 0; key0 < len && count <= kExactKeys; key0 += 512) {
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mine += key_ok(a, b, len, key0 + 128 * i + threadIdx.x);
+      mine = __reduce_add_sync(kFull, mine);
+      __syncthreads();
+      if (lane == 0) atomicAdd(&permitted, mine);
+      __syncthreads();
+      count = permitted;
+    }
+  }
+  if (count > kExactKeys) return;   // delta_kernel's will do
+  const __nv_bfloat16* kp = static_cast<const __nv_bfloat16*>(a.k) + b * a.ks[0] + hk * a.ks[2];
+  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + b * a.vs[0] + hk * a.vs[2];
+  uint32_t qr[2 * DC][4], gr[2 * DC][4];   // rows g and g + 8 of q and dout, as A fragments
+  float lse2[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + 8 * i + g;
+    const bool in = r < a.rows;
+    const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(a.q) + (in ? row_offset(a, a.qs, b, hk, r) : 0);
+    const __nv_bfloat16* gp = static_cast<const __nv_bfloat16*>(a.dout) + (in ? row_offset(a, a.dos, b, hk, r) : 0);
+    lse2[i] = in ? a.lse_in[row0 + r] * kLog2e : INFINITY;
+#pragma unroll
+    for (int kk = 0; kk < 2 * DC; ++kk)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int d = 16 * kk + 8 * e + 2 * t;
+        const bool real = in && d < a.dim;
+        qr[kk][2 * e + i] = real ? *reinterpret_cast<const uint32_t*>(qp + d) : 0u;
+        gr[kk][2 * e + i] = real ? *reinterpret_cast<const uint32_t*>(gp + d) : 0u;
+      }
+  }
+  const float c2 = a.scale * kLog2e;
+  for (int key0 = 0; key0 < len && count > 0; key0 += 32) {   // (count 0: no walk along the mask)
+    const uint32_t w = __ballot_sync(kFull, key_ok(a, b, len, key0 + lane));
+    if (w == 0) continue;   // the same in every warp
+    __syncthreads();
+    for (int e = threadIdx.x; e < 32 * C::CH; e += 128) {
+      const int row = e / C::CH, c = e % C::CH;
+      const bool real = (w >> row & 1u) && 8 * c < a.dim;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(kt + C::at(row, c)) =
+          real ? *reinterpret_cast<const uint4*>(kp + (key0 + row) * a.ks[1] + 8 * c) : zero;
+      *reinterpret_cast<uint4*>(vt + C::at(row, c)) =
+          real ? *reinterpret_cast<const uint4*>(vp + (key0 + row) * a.vs[1] + 8 * c) : zero;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float s[2][4] = {}, dp[2][4] = {};
+#pragma unroll
+      for (int kk = 0; kk < 2 * DC; ++kk) {
+        const uint32_t at = C::at(16 * h + (lane / 16) * 8 + lane % 8, 2 * kk + lane / 8 % 2);
+        uint32_t f[4];
+        ldm4(tc::smem_u32(kt) + at, f);
+        mma16816(s[0], qr[kk][0], qr[kk][1], qr[kk][2], qr[kk][3], f[0], f[1]);
+        mma16816(s[1], qr[kk][0], qr[kk][1], qr[kk][2], qr[kk][3], f[2], f[3]);
+        ldm4(tc::smem_u32(vt) + at, f);
+        mma16816(dp[0], gr[kk][0], gr[kk][1], gr[kk][2], gr[kk][3], f[0], f[1]);
+        mma16816(dp[1], gr[kk][0], gr[kk][1], gr[kk][2], gr[kk][3], f[2], f[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (w >> (16 * h + 8 * i + 2 * t + e % 2) & 1u)
+            sum[e / 2] = fmaf(exp2f(fmaf(s[i][e], c2, -lse2[e / 2])), dp[i][e], sum[e / 2]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float d = quad_sum(sum[i]);
+    const int r = r0 + 8 * i + g;
+    if (t == 0 && r < a.rows) a.delta[row0 + r] = d;
+  }
+}
+
 template <int DC, bool kCluster>
 kfac_status launch_token(const Args& a, cudaStream_t st) {
   using C = TokenCfg<DC>;
@@ -362,7 +463,21 @@ kfac_status dispatch_token(const Args& a, cudaStream_t st) {
                                                    : launch_token<DC, false>(a, st);
 }
 
+template <int DC>
+kfac_status launch_delta_keys(const Args& a, cudaStream_t st) {
+  launch_pdl(delta_keys_kernel<DC>, dim3((unsigned)cdiv(a.rows, 64), a.kv_heads, a.batch), dim3(128), 0, st, a);
+  count_launch();
+  return check_launch();
+}
+
 }  // namespace
+
+kfac_status delta_keys(const Args& a, cudaStream_t st) {
+  if (a.dim <= 32) return launch_delta_keys<1>(a, st);
+  if (a.dim <= 64) return launch_delta_keys<2>(a, st);
+  if (a.dim <= 96) return launch_delta_keys<3>(a, st);
+  return launch_delta_keys<4>(a, st);
+}
 
 kfac_status token_forward(const Args& a, cudaStream_t st) {
   if (a.dim <= 32) return dispatch_token<1>(a, st);

@@ -302,6 +302,28 @@ def test_attention_gradients_in_parts(dtype, keys, b, nq, nk, h, kv, d):
     _check_attention(*_inputs(dtype, b, nq, nk, h, kv, d, keys))
 
 
+@pytest.mark.parametrize("d", [64, 128, 36])
+@pytest.mark.parametrize("nk,few", [(2, 2), (7, 7), (130, 3), (700, 5), (128, 128), (129, 129)])
+def test_attention_gradients_with_few_keys(d, nk, few):
+    """bf16, few permitted keys (a short list, or all but a few masked): dS = P (dP - delta) is
+    then of the size of out's own rounding times dout, so delta may not be taken from out.  A
+    norm-wise check, relative to the gradients: P, dS and the result are rounded once each
+    (u = 2^-8 at most each and 0.4 u in the root mean square, so 1.5 u holds three of them
+    together with room)."""
+    q, k, v, g, *_ = _inputs(BF16, 2, 90, nk, 4, 2, d, "all", seed=nk)
+    mask = None
+    if few < nk:
+        mask = torch.zeros(2, nk, dtype=torch.uint8, device="cuda")
+        at = torch.from_numpy(np.random.default_rng(few).permutation(nk)[:few]).cuda()
+        mask[:, at] = 1
+    ok = np.ones((2, nk), bool) if mask is None else _np(mask) != 0
+    out, lse = K.cross_attention(q, k, v, key_mask=mask)
+    got = K.cross_attention_backward(g, q, k, v, out, lse, key_mask=mask)
+    ref = B.cross_attention_backward(_np(g), _np(q), _np(k), _np(v), ok)
+    for x, y in zip(got, ref):
+        assert np.linalg.norm(_np(x) - y) <= 3 * 2.0 ** -9 * np.linalg.norm(y)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_without_queries_or_keys(dtype):
     q, k, v, g, *_ = _inputs(dtype, 2, 5, 7, 2, 2, 64, "all")
