@@ -5,10 +5,11 @@
 // is generated again from (seed, offset) and never stored.
 //
 // Philox4x32-10: Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy as
-// 1, 2, 3" (SC 2011): ten rounds of two 32 x 32 -> 64 bit products.  20 wide products
-// per four elements are hidden behind memory traffic (bf16 with a residual: 24 bytes
-// per four elements).  A thread takes 16 bytes of x at a time: one generator block of
-// four fp32, two of bf16 elements.  Sums in fp32, one rounding at the store.  A
+// 1, 2, 3" (SC 2011): ten rounds of two 32 x 32 -> 64 bit products.  A thread takes two
+// 16-byte vectors of x: one generator block per four elements.  Bound by memory with a
+// residual or in fp32 (16384 x 2048 bf16 with residual, 201 MB: 30.6 us, 6.6 TB/s; one
+// vector per thread took 35 us, four 33.5), by the generator without one in bf16 (16 bytes
+// per generator block: 30 us, 4.5 TB/s).  Sums in fp32, one rounding at the store.  A
 // dropped x is not multiplied, so an infinity or NaN there does not reach y.
 #include "kfac_internal.cuh"
 
@@ -18,6 +19,7 @@ namespace kfac {
 namespace {
 
 constexpr int kDropThreads = 256;
+constexpr int kVecs = 2;         // 16-byte vectors per thread, a block's width apart
 
 struct DropArgs {
   const void *x, *r;
@@ -25,7 +27,8 @@ struct DropArgs {
   int64_t n;                    // rows * cols
   int64_t cols, ldx, ldr, ldy;
   uint32_t seed_lo, seed_hi, off_lo, off_hi;
-  uint64_t threshold;           // 0 .. 2^32
+  uint32_t threshold;           // below it: dropped
+  bool all;                     // p = 1: everything is
   float scale;
 };
 
@@ -46,13 +49,12 @@ __device__ __forceinline__ uint4 philox(uint64_t block, const DropArgs& a) {
 }
 
 __device__ __forceinline__ float drop1(float x, float r, uint32_t u, const DropArgs& a) {
-  return r + ((uint64_t)u >= a.threshold ? x * a.scale : 0.f);
+  return r + (u >= a.threshold && !a.all ? x * a.scale : 0.f);
 }
 
 template <typename T> struct alignas(16) Pack { T v[16 / sizeof(T)]; };
 
-// x, r, y contiguous and 16-byte aligned: one 16-byte vector per thread, the last
-// one element by element.
+// x, r, y contiguous and 16-byte aligned; the last threads' element by element.
 template <typename T, bool kRes>
 __global__ void __launch_bounds__(kDropThreads) dropout_flat_kernel(const __grid_constant__ DropArgs a) {
   pdl_wait();
@@ -61,30 +63,41 @@ __global__ void __launch_bounds__(kDropThreads) dropout_flat_kernel(const __grid
   const T* x = static_cast<const T*>(a.x);
   const T* r = static_cast<const T*>(a.r);
   T* y = static_cast<T*>(a.y);
-  const int64_t i = ((int64_t)blockIdx.x * kDropThreads + threadIdx.x) * N;
-  if (i >= a.n) return;
-  if (i + N <= a.n) {
-    const Pack<T> px = *reinterpret_cast<const Pack<T>*>(x + i);
-    Pack<T> pr{}, py;
-    if (kRes) pr = *reinterpret_cast<const Pack<T>*>(r + i);
+  const int64_t first = ((int64_t)blockIdx.x * kDropThreads * kVecs + threadIdx.x) * N;
+  if (first + (int64_t)(kVecs - 1) * kDropThreads * N + N <= a.n) {   // all of them whole
+    Pack<T> px[kVecs], pr[kVecs];
 #pragma unroll
-    for (int b = 0; b < N / 4; ++b) {
-      const uint4 u = philox((uint64_t)(i / 4 + b), a);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        py.v[4 * b + j] = (T)drop1(to_f32<T>(px.v[4 * b + j]),
-                                   kRes ? to_f32<T>(pr.v[4 * b + j]) : 0.f, w[j], a);
+    for (int v = 0; v < kVecs; ++v) {
+      const int64_t i = first + (int64_t)v * kDropThreads * N;
+      px[v] = *reinterpret_cast<const Pack<T>*>(x + i);
+      if (kRes) pr[v] = *reinterpret_cast<const Pack<T>*>(r + i);
     }
-    *reinterpret_cast<Pack<T>*>(y + i) = py;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int64_t i = first + (int64_t)v * kDropThreads * N;
+      Pack<T> py;
+#pragma unroll
+      for (int b = 0; b < N / 4; ++b) {
+        const uint4 u = philox((uint64_t)(i / 4 + b), a);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          py.v[4 * b + j] = (T)drop1(to_f32<T>(px[v].v[4 * b + j]),
+                                     kRes ? to_f32<T>(pr[v].v[4 * b + j]) : 0.f, w[j], a);
+      }
+      *reinterpret_cast<Pack<T>*>(y + i) = py;
+    }
     return;
   }
-  for (int b = 0; b < N / 4; ++b) {
-    const uint4 u = philox((uint64_t)(i / 4 + b), a);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    for (int j = 0; j < 4; ++j) {
-      const int64_t e = i + 4 * b + j;
-      if (e < a.n) y[e] = (T)drop1(to_f32<T>(x[e]), kRes ? to_f32<T>(r[e]) : 0.f, w[j], a);
+  for (int v = 0; v < kVecs; ++v) {
+    const int64_t i = first + (int64_t)v * kDropThreads * N;
+    for (int b = 0; b < N / 4 && i < a.n; ++b) {
+      const uint4 u = philox((uint64_t)(i / 4 + b), a);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      for (int j = 0; j < 4; ++j) {
+        const int64_t e = i + 4 * b + j;
+        if (e < a.n) y[e] = (T)drop1(to_f32<T>(x[e]), kRes ? to_f32<T>(r[e]) : 0.f, w[j], a);
+      }
     }
   }
 }
@@ -118,7 +131,7 @@ __global__ void __launch_bounds__(kDropThreads) dropout_strided_kernel(const __g
 
 template <typename T>
 void launch_dropout(const DropArgs& a, bool flat, cudaStream_t st) {
-  const int64_t per = flat ? 16 / (int64_t)sizeof(T) : 4;
+  const int64_t per = flat ? 16 / (int64_t)sizeof(T) * kVecs : 4;
   const dim3 grid((unsigned)cdiv(cdiv(a.n, per), kDropThreads)), block(kDropThreads);
   if (flat) {
     if (a.r) launch_pdl(dropout_flat_kernel<T, true>, grid, block, 0, st, a);
@@ -161,7 +174,8 @@ extern "C" kfac_status kfac_dropout(int dtype, const void* x, int64_t ldx, const
   a.seed_hi = (uint32_t)(seed >> 32);
   a.off_lo = (uint32_t)offset;
   a.off_hi = (uint32_t)(offset >> 32);
-  a.threshold = (uint64_t)std::floor(p * 4294967296.0);
+  a.all = p >= 1.0;
+  a.threshold = a.all ? 0u : (uint32_t)std::floor(p * 4294967296.0);
   a.scale = p < 1.0 ? (float)(1.0 / (1.0 - p)) : 0.f;
   auto dense = [&](const void* q, int64_t ld) {
     return !q || ((uintptr_t)q % 16 == 0 && (rows == 1 || ld == cols));
