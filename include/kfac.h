@@ -528,12 +528,14 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* desc, const void* q,
                                  cudaStream_t stream);
 
 /* Its gradients, from the forward call's out and lse and the output gradient:
- *   P = exp(S - lse), delta = sum_d dout out, dP = dout v^T,
+ *   P = exp(S - lse), dP = dout v^T, delta = sum_j P dP = sum_d dout out,
  *   dv = P^T dout, dS = P (dP - delta), dq = scale dS k, dk = scale dS^T q,
  * dk and dv summed over the query heads that share a key head.  Keys that are
  * not permitted get zero gradients; a query without permitted keys gets and
  * gives none.  dout as out, dq as q, dk as k, dv as v (written, not
- * accumulated).  No atomics: the same inputs give the same bits. */
+ * accumulated).  bf16: delta is taken from out where more than 128 keys are
+ * permitted, from P dP otherwise (out's rounding would be large beside a dS of
+ * few keys).  No atomics on sums: the same inputs give the same bits. */
 kfac_status kfac_cross_attention_backward(const kfac_attention_desc* desc,
                                           const kfac_attention_grad_desc* grads, const void* dout,
                                           const void* q, const void* k, const void* v,

@@ -1,6 +1,6 @@
-// Cross attention: argument checks, the choice of kernels, and the kernels on the
-// CUDA cores (fp32 inputs, and bf16 ones whose rows the tensor-memory accelerator
-// cannot address).
+// Cross attention: argument checks, the choice of kernels, and the kernels beside the
+// products: few query rows that the token kernel cannot take, the joins of parts of the
+// key axis, delta.
 //
 //   S = scale q k^T,  P = softmax over the permitted keys,  out = P v
 //   dV = P^T dO,  dS = P (dO v^T - delta),  dQ = scale dS k,  dK = scale dS^T q,
@@ -9,10 +9,11 @@
 // probabilities are exp(S - m), and what was summed so far is rescaled by
 // exp(m_old - m) when the maximum grows.
 //
-// Query heads that share a key head are packed into one row axis (heads of the
-// group x queries), so a tile of keys is loaded once for all of them.  Keys that
-// are not permitted enter shared memory as zeros and their scores as -infinity:
-// what stands there in memory never meets a product.
+// Except in the tcgen05 kernels, query heads that share a key head are packed into one
+// row axis (heads of the group x queries), so a tile of keys is loaded once for all of
+// them.  Keys that are not permitted enter shared memory as zeros (or are made zeros
+// there) and their scores as -infinity: what stands there in memory never meets a
+// product.
 #include "attn.cuh"
 
 #include <algorithm>
