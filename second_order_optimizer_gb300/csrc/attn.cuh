@@ -41,6 +41,20 @@ __device__ __forceinline__ int key_count(const Args& a, int b) {
 __device__ __forceinline__ bool key_ok(const Args& a, int b, int len, int key) {
   return key < len && (!a.key_mask || __ldg(a.key_mask + (int64_t)b * a.len_kv + key) != 0);
 }
+// Whether batch entry b has exactly one permitted key.  Its softmax is the constant 1 then,
+// and dQ and dK are exactly zero, where P (dP - delta) would leave the rounding of its
+// terms.  Whole warps; ends at the second key found.
+__device__ __forceinline__ bool one_key(const Args& a, int b, int len) {
+  if (!a.key_mask) return len == 1;
+  int n = 0;
+  for (int key0 = 0; key0 < len && n < 2; key0 += 512) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mine += key_ok(a, b, len, key0 + 32 * i + (int)(threadIdx.x % 32));
+    n += __reduce_add_sync(0xffffffffu, mine);
+  }
+  return n == 1;
+}
 // Offset of packed row r of key head hk.
 __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[3], int b, int hk,
                                               int r) {

@@ -434,6 +434,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
         add_values<C>(ds, Y0, dk);
       }
     }
+    if (one_key(a, b, len)) clear<C>(dk);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int own = 16 * warp + g + 8 * h, key = k0 + own;
@@ -487,6 +488,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
                        : 0.f;
     add_values<C>(ds, Y0, dq);
   }
+  if (one_key(a, b, len)) clear<C>(dq);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int r = r0 + 16 * warp + g + 8 * h;

@@ -694,6 +694,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     const uint32_t td = tmem + lanes + 128 + 64 * half;
     const int key = k0 + 32 * (warp % 4) + lane;
     const bool mine = key_ok(a, b, len, key);
+    const bool one = one_key(a, b, len);   // while the first tiles are on their way
     const float c2 = a.scale * kLog2e;
     const F2 cc2 = f2(c2, c2);
     bool ok = true;
@@ -771,6 +772,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     const int64_t* st = half ? a.dks : a.dvs;
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(half ? a.dk : a.dv) + b * st[0] + key * st[1] + hk * st[2];
     const float f = !ok ? kNaN : half ? a.scale : 1.f;
+    const bool zero = n == 0 || !mine || (half && one);
     float* part = (half ? a.part_dk : a.part_dv) +
                   ((((int64_t)split * a.batch + b) * a.kv_heads + hk) * a.len_kv + key) * a.dim;
     for (int c = 0; c < a.dim; c += 32) {
@@ -781,8 +783,8 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         tc::tmem_ld_use(o);
       }
       if (key >= a.len_kv) continue;
-      if (a.dkv_splits == 1) store_row(o, dst, c, a.dim, f, n == 0 || !mine);
-      else store_part(o, part, c, a.dim, ok, n == 0 || !mine);
+      if (a.dkv_splits == 1) store_row(o, dst, c, a.dim, f, zero);
+      else store_part(o, part, c, a.dim, ok, zero);
     }
     tc::tc_fence_before();
   }
@@ -909,6 +911,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     float lse = in ? __ldg(a.lse_in + row) * kLog2e : INFINITY;
     if (lse == -INFINITY) lse = INFINITY;   // no permitted key: P = 0
     const float delta = in ? a.delta[row] : 0.f;
+    const bool one = one_key(a, b, len);   // while the first tiles are on their way
     const float c2 = a.scale * kLog2e;
     const F2 cc2 = f2(c2, c2), nl2 = f2(-lse, -lse), nd2 = f2(-delta, -delta);
     bool ok = true;
@@ -974,6 +977,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     if (!ok) give_up(124);
     tc::tc_fence_after();
     __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.dq) + b * a.dqs[0] + q * a.dqs[1] + h * a.dqs[2];
+    const bool zero = n == 0 || one;
     float* part = a.part_dq + ((int64_t)split * a.batch * a.heads * a.len_q + row) * a.dim;
     for (int c = 32 * half; c < a.dim; c += 64) {   // the groups take 32 channels in turn
       uint32_t o[32];
@@ -983,8 +987,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         tc::tmem_ld_use(o);
       }
       if (!in) continue;
-      if (a.dq_splits == 1) store_row(o, dst, c, a.dim, ok ? a.scale : kNaN, n == 0);
-      else store_part(o, part, c, a.dim, ok, n == 0);
+      if (a.dq_splits == 1) store_row(o, dst, c, a.dim, ok ? a.scale : kNaN, zero);
+      else store_part(o, part, c, a.dim, ok, zero);
     }
     tc::tc_fence_before();
   }

@@ -325,6 +325,27 @@ def test_attention_gradients_with_few_keys(d, nk, few):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("d", [64, 128, 36])
+def test_attention_gradients_with_one_key_are_zero(dtype, d):
+    """A softmax over one key is constant: dq and dk are exactly zero, dv is the sum of dout."""
+    q, k, v, g, *_ = _inputs(dtype, 3, 150, 200, 2, 1, d, "all")
+    mask = torch.ones(3, 200, dtype=torch.uint8, device="cuda")
+    mask[1] = 0
+    mask[1, 177] = 1
+    for kv_len, m, b, at in ((torch.tensor([1, 5, 200], dtype=torch.int32, device="cuda"), None, 0, 0),
+                             (None, mask, 1, 177)):
+        out, lse = K.cross_attention(q, k, v, kv_len, m)
+        dq, dk, dv = K.cross_attention_backward(g, q, k, v, out, lse, kv_len, m)
+        assert (dq[b] == 0).all() and (dk[b] == 0).all()
+        assert all((dq[i] != 0).any() for i in range(3) if i != b)
+        want = _np(g[b]).sum(axis=(0, 1))
+        got = _np(dv[b])
+        assert (np.delete(got, at, axis=0) == 0).all()
+        bound = np.abs(_np(g[b])).sum(axis=(0, 1)) * (SLACK + U[dtype] * (dtype == BF16)) + U[dtype] * np.abs(want)
+        assert (np.abs(got[at, 0] - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_attention_without_queries_or_keys(dtype):
     q, k, v, g, *_ = _inputs(dtype, 2, 5, 7, 2, 2, 64, "all")
     out, lse = K.cross_attention(q, k[:, :0], v[:, :0])
