@@ -41,6 +41,24 @@ __device__ __forceinline__ int key_count(const Args& a, int b) {
 __device__ __forceinline__ bool key_ok(const Args& a, int b, int len, int key) {
   return key < len && (!a.key_mask || __ldg(a.key_mask + (int64_t)b * a.len_kv + key) != 0);
 }
+// Where a walk along the keys of batch entry b may end: behind the last permitted one (a
+// mask that pads, or leaves nothing, then costs no tiles).  Whole warps; the search runs
+// from the end, 512 keys at a time, and mostly ends with the first of them.
+__device__ __forceinline__ int walk_end(const Args& a, int b) {
+  const int len = key_count(a, b);
+  if (!a.key_mask) return len;
+  for (int key0 = (len - 1) / 512 * 512; key0 >= 0 && len > 0; key0 -= 512) {
+    int last = -1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int key = key0 + 32 * i + (int)(threadIdx.x % 32);
+      if (key_ok(a, b, len, key)) last = key;
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (last >= 0) return last + 1;
+  }
+  return 0;
+}
 // Whether batch entry b has exactly one permitted key.  Its softmax is the constant 1 then,
 // and dQ and dK are exactly zero, where P (dP - delta) would leave the rounding of its
 // terms.  Whole warps; ends at the second key found.

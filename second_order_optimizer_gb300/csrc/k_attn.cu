@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(C::THREADS) few_rows_kernel(const __grid_const
   const int tile = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
   const int hk = blockIdx.y, b = blockIdx.z, r0 = tile * BO;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   const int tiles = (len + BS - 1) / BS;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int t1 = (int)((int64_t)tiles * (split + 1) / a.splits);

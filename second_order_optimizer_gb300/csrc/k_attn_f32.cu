@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_forward_kernel(const __grid_c
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int split_id = blockIdx.x % a.splits, r0 = (int)(blockIdx.x / a.splits) * kRows;
   const int hk = blockIdx.y, b = blockIdx.z;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   const int tiles = (len + C::BS - 1) / C::BS;
   const int t0 = (int)((int64_t)tiles * split_id / a.splits);
   const int t1 = (int)((int64_t)tiles * (split_id + 1) / a.splits);
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_backward_kernel(const __grid_
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int hk = blockIdx.y, b = blockIdx.z;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   const int dkv_blocks = (a.len_kv + kRows - 1) / kRows * a.dkv_splits;
   const float c2 = a.scale * kLog2e;
   const float* lse_row = a.lse_in + ((int64_t)b * a.kv_heads + hk) * a.rows;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_con
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int hk = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * kRows;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   const float c2 = a.scale * kLog2e;
   const int64_t row0 = ((int64_t)b * a.kv_heads + hk) * a.rows;
   load_queries<T, C, kRows, false>(a, X0, X1, b, hk, r0);

@@ -248,7 +248,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int q0 = (int)(blockIdx.x / a.splits) * NT * BT, h = blockIdx.y, b = blockIdx.z;
   const int hk = h / a.group;
   const int nt = NT == 2 && q0 + BT < a.len_q ? 2 : 1;
-  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
+  const int len = __shfl_sync(kFull, walk_end(a, b), 0);   // known to be warp-uniform
   const int tiles = (len + BT - 1) / BT;
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int n = (int)((int64_t)tiles * (split + 1) / a.splits) - t0;
@@ -571,7 +571,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   auto s_at = [&](int i) { return tmem + (NC == 1 && i % 2 ? 384u : 0u); };
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int k0 = tile * BT;
-  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
+  const int len = __shfl_sync(kFull, walk_end(a, b), 0);   // known to be warp-uniform
   const int qtiles = (a.len_q + BT - 1) / BT;
   // this part of the group's query tiles
   const int steps = k0 < len ? a.group * qtiles : 0;
@@ -802,7 +802,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
   const int h = hk * a.group + tile / qtiles, q0 = tile % qtiles * BT;
-  const int len = __shfl_sync(kFull, key_count(a, b), 0);   // known to be warp-uniform
+  const int len = __shfl_sync(kFull, walk_end(a, b), 0);   // known to be warp-uniform
   // this part of the key tiles
   const int tiles = (len + BT - 1) / BT;
   const int first = (int)((int64_t)tiles * split / a.dq_splits);

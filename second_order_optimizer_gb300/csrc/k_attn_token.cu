@@ -92,7 +92,7 @@ token_kernel(const __grid_constant__ Args a) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int split = (int)(blockIdx.x % a.splits), r0 = (int)(blockIdx.x / a.splits) * 16;
   const int hk = blockIdx.y, b = blockIdx.z;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   int first, last;
   if (kCluster) {
     const int blocks = (len + 15) / 16;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(128) delta_keys_kernel(const __grid_constant__
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int hk = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * 64 + 16 * warp;
-  const int len = key_count(a, b);
+  const int len = walk_end(a, b);
   const int64_t row0 = ((int64_t)b * a.kv_heads + hk) * a.rows;
   int count = len;
   if (a.key_mask && len > kExactKeys) {
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(128) delta_keys_kernel(const __grid_constant__
       }
   }
   const float c2 = a.scale * kLog2e;
-  for (int key0 = 0; key0 < len && count > 0; key0 += 32) {   // (count 0: no walk along the mask)
+  for (int key0 = 0; key0 < len; key0 += 32) {
     const uint32_t w = __ballot_sync(kFull, key_ok(a, b, len, key0 + lane));
     if (w == 0) continue;   // the same in every warp
     __syncthreads();
