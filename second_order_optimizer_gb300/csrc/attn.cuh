@@ -25,6 +25,7 @@ struct Args {
   bool vec;                         // CUDA-core kernels: rows of whole 16-byte pieces
   int splits;                       // parts of the key axis (1: outputs written directly)
   int part_keys;                    // token kernel, more parts than a cluster: keys per part
+  bool longest_first;               // token kernel: order of the batch entries
   float* part_o;                    // [splits][batch][kv_heads][rows][dim], normalised
   float* part_lse;                  // [splits][batch][kv_heads][rows]
   // backward: parts of the query rows for dK and dV, of the keys for dQ (1: outputs
@@ -84,6 +85,7 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
 constexpr int kTokenWarps = 4;
 constexpr int kTokenPerSm = 3;      // resident blocks per SM
 constexpr int kTokenCluster = 8;    // parts that one cluster joins
+constexpr int kTokenOrdered = 32 * kTokenWarps;   // batch entries that it can order
 kfac_status token_forward(const Args& a, cudaStream_t st);
 // delta from P dP, of batch entries with at most kExactKeys permitted keys alone (bf16, the
 // tensors of tc_backward_ok).

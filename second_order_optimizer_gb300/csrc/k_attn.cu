@@ -482,18 +482,27 @@ constexpr int kTokenRows = 64;
 bool token_sizes(const kfac_attention_desc& d) {
   return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q <= kTokenRows;
 }
-// Parts of the key axis for the token kernel: as many blocks as are resident at once - no
-// more for equal lengths, where a second wave of a few blocks costs as much as a whole
-// one, and at least as many for ragged ones, which a part more evens out (32 x 8192 keys
-// on 4 key heads x 128: 84 us in 3 parts and 113 us in 4; ragged, 72 and 61).  Each warp
-// has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a cluster,
-// more are fixed lengths.
+// Parts of the key axis for the token kernel: as many blocks as are resident at once, and no
+// more for equal lengths, where a second wave of a few blocks costs as much as a whole one
+// (32 x 8192 keys on 4 key heads x 128: 84 us in 3 parts and 113 us in 4).  Ragged lengths
+// leave blocks idle, which the blocks of a second wave fill, if the walks are longer than a
+// wave's cost of about 5 us (128 channels, walks x keys: parts and us; the waves' choice
+// first): 128 x 512, 3: 11.0, 4: 13.3; 128 x 2048, 4: 20.8, 3: 24.0, 6: 25.7;
+// 256 x 4096, 3: 46.3, 2: 59.5, 4: 52.5; 128 x 8192, 6: 44.2, 4: 58.0, 8: 51.2.
+// Each warp has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a
+// cluster, more are fixed lengths, which are even by themselves.
+constexpr int kTokenWaves1 = 1024, kTokenWaves2 = 4096;   // keys: 1 wave below, 1.5 from
 int token_splits(const kfac_attention_desc& d, bool ragged, int* part_keys) {
   const int64_t ctas = std::max<int64_t>(
       1, cdiv((int64_t)d.heads / d.kv_heads * d.len_q, 16) * d.kv_heads * d.batch);
   const int step = 16 * kTokenWarps;
   const int64_t most = std::max<int64_t>(1, cdiv(d.len_kv, step)), slots = kTokenPerSm * num_sms();
-  int64_t parts = std::min<int64_t>(most, ragged ? cdiv(slots, ctas) : std::max<int64_t>(1, slots / ctas));
+  int64_t parts = std::max<int64_t>(1, slots / ctas);
+  const bool clustered = parts <= kTokenCluster;
+  if (ragged && d.batch > 1 && d.len_kv >= kTokenWaves1)
+    parts = cdiv(d.len_kv < kTokenWaves2 ? slots : slots + slots / 2, ctas);
+  if (clustered) parts = std::min<int64_t>(parts, kTokenCluster);
+  parts = std::min(parts, most);
   *part_keys = d.len_kv;
   if (parts > kTokenCluster) {
     *part_keys = (int)(cdiv(cdiv(d.len_kv, parts), step) * step);
@@ -651,6 +660,9 @@ kfac_status kfac_cross_attention(const kfac_attention_desc* d, const void* q, co
   a.key_mask = key_mask;
   const bool tc = d->dtype == KFAC_BF16 && tc_forward_ok(a), token = tc && token_sizes(*d);
   a.splits = token ? token_splits(*d, kv_len != nullptr, &a.part_keys) : tc ? tc_splits(*d) : plain_splits(*d);
+  // (the order costs 0.5 us, which short walks do not win back)
+  a.longest_first = token && kv_len && d->batch > 1 && d->batch <= kTokenOrdered && d->len_kv >= 512 &&
+                    cdiv(a.rows, 16) * a.splits * (int64_t)d->kv_heads * d->batch > kTokenPerSm * num_sms();
   a.part_o = static_cast<float*>(workspace);
   a.part_lse = a.part_o + (size_t)a.splits * d->batch * d->heads * d->len_q * d->head_dim;
   if (tc) {

@@ -3,8 +3,8 @@
 //
 // Bound by memory: k and v are read once, at 2 flop per byte and row.  Each warp walks
 // 16 keys at a time through a ring of its own in shared memory (16-byte cp.async, one
-// step ahead, no block-wide barrier; 128 channels: 65 KB a block, three blocks per SM -
-// two steps ahead and two blocks took 67 us where this takes 61): S = q k^T and O += P v by mma.sync m16n8k16 on
+// step ahead, no block-wide barrier; 128 channels: 65 KB a block, three blocks per SM;
+// two steps ahead and two blocks took 67 us where this took 61): S = q k^T and O += P v by mma.sync m16n8k16 on
 // fragments that ldmatrix reads, rows swizzled so that eight rows of one 16-byte
 // column hit all banks.  Keys that are not permitted are filled with zeros, their
 // scores are -infinity.  P enters as two bf16 parts (high and remainder): the second
@@ -13,7 +13,8 @@
 // The key axis is split.  Up to 8 parts are the blocks of one cluster, each taking its
 // share of the sequence's own length; they exchange maxima, sums and outputs through
 // distributed shared memory and the call is one launch.  More parts (few sequences,
-// long states) are fixed lengths of the axis, joined by the combine kernel.
+// long states) are fixed lengths of the axis, joined by the combine kernel.  Ragged lengths
+// that fill more than one wave start with the longest, so that the short ones fill the end.
 #include "attn.cuh"
 #include "tc_prims.cuh"
 
@@ -79,6 +80,20 @@ template <int DC> struct TokenCfg {            // dim <= 32 DC
   }
 };
 
+// The batch entry that `rank` others precede when the longest come first (equal ones in
+// their order).  A thread per entry, up to kTokenOrdered of them; whole blocks.
+__device__ __forceinline__ int entry_by_length(const Args& a, int rank) {
+  __shared__ int len[kTokenOrdered], entry;
+  const int i = threadIdx.x, mine = i < a.batch ? key_count(a, i) : 0;
+  len[i] = mine;
+  __syncthreads();
+  int before = 0;
+  for (int j = 0; j < a.batch; ++j) before += len[j] > mine || (len[j] == mine && j < i);
+  if (i < a.batch && before == rank) entry = i;
+  __syncthreads();
+  return entry;
+}
+
 // grid: (16-row tiles x parts, kv_heads, batch).  kCluster: a tile's parts are one
 // cluster and share the sequence's length; otherwise part s takes keys
 // [s, s + 1) x part_keys.
@@ -91,7 +106,7 @@ token_kernel(const __grid_constant__ Args a) {
   pdl_trigger();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int split = (int)(blockIdx.x % a.splits), r0 = (int)(blockIdx.x / a.splits) * 16;
-  const int hk = blockIdx.y, b = blockIdx.z;
+  const int hk = blockIdx.y, b = a.longest_first ? entry_by_length(a, blockIdx.z) : blockIdx.z;
   const int len = walk_end(a, b);
   int first, last;
   if (kCluster) {

@@ -293,6 +293,39 @@ def test_attention_few_rows_many_parts(dtype, keys, b, nq, nk, h, kv, d):
     _check_attention(*_inputs(dtype, b, nq, nk, h, kv, d, keys), backward=False)
 
 
+# more entries than one wave of blocks takes (they run in the order of their lengths), more
+# entries than are ordered, and parts of a fixed length
+@pytest.mark.parametrize("keys", ["len", "both"])
+@pytest.mark.parametrize("b,nq,nk,h,kv,d", [(60, 1, 1030, 8, 4, 64), (128, 1, 600, 4, 4, 32),
+                                            (130, 1, 600, 4, 4, 32), (12, 1, 4500, 4, 4, 64),
+                                            (40, 3, 1100, 8, 4, 36)])
+def test_attention_tokens_of_many_ragged_entries(keys, b, nq, nk, h, kv, d):
+    q, k, v, g, kv_len, mask, ok = _inputs(BF16, b, nq, nk, h, kv, d, keys, seed=23)
+    if keys == "len":   # equal lengths have an order too
+        kv_len[b // 2:] = kv_len[b // 2].clone()
+        ok = B.permitted(b, nk, kv_len.cpu().numpy(), None)
+        bad = torch.from_numpy(~ok).cuda()
+        k, v = (torch.nan_to_num(x.float(), nan=0.5, posinf=0.25).to(x.dtype) for x in (k, v))
+        k[bad], v[bad] = float("nan"), float("inf")
+    _check_attention(q, k, v, g, kv_len, mask, ok, backward=False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("nq,h", [(1, 4), (70, 2)])
+@pytest.mark.parametrize("nk", [40, 700, 1100])
+def test_attention_masks_that_pad(dtype, nq, h, nk):
+    """The mask permits the first keys of each entry: all, none, one, and ends at, before and
+    behind a boundary of 16, 128 and 512 keys."""
+    ends = sorted({min(e, nk) for e in (nk, 0, 1, 15, 16, 17, 127, 128, 129, 511, 512, 513, nk - 1)})
+    b = len(ends)
+    q, k, v, g, _, _, _ = _inputs(dtype, b, nq, nk, h, 2, 64, "all", seed=29)
+    ok = np.arange(nk)[None, :] < np.array(ends)[:, None]
+    mask = torch.from_numpy(ok.astype(np.uint8)).cuda()
+    bad = torch.from_numpy(~ok).cuda()
+    k[bad], v[bad] = float("nan"), float("inf")
+    _check_attention(q, k, v, g, None, mask, ok)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("keys", ["all", "both"])
 @pytest.mark.parametrize("b,nq,nk,h,kv,d", [(1, 20, 3100, 2, 1, 64), (1, 2500, 40, 2, 1, 128),
