@@ -467,7 +467,9 @@ int pick_splits(int64_t ctas, int per_sm, int len_kv, int tile) {
 
 int plain_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
-  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, 3, d.len_kv, 64);
+  // as many blocks as are resident
+  const int per_sm = rows <= 16 ? 3 : d.head_dim <= 64 ? 4 : 2;
+  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, per_sm, d.len_kv, 64);
 }
 // (a part of fewer than 512 keys costs more to join than it saves: 2 x 300 queries, 300
 // keys, 8 heads x 64: 10 us unsplit, 15 us in three parts)
