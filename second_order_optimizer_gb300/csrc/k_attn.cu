@@ -428,6 +428,10 @@ template <typename T>
 kfac_status backward(Args a, cudaStream_t st) {
   const int64_t n = (int64_t)a.batch * a.heads * a.len_q;
   const bool bf16 = sizeof(T) == 2, tc = bf16 && tc_backward_ok(a);
+  a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
+          vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
+          vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
+          vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   if (n > 0) {
     // bf16: out is rounded, and with few keys delta has to be better than that
     kfac_status e = KFAC_OK;
@@ -444,10 +448,6 @@ kfac_status backward(Args a, cudaStream_t st) {
   if (tc) {
     e = tc_backward(a, st);
   } else {
-    a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
-            vec_rows(a.dout, a.dos, a.len_q, a.heads, a.batch, a.dim, 4) &&
-            vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
-            vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
     e = f32_backward<T>(a, st);
   }
   const int64_t sums = (a.dq_splits > 1 ? n : 0) +
@@ -537,13 +537,12 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 // queries in steps (four products each), a dQ block owns as many queries and walks the
 // keys (three).  Where one block's walk is longer than its share of the whole work, it is
 // split, into pieces of at least four steps; the sums then take a launch more.
-// (bf16 layouts that the tensor-core kernels cannot take keep their parts.)
-void backward_splits(const kfac_attention_desc& d, Args& a) {
-  const bool bf16 = d.dtype == KFAC_BF16;
-  const int own = bf16 ? 128 : 64, step = bf16 ? 128 : 32, per_sm = bf16 ? 1 : 2;
+// tc: of the tensor-core kernels (bf16), else of the fp32 ones.
+void backward_splits(const kfac_attention_desc& d, Args& a, bool tc) {
+  const int own = tc ? 128 : 64, step = tc ? 128 : 32, per_sm = tc ? 1 : 2;
   const int64_t group = d.heads / d.kv_heads;
-  const int64_t rows = group * d.len_q, blocks_q = bf16 ? group * cdiv(d.len_q, own) : cdiv(rows, own);
-  const int64_t steps_q = bf16 ? blocks_q : cdiv(rows, step), steps_k = cdiv(d.len_kv, step);
+  const int64_t rows = group * d.len_q, blocks_q = tc ? group * cdiv(d.len_q, own) : cdiv(rows, own);
+  const int64_t steps_q = tc ? blocks_q : cdiv(rows, step), steps_k = cdiv(d.len_kv, step);
   const int64_t work = (4 * cdiv(d.len_kv, own) * steps_q + 3 * blocks_q * steps_k) * d.kv_heads * d.batch;
   const int64_t share = std::max<int64_t>(1, work / (per_sm * num_sms()));
   auto parts = [&](int64_t steps, int64_t weight) {
@@ -575,8 +574,11 @@ size_t workspace_bytes_for(const kfac_attention_desc& d, bool backward) {
   const size_t fwd = part_bytes(d, splits);
   if (!backward) return fwd;
   Args a{};
-  backward_splits(d, a);
-  return std::max(fwd, backward_bytes(d, a, nullptr));
+  backward_splits(d, a, false);
+  const size_t bytes = std::max(fwd, backward_bytes(d, a, nullptr));
+  if (d.dtype != KFAC_BF16) return bytes;
+  backward_splits(d, a, true);
+  return std::max(bytes, backward_bytes(d, a, nullptr));
 }
 
 struct Tensor {
@@ -714,14 +716,14 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* d,
   a.lse_in = lse;
   a.kv_len = kv_len;
   a.key_mask = key_mask;
-  backward_splits(*d, a);
-  backward_bytes(*d, a, static_cast<char*>(workspace));
   for (int i = 0; i < 3; ++i) {
     a.dos[i] = g->dout_stride[i];
     a.dqs[i] = g->dq_stride[i];
     a.dks[i] = g->dk_stride[i];
     a.dvs[i] = g->dv_stride[i];
   }
+  backward_splits(*d, a, d->dtype == KFAC_BF16 && tc_backward_ok(a));
+  backward_bytes(*d, a, static_cast<char*>(workspace));
   return d->dtype == KFAC_BF16 ? backward<__nv_bfloat16>(a, stream) : backward<float>(a, stream);
 }
 

@@ -11,6 +11,9 @@
 // 128: forward 400 us, 43 TFLOP/s; backward 1650 us; on 8 x 64: 216 and 732 us.  Bound by issue at
 // 8 to 16 warps per SM: the three products alone could run at 98 TFLOP/s.
 //
+// bf16 values are TF32 values: their scores take one product, and P or dS with one of them
+// two (h y + r y).
+//
 // A block owns 64 rows (queries, or keys for dK and dV), 16 per warp, and streams tiles
 // of BS rows of the other side past them, two buffers of them in shared memory, the next one
 // on its way (cp.async) while the present one is multiplied.  They lie there as they are and
@@ -72,6 +75,7 @@ __device__ __forceinline__ void mma3(float (&hi)[4], float (&lo)[4], const Split
   mma_tf32(lo, a[0].h, a[1].h, a[2].h, a[3].h, b0.r, b1.r);
   mma_tf32(hi, a[0].h, a[1].h, a[2].h, a[3].h, b0.h, b1.h);
 }
+__device__ __forceinline__ uint32_t bits(float v) { return __float_as_uint(v); }
 __device__ __forceinline__ float comp(const float4& v, int e) {
   return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
 }
@@ -86,7 +90,7 @@ __device__ __forceinline__ void read_parts(const float* y, uint4& h, uint4& r) {
 
 // s[nt] = 16 own rows (x) . 8 streamed rows (y)^T, summed over the
 // channels.
-template <typename C>
+template <typename C, bool kBf16>
 __device__ __forceinline__ void scores(const float* x, const float* y, float (&s)[C::NT][4]) {
   const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   float lo[C::NT][4];
@@ -99,32 +103,43 @@ __device__ __forceinline__ void scores(const float* x, const float* y, float (&s
     const int d = 32 * (bj / 2) + 8 * t + 4 * (bj % 2);
     const float4 x0 = *reinterpret_cast<const float4*>(x + g * C::DPP + d);
     const float4 x1 = *reinterpret_cast<const float4*>(x + (g + 8) * C::DPP + d);
-    Split a[2][4];
+    if constexpr (kBf16) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      a[h][0] = split(comp(x0, 2 * h));
-      a[h][1] = split(comp(x1, 2 * h));
-      a[h][2] = split(comp(x0, 2 * h + 1));
-      a[h][3] = split(comp(x1, 2 * h + 1));
-    }
+      for (int n = 0; n < C::NT; ++n) {
+        const float4 v = *reinterpret_cast<const float4*>(y + (8 * n + g) * C::DPP + d);
 #pragma unroll
-    for (int n = 0; n < C::NT; ++n) {
-      uint4 yh, yr;
-      read_parts(y + (8 * n + g) * C::DPP + d, yh, yr);
-      mma3(s[n], lo[n], a[0], {yh.x, yr.x}, {yh.y, yr.y});
-      mma3(s[n], lo[n], a[1], {yh.z, yr.z}, {yh.w, yr.w});
+        for (int h = 0; h < 2; ++h)
+          mma_tf32(s[n], bits(comp(x0, 2 * h)), bits(comp(x1, 2 * h)), bits(comp(x0, 2 * h + 1)),
+                   bits(comp(x1, 2 * h + 1)), bits(comp(v, 2 * h)), bits(comp(v, 2 * h + 1)));
+      }
+    } else {
+      Split a[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        a[h][0] = split(comp(x0, 2 * h));
+        a[h][1] = split(comp(x1, 2 * h));
+        a[h][2] = split(comp(x0, 2 * h + 1));
+        a[h][3] = split(comp(x1, 2 * h + 1));
+      }
+#pragma unroll
+      for (int n = 0; n < C::NT; ++n) {
+        uint4 yh, yr;
+        read_parts(y + (8 * n + g) * C::DPP + d, yh, yr);
+        mma3(s[n], lo[n], a[0], {yh.x, yr.x}, {yh.y, yr.y});
+        mma3(s[n], lo[n], a[1], {yh.z, yr.z}, {yh.w, yr.w});
+      }
     }
   }
 #pragma unroll
   for (int n = 0; n < C::NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[n][e] += lo[n][e];
+    for (int e = 0; e < 4; ++e) s[n][e] += lo[n][e];   // (bf16: zero)
 }
 
 // o += p (16 own rows x BS, as scores() leaves them) . y (BS streamed rows).
 // Lane (g, t) holds, of rows g (elements 0, 1) and g + 8 (2, 3), channels 32 b + 8 t + e in
 // o[4 b + e][0 or 2] and 32 b + 8 t + 4 + e in o[4 b + e][1 or 3].
-template <typename C>
+template <typename C, bool kBf16>
 __device__ __forceinline__ void add_values(const float (&p)[C::NT][4], const float* y,
                                            float (&o)[4 * C::NB][4]) {
   const int lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
@@ -146,13 +161,22 @@ __device__ __forceinline__ void add_values(const float (&p)[C::NT][4], const flo
 #pragma unroll
     for (int n = 0; n < C::NT; ++n) {
       const float* row = y + (8 * n + 2 * t) * C::DPP + 32 * blk + 4 * g;
-      uint4 h0, h1, r0, r1;
-      read_parts(row, h0, r0);
-      read_parts(row + C::DPP, h1, r1);
-      mma3(hi[0], lo[0], a[n], {h0.x, r0.x}, {h1.x, r1.x});
-      mma3(hi[1], lo[1], a[n], {h0.y, r0.y}, {h1.y, r1.y});
-      mma3(hi[2], lo[2], a[n], {h0.z, r0.z}, {h1.z, r1.z});
-      mma3(hi[3], lo[3], a[n], {h0.w, r0.w}, {h1.w, r1.w});
+      if constexpr (kBf16) {
+        const float4 y0 = *reinterpret_cast<const float4*>(row), y1 = *reinterpret_cast<const float4*>(row + C::DPP);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mma_tf32(lo[e], a[n][0].r, a[n][1].r, a[n][2].r, a[n][3].r, bits(comp(y0, e)), bits(comp(y1, e)));
+          mma_tf32(hi[e], a[n][0].h, a[n][1].h, a[n][2].h, a[n][3].h, bits(comp(y0, e)), bits(comp(y1, e)));
+        }
+      } else {
+        uint4 h0, h1, r0, r1;
+        read_parts(row, h0, r0);
+        read_parts(row + C::DPP, h1, r1);
+        mma3(hi[0], lo[0], a[n], {h0.x, r0.x}, {h1.x, r1.x});
+        mma3(hi[1], lo[1], a[n], {h0.y, r0.y}, {h1.y, r1.y});
+        mma3(hi[2], lo[2], a[n], {h0.z, r0.z}, {h1.z, r1.z});
+        mma3(hi[3], lo[3], a[n], {h0.w, r0.w}, {h1.w, r1.w});
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -196,6 +220,10 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int dim, boo
       if (o >= 0 && d < dim) {
         if (sizeof(T) == 4 && vec) {
           v = *reinterpret_cast<const float4*>(p + d);
+        } else if (vec) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p + d);
+          v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                          __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
         } else {
           v.x = to_f32<T>(p[d]);
           if (d + 1 < dim) v.y = to_f32<T>(p[d + 1]);
@@ -328,7 +356,7 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 4 : 2) f32_forward_
     if (tile + 1 < t1) fetch(tile + 1);
     if (!active) continue;
     float s[C::NT][4];
-    scores<C>(Qs + 16 * warp * C::DPP, Ks, s);
+    scores<C, sizeof(T) == 2>(Qs + 16 * warp * C::DPP, Ks, s);
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -357,7 +385,7 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 4 : 2) f32_forward_
         o[i][2 * h + 1] *= f;
       }
     }
-    add_values<C>(s, Ks + C::TILE, o);
+    add_values<C, sizeof(T) == 2>(s, Ks + C::TILE, o);
   }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -443,7 +471,7 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 3 : 2) f32_backward
         if (k0 + 16 * warp >= len) continue;
         // (a key that is not permitted has zero rows of K and V; its results are dropped
         // below)
-        scores<C>(x0, Y0, p);
+        scores<C, sizeof(T) == 2>(x0, Y0, p);
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -451,13 +479,13 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 3 : 2) f32_backward
             const int q = 8 * n + 2 * t + e % 2;
             p[n][e] = exp2f(fmaf(p[n][e], c2, -base2(st[q], r0 + q < a.rows)));
           }
-        add_values<C>(p, Y1, dv);   // (before dP: its registers are free here)
-        scores<C>(x1, Y1, ds);
+        add_values<C, sizeof(T) == 2>(p, Y1, dv);   // (before dP: its registers are free here)
+        scores<C, sizeof(T) == 2>(x1, Y1, ds);
 #pragma unroll
         for (int n = 0; n < C::NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) ds[n][e] = p[n][e] * (ds[n][e] - st[C::BS + 8 * n + 2 * t + e % 2]);
-        add_values<C>(ds, Y0, dk);
+        add_values<C, sizeof(T) == 2>(ds, Y0, dk);
       }
     }
     if (one_key(a, b, len)) clear<C>(dk);
@@ -516,8 +544,8 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 3 : 2) f32_backward
     __syncthreads();
     if (step + 1 < s1) fetch(step + 1);
     if (!active) continue;
-    scores<C>(x0, Y0, p);
-    scores<C>(x1, Y1, ds);
+    scores<C, sizeof(T) == 2>(x0, Y0, p);
+    scores<C, sizeof(T) == 2>(x1, Y1, ds);
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
@@ -525,7 +553,7 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 3 : 2) f32_backward
         ds[n][e] = ok[8 * n + 2 * t + e % 2]
                        ? exp2f(fmaf(p[n][e], c2, -lse[e / 2])) * (ds[n][e] - delta[e / 2])
                        : 0.f;
-    add_values<C>(ds, Y0, dq);
+    add_values<C, sizeof(T) == 2>(ds, Y0, dq);
   }
   if (one_key(a, b, len)) clear<C>(dq);
 #pragma unroll
@@ -571,8 +599,8 @@ __global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_con
     load_keys<T, C, C::BS>(keys, Y0, Y1, oks, k0);
     __syncthreads();
     float p[C::NT][4], dp[C::NT][4];
-    scores<C>(X0 + 16 * warp * C::DPP, Y0, p);
-    scores<C>(X1 + 16 * warp * C::DPP, Y1, dp);
+    scores<C, sizeof(T) == 2>(X0 + 16 * warp * C::DPP, Y0, p);
+    scores<C, sizeof(T) == 2>(X1 + 16 * warp * C::DPP, Y1, dp);
 #pragma unroll
     for (int n = 0; n < C::NT; ++n)
 #pragma unroll
