@@ -95,7 +95,7 @@ kfac_status delta_keys(const Args& a, cudaStream_t st);
 // fp32 arithmetic: forward of more than 16 rows, and backward (a.delta already written).
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st);
 template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st);
-// delta = sum_j P_j dP_j whatever the number of keys (bf16 inputs, whose out is rounded).
+// The same for the bf16 tensors that the fp32 kernels take.
 kfac_status f32_delta(const Args& a, cudaStream_t st);
 
 // Tensor-core kernels (bf16): whether these tensors can take them, and their launches.

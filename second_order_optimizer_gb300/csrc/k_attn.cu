@@ -435,13 +435,9 @@ kfac_status backward(Args a, cudaStream_t st) {
   if (n > 0) {
     // bf16: out is rounded, and with few keys delta has to be better than that
     kfac_status e = KFAC_OK;
-    if (bf16 && !tc) {
-      e = f32_delta(a, st);
-    } else {
-      const bool all_few = tc && a.len_kv <= kExactKeys;
-      if (!all_few) e = launch_delta<T>(a, st);
-      if (e == KFAC_OK && tc && (all_few || a.kv_len || a.key_mask)) e = delta_keys(a, st);
-    }
+    const bool all_few = bf16 && a.len_kv <= kExactKeys;
+    if (!all_few) e = launch_delta<T>(a, st);
+    if (e == KFAC_OK && bf16 && (all_few || a.kv_len || a.key_mask)) e = tc ? delta_keys(a, st) : f32_delta(a, st);
     if (e != KFAC_OK) return e;
   }
   kfac_status e;

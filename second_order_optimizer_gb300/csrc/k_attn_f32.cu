@@ -569,8 +569,9 @@ __global__ void __launch_bounds__(kF32Threads, C::DP <= 64 ? 3 : 2) f32_backward
   }
 }
 
-// delta of bf16 inputs (sum_d dout out would carry out's rounding into every dS): the first
-// half of a dQ block.  grid: (row tiles, kv_heads, batch)
+// delta of bf16 inputs where at most kExactKeys keys are permitted (sum_d dout out would carry
+// out's rounding into every dS): the first half of a dQ block.  grid: (row tiles, kv_heads,
+// batch)
 template <typename T, typename C>
 __global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) float sm[];
@@ -584,6 +585,17 @@ __global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_con
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int hk = blockIdx.y, b = blockIdx.z, r0 = blockIdx.x * kRows;
   const int len = walk_end(a, b);
+  int count = len;   // permitted keys, as far as it matters
+  if (a.key_mask && len > kExactKeys) {
+    count = 0;
+    for (int key0 = 0; key0 < len && count <= kExactKeys; key0 += 512) {
+      int mine = 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) mine += key_ok(a, b, len, key0 + 32 * i + lane);
+      count += __reduce_add_sync(kAll, mine);
+    }
+  }
+  if (count > kExactKeys) return;   // as delta_kernel took it from out
   const float c2 = a.scale * kLog2e;
   const int64_t row0 = ((int64_t)b * a.kv_heads + hk) * a.rows;
   load_queries<T, C, kRows>(a, X0, X1, b, hk, r0);
