@@ -177,10 +177,11 @@ constexpr int kHalf = 64 * 128;   // bytes from a tile's row 0 to its row 64
 // kernel, so it is kept short: P is handed over in halves of 64 keys, and a half's
 // exponentials do not wait for its maximum.  They are taken against the row's reference
 // maximum m_t so far; only when the half's own maximum, found alongside, has grown past it
-// are they taken again and O_t, l_t rescaled: by more than 2^8 in a tile's first half,
-// where O_t is at rest, 2^90 in its second, where the products of the first must first
-// end.  A reference that lags changes no result: P and the sums are floating point
-// (P <= 2^90, sums of at most 2^30 of them).
+// by more than 2^8 are they taken again and O_t, l_t rescaled (in a tile's second half the
+// products of the first must end before).  A reference that lags changes P, l and O by a
+// power of two at most: P <= 2^8, and O overflows only where 2^8 len_kv |v| does.  (The second
+// half may not wait longer for it: at 2^90 a row that grows by 60 within a tile took |v| past
+// 2.7e11 to infinity.)
 // Measured on 8 x 2048 queries, 4096 keys (half of them permitted), 16 heads x 128: 208 us,
 // 1480 TFLOP/s.  What was tried and cost more: S in two buffers of 64 keys (272 us: twice the
 // hand-overs), two groups of warps per tile (232 us).
@@ -191,7 +192,7 @@ template <int NC, int NT> struct FwdCfg {
   static constexpr int TMEM = 256 * NT, OCOL = 128 * NT;   // columns, and where O starts
   static constexpr size_t SMEM = (size_t)(NT + 2 * STAGES) * TILE + 512;
 };
-constexpr float kGrow0 = 8.f, kGrow1 = 90.f;
+constexpr float kGrow = 8.f;
 
 template <int NC, int NT>
 __global__ void __launch_bounds__(FwdCfg<NC, NT>::THREADS, 3 - NT)
@@ -410,7 +411,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
         exponentials();
         const float grown = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         // (m = -infinity: any key counts as growth)
-        if (__any_sync(kFull, (grown - m) * c2 > (half ? kGrow1 : kGrow0))) {
+        if (__any_sync(kFull, (grown - m) * c2 > kGrow)) {
           if (half == 1) ok = __all_sync(kFull, tc::mbar_wait(&half_done[t], (uint32_t)j & 1u, abort_flag));
           if (!ok) break;
           tc::tc_fence_after();

@@ -510,3 +510,20 @@ def test_attention_refusals_of_the_python_layer():
     with pytest.raises(K.KfacError, match="WORKSPACE"):
         K.cross_attention_backward(g, q, k, v, out, lse, kv_len, mask,
                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+# one query tile per block with 64 and with 128 channels, two with 128, and the fp32 kernels
+@pytest.mark.parametrize("size", [1.0, 1e30])
+@pytest.mark.parametrize("dtype,d,nq", [(BF16, 64, 200), (BF16, 128, 100), (BF16, 128, 300),
+                                        (BF16, 72, 300), (F32, 64, 100)])
+def test_attention_scores_that_leap(dtype, d, nq, size):
+    """A maximum that grows by 3 to 60 from one 64 keys to the next, in the first and in the second
+    half of a 128-key tile, by other amounts in every row, and v of any size that 2^8 len_kv |v|
+    keeps below 2^128: the weighted mean is finite, and so is out."""
+    nk = 640
+    q, k, v, g, *_ = _inputs(dtype, 1, nq, nk, 2, 1, d, "all", seed=31)
+    steps = torch.tensor([0.0, 4, 60, 20, 27, 90, 93, 150, 156, 175], device="cuda")
+    q[..., 0] = 8 * torch.linspace(0.05, 1, nq, device="cuda").view(1, -1, 1).to(dtype)
+    k[..., 0] = (steps.repeat_interleave(64) * d ** 0.5 / 8).view(1, -1, 1).to(dtype)
+    v = (size * v.float()).to(dtype)
+    _check_attention(q, k, v, g, None, None, B.permitted(1, nk), backward=size == 1.0)
