@@ -521,7 +521,8 @@ kfac_status kfac_cross_attention_workspace_size(const kfac_attention_desc* desc,
  * out as q; lse: fp32 [batch, heads, len_q] contiguous (NULL: not wanted).
  * Scores, softmax statistics and sums are fp32; bf16 inputs enter the tensor
  * cores as they are and the probabilities as bf16 (fp32 inputs: fp32
- * throughout).  v is summed before the division by the weights' sum, with
+ * throughout).  The tensor cores' fp32 sums round towards zero: 2^-12 of a sum
+ * of like signs at most, as no more than 32768 terms meet in one.  v is summed before the division by the weights' sum, with
  * weights up to 2^8: |v| has to stay below 2^120 / len_kv (10^36 / len_kv).
  * workspace: 256-byte aligned, at least the size above. */
 kfac_status kfac_cross_attention(const kfac_attention_desc* desc, const void* q, const void* k,

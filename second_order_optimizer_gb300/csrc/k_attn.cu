@@ -467,11 +467,21 @@ int plain_splits(const kfac_attention_desc& d) {
   const int per_sm = rows <= 16 ? 3 : d.head_dim <= 64 ? 4 : 2;
   return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, per_sm, d.len_kv, 64);
 }
+// Rows (keys, or queries of a group) that one tensor-core accumulator sums.  Its additions
+// round towards zero, about half an ulp each: of a sum of like signs that takes away 4e-5
+// after 8192 rows, 2.2e-4 after 32768, and 3.3e-3, more than the result's rounding to bf16,
+// after 524288 (measured: out, dV, single tokens).  Longer walks come in parts, which are
+// summed in fp32 registers: 16 heads x 128, 8192 queries, 65536 keys: forward 2.65 ms in one
+// part and in two, backward 8.3 and 8.4 ms; 4 heads that share a key head x 131072 queries,
+// 2048 keys, 64 channels: backward 1.71 and 1.74 ms.
+constexpr int kWalkRows = 32768;
 // (a part of fewer than 512 keys costs more to join than it saves: 2 x 300 queries, 300
 // keys, 8 heads x 64: 10 us unsplit, 15 us in three parts)
 int tc_splits(const kfac_attention_desc& d) {
   const int tiles = tc_forward_tiles(d.head_dim, d.len_q, d.len_kv);
-  return pick_splits((int64_t)cdiv(d.len_q, 128 * tiles) * d.heads * d.batch, tiles == 1 ? 2 : 1, d.len_kv, 512);
+  const int fill = pick_splits((int64_t)cdiv(d.len_q, 128 * tiles) * d.heads * d.batch,
+                               tiles == 1 ? 2 : 1, d.len_kv, 512);
+  return std::max(fill, (int)cdiv(d.len_kv, kWalkRows));
 }
 // The form of the forward pass for bf16 rows that TMA and 16-byte loads can address.
 // Few rows: the token kernel reads k and v once per 16 rows, while the tensor-core
@@ -487,7 +497,7 @@ bool token_sizes(const kfac_attention_desc& d) {
 // wave's cost of about 5 us (128 channels, walks x keys: parts and us; the waves' choice
 // first): 128 x 512, 3: 11.0, 4: 13.3; 128 x 2048, 4: 20.8, 3: 24.0, 6: 25.7;
 // 256 x 4096, 3: 46.3, 2: 59.5, 4: 52.5; 128 x 8192, 6: 44.2, 4: 58.0, 8: 51.2.
-// Each warp has at least one step of 16 keys.  Up to kTokenCluster parts are joined in a
+// Each warp has at least one step of 16 keys and at most kWalkRows keys.  Up to kTokenCluster parts are joined in a
 // cluster, more are fixed lengths, which are even by themselves.
 constexpr int kTokenWaves1 = 1024, kTokenWaves2 = 4096;   // keys: 1 wave below, 1.5 from
 int token_splits(const kfac_attention_desc& d, bool ragged, int* part_keys) {
@@ -500,6 +510,7 @@ int token_splits(const kfac_attention_desc& d, bool ragged, int* part_keys) {
   if (ragged && d.batch > 1 && d.len_kv >= kTokenWaves1)
     parts = cdiv(d.len_kv < kTokenWaves2 ? slots : slots + slots / 2, ctas);
   if (clustered) parts = std::min<int64_t>(parts, kTokenCluster);
+  parts = std::max(parts, cdiv(d.len_kv, kTokenWarps * kWalkRows));
   parts = std::min(parts, most);
   *part_keys = d.len_kv;
   if (parts > kTokenCluster) {
@@ -532,7 +543,8 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 // Parts of the backward pass's loops.  A dK/dV block owns `own` keys and walks the group's
 // queries in steps (four products each), a dQ block owns as many queries and walks the
 // keys (three).  Where one block's walk is longer than its share of the whole work, it is
-// split, into pieces of at least four steps; the sums then take a launch more.
+// split, into pieces of at least four steps; the sums then take a launch more.  The
+// tensor-core kernels' accumulators walk no further than kWalkRows.
 // tc: of the tensor-core kernels (bf16), else of the fp32 ones.
 void backward_splits(const kfac_attention_desc& d, Args& a, bool tc) {
   const int own = tc ? 128 : 64, step = tc ? 128 : 32, per_sm = tc ? 1 : 2;
@@ -542,7 +554,8 @@ void backward_splits(const kfac_attention_desc& d, Args& a, bool tc) {
   const int64_t work = (4 * cdiv(d.len_kv, own) * steps_q + 3 * blocks_q * steps_k) * d.kv_heads * d.batch;
   const int64_t share = std::max<int64_t>(1, work / (per_sm * num_sms()));
   auto parts = [&](int64_t steps, int64_t weight) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>({cdiv(steps * weight, share), steps / 4, 32}));
+    const int64_t fill = std::min<int64_t>({cdiv(steps * weight, share), steps / 4, 32});
+    return (int)std::max<int64_t>({1, fill, tc ? cdiv(steps, kWalkRows / step) : 1});
   };
   a.dkv_splits = parts(steps_q, 4);
   a.dq_splits = parts(steps_k, 3);

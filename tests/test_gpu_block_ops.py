@@ -527,3 +527,67 @@ def test_attention_scores_that_leap(dtype, d, nq, size):
     k[..., 0] = (steps.repeat_interleave(64) * d ** 0.5 / 8).view(1, -1, 1).to(dtype)
     v = (size * v.float()).to(dtype)
     _check_attention(q, k, v, g, None, None, B.permitted(1, nk), backward=size == 1.0)
+
+
+def _mean_error(got, ref):
+    return float(((got.double() - ref) / ref).mean())
+
+
+def _positive(seed, n, h, d):
+    """Uniform in [1, 2) times a factor of each channel's own: means that are spread over a binade
+    round to bf16 in both directions."""
+    x = torch.rand(1, n, h, d, device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+    return ((1 + x) * 2 ** (torch.arange(h * d, device="cuda").view(h, d) / (h * d))).to(BF16)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_long_walks_along_the_keys(d):
+    """524288 keys, v positive: what the tensor cores' accumulators lose to rounding towards zero
+    would add up.  No sum of like signs is off by more than 2^-12 on average; P's and the
+    result's roundings (2^-9 at most, of either sign, on 64 or more channels' means) average to a
+    tenth of that or two, so 2^-11 holds both.
+    dq, whose terms have both signs, in norm: P, dS and the result rounded once, and delta, which is
+    taken from the rounded out: u sum_d |dout out| in every dS of a row."""
+    nq, nk, h = 8192, 524288, 2
+    q, k, g = (_randn(i, 1, n, h, d, dtype=BF16) for i, n in ((1, nq), (2, nk), (3, nq)))
+    v = _positive(4, nk, h, d)
+    out, lse = K.cross_attention(q, k, v)
+    dq, _, _ = K.cross_attention_backward(g, q, k, v, out, lse)
+    at = torch.arange(5, nq, 171, device="cuda")
+    for j in range(h):
+        Q, Kk, V, G = q[0, at, j].double(), k[0, :, j].double(), v[0, :, j].double(), g[0, at, j].double()
+        p = torch.softmax(Q @ Kk.T * d ** -0.5, dim=-1)
+        o = p @ V
+        assert abs(_mean_error(out[0, at, j], o)) <= 2.0 ** -11
+        dp = G @ V.T
+        want = (p * (dp - (p * dp).sum(dim=-1, keepdim=True))) @ Kk * d ** -0.5
+        of_delta = U[BF16] * (G * o).abs().sum(dim=-1, keepdim=True) * (p @ Kk) * d ** -0.5
+        assert (dq[0, at, j].double() - want).norm() <= 3 * 2.0 ** -9 * want.norm() + of_delta.norm()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_long_walks_along_the_queries(d):
+    """The same for dV, summed over 4 heads x 131072 queries, dout positive."""
+    nq, nk, h = 131072, 9728, 4
+    q, k, v = (_randn(i, 1, n, x, d, dtype=BF16) for i, n, x in ((1, nq, h), (2, nk, 1), (3, nk, 1)))
+    g = _positive(4, nq, h, d)
+    out, lse = K.cross_attention(q, k, v)
+    _, _, dv = K.cross_attention_backward(g, q, k, v, out, lse)
+    at = torch.arange(3, nk, 101, device="cuda")
+    want = torch.zeros(len(at), d, device="cuda", dtype=torch.float64)
+    for j in range(h):
+        for x in range(0, nq, 16384):
+            s = q[0, x:x + 16384, j].double() @ k[0, :, 0].double().T * d ** -0.5
+            want += torch.softmax(s, dim=-1)[:, at].T @ g[0, x:x + 16384, j].double()
+    assert abs(_mean_error(dv[0, at, 0], want)) <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_long_walks_of_single_tokens(d):
+    """The same for out with one query per key head and more of them than blocks fit: one
+    encoder's 1048576 states read by all."""
+    b, nk, h = 64, 1048576, 8
+    q, k, v = _randn(1, b, 1, h, d, dtype=BF16), _randn(2, 1, nk, 1, d, dtype=BF16), _positive(3, nk, 1, d)
+    out, _ = K.cross_attention(q, k.expand(b, nk, h, d), v.expand(b, nk, h, d))
+    p = torch.softmax(q[:8].view(-1, d).double() @ k.view(nk, d).double().T * d ** -0.5, dim=-1)
+    assert abs(_mean_error(out[:8].view(-1, d), p @ v.view(nk, d).double())) <= 2.0 ** -11
