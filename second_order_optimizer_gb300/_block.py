@@ -9,7 +9,8 @@ Definitions: include/kfac.h.
 
 ``stream``: a torch stream or a raw handle; torch's current stream of the tensors' device
 unless one is given.  The inputs have to be ready there (as for every call of the package);
-tensors allocated here are marked as used on it.
+tensors allocated here belong to it and are marked as used on the current one, where the
+caller has to wait for it before reading them.
 """
 from __future__ import annotations
 
@@ -79,13 +80,24 @@ def _call(f, what, dev, stream, *args):
         raise KfacError(code, what)
 
 
-def _used_on(stream, dev, *made):
-    """Tensors allocated here belong to torch's current stream: tell its allocator where else
-    they are used."""
-    s = torch.cuda.ExternalStream(stream, device=dev) if isinstance(stream, int) else stream
-    for t in made:
-        if t is not None:
-            t.record_stream(s)
+def _empty(shape, dtype, dev, stream):
+    """A tensor that ``stream`` (not None) may write at once.  torch hands out memory whose last
+    use is still queued on the stream that it belongs to, which orders nothing on another: so it
+    has to be that stream's own."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    current, device = torch.cuda.current_stream(dev), torch.device("cuda", dev)
+    if dev != _current_device():
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
+    else:   # the same; the context takes 9 us more
+        torch.cuda.set_stream(stream)
+        try:
+            t = torch.empty(shape, dtype=dtype, device=device)
+        finally:
+            torch.cuda.set_stream(current)
+    t.record_stream(current)
+    return t
 
 
 # --------------------------------------------------------------------------- rotary positions
@@ -96,17 +108,18 @@ def rope_table(rows: int, rotary_dim: int, base: float = 10000.0, scaling: int =
     """kfac_rope_table: the cosines and sines of positions 0..rows-1, float32
     [rows, rotary_dim].  scaling: KFAC_ROPE_PLAIN, KFAC_ROPE_LINEAR, KFAC_ROPE_NTK or
     KFAC_ROPE_YARN (which reads original_length), over a context ``factor`` times as long."""
-    made = None
     if out is None:
-        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-        out = made = torch.empty(rows, rotary_dim, device=dev)
+        dev = None if device is None else torch.device(device)
+        dev = torch.cuda.current_device() if dev is None or dev.index is None else dev.index
+        if stream is None:
+            out = torch.empty(rows, rotary_dim, device=torch.device("cuda", dev))
+        else:
+            out = _empty((rows, rotary_dim), torch.float32, dev, stream)
     dev = _device(out, "rope_table")
     if out.dtype != torch.float32 or out.shape != (rows, rotary_dim) or not out.is_contiguous():
         raise ValueError("rope_table: out is float32 [rows, rotary_dim], contiguous")
     _call(LIB.kfac_rope_table, "kfac_rope_table", dev, stream, out.data_ptr(), rows, rotary_dim,
           float(base), scaling, float(factor), float(original_length))
-    if stream is not None:
-        _used_on(stream, dev, made)
     return out
 
 
@@ -126,14 +139,14 @@ def rope(q, k, table, positions=None, position_offset: int = 0, interleaved: boo
         raise ValueError("rope: table is float32 [rows, rotary_dim], contiguous")
     if table.get_device() != dev:
         _elsewhere("rope", "table", table, dev)
-    made_q = made_k = None
     h = kv = 0
     qs = ks = oqs = oks = (0, 0, 0, 0)
     if q is not None:
         shape, qs = q.shape, q.stride()
         h = shape[2]
         if out_q is None:
-            out_q = made_q = torch.empty(shape, dtype=dtype, device=q.device)
+            out_q = (torch.empty(shape, dtype=dtype, device=q.device) if stream is None
+                     else _empty(shape, dtype, dev, stream))
         oqs = out_q.stride()
         if out_q.shape != shape or out_q.dtype is not dtype or out_q.get_device() != dev or (
                 d > 1 and (qs[3] != 1 or oqs[3] != 1)):
@@ -143,7 +156,8 @@ def rope(q, k, table, positions=None, position_offset: int = 0, interleaved: boo
         shape, ks = k.shape, k.stride()
         kb, kn, kv, kd = shape
         if out_k is None:
-            out_k = made_k = torch.empty(shape, dtype=dtype, device=k.device)
+            out_k = (torch.empty(shape, dtype=dtype, device=k.device) if stream is None
+                     else _empty(shape, dtype, dev, stream))
         oks = out_k.stride()
         if kb != b or kn != n or kd != d or k.dtype is not dtype or k.get_device() != dev or (
                 out_k.shape != shape or out_k.dtype is not dtype or out_k.get_device() != dev) or (
@@ -165,8 +179,6 @@ def rope(q, k, table, positions=None, position_offset: int = 0, interleaved: boo
     _call(LIB.kfac_rope, "kfac_rope", dev, stream, desc, None if q is None else q.data_ptr(),
           None if k is None else k.data_ptr(), table.data_ptr(), pp,
           None if q is None else out_q.data_ptr(), None if k is None else out_k.data_ptr())
-    if stream is not None:
-        _used_on(stream, dev, made_q, made_k)
     return (None if q is None else out_q), (None if k is None else out_k)
 
 
@@ -193,9 +205,10 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, st
     if not (0 <= seed <= _MAX64 and 0 <= offset <= _MAX64):
         raise ValueError("dropout: seed and offset are 64-bit counts")
     dt, shape, dev = _dtype(x, "dropout"), x.shape, _device(x, "dropout")
-    made, rp = None, None
+    rp = None
     if out is None:
-        out = made = torch.empty(shape, dtype=x.dtype, device=x.device)
+        out = (torch.empty(shape, dtype=x.dtype, device=x.device) if stream is None
+               else _empty(shape, x.dtype, dev, stream))
     else:
         _like("out", out, x, shape, dev)
     flat = x.is_contiguous() and out.is_contiguous()
@@ -211,8 +224,6 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, out=None, st
         rows, cols = shape
     _call(LIB.kfac_dropout, "kfac_dropout", dev, stream, dt, x.data_ptr(), ldx, rp, ldr,
           out.data_ptr(), ldo, rows, cols, p, seed, offset)
-    if stream is not None:
-        _used_on(stream, dev, made)
     return out
 
 
@@ -280,6 +291,13 @@ def _workspace_bytes(desc, backward, dev):
     return nbytes.value
 
 
+def _workspace(desc, backward, dev, stream):
+    """A call's own workspace."""
+    n = _workspace_bytes(desc, backward, dev)
+    return (torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", dev)) if stream is None
+            else _empty((n,), torch.uint8, dev, stream))
+
+
 def cross_attention_workspace(q, k, backward: bool = False):
     """A workspace tensor for cross_attention (backward=True: and cross_attention_backward) of
     tensors like these, to be kept and passed to the calls."""
@@ -298,25 +316,24 @@ def cross_attention(q, k, v, kv_len=None, key_mask=None, scale=None, out=None, l
     pass."""
     what = "cross_attention"
     dev = _device(q, what)
-    made_o = made_l = made_w = None
     if out is None:
-        out = made_o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device) if stream is None
+               else _empty(q.shape, q.dtype, dev, stream))
     desc = _attention(what, q, k, v, out, scale, dev)
     lp, mp = _keys(what, kv_len, key_mask, k, dev)
     if lse is None:
-        lse = made_l = torch.empty(q.shape[0], q.shape[2], q.shape[1], device=q.device)
+        rows = (q.shape[0], q.shape[2], q.shape[1])
+        lse = (torch.empty(rows, device=q.device) if stream is None
+               else _empty(rows, torch.float32, dev, stream))
     else:
         _stats(what, lse, q, dev)
     if workspace is None:
-        workspace = made_w = torch.empty(_workspace_bytes(desc, False, dev), dtype=torch.uint8,
-                                         device=q.device)
+        workspace = _workspace(desc, False, dev, stream)
     elif workspace.get_device() != dev:
         _elsewhere(what, "workspace", workspace, dev)
     _call(LIB.kfac_cross_attention, "kfac_cross_attention", dev, stream, desc, q.data_ptr(),
           k.data_ptr(), v.data_ptr(), lp, mp, out.data_ptr(), lse.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
-    if stream is not None:
-        _used_on(stream, dev, made_o, made_l, made_w)
     return out, lse
 
 
@@ -331,13 +348,15 @@ def cross_attention_backward(dout, q, k, v, out, lse, kv_len=None, key_mask=None
     lp, mp = _keys(what, kv_len, key_mask, k, dev)
     _stats(what, lse, q, dev)
     dtype, shape, keys = q.dtype, q.shape, k.shape
-    made = [None] * 4
     if dq is None:
-        dq = made[0] = torch.empty(shape, dtype=dtype, device=q.device)
+        dq = (torch.empty(shape, dtype=dtype, device=q.device) if stream is None
+              else _empty(shape, dtype, dev, stream))
     if dk is None:
-        dk = made[1] = torch.empty(keys, dtype=dtype, device=q.device)
+        dk = (torch.empty(keys, dtype=dtype, device=q.device) if stream is None
+              else _empty(keys, dtype, dev, stream))
     if dv is None:
-        dv = made[2] = torch.empty(keys, dtype=dtype, device=q.device)
+        dv = (torch.empty(keys, dtype=dtype, device=q.device) if stream is None
+              else _empty(keys, dtype, dev, stream))
     gs = _heads(what, "dout", dout, dtype, shape, dev)
     qs = _heads(what, "dq", dq, dtype, shape, dev)
     ks = _heads(what, "dk", dk, dtype, keys, dev)
@@ -345,16 +364,13 @@ def cross_attention_backward(dout, q, k, v, out, lse, kv_len=None, key_mask=None
     grads = ATTENTION_GRAD_DESC.pack(gs[0], gs[1], gs[2], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2],
                                      vs[0], vs[1], vs[2])
     if workspace is None:
-        workspace = made[3] = torch.empty(_workspace_bytes(desc, True, dev), dtype=torch.uint8,
-                                          device=q.device)
+        workspace = _workspace(desc, True, dev, stream)
     elif workspace.get_device() != dev:
         _elsewhere(what, "workspace", workspace, dev)
     _call(LIB.kfac_cross_attention_backward, "kfac_cross_attention_backward", dev, stream, desc,
           grads, dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
           lse.data_ptr(), lp, mp, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
           workspace.data_ptr(), workspace.nbytes)
-    if stream is not None:
-        _used_on(stream, dev, *made)
     return dq, dk, dv
 
 

@@ -591,3 +591,51 @@ def test_attention_long_walks_of_single_tokens(d):
     out, _ = K.cross_attention(q, k.expand(b, nk, h, d), v.expand(b, nk, h, d))
     p = torch.softmax(q[:8].view(-1, d).double() @ k.view(nk, d).double().T * d ** -0.5, dim=-1)
     assert abs(_mean_error(out[:8].view(-1, d), p @ v.view(nk, d).double())) <= 2.0 ** -11
+
+
+def _owner(p):
+    """The stream whose memory address p is in."""
+    return next(x["stream"] for x in torch.cuda.memory_snapshot()
+                if x["address"] <= p < x["address"] + x["total_size"])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_and_workspaces_belong_to_the_given_stream(monkeypatch, raw):
+    """Memory that torch's allocator takes back is handed out again at once to the stream it belongs
+    to, before that stream's kernels have ended: what a call on another stream allocates has to be
+    that stream's.  (Shown by ownership alone: nothing here depends on timing.)"""
+    q, k, v, g, *_ = _inputs(BF16, 1, 20, 3100, 2, 1, 64, "all")
+    table = K.rope_table(64, 64)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    made, empty = [], torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: made.append(empty(*a, **kw)) or made[-1])
+    K.rope_table(64, 64, stream=stream)
+    K.rope_table(64, 64, device="cuda", stream=stream)
+    K.rope(q, q, table, stream=stream)
+    K.dropout(q, 0.5, 1, stream=stream)
+    K.dropout_backward(q, 0.5, 1, stream=stream)
+    out, lse = K.cross_attention(q, k, v, stream=stream)
+    K.cross_attention_backward(g, q, k, v, out, lse, stream=stream)
+    side.synchronize()
+    assert len(made) == 13 and all(t.numel() for t in made)
+    assert {_owner(t.data_ptr()) for t in made} == {side.cuda_stream}
+    made.clear()
+    K.dropout(q, 0.5, 1)
+    assert {_owner(t.data_ptr()) for t in made} == {torch.cuda.current_stream().cuda_stream}
+
+
+def test_another_stream_leaves_memory_with_queued_readers_alone():
+    """A tensor that was freed while its reader is queued, then calls on another stream that
+    allocate as much."""
+    n = 1 << 20
+    z, side = torch.randn(n, device="cuda"), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    x = torch.full((n,), 7.0, device="cuda")
+    torch.cuda._sleep(200_000_000)   # about 0.1 s
+    y = x + 1
+    del x
+    made = [K.dropout(z, 0.0, 1, stream=side) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert (y == 8).all() and all(torch.equal(t, z) for t in made)
