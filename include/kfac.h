@@ -547,8 +547,8 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* desc,
                                           void* workspace, size_t workspace_bytes,
                                           cudaStream_t stream);
 
-/* Synchronise the device and report the first device-side error of the block
- * operators in this process since the last call (then clear it): a pipeline
+/* Synchronise the current device and report the first device-side error of the
+ * block operators on it since the last call (then clear it): a pipeline
  * wait of the tensor-core attention that gave up (KFAC_ERR_TIMEOUT; info: which
  * role).  The outputs of the blocks concerned hold NaN.  KFAC_OK: none. */
 kfac_status kfac_operator_status(int* info);

@@ -375,7 +375,7 @@ def cross_attention_backward(dout, q, k, v, out, lse, kv_len=None, key_mask=None
 
 
 def operator_status():
-    """kfac_operator_status: synchronises; (code, info) of the first device error of these
-    operators since the last call (code 0: none)."""
+    """kfac_operator_status: synchronises the current device; (code, info) of the first device
+    error of these operators on it since the last call (code 0: none)."""
     info = ctypes.c_int(0)
     return LIB.kfac_operator_status(ctypes.byref(info)), info.value

@@ -1,6 +1,7 @@
 // Shared by the cross-attention translation units.
 #pragma once
 #include "kfac_internal.cuh"
+#include "per_device.h"
 
 namespace kfac {
 namespace attn {
@@ -79,6 +80,18 @@ __device__ __forceinline__ int64_t row_offset(const Args& a, const int64_t (&s)[
                                               int r) {
   const int g = r / a.len_q, i = r - g * a.len_q;
   return b * s[0] + i * s[1] + (int64_t)(hk * a.group + g) * s[2];
+}
+
+// Lets a kernel's blocks have this much dynamic shared memory on the current device.
+template <typename K> kfac_status allow_smem(OncePerDevice& once, K kern, size_t bytes) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && once(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
+               cudaSuccess;
+      }))
+    return KFAC_OK;
+  check_launch();   // keeps the runtime's message
+  return KFAC_ERR_CUDA;
 }
 
 // Few query rows (bf16, rows that tc_forward_ok accepts).

@@ -368,16 +368,11 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
   }
 }
 
-template <typename K>
-bool allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-         cudaSuccess;
-}
-
 template <typename T, typename C>
 kfac_status launch_few_rows(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(few_rows_kernel<T, C>, C::SMEM);
-  if (!ok) return KFAC_ERR_CUDA;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, few_rows_kernel<T, C>, C::SMEM);
+  if (e != KFAC_OK) return e;
   const dim3 grid((unsigned)(cdiv(a.rows, C::BO) * a.splits), a.kv_heads, a.batch);
   launch_pdl(few_rows_kernel<T, C>, grid, dim3(C::THREADS), C::SMEM, st, a);
   count_launch();

@@ -628,15 +628,11 @@ __global__ void __launch_bounds__(kF32Threads) f32_delta_kernel(const __grid_con
   }
 }
 
-template <typename K>
-bool allow_smem(K kern, size_t bytes) {
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) ==
-         cudaSuccess;
-}
 template <typename T, typename C>
 kfac_status launch_forward(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(f32_forward_kernel<T, C>, C::FWD);
-  if (!ok) return KFAC_ERR_CUDA;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, f32_forward_kernel<T, C>, C::FWD);
+  if (e != KFAC_OK) return e;
   const dim3 grid((unsigned)(cdiv(a.rows, kRows) * a.splits), a.kv_heads, a.batch);
   launch_pdl(f32_forward_kernel<T, C>, grid, dim3(kF32Threads), C::FWD, st, a);
   count_launch();
@@ -644,8 +640,9 @@ kfac_status launch_forward(const Args& a, cudaStream_t st) {
 }
 template <typename T, typename C>
 kfac_status launch_backward(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(f32_backward_kernel<T, C>, C::BWD);
-  if (!ok) return KFAC_ERR_CUDA;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, f32_backward_kernel<T, C>, C::BWD);
+  if (e != KFAC_OK) return e;
   const dim3 grid((unsigned)(cdiv(a.len_kv, kRows) * a.dkv_splits + cdiv(a.rows, kRows) * a.dq_splits),
                   a.kv_heads, a.batch);
   launch_pdl(f32_backward_kernel<T, C>, grid, dim3(kF32Threads), C::BWD, st, a);
@@ -655,8 +652,9 @@ kfac_status launch_backward(const Args& a, cudaStream_t st) {
 
 template <typename C>
 kfac_status launch_delta(const Args& a, cudaStream_t st) {
-  static const bool ok = allow_smem(f32_delta_kernel<__nv_bfloat16, C>, C::BWD);
-  if (!ok) return KFAC_ERR_CUDA;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, f32_delta_kernel<__nv_bfloat16, C>, C::BWD);
+  if (e != KFAC_OK) return e;
   launch_pdl(f32_delta_kernel<__nv_bfloat16, C>, dim3((unsigned)cdiv(a.rows, kRows), a.kv_heads, a.batch),
              dim3(kF32Threads), C::BWD, st, a);
   count_launch();

@@ -1070,12 +1070,12 @@ bool rows_ok(const void* p, const int64_t* s, int rows, int heads, int batch) {
 template <int NC, int NT>
 kfac_status launch_tc_forward(const Args& a, cudaStream_t st) {
   using C = FwdCfg<NC, NT>;
-  static const bool ok = cudaFuncSetAttribute(tc_forward_kernel<NC, NT>,
-                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)C::SMEM) == cudaSuccess;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, tc_forward_kernel<NC, NT>, C::SMEM);
+  if (e != KFAC_OK) return e;
   CUtensorMap mq, mk, mv;
   MapMul xq, xk, xv;
-  if (!ok || !make_map(&mq, &xq, a.q, a.qs, a.dim, a.len_q, a.heads, a.batch) ||
+  if (!make_map(&mq, &xq, a.q, a.qs, a.dim, a.len_q, a.heads, a.batch) ||
       !make_map(&mk, &xk, a.k, a.ks, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&mv, &xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch))
     return KFAC_ERR_CUDA;
@@ -1088,11 +1088,11 @@ kfac_status launch_tc_forward(const Args& a, cudaStream_t st) {
 template <int NC>
 kfac_status launch_tc_backward(const Args& a, cudaStream_t st) {
   using C = BwdCfg<NC>;
-  static const bool ok = cudaFuncSetAttribute(tc_backward_kernel<NC>,
-                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)C::SMEM) == cudaSuccess;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, tc_backward_kernel<NC>, C::SMEM);
+  if (e != KFAC_OK) return e;
   BwdMaps m;
-  if (!ok || !make_map(&m.q, &m.xq, a.q, a.qs, a.dim, a.len_q, a.heads, a.batch) ||
+  if (!make_map(&m.q, &m.xq, a.q, a.qs, a.dim, a.len_q, a.heads, a.batch) ||
       !make_map(&m.k, &m.xk, a.k, a.ks, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&m.v, &m.xv, a.v, a.vs, a.dim, a.len_kv, a.kv_heads, a.batch) ||
       !make_map(&m.g, &m.xg, a.dout, a.dos, a.dim, a.len_q, a.heads, a.batch))

@@ -451,10 +451,9 @@ __global__ void __launch_bounds__(128) delta_keys_kernel(const __grid_constant__
 template <int DC, bool kCluster>
 kfac_status launch_token(const Args& a, cudaStream_t st) {
   using C = TokenCfg<DC>;
-  static const bool ok = cudaFuncSetAttribute(token_kernel<DC, kCluster>,
-                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)C::SMEM) == cudaSuccess;
-  if (!ok) return KFAC_ERR_CUDA;
+  static OncePerDevice once;
+  const kfac_status e = allow_smem(once, token_kernel<DC, kCluster>, C::SMEM);
+  if (e != KFAC_OK) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(cdiv(a.rows, 16) * a.splits), a.kv_heads, a.batch);
   cfg.blockDim = dim3(kTokenWarps * 32);

@@ -216,3 +216,45 @@ def test_python_refuses_cpu_tensors_and_wrong_types(lib):
         K.dropout(x, 0.5, -1)
     with pytest.raises(ValueError, match="CUDA"):
         K.cross_attention(x, x, x)
+
+
+# ------------------------------------------------------------------- state kept per device
+
+def test_shared_memory_limits_are_set_on_every_device(tmp_path):
+    """The helper behind the attention launches, compiled for the host with a call that counts:
+    once per device, again where it failed, and past the devices it has room for every time.  No
+    launch keeps a flag of its own for the whole process."""
+    import os
+    import re
+    import shutil
+    import subprocess
+    import __graft_entry__
+    csrc = os.path.join(__graft_entry__.ROOT, "second_order_optimizer_gb300", "csrc")
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    src = tmp_path / "t.cpp"
+    src.write_text("""
+#include "per_device.h"
+int main() {
+  static kfac::OncePerDevice once;
+  int calls[3] = {0, 0, 0};
+  bool works = true;
+  auto set = [&](int d) { return once(d, [&] { ++calls[d % 3]; return works; }); };
+  if (!set(0) || !set(0) || calls[0] != 1) return 1;
+  if (!set(1) || calls[1] != 1) return 2;          // another device: set there too
+  works = false;
+  if (set(2) || set(2) || calls[2] != 2) return 3; // a failure is not remembered
+  works = true;
+  if (!set(2) || !set(2) || calls[2] != 3) return 4;
+  if (!set(99) || !set(99) || calls[0] != 3) return 5;
+  return 0;
+}
+""")
+    subprocess.run([gxx, "-std=c++17", "-I" + csrc, str(src), "-o", str(tmp_path / "t")], check=True)
+    assert subprocess.run([str(tmp_path / "t")]).returncode == 0
+    for name in sorted(os.listdir(csrc)):
+        if name.startswith(("attn", "k_attn")):
+            text = open(os.path.join(csrc, name)).read()
+            assert not re.search(r"static\s+const\s+bool\s+\w+\s*=", text), name
+            assert text.count("cudaFuncSetAttribute(") == (name == "attn.cuh"), name
