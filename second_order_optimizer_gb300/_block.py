@@ -15,6 +15,7 @@ caller has to wait for it before reading them.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -25,6 +26,7 @@ _DTYPE = {torch.float32: KFAC_F32, torch.bfloat16: KFAC_BF16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _MAX64 = (1 << 64) - 1
+_F32_MIN, _F32_MAX = 2.0 ** -126, (2 - 2.0 ** -23) * 2.0 ** 127
 
 # The checks below are spelled out call by call rather than looped over: a call of a few rows
 # takes the GPU two microseconds, and each attribute of a tensor costs about 0.1.
@@ -250,8 +252,11 @@ def _attention(what, q, k, v, out, scale, dev):
         _heads(what, "k", k, dtype, (b, nk, kv, d), dev)
     vs = _heads(what, "v", v, dtype, keys, dev) if v is not None else ks
     os = _heads(what, "out", out, dtype, shape, dev) if out is not None else qs
-    return ATTENTION_DESC.pack(_dtype(q, what), b, nq, nk, h, kv, d,
-                               0.0 if scale is None else scale, qs[0], qs[1], qs[2], ks[0], ks[1],
+    if scale is None:
+        scale = 0.0   # the library's default
+    elif abs(scale) < _F32_MIN or _F32_MAX < abs(scale) < math.inf:   # (it refuses the other bad ones)
+        raise ValueError(f"{what}: scale is a normal float32 number, not {scale} (None: 1/sqrt(head_dim))")
+    return ATTENTION_DESC.pack(_dtype(q, what), b, nq, nk, h, kv, d, scale, qs[0], qs[1], qs[2], ks[0], ks[1],
                                ks[2], vs[0], vs[1], vs[2], os[0], os[1], os[2])
 
 
@@ -312,7 +317,7 @@ def cross_attention(q, k, v, kv_len=None, key_mask=None, scale=None, out=None, l
     """kfac_cross_attention: softmax(scale q k^T) v over the permitted keys; returns (out, lse).
     q [batch, len_q, heads, head_dim]; k, v [batch, len_kv, kv_heads, head_dim]; kv_len int32
     [batch] and key_mask uint8 or bool [batch, len_kv] say which keys are permitted (None: all);
-    scale None: 1/sqrt(head_dim).  lse: float32 [batch, heads, len_q], kept for the backward
+    scale (above 0) None: 1/sqrt(head_dim).  lse: float32 [batch, heads, len_q], kept for the backward
     pass."""
     what = "cross_attention"
     dev = _device(q, what)

@@ -218,6 +218,23 @@ def test_python_refuses_cpu_tensors_and_wrong_types(lib):
         K.cross_attention(x, x, x)
 
 
+def test_python_refuses_a_scale_that_would_mean_the_default(lib):
+    """The library takes a scale of 0 for 1/sqrt(head_dim): a caller's own 0, or what rounds to 0,
+    may not become that."""
+    torch = pytest.importorskip("torch")
+    from second_order_optimizer_gb300 import _block
+    x = torch.zeros(2, 3, 4, 16)
+    desc = lambda scale: _block._attention("attention", x, x, x, x, scale, -1)
+    for scale in (0.0, 0, -0.0, 1e-50, 1e39, -1e300):
+        with pytest.raises(ValueError, match="scale"):
+            desc(scale)
+    at = lib.struct.calcsize("@7i")
+    assert [lib.struct.unpack_from("f", desc(x), at)[0] for x in (None, 0.25, 2.0 ** -126)] == [0.0, 0.25, 2.0 ** -126]
+    n = ctypes.c_size_t(0)
+    for scale in (-1.0, float("nan"), float("inf")):   # refused by the library
+        assert lib.LIB.kfac_cross_attention_workspace_size(desc(scale), 0, ctypes.byref(n)) == A
+
+
 # ------------------------------------------------------------------- state kept per device
 
 def test_shared_memory_limits_are_set_on_every_device(tmp_path):

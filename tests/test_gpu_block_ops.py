@@ -639,3 +639,14 @@ def test_another_stream_leaves_memory_with_queued_readers_alone():
     made = [K.dropout(z, 0.0, 1, stream=side) for _ in range(4)]
     torch.cuda.synchronize()
     assert (y == 8).all() and all(torch.equal(t, z) for t in made)
+
+
+def test_attention_refuses_a_scale_of_zero():
+    q, k, v, g, *_ = _inputs(BF16, 1, 4, 6, 2, 2, 64, "all")
+    out, lse = K.cross_attention(q, k, v, scale=0.25)
+    for call in (lambda s: K.cross_attention(q, k, v, scale=s),
+                 lambda s: K.cross_attention_backward(g, q, k, v, out, lse, scale=s)):
+        with pytest.raises(ValueError, match="scale"):
+            call(0.0)
+        with pytest.raises(K.KfacError):
+            call(-0.25)
