@@ -10,8 +10,10 @@
 //
 // Every wait is bounded (tc::mbar_wait); a role that gives up raises the block's abort
 // flag, records KFAC_ERR_TIMEOUT in the operators' status word, and the block leaves
-// NaN in its outputs.
+// NaN in its outputs.  Such a block does not let its shared and tensor memory go before the
+// producer's copies have landed and the issuer's products have ended (bounded as well).
 #include "attn.cuh"
+#include "ring.h"
 #include "tc_prims.cuh"
 #include "tensor_map.cuh"
 
@@ -142,6 +144,22 @@ __device__ __forceinline__ void load_chunks(uint8_t* dst, const CUtensorMap* m, 
   for (int c = 0; c < NC; ++c) tc::tma_load_4d(dst + c * kChunk, m, bar, 64 * c, row, head, batch);
 }
 
+constexpr long long kLandCycles = 1 << 20;   // 0.5 ms
+// The copies behind a barrier that was used this often, or behind a ring's.
+__device__ __forceinline__ void land(uint64_t* bar, int uses) {
+  int never = 0;
+  if (uses > 0) tc::mbar_wait(bar, ring_last_parity(uses), &never, kLandCycles);
+}
+template <int kStages> __device__ __forceinline__ void land_ring(uint64_t* bars, int issued) {
+  for (int s = 0; s < kStages; ++s) land(&bars[s], ring_uses(issued, s, kStages));
+}
+// Everything that this warp has issued.  `bar` is used for nothing else.
+__device__ __forceinline__ void end_mmas(uint64_t* bar) {
+  int never = 0;
+  tc::umma_commit_by(tc::elect_leader(), bar);
+  tc::mbar_wait(bar, 0, &never, kLandCycles);
+}
+
 // D[128 x 128] = A[128 x dim] . B[128 x dim]^T, both tiles in shared memory, channels
 // contiguous.
 __device__ __forceinline__ void mma_scores(uint32_t leader, uint32_t d, const uint8_t* a, const uint8_t* b,
@@ -209,8 +227,8 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   uint64_t *q_full = bars, *k_full = q_full + 2, *k_empty = k_full + ST, *v_full = k_empty + ST,
            *v_empty = v_full + ST, *v_ready = v_empty + ST, *w_full = v_ready + ST,
            *s_full = w_full + ST, *p_ready = s_full + 2 /* [2 t + half] */, *half_done = p_ready + 4,
-           *o_full = half_done + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_full + 2);
+           *o_full = half_done + 2, *ended = o_full + 2 /* and one that keeps `words` aligned */;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ended + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint4* words = reinterpret_cast<uint4*>(tmem_slot + 4);   // [ST] permitted keys of a tile
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -223,6 +241,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       tc::mbar_init(&half_done[t], 1);
       tc::mbar_init(&o_full[t], 1);
     }
+    tc::mbar_init(ended, 1);
     for (int s = 0; s < ST; ++s) {
       tc::mbar_init(&k_full[s], 1);
       tc::mbar_init(&k_empty[s], 1);
@@ -254,6 +273,7 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   const int t0 = (int)((int64_t)tiles * split / a.splits);
   const int n = (int)((int64_t)tiles * (split + 1) / a.splits) - t0;
   const int ksteps = (a.dim + 15) / 16;
+  int ks = 0, vs = 0;   // the producer's: tiles of k and v issued
   auto give_up = [&](int info) {
     *abort_flag = 1;
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
@@ -266,25 +286,19 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
       tc::tma_prefetch_desc(&mk);
       tc::tma_prefetch_desc(&mv);
       load_chunks<NC>(Qs, &mq, &q_full[0], q0, h * xq.head, b * xq.batch);
-      int j = 0;
-      for (; j < n; ++j) {
+      for (int j = 0; j < n; ++j) {
         const int s = j % ST;
         const uint32_t ph = (uint32_t)(j / ST) & 1u;
         if (!tc::mbar_wait(&k_empty[s], ph ^ 1, abort_flag)) break;
         load_chunks<NC>(Ks + s * C::TILE, &mk, &k_full[s], (t0 + j) * BT, hk * xk.head, b * xk.batch);
+        ++ks;
         if (j == 0 && nt == 2)
           load_chunks<NC>(Qs + C::TILE, &mq, &q_full[1], q0 + BT, h * xq.head, b * xq.batch);
         if (!tc::mbar_wait(&v_empty[s], ph ^ 1, abort_flag)) break;
         load_chunks<NC>(Vs + s * C::TILE, &mv, &v_full[s], (t0 + j) * BT, hk * xv.head, b * xv.batch);
+        ++vs;
       }
-      if (j < n) {   // winding down: let the copies in flight land before the block ends
-        give_up(101);
-        int never = 0;
-        for (int s = 0; s < ST; ++s) {
-          tc::mbar_wait(&k_full[s], (uint32_t)(j / ST) & 1u, &never, 1 << 20);
-          tc::mbar_wait(&v_full[s], (uint32_t)(j / ST) & 1u, &never, 1 << 20);
-        }
-      }
+      if (vs < n) give_up(101);
     }
   } else if (warp == 1) {
     if (n > 0) {  // ----------------------------------------------------- MMA issuer
@@ -487,6 +501,16 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
   }
   }
   __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) {
+      land(&q_full[0], n > 0);
+      land(&q_full[1], nt == 2 && ks > 0);
+      land_ring<ST>(k_full, ks);
+      land_ring<ST>(v_full, vs);
+    }
+    if (warp == 1) end_mmas(ended);
+    __syncthreads();
+  }
   if (warp == 1) tc::tmem_dealloc(tmem, C::TMEM);
 }
 
@@ -565,7 +589,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   uint64_t *kv_full = bars, *q_full = bars + 1, *q_empty = bars + 4, *g_full = bars + 7,
            *g_empty = bars + 9, *dp_full = bars + 12, *p_ready = bars + 13,
            *ds_ready = bars + 14, *st_full = bars + 15, *st_empty = bars + 17, *done = bars + 19,
-           *kv_ready = bars + 20;
+           *kv_ready = bars + 20, *ended = bars + 22;
   // S^T of step i: one buffer, or with 64 channels two (the second behind dK)
   auto s_full = [&](int i) { return NC == 1 && i % 2 ? bars + 21 : bars + 11; };
   auto s_phase = [&](int i) { return (uint32_t)(NC == 1 ? i / 2 : i) & 1u; };
@@ -579,6 +603,7 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
   const int first = (int)((int64_t)steps * split / a.dkv_splits);
   const int n = (int)((int64_t)steps * (split + 1) / a.dkv_splits) - first;
   const int ksteps = (a.dim + 15) / 16;
+  int qs = 0, gs = 0;   // the producer's: tiles of q and dO issued
   auto give_up = [&](int info) {
     *abort_flag = 1;
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
@@ -592,21 +617,17 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
         tc::tma_load_4d(Ks + c * kChunk, &mp.k, kv_full, 64 * c, k0, hk * mp.xk.head, b * mp.xk.batch);
         tc::tma_load_4d(Vs + c * kChunk, &mp.v, kv_full, 64 * c, k0, hk * mp.xv.head, b * mp.xv.batch);
       }
-      int i = 0;
-      for (; i < n; ++i) {
+      for (int i = 0; i < n; ++i) {
         const int h = hk * a.group + (first + i) / qtiles, row = (first + i) % qtiles * BT;
         const int sq = i % 3, sg = i % 2;
         if (!tc::mbar_wait(&q_empty[sq], ((uint32_t)(i / 3) & 1u) ^ 1u, abort_flag)) break;
         load_chunks<NC>(Qs + sq * C::TILE, &mp.q, &q_full[sq], row, h * mp.xq.head, b * mp.xq.batch);
+        ++qs;
         if (!tc::mbar_wait(&g_empty[sg], ((uint32_t)(i / 2) & 1u) ^ 1u, abort_flag)) break;
         load_chunks<NC>(Gs + sg * C::TILE, &mp.g, &g_full[sg], row, h * mp.xg.head, b * mp.xg.batch);
+        ++gs;
       }
-      if (i < n) {   // winding down: let the copies in flight land
-        give_up(111);
-        int never = 0;
-        for (int s = 0; s < 3; ++s) tc::mbar_wait(&q_full[s], (uint32_t)(i / 3) & 1u, &never, 1 << 20);
-        for (int s = 0; s < 2; ++s) tc::mbar_wait(&g_full[s], (uint32_t)(i / 2) & 1u, &never, 1 << 20);
-      }
+      if (gs < n) give_up(111);
     }
   } else if (warp == 1) {
     if (n > 0) {  // ------------------------------------------------------- MMA issuer
@@ -789,6 +810,16 @@ __device__ __forceinline__ void dkv_block(const Args& a, const BwdMaps& mp, int 
     }
     tc::tc_fence_before();
   }
+  __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) {
+      land(kv_full, n > 0);
+      land_ring<3>(q_full, qs);
+      land_ring<2>(g_full, gs);
+    }
+    if (warp == 1) end_mmas(ended);
+    __syncthreads();
+  }
 }
 
 template <int NC>
@@ -798,7 +829,8 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   uint8_t *Qs = smem, *Gs = Qs + C::TILE, *Ks = Gs + C::TILE, *Vs = Ks + 3 * C::TILE;
   uint64_t *qg_full = bars, *k_full = bars + 1, *k_empty = bars + 4, *v_full = bars + 7,
            *v_empty = bars + 9, *dp_full = bars + 11, *s_read = bars + 13, *ds_ready = bars + 14,
-           *s_full = bars + 15, *done = bars + 19, *k_ready = bars + 20, *w_full = bars + 23;
+           *s_full = bars + 15, *ended = bars + 16, *done = bars + 19, *k_ready = bars + 20,
+           *w_full = bars + 23;
   uint4* words = reinterpret_cast<uint4*>(bars + 28);   // [3] permitted keys of a tile
   const int warp = __shfl_sync(kFull, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int qtiles = (a.len_q + BT - 1) / BT;
@@ -809,6 +841,7 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
   const int first = (int)((int64_t)tiles * split / a.dq_splits);
   const int n = (int)((int64_t)tiles * (split + 1) / a.dq_splits) - first;
   const int ksteps = (a.dim + 15) / 16;
+  int ks = 0, vs = 0;   // the producer's: tiles of k and v issued
   auto give_up = [&](int info) {
     *abort_flag = 1;
     if (lane == 0) report_error(&g_op_status, KFAC_ERR_TIMEOUT, -1, info);
@@ -822,20 +855,16 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
         tc::tma_load_4d(Qs + c * kChunk, &mp.q, qg_full, 64 * c, q0, h * mp.xq.head, b * mp.xq.batch);
         tc::tma_load_4d(Gs + c * kChunk, &mp.g, qg_full, 64 * c, q0, h * mp.xg.head, b * mp.xg.batch);
       }
-      int j = 0;
-      for (; j < n; ++j) {
+      for (int j = 0; j < n; ++j) {
         const int sk = j % 3, sv = j % 2;
         if (!tc::mbar_wait(&k_empty[sk], ((uint32_t)(j / 3) & 1u) ^ 1u, abort_flag)) break;
         load_chunks<NC>(Ks + sk * C::TILE, &mp.k, &k_full[sk], (first + j) * BT, hk * mp.xk.head, b * mp.xk.batch);
+        ++ks;
         if (!tc::mbar_wait(&v_empty[sv], ((uint32_t)(j / 2) & 1u) ^ 1u, abort_flag)) break;
         load_chunks<NC>(Vs + sv * C::TILE, &mp.v, &v_full[sv], (first + j) * BT, hk * mp.xv.head, b * mp.xv.batch);
+        ++vs;
       }
-      if (j < n) {   // winding down: let the copies in flight land
-        give_up(121);
-        int never = 0;
-        for (int s = 0; s < 3; ++s) tc::mbar_wait(&k_full[s], (uint32_t)(j / 3) & 1u, &never, 1 << 20);
-        for (int s = 0; s < 2; ++s) tc::mbar_wait(&v_full[s], (uint32_t)(j / 2) & 1u, &never, 1 << 20);
-      }
+      if (vs < n) give_up(121);
     }
   } else if (warp == 1) {
     if (n > 0) {  // ------------------------------------------------------- MMA issuer
@@ -993,6 +1022,16 @@ __device__ __forceinline__ void dq_block(const Args& a, const BwdMaps& mp, int t
     }
     tc::tc_fence_before();
   }
+  __syncthreads();
+  if (*abort_flag) {
+    if (threadIdx.x == 0) {
+      land(qg_full, n > 0);
+      land_ring<3>(k_full, ks);
+      land_ring<2>(v_full, vs);
+    }
+    if (warp == 1) end_mmas(ended);
+    __syncthreads();
+  }
 }
 
 // grid: every dK/dV block, then every dQ block: the longer ones start first.
@@ -1033,8 +1072,7 @@ tc_backward_kernel(const __grid_constant__ Args a, const __grid_constant__ BwdMa
   pdl_trigger();
   if (dkv) dkv_block<NC>(a, mp, tile, split, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
   else dq_block<NC>(a, mp, tile, split, pair % a.kv_heads, pair / a.kv_heads, smem, bars, abort_flag, tmem);
-  __syncthreads();
-  if (warp == 1) tc::tmem_dealloc(tmem, 512);
+  if (warp == 1) tc::tmem_dealloc(tmem, 512);   // (both end behind a barrier)
 }
 
 // ------------------------------------------------------------------------ tensor maps

@@ -275,3 +275,45 @@ int main() {
             text = open(os.path.join(csrc, name)).read()
             assert not re.search(r"static\s+const\s+bool\s+\w+\s*=", text), name
             assert text.count("cudaFuncSetAttribute(") == (name == "attn.cuh"), name
+
+
+def test_rings_wait_for_the_last_copy_of_every_slot(tmp_path):
+    """A block that gives up may not end while copies into its shared memory are under way.  Every
+    count of issued tiles and every landed part of them, against a model of the slots' barriers
+    (phase c has begun once c copies have landed; a wait for parity p ends unless phase c with
+    c % 2 == p is the present one): the wait ends exactly when the slot's last copy has landed.  The
+    parity of the tile at which the producer stopped, for every slot, does not do that."""
+    import os
+    import shutil
+    import subprocess
+    import __graft_entry__
+    csrc = os.path.join(__graft_entry__.ROOT, "second_order_optimizer_gb300", "csrc")
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    src = tmp_path / "t.cpp"
+    src.write_text("""
+#include "ring.h"
+int main() {
+  bool other_fails = false;
+  for (int stages = 1; stages <= 4; ++stages)
+    for (int issued = 0; issued <= 40; ++issued) {
+      int all = 0;
+      for (int s = 0; s < stages; ++s) {
+        int uses = 0;
+        for (int i = 0; i < issued; ++i) uses += i % stages == s;
+        if (kfac::ring_uses(issued, s, stages) != uses) return 1;
+        all += uses;
+        for (int landed = uses > 0 ? uses - 1 : 0; landed <= uses && uses > 0; ++landed) {
+          auto ends = [&](unsigned parity) { return (unsigned)(landed & 1) != parity; };
+          if (ends(kfac::ring_last_parity(uses)) != (landed == uses)) return 2;
+          other_fails |= ends((unsigned)(issued / stages) & 1u) != (landed == uses);
+        }
+      }
+      if (all != issued) return 3;
+    }
+  return other_fails ? 0 : 4;
+}
+""")
+    subprocess.run([gxx, "-std=c++17", "-I" + csrc, str(src), "-o", str(tmp_path / "t")], check=True)
+    assert subprocess.run([str(tmp_path / "t")]).returncode == 0
