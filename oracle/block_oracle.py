@@ -133,3 +133,36 @@ def cross_attention_backward(dout, q, k, v, ok, scale=None):
             dk[i, at, n] += scale * ds.T @ qq
             dv[i, at, n] += p.T @ g
     return dq, dk, dv
+
+
+def gradient_norm_bounds(dout, q, k, v, ok, scale=None, from_products=128):
+    """(gradients, bounds): dq, dk, dv in float64, and how far from them in norm the roundings of
+    bf16 may take an implementation that rounds P, dS and the results once each and, for sequences
+    of more than ``from_products`` permitted keys, takes delta from the rounded out.
+
+    u = 2^-8; a rounding is off by at most u and by u / sqrt(3) in the root mean square, so 1.5 u of
+    the gradient's norm holds three of them with room.  A row's delta is off by
+    u / sqrt(3) |dout out|, and with it the row's whole dS by P times that: scale P k in dq, and in dk
+    scale P q, where the rows' errors are independent.  Twice its root mean square is allowed."""
+    b, nq, h, d = q.shape
+    kv = k.shape[2]
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    u = 2.0 ** -8
+    grads = cross_attention_backward(dout, q, k, v, ok, scale)
+    off = [0.0, 0.0]
+    for i in range(b):
+        at = np.nonzero(ok[i])[0]
+        if at.size <= from_products:
+            continue
+        for j in range(h):
+            n = j * kv // h
+            qq, kk, vv, g = (np.asarray(t, np.float64) for t in
+                             (q[i, :, j], k[i, at, n], v[i, at, n], dout[i, :, j]))
+            s = scale * qq @ kk.T
+            p = np.exp(s - s.max(axis=1, keepdims=True))
+            p /= p.sum(axis=1, keepdims=True)
+            e = (u * scale) ** 2 / 3 * ((g * (p @ vv)) ** 2).sum(axis=1)
+            off[0] += (e * ((p @ kk) ** 2).sum(axis=1)).sum()
+            off[1] += (e * (qq ** 2).sum(axis=1) * (p ** 2).sum(axis=1)).sum()
+    off.append(0.0)
+    return grads, [1.5 * u * np.linalg.norm(x) + 2 * math.sqrt(o) for x, o in zip(grads, off)]

@@ -95,6 +95,43 @@ def test_attention_without_permitted_keys_is_zero():
     assert all((t == 0).all() for t in B.cross_attention_backward(q, q, k, v, ok))
 
 
+def _bf16(x):
+    """Rounded to bf16, to nearest even."""
+    i = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    i = (i + 0x7FFF + ((i >> 16) & 1)) & 0xFFFF0000
+    return i.astype(np.uint32).view(np.float32).astype(np.float64)
+
+
+@pytest.mark.parametrize("nq,nk,d", [(20, 3100, 64), (700, 1100, 72), (2500, 40, 128), (300, 129, 80)])
+def test_gradient_norm_bounds_tell_roundings_from_mistakes(nq, nk, d):
+    """Products with P, dS, out and the results rounded to bf16 stay within the bounds; without delta,
+    or without the last tile of keys (dq) or of queries (dk, dv), they do not."""
+    rng = np.random.default_rng(nq)
+    q, g = (_bf16(rng.standard_normal((1, nq, 1, d))) for _ in range(2))
+    k, v = (_bf16(rng.standard_normal((1, nk, 1, d))) for _ in range(2))
+    ref, bound = B.gradient_norm_bounds(g, q, k, v, np.ones((1, nk), bool))
+    out, lse = B.cross_attention(q, k, v, np.ones((1, nk), bool))
+    Q, Kk, V, G, scale = q[0, :, 0], k[0, :, 0], v[0, :, 0], g[0, :, 0], d ** -0.5
+
+    def grads(delta=True, keys=nk, queries=nq):
+        p = np.exp(scale * Q @ Kk.T - lse[0, 0][:, None])
+        dp = G @ V.T
+        o = _bf16(out[0, :, 0])
+        t = (p * dp).sum(axis=1) if nk <= 128 else (G * o).sum(axis=1)
+        ds = _bf16(p * (dp - t[:, None] * delta))
+        return (_bf16(scale * ds[:, :keys] @ Kk[:keys]), _bf16(scale * ds[:queries].T @ Q[:queries]),
+                _bf16(_bf16(p)[:queries].T @ G[:queries]))
+
+    off = lambda got: [np.linalg.norm(x - y.reshape(x.shape)) / b for x, y, b in zip(
+        (r[0, :, 0] for r in ref), got, bound)]
+    assert max(off(grads())) <= 1
+    assert min(off(grads(delta=False))[:2]) > 1
+    if nk > 128:
+        assert off(grads(keys=(nk - 1) // 128 * 128))[0] > 1
+    if nq > 128:
+        assert min(off(grads(queries=(nq - 1) // 128 * 128))[1:]) > 1
+
+
 # ------------------------------------------------------------- refusals (nothing is launched)
 
 @pytest.fixture(scope="module")

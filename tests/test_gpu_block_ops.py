@@ -650,3 +650,19 @@ def test_attention_refuses_a_scale_of_zero():
             call(0.0)
         with pytest.raises(K.KfacError):
             call(-0.25)
+
+
+@pytest.mark.parametrize("keys", ["all", "both"])
+@pytest.mark.parametrize("b,nq,nk,h,kv,d", [
+    (1, 20, 3100, 2, 1, 64), (1, 2500, 40, 2, 1, 128), (2, 700, 1100, 2, 1, 72), (1, 1, 2000, 3, 3, 33),
+    (2, 129, 257, 4, 1, 128), (1, 300, 129, 2, 2, 80), (1, 260, 500, 1, 1, 40), (1, 513, 385, 2, 1, 16),
+    (2, 70, 130, 2, 2, 120), (3, 577, 1531, 4, 1, 64), (1, 900, 1400, 2, 2, 128)])
+def test_attention_gradients_in_norm(keys, b, nq, nk, h, kv, d):
+    """bf16 over several tiles and parts: the gradients as whole arrays, within what the roundings
+    alone explain (a term or a tile that is missing does not fit: see the bounds' own test)."""
+    q, k, v, g, kv_len, mask, ok = _inputs(BF16, b, nq, nk, h, kv, d, keys, seed=37)
+    out, lse = K.cross_attention(q, k, v, kv_len, mask)
+    got = K.cross_attention_backward(g, q, k, v, out, lse, kv_len, mask)
+    ref, bound = B.gradient_norm_bounds(_np(g), _np(q), _np(k), _np(v), ok)
+    for x, y, most in zip(got, ref, bound):
+        assert np.linalg.norm(_np(x) - y) <= most
