@@ -105,7 +105,7 @@ kfac_status token_forward(const Args& a, cudaStream_t st);
 constexpr int kExactKeys = 128;
 kfac_status delta_keys(const Args& a, cudaStream_t st);
 
-// fp32 arithmetic: forward of more than 16 rows, and backward (a.delta already written).
+// fp32 arithmetic: forward and backward (a.delta already written).
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st);
 template <typename T> kfac_status f32_backward(const Args& a, cudaStream_t st);
 // The same for the bf16 tensors that the fp32 kernels take.

@@ -1,5 +1,5 @@
 // Cross attention: argument checks, the choice of kernels, and the kernels beside the
-// products: few query rows that the token kernel cannot take, the joins of parts of the
+// products: the smallest calls that the token kernel cannot take, the joins of parts of the
 // key axis, delta.
 //
 //   S = scale q k^T,  P = softmax over the permitted keys,  out = P v
@@ -24,11 +24,12 @@ namespace kfac {
 namespace attn {
 namespace {
 
-// The forward kernel for few rows that the token kernel cannot take (fp32, or rows that
-// are not whole 16 bytes), on the FMA pipe: a block of 16 x 16 threads owns 16 query rows
-// and streams tiles of 64 keys past them; thread (ty, tx) holds row ty, keys tx + 16 j of
-// a score tile and channels 4 tx + 64 c of the result.  Bound by reading k and v: the key
-// axis is split over as many blocks as fit.
+// The forward kernel for few rows and few keys that the token kernel cannot take (fp32, or
+// rows that are not whole 16 bytes), on the FMA pipe: a block of 16 x 16 threads owns 16
+// query rows and streams tiles of 64 keys past them; thread (ty, tx) holds row ty, keys tx +
+// 16 j of a score tile and channels 4 tx + 64 c of the result.  Bound by the start of a
+// block and its first tile: it has fewer steps before the first product than the kernel on
+// the tensor cores, and fewer FMAs in flight for the rest (see few_rows).
 template <int DP_> struct Few {
   static constexpr int BO = 16, RT = 1, BS = 64, DP = DP_;
   static constexpr int THREADS = BO / RT * 16;
@@ -393,13 +394,25 @@ bool vec_rows(const void* p, const int64_t* s, int rows, int heads, int batch, i
          (rows <= 1 || s[1] % v == 0) && (heads <= 1 || s[2] % v == 0);
 }
 
+// Up to 16 rows against up to kFewKeys keys of all batch entries and key heads: there a call
+// is one wave of blocks of a tile or two.  One row, batch entries x key heads x keys, fp32,
+// us of few_rows_kernel and of f32_forward_kernel:
+//   64 channels   16 x 64: 6.6, 7.9; 16 x 256: 8.7, 10.3; 4 x 1024: 9.5, 10.9; 16 x 333: 9.1,
+//                 10.6; 16 x 512: 11.7, 10.8; 4 x 2048: 12.7, 11.7; 256 x 256: 32, 18
+//   128 channels  16 x 64: 9.1, 11.2; 16 x 256: 14.2, 14.0; 4 x 1024: 14.9, 14.5;
+//                 64 x 128: 15.3, 14.6; 256 x 256: 61, 37; 128 x 8192: 924, 537
+constexpr int64_t kFewKeys = 6144;
+bool few_rows(int64_t rows, int64_t batch, int64_t kv_heads, int64_t len_kv) {
+  return rows <= 16 && batch * kv_heads * len_kv <= kFewKeys;
+}
+
 template <typename T>
 kfac_status plain_forward(Args a, cudaStream_t st) {
   a.vec = vec_rows(a.q, a.qs, a.len_q, a.heads, a.batch, a.dim, 4) &&
           vec_rows(a.k, a.ks, a.len_kv, a.kv_heads, a.batch, a.dim, 4) &&
           vec_rows(a.v, a.vs, a.len_kv, a.kv_heads, a.batch, a.dim, 4);
   kfac_status e;
-  if (a.rows <= 16)
+  if (few_rows(a.rows, a.batch, a.kv_heads, a.len_kv))
     e = a.dim <= 64 ? launch_few_rows<T, Few<64>>(a, st)
                     : launch_few_rows<T, Few<128>>(a, st);
   else
@@ -458,9 +471,10 @@ int pick_splits(int64_t ctas, int per_sm, int len_kv, int tile) {
 
 int plain_splits(const kfac_attention_desc& d) {
   const int rows = d.heads / d.kv_heads * d.len_q;
+  const bool few = few_rows(rows, d.batch, d.kv_heads, d.len_kv);   // (no more tiles than blocks fit)
   // as many blocks as are resident
-  const int per_sm = rows <= 16 ? 3 : d.head_dim <= 64 ? 4 : 2;
-  return pick_splits((int64_t)cdiv(rows, rows <= 16 ? 16 : 64) * d.kv_heads * d.batch, per_sm, d.len_kv, 64);
+  const int per_sm = d.head_dim <= 64 ? 4 : 2;
+  return pick_splits((int64_t)cdiv(rows, few ? 16 : 64) * d.kv_heads * d.batch, per_sm, d.len_kv, 64);
 }
 // Rows (keys, or queries of a group) that one tensor-core accumulator sums.  Its additions
 // round towards zero, about half an ulp each: of a sum of like signs that takes away 4e-5

@@ -1,5 +1,5 @@
 // Cross attention of fp32 inputs (and of bf16 rows that the tensor-memory accelerator
-// cannot address): forward for more than 16 query rows, and the backward pass.
+// cannot address): forward but for the smallest calls, and the backward pass.
 //
 // Products run on the tensor cores with fp32 accuracy.  Each operand v enters as its
 // TF32 rounding h and the remainder r = v - h (exact in fp32); x y = h h' + (h r' + r h'),
