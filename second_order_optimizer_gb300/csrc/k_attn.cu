@@ -492,12 +492,25 @@ int tc_splits(const kfac_attention_desc& d) {
                                tiles == 1 ? 2 : 1, d.len_kv, 512);
   return std::max(fill, (int)cdiv(d.len_kv, kWalkRows));
 }
-// The form of the forward pass for bf16 rows that TMA and 16-byte loads can address.
-// Few rows: the token kernel reads k and v once per 16 rows, while the tensor-core
-// kernel spends two tiles of 128 rows on them.
-constexpr int kTokenRows = 64;
+// The form of the forward pass for bf16 rows that TMA and 16-byte loads can address.  The
+// token kernel passes k and v by once per 16 packed rows of a key head, the tcgen05 kernel once
+// per query head (in tiles of 128 or 256 queries): the first while it has at most 3/4 as many
+// passes, or one.  Batch entries x queries x keys (r: ragged), heads on key heads x channels, us
+// of the token and of the tcgen05 kernel:
+//   1 head per key head  16 x 4 x 1024, 8 x 64: 11.0, 14.5; 8 x 16 x 4096 r, 8 x 128: 25.6, 23.9;
+//                        8 x 8 x 4096, 8 x 128: 40.7, 28.9; 16 x 32 x 1024, 8 x 64: 22.0, 18.3;
+//                        64 x 32 x 512, 8 x 64: 33, 20; 8 x 64 x 4096, 8 x 128: 117, 35
+//   4                    16 x 4 x 4096, 16 x 128: 44, 54; 16 x 8: 47, 54; 16 x 12: 65, 54;
+//                        32 x 12 x 512 r, 16 x 64: 13.4, 15.8; 16 x 16 x 4096: 117, 54
+//   8                    16 x 4 x 4096, 32 x 128: 47, 104; 16 x 12: 118, 104, r 68, 80;
+//                        16 x 16: 171, 104, r 89, 71
+//   16                   16 x 8 x 4096, 16 x 128: 47, 53; 64 x 12 x 1024 r, 16 x 64: 27, 37;
+//                        16 x 16 x 4096: 116, 53
+// (A single query on one head per key head is near even, 0.7 to 1.4 times; it stays with the
+// token kernel, which needs no tensor maps, 1 us of the host's time.)
 bool token_sizes(const kfac_attention_desc& d) {
-  return d.dtype == KFAC_BF16 && d.heads / d.kv_heads * d.len_q <= kTokenRows;
+  const int64_t group = d.heads / d.kv_heads;
+  return d.dtype == KFAC_BF16 && cdiv(group * d.len_q, 16) <= std::max<int64_t>(1, 3 * group / 4);
 }
 // Parts of the key axis for the token kernel: as many blocks as are resident at once, and no
 // more for equal lengths, where a second wave of a few blocks costs as much as a whole one
@@ -552,8 +565,12 @@ size_t part_bytes(const kfac_attention_desc& d, int splits) {
 // Parts of the backward pass's loops.  A dK/dV block owns `own` keys and walks the group's
 // queries in steps (four products each), a dQ block owns as many queries and walks the
 // keys (three).  Where one block's walk is longer than its share of the whole work, it is
-// split, into pieces of at least four steps; the sums then take a launch more.  The
-// tensor-core kernels' accumulators walk no further than kWalkRows.
+// split, into at most 32 pieces of at least four steps; the sums then take a launch more.  us with
+// pieces of 2, 4 and 8 steps at least, queries x keys (channels): bf16 2500 x 40 (128): 30, 26, 25;
+// 20 x 3100 (64): 13.0, 12.0, 14.7; 64 x 8192 (128): 35, 25, 23; fp32 20 x 3100 (64): 33, 36, 44;
+// 2500 x 40 (128): 101, 101, 135.  With 16, 32 and 64 pieces at most: bf16 128 x 32768 (64): 32, 32,
+// 44; 65536 x 64 (64): 56, 49, 60; fp32 8192 x 64 (128): 241, 153, 124; 128 x 32768 (64): 282, 184, 165.
+// The tensor-core kernels' accumulators walk no further than kWalkRows.
 // tc: of the tensor-core kernels (bf16), else of the fp32 ones.
 void backward_splits(const kfac_attention_desc& d, Args& a, bool tc) {
   const int own = tc ? 128 : 64, step = tc ? 128 : 32, per_sm = tc ? 1 : 2;

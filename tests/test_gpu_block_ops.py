@@ -666,3 +666,13 @@ def test_attention_gradients_in_norm(keys, b, nq, nk, h, kv, d):
     ref, bound = B.gradient_norm_bounds(_np(g), _np(q), _np(k), _np(v), ok)
     for x, y, most in zip(got, ref, bound):
         assert np.linalg.norm(_np(x) - y) <= most
+
+
+# the last sizes that the token kernel takes and the first that it does not, by heads per key head
+@pytest.mark.parametrize("keys", ["all", "both"])
+@pytest.mark.parametrize("b,nq,nk,h,kv,d", [
+    (2, 16, 300, 2, 2, 64), (2, 17, 300, 2, 2, 64), (2, 8, 300, 4, 2, 96), (2, 9, 300, 4, 2, 96),
+    (2, 12, 1030, 4, 1, 128), (2, 13, 1030, 4, 1, 128), (1, 12, 513, 16, 2, 32), (1, 13, 513, 16, 2, 32),
+    (3, 12, 129, 16, 1, 128), (3, 13, 129, 16, 1, 128), (1, 12, 700, 32, 1, 64), (1, 13, 700, 32, 1, 64)])
+def test_attention_few_queries_of_shared_key_heads(keys, b, nq, nk, h, kv, d):
+    _check_attention(*_inputs(BF16, b, nq, nk, h, kv, d, keys, seed=41))
