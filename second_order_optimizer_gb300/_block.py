@@ -5,6 +5,8 @@ Argument marshalling only, as in the rest of the package: outputs and workspace 
 (a training loop keeps them) or are allocated with torch.  Activations are
 [batch, length, heads, head_dim] tensors with contiguous channels and any other strides.  A
 wrong shape, type or device raises ValueError; what the library itself refuses raises KfacError.
+The calls are outside torch's autograd, like the rest of the package: a result has no graph,
+whatever its inputs require, and the backward passes here are called by hand.
 Definitions: include/kfac.h.
 
 ``stream``: a torch stream or a raw handle; torch's current stream of the tensors' device

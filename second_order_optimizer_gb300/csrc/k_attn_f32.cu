@@ -8,7 +8,7 @@
 // tile: the tensor cores' additions round towards zero, and what is summed over tiles is
 // summed in fp32 registers.  (On the FMA pipe the same tiles were bound by shared-memory
 // reads, 8 16-byte loads per 64 FMAs: 25 TFLOP/s.)  4 x 1024 queries and keys, 8 heads on 4 x
-// 128: forward 400 us, 43 TFLOP/s; backward 1650 us; on 8 x 64: 216 and 732 us.  Bound by issue at
+// 128: forward 406 us, 42 TFLOP/s; backward 1660 us; on 8 x 64: 218 and 741 us.  Bound by issue at
 // 8 to 16 warps per SM: the three products alone could run at 98 TFLOP/s.
 //
 // bf16 values are TF32 values: their scores take one product, and P or dS with one of them
@@ -665,6 +665,9 @@ kfac_status launch_delta(const Args& a, cudaStream_t st) {
 
 // Tiles as long as the registers of 4 (128 channels: 2) and 3 (2) blocks per SM allow;
 // backward with 32 channels: 430 us in tiles of 16 and 440 in tiles of 32; with 64, 777 and 735.
+// The blocks per SM are worth their spills (up to 76 bytes a thread forward, 88 backward; bf16
+// rows 100 and 280).  4 x 1024 x 1024, 8 heads, us with 4 and 3 blocks forward: 64 channels 218,
+// 232; 32: 132, 153; 36 in bf16: 203, 355; with 3 and 2 backward: 742, 769; 439, 489; 576, 687.
 template <typename T> kfac_status f32_forward(const Args& a, cudaStream_t st) {
   if (a.dim <= 32) return launch_forward<T, Cfg<64, 32>>(a, st);
   return a.dim <= 64 ? launch_forward<T, Cfg<32, 64>>(a, st) : launch_forward<T, Cfg<32, 128>>(a, st);

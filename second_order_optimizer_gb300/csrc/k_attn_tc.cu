@@ -200,9 +200,10 @@ constexpr int kHalf = 64 * 128;   // bytes from a tile's row 0 to its row 64
 // power of two at most: P <= 2^8, and O overflows only where 2^8 len_kv |v| does.  (The second
 // half may not wait longer for it: at 2^90 a row that grows by 60 within a tile took |v| past
 // 2.7e11 to infinity.)
-// Measured on 8 x 2048 queries, 4096 keys (half of them permitted), 16 heads x 128: 208 us,
-// 1480 TFLOP/s.  What was tried and cost more: S in two buffers of 64 keys (272 us: twice the
-// hand-overs), two groups of warps per tile (232 us).
+// Measured on 8 x 2048 queries, 4096 keys (ragged: 56 % of them permitted), 16 heads x 128:
+// 222 us, 1390 TFLOP/s, the tensor pipe active in 66 % of the cycles.  What was tried and cost
+// more: S in two buffers of 64 keys (a quarter more: twice the hand-overs), two groups of warps
+// per tile (a twentieth).
 template <int NC, int NT> struct FwdCfg {
   static constexpr int TILE = NC * kChunk;
   static constexpr int THREADS = 128 + 128 * NT;
@@ -538,8 +539,9 @@ tc_forward_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtens
 // waited for dQ(j): 2870 cycles a step; three products of 128 x 128 x 128 take 1536.)
 //
 // Two groups of four warps share a tile's columns, 64 each.
-// Measured: 8 x 2048 queries, 4096 keys (half of them permitted), 16 heads x 128: 750 us, the
-// tensor pipe active 74 % of the cycles (1430 TFLOP/s of the seven products).
+// Measured: 8 x 2048 queries, 4096 keys (56 % of them permitted), 16 heads x 128: 770 us, 1400
+// TFLOP/s of the seven products, the tensor pipe active in 64 % of the cycles; 5 x 577, 1531, 16
+// heads on 4 x 64: 69 us, 35 % (a block's set-up, chain and end are not hidden).
 constexpr int kBwdBars = 26;   // then the TMEM slot and abort flag, then the mask words
 template <int NC> struct BwdCfg {
   static constexpr int TILE = NC * kChunk;
@@ -1155,10 +1157,11 @@ bool tc_forward_ok(const Args& a) {
 
 // Query tiles per block.  One (two blocks per SM) up to 64 channels, where the
 // exponentials bound the kernel and two independent blocks hide each other's chains (2 x
-// 2432 queries, 4096 keys, 16 heads x 64: 88 us, with two tiles 121 us), and where a block's
-// walk is short and its set-up and end weigh (14 x 316 queries, 35 keys, 32 heads x 128: 35 us
-// against 42 us).  Two where the products bound it and share each tile of keys (8 x 2048
-// queries, 4096 keys, 16 heads x 128: 220 us against 241 us).
+// 2432 queries, 4096 ragged keys, 16 heads x 64: 73 us, with two tiles 105 us), and where a
+// block's walk is short and its set-up and end weigh (14 x 316 queries, 35 keys, 32 heads x 128:
+// 42 us against 50 us).  Two where the products bound it and share each tile of keys (8 x 2048
+// queries, 4096 ragged keys, 16 heads x 128: 222 us against 242 us; 4 x 1000 queries, 8192 keys:
+// 141 us against 156 us).  (Times with a flushed L2.)
 int tc_forward_tiles(int dim, int len_q, int len_kv) {
   return dim <= 64 || len_q <= BT || len_kv <= 2 * BT ? 1 : 2;
 }

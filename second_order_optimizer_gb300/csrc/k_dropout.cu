@@ -103,7 +103,8 @@ __global__ void __launch_bounds__(kDropThreads) dropout_flat_kernel(const __grid
 }
 
 // Any leading dimensions and alignment: one generator block (four elements of the
-// row-major index) per thread, element by element.
+// row-major index) per thread, element by element.  Bound by its loads and stores of single
+// elements (16384 x 2047 with residual, bf16 85 us, fp32 91 us; without 73 and 78 us).
 template <typename T, bool kRes>
 __global__ void __launch_bounds__(kDropThreads) dropout_strided_kernel(const __grid_constant__ DropArgs a) {
   pdl_wait();

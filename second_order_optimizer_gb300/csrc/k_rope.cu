@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-// Angles in 64 bits: at position 10^6 an fp32 angle is off by 0.03 rad.
+// Angles in 64 bits: at position 10^6 an fp32 angle is off by 0.03 rad.  Bound by the 64-bit
+// sines, cosines and powers (131072 rows x 128: 1.1 ms, YARN 1.4 ms; a table is made once).
 struct RopeTableArgs {
   float* table;
   int64_t rows;
@@ -310,6 +311,8 @@ kfac_status kfac_rope_table(float* table, int64_t rows, int rotary_dim, double b
   if (scaling == KFAC_ROPE_NTK)
     a.log2_base += std::log2(factor) * rotary_dim / (rotary_dim - 2.0);
   if (scaling == KFAC_ROPE_YARN) {
+    // (Peng, Quesnelle, Fan, Shippole, "YaRN: efficient context window extension of large
+    // language models", 2023.)
     // pair i turns original_length f_i / 2 pi times within the original length; pairs
     // with 32 turns or more keep their frequency, those with one or less are
     // interpolated, a linear blend over the index between
