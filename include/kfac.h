@@ -557,6 +557,99 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* desc,
                                           void* workspace, size_t workspace_bytes,
                                           cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Parameters without Kronecker factors: the norms' gains and the token embedding
+ * (forward and backward, with the diagonal factors that kfac_diag_step takes), and
+ * weight matrices stepped along their orthogonalised momentum instead of a
+ * preconditioned gradient.  Conventions as for the block operators above: no handle,
+ * caller-owned device pointers, no device allocation, work enqueued on the given
+ * stream of the current device, argument errors returned before any launch, device
+ * errors reported by kfac_operator_status. */
+
+typedef struct {
+  int dtype;            /* kfac_dtype of x, residual, h, y and their gradients            */
+  int64_t rows, cols;   /* cols <= 2^20                                                   */
+  double eps;           /* >= 0                                                           */
+  int64_t ldx, ldr;     /* rows of x and of residual                                      */
+  int64_t ldh, ldy;     /* of h and of y                                                  */
+  int64_t ldq;          /* of q (bytes)                                                   */
+  int group;            /* q: channels per scale, 32, 64 or 128; 0: one scale per row     */
+} kfac_norm_desc;
+
+/* Root-mean-square norm of x + residual:
+ *   s = x + residual (residual NULL: x),  r = (mean_j s_j^2 + eps)^(-1/2),
+ *   h = s,  y = s r gain  (gain: fp32 [cols]; NULL: ones).
+ * s and the statistics are fp32 (y is taken from s before h is rounded).  h (the
+ * residual stream, which the backward pass reads), y and rstd (r: fp32 [rows]) may be
+ * NULL, not y and q both.  q: y in 8 bits (e4m3: 3 mantissa bits, largest value 448)
+ * with fp32 scales [rows x ceil(cols / group)] contiguous: over each group of
+ * channels scale = max |y| / 448 and q = e4m3(y / scale), nearest even (a group of
+ * zeros: scale 0, q 0); at most 8192 groups.  Inf or NaN in a row makes that row's results NaN or, where
+ * exact arithmetic gives it, zero or Inf.  Outputs may not overlap inputs, except that
+ * h may be x or residual with the same leading dimension. */
+kfac_status kfac_rms_norm(const kfac_norm_desc* desc, const void* x, const void* residual,
+                          const float* gain, void* h, void* y, float* rstd, void* q,
+                          float* scales, cudaStream_t stream);
+
+typedef struct {
+  int dtype;                    /* kfac_dtype of dy, h, dh and dx                  */
+  int64_t rows, cols;           /* cols <= 2^20                                    */
+  int64_t lddy, ldh, lddh, lddx;
+} kfac_norm_grad_desc;
+
+/* Bytes of workspace that kfac_rms_norm_backward needs on the current device (a
+ * 256-byte multiple).  It holds nothing between calls; calls that share one must be
+ * ordered. */
+kfac_status kfac_rms_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Its gradients, from the forward call's h (x where it had no residual) and rstd:
+ *   n_j = h_j r,  w = dy gain,  dx = r (w - n mean_j(w_j n_j)) + dh,
+ *   dgain_j = sum_rows dy_j n_j,  dgain_square_j = mean_rows (dy_j n_j)^2.
+ * dx is the gradient of x and of residual alike; dh: the gradient of the stream h from
+ * its other readers (NULL: none).  dgain and dgain_square: fp32 [cols], each may be
+ * NULL, as may dx; written, not accumulated.  dgain_square is the gain's diagonal
+ * Fisher factor: a KFAC_DIAG layer of d_out = cols, d_in = 1 takes it as g_new with
+ * a_new = 1.  dx may be dy or dh with the same leading dimension.  Sums are fp32 in a
+ * fixed order: the same inputs give the same bits. */
+kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* desc, const void* dy, const void* h,
+                                   const float* gain, const float* rstd, const void* dh, void* dx,
+                                   float* dgain, float* dgain_square, void* workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+typedef struct {
+  int dtype;             /* kfac_dtype of table and out, or of dout                 */
+  int id_bits;           /* 32 or 64: signed ids                                    */
+  int64_t tokens, rows;  /* ids, rows of the table (< 2^31 - 1 each)                */
+  int64_t width;         /* channels of a row                                       */
+  double scale;          /* finite                                                  */
+  int64_t ldt;           /* rows of table (forward) or of dtable (backward)         */
+  int64_t ldo;           /* rows of out (forward) or of dout (backward)             */
+} kfac_embedding_desc;
+
+/* out[t] = scale table[ids[t]]; ids contiguous.  The row of an id outside [0, rows)
+ * is NaN. */
+kfac_status kfac_embedding(const kfac_embedding_desc* desc, const void* ids, const void* table,
+                           void* out, cudaStream_t stream);
+
+/* Bytes of workspace that kfac_embedding_backward needs (a 256-byte multiple).  It holds
+ * nothing between calls; calls that share one must be ordered. */
+kfac_status kfac_embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width,
+                                          size_t* bytes);
+
+/* Its gradient, by tokens sorted by id: dtable[v] = scale sum_{t: ids[t] = v} dout[t]
+ * (fp32 [rows x width]), over the tokens whose id is not padding_id (-1: none is
+ * padding); ids outside [0, rows) are left out.  accumulate = 0: every row is written,
+ * zeros where no token is; 1: added to dtable, whose other rows are not touched.
+ * frequency (fp32 [rows], NULL: not wanted, always written whole): the share of the
+ * tokens that dtable[v] sums, count / tokens.  It is the diagonal of the A factor of the
+ * one-hot inputs: a KFAC_DIAG layer of d_out = rows, d_in = width takes it as g_new, with
+ * the mean squares of dout as a_new.  Sums are fp32 in a fixed order, no atomics: the
+ * same inputs give the same bits. */
+kfac_status kfac_embedding_backward(const kfac_embedding_desc* desc, const void* ids,
+                                    const void* dout, float* dtable, int64_t padding_id,
+                                    int accumulate, float* frequency, void* workspace,
+                                    size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronise the current device and report the first device-side error of the
  * block operators on it since the last call (then clear it): a pipeline
  * wait of the tensor-core attention that gave up (KFAC_ERR_TIMEOUT; info: which

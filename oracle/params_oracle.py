@@ -1,0 +1,64 @@
+"""Float64 reference of the operators of the parameters without Kronecker factors: root-mean-square
+norms, the token embedding, orthogonalised updates.  NumPy, plain and slow; shares no code with the
+GPU path."""
+from __future__ import annotations
+
+import numpy as np
+
+
+def rms_norm(x, gain=None, residual=None, eps=1e-6):
+    """(y, s, r): s = x + residual, r = (mean s^2 + eps)^(-1/2) per row, y = s r gain."""
+    s = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
+    r = 1.0 / np.sqrt((s * s).mean(axis=-1) + eps)
+    y = s * r[..., None] * (1.0 if gain is None else np.asarray(gain, np.float64))
+    return y, s, r
+
+
+def rms_norm_backward(dy, h, gain, r, dh=None):
+    """(dx, dgain, dgain_square) from the forward pass's h and r."""
+    h, dy = np.asarray(h, np.float64), np.asarray(dy, np.float64)
+    n = h * r[..., None]
+    w = dy * (1.0 if gain is None else np.asarray(gain, np.float64))
+    dx = r[..., None] * (w - n * (w * n).mean(axis=-1, keepdims=True))
+    each = (dy * n).reshape(-1, h.shape[-1])
+    return (dx if dh is None else dx + dh), each.sum(axis=0), (each * each).mean(axis=0)
+
+
+def e4m3(v):
+    """v rounded to 8 bits: three mantissa bits (ties to even), least exponent -6, largest value 448."""
+    v = np.asarray(v, np.float64)
+    e = np.floor(np.log2(np.maximum(np.abs(v), 2.0 ** -40)))
+    step = 2.0 ** (np.maximum(e, -6.0) - 3.0)
+    return np.clip(np.rint(v / step) * step, -448.0, 448.0)
+
+
+def quantize(y, group=0):
+    """(q, scales): the largest magnitude of each group of channels (0: of the row) becomes 448."""
+    cols = y.shape[-1]
+    group = group or cols
+    q, scales = np.zeros_like(y), []
+    for c in range(0, cols, group):
+        top = np.abs(y[..., c:c + group]).max(axis=-1) / 448.0
+        scales.append(top)
+        q[..., c:c + group] = e4m3(y[..., c:c + group] / np.where(top > 0, top, 1.0)[..., None])
+    return q, np.stack(scales, axis=-1)
+
+
+def embedding(ids, table, scale=1.0):
+    ids, table = np.asarray(ids), np.asarray(table, np.float64)
+    out = np.full((*ids.shape, table.shape[1]), np.nan)
+    ok = (ids >= 0) & (ids < table.shape[0])
+    out[ok] = scale * table[ids[ok]]
+    return out
+
+
+def embedding_backward(ids, dout, rows, scale=1.0, padding_id=-1):
+    """(dtable, frequency): a sum over the tokens of each row, one token at a time."""
+    ids = np.asarray(ids).reshape(-1)
+    dout = np.asarray(dout, np.float64).reshape(ids.size, -1)
+    dtable, count = np.zeros((rows, dout.shape[1])), np.zeros(rows)
+    for t, v in enumerate(ids):
+        if 0 <= v < rows and v != padding_id:
+            dtable[v] += scale * dout[t]
+            count[v] += 1
+    return dtable, count / max(1, ids.size)

@@ -26,6 +26,9 @@ from ._lib import (LIB, KFAC_KRON, KFAC_DIAG, KFAC_F32, KFAC_BF16, KFAC_MATH_3XT
 # imports without torch
 _BLOCK = ("rope", "rope_table", "dropout", "dropout_backward", "cross_attention",
           "cross_attention_backward", "cross_attention_workspace", "operator_status")
+# those of _params.py likewise
+_PARAMS = ("rms_norm", "rms_norm_e4m3", "rms_norm_backward", "rms_norm_workspace", "embedding",
+           "embedding_backward", "embedding_workspace")
 
 
 def __getattr__(name):
@@ -33,6 +36,11 @@ def __getattr__(name):
         from . import _block
         for n in _BLOCK:
             globals()[n] = getattr(_block, n)
+        return globals()[name]
+    if name in _PARAMS:
+        from . import _params
+        for n in _PARAMS:
+            globals()[n] = getattr(_params, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
@@ -43,7 +51,7 @@ __all__ = ["Kfac", "diag_factors_static", "conv2d_geom", "LayerDesc", "HParams",
            "KFAC_MATH_BF16", "KFAC_EMA_INIT_ZERO", "KFAC_EMA_INIT_FIRST", "KFAC_FACTOR_A",
            "KFAC_IKFAC_OFF", "KFAC_IKFAC_TF32", "KFAC_IKFAC_BF16",
            "KFAC_FACTOR_G", "LIB",
-           *_BLOCK,
+           *_BLOCK, *_PARAMS,
            "KFAC_ROPE_PLAIN", "KFAC_ROPE_LINEAR", "KFAC_ROPE_NTK", "KFAC_ROPE_YARN"]
 
 

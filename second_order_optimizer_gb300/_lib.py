@@ -67,6 +67,10 @@ _u64 = ctypes.c_uint64
 ROPE_DESC = struct.Struct("@9i15q")
 ATTENTION_DESC = struct.Struct("@7if12q")
 ATTENTION_GRAD_DESC = struct.Struct("@12q")
+# kfac_norm_desc, kfac_norm_grad_desc and kfac_embedding_desc likewise
+NORM_DESC = struct.Struct("@iqqd5qi")
+NORM_GRAD_DESC = struct.Struct("@i6q")
+EMBEDDING_DESC = struct.Struct("@iiqqqdqq")
 
 # (name, restype, argtypes): one line per entry point of include/kfac.h
 SIGNATURES = [
@@ -106,6 +110,12 @@ SIGNATURES = [
     ("kfac_cross_attention", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     ("kfac_cross_attention_backward", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_rms_norm", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    ("kfac_rms_norm_workspace_size", _i, [_i64, _i64, ctypes.POINTER(_sz)]),
+    ("kfac_rms_norm_backward", _i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_embedding", _i, [_vp, _vp, _vp, _vp, _vp]),
+    ("kfac_embedding_workspace_size", _i, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
+    ("kfac_embedding_backward", _i, [_vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _sz, _vp]),
     ("kfac_operator_status", _i, [ctypes.POINTER(_i)]),
 ]
 

@@ -1,0 +1,263 @@
+"""Operators of the parameters without Kronecker factors: root-mean-square norms and the token
+embedding, forward and backward, with the diagonal factors that Kfac.diag_step takes.
+
+Argument marshalling only, in the manner of _block.py: outputs and workspaces may be given or are
+allocated with torch; ValueError for a wrong shape, type or device, KfacError for what the library
+refuses; ``stream`` as there; outside torch's autograd.  Definitions: include/kfac.h.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._block import _call, _check, _device, _dtype, _elsewhere, _empty
+from ._lib import LIB, NORM_DESC, NORM_GRAD_DESC, EMBEDDING_DESC
+
+
+def _new(shape, dtype, dev, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    return _empty(shape, dtype, dev, stream)
+
+
+def _sized(f, what, dev, *args):
+    """The bytes that f(*args, &bytes) gives on the tensors' device."""
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(dev):   # the plan may depend on the device's SM count
+        _check(f(*args, ctypes.byref(n)), what)
+    return n.value
+
+
+def _kept(nbytes, dev):
+    """A workspace tensor to be kept by the caller."""
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=torch.device("cuda", dev))
+
+
+def _workspace(what, workspace, nbytes, dev, stream):
+    """A call's workspace: the caller's, or its own."""
+    if workspace is None:
+        return _new((max(nbytes, 256),), torch.uint8, dev, stream)
+    if workspace.get_device() != dev:
+        _elsewhere(what, "workspace", workspace, dev)
+    if not workspace.is_contiguous():
+        raise ValueError(f"{what}: workspace is contiguous")
+    return workspace
+
+
+# ------------------------------------------------------------------------------------- norms
+
+def _rows(what, name, t, shape, dtype, dev):
+    """(rows, cols, leading dimension) of t [..., cols]: contiguous, or 2-D with contiguous rows."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{what}: {name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
+    if t.get_device() != dev:
+        _elsewhere(what, name, t, dev)
+    cols = shape[-1]
+    if t.is_contiguous():
+        return cols
+    if t.dim() != 2 or (t.stride(1) != 1 and cols > 1):
+        raise ValueError(f"{what}: {name} is contiguous, or 2-D with contiguous rows")
+    return t.stride(0)
+
+
+def _vector(what, name, t, n, dev):
+    """Address of a contiguous float32 [n] tensor (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} is float32 [{n}], contiguous")
+    if t.get_device() != dev:
+        _elsewhere(what, name, t, dev)
+    return t.data_ptr()
+
+
+def _norm(what, x, gain, residual, eps, out, residual_out, rstd, q, scales, group, stream):
+    dt, dev = _dtype(x, what), _device(x, what)
+    if x.dim() < 1:
+        raise ValueError(f"{what}: x is [..., channels]")
+    shape, dtype = x.shape, x.dtype
+    cols = shape[-1]
+    rows = x.numel() // cols if cols else 0
+    ldx = _rows(what, "x", x, shape, dtype, dev)
+    ldr = ldh = ldy = ldq = 0
+    if residual is not None:
+        ldr = _rows(what, "residual", residual, shape, dtype, dev)
+        if residual_out is None:
+            residual_out = _new(shape, dtype, dev, stream)
+    if residual_out is not None:
+        ldh = _rows(what, "residual_out", residual_out, shape, dtype, dev)
+    if out is not None:
+        ldy = _rows(what, "out", out, shape, dtype, dev)
+    if q is not None:
+        ldq = _rows(what, "out", q, shape, torch.float8_e4m3fn, dev)
+    if rstd is None:
+        rstd = _new(shape[:-1], torch.float32, dev, stream)
+    elif rstd.dtype is not torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
+        raise ValueError(f"{what}: rstd is float32 {tuple(shape[:-1])}, contiguous")
+    elif rstd.get_device() != dev:
+        _elsewhere(what, "rstd", rstd, dev)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    _call(LIB.kfac_rms_norm, "kfac_rms_norm", dev, stream,
+          NORM_DESC.pack(dt, rows, cols, float(eps), ldx, ldr, ldh, ldy, ldq, group), x.data_ptr(),
+          ptr(residual), _vector(what, "gain", gain, cols, dev), ptr(residual_out), ptr(out),
+          rstd.data_ptr(), ptr(q), ptr(scales))
+    return residual_out, rstd
+
+
+def rms_norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, residual_out=None,
+             rstd=None, stream=None):
+    """kfac_rms_norm: the root-mean-square norm of x + residual, times gain (float32 [channels]);
+    returns (out, residual_out, rstd).  x: [..., channels], contiguous, or 2-D with contiguous
+    rows.  residual_out = x + residual (None without a residual); it may be x or residual.  The
+    backward pass takes it (x without a residual) and rstd, float32 [...]."""
+    _dtype(x, "rms_norm")
+    if out is None:
+        out = _new(x.shape, x.dtype, _device(x, "rms_norm"), stream)
+    residual_out, rstd = _norm("rms_norm", x, gain, residual, eps, out, residual_out, rstd, None,
+                               None, 0, stream)
+    return out, residual_out, rstd
+
+
+def rms_norm_e4m3(x, gain=None, residual=None, eps: float = 1e-6, group: int = 0, out=None,
+                  scales=None, residual_out=None, stream=None):
+    """kfac_rms_norm with its result in 8 bits: (out float8_e4m3fn, scales float32 [..., groups],
+    residual_out); out * scale of its group is the norm.  group: 32, 64 or 128 channels per scale, or
+    0 for one per row."""
+    what = "rms_norm_e4m3"
+    dev = _device(x, what)
+    if x.dim() < 1:
+        raise ValueError(f"{what}: x is [..., channels]")
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"{what}: group is 32, 64 or 128 channels, or 0 for the whole row")
+    if out is None:
+        out = _new(x.shape, torch.float8_e4m3fn, dev, stream)
+    groups = -(-x.shape[-1] // group) if group else 1
+    if scales is None:
+        scales = _new((*x.shape[:-1], groups), torch.float32, dev, stream)
+    elif scales.dtype is not torch.float32 or scales.shape != (*x.shape[:-1], groups) or (
+            not scales.is_contiguous()):
+        raise ValueError(f"{what}: scales is float32 {(*x.shape[:-1], groups)}, contiguous")
+    elif scales.get_device() != dev:
+        _elsewhere(what, "scales", scales, dev)
+    residual_out, _ = _norm(what, x, gain, residual, eps, None, residual_out, None, out, scales,
+                            group, stream)
+    return out, scales, residual_out
+
+
+def rms_norm_workspace(x):
+    """A workspace tensor for rms_norm_backward of tensors like x, to be kept and passed to it."""
+    dev = _device(x, "rms_norm_workspace")
+    cols = x.shape[-1]
+    return _kept(_sized(LIB.kfac_rms_norm_workspace_size, "kfac_rms_norm_workspace_size", dev,
+                        x.numel() // cols if cols else 0, cols), dev)
+
+
+def rms_norm_backward(dout, x, gain, rstd, dresidual=None, dx=None, dgain=None, dgain_square=None,
+                      square: bool = False, workspace=None, stream=None):
+    """kfac_rms_norm_backward: (dx, dgain, dgain_square) for the gradient dout of rms_norm's out.
+    x: its residual_out (its x without a residual); dresidual: the gradient of residual_out from
+    its other readers, added to dx, which is the gradient of x and of residual.  dgain_square
+    (square=True, or a tensor given): the mean over the rows of the gain's squared gradient, which
+    Kfac.diag_step takes as g_new; otherwise None."""
+    what = "rms_norm_backward"
+    dt, dev = _dtype(dout, what), _device(dout, what)
+    if dout.dim() < 1:
+        raise ValueError(f"{what}: dout is [..., channels]")
+    shape, dtype = dout.shape, dout.dtype
+    cols = shape[-1]
+    rows = dout.numel() // cols if cols else 0
+    lddy = _rows(what, "dout", dout, shape, dtype, dev)
+    ldh = _rows(what, "x", x, shape, dtype, dev)
+    lddh = _rows(what, "dresidual", dresidual, shape, dtype, dev) if dresidual is not None else 0
+    if rstd.dtype is not torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
+        raise ValueError(f"{what}: rstd is float32 {tuple(shape[:-1])}, contiguous")
+    if rstd.get_device() != dev:
+        _elsewhere(what, "rstd", rstd, dev)
+    if dx is None:
+        dx = _new(shape, dtype, dev, stream)
+    lddx = _rows(what, "dx", dx, shape, dtype, dev)
+    if dgain is None:
+        dgain = _new((cols,), torch.float32, dev, stream)
+    if dgain_square is None and square:
+        dgain_square = _new((cols,), torch.float32, dev, stream)
+    workspace = _workspace(what, workspace, 0 if workspace is not None else _sized(
+        LIB.kfac_rms_norm_workspace_size, "kfac_rms_norm_workspace_size", dev, rows, cols), dev, stream)
+    _call(LIB.kfac_rms_norm_backward, "kfac_rms_norm_backward", dev, stream,
+          NORM_GRAD_DESC.pack(dt, rows, cols, lddy, ldh, lddh, lddx), dout.data_ptr(), x.data_ptr(),
+          _vector(what, "gain", gain, cols, dev), rstd.data_ptr(),
+          None if dresidual is None else dresidual.data_ptr(), dx.data_ptr(),
+          _vector(what, "dgain", dgain, cols, dev),
+          _vector(what, "dgain_square", dgain_square, cols, dev), workspace.data_ptr(),
+          workspace.nbytes)
+    return dx, dgain, dgain_square
+
+
+# --------------------------------------------------------------------------------- embedding
+
+_ID_BITS = {torch.int32: 32, torch.int64: 64}
+
+
+def _ids(what, ids, dev):
+    bits = _ID_BITS.get(ids.dtype)
+    if bits is None or not ids.is_contiguous():
+        raise ValueError(f"{what}: ids are int32 or int64, contiguous, not {ids.dtype}")
+    if ids.get_device() != dev:
+        _elsewhere(what, "ids", ids, dev)
+    return bits
+
+
+def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
+    """kfac_embedding: out [..., width] = scale * table[ids] for ids int32 or int64 [...]; the row of
+    an id outside the table is NaN.  table: [rows, width], rows contiguous."""
+    what = "embedding"
+    dt, dev = _dtype(table, what), _device(table, what)
+    bits = _ids(what, ids, dev)
+    if table.dim() != 2:
+        raise ValueError(f"{what}: table is [rows, width]")
+    rows, width = table.shape
+    ldt = _rows(what, "table", table, table.shape, table.dtype, dev)
+    shape = (*ids.shape, width)
+    if out is None:
+        out = _new(shape, table.dtype, dev, stream)
+    ldo = _rows(what, "out", out, shape, table.dtype, dev)
+    _call(LIB.kfac_embedding, "kfac_embedding", dev, stream,
+          EMBEDDING_DESC.pack(dt, bits, ids.numel(), rows, width, float(scale), ldt, ldo),
+          ids.data_ptr(), table.data_ptr(), out.data_ptr())
+    return out
+
+
+def embedding_workspace(ids, rows: int, width: int):
+    """A workspace tensor for embedding_backward of as many ids, to be kept and passed to it."""
+    dev = _device(ids, "embedding_workspace")
+    return _kept(_sized(LIB.kfac_embedding_workspace_size, "kfac_embedding_workspace_size", dev,
+                        ids.numel(), rows, width), dev)
+
+
+def embedding_backward(ids, dout, rows: int, scale: float = 1.0, padding_id: int = -1, out=None,
+                       accumulate: bool = False, frequency=None, workspace=None, stream=None):
+    """kfac_embedding_backward: the gradient (float32 [rows, width]) of embedding's table for the
+    gradient dout [..., width] of its out; returns out.  Tokens of padding_id (-1: none) and ids
+    outside the table are left out.  accumulate=True adds to the given out, whose rows without
+    tokens are not touched.  frequency (float32 [rows], given): each row's share of the tokens, which
+    Kfac.diag_step takes as g_new of a layer of d_out = rows."""
+    what = "embedding_backward"
+    dt, dev = _dtype(dout, what), _device(dout, what)
+    bits = _ids(what, ids, dev)
+    if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
+        raise ValueError(f"{what}: dout is [..., width] for ids [...], not {tuple(dout.shape)}")
+    width, tokens = dout.shape[-1], ids.numel()
+    ldo = _rows(what, "dout", dout, dout.shape, dout.dtype, dev)
+    if out is None:
+        if accumulate:
+            raise ValueError(f"{what}: accumulate adds to a given out")
+        out = _new((rows, width), torch.float32, dev, stream)
+    ldt = _rows(what, "out", out, (rows, width), torch.float32, dev)
+    workspace = _workspace(what, workspace, 0 if workspace is not None else _sized(
+        LIB.kfac_embedding_workspace_size, "kfac_embedding_workspace_size", dev, tokens, rows, width),
+        dev, stream)
+    _call(LIB.kfac_embedding_backward, "kfac_embedding_backward", dev, stream,
+          EMBEDDING_DESC.pack(dt, bits, tokens, rows, width, float(scale), ldt, ldo),
+          ids.data_ptr(), dout.data_ptr(), out.data_ptr(), padding_id, int(accumulate),
+          _vector(what, "frequency", frequency, rows, dev), workspace.data_ptr(), workspace.nbytes)
+    return out

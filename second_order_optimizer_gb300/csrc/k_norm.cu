@@ -1,0 +1,655 @@
+// Root-mean-square norm with the residual's addition, an 8-bit output, and the gradients:
+//   s = x + residual,  r = (mean_j s_j^2 + eps)^(-1/2),  h = s,  y = s r gain,
+//   q = e4m3(y / scale), scale = max |y| / 448 over a group of channels;
+//   n = h r,  w = dy gain,  dx = r (w - n mean_j(w_j n_j)) + dh,
+//   dgain_j = sum_rows dy_j n_j,  dgain_square_j = mean_rows (dy_j n_j)^2.
+//
+// Bound by memory: each tensor crosses it once.  A row stays in the registers of the threads
+// that share it (a warp, 256 or 1024 threads) between its sum and its use, in vectors of 16
+// bytes where rows and columns allow, else element by element; rows wider than that are read
+// again (from L2).  Statistics, sums and products in fp32, one rounding at each store.
+//
+// The gradients of the gain sum over the rows.  A block walks rows a grid apart and keeps its
+// threads' columns in registers; its sums go to the workspace and a second launch adds the
+// blocks' in order, so that no atomics are needed and the same inputs give the same bits.
+#include "kfac_internal.cuh"
+
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+
+namespace kfac {
+namespace {
+
+constexpr float kE4m3Max = 448.f;
+constexpr int64_t kMaxCols = 1 << 20;
+constexpr int kMaxGroups = 8192;   // of a row's 8-bit output: their maxima are in shared memory
+
+struct NormArgs {
+  const void *x, *r;
+  const float* gain;
+  void *h, *y;
+  float* rstd;
+  uint8_t* q;
+  float* scales;
+  int64_t rows, ldx, ldr, ldh, ldy, ldq;
+  int cols, group, groups;
+  float inv_cols, eps;
+};
+
+template <typename T, int N> struct alignas(N * sizeof(T)) Vec { T v[N]; };
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the TPR threads of a row; every thread gets it.  red: a float per warp and slot
+// of the block, the slot another than in the call before.
+template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red) {
+  v = warp_sum(v);
+  if constexpr (TPR > 32) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    constexpr int W = TPR / 32;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = lane < W ? red[lane] : 0.f;
+    v = warp_sum(v);
+  }
+  return v;
+}
+
+// gain[c .. c + N), ones where there is none (N > 1: 16-byte aligned).
+template <int N>
+__device__ __forceinline__ void load_gain(const float* gain, int c, int cols, float (&g)[N]) {
+  if (!gain || c >= cols) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) g[i] = 1.f;
+  } else if constexpr (N == 1) {
+    g[0] = __ldg(gain + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(&g[i]) = __ldg(reinterpret_cast<const float4*>(gain + c + i));
+  }
+}
+
+// |v| as an integer: ordered like the values, NaN above infinity.
+__device__ __forceinline__ int abs_bits(float v) { return __float_as_int(v) & 0x7fffffff; }
+
+__device__ __forceinline__ uint8_t e4m3_of(float v, float scale) {
+  return (uint8_t)__nv_cvt_float_to_fp8(scale == 0.f ? 0.f : v / scale, __NV_SATFINITE, __NV_E4M3);
+}
+
+// A row per TPR threads, all of it in registers: thread t holds vectors t, t + TPR, ... of N
+// elements.  kQuant: with the 8-bit output; the groups' maxima meet in shared memory (a
+// maximum is the same in any order).
+template <typename T, int N, int TPR, int V, bool kRes, bool kQuant>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
+    norm_rows_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR;
+  extern __shared__ int amax[];   // kQuant: [RPB][groups]
+  __shared__ float red[32];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPB + sub;
+  const bool live = row < a.rows;
+  pdl_wait();
+  pdl_trigger();
+  using Pack = Vec<T, N>;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* r = static_cast<const T*>(a.r) + row * a.ldr;
+  float s[V][N], gain[V][N];
+  float sum = 0.f;
+  if (live) {
+    Pack px[V], pr[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * TPR + t) * N;
+      if (c < a.cols) {
+        px[v] = *reinterpret_cast<const Pack*>(x + c);
+        if (kRes) pr[v] = *reinterpret_cast<const Pack*>(r + c);
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_gain<N>(a.gain, (v * TPR + t) * N, a.cols, gain[v]);
+    T* h = static_cast<T*>(a.h) + row * a.ldh;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * TPR + t) * N;
+      if (c < a.cols) {
+        Pack ph;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          s[v][i] = to_f32<T>(px[v].v[i]);
+          if (kRes) s[v][i] += to_f32<T>(pr[v].v[i]);
+          ph.v[i] = (T)s[v][i];
+          sum = fmaf(s[v][i], s[v][i], sum);
+        }
+        if (a.h) *reinterpret_cast<Pack*>(h + c) = ph;
+      }
+    }
+  }
+  if (kQuant) {
+    for (int g = threadIdx.x; g < RPB * a.groups; g += BLOCK) amax[g] = 0;
+    if (TPR == 32) __syncthreads();   // otherwise the one inside row_sum
+  }
+  sum = row_sum<TPR>(sum, red);
+  const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
+  if (live && t == 0 && a.rstd) a.rstd[row] = rstd;
+  T* y = static_cast<T*>(a.y) + row * a.ldy;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * TPR + t) * N;
+    if (live && c < a.cols) {
+      Pack py;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s[v][i] = s[v][i] * rstd * gain[v][i];
+        py.v[i] = (T)s[v][i];
+      }
+      if (a.y) *reinterpret_cast<Pack*>(y + c) = py;
+    }
+  }
+  if constexpr (kQuant) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * TPR + t) * N;
+      int top = 0;
+      if (live && c < a.cols) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = max(top, abs_bits(s[v][i]));
+      }
+      if (a.group == 0) {   // one maximum per warp
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (threadIdx.x % 32 == 0) atomicMax(&amax[sub * a.groups], top);
+      } else if (live && c < a.cols) {
+        atomicMax(&amax[sub * a.groups + c / a.group], top);   // N divides the group
+      }
+    }
+    __syncthreads();
+    if (live) {
+      for (int g = t; g < a.groups; g += TPR)
+        a.scales[row * a.groups + g] = __int_as_float(amax[sub * a.groups + g]) / kE4m3Max;
+      uint8_t* q = a.q + row * a.ldq;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * TPR + t) * N;
+        if (c < a.cols) {
+          const float scale =
+              __int_as_float(amax[sub * a.groups + (a.group ? c / a.group : 0)]) / kE4m3Max;
+          Vec<uint8_t, N> pq;
+#pragma unroll
+          for (int i = 0; i < N; ++i) pq.v[i] = e4m3_of(s[v][i], scale);
+          *reinterpret_cast<Vec<uint8_t, N>*>(q + c) = pq;
+        }
+      }
+    }
+  }
+}
+
+// A row of any width per block, read twice (three times with the 8-bit output).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_wide_kernel(const __grid_constant__ NormArgs a) {
+  extern __shared__ int amax[];
+  __shared__ float red[32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = blockIdx.x;
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+  const T* r = a.r ? static_cast<const T*>(a.r) + row * a.ldr : nullptr;
+  // h may be x or residual: what is read again after it was written there comes from it
+  T* h = a.h ? static_cast<T*>(a.h) + row * a.ldh : nullptr;
+  T* y = a.y ? static_cast<T*>(a.y) + row * a.ldy : nullptr;
+  auto at = [&](int c) { return to_f32<T>(x[c]) + (r ? to_f32<T>(r[c]) : 0.f); };
+  float sum = 0.f;
+  for (int c = threadIdx.x; c < a.cols; c += 1024) {
+    const float s = at(c);
+    sum = fmaf(s, s, sum);
+  }
+  if (a.q)
+    for (int g = threadIdx.x; g < a.groups; g += 1024) amax[g] = 0;
+  sum = row_sum<1024>(sum, red);
+  const float rstd = rsqrtf(fmaf(sum, a.inv_cols, a.eps));
+  if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+  auto norm = [&](int c, float s) { return s * rstd * (a.gain ? __ldg(a.gain + c) : 1.f); };
+  if (a.q) {
+    for (int c = threadIdx.x; c < a.cols; c += 1024)
+      atomicMax(&amax[a.group ? c / a.group : 0], abs_bits(norm(c, at(c))));
+    __syncthreads();
+    for (int g = threadIdx.x; g < a.groups; g += 1024)
+      a.scales[row * a.groups + g] = __int_as_float(amax[g]) / kE4m3Max;
+  }
+  for (int c = threadIdx.x; c < a.cols; c += 1024) {   // each element by one thread: h in place
+    const float s = at(c), v = norm(c, s);
+    if (h) h[c] = (T)s;
+    if (y) y[c] = (T)v;
+    if (a.q)
+      a.q[row * a.ldq + c] = e4m3_of(v, __int_as_float(amax[a.group ? c / a.group : 0]) / kE4m3Max);
+  }
+}
+
+template <typename T, int N, int TPR, int V>
+void launch_norm_rows(const NormArgs& a, cudaStream_t st) {
+  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR;
+  const dim3 grid((unsigned)cdiv(a.rows, RPB)), block(BLOCK);
+  if (a.q) {
+    const size_t smem = (size_t)RPB * a.groups * sizeof(int);
+    if (a.r) launch_pdl(norm_rows_kernel<T, N, TPR, V, true, true>, grid, block, smem, st, a);
+    else launch_pdl(norm_rows_kernel<T, N, TPR, V, false, true>, grid, block, smem, st, a);
+  } else {
+    if (a.r) launch_pdl(norm_rows_kernel<T, N, TPR, V, true, false>, grid, block, 0, st, a);
+    else launch_pdl(norm_rows_kernel<T, N, TPR, V, false, false>, grid, block, 0, st, a);
+  }
+}
+
+// Threads per row: 256 with as many vectors each as the row needs; a warp for narrow rows;
+// 1024 for wide ones.
+template <typename T, int N> bool launch_norm(const NormArgs& a, cudaStream_t st) {
+  const int64_t vecs = cdiv(a.cols, N);
+  if (vecs <= 32) launch_norm_rows<T, N, 32, 1>(a, st);
+  else if (vecs <= 64) launch_norm_rows<T, N, 32, 2>(a, st);
+  else if (vecs <= 256) launch_norm_rows<T, N, 256, 1>(a, st);
+  else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
+  else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
+  else if (vecs <= 2048) launch_norm_rows<T, N, 1024, 2>(a, st);
+  else return false;
+  return true;
+}
+
+// ------------------------------------------------------------------------------ backward
+
+struct NormGradArgs {
+  const void *dy, *h, *dh;
+  const float *gain, *rstd;
+  void* dx;
+  float *part;            // [parts][2][cols]
+  float *dgain, *dgain_sq;
+  int64_t rows, lddy, ldh, lddh, lddx;
+  int cols, parts;
+  float inv_cols, inv_rows;
+};
+
+// Rows a grid apart, R at a time, TPR threads each; thread t holds vectors t, t + TPR, ...
+template <typename T, int N, int TPR, int V, int R, bool kDh>
+__global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
+    norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
+  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR, W = TPR / 32;
+  extern __shared__ float fold[];          // TPR == 32: [RPB][2][32 V N]
+  __shared__ float red[2][R][32];
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  using Pack = Vec<T, N>;
+  pdl_wait();
+  pdl_trigger();
+  float gain[V][N], dg[V][N], sq[V][N];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    load_gain<N>(a.gain, (v * TPR + t) * N, a.cols, gain[v]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dg[v][i] = sq[v][i] = 0.f;
+  }
+  const int64_t step = (int64_t)gridDim.x * RPB;
+  int turn = 0;
+  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += R * step, turn ^= 1) {
+    Pack pg[R][V], ph[R][V], pd[R][V];
+    float rstd[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const int64_t row = row0 + j * step + sub;
+      if (row >= a.rows) continue;
+      rstd[j] = __ldg(a.rstd + row);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * TPR + t) * N;
+        if (c >= a.cols) continue;
+        pg[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.dy) + row * a.lddy + c);
+        ph[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.h) + row * a.ldh + c);
+        if (kDh)
+          pd[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.dh) + row * a.lddh + c);
+      }
+    }
+    float dot[R];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      dot[j] = 0.f;
+      if (row0 + j * step + sub >= a.rows) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if ((v * TPR + t) * N >= a.cols) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float n = to_f32<T>(ph[j][v].v[i]) * rstd[j], g = to_f32<T>(pg[j][v].v[i]);
+          const float e = g * n;
+          dot[j] = fmaf(e, gain[v][i], dot[j]);
+          dg[v][i] += e;
+          sq[v][i] = fmaf(e, e, sq[v][i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) dot[j] = warp_sum(dot[j]);
+    if constexpr (TPR > 32) {   // two slots in turn: one barrier per round
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) red[turn][j][warp] = dot[j];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < R; ++j) dot[j] = warp_sum(lane < W ? red[turn][j][lane] : 0.f);
+    }
+    if (a.dx) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int64_t row = row0 + j * step + sub;
+        if (row >= a.rows) continue;
+        const float mean = dot[j] * a.inv_cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int c = (v * TPR + t) * N;
+          if (c >= a.cols) continue;
+          Pack px;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float n = to_f32<T>(ph[j][v].v[i]) * rstd[j];
+            float d = rstd[j] * (to_f32<T>(pg[j][v].v[i]) * gain[v][i] - n * mean);
+            if (kDh) d += to_f32<T>(pd[j][v].v[i]);
+            px.v[i] = (T)d;
+          }
+          *reinterpret_cast<Pack*>(static_cast<T*>(a.dx) + row * a.lddx + c) = px;
+        }
+      }
+    }
+  }
+  if (!a.part) return;
+  float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
+  if constexpr (RPB > 1) {   // the block's row groups, in order
+    constexpr int C = TPR * V * N;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        fold[(sub * 2 + 0) * C + (v * TPR + t) * N + i] = dg[v][i];
+        fold[(sub * 2 + 1) * C + (v * TPR + t) * N + i] = sq[v][i];
+      }
+    }
+    __syncthreads();
+    for (int k = threadIdx.x; k < 2 * a.cols; k += BLOCK) {
+      const int which = k >= a.cols, c = k - which * a.cols;
+      float s = 0.f;
+      for (int u = 0; u < RPB; ++u) s += fold[(u * 2 + which) * C + c];
+      part[k] = s;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * TPR + t) * N;
+      if (c >= a.cols) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        part[c + i] = dg[v][i];
+        part[a.cols + c + i] = sq[v][i];
+      }
+    }
+  }
+}
+
+// Rows too wide for registers: the means first (rows x parts blocks would re-read them), then
+// columns by thread over the rows of a part.
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_wide_dot_kernel(const __grid_constant__ NormGradArgs a,
+                                                             float* means) {
+  __shared__ float red[32];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t row = blockIdx.x;
+  const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+  const T* h = static_cast<const T*>(a.h) + row * a.ldh;
+  const float rstd = a.rstd[row];
+  float dot = 0.f;
+  for (int c = threadIdx.x; c < a.cols; c += 1024)
+    dot = fmaf(to_f32<T>(dy[c]) * (to_f32<T>(h[c]) * rstd), a.gain ? __ldg(a.gain + c) : 1.f, dot);
+  dot = row_sum<1024>(dot, red);
+  if (threadIdx.x == 0) means[row] = dot * a.inv_cols;
+}
+template <typename T>
+__global__ void __launch_bounds__(256) norm_wide_backward_kernel(const __grid_constant__ NormGradArgs a,
+                                                                 const float* means) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.cols) return;
+  const float gain = a.gain ? a.gain[c] : 1.f;
+  float dg = 0.f, sq = 0.f;
+  for (int64_t row = blockIdx.y; row < a.rows; row += a.parts) {
+    const float rstd = __ldg(a.rstd + row);
+    const float g = to_f32<T>(static_cast<const T*>(a.dy)[row * a.lddy + c]);
+    const float n = to_f32<T>(static_cast<const T*>(a.h)[row * a.ldh + c]) * rstd;
+    const float e = g * n;
+    dg += e;
+    sq = fmaf(e, e, sq);
+    if (a.dx) {
+      float d = rstd * (g * gain - n * means[row]);
+      if (a.dh) d += to_f32<T>(static_cast<const T*>(a.dh)[row * a.lddh + c]);
+      static_cast<T*>(a.dx)[row * a.lddx + c] = (T)d;
+    }
+  }
+  if (!a.part) return;
+  a.part[((int64_t)blockIdx.y * 2) * a.cols + c] = dg;
+  a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = sq;
+}
+
+// The parts' sums, in order: a block takes 32 of the 2 cols columns, warp w every 8th part.
+__global__ void __launch_bounds__(256) norm_parts_kernel(const __grid_constant__ NormGradArgs a) {
+  __shared__ float s[8][32];
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int k = blockIdx.x * 32 + lane;
+  float sum = 0.f;
+  if (k < 2 * a.cols)
+    for (int p = warp; p < a.parts; p += 8) sum += a.part[(int64_t)p * 2 * a.cols + k];
+  s[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0 && k < 2 * a.cols) {
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) sum += s[w][lane];
+    if (k < a.cols) {
+      if (a.dgain) a.dgain[k] = sum;
+    } else if (a.dgain_sq) {
+      a.dgain_sq[k - a.cols] = sum * a.inv_rows;
+    }
+  }
+}
+
+// Blocks of the backward pass: two per SM.
+int64_t backward_parts(int64_t rows) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, 2 * (int64_t)num_sms()));
+}
+
+template <typename T, int N, int TPR, int V, int R>
+void launch_backward_rows(const NormGradArgs& a, cudaStream_t st) {
+  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR;
+  const size_t smem = RPB > 1 ? (size_t)2 * RPB * TPR * V * N * sizeof(float) : 0;
+  const dim3 grid((unsigned)a.parts), block(BLOCK);
+  if (a.dh) launch_pdl(norm_backward_kernel<T, N, TPR, V, R, true>, grid, block, smem, st, a);
+  else launch_pdl(norm_backward_kernel<T, N, TPR, V, R, false>, grid, block, smem, st, a);
+}
+
+template <typename T, int N> bool launch_backward(const NormGradArgs& a, cudaStream_t st) {
+  const int64_t vecs = cdiv(a.cols, N);
+  if (vecs <= 32) launch_backward_rows<T, N, 32, 1, 4>(a, st);
+  else if (vecs <= 256) launch_backward_rows<T, N, 256, 1, 4>(a, st);
+  else if (vecs <= 512) launch_backward_rows<T, N, 256, 2, 2>(a, st);
+  else if (vecs <= 1024) launch_backward_rows<T, N, 256, 4, 1>(a, st);
+  else if constexpr (N == 1) {
+    if (vecs <= 2048) launch_backward_rows<T, N, 256, 8, 1>(a, st);
+    else if (vecs <= 8192) launch_backward_rows<T, N, 1024, 8, 1>(a, st);
+    else return false;
+  } else {
+    return false;
+  }
+  return true;
+}
+
+// Whether rows of p are whole aligned vectors.
+bool wide_ok(const void* p, int64_t ld, int64_t rows, int vec_bytes, size_t es) {
+  return !p || ((uintptr_t)p % vec_bytes == 0 && (rows == 1 || ld * (int64_t)es % vec_bytes == 0));
+}
+
+}  // namespace
+}  // namespace kfac
+
+using namespace kfac;
+
+extern "C" kfac_status kfac_rms_norm(const kfac_norm_desc* d, const void* x, const void* residual,
+                                     const float* gain, void* h, void* y, float* rstd, void* q,
+                                     float* scales, cudaStream_t stream) {
+  if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16)) return KFAC_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->cols < 0 || !(d->eps >= 0.0) || !std::isfinite(d->eps))
+    return KFAC_ERR_INVALID_ARG;
+  if (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128)
+    return KFAC_ERR_INVALID_ARG;
+  if (d->rows == 0 || d->cols == 0) return KFAC_OK;
+  if (d->rows >= (int64_t(1) << 31) || d->cols > kMaxCols ||
+      (q && d->group && cdiv(d->cols, d->group) > kMaxGroups))
+    return KFAC_ERR_UNSUPPORTED;
+  const size_t es = d->dtype == KFAC_BF16 ? 2 : 4;
+  auto bad = [&](const void* p, int64_t ld, size_t e) {
+    return p && ((uintptr_t)p % e || ld < 0 || ld > (int64_t(1) << 40) || (d->rows > 1 && ld < d->cols));
+  };
+  if (!x || (!y && !q) || (q && !scales) || bad(x, d->ldx, es) || bad(residual, d->ldr, es) ||
+      bad(h, d->ldh, es) || bad(y, d->ldy, es) || bad(q, d->ldq, 1) || (uintptr_t)gain % 4 ||
+      (uintptr_t)rstd % 4 || (uintptr_t)scales % 4)
+    return KFAC_ERR_INVALID_ARG;
+  if ((h == x && d->rows > 1 && d->ldh != d->ldx) ||
+      (h && h == residual && d->rows > 1 && d->ldh != d->ldr) || y == x || (residual && y == residual) || (y && y == h))
+    return KFAC_ERR_INVALID_ARG;
+  NormArgs a{};
+  a.x = x;
+  a.r = residual;
+  a.gain = gain;
+  a.h = h;
+  a.y = y;
+  a.rstd = rstd;
+  a.q = static_cast<uint8_t*>(q);
+  a.scales = scales;
+  a.rows = d->rows;
+  a.ldx = d->ldx;
+  a.ldr = d->ldr;
+  a.ldh = d->ldh;
+  a.ldy = d->ldy;
+  a.ldq = d->ldq;
+  a.cols = (int)d->cols;
+  a.group = d->group;
+  a.groups = d->group ? (int)cdiv(d->cols, d->group) : 1;
+  a.inv_cols = (float)(1.0 / (double)d->cols);
+  a.eps = (float)d->eps;
+  const int n = 16 / (int)es;
+  const bool vec = d->cols % n == 0 && wide_ok(x, d->ldx, d->rows, 16, es) &&
+                   wide_ok(residual, d->ldr, d->rows, 16, es) && wide_ok(h, d->ldh, d->rows, 16, es) &&
+                   wide_ok(y, d->ldy, d->rows, 16, es) && wide_ok(q, d->ldq, d->rows, n, 1) &&
+                   (uintptr_t)gain % 16 == 0;
+  bool done;
+  if (d->dtype == KFAC_BF16)
+    done = vec ? launch_norm<__nv_bfloat16, 8>(a, stream) : launch_norm<__nv_bfloat16, 1>(a, stream);
+  else
+    done = vec ? launch_norm<float, 4>(a, stream) : launch_norm<float, 1>(a, stream);
+  if (!done) {
+    const size_t smem = q ? (size_t)a.groups * sizeof(int) : 0;
+    const dim3 grid((unsigned)a.rows), block(1024);
+    if (d->dtype == KFAC_BF16) launch_pdl(norm_wide_kernel<__nv_bfloat16>, grid, block, smem, stream, a);
+    else launch_pdl(norm_wide_kernel<float>, grid, block, smem, stream, a);
+  }
+  count_launch();
+  return check_launch();
+}
+
+extern "C" kfac_status kfac_rms_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes || rows < 0 || cols < 0) return KFAC_ERR_INVALID_ARG;
+  if (rows >= (int64_t(1) << 31) || cols > kMaxCols) return KFAC_ERR_UNSUPPORTED;
+  *bytes = align_up((size_t)(backward_parts(rows) * 2 * cols) * sizeof(float)) +
+           align_up((size_t)rows * sizeof(float));
+  return KFAC_OK;
+}
+
+extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, const void* dy,
+                                              const void* h, const float* gain, const float* rstd,
+                                              const void* dh, void* dx, float* dgain,
+                                              float* dgain_square, void* workspace,
+                                              size_t workspace_bytes, cudaStream_t stream) {
+  if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16)) return KFAC_ERR_INVALID_ARG;
+  if (d->rows < 0 || d->cols < 0) return KFAC_ERR_INVALID_ARG;
+  if ((uintptr_t)dgain % 4 || (uintptr_t)dgain_square % 4) return KFAC_ERR_INVALID_ARG;
+  if (d->cols == 0 || (d->rows == 0 && !dgain && !dgain_square)) return KFAC_OK;
+  if (d->rows >= (int64_t(1) << 31) || d->cols > kMaxCols) return KFAC_ERR_UNSUPPORTED;
+  const size_t es = d->dtype == KFAC_BF16 ? 2 : 4;
+  auto bad = [&](const void* p, int64_t ld) {
+    return (uintptr_t)p % es || ld < 0 || ld > (int64_t(1) << 40) || (d->rows > 1 && ld < d->cols);
+  };
+  if (d->rows > 0) {
+    if (!dy || !h || !rstd || bad(dy, d->lddy) || bad(h, d->ldh) || (dh && bad(dh, d->lddh)) ||
+        (dx && bad(dx, d->lddx)) || (uintptr_t)gain % 4 || (uintptr_t)rstd % 4)
+      return KFAC_ERR_INVALID_ARG;
+    if (dx && ((dx == dy && d->rows > 1 && d->lddx != d->lddy) ||
+               (dx == dh && d->rows > 1 && d->lddx != d->lddh) || dx == h))
+      return KFAC_ERR_INVALID_ARG;
+  }
+  size_t need = 0;
+  if (kfac_status e = kfac_rms_norm_workspace_size(d->rows, d->cols, &need)) return e;
+  if (!workspace || (uintptr_t)workspace % kAlign || workspace_bytes < need) return KFAC_ERR_WORKSPACE;
+  if (!dx && !dgain && !dgain_square) return KFAC_OK;
+  NormGradArgs a{};
+  a.dy = dy;
+  a.h = h;
+  a.dh = dh;
+  a.gain = gain;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.dgain = dgain;
+  a.dgain_sq = dgain_square;
+  a.rows = d->rows;
+  a.lddy = d->lddy;
+  a.ldh = d->ldh;
+  a.lddh = d->lddh;
+  a.lddx = d->lddx;
+  a.cols = (int)d->cols;
+  a.parts = (int)backward_parts(d->rows);
+  a.inv_cols = (float)(1.0 / (double)d->cols);
+  a.inv_rows = d->rows > 0 ? (float)(1.0 / (double)d->rows) : 0.f;
+  if (dgain || dgain_square) a.part = static_cast<float*>(workspace);
+  const int n = 16 / (int)es;
+  const bool vec = d->cols % n == 0 && wide_ok(dy, d->lddy, d->rows, 16, es) &&
+                   wide_ok(h, d->ldh, d->rows, 16, es) && wide_ok(dh, d->lddh, d->rows, 16, es) &&
+                   wide_ok(dx, d->lddx, d->rows, 16, es) && (uintptr_t)gain % 16 == 0;
+  int launches = 1;
+  bool done;
+  if (d->dtype == KFAC_BF16)
+    done = vec ? launch_backward<__nv_bfloat16, 8>(a, stream) : launch_backward<__nv_bfloat16, 1>(a, stream);
+  else
+    done = vec ? launch_backward<float, 4>(a, stream) : launch_backward<float, 1>(a, stream);
+  if (!done) {
+    float* means = reinterpret_cast<float*>(
+        static_cast<char*>(workspace) + align_up((size_t)(a.parts * 2 * d->cols) * sizeof(float)));
+    const dim3 grid((unsigned)cdiv(d->cols, 256), (unsigned)a.parts);
+    if (d->dtype == KFAC_BF16) {
+      if (d->rows > 0)
+        launch_pdl(norm_wide_dot_kernel<__nv_bfloat16>, dim3((unsigned)d->rows), dim3(1024), 0, stream, a, means);
+      launch_pdl(norm_wide_backward_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, a,
+                 (const float*)means);
+    } else {
+      if (d->rows > 0)
+        launch_pdl(norm_wide_dot_kernel<float>, dim3((unsigned)d->rows), dim3(1024), 0, stream, a, means);
+      launch_pdl(norm_wide_backward_kernel<float>, grid, dim3(256), 0, stream, a, (const float*)means);
+    }
+    launches = d->rows > 0 ? 2 : 1;
+  }
+  if (a.part) {
+    launch_pdl(norm_parts_kernel, dim3((unsigned)cdiv(2 * (int64_t)a.cols, 32)), dim3(256), 0, stream, a);
+    ++launches;
+  }
+  count_launch(launches);
+  return check_launch();
+}
