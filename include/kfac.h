@@ -650,10 +650,70 @@ kfac_status kfac_embedding_backward(const kfac_embedding_desc* desc, const void*
                                     int accumulate, float* frequency, void* workspace,
                                     size_t workspace_bytes, cudaStream_t stream);
 
+/* Arithmetic of the orthogonalised update.  FULL: operands as two fp16 values each (22
+ * bits), three products, fp32 sums: results within about 1e-6 of exact ones in norm.
+ * HALF: operands as one fp16 value, scaled by powers of two to their bounds: within 2e-3
+ * to 3e-3 after five steps of a matrix with a few strong directions and noise, more where
+ * nearly all singular values are tiny (1e-2 where they fall to 1e-4 of the largest). */
+typedef enum { KFAC_ORTHO_FULL = 0, KFAC_ORTHO_HALF = 1 } kfac_ortho_math;
+
+typedef struct {
+  int dtype;   /* kfac_dtype of x and out, or of grad                                  */
+  int math;    /* kfac_ortho_math                                                      */
+  int steps;   /* 1..32                                                                */
+  double eps;  /* >= 0, added to the norm                                              */
+  const double* coefficients;  /* host [steps][3]: (a, b, c) of each step; NULL: every step
+                                  (3.4445, -4.7750, 2.0315), which lifts singular values
+                                  from 0.01 into 0.7..1.2 in five                      */
+} kfac_ortho_desc;
+
+/* Bytes of workspace that kfac_orthogonalize and kfac_orthogonal_step need for `count`
+ * matrices of these sizes (host arrays; a 256-byte multiple): about 4 bytes per element
+ * and 4 per element of the square of the smaller side, twice that in full arithmetic.  It
+ * holds nothing between calls; calls that share one must be ordered. */
+kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int count, const int* rows,
+                                              const int* cols, size_t* bytes);
+
+/* The orthogonal factor of each matrix, by Newton-Schulz products:
+ *   X = x / (|x|_F + eps);  per step: L = X X^T, X <- (a I + b L + c L^2) X;  out = X
+ * (L = X^T X and X <- X (...) where rows > cols).  A singular value t of X becomes a t +
+ * b t^3 + c t^5, its singular vectors stay.  A matrix of zeros gives zeros; Inf or NaN
+ * anywhere in x makes all of its out NaN.  x, out: [rows x cols], sides up to 32768 (else
+ * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
+ * count.  out may be x with the same leading dimension.  All matrices go through each
+ * product together, up to 32 at a time.  The coefficients have to keep the bound of the
+ * singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at each step (else
+ * KFAC_ERR_INVALID_ARG). */
+kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int* rows,
+                               const int* cols, const void* const* x, const int64_t* ldx,
+                               void* const* out, const int64_t* ldo, void* workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+typedef struct {
+  double lr;            /* eta                                                         */
+  double momentum;      /* mu                                                          */
+  double weight_decay;  /* lambda                                                      */
+  double update_scale;  /* kappa                                                       */
+  int nesterov;         /* 0/1                                                         */
+} kfac_ortho_step;
+
+/* A whole optimizer step of each matrix along its orthogonalised momentum:
+ *   m <- mu m + g;   u = g + mu m (nesterov) or m;   O = kfac_orthogonalize(u);
+ *   W <- W - eta (kappa sqrt(max(1, rows / cols)) O + lambda W).
+ * grad: dtype, [rows x cols]; momentum and param: fp32, updated in place.  The momentum
+ * is read and written by the pass that takes the norm, the weights by the last product.
+ * Otherwise as kfac_orthogonalize. */
+kfac_status kfac_orthogonal_step(const kfac_ortho_desc* desc, const kfac_ortho_step* hp, int count,
+                                 const int* rows, const int* cols, const void* const* grad,
+                                 const int64_t* ldg, float* const* momentum, const int64_t* ldm,
+                                 float* const* param, const int64_t* ldp, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream);
+
 /* Synchronise the current device and report the first device-side error of the
- * block operators on it since the last call (then clear it): a pipeline
- * wait of the tensor-core attention that gave up (KFAC_ERR_TIMEOUT; info: which
- * role).  The outputs of the blocks concerned hold NaN.  KFAC_OK: none. */
+ * block operators, or of the orthogonalised updates, on it since the last call (then
+ * clear it): a pipeline wait of their tensor-core kernels that gave up
+ * (KFAC_ERR_TIMEOUT; info: which role).  The outputs of the blocks concerned hold NaN
+ * (weights: keep their values).  KFAC_OK: none. */
 kfac_status kfac_operator_status(int* info);
 
 /* Diagnostics: number of kernels this library has launched in this process. */

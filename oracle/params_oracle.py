@@ -62,3 +62,57 @@ def embedding_backward(ids, dout, rows, scale=1.0, padding_id=-1):
             dtable[v] += scale * dout[t]
             count[v] += 1
     return dtable, count / max(1, ids.size)
+
+
+COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    """Singular values mapped by the steps' polynomials, the singular vectors kept."""
+    x = np.asarray(x, np.float64)
+    norm = np.sqrt((x * x).sum()) + eps
+    if norm == 0:
+        return x.copy()
+    u, t, vt = np.linalg.svd(x / norm, full_matrices=False)
+    per_step = [coefficients] * steps if np.ndim(coefficients) == 1 else coefficients
+    for a, b, c in per_step:
+        t = a * t + b * t ** 3 + c * t ** 5
+    return (u * t) @ vt
+
+
+def newton_schulz(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    """The same by its products."""
+    x = np.asarray(x, np.float64)
+    x = x / (np.sqrt((x * x).sum()) + eps)
+    a, b, c = coefficients
+    for _ in range(steps):
+        g = x @ x.T
+        x = a * x + (b * g + c * g @ g) @ x
+    return x
+
+
+def orthogonal_step(grad, m, w, lr, momentum=0.95, weight_decay=0.0, nesterov=True, update_scale=1.0,
+                    **kw):
+    """(momentum, weights) after one step."""
+    m = momentum * np.asarray(m, np.float64) + grad
+    o = orthogonalize(grad + momentum * m if nesterov else m, **kw)
+    scale = update_scale * np.sqrt(max(1.0, w.shape[0] / w.shape[1]))
+    return m, w - lr * (scale * o + weight_decay * w)
+
+
+def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    """The products with every matrix between them rounded to fp16's 11 bits (x too): the error that
+    such operands cannot avoid."""
+    def near(v):
+        m, e = np.frexp(v)
+        return np.ldexp(np.rint(m * 2.0 ** 11), e - 11)
+    x = np.asarray(x, np.float64)
+    x = x.T if x.shape[0] > x.shape[1] else x
+    x = near(x) / (np.sqrt((x * x).sum()) + eps)
+    a, b, c = coefficients
+    eye = np.eye(x.shape[0])
+    for k in range(steps):
+        g = near(x @ x.T)
+        x = near(a * eye + b * g + c * g @ g) @ x
+        x = x if k + 1 == steps else near(x)
+    return x

@@ -20,7 +20,7 @@ from ._lib import (LIB, KFAC_KRON, KFAC_DIAG, KFAC_F32, KFAC_BF16, KFAC_MATH_3XT
                    KFAC_STATE_G, KFAC_STATE_AINV, KFAC_STATE_GINV, KFAC_STATE_MOMENTUM,
                    KFAC_STATE_GDIAG, KFAC_STATE_ADIAG, LayerDesc, HParams, Conv2dGeom, KfacError,
                    status_string, launch_count, KFAC_ROPE_PLAIN, KFAC_ROPE_LINEAR,
-                   KFAC_ROPE_NTK, KFAC_ROPE_YARN)
+                   KFAC_ROPE_NTK, KFAC_ROPE_YARN, KFAC_ORTHO_FULL, KFAC_ORTHO_HALF)
 
 # the operators of _block.py, loaded with torch at their first use: the rest of the package
 # imports without torch
@@ -28,7 +28,8 @@ _BLOCK = ("rope", "rope_table", "dropout", "dropout_backward", "cross_attention"
           "cross_attention_backward", "cross_attention_workspace", "operator_status")
 # those of _params.py likewise
 _PARAMS = ("rms_norm", "rms_norm_e4m3", "rms_norm_backward", "rms_norm_workspace", "embedding",
-           "embedding_backward", "embedding_workspace")
+           "embedding_backward", "embedding_workspace", "orthogonalize", "orthogonal_step",
+           "orthogonalize_workspace")
 
 
 def __getattr__(name):
@@ -52,7 +53,8 @@ __all__ = ["Kfac", "diag_factors_static", "conv2d_geom", "LayerDesc", "HParams",
            "KFAC_IKFAC_OFF", "KFAC_IKFAC_TF32", "KFAC_IKFAC_BF16",
            "KFAC_FACTOR_G", "LIB",
            *_BLOCK, *_PARAMS,
-           "KFAC_ROPE_PLAIN", "KFAC_ROPE_LINEAR", "KFAC_ROPE_NTK", "KFAC_ROPE_YARN"]
+           "KFAC_ROPE_PLAIN", "KFAC_ROPE_LINEAR", "KFAC_ROPE_NTK", "KFAC_ROPE_YARN",
+           "KFAC_ORTHO_FULL", "KFAC_ORTHO_HALF"]
 
 
 def _ptr(t) -> Optional[int]:

@@ -21,6 +21,7 @@ KFAC_MATH_3XTF32, KFAC_MATH_BF16 = 0, 1
 KFAC_EMA_INIT_ZERO, KFAC_EMA_INIT_FIRST = 0, 1
 KFAC_IKFAC_OFF, KFAC_IKFAC_TF32, KFAC_IKFAC_BF16 = 0, 1, 2
 KFAC_FACTOR_A, KFAC_FACTOR_G = 1, 2
+KFAC_ORTHO_FULL, KFAC_ORTHO_HALF = 0, 1
 KFAC_ROPE_PLAIN, KFAC_ROPE_LINEAR, KFAC_ROPE_NTK, KFAC_ROPE_YARN = range(4)
 (KFAC_STATE_A, KFAC_STATE_G, KFAC_STATE_AINV, KFAC_STATE_GINV, KFAC_STATE_MOMENTUM,
  KFAC_STATE_GDIAG, KFAC_STATE_ADIAG) = range(7)
@@ -71,6 +72,9 @@ ATTENTION_GRAD_DESC = struct.Struct("@12q")
 NORM_DESC = struct.Struct("@iqqd5qi")
 NORM_GRAD_DESC = struct.Struct("@i6q")
 EMBEDDING_DESC = struct.Struct("@iiqqqdqq")
+# kfac_ortho_desc and kfac_ortho_step likewise
+ORTHO_DESC = struct.Struct("@iiidP")
+ORTHO_STEP = struct.Struct("@4di")
 
 # (name, restype, argtypes): one line per entry point of include/kfac.h
 SIGNATURES = [
@@ -116,6 +120,9 @@ SIGNATURES = [
     ("kfac_embedding", _i, [_vp, _vp, _vp, _vp, _vp]),
     ("kfac_embedding_workspace_size", _i, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
     ("kfac_embedding_backward", _i, [_vp, _vp, _vp, _vp, _i64, _i, _vp, _vp, _sz, _vp]),
+    ("kfac_orthogonalize_workspace_size", _i, [_vp, _i, _vp, _vp, ctypes.POINTER(_sz)]),
+    ("kfac_orthogonalize", _i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_orthogonal_step", _i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     ("kfac_operator_status", _i, [ctypes.POINTER(_i)]),
 ]
 

@@ -1,5 +1,6 @@
 """Operators of the parameters without Kronecker factors: root-mean-square norms and the token
-embedding, forward and backward, with the diagonal factors that Kfac.diag_step takes.
+embedding, forward and backward, with the diagonal factors that Kfac.diag_step takes; weight
+matrices stepped along their orthogonalised momentum.
 
 Argument marshalling only, in the manner of _block.py: outputs and workspaces may be given or are
 allocated with torch; ValueError for a wrong shape, type or device, KfacError for what the library
@@ -12,7 +13,8 @@ import ctypes
 import torch
 
 from ._block import _call, _check, _device, _dtype, _elsewhere, _empty
-from ._lib import LIB, NORM_DESC, NORM_GRAD_DESC, EMBEDDING_DESC
+from ._lib import (LIB, KFAC_BF16, KFAC_ORTHO_FULL, KFAC_ORTHO_HALF, NORM_DESC, NORM_GRAD_DESC,
+                   EMBEDDING_DESC, ORTHO_DESC, ORTHO_STEP)
 
 
 def _new(shape, dtype, dev, stream):
@@ -261,3 +263,115 @@ def embedding_backward(ids, dout, rows: int, scale: float = 1.0, padding_id: int
           ids.data_ptr(), dout.data_ptr(), out.data_ptr(), padding_id, int(accumulate),
           _vector(what, "frequency", frequency, rows, dev), workspace.data_ptr(), workspace.nbytes)
     return out
+
+
+# ----------------------------------------------------------------------- orthogonalised updates
+
+class _Matrices:
+    """A list of 2-D tensors with contiguous rows (3-D ones: their entries) as the C call takes it."""
+
+    def __init__(self, what, name, tensors, dtype=None, like=None):
+        ts = []
+        for t in ([tensors] if isinstance(tensors, torch.Tensor) else tensors):
+            if t.dim() == 3:
+                ts.extend(t.unbind(0))
+            elif t.dim() == 2:
+                ts.append(t)
+            else:
+                raise ValueError(f"{what}: {name} is [rows, columns], or [batch, rows, columns]")
+        self.count = n = len(ts)
+        if like is None:
+            self.dev = _device(ts[0], what) if n else torch.cuda.current_device()
+            self.dtype = ts[0].dtype if n else torch.float32
+            self.dt = _dtype(ts[0], what) if n else 0
+            self.shapes = [t.shape for t in ts]
+            self.rows = (ctypes.c_int * n)(*[s[0] for s in self.shapes])
+            self.cols = (ctypes.c_int * n)(*[s[1] for s in self.shapes])
+        else:
+            self.dev, self.dtype, self.shapes = like.dev, dtype or like.dtype, like.shapes
+            if n != like.count:
+                raise ValueError(f"{what}: {name} has {n} matrices, not {like.count}")
+        lds = []
+        for t, shape in zip(ts, self.shapes):
+            if t.dtype is not self.dtype or t.shape != shape:
+                raise ValueError(f"{what}: {name} holds {t.dtype} {tuple(t.shape)}, not {self.dtype} "
+                                 f"{tuple(shape)}")
+            if t.get_device() != self.dev:
+                _elsewhere(what, name, t, self.dev)
+            s0, s1 = t.stride()
+            if s1 != 1 and shape[1] > 1:
+                raise ValueError(f"{what}: {name}'s rows are contiguous")
+            lds.append(s0)
+        self.ld = (ctypes.c_int64 * n)(*lds)
+        self.ptr = (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])
+
+
+def _ortho_desc(what, dt, math, steps, eps, coefficients):
+    """(descriptor bytes, the coefficients that it points to)."""
+    if math is None:
+        math = KFAC_ORTHO_HALF if dt == KFAC_BF16 else KFAC_ORTHO_FULL
+    flat = None
+    if coefficients is not None:
+        rows = list(coefficients)
+        if len(rows) == 3 and not hasattr(rows[0], "__len__"):
+            rows = [rows] * steps
+        if len(rows) != steps or any(len(r) != 3 for r in rows):
+            raise ValueError(f"{what}: coefficients are (a, b, c), or one such triple per step")
+        flat = (ctypes.c_double * (3 * steps))(*[float(v) for r in rows for v in r])
+    return ORTHO_DESC.pack(dt, math, steps, float(eps), ctypes.addressof(flat) if flat else 0), flat
+
+
+def orthogonalize_workspace(x, math=None):
+    """A workspace tensor for orthogonalize or orthogonal_step of matrices like x (tensor or list;
+    orthogonal_step: the gradients), to be kept and passed to the calls."""
+    what = "orthogonalize_workspace"
+    m = _Matrices(what, "x", x)
+    # (any number of steps but one takes the same)
+    desc, _ = _ortho_desc(what, m.dt, math, 2, 0.0, None)
+    return _kept(_sized(LIB.kfac_orthogonalize_workspace_size, "kfac_orthogonalize_workspace_size",
+                        m.dev, desc, m.count, m.rows, m.cols), m.dev)
+
+
+def _ortho_workspace(what, desc, m, workspace, stream):
+    return _workspace(what, workspace, 0 if workspace is not None else _sized(
+        LIB.kfac_orthogonalize_workspace_size, "kfac_orthogonalize_workspace_size", m.dev, desc,
+        m.count, m.rows, m.cols), m.dev, stream)
+
+
+def orthogonalize(x, out=None, steps: int = 5, coefficients=None, eps: float = 1e-7, math=None,
+                  workspace=None, stream=None):
+    """kfac_orthogonalize: the orthogonal factor of each matrix by Newton-Schulz products; returns
+    out.  x: a tensor [rows, columns] or [batch, rows, columns], or a list of such, float32 or
+    bfloat16, rows contiguous; out alike (may be x).  math: KFAC_ORTHO_FULL (the default for
+    float32) or KFAC_ORTHO_HALF (for bfloat16).  coefficients: (a, b, c) of x -> a x + b x^3 + c x^5
+    for every step, or one triple per step."""
+    what = "orthogonalize"
+    m = _Matrices(what, "x", x)
+    if out is None:
+        one = isinstance(x, torch.Tensor)
+        new = [_new(t.shape, t.dtype, m.dev, stream) for t in ([x] if one else x)]
+        out = new[0] if one else new
+    o = _Matrices(what, "out", out, like=m)
+    desc, keep = _ortho_desc(what, m.dt, math, steps, eps, coefficients)
+    workspace = _ortho_workspace(what, desc, m, workspace, stream)
+    _call(LIB.kfac_orthogonalize, "kfac_orthogonalize", m.dev, stream, desc, m.count, m.rows, m.cols,
+          m.ptr, m.ld, o.ptr, o.ld, workspace.data_ptr(), workspace.nbytes)
+    return out
+
+
+def orthogonal_step(grads, momenta, params, lr: float, momentum: float = 0.95,
+                    weight_decay: float = 0.0, nesterov: bool = True, update_scale: float = 1.0,
+                    steps: int = 5, coefficients=None, eps: float = 1e-7, math=None, workspace=None,
+                    stream=None):
+    """kfac_orthogonal_step: one optimizer step of each matrix along its orthogonalised momentum.
+    grads: as orthogonalize's x; momenta, params: float32 of the same shapes, updated in place."""
+    what = "orthogonal_step"
+    g = _Matrices(what, "grads", grads)
+    m = _Matrices(what, "momenta", momenta, torch.float32, like=g)
+    p = _Matrices(what, "params", params, torch.float32, like=g)
+    desc, keep = _ortho_desc(what, g.dt, math, steps, eps, coefficients)
+    hp = ORTHO_STEP.pack(float(lr), float(momentum), float(weight_decay), float(update_scale),
+                         bool(nesterov))
+    workspace = _ortho_workspace(what, desc, g, workspace, stream)
+    _call(LIB.kfac_orthogonal_step, "kfac_orthogonal_step", g.dev, stream, desc, hp, g.count, g.rows,
+          g.cols, g.ptr, g.ld, m.ptr, m.ld, p.ptr, p.ld, workspace.data_ptr(), workspace.nbytes)

@@ -1196,8 +1196,11 @@ extern "C" kfac_status kfac_operator_status(int* info) {
   if (cudaDeviceSynchronize() != cudaSuccess) return KFAC_ERR_CUDA;
   DevStatus s{}, zero{};
   if (cudaMemcpyFromSymbol(&s, attn::g_op_status, sizeof(s)) != cudaSuccess) return KFAC_ERR_CUDA;
-  if (info) *info = s.code ? s.info : 0;
   if (s.code && cudaMemcpyToSymbol(attn::g_op_status, &zero, sizeof(zero)) != cudaSuccess)
     return KFAC_ERR_CUDA;
+  DevStatus o{};   // the orthogonalised updates' own word, cleared with this one
+  if (kfac_status e = ortho::take_status(&o)) return e;
+  if (!s.code) s = o;
+  if (info) *info = s.code ? s.info : 0;
   return (kfac_status)s.code;
 }

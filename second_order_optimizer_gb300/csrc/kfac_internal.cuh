@@ -309,6 +309,11 @@ constexpr size_t kPrecondScratchBudget = size_t(4) << 30;
 size_t tc_pack_bytes(int n, int64_t max_rows, bool bf16);
 size_t tc_part_floats();
 
+// the orthogonalised updates' part of kfac_operator_status: the first device error, cleared
+namespace ortho {
+kfac_status take_status(DevStatus* s);
+}
+
 // scratch sizing helpers (used by the workspace planner)
 size_t k1_scratch_floats(int n, int64_t max_rows, size_t* tickets);
 size_t k5_scratch_floats(int n_plus_o, int64_t max_rows);

@@ -81,6 +81,29 @@ def test_embedding_gradient_is_the_transpose_of_the_lookup():
     assert (R.embedding_backward(ids, dout, 6, 1.5, padding_id=1)[0][1] == 0).all()
 
 
+def test_orthogonalize_is_the_newton_schulz_iteration():
+    rng = np.random.default_rng(4)
+    for shape in ((5, 9), (9, 5), (6, 6), (1, 7)):
+        x = rng.standard_normal(shape)
+        assert np.allclose(R.orthogonalize(x), R.newton_schulz(x), atol=1e-10)
+        t = np.linalg.svd(R.orthogonalize(x), compute_uv=False)
+        assert t.max() < 1.21 and np.allclose(R.orthogonalize(x), R.orthogonalize(5 * x), atol=1e-6)
+    # the classic coefficients converge to the orthogonal factor itself
+    x = rng.standard_normal((4, 8))
+    u, _, vt = np.linalg.svd(x, full_matrices=False)
+    assert np.allclose(R.orthogonalize(x, 30, (1.5, -0.5, 0.0)), u @ vt)
+    assert (R.orthogonalize(np.zeros((3, 4))) == 0).all()
+
+
+def test_orthogonal_step_by_hand():
+    """One singular value: the direction is a multiple of the update."""
+    g, m, w = np.array([[3.0, 4.0]]), np.array([[1.0, 0.0]]), np.array([[1.0, 2.0]])
+    m1, w1 = R.orthogonal_step(g, m, w, 0.1, momentum=0.5, weight_decay=0.2, nesterov=False, steps=1,
+                               coefficients=(2.0, -1.0, 0.0), eps=0.0)
+    assert np.allclose(m1, [[3.5, 4.0]])                     # of norm t: 2 t - t^3 at t = 1 is 1
+    assert np.allclose(w1, w - 0.1 * (m1 / np.sqrt(28.25) + 0.2 * w))
+
+
 # ------------------------------------------------------------- refusals (nothing is launched)
 
 @pytest.fixture(scope="module")
@@ -207,3 +230,73 @@ def test_python_refuses_cpu_tensors_and_wrong_types(lib):
         K.rms_norm(x.half())
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         K.embedding(torch.zeros(3, dtype=torch.int64), x.double())
+
+
+def _ortho(lib, rows=(8, 4), cols=(4, 4), x=None, ldx=(4, 4), out=None, ldo=(4, 4), ws=P, nb=1 << 30,
+           coefficients=None, hp=None, m=None, step=False, count=None, **kw):
+    d = dict(dtype=1, math=1, steps=5, eps=1e-7)
+    d.update(kw)
+    co = None if coefficients is None else (ctypes.c_double * len(coefficients))(*coefficients)
+    desc = lib.ORTHO_DESC.pack(*d.values(), 0 if co is None else ctypes.addressof(co))
+    n = len(rows)
+    ints = lambda v: (ctypes.c_int * n)(*v)
+    ptrs = lambda v, e: (ctypes.c_void_p * n)(*(v or (e,) * n))
+    i64 = lambda v: (ctypes.c_int64 * n)(*v)
+    count = n if count is None else count
+    if step:
+        hp = dict(lr=0.1, momentum=0.9, decay=0.0, scale=1.0, nesterov=1, **{}) | (hp or {})
+        return lib.LIB.kfac_orthogonal_step(desc, lib.ORTHO_STEP.pack(*hp.values()), count, ints(rows),
+                                            ints(cols), ptrs(x, P), i64(ldx), ptrs(m, 2 * P), i64(ldx),
+                                            ptrs(out, 3 * P), i64(ldo), ws, nb, None)
+    return lib.LIB.kfac_orthogonalize(desc, count, ints(rows), ints(cols), ptrs(x, P), i64(ldx),
+                                      ptrs(out, 3 * P), i64(ldo), ws, nb, None)
+
+
+@pytest.mark.parametrize("step", [False, True])
+@pytest.mark.parametrize("kw", [
+    dict(dtype=2), dict(math=2), dict(steps=0), dict(steps=33), dict(eps=-1.0), dict(eps=float("nan")),
+    dict(rows=(8, -1)), dict(cols=(-4, 4)), dict(count=-1), dict(x=(P, None)), dict(x=(P + 1, P)),
+    dict(out=(None, P)), dict(out=(P, P + 1)), dict(ldx=(3, 4)), dict(ldo=(4, -4)),
+    dict(steps=1, coefficients=(float("nan"), 0, 0)), dict(steps=1, coefficients=(0.0, 0.0, 0.0)),
+    dict(steps=2, coefficients=(1e5, 0, 0, 1e5, 0, 0)), dict(steps=1, coefficients=(1e9, 0, 0))])
+def test_orthogonalize_refuses(lib, kw, step):
+    assert _ortho(lib, step=step, **kw) == A
+
+
+def test_orthogonal_step_refuses(lib):
+    bad = [dict(lr=float("nan")), dict(momentum=float("inf")), dict(decay=float("nan")),
+           dict(scale=float("inf")), dict(nesterov=2)]
+    assert [_ortho(lib, step=True, hp=h) for h in bad] == [A] * len(bad)
+    assert _ortho(lib, step=True, m=(P, None)) == A and _ortho(lib, step=True, m=(P, P + 2)) == A
+
+
+def test_orthogonalize_limits_and_workspace(lib):
+    assert _ortho(lib, count=0) == 0 and _ortho(lib, step=True, count=0) == 0
+    assert _ortho(lib, rows=(0, 5), cols=(3, 0), x=(None, None), ws=None) == 0   # nothing to do
+    assert _ortho(lib, rows=(32769, 4)) == U
+    assert [_ortho(lib, ws=None), _ortho(lib, ws=P + 128), _ortho(lib, nb=512)] == [W] * 3
+    n = ctypes.c_size_t(0)
+    one = (ctypes.c_int * 1)
+    size = lambda math, r, c: (lib.LIB.kfac_orthogonalize_workspace_size(
+        lib.ORTHO_DESC.pack(1, math, 5, 0.0, 0), 1, one(r), one(c), ctypes.byref(n)), n.value)
+    assert size(1, 100, 300)[0] == 0 and size(1, 100, 300)[1] % 256 == 0
+    assert size(1, 100, 300)[1] >= 4 * 100 * 300 + 4 * 100 * 100
+    assert size(0, 100, 300)[1] >= 2 * (4 * 100 * 300 + 4 * 100 * 100)
+    assert size(1, 0, 300) == (0, 0)
+    assert lib.LIB.kfac_orthogonalize_workspace_size(lib.ORTHO_DESC.pack(1, 0, 5, 0.0, 0), 1, one(1),
+                                                     one(1), None) == A
+
+
+def test_python_refuses_matrices_that_do_not_fit(lib):
+    torch = pytest.importorskip("torch")
+    import second_order_optimizer_gb300 as K
+    x = torch.zeros(4, 6)
+    with pytest.raises(ValueError, match="CUDA"):
+        K.orthogonalize(x)
+    with pytest.raises(ValueError, match="rows, columns"):
+        K.orthogonalize(x[0])
+    from second_order_optimizer_gb300 import _params
+    with pytest.raises(ValueError, match="triple"):
+        _params._ortho_desc("orthogonalize", 0, None, 3, 0.0, [(1, 2, 3), (1, 2, 3)])
+    desc, flat = _params._ortho_desc("orthogonalize", 0, None, 2, 0.0, (1.5, -0.5, 0))
+    assert list(flat) == [1.5, -0.5, 0, 1.5, -0.5, 0]
