@@ -17,10 +17,21 @@ from ._lib import (LIB, KFAC_BF16, KFAC_ORTHO_FULL, KFAC_ORTHO_HALF, NORM_DESC, 
                    EMBEDDING_DESC, ORTHO_DESC, ORTHO_STEP)
 
 
+_cuda = {}   # devices by index: making one costs as much as two checks
+
+
 def _new(shape, dtype, dev, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+        device = _cuda.get(dev)
+        if device is None:
+            device = _cuda[dev] = torch.device("cuda", dev)
+        return torch.empty(shape, dtype=dtype, device=device)
     return _empty(shape, dtype, dev, stream)
+
+
+def _like(t, shape, dtype, dev, stream):
+    """A contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if stream is None and t.is_contiguous() else _new(shape, dtype, dev, stream)
 
 
 def _sized(f, what, dev, *args):
@@ -49,16 +60,15 @@ def _workspace(what, workspace, nbytes, dev, stream):
 
 # ------------------------------------------------------------------------------------- norms
 
-def _rows(what, name, t, shape, dtype, dev):
-    """(rows, cols, leading dimension) of t [..., cols]: contiguous, or 2-D with contiguous rows."""
+def _ld(what, name, t, shape, dtype, dev):
+    """Leading dimension of t [..., cols]: contiguous, or 2-D with contiguous rows."""
+    if t.shape == shape and t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return shape[-1]
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{what}: {name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
     if t.get_device() != dev:
         _elsewhere(what, name, t, dev)
-    cols = shape[-1]
-    if t.is_contiguous():
-        return cols
-    if t.dim() != 2 or (t.stride(1) != 1 and cols > 1):
+    if t.dim() != 2 or (t.stride(1) != 1 and shape[1] > 1):
         raise ValueError(f"{what}: {name} is contiguous, or 2-D with contiguous rows")
     return t.stride(0)
 
@@ -74,37 +84,22 @@ def _vector(what, name, t, n, dev):
     return t.data_ptr()
 
 
-def _norm(what, x, gain, residual, eps, out, residual_out, rstd, q, scales, group, stream):
-    dt, dev = _dtype(x, what), _device(x, what)
-    if x.dim() < 1:
-        raise ValueError(f"{what}: x is [..., channels]")
-    shape, dtype = x.shape, x.dtype
+def _statistics(what, name, t, shape, dev):
+    """Address of a contiguous float32 tensor of this shape."""
+    if t.dtype is not torch.float32 or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} is float32 {tuple(shape)}, contiguous")
+    if t.get_device() != dev:
+        _elsewhere(what, name, t, dev)
+    return t.data_ptr()
+
+
+def _channels(what, name, t):
+    """(kfac_dtype, device, shape, rows, channels) of t [..., channels]."""
+    dt, dev, shape = _dtype(t, what), _device(t, what), t.shape
+    if not shape:
+        raise ValueError(f"{what}: {name} is [..., channels]")
     cols = shape[-1]
-    rows = x.numel() // cols if cols else 0
-    ldx = _rows(what, "x", x, shape, dtype, dev)
-    ldr = ldh = ldy = ldq = 0
-    if residual is not None:
-        ldr = _rows(what, "residual", residual, shape, dtype, dev)
-        if residual_out is None:
-            residual_out = _new(shape, dtype, dev, stream)
-    if residual_out is not None:
-        ldh = _rows(what, "residual_out", residual_out, shape, dtype, dev)
-    if out is not None:
-        ldy = _rows(what, "out", out, shape, dtype, dev)
-    if q is not None:
-        ldq = _rows(what, "out", q, shape, torch.float8_e4m3fn, dev)
-    if rstd is None:
-        rstd = _new(shape[:-1], torch.float32, dev, stream)
-    elif rstd.dtype is not torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
-        raise ValueError(f"{what}: rstd is float32 {tuple(shape[:-1])}, contiguous")
-    elif rstd.get_device() != dev:
-        _elsewhere(what, "rstd", rstd, dev)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    _call(LIB.kfac_rms_norm, "kfac_rms_norm", dev, stream,
-          NORM_DESC.pack(dt, rows, cols, float(eps), ldx, ldr, ldh, ldy, ldq, group), x.data_ptr(),
-          ptr(residual), _vector(what, "gain", gain, cols, dev), ptr(residual_out), ptr(out),
-          rstd.data_ptr(), ptr(q), ptr(scales))
-    return residual_out, rstd
+    return dt, dev, shape, t.numel() // cols if cols else 0, cols
 
 
 def rms_norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, residual_out=None,
@@ -113,11 +108,31 @@ def rms_norm(x, gain=None, residual=None, eps: float = 1e-6, out=None, residual_
     returns (out, residual_out, rstd).  x: [..., channels], contiguous, or 2-D with contiguous
     rows.  residual_out = x + residual (None without a residual); it may be x or residual.  The
     backward pass takes it (x without a residual) and rstd, float32 [...]."""
-    _dtype(x, "rms_norm")
+    what = "rms_norm"
+    dt, dev, shape, rows, cols = _channels(what, "x", x)
+    dtype = x.dtype
+    ldx = _ld(what, "x", x, shape, dtype, dev)
+    ldr = ldh = 0
+    rp = hp = None
+    if residual is not None:
+        ldr, rp = _ld(what, "residual", residual, shape, dtype, dev), residual.data_ptr()
+        if residual_out is None:
+            residual_out, ldh = _like(x, shape, dtype, dev, stream), cols
+            hp = residual_out.data_ptr()
+    if residual_out is not None and hp is None:
+        ldh, hp = _ld(what, "residual_out", residual_out, shape, dtype, dev), residual_out.data_ptr()
     if out is None:
-        out = _new(x.shape, x.dtype, _device(x, "rms_norm"), stream)
-    residual_out, rstd = _norm("rms_norm", x, gain, residual, eps, out, residual_out, rstd, None,
-                               None, 0, stream)
+        out, ldy = _like(x, shape, dtype, dev, stream), cols
+    else:
+        ldy = _ld(what, "out", out, shape, dtype, dev)
+    if rstd is None:
+        rstd = _new(shape[:-1], torch.float32, dev, stream)
+        sp = rstd.data_ptr()
+    else:
+        sp = _statistics(what, "rstd", rstd, shape[:-1], dev)
+    _call(LIB.kfac_rms_norm, "kfac_rms_norm", dev, stream,
+          NORM_DESC.pack(dt, rows, cols, eps, ldx, ldr, ldh, ldy, 0, 0), x.data_ptr(), rp,
+          _vector(what, "gain", gain, cols, dev), hp, out.data_ptr(), sp, None, None)
     return out, residual_out, rstd
 
 
@@ -127,23 +142,32 @@ def rms_norm_e4m3(x, gain=None, residual=None, eps: float = 1e-6, group: int = 0
     residual_out); out * scale of its group is the norm.  group: 32, 64 or 128 channels per scale, or
     0 for one per row."""
     what = "rms_norm_e4m3"
-    dev = _device(x, what)
-    if x.dim() < 1:
-        raise ValueError(f"{what}: x is [..., channels]")
+    dt, dev, shape, rows, cols = _channels(what, "x", x)
+    dtype = x.dtype
     if group not in (0, 32, 64, 128):
         raise ValueError(f"{what}: group is 32, 64 or 128 channels, or 0 for the whole row")
+    ldx = _ld(what, "x", x, shape, dtype, dev)
+    ldr = ldh = 0
+    rp = hp = None
+    if residual is not None:
+        ldr, rp = _ld(what, "residual", residual, shape, dtype, dev), residual.data_ptr()
+        if residual_out is None:
+            residual_out = _new(shape, dtype, dev, stream)
+    if residual_out is not None:
+        ldh, hp = _ld(what, "residual_out", residual_out, shape, dtype, dev), residual_out.data_ptr()
     if out is None:
-        out = _new(x.shape, torch.float8_e4m3fn, dev, stream)
-    groups = -(-x.shape[-1] // group) if group else 1
+        out, ldq = _new(shape, torch.float8_e4m3fn, dev, stream), cols
+    else:
+        ldq = _ld(what, "out", out, shape, torch.float8_e4m3fn, dev)
+    groups = (*shape[:-1], -(-cols // group) if group else 1)
     if scales is None:
-        scales = _new((*x.shape[:-1], groups), torch.float32, dev, stream)
-    elif scales.dtype is not torch.float32 or scales.shape != (*x.shape[:-1], groups) or (
-            not scales.is_contiguous()):
-        raise ValueError(f"{what}: scales is float32 {(*x.shape[:-1], groups)}, contiguous")
-    elif scales.get_device() != dev:
-        _elsewhere(what, "scales", scales, dev)
-    residual_out, _ = _norm(what, x, gain, residual, eps, None, residual_out, None, out, scales,
-                            group, stream)
+        scales = _new(groups, torch.float32, dev, stream)
+        sp = scales.data_ptr()
+    else:
+        sp = _statistics(what, "scales", scales, groups, dev)
+    _call(LIB.kfac_rms_norm, "kfac_rms_norm", dev, stream,
+          NORM_DESC.pack(dt, rows, cols, eps, ldx, ldr, ldh, 0, ldq, group), x.data_ptr(), rp,
+          _vector(what, "gain", gain, cols, dev), hp, None, None, out.data_ptr(), sp)
     return out, scales, residual_out
 
 
@@ -163,33 +187,30 @@ def rms_norm_backward(dout, x, gain, rstd, dresidual=None, dx=None, dgain=None, 
     (square=True, or a tensor given): the mean over the rows of the gain's squared gradient, which
     Kfac.diag_step takes as g_new; otherwise None."""
     what = "rms_norm_backward"
-    dt, dev = _dtype(dout, what), _device(dout, what)
-    if dout.dim() < 1:
-        raise ValueError(f"{what}: dout is [..., channels]")
-    shape, dtype = dout.shape, dout.dtype
-    cols = shape[-1]
-    rows = dout.numel() // cols if cols else 0
-    lddy = _rows(what, "dout", dout, shape, dtype, dev)
-    ldh = _rows(what, "x", x, shape, dtype, dev)
-    lddh = _rows(what, "dresidual", dresidual, shape, dtype, dev) if dresidual is not None else 0
-    if rstd.dtype is not torch.float32 or rstd.shape != shape[:-1] or not rstd.is_contiguous():
-        raise ValueError(f"{what}: rstd is float32 {tuple(shape[:-1])}, contiguous")
-    if rstd.get_device() != dev:
-        _elsewhere(what, "rstd", rstd, dev)
+    dt, dev, shape, rows, cols = _channels(what, "dout", dout)
+    dtype = dout.dtype
+    lddy = _ld(what, "dout", dout, shape, dtype, dev)
+    ldh = _ld(what, "x", x, shape, dtype, dev)
+    lddh, dhp = 0, None
+    if dresidual is not None:
+        lddh, dhp = _ld(what, "dresidual", dresidual, shape, dtype, dev), dresidual.data_ptr()
+    sp = _statistics(what, "rstd", rstd, shape[:-1], dev)
     if dx is None:
-        dx = _new(shape, dtype, dev, stream)
-    lddx = _rows(what, "dx", dx, shape, dtype, dev)
+        dx, lddx = _like(dout, shape, dtype, dev, stream), cols
+    else:
+        lddx = _ld(what, "dx", dx, shape, dtype, dev)
     if dgain is None:
         dgain = _new((cols,), torch.float32, dev, stream)
+        gp = dgain.data_ptr()
+    else:
+        gp = _vector(what, "dgain", dgain, cols, dev)
     if dgain_square is None and square:
         dgain_square = _new((cols,), torch.float32, dev, stream)
     workspace = _workspace(what, workspace, 0 if workspace is not None else _sized(
         LIB.kfac_rms_norm_workspace_size, "kfac_rms_norm_workspace_size", dev, rows, cols), dev, stream)
     _call(LIB.kfac_rms_norm_backward, "kfac_rms_norm_backward", dev, stream,
           NORM_GRAD_DESC.pack(dt, rows, cols, lddy, ldh, lddh, lddx), dout.data_ptr(), x.data_ptr(),
-          _vector(what, "gain", gain, cols, dev), rstd.data_ptr(),
-          None if dresidual is None else dresidual.data_ptr(), dx.data_ptr(),
-          _vector(what, "dgain", dgain, cols, dev),
+          _vector(what, "gain", gain, cols, dev), sp, dhp, dx.data_ptr(), gp,
           _vector(what, "dgain_square", dgain_square, cols, dev), workspace.data_ptr(),
           workspace.nbytes)
     return dx, dgain, dgain_square
@@ -218,11 +239,12 @@ def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
     if table.dim() != 2:
         raise ValueError(f"{what}: table is [rows, width]")
     rows, width = table.shape
-    ldt = _rows(what, "table", table, table.shape, table.dtype, dev)
+    ldt = _ld(what, "table", table, table.shape, table.dtype, dev)
     shape = (*ids.shape, width)
     if out is None:
-        out = _new(shape, table.dtype, dev, stream)
-    ldo = _rows(what, "out", out, shape, table.dtype, dev)
+        out, ldo = _new(shape, table.dtype, dev, stream), width
+    else:
+        ldo = _ld(what, "out", out, shape, table.dtype, dev)
     _call(LIB.kfac_embedding, "kfac_embedding", dev, stream,
           EMBEDDING_DESC.pack(dt, bits, ids.numel(), rows, width, float(scale), ldt, ldo),
           ids.data_ptr(), table.data_ptr(), out.data_ptr())
@@ -249,12 +271,12 @@ def embedding_backward(ids, dout, rows: int, scale: float = 1.0, padding_id: int
     if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
         raise ValueError(f"{what}: dout is [..., width] for ids [...], not {tuple(dout.shape)}")
     width, tokens = dout.shape[-1], ids.numel()
-    ldo = _rows(what, "dout", dout, dout.shape, dout.dtype, dev)
+    ldo = _ld(what, "dout", dout, dout.shape, dout.dtype, dev)
     if out is None:
         if accumulate:
             raise ValueError(f"{what}: accumulate adds to a given out")
         out = _new((rows, width), torch.float32, dev, stream)
-    ldt = _rows(what, "out", out, (rows, width), torch.float32, dev)
+    ldt = _ld(what, "out", out, (rows, width), torch.float32, dev)
     workspace = _workspace(what, workspace, 0 if workspace is not None else _sized(
         LIB.kfac_embedding_workspace_size, "kfac_embedding_workspace_size", dev, tokens, rows, width),
         dev, stream)

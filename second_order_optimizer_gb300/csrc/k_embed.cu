@@ -4,16 +4,17 @@
 // Both are bound by memory: the forward pass reads and writes a row per token, the gradient
 // reads dout once and writes the whole table (the larger part for a large vocabulary).
 // The gradient needs the tokens of each row together.  They are sorted by id with a stable
-// radix sort (8 bits a pass, ranks from warp matches), so that every row is summed in the order
-// of its tokens: no atomics, the same inputs give the same bits.  Up to 16384 tokens one block
-// sorts in shared memory; beyond that, histogram, scan and scatter launches per pass.
-// A row's run in the sorted order is found through start[v], which only rows with tokens have:
-// start[v] counts only if the sorted key there is v and the one before it is not, so that the
-// array needs no clearing.
-// Text has hot ids (padding, articles): runs longer than a chunk of the sorted order are summed
-// chunk by chunk first, by blocks of their own, and their row adds the chunks' sums in order.
+// radix sort (8 bits a pass, ranks from warp ballots), so that every row is summed in the order
+// of its tokens: no atomics, the same inputs give the same bits.  Up to 16384 tokens a cluster of
+// eight blocks sorts through distributed shared memory while the launch's other blocks clear
+// the table (one block alone took 42 us for 16384 tokens); beyond that, histogram, scan and scatter
+// launches per pass.
+// Text has hot ids (padding, articles), so the sums are divided by tokens, not by rows: a chunk of
+// the sorted order per block, each run inside it to its row; a second launch joins the parts of
+// runs that cross chunks, in order.
 #include "kfac_internal.cuh"
 #include "per_device.h"
+#include "tc_prims.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -22,8 +23,8 @@ namespace kfac {
 namespace {
 
 constexpr int64_t kMaxIds = (int64_t(1) << 31) - 2;
-constexpr int kSmallTokens = 16384;    // sorted by one block
-constexpr int kSortThreads = 1024;
+constexpr int kSmallTokens = 16384;    // sorted by one cluster
+constexpr int kCluster = 8, kSortThreads = 512;
 constexpr int kTileThreads = 256, kTileItems = 4096;   // of the launches per pass beyond that
 constexpr int kBits = 8, kDigits = 1 << kBits;
 
@@ -95,59 +96,75 @@ __global__ void __launch_bounds__(256) embedding_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------------------- sorting
 
-// Rank of this lane's digit among the equal ones of the warp's items so far, in order:
-// counts[d] is the warp's count of digit d before these 32 items and after them, `valid` lanes
-// only.
-__device__ __forceinline__ uint32_t warp_rank(uint32_t digit, bool valid, uint16_t* counts) {
-  const uint32_t peers = __match_any_sync(0xffffffffu, valid ? digit : 0xffffffffu);
+// The warps' counts of each digit, a row per digit (padded: the rows of 32 digits start on
+// different banks).
+template <int WARPS> struct DigitCounts {
+  uint16_t n[kDigits][WARPS + 2];
+  uint32_t scan[kDigits];
+  uint32_t warps[32];
+};
+
+// Rank of this lane's digit among the equal ones of the warp's items so far, in order; `valid`
+// lanes only.  The lanes with an equal digit are found bit by bit (eight ballots; a match
+// instruction took several times as long).
+template <int WARPS>
+__device__ __forceinline__ uint32_t warp_rank(uint32_t digit, bool valid, DigitCounts<WARPS>& c) {
+  uint32_t peers = __ballot_sync(0xffffffffu, valid);
+#pragma unroll
+  for (int b = 0; b < kBits; ++b) {
+    const bool one = digit >> b & 1;
+    const uint32_t ones = __ballot_sync(0xffffffffu, one);
+    peers &= one ? ones : ~ones;
+  }
   const uint32_t below = peers & ((1u << (threadIdx.x % 32)) - 1);
-  const uint32_t before = valid ? counts[digit] : 0;
+  uint16_t* at = &c.n[digit][threadIdx.x / 32];
+  const uint32_t before = *at;
   __syncwarp();
-  if (valid && below == 0) counts[digit] = (uint16_t)(before + __popc(peers));
+  if (valid && below == 0) *at = (uint16_t)(before + __popc(peers));
   __syncwarp();
   return before + __popc(below);
 }
 
-// Turns the warps' digit counts into each warp's first position of each digit, counted from the
-// digits before it in the block; `base` (or null) is added per digit.  Threads >= kDigits.
+// Turns the warps' digit counts into each warp's first position within the digit, and scan[d] into
+// the digit's first position: after the smaller digits of the block, or base[d] (not null).  All
+// threads, a power of two of warps.
 template <int WARPS>
-__device__ __forceinline__ void digit_starts(uint16_t (*counts)[kDigits], uint32_t* scan,
-                                             const uint32_t* base) {
+__device__ __forceinline__ void digit_starts(DigitCounts<WARPS>& c, const uint32_t* base) {
   __syncthreads();
-  const int d = threadIdx.x;
-  uint32_t mine = 0;
-  if (d < kDigits)
-    for (int w = 0; w < WARPS; ++w) mine += counts[w][d];
-  // exclusive scan over the digits
-  if (d < kDigits) scan[d] = mine;
-  __syncthreads();
-  if (d < 32) {
-    uint32_t v[kDigits / 32], sum = 0;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int PER = 32 / WARPS;          // digits that a warp scans at once, WARPS lanes each
+  for (int d0 = warp * (kDigits / WARPS); d0 < (warp + 1) * (kDigits / WARPS); d0 += PER) {
+    const int d = d0 + lane / WARPS, w = lane % WARPS;
+    const uint32_t v = c.n[d][w];
+    uint32_t incl = v;
 #pragma unroll
-    for (int i = 0; i < kDigits / 32; ++i) {
-      v[i] = sum;
-      sum += scan[d * (kDigits / 32) + i];
+    for (int o = 1; o < WARPS; o <<= 1) {
+      const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (w >= o) incl += up;
     }
-    uint32_t incl = sum;
+    c.n[d][w] = (uint16_t)(incl - v);
+    if (w == WARPS - 1) c.scan[d] = incl;
+  }
+  __syncthreads();
+  if (base) {
+    if (threadIdx.x < kDigits) c.scan[threadIdx.x] = base[threadIdx.x];
+  } else if (warp < kDigits / 32) {        // exclusive scan over the digits
+    const uint32_t v = c.scan[threadIdx.x];
+    uint32_t incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (d >= o) incl += up;
+      if (lane >= o) incl += up;
     }
-#pragma unroll
-    for (int i = 0; i < kDigits / 32; ++i) scan[d * (kDigits / 32) + i] = v[i] + incl - sum;
+    c.scan[threadIdx.x] = incl - v;
+    if (lane == 31) c.warps[warp] = incl;
   }
   __syncthreads();
-  if (d < kDigits) {
-    if (base) scan[d] = base[d];
-    uint32_t at = 0;
-    for (int w = 0; w < WARPS; ++w) {   // within the digit
-      const uint32_t n = counts[w][d];
-      counts[w][d] = (uint16_t)at;
-      at += n;
-    }
+  if (!base) {
+    if (threadIdx.x < kDigits)
+      for (int w = 0; w < warp; ++w) c.scan[threadIdx.x] += c.warps[w];
+    __syncthreads();
   }
-  __syncthreads();
 }
 
 // start[v], end[v] from neighbouring keys.
@@ -158,66 +175,143 @@ __device__ __forceinline__ void mark_run(const EmbedArgs& a, int64_t i, uint32_t
   if (i == a.tokens - 1 || after != key) a.end[key] = (uint32_t)i + 1;
 }
 
-// Up to kSmallTokens tokens.  Warp w takes items [w I, (w + 1) I) of every pass, 32 at a time.
-struct SmallSort {
-  uint32_t keys[kSmallTokens];
-  uint32_t vals[kSmallTokens];
-  uint16_t counts[kSortThreads / 32][kDigits];
-  uint32_t scan[kDigits];
-};
-__global__ void __launch_bounds__(kSortThreads) sort_small_kernel(const __grid_constant__ EmbedArgs a) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  SmallSort& s = *reinterpret_cast<SmallSort*>(raw);
-  constexpr int WARPS = kSortThreads / 32, ROUNDS = kSmallTokens / kSortThreads;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int n = (int)a.tokens;
-  const int rounds = (int)((n + kSortThreads - 1) / kSortThreads);
+// Clears the table (unless the gradient is added to it) and the frequencies: block `block` of
+// `blocks`, `threads` threads each.
+__device__ __forceinline__ void clear_table(const EmbedArgs& a, int64_t block, int64_t blocks, int threads) {
+  const int64_t first = block * threads + threadIdx.x, step = blocks * threads;
+  if (!a.accumulate) {
+    const int64_t n = a.rows * a.width;
+    if (a.ld_out == a.width || a.rows == 1) {
+      const int64_t head = min(n, (int64_t)((16 - (uintptr_t)a.dtable % 16) % 16 / 4));
+      float4* body = reinterpret_cast<float4*>(a.dtable + head);
+      const int64_t vecs = (n - head) / 4;
+      for (int64_t i = first; i < vecs; i += step) body[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (first < head) a.dtable[first] = 0.f;
+      if (first < n - head - vecs * 4) a.dtable[head + vecs * 4 + first] = 0.f;
+    } else {
+      for (int64_t row = block; row < a.rows; row += blocks)
+        for (int64_t c = threadIdx.x; c < a.width; c += threads) a.dtable[row * a.ld_out + c] = 0.f;
+    }
+  }
+  if (a.frequency)
+    for (int64_t i = first; i < a.rows; i += step) a.frequency[i] = 0.f;
+}
+__global__ void __launch_bounds__(kSortThreads) clear_kernel(const __grid_constant__ EmbedArgs a) {
   pdl_wait();
   pdl_trigger();
+  clear_table(a, blockIdx.x, gridDim.x, kSortThreads);
+}
+
+// Up to kSmallTokens tokens by the first cluster: block b holds items [b I, (b + 1) I) in every
+// pass, its warp w 32 at a time from w I / 16 on.  The other clusters clear the table.
+struct SmallSort {
+  uint32_t keys[kSmallTokens / kCluster];
+  uint32_t vals[kSmallTokens / kCluster];
+  DigitCounts<kSortThreads / 32> counts;
+  uint32_t total[kDigits], base[kDigits];
+};
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
+    sort_small_kernel(const __grid_constant__ EmbedArgs a) {
+  __shared__ SmallSort s;
+  constexpr int ROUNDS = kSmallTokens / kCluster / kSortThreads;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x >= kCluster) {
+    clear_table(a, blockIdx.x - kCluster, gridDim.x - kCluster, kSortThreads);
+    return;
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank_in = tc::cluster_rank();
+  const int n = (int)a.tokens;
+  const int rounds = (n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads);
+  const int items = rounds * kSortThreads;          // of a block
+  const int base_item = (int)rank_in * items;
+  auto local = [&](int r) { return (warp * rounds + r) * 32 + lane; };
   uint32_t key[ROUNDS], val[ROUNDS], rank[ROUNDS];
-  auto item = [&](int r) { return (warp * rounds + r) * 32 + lane; };
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r) {
     if (r < rounds) {
-      const int i = item(r);
+      const int i = base_item + local(r);
       key[r] = i < n ? key_at(a, i) : 0;
       val[r] = (uint32_t)i;
     }
   }
   for (int pass = 0; pass < a.passes; ++pass) {
-    for (int i = threadIdx.x; i < WARPS * kDigits; i += kSortThreads) s.counts[0][i] = 0;
+    for (int i = threadIdx.x; i < kDigits * (kSortThreads / 32 + 2); i += kSortThreads)
+      s.counts.n[0][i] = 0;
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < ROUNDS; ++r)
       if (r < rounds)
-        rank[r] = warp_rank((key[r] >> (kBits * pass)) % kDigits, item(r) < n, s.counts[warp]);
-    digit_starts<WARPS>(s.counts, s.scan, nullptr);
+        rank[r] = warp_rank((key[r] >> (kBits * pass)) % kDigits, base_item + local(r) < n, s.counts);
+    digit_starts(s.counts, nullptr);
+    // every block's totals: the digits before this one, and this digit's in the blocks before
+    const int d = threadIdx.x;
+    if (d < kDigits)
+      s.total[d] = (d + 1 < kDigits ? s.counts.scan[d + 1] : (uint32_t)max(0, min(items, n - base_item))) -
+                   s.counts.scan[d];
+    tc::cluster_sync();
+    uint32_t before = 0, all = 0;
+    if (d < kDigits) {
 #pragma unroll
-    for (int r = 0; r < ROUNDS; ++r) {
-      if (r < rounds && item(r) < n) {
-        const uint32_t d = (key[r] >> (kBits * pass)) % kDigits;
-        const uint32_t at = s.scan[d] + s.counts[warp][d] + rank[r];
-        s.keys[at] = key[r];
-        s.vals[at] = val[r];
+      for (uint32_t c = 0; c < kCluster; ++c) {
+        const uint32_t v = ld_cluster_u32(tc::mapa(&s.total[d], c));
+        before += c < rank_in ? v : 0;
+        all += v;
       }
+      uint32_t incl = all;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      s.base[d] = incl - all + before;
+      if (lane == 31) s.counts.warps[warp] = incl;
     }
     __syncthreads();
+    if (d < kDigits)
+      for (int w = 0; w < warp; ++w) s.base[d] += s.counts.warps[w];
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < ROUNDS; ++r) {
+      if (r < rounds && base_item + local(r) < n) {
+        const uint32_t g = (key[r] >> (kBits * pass)) % kDigits;
+        const uint32_t at = s.base[g] + s.counts.n[g][warp] + rank[r];
+        const uint32_t to = at / (uint32_t)items, off = at - to * (uint32_t)items;
+        tc::st_cluster_u32(tc::mapa(&s.keys[off], to), key[r]);
+        tc::st_cluster_u32(tc::mapa(&s.vals[off], to), val[r]);
+      }
+    }
+    tc::cluster_sync();
     if (pass + 1 < a.passes) {
 #pragma unroll
       for (int r = 0; r < ROUNDS; ++r) {
-        if (r < rounds && item(r) < n) {
-          key[r] = s.keys[item(r)];
-          val[r] = s.vals[item(r)];
+        if (r < rounds && base_item + local(r) < n) {
+          key[r] = s.keys[local(r)];
+          val[r] = s.vals[local(r)];
         }
       }
     }
   }
-  for (int i = threadIdx.x; i < n; i += kSortThreads) {
-    const uint32_t k = s.keys[i];
+  for (int j = threadIdx.x; j < items && base_item + j < n; j += kSortThreads) {
+    const int i = base_item + j;
+    auto neighbour = [&](int k) -> uint32_t {      // the key at item k, of this block or the next one
+      if (k < 0 || k >= n) return 0;
+      const int b = k / items;
+      return ld_cluster_u32(tc::mapa(&s.keys[k - b * items], (uint32_t)b));
+    };
+    const uint32_t k = s.keys[j];
     a.keys[i] = k;
-    a.vals[i] = s.vals[i];
-    mark_run(a, i, k, i > 0 ? s.keys[i - 1] : 0, i + 1 < n ? s.keys[i + 1] : 0);
+    a.vals[i] = s.vals[j];
+    mark_run(a, i, k, j > 0 ? s.keys[j - 1] : neighbour(i - 1),
+             j + 1 < items && i + 1 < n ? s.keys[j + 1] : neighbour(i + 1));
   }
+  tc::cluster_sync();   // no block's shared memory goes while another reads it
 }
 
 // A tile's counts of each digit.
@@ -271,17 +365,17 @@ __global__ void __launch_bounds__(kTileThreads)
     sort_scatter_kernel(const __grid_constant__ EmbedArgs a, const uint32_t* keys, const uint32_t* vals,
                         uint32_t* keys_out, uint32_t* vals_out, int pass) {
   constexpr int WARPS = kTileThreads / 32, ROUNDS = kTileItems / kTileThreads;
-  __shared__ uint16_t counts[WARPS][kDigits];
-  __shared__ uint32_t scan[kDigits], base[kDigits];
+  __shared__ DigitCounts<WARPS> counts;
+  __shared__ uint32_t base[kDigits];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   pdl_wait();
   pdl_trigger();
-  for (int i = threadIdx.x; i < WARPS * kDigits; i += kTileThreads) counts[0][i] = 0;
+  for (int i = threadIdx.x; i < kDigits * (WARPS + 2); i += kTileThreads) counts.n[0][i] = 0;
   // digits before this one in the whole order, and this digit's items in the tiles before
-  scan[threadIdx.x] = a.total[threadIdx.x];
+  counts.scan[threadIdx.x] = a.total[threadIdx.x];
   __syncthreads();
   uint32_t before = 0;
-  for (int d = 0; d < (int)threadIdx.x; ++d) before += scan[d];
+  for (int d = 0; d < (int)threadIdx.x; ++d) before += counts.scan[d];
   base[threadIdx.x] = before + a.hist[(int64_t)threadIdx.x * a.tiles + blockIdx.x];
   __syncthreads();
   uint32_t key[ROUNDS], val[ROUNDS], rank[ROUNDS];
@@ -292,14 +386,14 @@ __global__ void __launch_bounds__(kTileThreads)
     const bool valid = i < a.tokens;
     key[r] = !valid ? 0 : keys ? keys[i] : key_at(a, i);
     val[r] = !valid ? 0 : vals ? vals[i] : (uint32_t)i;
-    rank[r] = warp_rank((key[r] >> (kBits * pass)) % kDigits, valid, counts[warp]);
+    rank[r] = warp_rank((key[r] >> (kBits * pass)) % kDigits, valid, counts);
   }
-  digit_starts<WARPS>(counts, scan, base);
+  digit_starts(counts, base);
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r) {
     if (first + r * 32 < a.tokens) {
       const uint32_t d = (key[r] >> (kBits * pass)) % kDigits;
-      const uint32_t at = scan[d] + counts[warp][d] + rank[r];
+      const uint32_t at = counts.scan[d] + counts.n[d][warp] + rank[r];
       keys_out[at] = key[r];
       vals_out[at] = val[r];
     }
@@ -315,114 +409,148 @@ __global__ void __launch_bounds__(256) sort_runs_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------------------- summing
 
-template <typename T, int N> struct Sum {
+template <int N> __device__ __forceinline__ void load_floats(const float* p, float (&v)[N]) {
+  if constexpr (N == 1) {
+    v[0] = __ldcg(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(&v[i]) = __ldcg(reinterpret_cast<const float4*>(p + i));
+  }
+}
+template <int N> __device__ __forceinline__ void store_floats(float* p, const float (&v)[N]) {
+  if constexpr (N == 1) {
+    p[0] = v[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      *reinterpret_cast<float4*>(p + i) = *reinterpret_cast<const float4*>(&v[i]);
+  }
+}
+// A finished sum to its row's channels from c.
+template <int N>
+__device__ __forceinline__ void store_row(const EmbedArgs& a, uint32_t row, int64_t c, const float (&sum)[N]) {
+  float* out = a.dtable + (int64_t)row * a.ld_out + c;
   float v[N];
-  __device__ __forceinline__ void clear() {
+  if (a.accumulate) load_floats<N>(out, v);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-  }
-  __device__ __forceinline__ void add(const Vec<T, N>& p) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += to_f32<T>(p.v[i]);
-  }
-};
-
-// dout rows of sorted positions [lo, hi), channels from c, in order.
-template <typename T, int N>
-__device__ __forceinline__ void sum_rows(const EmbedArgs& a, uint32_t lo, uint32_t hi, int64_t c,
-                                         Sum<T, N>& s) {
-  const T* src = static_cast<const T*>(a.src) + c;
-  uint32_t i = lo;
-  for (; i + 4 <= hi; i += 4) {
-    Vec<T, N> p[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      p[j] = *reinterpret_cast<const Vec<T, N>*>(src + (int64_t)__ldg(a.vals + i + j) * a.ld_src);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.add(p[j]);
-  }
-  for (; i < hi; ++i)
-    s.add(*reinterpret_cast<const Vec<T, N>*>(src + (int64_t)__ldg(a.vals + i) * a.ld_src));
+  for (int i = 0; i < N; ++i) v[i] = a.accumulate ? fmaf(sum[i], a.scale, v[i]) : sum[i] * a.scale;
+  store_floats<N>(out, v);
 }
 
-// A chunk's share of the runs longer than a chunk: slot 0 of the one that covers its first
-// position, slot 1 of one that begins behind it and covers its last.
+// A chunk of the sorted order per TPR threads: its tokens' rows are read whatever their ids, and
+// summed run by run.  A run inside the chunk goes to its row; the part of one that crosses into the
+// chunk before or behind goes to the workspace: slot 0 if the run began before the chunk, slot 1
+// if it begins in it.  Each thread copies what it will add itself into slots of its own in shared
+// memory, two stages of eight rows (cp.async; single bf16 elements by way of registers), so that
+// sixteen rows are in flight and no barrier orders them; with the rows in registers the code for a
+// run's end stood there eight times over, and the kernel took 40 us for 16384 x 2048 (bf16).
+constexpr int kStageRows = 8;
 template <typename T, int N, int TPR>
 __global__ void __launch_bounds__(256) embedding_chunks_kernel(const __grid_constant__ EmbedArgs a) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  using Pack = Vec<T, N>;
+  Pack* slots = reinterpret_cast<Pack*>(raw) + threadIdx.x;   // [2][kStageRows][256]
   pdl_wait();
   pdl_trigger();
-  constexpr int RPB = 256 / TPR;
+  constexpr int RPB = 256 / TPR, R = kStageRows;
   const int t = threadIdx.x % TPR;
   const int64_t chunk = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
   const int64_t lo = chunk * a.chunk;
   if (lo >= a.tokens) return;
   const int64_t hi = min(lo + a.chunk, a.tokens);
+  const uint32_t rows = (uint32_t)a.rows;
+  const uint32_t before = lo > 0 ? __ldg(a.keys + lo - 1) : 0xffffffffu;   // (no key: see kMaxIds)
+  const uint32_t after = hi < a.tokens ? __ldg(a.keys + hi) : 0xffffffffu;
+  for (int64_t c = (int64_t)t * N; c < a.width; c += TPR * N) {
+    const T* src = static_cast<const T*>(a.src) + c;
+    auto fetch = [&](int64_t i, int stage) {
 #pragma unroll
-  for (int slot = 0; slot < 2; ++slot) {
-    const uint32_t key = __ldg(a.keys + (slot ? hi - 1 : lo));
-    if (key >= (uint32_t)a.rows) continue;
-    const uint32_t start = __ldg(a.start + key), end = __ldg(a.end + key);
-    if (end - start <= (uint32_t)a.chunk || (slot && start <= (uint32_t)lo)) continue;
-    const uint32_t from = max(start, (uint32_t)lo), to = min(end, (uint32_t)hi);
-    for (int64_t c = (int64_t)t * N; c < a.width; c += TPR * N) {
-      Sum<T, N> s;
-      s.clear();
-      sum_rows<T, N>(a, from, to, c, s);
-      float* p = a.part + (chunk * 2 + slot) * a.width + c;
+      for (int j = 0; j < R; ++j) {
+        if (i + j < hi && __ldg(a.keys + i + j) < rows) {
+          const T* from = src + (int64_t)__ldg(a.vals + i + j) * a.ld_src;
+          Pack* to = slots + (stage * R + j) * 256;
+          if constexpr (sizeof(Pack) == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from)
+                         : "memory");
+          else if constexpr (sizeof(Pack) == 4)
+            tc::cp_async4(to, from);
+          else
+            *to = *reinterpret_cast<const Pack*>(from);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float sum[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) p[i] = s.v[i];
+    for (int i = 0; i < N; ++i) sum[i] = 0.f;
+    uint32_t run = __ldg(a.keys + lo);
+    int64_t begin = lo;                  // of the run, in this chunk
+    fetch(lo, 0);
+    fetch(lo + R, 1);
+    int stage = 0;
+    for (int64_t i = lo;;) {             // position i, the first behind the run included
+      const uint32_t key = i < hi ? __ldg(a.keys + i) : 0xffffffffu;
+      if (key != run) {
+        if (run < rows) {
+          const bool from_before = begin == lo && before == run, goes_on = i == hi && after == run;
+          if (from_before || goes_on) {
+            store_floats<N>(a.part + (chunk * 2 + (from_before ? 0 : 1)) * a.width + c, sum);
+          } else {
+            store_row<N>(a, run, c, sum);
+            if (c == 0 && a.frequency) a.frequency[run] = (float)(i - begin) * a.inv_tokens;
+          }
+        }
+        if (i >= hi) break;
+        run = key;
+        begin = i;
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] = 0.f;
+      }
+      const int j = (int)(i - lo) % R;
+      if (j == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+      if (run < rows) {
+        const Pack p = slots[(stage * R + j) * 256];
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum[k] += to_f32<T>(p.v[k]);
+      }
+      ++i;
+      if (j == R - 1) {
+        fetch(i + R, stage);             // the slots just read
+        stage ^= 1;
+      }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
 }
 
-// A row of the table per TPR threads.
+// The runs that cross chunks: the threads of the first border that one crosses add its parts in order.
 template <typename T, int N, int TPR>
-__global__ void __launch_bounds__(256) embedding_rows_kernel(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(256) embedding_join_kernel(const __grid_constant__ EmbedArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr int RPB = 256 / TPR;
   const int t = threadIdx.x % TPR;
-  const int64_t row = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
-  if (row >= a.rows) return;
-  uint32_t start = a.start[row], end = 0;
-  // whatever stands in start[row] where the row has no tokens, the keys do not agree with it
-  if ((int64_t)start < a.tokens && a.keys[start] == (uint32_t)row &&
-      (start == 0 || a.keys[start - 1] != (uint32_t)row))
-    end = a.end[row];
-  else
-    start = 0;
-  const uint32_t count = end - start;
-  if (t == 0 && a.frequency) a.frequency[row] = (float)count * a.inv_tokens;
-  if (count == 0 && a.accumulate) return;
-  const uint32_t c0 = start / (uint32_t)a.chunk, c1 = count ? (end - 1) / (uint32_t)a.chunk : 0;
+  const int64_t chunk = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR + 1;
+  const int64_t at = chunk * a.chunk;
+  if (at >= a.tokens) return;
+  const uint32_t run = __ldg(a.keys + at);
+  if (run >= (uint32_t)a.rows || __ldg(a.keys + at - 1) != run) return;
+  const uint32_t start = __ldg(a.start + run), end = __ldg(a.end + run);
+  if ((int64_t)start < at - a.chunk) return;         // it crossed a border before
+  if (t == 0 && a.frequency) a.frequency[run] = (float)(end - start) * a.inv_tokens;
+  const int64_t last = (end - 1) / (uint32_t)a.chunk;
   for (int64_t c = (int64_t)t * N; c < a.width; c += TPR * N) {
-    Sum<T, N> s;
-    s.clear();
-    if (count <= (uint32_t)a.chunk) {
-      sum_rows<T, N>(a, start, end, c, s);
-    } else {
-      for (uint32_t k = c0; k <= c1; ++k) {
-        const int slot = k == c0 && start != c0 * (uint32_t)a.chunk;
-        const float* p = a.part + ((int64_t)k * 2 + slot) * a.width + c;
+    float sum[N];
+    load_floats<N>(a.part + ((chunk - 1) * 2 + 1) * a.width + c, sum);
+#pragma unroll 4
+    for (int64_t k = chunk; k <= last; ++k) {
+      float v[N];
+      load_floats<N>(a.part + k * 2 * a.width + c, v);
 #pragma unroll
-        for (int i = 0; i < N; ++i) s.v[i] += p[i];
-      }
+      for (int i = 0; i < N; ++i) sum[i] += v[i];
     }
-    float* out = a.dtable + row * a.ld_out + c;
-    if constexpr (N > 1) {
-#pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        float4 o = make_float4(s.v[i] * a.scale, s.v[i + 1] * a.scale, s.v[i + 2] * a.scale,
-                               s.v[i + 3] * a.scale);
-        if (a.accumulate) {
-          const float4 old = *reinterpret_cast<const float4*>(out + i);
-          o = make_float4(o.x + old.x, o.y + old.y, o.z + old.z, o.w + old.w);
-        }
-        *reinterpret_cast<float4*>(out + i) = o;
-      }
-    } else {
-      out[0] = s.v[0] * a.scale + (a.accumulate ? out[0] : 0.f);
-    }
+    store_row<N>(a, run, c, sum);
   }
 }
 
@@ -440,23 +568,32 @@ template <typename T, int N> void launch_forward(const EmbedArgs& a, cudaStream_
   }
 }
 
-template <typename T, int N> void launch_sums(const EmbedArgs& a, cudaStream_t st) {
-  const dim3 block(256);
+template <typename T, int N, int TPR> kfac_status launch_sums_by(const EmbedArgs& a, cudaStream_t st) {
   const int64_t chunks = cdiv(a.tokens, a.chunk);
-  if (cdiv(a.width, N) <= 64) {
-    if (a.tokens > a.chunk)
-      launch_pdl(embedding_chunks_kernel<T, N, 32>, dim3((unsigned)cdiv(chunks, 8)), block, 0, st, a);
-    launch_pdl(embedding_rows_kernel<T, N, 32>, dim3((unsigned)cdiv(a.rows, 8)), block, 0, st, a);
-  } else {
-    if (a.tokens > a.chunk)
-      launch_pdl(embedding_chunks_kernel<T, N, 256>, dim3((unsigned)chunks), block, 0, st, a);
-    launch_pdl(embedding_rows_kernel<T, N, 256>, dim3((unsigned)a.rows), block, 0, st, a);
+  constexpr size_t smem = 2 * kStageRows * 256 * N * sizeof(T);
+  static OncePerDevice once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !once(dev, [] {
+        return cudaFuncSetAttribute(embedding_chunks_kernel<T, N, TPR>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+      })) {
+    check_launch();   // keeps the runtime's message
+    return KFAC_ERR_CUDA;
   }
+  launch_pdl(embedding_chunks_kernel<T, N, TPR>, dim3((unsigned)cdiv(chunks, 256 / TPR)), dim3(256), smem, st, a);
+  if (chunks > 1)
+    launch_pdl(embedding_join_kernel<T, N, TPR>, dim3((unsigned)cdiv(chunks - 1, 256 / TPR)), dim3(256), 0,
+               st, a);
+  return KFAC_OK;
+}
+template <typename T, int N> kfac_status launch_sums(const EmbedArgs& a, cudaStream_t st) {
+  return cdiv(a.width, N) <= 64 ? launch_sums_by<T, N, 32>(a, st) : launch_sums_by<T, N, 256>(a, st);
 }
 
-// Sorted positions per chunk: few enough that a row of one hot run adds few of them.
+// Sorted positions per chunk: two rounds of rows in flight, more where a row of one hot run would
+// add up thousands of parts.
 int chunk_of(int64_t tokens) {
-  int c = 64;
+  int c = 16;
   while (cdiv(tokens, c) > 4096) c *= 2;
   return c;
 }
@@ -596,19 +733,23 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
   a.part = reinterpret_cast<float*>(at(l.part));
   a.chunk = chunk_of(d->tokens);
   int launches = 0;
+  // blocks that clear: a few per SM, or what there is to clear
+  const int64_t clears = std::min<int64_t>(
+      4 * (int64_t)num_sms(),
+      cdiv((accumulate ? 0 : d->rows * d->width / 4) + (frequency ? d->rows : 0), kSortThreads));
   if (d->tokens > 0 && d->tokens <= kSmallTokens) {
-    static OncePerDevice once;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || !once(dev, [] {
-          return cudaFuncSetAttribute(sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      (int)sizeof(SmallSort)) == cudaSuccess;
-        })) {
-      check_launch();
-      return KFAC_ERR_CUDA;
-    }
-    launch_pdl(sort_small_kernel, dim3(1), dim3(kSortThreads), sizeof(SmallSort), stream, a);
+    const dim3 grid((unsigned)(kCluster + cdiv(std::max<int64_t>(clears, accumulate && !frequency ? 0 : 1), kCluster) * kCluster));
+    launch_pdl(sort_small_kernel, grid, dim3(kSortThreads), 0, stream, a);
     launches = 1;
-  } else if (d->tokens > 0) {
+  } else if (!accumulate || frequency) {
+    launch_pdl(clear_kernel, dim3((unsigned)std::max<int64_t>(1, clears)), dim3(kSortThreads), 0, stream, a);
+    launches = 1;
+  }
+  if (d->tokens == 0) {
+    count_launch(launches);
+    return check_launch();
+  }
+  if (d->tokens > kSmallTokens) {
     // the last pass ends in keys, vals
     const uint32_t *k = nullptr, *v = nullptr;
     for (int pass = 0; pass < a.passes; ++pass) {
@@ -622,18 +763,16 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
       v = vo;
     }
     launch_pdl(sort_runs_kernel, dim3((unsigned)cdiv(d->tokens, 256)), dim3(256), 0, stream, a);
-    launches = 3 * a.passes + 1;
+    launches += 3 * a.passes + 1;
   }
   const int n = 16 / (int)es;
-  const bool vec = d->width % n == 0 && (d->tokens == 0 || whole_vectors(dout, d->ldo, d->tokens, es)) &&
+  const bool vec = d->width % n == 0 && whole_vectors(dout, d->ldo, d->tokens, es) &&
                    whole_vectors(dtable, d->ldt, d->rows, 4);
-  if (d->dtype == KFAC_BF16) {
-    if (vec) launch_sums<__nv_bfloat16, 8>(a, stream);
-    else launch_sums<__nv_bfloat16, 1>(a, stream);
-  } else {
-    if (vec) launch_sums<float, 4>(a, stream);
-    else launch_sums<float, 1>(a, stream);
-  }
+  const kfac_status e =
+      d->dtype == KFAC_BF16
+          ? (vec ? launch_sums<__nv_bfloat16, 8>(a, stream) : launch_sums<__nv_bfloat16, 1>(a, stream))
+          : (vec ? launch_sums<float, 4>(a, stream) : launch_sums<float, 1>(a, stream));
+  if (e) return e;
   count_launch(launches + 1 + (d->tokens > a.chunk));
   return check_launch();
 }

@@ -13,6 +13,7 @@
 // threads' columns in registers; its sums go to the workspace and a second launch adds the
 // blocks' in order, so that no atomics are needed and the same inputs give the same bits.
 #include "kfac_internal.cuh"
+#include "per_device.h"
 
 #include <cuda_fp8.h>
 
@@ -253,8 +254,15 @@ template <typename T, int N> bool launch_norm(const NormArgs& a, cudaStream_t st
   else if (vecs <= 256) launch_norm_rows<T, N, 256, 1>(a, st);
   else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
   else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
-  else if (vecs <= 2048) launch_norm_rows<T, N, 1024, 2>(a, st);
-  else return false;
+  else if constexpr (N == 1) {
+    if (vecs <= 2048) launch_norm_rows<T, N, 256, 8>(a, st);
+    else if (vecs <= 4096) launch_norm_rows<T, N, 256, 16>(a, st);
+    else if (vecs <= 8192) launch_norm_rows<T, N, 1024, 8>(a, st);
+    else return false;
+  } else {
+    if (vecs <= 2048) launch_norm_rows<T, N, 1024, 2>(a, st);
+    else return false;
+  }
   return true;
 }
 
@@ -272,15 +280,40 @@ struct NormGradArgs {
 };
 
 // Rows a grid apart, R at a time, TPR threads each; thread t holds vectors t, t + TPR, ...
+// Each thread copies what it will use itself into a ring of its own in shared memory (cp.async,
+// STAGES - 1 rounds of R rows ahead), so that loads stay in flight through the sums and stores and no
+// barrier orders the ring.  Single bf16 elements are below cp.async's 4 bytes: they are loaded
+// when they are used.  Of 16384 x 2048 (bf16, 268 MB) loads of four rows at a time into registers
+// took 111 us.
+template <typename T, int N, int TPR, int V, int R, bool kDh> struct GradRing {
+  static constexpr bool kOn = N * sizeof(T) >= 4;
+  static constexpr int BLOCK = TPR > 256 ? TPR : 256, TENSORS = kDh ? 3 : 2;
+  static constexpr size_t ROUND = (size_t)R * TENSORS * V * BLOCK * N * sizeof(T);
+  // two blocks an SM where two rounds allow it
+  static constexpr int STAGES = ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
+  static constexpr size_t BYTES = kOn ? STAGES * ROUND : 0;
+};
+template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
 template <typename T, int N, int TPR, int V, int R, bool kDh>
 __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     norm_backward_kernel(const __grid_constant__ NormGradArgs a) {
-  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR, W = TPR / 32;
-  extern __shared__ float fold[];          // TPR == 32: [RPB][2][32 V N]
+  using Ring = GradRing<T, N, TPR, V, R, kDh>;
+  constexpr int BLOCK = Ring::BLOCK, RPB = BLOCK / TPR, W = TPR / 32, TENSORS = Ring::TENSORS;
+  constexpr int STAGES = Ring::STAGES;
+  extern __shared__ __align__(16) uint8_t shared[];   // the ring; then, TPR == 32: [RPB][2][32 V N]
   __shared__ float red[2][R][32];
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   using Pack = Vec<T, N>;
+  Pack* ring = reinterpret_cast<Pack*>(shared);
   pdl_wait();
   pdl_trigger();
   float gain[V][N], dg[V][N], sq[V][N];
@@ -291,30 +324,71 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     for (int i = 0; i < N; ++i) dg[v][i] = sq[v][i] = 0.f;
   }
   const int64_t step = (int64_t)gridDim.x * RPB;
-  int turn = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < a.rows; row0 += R * step, turn ^= 1) {
+  const int64_t first = (int64_t)blockIdx.x * RPB + sub;
+  const int rounds = (int)((a.rows - (int64_t)blockIdx.x * RPB + R * step - 1) / (R * step));
+  const T* src[TENSORS] = {static_cast<const T*>(a.dy), static_cast<const T*>(a.h)};
+  int64_t ld[TENSORS] = {a.lddy, a.ldh};
+  if constexpr (kDh) {
+    src[2] = static_cast<const T*>(a.dh);
+    ld[2] = a.lddh;
+  }
+  auto slot = [&](int round, int j, int k, int v) {
+    return ring + ((((round % STAGES) * R + j) * TENSORS + k) * V + v) * BLOCK + threadIdx.x;
+  };
+  auto fetch = [&](int round) {   // always a group, so that the waits count rounds
+    if constexpr (Ring::kOn) {
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        const int64_t row = first + ((int64_t)round * R + j) * step;
+        if (round < rounds && row < a.rows) {
+#pragma unroll
+          for (int k = 0; k < TENSORS; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              const int c = (v * TPR + t) * N;
+              if (c < a.cols) copy_async<N * sizeof(T)>(slot(round, j, k, v), src[k] + row * ld[k] + c);
+            }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) fetch(s);
+  for (int round = 0; round < rounds; ++round) {
+    const int turn = round & 1;
+    const int64_t row0 = first + (int64_t)round * R * step;
     Pack pg[R][V], ph[R][V], pd[R][V];
     float rstd[R];
 #pragma unroll
+    for (int j = 0; j < R; ++j)
+      rstd[j] = row0 + j * step < a.rows ? __ldg(a.rstd + row0 + j * step) : 0.f;
+    if constexpr (Ring::kOn) asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+#pragma unroll
     for (int j = 0; j < R; ++j) {
-      const int64_t row = row0 + j * step + sub;
+      const int64_t row = row0 + j * step;
       if (row >= a.rows) continue;
-      rstd[j] = __ldg(a.rstd + row);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * TPR + t) * N;
         if (c >= a.cols) continue;
-        pg[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.dy) + row * a.lddy + c);
-        ph[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.h) + row * a.ldh + c);
-        if (kDh)
-          pd[j][v] = *reinterpret_cast<const Pack*>(static_cast<const T*>(a.dh) + row * a.lddh + c);
+        if constexpr (Ring::kOn) {
+          pg[j][v] = *slot(round, j, 0, v);
+          ph[j][v] = *slot(round, j, 1, v);
+          if constexpr (kDh) pd[j][v] = *slot(round, j, 2, v);
+        } else {
+          pg[j][v] = *reinterpret_cast<const Pack*>(src[0] + row * ld[0] + c);
+          ph[j][v] = *reinterpret_cast<const Pack*>(src[1] + row * ld[1] + c);
+          if constexpr (kDh) pd[j][v] = *reinterpret_cast<const Pack*>(src[2] + row * ld[2] + c);
+        }
       }
     }
+    fetch(round + STAGES - 1);   // into the slots of the round before, which this thread has read
     float dot[R];
 #pragma unroll
     for (int j = 0; j < R; ++j) {
       dot[j] = 0.f;
-      if (row0 + j * step + sub >= a.rows) continue;
+      if (row0 + j * step >= a.rows) continue;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if ((v * TPR + t) * N >= a.cols) continue;
@@ -337,12 +411,17 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
       }
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < R; ++j) dot[j] = warp_sum(lane < W ? red[turn][j][lane] : 0.f);
+      for (int j = 0; j < R; ++j) {
+        float all = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) all += red[turn][j][w];
+        dot[j] = all;
+      }
     }
     if (a.dx) {
 #pragma unroll
       for (int j = 0; j < R; ++j) {
-        const int64_t row = row0 + j * step + sub;
+        const int64_t row = row0 + j * step;
         if (row >= a.rows) continue;
         const float mean = dot[j] * a.inv_cols;
 #pragma unroll
@@ -366,6 +445,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
   float* part = a.part + (int64_t)blockIdx.x * 2 * a.cols;
   if constexpr (RPB > 1) {   // the block's row groups, in order
     constexpr int C = TPR * V * N;
+    float* fold = reinterpret_cast<float*>(shared + Ring::BYTES);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
@@ -440,22 +520,23 @@ __global__ void __launch_bounds__(256) norm_wide_backward_kernel(const __grid_co
   a.part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = sq;
 }
 
-// The parts' sums, in order: a block takes 32 of the 2 cols columns, warp w every 8th part.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const __grid_constant__ NormGradArgs a) {
-  __shared__ float s[8][32];
+// The parts' sums, in order: a block takes 32 of the 2 cols columns, warp w every 32nd part.
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const __grid_constant__ NormGradArgs a) {
+  __shared__ float s[32][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   const int k = blockIdx.x * 32 + lane;
   float sum = 0.f;
   if (k < 2 * a.cols)
-    for (int p = warp; p < a.parts; p += 8) sum += a.part[(int64_t)p * 2 * a.cols + k];
+#pragma unroll 10
+    for (int p = warp; p < a.parts; p += 32) sum += __ldcg(a.part + (int64_t)p * 2 * a.cols + k);
   s[warp][lane] = sum;
   __syncthreads();
   if (warp == 0 && k < 2 * a.cols) {
     sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) sum += s[w][lane];
+    for (int w = 0; w < 32; ++w) sum += s[w][lane];
     if (k < a.cols) {
       if (a.dgain) a.dgain[k] = sum;
     } else if (a.dgain_sq) {
@@ -469,29 +550,44 @@ int64_t backward_parts(int64_t rows) {
   return std::max<int64_t>(1, std::min<int64_t>(rows, 2 * (int64_t)num_sms()));
 }
 
+template <typename T, int N, int TPR, int V, int R, bool kDh>
+kfac_status launch_backward_kernel(const NormGradArgs& a, cudaStream_t st) {
+  using Ring = GradRing<T, N, TPR, V, R, kDh>;
+  constexpr int RPB = Ring::BLOCK / TPR;
+  constexpr size_t smem = Ring::BYTES + (RPB > 1 ? (size_t)2 * RPB * TPR * V * N * sizeof(float) : 0);
+  static OncePerDevice once;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || !once(dev, [] {
+        return cudaFuncSetAttribute(norm_backward_kernel<T, N, TPR, V, R, kDh>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) == cudaSuccess;
+      })) {
+    check_launch();   // keeps the runtime's message
+    return KFAC_ERR_CUDA;
+  }
+  launch_pdl(norm_backward_kernel<T, N, TPR, V, R, kDh>, dim3((unsigned)a.parts), dim3(Ring::BLOCK), smem,
+             st, a);
+  return KFAC_OK;
+}
 template <typename T, int N, int TPR, int V, int R>
-void launch_backward_rows(const NormGradArgs& a, cudaStream_t st) {
-  constexpr int BLOCK = TPR > 256 ? TPR : 256, RPB = BLOCK / TPR;
-  const size_t smem = RPB > 1 ? (size_t)2 * RPB * TPR * V * N * sizeof(float) : 0;
-  const dim3 grid((unsigned)a.parts), block(BLOCK);
-  if (a.dh) launch_pdl(norm_backward_kernel<T, N, TPR, V, R, true>, grid, block, smem, st, a);
-  else launch_pdl(norm_backward_kernel<T, N, TPR, V, R, false>, grid, block, smem, st, a);
+kfac_status launch_backward_rows(const NormGradArgs& a, cudaStream_t st) {
+  return a.dh ? launch_backward_kernel<T, N, TPR, V, R, true>(a, st)
+              : launch_backward_kernel<T, N, TPR, V, R, false>(a, st);
 }
 
-template <typename T, int N> bool launch_backward(const NormGradArgs& a, cudaStream_t st) {
+// Threads per row as in the forward pass; *done false: too wide.
+template <typename T, int N> kfac_status launch_backward(const NormGradArgs& a, cudaStream_t st, bool* done) {
   const int64_t vecs = cdiv(a.cols, N);
-  if (vecs <= 32) launch_backward_rows<T, N, 32, 1, 4>(a, st);
-  else if (vecs <= 256) launch_backward_rows<T, N, 256, 1, 4>(a, st);
-  else if (vecs <= 512) launch_backward_rows<T, N, 256, 2, 2>(a, st);
-  else if (vecs <= 1024) launch_backward_rows<T, N, 256, 4, 1>(a, st);
-  else if constexpr (N == 1) {
-    if (vecs <= 2048) launch_backward_rows<T, N, 256, 8, 1>(a, st);
-    else if (vecs <= 8192) launch_backward_rows<T, N, 1024, 8, 1>(a, st);
-    else return false;
-  } else {
-    return false;
+  *done = true;
+  if (vecs <= 32) return launch_backward_rows<T, N, 32, 1, 2>(a, st);
+  if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 2>(a, st);
+  if (vecs <= 512) return launch_backward_rows<T, N, 256, 2, 1>(a, st);
+  if (vecs <= 1024) return launch_backward_rows<T, N, 256, 4, 1>(a, st);
+  if constexpr (N == 1) {
+    if (vecs <= 2048) return launch_backward_rows<T, N, 256, 8, 1>(a, st);
+    if (vecs <= 8192) return launch_backward_rows<T, N, 1024, 8, 1>(a, st);
   }
-  return true;
+  *done = false;
+  return KFAC_OK;
 }
 
 // Whether rows of p are whole aligned vectors.
@@ -626,10 +722,12 @@ extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, cons
                    wide_ok(dx, d->lddx, d->rows, 16, es) && (uintptr_t)gain % 16 == 0;
   int launches = 1;
   bool done;
-  if (d->dtype == KFAC_BF16)
-    done = vec ? launch_backward<__nv_bfloat16, 8>(a, stream) : launch_backward<__nv_bfloat16, 1>(a, stream);
-  else
-    done = vec ? launch_backward<float, 4>(a, stream) : launch_backward<float, 1>(a, stream);
+  const kfac_status e =
+      d->dtype == KFAC_BF16
+          ? (vec ? launch_backward<__nv_bfloat16, 8>(a, stream, &done)
+                 : launch_backward<__nv_bfloat16, 1>(a, stream, &done))
+          : (vec ? launch_backward<float, 4>(a, stream, &done) : launch_backward<float, 1>(a, stream, &done));
+  if (e) return e;
   if (!done) {
     float* means = reinterpret_cast<float*>(
         static_cast<char*>(workspace) + align_up((size_t)(a.parts * 2 * d->cols) * sizeof(float)));
@@ -647,7 +745,7 @@ extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, cons
     launches = d->rows > 0 ? 2 : 1;
   }
   if (a.part) {
-    launch_pdl(norm_parts_kernel, dim3((unsigned)cdiv(2 * (int64_t)a.cols, 32)), dim3(256), 0, stream, a);
+    launch_pdl(norm_parts_kernel, dim3((unsigned)cdiv(2 * (int64_t)a.cols, 32)), dim3(1024), 0, stream, a);
     ++launches;
   }
   count_launch(launches);
