@@ -100,9 +100,10 @@ def orthogonal_step(grad, m, w, lr, momentum=0.95, weight_decay=0.0, nesterov=Tr
     return m, w - lr * (scale * o + weight_decay * w)
 
 
-def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, groups=None):
     """The products with every matrix between them rounded to fp16's 11 bits (x too): the error that
-    such operands cannot avoid."""
+    such operands cannot avoid.  groups: sizes of the groups of steps taken on the small side before x
+    is formed (None: single steps)."""
     def near(v):
         m, e = np.frexp(v)
         return np.ldexp(np.rint(m * 2.0 ** 11), e - 11)
@@ -111,8 +112,15 @@ def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
     x = near(x) / (np.sqrt((x * x).sum()) + eps)
     a, b, c = coefficients
     eye = np.eye(x.shape[0])
-    for k in range(steps):
-        g = near(x @ x.T)
-        x = near(a * eye + b * g + c * g @ g) @ x
-        x = x if k + 1 == steps else near(x)
+    k = 0
+    for size in groups or [1] * steps:
+        g, p = near(x @ x.T), None
+        for j in range(size):
+            m = near(a * eye + b * g + c * g @ g)
+            p = m if p is None else near(m @ p)
+            if j + 1 < size:
+                g = near(near(g @ m) @ m)
+        k += size
+        x = p @ x
+        x = x if k == steps else near(x)
     return x

@@ -5,7 +5,16 @@
 //
 // Per step two symmetric products (s^2 l and s^3 multiply-adds over their distinct halves) and one
 // whole one (s^2 l): bound by the tensor cores where there are tiles for every SM, by the chain of
-// 3 steps launches where there are not.
+// launches where there are not.
+//
+// All these matrices are polynomials of one L, so they commute, and steps can be taken on the small
+// side alone: L' = M L M and P = M' M are symmetric products of size s, and X is read and written
+// once per group of steps (X <- P X) instead of once per step.  With r = l / s a group of g steps
+// costs s^3 (3 r + 4 g - 3) instead of s^3 g (3 r + 1): at l = 4 s, three and two steps together take
+// 38 s^3 for 65.  What L was rounded by grows by max |M|^2 (11.9 for the default coefficients) with
+// every step that it is not formed anew from X, so groups end before that passes 150: three
+// steps.  X is rounded less often and L_0 is formed from X_0 itself, so the result is no less
+// exact (emulated: 1.9e-3 to 3.6e-3 off where single steps are 1.9e-3 to 7e-3).
 //
 // Operands are fp16, not bf16: every matrix here is bounded (|X| <= u, |L| <= u^2, |M| <= v with u, v
 // from the polynomial on [0, u]), so a power of two per matrix and step brings it to just below
@@ -17,12 +26,13 @@
 // drains the accumulator every 64 k into fp32 registers (the tensor cores' sums round towards
 // zero; every 128 k, the small products in between, were 6e-6 off): about 1e-6 off.
 //
-// One kernel serves the three products: CTA pairs (tcgen05 cta_group::2) on 256 x 256 tiles of all
-// the call's matrices, persistent, a warp for TMA, one for the MMAs, eight for the epilogue, two
-// accumulators in TMEM so that a tile's epilogue runs beside the next one's products.  A matrix
+// One kernel serves all products: CTA pairs (tcgen05 cta_group::2) on 256 x 256 tiles of all the
+// call's matrices, persistent, a warp for TMA, one for the MMAs, eight for the epilogue, two
+// accumulators in TMEM so that a tile's epilogue runs beside the next one's products; single CTAs
+// on 128 x 128 tiles where the larger ones would leave SMs idle.  A matrix
 // is never transposed: the operand whose k runs down the rows of X is read as it lies, as an
 // MN-major tile.  Of a symmetric product the tiles on and above the diagonal are computed; the
-// epilogue stores each of them and its transpose through shared memory by TMA.
+// epilogue stores each of them (through shared memory, by TMA) and its transpose.
 #include "kfac_internal.cuh"
 #include "per_device.h"
 #include "ring.h"
@@ -45,7 +55,7 @@ __device__ DevStatus g_status;   // device-side errors, read by kfac_operator_st
 
 namespace {
 
-constexpr int kMaxGroup = 32;        // matrices per launch
+constexpr int kMaxGroup = 24;        // matrices per launch of the norm
 constexpr int kMaxSide = 32768;      // no accumulator sums more terms
 constexpr int kMaxSteps = 32;
 constexpr int kPrepThreads = 256;
@@ -81,54 +91,120 @@ __device__ __forceinline__ int task_of(const int* start, int count, int block) {
 
 template <typename T, int N> struct alignas(N * sizeof(T)) Vec { T v[N]; };
 
-// Squares in three ranges, so that none of 2^30 overflows or vanishes: of values from 2^40 (scaled
-// by 2^-84), below 2^-40 (by 2^88: from 2^-149 on), and the others.
-struct Squares {
-  float big = 0.f, mid = 0.f, small = 0.f;
-  __device__ __forceinline__ void add(float v) {
-    const float m = fabsf(v);
-    if (m < 0x1p-40f) {
-      const float t = v * 0x1p88f;
-      small = fmaf(t, t, small);
-    } else if (m < 0x1p40f) {
-      mid = fmaf(v, v, mid);
-    } else {   // Inf and NaN too
-      const float t = v * 0x1p-84f;
-      big = fmaf(t, t, big);
+// The pieces of n elements that a thread takes of a matrix: tx threads per row, rows apart by the
+// matrix's blocks.
+struct Pieces {
+  int64_t row, row_step;
+  int c, c0, c_step;
+  __device__ __forceinline__ Pieces(const PrepTask& t, int n, int block, int blocks) {
+    const int rpb = kPrepThreads / t.tx;
+    row = (int64_t)block * rpb + threadIdx.x / t.tx;
+    row_step = (int64_t)blocks * rpb;
+    c = c0 = (int)(threadIdx.x % t.tx) * n;
+    c_step = t.tx * n;
+  }
+  __device__ __forceinline__ bool next(const PrepTask& t, int64_t* r, int* col) {
+    if (c >= t.cols) {
+      c = c0;
+      row += row_step;
     }
+    if (row >= t.rows || c >= t.cols) return false;
+    *r = row;
+    *col = c;
+    c += c_step;
+    return true;
   }
 };
 
 // N values of the matrix to orthogonalise from column c of a row: x, or with the momentum
-// m <- mu m + g the update g + mu m (nesterov) or m.  kStore: m is written.
-template <typename T, int N, bool kStep, bool kStore>
-__device__ __forceinline__ void load_update(const PrepLaunch& g, const PrepTask& t, int64_t row, int c,
-                                            float (&u)[N]) {
-  const Vec<T, N> p = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(t.x) + row * t.ldx + c);
+// m <- mu m + g the update g + mu m (nesterov) or m.  Loading and using them are apart, so that
+// several pieces' loads are in flight.
+template <typename T, int N, bool kStep> struct Piece {
+  static constexpr int F = N < 4 ? N : 4;
+  Vec<T, N> g;
+  Vec<float, F> m[kStep ? N / F : 1];
+  __device__ __forceinline__ void load(const PrepTask& t, int64_t row, int c) {
+    g = *reinterpret_cast<const Vec<T, N>*>(static_cast<const T*>(t.x) + row * t.ldx + c);
+    if constexpr (kStep) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) u[i] = to_f32<T>(p.v[i]);
-  if constexpr (kStep) {
-    constexpr int F = N < 4 ? N : 4;
-    float* m = t.m + row * t.ldm + c;
-#pragma unroll
-    for (int j = 0; j < N; j += F) {
-      Vec<float, F> v = *reinterpret_cast<const Vec<float, F>*>(m + j);
-      if (kStore) {
-#pragma unroll
-        for (int i = 0; i < F; ++i) v.v[i] = fmaf(g.mu, v.v[i], u[j + i]);
-        *reinterpret_cast<Vec<float, F>*>(m + j) = v;
-      }
-#pragma unroll
-      for (int i = 0; i < F; ++i) u[j + i] = g.nesterov ? fmaf(g.mu, v.v[i], u[j + i]) : v.v[i];
+      for (int j = 0; j < N / F; ++j)
+        m[j] = *reinterpret_cast<const Vec<float, F>*>(t.m + row * t.ldm + c + j * F);
     }
+  }
+  // kFresh: m is still the one before this step; it is updated and written.
+  template <bool kFresh>
+  __device__ __forceinline__ void use(const PrepLaunch& l, const PrepTask& t, int64_t row, int c,
+                                      float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = to_f32<T>(g.v[i]);
+    if constexpr (kStep) {
+#pragma unroll
+      for (int j = 0; j < N / F; ++j) {
+        if (kFresh) {
+#pragma unroll
+          for (int i = 0; i < F; ++i) m[j].v[i] = fmaf(l.mu, m[j].v[i], u[j * F + i]);
+          *reinterpret_cast<Vec<float, F>*>(t.m + row * t.ldm + c + j * F) = m[j];
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+          u[j * F + i] = l.nesterov ? fmaf(l.mu, m[j].v[i], u[j * F + i]) : m[j].v[i];
+      }
+    }
+  }
+};
+// f(row, column, values) for every piece of a thread.
+template <typename T, int N, bool kStep, bool kFresh, typename F>
+__device__ __forceinline__ void each_piece(const PrepLaunch& l, const PrepTask& t, int block, int blocks, F f) {
+  constexpr int AHEAD = 4;
+  Pieces walk(t, N, block, blocks);
+  for (bool more = true; more;) {
+    Piece<T, N, kStep> p[AHEAD];
+    int64_t row[AHEAD];
+    int c[AHEAD];
+    bool ok[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      ok[k] = walk.next(t, &row[k], &c[k]);
+      if (ok[k]) p[k].load(t, row[k], c[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (!ok[k]) continue;
+      float u[N];
+      p[k].template use<kFresh>(l, t, row[k], c[k], u);
+      f(row[k], c[k], u);
+    }
+    more = ok[AHEAD - 1];
   }
 }
 
-template <typename F> __device__ __forceinline__ void each_row_piece(const PrepTask& t, int n, int block,
-                                                                    int blocks, F f) {
-  const int tc = threadIdx.x % t.tx, tr = threadIdx.x / t.tx, rpb = kPrepThreads / t.tx;
-  for (int64_t row = (int64_t)block * rpb + tr; row < t.rows; row += (int64_t)blocks * rpb)
-    for (int c = tc * n; c < t.cols; c += t.tx * n) f(row, c);
+// A thread's squares: plainly, unless its largest value says that they overflow or vanish; then of
+// the values times 2^-84 (from 2^40 on: 2^30 squares below 2^128) or 2^88 (below 2^-30, down to
+// 2^-149).  A value so small that its square vanishes beside a larger one is not missed.
+template <typename T, int N, bool kStep>
+__device__ __forceinline__ void sum_squares(const PrepLaunch& l, const PrepTask& t, int block, int blocks,
+                                            float (&sums)[3]) {
+  float mid = 0.f, top = 0.f;
+  each_piece<T, N, kStep, true>(l, t, block, blocks, [&](int64_t, int, const float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      mid = fmaf(u[i], u[i], mid);
+      top = fmaxf(top, fabsf(u[i]));
+    }
+  });
+  sums[0] = sums[2] = 0.f;
+  if (top >= 0x1p40f || (top < 0x1p-30f && top > 0.f && mid == mid)) {   // (a NaN is in mid)
+    const bool big = top >= 0x1p40f;
+    const float by = big ? 0x1p-84f : 0x1p88f;
+    float sum = 0.f;
+    each_piece<T, N, kStep, false>(l, t, block, blocks, [&](int64_t, int, const float (&u)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum = fmaf(u[i] * by, u[i] * by, sum);
+    });
+    sums[big ? 0 : 2] = sum;
+    if (mid == mid) mid = 0.f;
+  }
+  sums[1] = mid;
 }
 
 template <typename T, bool kStep>
@@ -139,23 +215,9 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const __grid_c
   const int q = task_of(g.block_start, g.count, blockIdx.x);
   const PrepTask& t = g.task[q];
   const int block = blockIdx.x - g.block_start[q], blocks = g.block_start[q + 1] - g.block_start[q];
-  constexpr int N = 16 / (int)sizeof(T);
-  Squares s;
-  if (t.vec) {
-    each_row_piece(t, N, block, blocks, [&](int64_t row, int c) {
-      float u[N];
-      load_update<T, N, kStep, true>(g, t, row, c, u);
-#pragma unroll
-      for (int i = 0; i < N; ++i) s.add(u[i]);
-    });
-  } else {
-    each_row_piece(t, 1, block, blocks, [&](int64_t row, int c) {
-      float u[1];
-      load_update<T, 1, kStep, true>(g, t, row, c, u);
-      s.add(u[0]);
-    });
-  }
-  float v[3] = {s.big, s.mid, s.small};
+  float v[3];
+  if (t.vec) sum_squares<T, 16 / (int)sizeof(T), kStep>(g, t, block, blocks, v);
+  else sum_squares<T, 1, kStep>(g, t, block, blocks, v);
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
 #pragma unroll
@@ -170,11 +232,30 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const __grid_c
   }
 }
 
-// X_0 = x 2^k with |X_0|_F in (2^13, 2^14], and r with x / (|x| + eps) = r X_0.
+// From the squares by range (big, plain, small): 2^k (in two factors, each within fp32's range)
+// with |x 2^k|_F in (2^13, 2^14], and r with x / (|x| + eps) = r x 2^k.
+__device__ __forceinline__ void scale_factors(const double (&sums)[3], float eps, float (&up)[2], float* r_out) {
+  const double norm = sqrt(sums[0] * 0x1p168 + sums[1] + sums[2] * 0x1p-176) + (double)eps;
+  float r = 0.f;
+  int k = 0;
+  if (norm > 0.0 && isfinite(norm)) {
+    int e = 0;
+    frexp(norm, &e);                         // norm < 2^e
+    k = 14 - e;
+    r = (float)ldexp(1.0 / norm, -k);
+  } else if (norm != 0.0) {                  // Inf and NaN reach everything through r
+    r = __int_as_float(0x7fffffff);
+  }
+  const int k0 = min(max(k, -126), 126);
+  up[0] = ldexpf(1.f, k0);
+  up[1] = ldexpf(1.f, k - k0);
+  *r_out = r;
+}
+
 template <typename T, bool kStep, bool kFull>
 __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_constant__ PrepLaunch g) {
   __shared__ double sums[3];
-  __shared__ float factor[2];   // 2^k in two, each within fp32's range
+  __shared__ float factor[2];
   pdl_wait();
   pdl_trigger();
   const int q = task_of(g.block_start, g.count, blockIdx.x);
@@ -190,26 +271,16 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    const double norm = sqrt(sums[0] * 0x1p168 + sums[1] + sums[2] * 0x1p-176) + (double)g.eps;
-    float r = 0.f;
-    int k = 0;
-    if (norm > 0.0 && isfinite(norm)) {
-      int e = 0;
-      frexp(norm, &e);                         // norm < 2^e
-      k = 14 - e;
-      r = (float)ldexp(1.0 / norm, -k);
-    } else if (norm != 0.0) {                  // Inf and NaN reach everything through r
-      r = __int_as_float(0x7fffffff);
-    }
-    const int k0 = min(max(k, -126), 126);
-    factor[0] = ldexpf(1.f, k0);
-    factor[1] = ldexpf(1.f, k - k0);
+    const double all[3] = {sums[0], sums[1], sums[2]};
+    float up[2], r;
+    scale_factors(all, g.eps, up, &r);
+    factor[0] = up[0];
+    factor[1] = up[1];
     if (block == 0) *t.r = r;
   }
   __syncthreads();
   const float up0 = factor[0], up1 = factor[1];
-  constexpr int N = 16 / (int)sizeof(T);
-  auto store = [&](auto& u, int64_t row, int c) {
+  auto store = [&](int64_t row, int c, auto& u) {
     constexpr int n = sizeof(u) / sizeof(float);
     Vec<__half, n> h, l;
 #pragma unroll
@@ -221,47 +292,42 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_
     *reinterpret_cast<Vec<__half, n>*>(t.hi + row * t.pitch + c) = h;
     if (kFull) *reinterpret_cast<Vec<__half, n>*>(t.lo + row * t.pitch + c) = l;
   };
-  if (t.vec) {
-    each_row_piece(t, N, block, blocks, [&](int64_t row, int c) {
-      float u[N];
-      load_update<T, N, kStep, false>(g, t, row, c, u);
-      store(u, row, c);
-    });
-  } else {
-    each_row_piece(t, 1, block, blocks, [&](int64_t row, int c) {
-      float u[1];
-      load_update<T, 1, kStep, false>(g, t, row, c, u);
-      store(u, row, c);
-    });
-  }
+  if (t.vec) each_piece<T, 16 / (int)sizeof(T), kStep, false>(g, t, block, blocks, store);
+  else each_piece<T, 1, kStep, false>(g, t, block, blocks, store);
 }
 
 // -------------------------------------------------------------------------------- products
 
-enum { PH_GRAM, PH_POLY, PH_APPLY, PH_OUT, PH_STEP };   // L, M, X, the last X, and with it W
+// What becomes of a product: another matrix of the iteration, or with the last X the direction or
+// the weights.
+enum { TO_MATRIX, TO_OUT, TO_WEIGHTS };
 
-// out = alpha r^rpow A B^T [+ beta add + diag I], stored as fp16 (or PH_OUT, PH_STEP below)
+// out = alpha r^rpow A B^T [+ beta add + diag I], stored as fp16, or as it is below
 struct Task {
   int64_t out_ld;
-  void* out;                    // PH_OUT: the direction; PH_STEP: the weights, fp32
-  const __half *add_hi, *add_lo;   // PH_POLY: L
+  void* out;                    // TO_OUT: the direction; TO_WEIGHTS: the weights, fp32
+  const __half *add_hi, *add_lo;   // or null
+  __half *mirror_hi, *mirror_lo;   // upper: the result itself, whose other half is stored directly
   const float* r;
   float alpha, beta, diag;
-  float keep, rate;             // PH_STEP: W <- keep W - rate X
-  int rpow, add_pitch;
+  float keep, rate;             // TO_WEIGHTS: W <- keep W - rate X
+  int rpow, add_pitch, mirror_pitch;
   int M, N, kblocks;            // sizes of the product; k in blocks of 64
-  int tiles_m, tiles_n, upper;  // upper: symmetric, tiles on and above the diagonal
+  int tiles_m, upper;           // upper: symmetric, tiles on and above the diagonal
   int mn_a, mn_b;               // operands read as MN-major tiles
+  int same_ab;                  // A is B
 };
+enum { MAP_A, MAP_B, MAP_STORE, MAPS };   // operands and result
 template <bool kFull> struct Launch {
-  // operand A, operand B, direct store; mirror store in B's place where A is B (GRAM, POLY)
-  CUtensorMap maps[kMaxGroup][kFull ? 6 : 3];
-  Task task[kMaxGroup];
-  int tile_start[kMaxGroup + 1];
+  static constexpr int TASKS = kFull ? 24 : 48;   // a kernel's parameters end at 32764 bytes
+  CUtensorMap maps[TASKS][MAPS * (kFull ? 2 : 1)];
+  Task task[TASKS];
+  int tile_start[TASKS + 1];
   int count;
 };
 
-template <bool kFull> struct Cfg {
+template <bool kFull, bool kPair> struct Cfg {
+  static constexpr int TILE = kPair ? 256 : 128;
   static constexpr int BK = 64;
   static constexpr int HALF = 128 * BK * 2;              // 128 rows (or features) of an operand
   static constexpr int STAGE = HALF * 2 * (kFull ? 2 : 1);
@@ -269,10 +335,19 @@ template <bool kFull> struct Cfg {
   static constexpr int NBUF = kFull ? 1 : 2;             // 16 KB store buffers per epilogue group
   static constexpr int BUF = 128 * 64 * 2;
   static constexpr int SUB = kFull ? 1 : 1 << 20;        // k blocks per drain
-  static constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int CW = TILE / 2;                    // columns of an epilogue warp
+  static constexpr int TMEM = 2 * TILE;
+  // warps 0 and 1: TMA, MMA; 4 to 11: epilogue (whole warpgroups, for the register split below)
+  static constexpr int EPI0 = 4, EPI_WARPS = 8, THREADS = 32 * (EPI0 + EPI_WARPS);
   static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + 2 * NBUF * BUF + 512;
   static_assert(SMEM <= 232448, "fits the per-CTA shared memory");
 };
+// Full arithmetic on pairs keeps 128 running sums a thread.  384 threads are launched with at most
+// 168 registers each, 64512; the epilogue's 256 take 232 and leave the others 40.
+constexpr int kLaunchRegs = 168, kEpilogueRegs = 232, kOtherRegs = 40;
+static_assert(sizeof(Launch<true>) <= 32764 && sizeof(Launch<false>) <= 32764 &&
+              Launch<true>::TASKS <= 2 * kMaxGroup && Launch<false>::TASKS <= 2 * kMaxGroup, "one launch");
+static_assert(256 * kEpilogueRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "register split");
 
 __device__ __forceinline__ void umma_pair_by(uint32_t leader, uint32_t d, uint64_t a, uint64_t b,
                                              uint32_t idesc, uint32_t accumulate) {
@@ -290,16 +365,18 @@ __device__ __forceinline__ void commit_pair_by(uint32_t leader, uint64_t* bar) {
       "h"((uint16_t)3), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
+                                            int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(tc::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(x), "r"(y), "r"(tc::smem_u32(src))
-               : "memory");
-}
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(tc::smem_u32(src))
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
@@ -311,7 +388,7 @@ __device__ __forceinline__ void group_sync(int id) {   // the 128 threads of an 
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
 
-// Tile t of the launch: its matrix, row and column block.
+// Tile t of the launch: its task, row and column block.
 template <bool kFull>
 __device__ __forceinline__ void tile_of(const Launch<kFull>& g, int t, int* q, int* ti, int* tj) {
   int p = 0;
@@ -347,37 +424,66 @@ __device__ __forceinline__ void put_rows(uint8_t* buf, int row, const uint32_t (
     *reinterpret_cast<uint4*>(buf + row * 128 + ((j ^ (row & 7)) << 4)) =
         make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
 }
-// Transposed: two blocks (rows 0-63, 64-127) of 64 columns x 64 rows.  Neighbouring lanes trade
-// values so that each writes whole words, of columns c and c + 4, which fall on different banks.
-__device__ __forceinline__ void put_columns(uint8_t* buf, int row, const uint32_t (&w)[32]) {
-  const bool odd = row & 1;
-  uint8_t* block = buf + (row >> 6) * 8192;
-  const int e = row & 62;   // the even row of the pair, within the block
+// The same transposed, straight to memory: row c of the other half of the symmetric matrix gets
+// this tile's column c.  Neighbouring lanes trade values so that each writes whole words of
+// columns c and c + 1, 64 bytes of each per warp.  (By way of shared memory and TMA, as above, it
+// took part of the bandwidth that the operands need: 13 to 14 us a tile of 2048 k against 11.5.)
+// out: at row c0, column of this thread's row rounded down to even; cols: columns that exist.
+__device__ __forceinline__ void put_columns(__half* out, int64_t pitch, bool row_ok, int cols,
+                                            const uint32_t (&w)[32]) {
+  const bool odd = threadIdx.x & 1;
+  out += odd ? pitch : 0;
+  const int mine = row_ok ? cols - (odd ? 1 : 0) : 0;
 #pragma unroll
-  for (int j = 0; j < 32; j += 4) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // columns c = 2 (j + k) + {0, 1} and c + 4
-      const uint32_t lo = w[j + k], hi = w[j + k + 2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int c = 2 * (j + k) + b;
-        const uint32_t p = __byte_perm(lo, hi, b ? 0x7632 : 0x5410);   // (column c, column c + 4)
-        const uint32_t o = __shfl_xor_sync(0xffffffffu, p, 1);
-        const uint32_t word = odd ? __byte_perm(p, o, 0x3276) : __byte_perm(p, o, 0x5410);
-        const int cc = odd ? c + 4 : c;
-        *reinterpret_cast<uint32_t*>(block + cc * 128 + (((e >> 3) ^ (cc & 7)) << 4) + (e & 7) * 2) = word;
-      }
-    }
+  for (int j = 0; j < 32; ++j) {   // columns 2 j, 2 j + 1
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+    const uint32_t word = odd ? __byte_perm(w[j], o, 0x3276) : __byte_perm(w[j], o, 0x5410);
+    if (2 * j < mine) *reinterpret_cast<uint32_t*>(out + 2 * j * pitch) = word;
   }
 }
 
-template <int PH, typename TO, bool kFull>
-__global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
+// A tile on the diagonal of a product of two different matrices: the elements on and above it as
+// they are, those above it transposed, so that the matrix is symmetric to the last bit (as A A^T is
+// by itself).  (Rounding leaves the product of two matrices that
+// commute a little unsymmetric, and of that part the polynomial's next step sees b L without c L^2,
+// which for the symmetric part takes most of it back: three steps on the small side, then three
+// more, were 1.2e-2 off where 2e-3 is due.)  to: row gr (its column c0); mirror: row c0, column gr
+// rounded down to even.
+__device__ __forceinline__ void put_diagonal(__half* to, __half* mirror, int64_t pitch, int gr, int c0, int n,
+                                             const uint32_t (&w)[32]) {
+  if (gr < n) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + 8 * j;
+      if (c >= gr) {       // (columns from n to the pitch take whatever there is)
+        *reinterpret_cast<uint4*>(to + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      } else if (c + 8 > gr) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const __half2 h = *reinterpret_cast<const __half2*>(&w[4 * j + i / 2]);
+          if (c + i >= gr) to[8 * j + i] = i & 1 ? h.y : h.x;
+        }
+      }
+    }
+  }
+  const bool odd = gr & 1;
+  const int e = gr & ~1;   // this lane's words hold rows e and e + 1
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {   // columns 2 j, 2 j + 1
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, w[j], 1);
+    const uint32_t word = odd ? __byte_perm(w[j], o, 0x3276) : __byte_perm(w[j], o, 0x5410);
+    const int k = 2 * j + odd, c = c0 + k;
+    __half* at = mirror + (int64_t)k * pitch;
+    if (c < n && c > e + 1) *reinterpret_cast<uint32_t*>(at) = word;
+    else if (c < n && c == e + 1) *at = __ushort_as_half((unsigned short)(word & 0xffffu));
+  }
+}
+
+template <int TO, typename T, bool kFull, bool kPair>
+__global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
     ortho_product_kernel(const __grid_constant__ Launch<kFull> g) {
-  using C = Cfg<kFull>;
-  constexpr int STAGES = C::STAGES;
-  constexpr bool kSym = PH == PH_GRAM || PH == PH_POLY, kLast = PH == PH_OUT || PH == PH_STEP;
+  using C = Cfg<kFull, kPair>;
+  constexpr int STAGES = C::STAGES, TILE = C::TILE, CTAS = kPair ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* bufs = smem + (size_t)STAGES * C::STAGE;
@@ -390,14 +496,18 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int total = g.tile_start[g.count];
-  const uint32_t rank = tc::cluster_rank();
-  const int pair = (int)(blockIdx.x / 2), npairs = (int)(gridDim.x / 2);
+  const uint32_t rank = kPair ? tc::cluster_rank() : 0;
+  const int unit = (int)(blockIdx.x / CTAS), units = (int)(gridDim.x / CTAS);
   // a role that gives up stops the peer CTA's roles too
-  const uint32_t peer_abort = tc::mapa((const void*)abort_flag, rank ^ 1u);
+  const uint32_t peer_abort = kPair ? tc::mapa((const void*)abort_flag, rank ^ 1u) : 0;
   auto give_up = [&](int info) {
     report_error(&g_status, KFAC_ERR_TIMEOUT, -1, info);
     *abort_flag = 1;
-    tc::st_cluster_u32(peer_abort, 1u);
+    if (kPair) tc::st_cluster_u32(peer_abort, 1u);
+  };
+  auto block_sync = [&]() {
+    if constexpr (kPair) tc::cluster_sync();
+    else __syncthreads();
   };
 
   if (threadIdx.x == 0) {
@@ -407,42 +517,53 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&acc_full[b], 1);
-      tc::mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);
+      tc::mbar_init(&acc_empty[b], CTAS * C::EPI_WARPS);
     }
     tc::mbar_init(drained, 1);
     *abort_flag = 0;
     tc::fence_mbar_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc_pair(tmem_slot, 512);
-    tc::tmem_relinquish_pair();
+    if constexpr (kPair) {
+      tc::tmem_alloc_pair(tmem_slot, C::TMEM);
+      tc::tmem_relinquish_pair();
+    } else {
+      tc::tmem_alloc(tmem_slot, C::TMEM);
+      tc::tmem_relinquish();
+    }
+  }
+  if (warp == 0 && unit < total) {   // the first tile's maps, before anything waits
+    int q, ti, tj;
+    tile_of(g, unit, &q, &ti, &tj);
+    if (lane < MAPS) tc::tma_prefetch_desc(&g.maps[q][lane]);
   }
   tc::tc_fence_before();
   __syncwarp();
-  tc::cluster_sync();   // both CTAs' barriers initialised and TMEM allocated
+  block_sync();   // the barriers initialised and TMEM allocated (of both CTAs)
   tc::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_wait();
   pdl_trigger();
-  // a diagonal tile of a symmetric product: this CTA's rows of A are its half of B
-  auto shared_ab = [&](int ti, int tj) { return kSym && ti == tj; };
+  // a diagonal tile of a matrix with itself: this CTA's rows of A are its rows of B
+  auto shared_ab = [&](const Task& k, int ti, int tj) { return k.same_ab && ti == tj; };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint32_t full0 = tc::mapa(full, 0);   // the even CTA's stage barriers
+  if (warp < C::EPI0) {
+    if constexpr (kFull && kPair) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == 0 && lane == 0) {
+      // -------------------------------------------------------------- TMA producer
+      const uint32_t full0 = kPair ? tc::mapa(full, 0) : 0;   // the even CTA's stage barriers
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
+      for (int t = unit; t < total && ok; t += units) {
         int q, ti, tj;
         tile_of(g, t, &q, &ti, &tj);
         const Task& k = g.task[q];
-        const bool ab = shared_ab(ti, tj);
-        const int arow = ti * 256 + (int)rank * 128, brow = tj * 256 + (int)rank * 128;
-        const CUtensorMap *ma = &g.maps[q][0], *mb = kSym ? ma : &g.maps[q][1];
-        constexpr int LO = 3;   // the lo halves' maps
-        for (int kb = 0; kb < k.kblocks; ++kb) {
+        const bool ab = shared_ab(k, ti, tj);
+        const int arow = ti * TILE + (int)rank * 128, brow = tj * TILE + (int)rank * 128;
+        const int mn_a = k.mn_a, mn_b = k.mn_b, kblocks = k.kblocks;
+        const CUtensorMap* maps = g.maps[q];
+        for (int kb = 0; kb < kblocks; ++kb) {
           if (!tc::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
             give_up(41);
             ok = false;
@@ -450,16 +571,21 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
           }
           const uint32_t fb = full0 + (uint32_t)(stage * sizeof(uint64_t));
           if (rank == 0)
-            tc::mbar_expect_tx(&full[stage], 2 * (ab ? C::STAGE / 2 : C::STAGE));   // both CTAs' loads
+            tc::mbar_expect_tx(&full[stage], CTAS * (ab ? C::STAGE / 2 : C::STAGE));   // (both CTAs' loads)
           uint8_t* at = smem + (size_t)stage * C::STAGE;
           auto load = [&](uint8_t* dst, const CUtensorMap* m, int mn, int row) {
-            if (mn) tc::tma_load_3d_pair(dst, m, fb, 0, kb * C::BK, row / 64);
-            else tc::tma_load_2d_pair(dst, m, fb, kb * C::BK, row);
+            if constexpr (kPair) {
+              if (mn) tc::tma_load_3d_pair(dst, m, fb, 0, kb * C::BK, row / 64);
+              else tc::tma_load_2d_pair(dst, m, fb, kb * C::BK, row);
+            } else {
+              if (mn) tma_load_3d(dst, m, &full[stage], 0, kb * C::BK, row / 64);
+              else tc::tma_load_2d(dst, m, &full[stage], kb * C::BK, row);
+            }
           };
 #pragma unroll
           for (int part = 0; part < (kFull ? 2 : 1); ++part) {
-            if (!ab) load(at + part * 2 * C::HALF, ma + part * LO, k.mn_a, arow);
-            load(at + part * 2 * C::HALF + C::HALF, mb + part * LO, k.mn_b, brow);
+            if (!ab) load(at + part * 2 * C::HALF, maps + MAP_A + part * MAPS, mn_a, arow);
+            load(at + part * 2 * C::HALF + C::HALF, maps + MAP_B + part * MAPS, mn_b, brow);
           }
           ++issued;
           if (++stage == STAGES) {
@@ -476,20 +602,26 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
           if (const int uses = ring_uses(issued, s, STAGES))
             tc::mbar_wait(&full[s], ring_last_parity(uses), &never);
       }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (rank == 0) {
+    } else if (warp == 1 && rank == 0) {
+      // ---------------------------------------------------------------- MMA issuer
       const uint32_t leader = tc::elect_leader();
+      auto mma = [&](uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+        if constexpr (kPair) umma_pair_by(leader, d, a, b, idesc, accumulate);
+        else tc::umma_f16_by(leader, d, a, b, idesc, accumulate);
+      };
+      auto commit = [&](uint64_t* bar) {
+        if constexpr (kPair) commit_pair_by(leader, bar);
+        else tc::umma_commit_by(leader, bar);
+      };
       int stage = 0, gsub = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += npairs) {
+      for (int t = unit; t < total && ok; t += units) {
         int q, ti, tj;
         tile_of(g, t, &q, &ti, &tj);
-        const bool ab = shared_ab(ti, tj);
+        const bool ab = shared_ab(g.task[q], ti, tj);
         const int kblocks = g.task[q].kblocks, mn_a = g.task[q].mn_a, mn_b = g.task[q].mn_b;
-        const uint32_t idesc = tc::make_idesc(0, 256, 256) | (mn_a ? tc::kIdescMnA : 0) |
+        const uint32_t idesc = tc::make_idesc(0, TILE, TILE) | (mn_a ? tc::kIdescMnA : 0) |
                                (mn_b ? tc::kIdescMnB : 0);
         // per 16 k: 32 bytes along a K-major row, two groups of 8 rows down an MN-major tile
         const uint64_t step_a = mn_a ? 2048 >> 4 : 32 >> 4, step_b = mn_b ? 2048 >> 4 : 32 >> 4;
@@ -504,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
             break;
           }
           tc::tc_fence_after();
-          const uint32_t d = tmem + (uint32_t)(buf * 256);
+          const uint32_t d = tmem + (uint32_t)(buf * TILE);
           const int kb1 = min(kblocks, kb0 + C::SUB);
           for (int kb = kb0; kb < kb1; ++kb) {
             if (!tc::mbar_wait(&full[stage], phase, abort_flag)) {
@@ -520,53 +652,89 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
 #pragma unroll
               for (int kk = 0; kk < C::BK / 16; ++kk) {
                 const uint64_t ak = a + kk * step_a, bk = b + kk * step_b;
-                umma_pair_by(leader, d, ak, bk + LO, idesc, kb > kb0 || kk > 0);
-                umma_pair_by(leader, d, ak + LO, bk, idesc, 1u);
+                mma(d, ak, bk + LO, idesc, kb > kb0 || kk > 0);
+                mma(d, ak + LO, bk, idesc, 1u);
               }
             }
 #pragma unroll
             for (int kk = 0; kk < C::BK / 16; ++kk)
-              umma_pair_by(leader, d, a + kk * step_a, b + kk * step_b, idesc, kFull || kb > kb0 || kk > 0);
-            commit_pair_by(leader, &empty[stage]);
+              mma(d, a + kk * step_a, b + kk * step_b, idesc, kFull || kb > kb0 || kk > 0);
+            commit(&empty[stage]);
             if (++stage == STAGES) {
               stage = 0;
               phase ^= 1;
             }
           }
-          if (ok) commit_pair_by(leader, &acc_full[buf]);
+          if (ok) commit(&acc_full[buf]);
         }
       }
       if (!ok || *abort_flag) {   // the products in flight end before TMEM and the tiles go
-        commit_pair_by(leader, drained);
+        commit(drained);
         volatile int never = 0;
         tc::mbar_wait(drained, 0, &never);
       }
     }
   } else {
     // -------------------------------------------------------------------- epilogue
+    if constexpr (kFull && kPair) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+    constexpr int CW = C::CW;
     const int qd = warp & 3;                 // TMEM lane quarter this warp may access
-    const int h = (warp - 2) >> 2;           // columns [128 h, 128 h + 128) of the tile
+    const int h = (warp - C::EPI0) >> 2;     // columns [CW h, CW h + CW) of the tile
     const int row = 32 * qd + lane;
-    const bool issuer = warp == 2 + 4 * h && lane == 0;
+    const bool issuer = qd == 0 && lane == 0;
     uint8_t* mybufs = bufs + h * C::NBUF * C::BUF;
-    const uint32_t acc_empty0 = tc::mapa(acc_empty, 0);
+    const uint32_t acc_empty0 = kPair ? tc::mapa(acc_empty, 0) : 0;
+    auto release = [&](int buf) {   // this warp has read the accumulator
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair) tc::mbar_arrive_remote(acc_empty0 + (uint32_t)(buf * sizeof(uint64_t)));
+        else tc::mbar_arrive(&acc_empty[buf]);
+      }
+    };
     int gsub = 0, turn = 0;
     bool ok = true;
-    for (int t = pair; t < total; t += npairs) {
+    for (int t = unit; t < total; t += units) {
       int q, ti, tj;
       tile_of(g, t, &q, &ti, &tj);
       const Task& k = g.task[q];
-      const int r0 = ti * 256 + (int)rank * 128, gr = r0 + row;
-      const int nsub = (k.kblocks + C::SUB - 1) / C::SUB;
+      const int kM = k.M, kN = k.N;
+      const int r0 = ti * TILE + (int)rank * 128, gr = r0 + row;
+      const int cols0 = tj * TILE + h * CW;
+      const uint32_t lane_tmem = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(h * CW);
+      // TO_WEIGHTS: 32 rows x 32 columns of W, loaded ahead of their use
+      float w_old[TO == TO_WEIGHTS ? 32 : 1];
+      auto load_weights = [&](int c0) {
+        if constexpr (TO == TO_WEIGHTS) {
+          const float* from = static_cast<const float*>(k.out) + (int64_t)(r0 + 32 * qd) * k.out_ld + c0 + lane;
+          const int rows = min(32, kM - (r0 + 32 * qd));
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            w_old[i] = i < rows && c0 + lane < kN ? from[(int64_t)i * k.out_ld] : 0.f;
+        }
+      };
+      load_weights(cols0);
+      // 64 columns of this thread's row of the matrix to add, likewise
+      // (full arithmetic has no registers to spare: there it is loaded when it is added)
+      uint4 add[TO == TO_MATRIX ? 8 : 1];
+      auto load_addend = [&](const __half* from, int c0) {
+        if constexpr (TO == TO_MATRIX) {
+          const uint4* at = reinterpret_cast<const uint4*>(from + (int64_t)gr * k.add_pitch + c0);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) add[j] = gr < kM && c0 < kN ? at[j] : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      if (TO == TO_MATRIX && !kFull && k.add_hi) load_addend(k.add_hi, cols0);
       float alpha = k.alpha;
       if (k.rpow) {
         const float r = __ldg(k.r);
         alpha *= k.rpow == 2 ? r * r : r;
       }
-      float sum[kFull ? 128 : 1];
+      float sum[kFull ? CW : 1];
       if constexpr (kFull) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        for (int i = 0; i < CW; ++i) sum[i] = 0.f;
+        const int nsub = (k.kblocks + C::SUB - 1) / C::SUB;
         for (int sub = 0; sub < nsub && ok; ++sub, ++gsub) {
           const int buf = gsub & 1, use = gsub >> 1;
           if (!tc::mbar_wait(&acc_full[buf], use & 1, abort_flag)) {
@@ -576,15 +744,13 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
           }
           tc::tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < CW / 32; ++c) {
             float v[32];
-            tc::tmem_ld32(tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(buf * 256 + h * 128 + c * 32), v);
+            tc::tmem_ld32(lane_tmem + (uint32_t)(buf * TILE + c * 32), v);
 #pragma unroll
             for (int i = 0; i < 32; ++i) sum[c * 32 + i] += v[i];
           }
-          tc::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive_remote(acc_empty0 + (uint32_t)(buf * sizeof(uint64_t)));
+          release(buf);
         }
       } else if (ok) {
         if (!tc::mbar_wait(&acc_full[gsub & 1], (gsub >> 1) & 1, abort_flag)) {
@@ -594,10 +760,10 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
         tc::tc_fence_after();
       }
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok && PH != PH_OUT) break;        // PH_OUT: the tiles from here on become NaN
+      if (!ok && TO != TO_OUT) break;        // TO_OUT: the tiles from here on become NaN
 #pragma unroll
-      for (int ch = 0; ch < 2; ++ch) {       // 64 columns at a time
-        const int c0 = tj * 256 + h * 128 + ch * 64;
+      for (int ch = 0; ch < CW / 64; ++ch) {       // 64 columns at a time
+        const int c0 = cols0 + ch * 64;
         float v[64];
         if constexpr (kFull) {
 #pragma unroll
@@ -605,18 +771,13 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
         } else {
           if (ok) {
             uint32_t w0[32], w1[32];
-            const uint32_t at =
-                tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)((gsub & 1) * 256 + h * 128 + ch * 64);
+            const uint32_t at = lane_tmem + (uint32_t)((gsub & 1) * TILE + ch * 64);
             tc::tmem_ld32_issue(at, w0);
             tc::tmem_ld32_issue(at + 32, w1);
             tc::tmem_ld_wait();
             tc::tmem_ld_use(w0);
             tc::tmem_ld_use(w1);
-            if (ch == 1) {
-              tc::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive_remote(acc_empty0 + (uint32_t)((gsub & 1) * sizeof(uint64_t)));
-            }
+            if (ch == CW / 64 - 1) release(gsub & 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               v[i] = __uint_as_float(w0[i]) * alpha;
@@ -627,8 +788,8 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
             for (int i = 0; i < 64; ++i) v[i] = 0.f;
           }
         }
-        if (c0 >= k.N || r0 >= k.M) continue;   // (the whole group)
-        if constexpr (kLast) {
+        if (c0 >= kN || r0 >= kM) continue;   // (the whole group)
+        if constexpr (TO != TO_MATRIX) {
           // 32 rows x 32 columns of the warp through shared memory, so that rows are written whole
           float* mine = reinterpret_cast<float*>(mybufs) + qd * 1024;
 #pragma unroll
@@ -641,49 +802,42 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
                               v[half * 32 + 4 * j + 3]);
             __syncwarp();
             const int c = c0 + half * 32 + lane;
-            const int rows = min(32, k.M - (r0 + 32 * qd));
-            TO* out = static_cast<TO*>(k.out) + (int64_t)(r0 + 32 * qd) * k.out_ld + c;
-            if (c < k.N) {
-#pragma unroll 8
-              for (int i = 0; i < rows; ++i) {
-                float x = mine[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)];
-                if constexpr (PH == PH_STEP) {
-                  const float w = to_f32<TO>(out[(int64_t)i * k.out_ld]);
-                  x = fmaf(-k.rate, x, k.keep * w);
-                } else if (!ok) {
-                  x = __int_as_float(0x7fffffff);
+            const int rows = min(32, kM - (r0 + 32 * qd));
+            T* out = static_cast<T*>(k.out) + (int64_t)(r0 + 32 * qd) * k.out_ld + c;
+            if (c < kN) {
+              const int64_t ld = k.out_ld;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (i < rows) {
+                  float x = mine[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)];
+                  if constexpr (TO == TO_WEIGHTS) x = fmaf(-k.rate, x, k.keep * w_old[i]);
+                  else if (!ok) x = __int_as_float(0x7fffffff);
+                  out[(int64_t)i * ld] = (T)x;
                 }
-                out[(int64_t)i * k.out_ld] = (TO)x;
               }
             }
+            if (ch * 2 + half + 1 < CW / 32) load_weights(c0 + half * 32 + 32);
           }
         } else {
-          if constexpr (PH == PH_POLY) {
-            if (gr < k.M) {
-              const __half* add = k.add_hi + (int64_t)gr * k.add_pitch + c0;
-              const __half* add_lo = kFull ? k.add_lo + (int64_t)gr * k.add_pitch + c0 : nullptr;
+          if (k.add_hi) {
+            const float beta = k.beta;
+#pragma unroll
+            for (int p = 0; p < (kFull ? 2 : 1); ++p) {
+              if (kFull) load_addend(p ? k.add_lo : k.add_hi, c0);
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
-                const uint4 w = *reinterpret_cast<const uint4*>(add + 8 * j);
-                const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+                const uint32_t e[4] = {add[j].x, add[j].y, add[j].z, add[j].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float2 f = unpack2(e[i]);
-                  v[8 * j + 2 * i] = fmaf(k.beta, f.x, v[8 * j + 2 * i]);
-                  v[8 * j + 2 * i + 1] = fmaf(k.beta, f.y, v[8 * j + 2 * i + 1]);
-                }
-                if constexpr (kFull) {
-                  const uint4 wl = *reinterpret_cast<const uint4*>(add_lo + 8 * j);
-                  const uint32_t el[4] = {wl.x, wl.y, wl.z, wl.w};
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const float2 f = unpack2(el[i]);
-                    v[8 * j + 2 * i] = fmaf(k.beta, f.x, v[8 * j + 2 * i]);
-                    v[8 * j + 2 * i + 1] = fmaf(k.beta, f.y, v[8 * j + 2 * i + 1]);
-                  }
+                  v[8 * j + 2 * i] = fmaf(beta, f.x, v[8 * j + 2 * i]);
+                  v[8 * j + 2 * i + 1] = fmaf(beta, f.y, v[8 * j + 2 * i + 1]);
                 }
               }
             }
+            if (!kFull && ch + 1 < CW / 64) load_addend(k.add_hi, c0 + 64);
+          }
+          if (ti == tj) {   // (diag is 0 where there is no identity to add)
 #pragma unroll
             for (int i = 0; i < 64; ++i)
               if (c0 + i == gr) v[i] += k.diag;
@@ -701,23 +855,25 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
                 w[i] = pack2(v[2 * i], v[2 * i + 1]);
               }
             }
-#pragma unroll
-            for (int mirror = 0; mirror < (kSym ? 2 : 1); ++mirror) {
-              if (mirror && ti == tj) continue;
-              uint8_t* buf = mybufs + (turn % C::NBUF) * C::BUF;
-              ++turn;
-              if (issuer) bulk_wait_read<C::NBUF - 1>();   // the buffer's last store has read it
-              group_sync(1 + h);
-              if (mirror) put_columns(buf, row, w);
-              else put_rows(buf, row, w);
-              tc::fence_proxy_async();
-              group_sync(1 + h);
-              if (issuer) {
-                if (mirror) tma_store_3d(&g.maps[q][1 + 3 * part], buf, 0, c0, r0 / 64);
-                else tma_store_2d(&g.maps[q][2 + 3 * part], buf, c0, r0);
-                bulk_commit();
-              }
+            __half* const other = k.upper ? (part ? k.mirror_lo : k.mirror_hi) : nullptr;
+            const int64_t pitch = k.mirror_pitch;
+            if (k.upper && ti == tj && !k.same_ab) {
+              if (c0 + 64 > r0 + 32 * qd)   // (all of the warp's are below it otherwise)
+                put_diagonal(other + gr * pitch + c0, other + c0 * pitch + (gr & ~1), pitch, gr, c0, kN, w);
+              continue;
             }
+            uint8_t* buf = mybufs + (turn % C::NBUF) * C::BUF;
+            ++turn;
+            if (issuer) bulk_wait_read<C::NBUF - 1>();   // the buffer's last store has read it
+            group_sync(1 + h);
+            put_rows(buf, row, w);
+            tc::fence_proxy_async();
+            group_sync(1 + h);
+            if (issuer) {
+              tma_store_2d(&g.maps[q][part * MAPS + MAP_STORE], buf, c0, r0);
+              bulk_commit();
+            }
+            if (k.upper && ti != tj) put_columns(other + c0 * pitch + (gr & ~1), pitch, gr < kM, min(64, kN - c0), w);
           }
         }
       }
@@ -727,8 +883,11 @@ __global__ void __launch_bounds__(Cfg<kFull>::THREADS, 1)
   }
   tc::tc_fence_before();
   __syncwarp();
-  tc::cluster_sync();   // every MMA of the pair has completed; no peer arrival is pending
-  if (warp == 1) tc::tmem_dealloc_pair(tmem, 512);
+  block_sync();   // every MMA has completed; no peer arrival is pending
+  if (warp == 1) {
+    if constexpr (kPair) tc::tmem_dealloc_pair(tmem, C::TMEM);
+    else tc::tmem_dealloc(tmem, C::TMEM);
+  }
 }
 
 // ------------------------------------------------------------------------------------ host
@@ -758,13 +917,17 @@ bool make_map(CUtensorMap* m, const __half* base, int rows, int cols, int pitch,
   return r == CUDA_SUCCESS;
 }
 
-// A call's polynomial: coefficients and the powers of two that the matrices are stored with.
+// A call's polynomial: coefficients, bounds, and how many steps the long matrices take on their
+// small side before X is formed.
 struct Plan {
   int steps = 0;
   double a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
-  double sx[kMaxSteps + 1], sl[kMaxSteps], sm[kMaxSteps];   // of X_k, L and M of step k
+  double u[kMaxSteps + 1], v[kMaxSteps];   // of the singular values before step k, of |M|
+  std::vector<int> groups;
 };
-double below_2_15(double bound) { return std::exp2(std::floor(std::log2(32000.0 / bound))); }
+// The power of two that brings a matrix of this bound below 2^15.
+double scale_of(double bound) { return std::exp2(std::floor(std::log2(32000.0 / bound))); }
+constexpr double kMaxGrowth = 150.0;   // of L's rounding within a group
 kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
   p->steps = d->steps;
   double u = 1.0;   // bound of the singular values, a little above what exact arithmetic gives
@@ -779,7 +942,7 @@ kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
       const double t = -b / (2.0 * c);
       if (t > 0.0 && t < u * u) v = std::max(v, poly(t));
     }
-    double next = std::sqrt(u * u) * poly(u * u);
+    double next = u * poly(u * u);
     // where a + 3 b t + 5 c t^2 = 0
     const double disc = 9.0 * b * b - 20.0 * a * c;
     double at[2];
@@ -797,21 +960,92 @@ kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
     p->a[k] = a;
     p->b[k] = b;
     p->c[k] = c;
-    p->sx[k] = k == 0 ? 1.0 : below_2_15(u);   // X_0's factor is r, on the device
-    p->sl[k] = below_2_15(u * u);
-    p->sm[k] = below_2_15(v);
+    p->u[k] = u;
+    p->v[k] = v;
     u = next;
   }
-  p->sx[d->steps] = 1.0;
+  p->u[d->steps] = u;
+  for (int k = 0; k < d->steps;) {
+    int g = 1;
+    double growth = p->v[k] * p->v[k];
+    while (k + g < d->steps && growth <= kMaxGrowth) {
+      growth *= p->v[k + g] * p->v[k + g];
+      ++g;
+    }
+    p->groups.push_back(g);
+    k += g;
+  }
   return KFAC_OK;
 }
 
+// Steps are grouped where X is long enough for that to pay.
+bool grouped(int s, int l) { return s >= 1024 && l >= s + s / 2; }
+
+enum { X_0, X_1, GRAM, TEMP, POLY, PROD_0, PROD_1, BUFFERS };
 struct Matrix {
-  int rows, cols, s, l, tall, xp, sp;    // pitches of X and of the s x s matrices
-  size_t x[2][2], gram[2], poly[2], part, r;   // [buffer][hi, lo]
-  int prep_blocks, tx;
+  int rows, cols, s, l, tall, group, xp, sp;    // pitches of X and of the s x s matrices
+  size_t at[BUFFERS][2], part, r;               // [buffer][hi, lo]
 };
+// X_1 where X is formed more than once; two s x s matrices, five where steps are grouped
+bool has_buffer(const Matrix& m, int steps, int b) {
+  switch (b) {
+    case X_0: case GRAM: case PROD_0: return true;
+    case X_1: return steps > 1;
+    default: return m.group;
+  }
+}
 int64_t pitch_of(int64_t cols) { return cdiv(cols, 64) * 64; }
+
+// One product of a matrix: buffers, scales; out BUFFERS: the call's result.
+struct Op {
+  int a, b, out, add;           // add: buffer or -1
+  double alpha, beta, diag;
+  int rpow, upper;
+};
+// A matrix's products, those of one entry at the same time.
+std::vector<std::vector<Op>> ops_of(const Plan& p, bool group) {
+  std::vector<std::vector<Op>> ops;
+  std::vector<int> sizes = group ? p.groups : std::vector<int>(p.steps, 1);
+  int x = X_0, k = 0;
+  for (int g : sizes) {
+    const bool first = k == 0, last = k + g == p.steps;
+    const double sx = first ? 1.0 : scale_of(p.u[k]);   // X_0's factor is r, on the device
+    double sl = scale_of(p.u[k] * p.u[k]);
+    ops.push_back({{x, x, GRAM, -1, sl / (sx * sx), 0.0, 0.0, first ? 2 : 0, 1}});
+    int prod = PROD_0;
+    double sp = 1.0, bound = 1.0;
+    for (int j = 0; j < g; ++j, ++k) {
+      const double sm = scale_of(p.v[k]);
+      const int poly = j == 0 ? PROD_0 : POLY;
+      ops.push_back({{GRAM, GRAM, poly, GRAM, sm * p.c[k] / (sl * sl), sm * p.b[k] / sl, sm * p.a[k], 0, 1}});
+      std::vector<Op> both;
+      bound *= p.v[k];
+      if (j == 0) {
+        sp = sm;
+      } else {   // P <- M P
+        const double to = scale_of(bound);
+        const int next = prod == PROD_0 ? PROD_1 : PROD_0;
+        both.push_back({POLY, prod, next, -1, to / (sm * sp), 0.0, 0.0, 0, 1});
+        prod = next;
+        sp = to;
+      }
+      if (j + 1 < g) {   // L <- (L M) M
+        const double st = scale_of(p.u[k] * p.u[k] * p.v[k]), to = scale_of(p.u[k + 1] * p.u[k + 1]);
+        both.push_back({GRAM, poly, TEMP, -1, st / (sl * sm), 0.0, 0.0, 0, 1});
+        ops.push_back(both);
+        ops.push_back({{TEMP, poly, GRAM, -1, to / (st * sm), 0.0, 0.0, 0, 1}});
+        sl = to;
+      } else if (!both.empty()) {
+        ops.push_back(both);
+      }
+    }
+    const double to = last ? 1.0 : scale_of(p.u[k]);
+    const int next = last ? BUFFERS : x == X_0 ? X_1 : X_0;
+    ops.push_back({{prod, x, next, -1, to / (sp * sx), 0.0, 0.0, first ? 1 : 0, 0}});
+    x = next;
+  }
+  return ops;
+}
 
 kfac_status check_sizes(const kfac_ortho_desc* d, int count, const int* rows, const int* cols) {
   if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16) ||
@@ -844,15 +1078,13 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
     m.s = std::min(rows[i], cols[i]);
     m.l = std::max(rows[i], cols[i]);
     m.tall = rows[i] > cols[i];
+    m.group = d->steps > 1 && grouped(m.s, m.l);
     if (m.s > 0) {
       m.xp = (int)pitch_of(m.cols);
       m.sp = (int)pitch_of(m.s);
-      for (int b = 0; b < (d->steps > 1 ? 2 : 1); ++b)
-        for (int h = 0; h < halves; ++h) m.x[b][h] = take((size_t)m.rows * m.xp * 2);
-      for (int h = 0; h < halves; ++h) {
-        m.gram[h] = take((size_t)m.s * m.sp * 2);
-        m.poly[h] = take((size_t)m.s * m.sp * 2);
-      }
+      for (int b = 0; b < BUFFERS; ++b)
+        for (int h = 0; h < halves && has_buffer(m, d->steps, b); ++h)
+          m.at[b][h] = take(b == X_0 || b == X_1 ? (size_t)m.rows * m.xp * 2 : (size_t)m.s * m.sp * 2);
       m.part = take(kPrepBlocks * 3 * sizeof(float));
       m.r = take(sizeof(float));
     }
@@ -872,29 +1104,47 @@ template <typename K> kfac_status allow_smem(OncePerDevice& once, K kern, size_t
   return KFAC_ERR_CUDA;
 }
 
-template <int PH, typename TO, bool kFull>
-kfac_status launch_product(const Launch<kFull>& g, cudaStream_t st) {
-  using C = Cfg<kFull>;
+template <int TO, typename T, bool kFull, bool kPair>
+kfac_status launch_tiles(const Launch<kFull>& g, cudaStream_t st) {
+  using C = Cfg<kFull, kPair>;
   static OncePerDevice once;
-  if (kfac_status e = allow_smem(once, ortho_product_kernel<PH, TO, kFull>, C::SMEM)) return e;
-  const int pairs = std::max(1, std::min(g.tile_start[g.count], num_sms() / 2));
+  if (kfac_status e = allow_smem(once, ortho_product_kernel<TO, T, kFull, kPair>, C::SMEM)) return e;
+  constexpr int CTAS = kPair ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.gridDim = dim3((unsigned)(CTAS * std::max(1, std::min(g.tile_start[g.count], num_sms() / CTAS))));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CTAS;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  cudaLaunchKernelEx(&cfg, ortho_product_kernel<PH, TO, kFull>, g);
+  cudaLaunchKernelEx(&cfg, ortho_product_kernel<TO, T, kFull, kPair>, g);
   count_launch();
   return check_launch();
+}
+// Numbers the tasks' tiles and launches them: pairs on 256 x 256 tiles, or, where these would be
+// fewer than half a tile per pair, single CTAs on 128 x 128 ones.
+template <int TO, typename T, bool kFull> kfac_status launch_product(Launch<kFull>& g, cudaStream_t st) {
+  auto number = [&](int tile) {
+    int64_t tiles = 0;
+    for (int i = 0; i < g.count; ++i) {
+      Task& t = g.task[i];
+      t.tiles_m = (int)cdiv(t.M, tile);
+      g.tile_start[i] = (int)tiles;
+      tiles += t.upper ? (int64_t)t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * cdiv(t.N, tile);
+    }
+    g.tile_start[g.count] = (int)tiles;
+    return tiles;
+  };
+  if (number(256) > num_sms() / 4) return launch_tiles<TO, T, kFull, true>(g, st);
+  number(128);
+  return launch_tiles<TO, T, kFull, false>(g, st);
 }
 
 // What a call works on, matrix by matrix.
@@ -909,12 +1159,12 @@ struct Call {
   const kfac_ortho_step* hp;    // null: orthogonalize
 };
 
-// The matrices of `idx` (at most kMaxGroup, none empty), all launches.
+// The matrices of `idx` (at most half of a launch's tasks, none empty), all launches.
 template <bool kFull>
 kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>& ms,
                       const std::vector<int>& idx, char* ws, cudaStream_t st) {
   const int n = (int)idx.size();
-  const int halves = kFull ? 2 : 1;
+  constexpr int halves = kFull ? 2 : 1;
   auto half_at = [&](size_t off) { return reinterpret_cast<__half*>(ws + off); };
   const bool bf16 = c.d->dtype == KFAC_BF16;
   const size_t es = bf16 ? 2 : 4;
@@ -928,8 +1178,8 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
       t.ldx = c.ldx[idx[i]];
       t.m = c.hp ? c.momentum[idx[i]] : nullptr;
       t.ldm = c.hp ? c.ldm[idx[i]] : 0;
-      t.hi = half_at(m.x[0][0]);
-      t.lo = kFull ? half_at(m.x[0][1]) : nullptr;
+      t.hi = half_at(m.at[X_0][0]);
+      t.lo = kFull ? half_at(m.at[X_0][1]) : nullptr;
       t.part = reinterpret_cast<float*>(ws + m.part);
       t.r = reinterpret_cast<float*>(ws + m.r);
       t.rows = m.rows;
@@ -942,9 +1192,10 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
       t.tx = 1;
       while (t.tx < pieces && t.tx < kPrepThreads) t.tx *= 2;
       g->block_start[i] = blocks;
-      // a few pieces per thread; one wave of the largest matrices
-      const int64_t rpb = kPrepThreads / t.tx, per = cdiv(pieces, t.tx);
-      blocks += (int)std::max<int64_t>(1, std::min<int64_t>(kPrepBlocks, cdiv((int64_t)m.rows * per, rpb * 4)));
+      // 4 to 16 pieces a thread, by the matrix alone: its norm is summed the same in every company
+      const int64_t rounds = cdiv((int64_t)m.rows, kPrepThreads / t.tx) * cdiv(pieces, t.tx);
+      const int64_t each = std::max<int64_t>(4, std::min<int64_t>(16, rounds / 256));
+      blocks += (int)std::min<int64_t>(kPrepBlocks, cdiv(rounds, each));
     }
     g->block_start[n] = blocks;
     g->count = n;
@@ -966,100 +1217,92 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
     count_launch(2);
     if (kfac_status e = check_launch()) return e;
   }
-  // every matrix's maps, once: X (two buffers) and the s x s matrices, in both kinds of boxes
+  // every buffer's maps, once, in both kinds of boxes
   struct Maps {
-    CUtensorMap x[2][2][2], gram[2][2], poly[2][2];   // [buffer][hi, lo][rows, chunks]
+    CUtensorMap of[BUFFERS][2][2];   // [hi, lo][rows, chunks]
   };
   std::vector<Maps> maps(n);
+  std::vector<std::vector<std::vector<Op>>> ops(n);
+  size_t rounds = 0;
   for (int i = 0; i < n; ++i) {
     const Matrix& m = ms[idx[i]];
-    for (int h = 0; h < halves; ++h) {
-      for (int k = 0; k < 2; ++k) {
-        for (int b = 0; b < (plan.steps > 1 ? 2 : 1); ++b)
-          if (!make_map(&maps[i].x[b][h][k], half_at(m.x[b][h]), m.rows, m.cols, m.xp, k)) return KFAC_ERR_CUDA;
-        if (!make_map(&maps[i].gram[h][k], half_at(m.gram[h]), m.s, m.s, m.sp, k) ||
-            !make_map(&maps[i].poly[h][k], half_at(m.poly[h]), m.s, m.s, m.sp, k))
-          return KFAC_ERR_CUDA;
-      }
+    for (int b = 0; b < BUFFERS; ++b) {
+      const bool x = b == X_0 || b == X_1;
+      for (int h = 0; h < halves && has_buffer(m, plan.steps, b); ++h)
+        for (int k = 0; k < (x ? 2 : 1); ++k)   // (only an X is read as MN-major tiles)
+          if (!make_map(&maps[i].of[b][h][k], half_at(m.at[b][h]), x ? m.rows : m.s, x ? m.cols : m.s,
+                        x ? m.xp : m.sp, k))
+            return KFAC_ERR_CUDA;
     }
+    ops[i] = ops_of(plan, m.group);
+    rounds = std::max(rounds, ops[i].size());
   }
+  // the matrices' products side by side, the last ones of all together in the last launch
   std::unique_ptr<Launch<kFull>> g(new Launch<kFull>());
-  for (int step = 0; step < plan.steps; ++step) {
-    const int cur = step & 1;
-    const bool last = step + 1 == plan.steps;
-    for (int ph = 0; ph < 3; ++ph) {
-      int tiles = 0;
-      for (int i = 0; i < n; ++i) {
-        const Matrix& m = ms[idx[i]];
-        Task& t = g->task[i];
+  for (size_t round = 0; round < rounds; ++round) {
+    g->count = 0;
+    const bool last = round + 1 == rounds;
+    for (int i = 0; i < n; ++i) {
+      if (round + ops[i].size() < rounds) continue;
+      const Matrix& m = ms[idx[i]];
+      for (const Op& op : ops[i][round + ops[i].size() - rounds]) {
+        Task& t = g->task[g->count];
+        CUtensorMap* to = g->maps[g->count++];
         t = Task{};
         t.r = reinterpret_cast<const float*>(ws + m.r);
-        const double sx = plan.sx[step], sl = plan.sl[step], sm = plan.sm[step];
-        for (int h = 0; h < halves; ++h) {
-          CUtensorMap* to = &g->maps[i][3 * h];
-          if (ph == 0) {
-            to[0] = maps[i].x[cur][h][m.tall];
-            to[1] = maps[i].gram[h][1];
-            to[2] = maps[i].gram[h][0];
-          } else if (ph == 1) {
-            to[0] = maps[i].gram[h][0];
-            to[1] = maps[i].poly[h][1];
-            to[2] = maps[i].poly[h][0];
-          } else {
-            to[0] = m.tall ? maps[i].x[cur][h][0] : maps[i].poly[h][0];
-            to[1] = m.tall ? maps[i].poly[h][0] : maps[i].x[cur][h][1];
-            if (!last) to[2] = maps[i].x[cur ^ 1][h][0];
-          }
-        }
-        if (ph == 0) {
+        t.alpha = (float)op.alpha;
+        t.beta = (float)op.beta;
+        t.diag = (float)op.diag;
+        t.rpow = op.rpow;
+        t.upper = op.upper;
+        t.same_ab = op.a == op.b;
+        int a = op.a, b = op.b;
+        if (op.upper) {
+          const bool x = a == X_0 || a == X_1;   // L = X X^T, or X^T X of a tall X
           t.M = t.N = m.s;
-          t.kblocks = (int)cdiv(m.l, 64);
-          t.mn_a = t.mn_b = m.tall;
-          t.alpha = (float)(sl / (sx * sx));
-          t.rpow = step == 0 ? 2 : 0;
-        } else if (ph == 1) {
-          t.M = t.N = m.s;
-          t.kblocks = (int)cdiv(m.s, 64);
-          t.alpha = (float)(sm * plan.c[step] / (sl * sl));
-          t.beta = (float)(sm * plan.b[step] / sl);
-          t.diag = (float)(sm * plan.a[step]);
-          t.add_hi = half_at(m.gram[0]);
-          t.add_lo = kFull ? half_at(m.gram[1]) : nullptr;
-          t.add_pitch = m.sp;
-        } else {
+          t.kblocks = (int)cdiv(x ? m.l : m.s, 64);
+          t.mn_a = t.mn_b = x && m.tall;
+        } else {                                 // P X, or X P of a tall X (P is symmetric)
           t.M = m.rows;
           t.N = m.cols;
           t.kblocks = (int)cdiv(m.s, 64);
-          t.mn_b = !m.tall;
-          t.alpha = (float)(plan.sx[step + 1] / (sm * sx));
-          t.rpow = step == 0 ? 1 : 0;
-          if (last) {
-            t.out = c.out[idx[i]];
-            t.out_ld = c.ldo[idx[i]];
-            if (c.hp) {
-              t.keep = (float)(1.0 - c.hp->lr * c.hp->weight_decay);
-              t.rate = (float)(c.hp->lr * c.hp->update_scale *
-                               std::sqrt(std::max(1.0, (double)m.rows / (double)m.cols)));
-            }
+          if (m.tall) std::swap(a, b);
+          else t.mn_b = 1;
+        }
+        if (op.add >= 0) {
+          t.add_hi = half_at(m.at[op.add][0]);
+          t.add_lo = kFull ? half_at(m.at[op.add][1]) : nullptr;
+          t.add_pitch = m.sp;
+        }
+        for (int h = 0; h < halves; ++h) {
+          to[h * MAPS + MAP_A] = maps[i].of[a][h][t.mn_a];
+          to[h * MAPS + MAP_B] = maps[i].of[b][h][t.mn_b];
+          if (op.out < BUFFERS) {
+            to[h * MAPS + MAP_STORE] = maps[i].of[op.out][h][0];
           }
         }
-        t.upper = ph < 2;
-        t.tiles_m = (int)cdiv(t.M, 256);
-        t.tiles_n = (int)cdiv(t.N, 256);
-        g->tile_start[i] = tiles;
-        tiles += t.upper ? t.tiles_m * (t.tiles_m + 1) / 2 : t.tiles_m * t.tiles_n;
+        if (op.upper) {
+          t.mirror_hi = half_at(m.at[op.out][0]);
+          t.mirror_lo = kFull ? half_at(m.at[op.out][1]) : nullptr;
+          t.mirror_pitch = m.sp;
+        }
+        if (op.out == BUFFERS) {
+          t.out = c.out[idx[i]];
+          t.out_ld = c.ldo[idx[i]];
+          if (c.hp) {
+            t.keep = (float)(1.0 - c.hp->lr * c.hp->weight_decay);
+            t.rate = (float)(c.hp->lr * c.hp->update_scale *
+                             std::sqrt(std::max(1.0, (double)m.rows / (double)m.cols)));
+          }
+        }
       }
-      g->tile_start[n] = tiles;
-      g->count = n;
-      kfac_status e;
-      if (ph == 0) e = launch_product<PH_GRAM, float, kFull>(*g, st);
-      else if (ph == 1) e = launch_product<PH_POLY, float, kFull>(*g, st);
-      else if (!last) e = launch_product<PH_APPLY, float, kFull>(*g, st);
-      else if (c.hp) e = launch_product<PH_STEP, float, kFull>(*g, st);
-      else if (bf16) e = launch_product<PH_OUT, __nv_bfloat16, kFull>(*g, st);
-      else e = launch_product<PH_OUT, float, kFull>(*g, st);
-      if (e) return e;
     }
+    kfac_status e;
+    if (!last) e = launch_product<TO_MATRIX, float, kFull>(*g, st);
+    else if (c.hp) e = launch_product<TO_WEIGHTS, float, kFull>(*g, st);
+    else if (bf16) e = launch_product<TO_OUT, __nv_bfloat16, kFull>(*g, st);
+    else e = launch_product<TO_OUT, float, kFull>(*g, st);
+    if (e) return e;
   }
   return KFAC_OK;
 }
@@ -1076,9 +1319,11 @@ kfac_status run(const Call& c, int count, const int* rows, const int* cols, void
   for (int i = 0; i < count; ++i)
     if (ms[i].s > 0) order.push_back(i);
   std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return ms[a].l > ms[b].l; });
-  for (size_t at = 0; at < order.size(); at += kMaxGroup) {
-    const std::vector<int> idx(order.begin() + at, order.begin() + std::min(order.size(), at + kMaxGroup));
-    kfac_status e = c.d->math == KFAC_ORTHO_FULL
+  const bool full = c.d->math == KFAC_ORTHO_FULL;
+  const size_t most = (full ? Launch<true>::TASKS : Launch<false>::TASKS) / 2;   // two tasks each, at times
+  for (size_t at = 0; at < order.size(); at += most) {
+    const std::vector<int> idx(order.begin() + at, order.begin() + std::min(order.size(), at + most));
+    kfac_status e = full
                         ? run_group<true>(c, plan, ms, idx, static_cast<char*>(workspace), st)
                         : run_group<false>(c, plan, ms, idx, static_cast<char*>(workspace), st);
     if (e) return e;

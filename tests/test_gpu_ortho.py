@@ -37,9 +37,9 @@ def _gradient(seed, rows, cols, dtype=F32, size=1e-4):
     return (size * ((randn(rows, r) * strong) @ randn(r, cols) / r ** 0.5 + 0.2 * randn(rows, cols))).to(dtype)
 
 
-def _tolerance(x, dtype, math, **kw):
+def _tolerance(x, dtype, math, groups=None, **kw):
     x = _np(x)
-    off = R.newton_schulz_fp16(x, **kw)
+    off = R.newton_schulz_fp16(x, groups=groups, **kw)
     ref = R.orthogonalize(x, **kw)
     off = off.T if x.shape[0] > x.shape[1] else off
     e = np.linalg.norm(off - ref) / np.linalg.norm(ref)
@@ -74,11 +74,34 @@ def test_orthogonalize(dtype, math, rows, cols):
     assert torch.equal(got, K.orthogonalize(x, math=math))   # the same bits
 
 
+@pytest.mark.parametrize("dtype,math", [(BF16, HALF), (F32, FULL), (F32, HALF)])
+@pytest.mark.parametrize("rows,cols", [(1024, 1600), (2100, 1030)])
+def test_long_matrices_take_steps_in_groups(dtype, math, rows, cols):
+    x = _gradient(rows + cols, rows, cols, dtype)
+    ref, tol = _tolerance(x, dtype, math, groups=(3, 2))
+    _check(K.orthogonalize(x, math=math), ref, tol)
+    if math == HALF and dtype is BF16:
+        # a first step that lifts small values more (L's rounding by 4.2^2 11.9 > 150): a group of two
+        co = [(4.2, -10.5, 7.35)] + [(3.4445, -4.7750, 2.0315)] * 2
+        want = R.orthogonalize(_np(x), 3, co)
+        # the roundings are those of the default's three; the first step lifts them 4.2 / 3.4445 times more
+        _, tol = _tolerance(x, dtype, math, groups=(2, 1), steps=3)
+        _check(K.orthogonalize(x, steps=3, coefficients=co), want, 4.2 / 3.4445 * tol)
+        # these would take singular values to 2.06, then to 45, then past every bound
+        with pytest.raises(K.KfacError, match="INVALID_ARG"):
+            K.orthogonalize(x, steps=3, coefficients=[(8.0, -20.0, 14.0)] + co[1:])
+        # one step alone, and steps that are not a whole number of groups
+        for steps, groups in ((1, (1,)), (4, (3, 1)), (7, (3, 3, 1))):
+            ref, tol = _tolerance(x, dtype, math, groups=groups, steps=steps)
+            _check(K.orthogonalize(x, steps=steps), ref, tol)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_many_matrices_at_once(dtype):
     """More than one launch takes, of all kinds, each as by itself; defaults by type."""
     rng = np.random.default_rng(0)
-    shapes = [tuple(rng.integers(1, 400, 2)) for _ in range(36)] + [(600, 90), (0, 5), (90, 700), (4, 0)]
+    shapes = [tuple(rng.integers(1, 400, 2)) for _ in range(36)] + [(600, 90), (0, 5), (90, 700), (4, 0),
+                                                                     (1024, 1536)]
     xs = [_gradient(i, *s, dtype) for i, s in enumerate(shapes)]
     ws = K.orthogonalize_workspace(xs)
     ws.fill_(255)         # whatever an earlier call left there: NaNs
