@@ -45,7 +45,7 @@
 #include <cmath>
 #include <cstring>
 #include <memory>
-#include <numeric>
+#include <type_traits>
 #include <vector>
 
 namespace kfac {
@@ -133,7 +133,7 @@ template <typename T, int N, bool kStep> struct Piece {
   }
   // kFresh: m is still the one before this step; it is updated and written.
   template <bool kFresh>
-  __device__ __forceinline__ void use(const PrepLaunch& l, const PrepTask& t, int64_t row, int c,
+  __device__ __forceinline__ void use(float mu, int nesterov, const PrepTask& t, int64_t row, int c,
                                       float (&u)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) u[i] = to_f32<T>(g.v[i]);
@@ -142,12 +142,12 @@ template <typename T, int N, bool kStep> struct Piece {
       for (int j = 0; j < N / F; ++j) {
         if (kFresh) {
 #pragma unroll
-          for (int i = 0; i < F; ++i) m[j].v[i] = fmaf(l.mu, m[j].v[i], u[j * F + i]);
+          for (int i = 0; i < F; ++i) m[j].v[i] = fmaf(mu, m[j].v[i], u[j * F + i]);
           *reinterpret_cast<Vec<float, F>*>(t.m + row * t.ldm + c + j * F) = m[j];
         }
 #pragma unroll
         for (int i = 0; i < F; ++i)
-          u[j * F + i] = l.nesterov ? fmaf(l.mu, m[j].v[i], u[j * F + i]) : m[j].v[i];
+          u[j * F + i] = nesterov ? fmaf(mu, m[j].v[i], u[j * F + i]) : m[j].v[i];
       }
     }
   }
@@ -171,7 +171,7 @@ __device__ __forceinline__ void each_piece(const PrepLaunch& l, const PrepTask& 
     for (int k = 0; k < AHEAD; ++k) {
       if (!ok[k]) continue;
       float u[N];
-      p[k].template use<kFresh>(l, t, row[k], c[k], u);
+      p[k].template use<kFresh>(l.mu, l.nesterov, t, row[k], c[k], u);
       f(row[k], c[k], u);
     }
     more = ok[AHEAD - 1];
@@ -180,31 +180,42 @@ __device__ __forceinline__ void each_piece(const PrepLaunch& l, const PrepTask& 
 
 // A thread's squares: plainly, unless its largest value says that they overflow or vanish; then of
 // the values times 2^-84 (from 2^40 on: 2^30 squares below 2^128) or 2^88 (below 2^-30, down to
-// 2^-149).  A value so small that its square vanishes beside a larger one is not missed.
-template <typename T, int N, bool kStep>
-__device__ __forceinline__ void sum_squares(const PrepLaunch& l, const PrepTask& t, int block, int blocks,
-                                            float (&sums)[3]) {
-  float mid = 0.f, top = 0.f;
-  each_piece<T, N, kStep, true>(l, t, block, blocks, [&](int64_t, int, const float (&u)[N]) {
+// 2^-149), in a second round.  A value so small that its square vanishes beside a larger one is
+// not missed.
+struct Squares {
+  float mid = 0.f, top = 0.f, scaled = 0.f;
+  template <int N> __device__ __forceinline__ void add(const float (&u)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       mid = fmaf(u[i], u[i], mid);
       top = fmaxf(top, fabsf(u[i]));
     }
-  });
-  sums[0] = sums[2] = 0.f;
-  if (top >= 0x1p40f || (top < 0x1p-30f && top > 0.f && mid == mid)) {   // (a NaN is in mid)
-    const bool big = top >= 0x1p40f;
-    const float by = big ? 0x1p-84f : 0x1p88f;
-    float sum = 0.f;
-    each_piece<T, N, kStep, false>(l, t, block, blocks, [&](int64_t, int, const float (&u)[N]) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) sum = fmaf(u[i] * by, u[i] * by, sum);
-    });
-    sums[big ? 0 : 2] = sum;
-    if (mid == mid) mid = 0.f;
   }
-  sums[1] = mid;
+  __device__ __forceinline__ bool big() const { return top >= 0x1p40f; }
+  __device__ __forceinline__ bool unsafe() const {   // (a NaN is in mid)
+    return big() || (top < 0x1p-30f && top > 0.f && mid == mid);
+  }
+  template <int N> __device__ __forceinline__ void add_scaled(const float (&u)[N]) {
+    const float by = big() ? 0x1p-84f : 0x1p88f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) scaled = fmaf(u[i] * by, u[i] * by, scaled);
+  }
+  // scale_factors' three sums
+  __device__ __forceinline__ void finish(float (&sums)[3]) const {
+    sums[0] = big() ? scaled : 0.f;
+    sums[1] = unsafe() && mid == mid ? 0.f : mid;
+    sums[2] = unsafe() && !big() ? scaled : 0.f;
+  }
+};
+template <typename T, int N, bool kStep>
+__device__ __forceinline__ void sum_squares(const PrepLaunch& l, const PrepTask& t, int block, int blocks,
+                                            float (&sums)[3]) {
+  Squares s;
+  each_piece<T, N, kStep, true>(l, t, block, blocks, [&](int64_t, int, const float (&u)[N]) { s.add(u); });
+  if (s.unsafe())
+    each_piece<T, N, kStep, false>(l, t, block, blocks,
+                                   [&](int64_t, int, const float (&u)[N]) { s.add_scaled(u); });
+  s.finish(sums);
 }
 
 template <typename T, bool kStep>
@@ -891,6 +902,10 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
   }
 }
 
+// --------------------------------------------------------------------------- small matrices
+
+#include "ortho_small.cuh"
+
 // ------------------------------------------------------------------------------------ host
 
 // [rows x cols] fp16 in rows of `pitch` (a multiple of 64): boxes of 64 columns x 128 rows, or
@@ -985,6 +1000,7 @@ bool grouped(int s, int l) { return s >= 1024 && l >= s + s / 2; }
 enum { X_0, X_1, GRAM, TEMP, POLY, PROD_0, PROD_1, BUFFERS };
 struct Matrix {
   int rows, cols, s, l, tall, group, xp, sp;    // pitches of X and of the s x s matrices
+  int cluster;                                  // not 0: blocks of the small matrices' kernel
   size_t at[BUFFERS][2], part, r;               // [buffer][hi, lo]
 };
 // X_1 where X is formed more than once; two s x s matrices, five where steps are grouped
@@ -1080,7 +1096,8 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
     m.l = std::max(rows[i], cols[i]);
     m.tall = rows[i] > cols[i];
     m.group = d->steps > 1 && grouped(m.s, m.l);
-    if (m.s > 0) {
+    if (m.s <= kSide) m.cluster = halves == 2 ? small_cluster<true>(m.l) : small_cluster<false>(m.l);
+    if (m.s > 0 && !m.cluster) {
       m.xp = (int)pitch_of(m.cols);
       m.sp = (int)pitch_of(m.s);
       for (int b = 0; b < BUFFERS; ++b)
@@ -1160,6 +1177,101 @@ struct Call {
   const kfac_ortho_step* hp;    // null: orthogonalize
 };
 
+// What the passes over x (and the momentum) need to know of matrix i of the call.
+PrepTask prep_task(const Call& c, const Matrix& m, int i) {
+  PrepTask t{};
+  t.x = c.x[i];
+  t.ldx = c.ldx[i];
+  t.m = c.hp ? c.momentum[i] : nullptr;
+  t.ldm = c.hp ? c.ldm[i] : 0;
+  t.rows = m.rows;
+  t.cols = m.cols;
+  const int n = c.d->dtype == KFAC_BF16 ? 8 : 4;
+  t.vec = m.cols % n == 0 && (uintptr_t)t.x % 16 == 0 && (m.rows == 1 || t.ldx % n == 0) &&
+          (!c.hp || ((uintptr_t)t.m % 16 == 0 && (m.rows == 1 || t.ldm % 4 == 0)));
+  const int pieces = (int)cdiv(m.cols, t.vec ? n : 1);
+  t.tx = 1;
+  while (t.tx < pieces && t.tx < kPrepThreads) t.tx *= 2;
+  return t;
+}
+float rate_of(const Call& c, const Matrix& m) {
+  return (float)(c.hp->lr * c.hp->update_scale * std::sqrt(std::max(1.0, (double)m.rows / (double)m.cols)));
+}
+float keep_of(const Call& c) { return (float)(1.0 - c.hp->lr * c.hp->weight_decay); }
+
+template <int TO, typename TI, typename T, bool kFull>
+kfac_status launch_small(const SmallLaunch& g, int count, cudaStream_t st) {
+  static OncePerDevice once;
+  using C = SmallCfg<kFull>;
+  if (kfac_status e = allow_smem(once, ortho_small_kernel<TO, TI, T, kFull>,
+                                 std::max(C::smem(C::most_tiles(1), 1), C::smem(C::most_tiles(8), 8))))
+    return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(count * g.cluster));
+  cfg.blockDim = dim3(kSmallThreads);
+  cfg.dynamicSmemBytes = C::smem(g.tiles, g.cluster);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)g.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaLaunchKernelEx(&cfg, ortho_small_kernel<TO, TI, T, kFull>, g);
+  count_launch();
+  return check_launch();
+}
+
+// The matrices with a side of at most kSide: a launch for each size of cluster.
+template <bool kFull>
+kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>& ms, cudaStream_t st) {
+  std::unique_ptr<SmallLaunch> g;
+  for (int cs = 1; cs <= 8; cs *= 2) {
+    for (size_t at = 0; at < ms.size();) {
+      int n = 0, longest = 0;
+      for (; at < ms.size() && n < kSmallTasks; ++at) {
+        const Matrix& m = ms[at];
+        if (m.cluster != cs || m.s == 0) continue;
+        if (!g) g.reset(new SmallLaunch());
+        SmallTask& t = g->task[n++];
+        t.in = prep_task(c, m, (int)at);
+        t.out = c.out[at];
+        t.ldo = c.ldo[at];
+        t.rate = c.hp ? rate_of(c, m) : 0.f;
+        longest = std::max(longest, m.l);
+      }
+      if (n == 0) continue;
+      g->steps = plan.steps;
+      for (int k = 0; k < plan.steps; ++k) {   // ops_of, steps one by one
+        const double sx = k == 0 ? 1.0 : scale_of(plan.u[k]), to = k + 1 == plan.steps ? 1.0 : scale_of(plan.u[k + 1]);
+        const double sl = scale_of(plan.u[k] * plan.u[k]), sm = scale_of(plan.v[k]);
+        g->step[k] = {(float)(sl / (sx * sx)), (float)(sm * plan.c[k] / (sl * sl)),
+                      (float)(sm * plan.b[k] / sl), (float)(sm * plan.a[k]), (float)(to / (sm * sx))};
+      }
+      g->cluster = cs;
+      // a matrix's columns are divided by its own length alone: the sums' order is the same in any company
+      g->tiles = cs == 1 ? (int)cdiv(longest, 64) : SmallCfg<kFull>::most_tiles(cs);
+      g->nesterov = c.hp ? c.hp->nesterov : 0;
+      g->mu = c.hp ? (float)c.hp->momentum : 0.f;
+      g->eps = (float)c.d->eps;
+      g->keep = c.hp ? keep_of(c) : 1.f;
+      kfac_status e;
+      const bool bf16 = c.d->dtype == KFAC_BF16;
+      if (c.hp)
+        e = bf16 ? launch_small<TO_WEIGHTS, __nv_bfloat16, float, kFull>(*g, n, st)
+                 : launch_small<TO_WEIGHTS, float, float, kFull>(*g, n, st);
+      else
+        e = bf16 ? launch_small<TO_OUT, __nv_bfloat16, __nv_bfloat16, kFull>(*g, n, st)
+                 : launch_small<TO_OUT, float, float, kFull>(*g, n, st);
+      if (e) return e;
+    }
+  }
+  return KFAC_OK;
+}
+
 // The matrices of `idx` (at most half of a launch's tasks, none empty), all launches.
 template <bool kFull>
 kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>& ms,
@@ -1175,23 +1287,13 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
     for (int i = 0; i < n; ++i) {
       const Matrix& m = ms[idx[i]];
       PrepTask& t = g->task[i];
-      t.x = c.x[idx[i]];
-      t.ldx = c.ldx[idx[i]];
-      t.m = c.hp ? c.momentum[idx[i]] : nullptr;
-      t.ldm = c.hp ? c.ldm[idx[i]] : 0;
+      t = prep_task(c, m, idx[i]);
       t.hi = half_at(m.at[X_0][0]);
       t.lo = kFull ? half_at(m.at[X_0][1]) : nullptr;
       t.part = reinterpret_cast<float*>(ws + m.part);
       t.r = reinterpret_cast<float*>(ws + m.r);
-      t.rows = m.rows;
-      t.cols = m.cols;
       t.pitch = m.xp;
-      const int vn = 16 / (int)es;
-      t.vec = m.cols % vn == 0 && (uintptr_t)t.x % 16 == 0 && (m.rows == 1 || t.ldx % vn == 0) &&
-              (!c.hp || ((uintptr_t)t.m % 16 == 0 && (m.rows == 1 || t.ldm % 4 == 0)));
-      const int pieces = (int)cdiv(m.cols, t.vec ? vn : 1);
-      t.tx = 1;
-      while (t.tx < pieces && t.tx < kPrepThreads) t.tx *= 2;
+      const int pieces = (int)cdiv(m.cols, t.vec ? 16 / (int)es : 1);
       g->block_start[i] = blocks;
       // 4 to 16 pieces a thread, by the matrix alone: its norm is summed the same in every company
       const int64_t rounds = cdiv((int64_t)m.rows, kPrepThreads / t.tx) * cdiv(pieces, t.tx);
@@ -1291,9 +1393,8 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
           t.out = c.out[idx[i]];
           t.out_ld = c.ldo[idx[i]];
           if (c.hp) {
-            t.keep = (float)(1.0 - c.hp->lr * c.hp->weight_decay);
-            t.rate = (float)(c.hp->lr * c.hp->update_scale *
-                             std::sqrt(std::max(1.0, (double)m.rows / (double)m.cols)));
+            t.keep = keep_of(c);
+            t.rate = rate_of(c, m);
           }
         }
       }
@@ -1318,7 +1419,10 @@ kfac_status run(const Call& c, int count, const int* rows, const int* cols, void
   // longest reductions first: the last round of tiles then holds the shortest
   std::vector<int> order;
   for (int i = 0; i < count; ++i)
-    if (ms[i].s > 0) order.push_back(i);
+    if (ms[i].s > 0 && !ms[i].cluster) order.push_back(i);
+  if (kfac_status e = c.d->math == KFAC_ORTHO_FULL ? run_small<true>(c, plan, ms, st)
+                                                   : run_small<false>(c, plan, ms, st))
+    return e;
   std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return ms[a].l > ms[b].l; });
   const bool full = c.d->math == KFAC_ORTHO_FULL;
   const size_t most = (full ? Launch<true>::TASKS : Launch<false>::TASKS) / 2;   // two tasks each, at times

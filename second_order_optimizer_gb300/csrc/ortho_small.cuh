@@ -1,0 +1,412 @@
+// Matrices whose smaller side is at most 128: all steps of one in one launch, X in shared memory.
+// Included by k_ortho.cu, inside its namespace.
+//
+// A matrix takes a cluster of 1, 2, 4 or 8 blocks; block b holds its columns (rows of a tall
+// matrix: X is G^T then) [b w, (b + 1) w) as an fp16 tile of 128 rows, padded with zeros.  Per step:
+//   L = X X^T      one 128 x 128 tcgen05 product per block; the blocks' parts are added in fp32 through
+//                  distributed shared memory, each block a share of the columns, in the blocks' order
+//   M = a I + b L + c L^2   by every block
+//   X <- M X       by every block, its columns (X is the K-major operand above and, as it lies, the
+//                  MN-major one here)
+// What bounds it is the chain: three products, three passes through TMEM and registers and, with
+// several blocks, two cluster barriers per step.  A product launch per step and product (the
+// large matrices' form) pays 6 to 8 us for each.
+
+constexpr int kSide = 128;
+constexpr int kSmallThreads = 256;
+constexpr int kSmallTasks = 64;                  // matrices per launch
+constexpr int kTileBytes = kSide * 64 * 2;       // 128 rows x 64 columns
+
+struct SmallTask {
+  PrepTask in;                                   // (x, m and their layout alone)
+  void* out;                                     // the direction or the weights
+  int64_t ldo;
+  float rate;
+};
+struct SmallStep { float gram, poly, beta, diag, apply; };
+struct SmallLaunch {
+  SmallTask task[kSmallTasks];
+  SmallStep step[kMaxSteps];
+  int steps, cluster, tiles;                     // tiles: of 64 columns per block
+  int nesterov;
+  float mu, eps, keep;
+};
+
+template <bool kFull> struct SmallCfg {
+  static constexpr int HALVES = kFull ? 2 : 1;
+  // columns per block: what shared memory holds beside L (or M) and, in a cluster, the parts of L
+  static constexpr int most_tiles(int cluster) { return kFull ? (cluster > 1 ? 3 : 4) : 8; }
+  static constexpr size_t smem(int tiles, int cluster) {
+    return 1024 + (size_t)HALVES * (tiles + 2) * kTileBytes + (cluster > 1 ? kSide * kSide * 4 : 0);
+  }
+  static_assert(smem(most_tiles(1), 1) <= 231424 && smem(most_tiles(8), 8) <= 231424, "shared memory");
+};
+
+__device__ __forceinline__ void st_cluster_f4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
+__device__ __forceinline__ void st_cluster_u2(uint32_t addr, uint32_t a, uint32_t b) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// Offset of (row, column) in tiles of 128 rows x 64 columns, 128-byte swizzle.
+__device__ __forceinline__ int tile_offset(int row, int col) {
+  return (col >> 6) * kTileBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+template <int TO, typename TI, typename T, bool kFull>
+__global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __grid_constant__ SmallLaunch g) {
+  constexpr bool kStep = TO == TO_WEIGHTS;
+  constexpr int HALVES = kFull ? 2 : 1;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float red[3][kSmallThreads / 32];
+  __shared__ float parts[8][3];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* const xs = smem;                                            // [halves][tiles]
+  uint8_t* const ls = xs + (size_t)HALVES * g.tiles * kTileBytes;      // [halves][2]: L, then M
+  float* const recv = reinterpret_cast<float*>(ls + HALVES * 2 * kTileBytes);   // [src][column / 4][row][4]
+  const int x_lo = g.tiles * kTileBytes, l_lo = 2 * kTileBytes;        // from a hi tile to its lo tile
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int cs = g.cluster, rank = (int)(blockIdx.x % cs);
+  const SmallTask& task = g.task[blockIdx.x / cs];
+  const PrepTask& t = task.in;
+  const bool tall = t.rows > t.cols;
+  const int s = tall ? t.cols : t.rows, l = tall ? t.rows : t.cols;
+  const int l0 = rank * g.tiles * 64, width = max(0, min(l - l0, g.tiles * 64));
+  const int used = (width + 63) / 64;                                  // tiles with columns
+
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&done, 1);
+    abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(&tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < HALVES * g.tiles * kTileBytes / 16; i += kSmallThreads)
+    reinterpret_cast<uint4*>(xs)[i] = make_uint4(0u, 0u, 0u, 0u);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+  bool ok = true;
+  uint32_t phase = 0;
+  auto cluster_sync = [&]() {
+    if (cs > 1) tc::cluster_sync();
+    else __syncthreads();
+  };
+
+  // ------------------------------------------------------------------ norm, X_0
+  // f(row of X, column of X in this block, values) for this block's part of the matrix; values run
+  // along the columns of X, or (tall) along its rows
+  auto visit = [&](auto n_, auto fresh, auto f) {
+    constexpr int N = decltype(n_)::value;
+    const int per = ((tall ? s : width) + N - 1) / N;
+    const int total = per * (tall ? width : s);
+    constexpr int AHEAD = 4;
+    for (int i = threadIdx.x; i < total; i += AHEAD * kSmallThreads) {
+      Piece<TI, N, kStep> p[AHEAD];
+      int row[AHEAD], c[AHEAD];
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        const int at = i + k * kSmallThreads;
+        if (at >= total) continue;
+        row[k] = at / per;
+        c[k] = (at - row[k] * per) * N;
+        p[k].load(t, row[k] + (tall ? l0 : 0), c[k] + (tall ? 0 : l0));
+      }
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) {
+        if (i + k * kSmallThreads >= total) continue;
+        float u[N];
+        p[k].template use<decltype(fresh)::value>(g.mu, g.nesterov, t, row[k] + (tall ? l0 : 0),
+                                                  c[k] + (tall ? 0 : l0), u);
+        f(row[k], c[k], u);
+      }
+    }
+  };
+  auto visit_by = [&](auto fresh, auto f) {
+    if (t.vec) visit(std::integral_constant<int, 16 / (int)sizeof(TI)>(), fresh, f);
+    else visit(std::integral_constant<int, 1>(), fresh, f);
+  };
+  float up0, up1, r;
+  {
+    Squares sq;
+    visit_by(std::true_type(), [&](int, int, auto& u) { sq.add(u); });
+    if (sq.unsafe()) visit_by(std::false_type(), [&](int, int, auto& u) { sq.add_scaled(u); });
+    float v[3];
+    sq.finish(v);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+      if (lane == 0) red[k][warp] = v[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+      float sum = 0.f;
+      for (int w = 0; w < kSmallThreads / 32; ++w) sum += red[threadIdx.x][w];
+      for (int c = 0; c < cs; ++c)   // to every block of the cluster
+        tc::st_cluster_u32(tc::mapa(&parts[rank][threadIdx.x], (uint32_t)c), __float_as_uint(sum));
+    }
+    cluster_sync();
+    double sums[3] = {0.0, 0.0, 0.0};
+    for (int c = 0; c < cs; ++c)
+      for (int k = 0; k < 3; ++k) sums[k] += (double)parts[c][k];
+    float up[2];
+    scale_factors(sums, g.eps, up, &r);
+    up0 = up[0];
+    up1 = up[1];
+  }
+  visit_by(std::false_type(), [&](int row, int c, auto& u) {
+    constexpr int n = sizeof(u) / sizeof(float);
+    Vec<__half, n> hi, lo;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float v = u[i] * up0 * up1;
+      hi.v[i] = __float2half_rn(v);
+      if (kFull) lo.v[i] = __float2half_rn(v - __half2float(hi.v[i]));
+    }
+    if (!tall) {
+      *reinterpret_cast<Vec<__half, n>*>(xs + tile_offset(row, c)) = hi;
+      if (kFull) *reinterpret_cast<Vec<__half, n>*>(xs + x_lo + tile_offset(row, c)) = lo;
+    } else {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        *reinterpret_cast<__half*>(xs + tile_offset(c + i, row)) = hi.v[i];
+        if (kFull) *reinterpret_cast<__half*>(xs + x_lo + tile_offset(c + i, row)) = lo.v[i];
+      }
+    }
+  });
+
+  // --------------------------------------------------------------------- steps
+  const uint32_t xa = tc::smem_u32(xs), la = tc::smem_u32(ls);
+  // what the threads wrote is visible to the tensor core, and what they read of TMEM may go;
+  // then `issue` by one lane of warp 0, and everyone waits for its products
+  auto products = [&](auto issue) {
+    tc::fence_proxy_async();
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+      tc::tc_fence_after();
+      const uint32_t leader = tc::elect_leader();
+      issue(leader);
+      tc::umma_commit_by(leader, &done);
+      __syncwarp();
+    }
+    if (ok && !tc::mbar_wait(&done, phase, &abort_flag)) {
+      ok = false;
+      report_error(&g_status, KFAC_ERR_TIMEOUT, -1, 46);
+      *(volatile int*)&abort_flag = 1;
+    }
+    phase ^= 1;
+    ok = __syncthreads_and(ok);   // one that gave up is joined by all: the barriers below stay whole
+    tc::tc_fence_after();
+  };
+  constexpr uint32_t kSquare = tc::make_idesc(0, kSide, kSide);
+  // hi hi, and in full arithmetic hi lo and lo hi before it
+  auto mma = [&](uint32_t leader, uint32_t d, uint64_t a, uint64_t b, int a_lo, int b_lo, uint32_t idesc,
+                 int pass, uint32_t acc) {
+    if (!kFull || pass == 1) {
+      tc::umma_f16_by(leader, d, a, b, idesc, acc);
+    } else {
+      tc::umma_f16_by(leader, d, a, b + (uint64_t)(b_lo >> 4), idesc, acc);
+      tc::umma_f16_by(leader, d, a + (uint64_t)(a_lo >> 4), b, idesc, 1u);
+    }
+  };
+  const int qd = warp & 3, h = warp >> 2;                  // TMEM quarter, column half
+  const int row = 32 * qd + lane;                          // of X, L and M
+  const uint32_t lane_tmem = tmem + ((uint32_t)(32 * qd) << 16);
+  auto load64 = [&](int col, float (&v)[64]) {
+    uint32_t w0[32], w1[32];
+    tc::tmem_ld32_issue(lane_tmem + (uint32_t)col, w0);
+    tc::tmem_ld32_issue(lane_tmem + (uint32_t)col + 32, w1);
+    tc::tmem_ld_wait();
+    tc::tmem_ld_use(w0);
+    tc::tmem_ld_use(w1);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = __uint_as_float(w0[i]);
+      v[32 + i] = __uint_as_float(w1[i]);
+    }
+  };
+  // 64 values of this thread's row to a tile as hi (and lo) halves
+  auto store64 = [&](uint8_t* tile, int lo, const float (&v)[64]) {
+    uint32_t w[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
+    put_rows(tile, row, w);
+    if constexpr (kFull) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float2 hi = unpack2(w[i]);
+        w[i] = pack2(v[2 * i] - hi.x, v[2 * i + 1] - hi.y);
+      }
+      put_rows(tile + lo, row, w);
+    }
+  };
+  const int k16 = (s + 15) / 16;                           // of the small side
+  for (int step = 0; step < g.steps; ++step) {
+    const SmallStep p = g.step[step];
+    const bool last = step + 1 == g.steps;
+    // ---- L: this block's part
+    products([&](uint32_t leader) {
+      for (int pass = kFull ? 0 : 1; pass < 2; ++pass)
+        for (int c = 0; c < used; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t a = tc::sdesc_kmajor_sw128(xa + c * kTileBytes + kk * 32);
+            mma(leader, tmem, a, a, x_lo, x_lo, kSquare, pass, c > 0 || kk > 0 || (kFull && pass == 1));
+          }
+    });
+    const float gram = step == 0 ? p.gram * r * r : p.gram;
+    float v[64];
+    if (used > 0) {
+      load64(64 * h, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] = 0.f;
+    }
+    if (cs == 1) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] *= gram;
+      store64(ls + h * kTileBytes, l_lo, v);
+    } else {
+      const int own = kSide / cs;                          // columns that a block adds up
+#pragma unroll
+      for (int i = 0; i < 64; i += 4) {
+        const int col = 64 * h + i, to = col / own, group = (col - to * own) / 4;
+        const float* at = recv + (((rank * (own / 4) + group) * kSide) + row) * 4;
+        st_cluster_f4(tc::mapa(at, (uint32_t)to), v[i], v[i + 1], v[i + 2], v[i + 3]);
+      }
+      tc::cluster_sync();
+      const int mine = threadIdx.x % kSide;
+      for (int group = threadIdx.x / kSide; group < own / 4; group += kSmallThreads / kSide) {
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < cs; ++c) {
+          const float4 q = *reinterpret_cast<const float4*>(
+              recv + (((c * (own / 4) + group) * kSide) + mine) * 4);
+          sum.x += q.x;
+          sum.y += q.y;
+          sum.z += q.z;
+          sum.w += q.w;
+        }
+        const float q[4] = {sum.x * gram, sum.y * gram, sum.z * gram, sum.w * gram};
+        const uint32_t a = pack2(q[0], q[1]), b = pack2(q[2], q[3]);
+        uint8_t* at = ls + tile_offset(mine, rank * own + group * 4);
+        for (int c = 0; c < cs; ++c) st_cluster_u2(tc::mapa(at, (uint32_t)c), a, b);
+        if constexpr (kFull) {
+          const float2 ha = unpack2(a), hb = unpack2(b);
+          const uint32_t al = pack2(q[0] - ha.x, q[1] - ha.y), bl = pack2(q[2] - hb.x, q[3] - hb.y);
+          for (int c = 0; c < cs; ++c) st_cluster_u2(tc::mapa(at + l_lo, (uint32_t)c), al, bl);
+        }
+      }
+      // (also: every block has read its parts before the next step's arrive)
+      tc::cluster_sync();
+    }
+    // ---- M, over L
+    products([&](uint32_t leader) {
+      for (int pass = kFull ? 0 : 1; pass < 2; ++pass)
+        for (int k = 0; k < k16; ++k) {
+          const uint64_t a = tc::sdesc_kmajor_sw128(la + (k / 4) * kTileBytes + (k % 4) * 32);
+          mma(leader, tmem, a, a, l_lo, l_lo, kSquare, pass, k > 0 || (kFull && pass == 1));
+        }
+    });
+    load64(64 * h, v);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) v[i] *= p.poly;
+    for (int half = 0; half < HALVES; ++half) {
+      const uint8_t* from = ls + half * l_lo + h * kTileBytes;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 q = *reinterpret_cast<const uint4*>(from + row * 128 + ((j ^ (row & 7)) << 4));
+        const uint32_t e[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack2(e[i]);
+          v[8 * j + 2 * i] = fmaf(p.beta, f.x, v[8 * j + 2 * i]);
+          v[8 * j + 2 * i + 1] = fmaf(p.beta, f.y, v[8 * j + 2 * i + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if (64 * h + i == row) v[i] += p.diag;
+    store64(ls + h * kTileBytes, l_lo, v);
+    // ---- X
+    products([&](uint32_t leader) {
+      for (int pass = kFull ? 0 : 1; pass < 2; ++pass)
+        for (int k = 0; k < k16; ++k) {
+          const uint64_t a = tc::sdesc_kmajor_sw128(la + (k / 4) * kTileBytes + (k % 4) * 32);
+          for (int c = 0; c < used; c += 4) {
+            const uint64_t b = tc::sdesc_mnmajor_sw128(xa + c * kTileBytes + k * 2048, kTileBytes);
+            mma(leader, tmem + (uint32_t)(64 * c), a, b, l_lo, x_lo,
+                tc::make_idesc(0, kSide, 64 * min(4, used - c)) | tc::kIdescMnB, pass,
+                k > 0 || (kFull && pass == 1));
+          }
+        }
+    });
+    const float apply = step == 0 ? p.apply * r : p.apply;
+    for (int c = h; c < used; c += 2) {
+      load64(64 * c, v);
+#pragma unroll
+      for (int i = 0; i < 64; ++i) v[i] *= apply;
+      if (!last) {
+        store64(xs + c * kTileBytes, x_lo, v);
+        continue;
+      }
+      auto emit = [&](T* at, float x) {
+        if constexpr (TO == TO_WEIGHTS) {
+          if (ok) *at = fmaf(-task.rate, x, g.keep * *at);
+        } else {
+          *at = (T)(ok ? x : __int_as_float(0x7fffffff));
+        }
+      };
+      if (tall) {                          // lanes along the rows of out
+        T* at = static_cast<T*>(task.out) + (int64_t)(l0 + 64 * c) * task.ldo + row;
+        const int n = min(64, width - 64 * c);
+        if (row < s) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < n) emit(at + (int64_t)i * task.ldo, v[i]);
+        }
+      } else {                             // through the space of M: rows of out in whole pieces
+        float* mine = reinterpret_cast<float*>(ls) + warp * 1024;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(mine + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                make_float4(v[half * 32 + 4 * j], v[half * 32 + 4 * j + 1], v[half * 32 + 4 * j + 2],
+                            v[half * 32 + 4 * j + 3]);
+          __syncwarp();
+          const int col = 64 * c + half * 32 + lane, rows = min(32, s - 32 * qd);
+          T* at = static_cast<T*>(task.out) + (int64_t)(32 * qd) * task.ldo + l0 + col;
+          if (col < width) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < rows)
+                emit(at + (int64_t)i * task.ldo, mine[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)]);
+          }
+        }
+      }
+    }
+  }
+  tc::tc_fence_before();
+  cluster_sync();   // no block's shared memory goes while another may write to it
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
+}
+
+// Blocks in a cluster for a matrix of this long side (0: too long).
+template <bool kFull> int small_cluster(int l) {
+  for (int cs = 1; cs <= 8; cs *= 2)
+    if (l <= cs * SmallCfg<kFull>::most_tiles(cs) * 64) return cs;
+  return 0;
+}

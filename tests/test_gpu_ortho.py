@@ -57,9 +57,11 @@ def no_device_error():
     assert K.operator_status() == (0, 0)
 
 
-# a lone element, vectors, one tile and its borders, several tiles of either orientation
+# a lone element, vectors; up to 128 on one side by one block and by clusters of two, four and eight,
+# and too long for them; one tile and its borders, several tiles of either orientation
 SIZES = [(1, 1), (1, 7), (9, 1), (5, 3), (16, 16), (40, 64), (64, 65), (33, 100), (100, 33), (128, 128),
-         (130, 500), (256, 256), (257, 300), (300, 257), (513, 1000), (1000, 513), (520, 2100), (2100, 260)]
+         (128, 512), (129, 512), (128, 513), (77, 1000), (1024, 100), (128, 1025), (2047, 65), (17, 2049),
+         (128, 4096), (4096, 9), (4097, 40), (130, 500), (256, 256), (257, 300), (300, 257), (513, 1000), (1000, 513), (520, 2100), (2100, 260)]
 
 
 @pytest.mark.parametrize("dtype,math", [(BF16, HALF), (F32, FULL), (F32, HALF), (BF16, FULL)])
@@ -132,19 +134,22 @@ def test_steps_and_coefficients():
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strides_and_in_place(dtype):
     wide = _gradient(1, 300, 500, dtype)
-    x = wide[:, 3:180]                       # rows of odd alignment
-    want = K.orthogonalize(x.contiguous())
-    out = torch.full((300, 200), 7.0, device="cuda", dtype=dtype)
-    assert torch.equal(K.orthogonalize(x, out=out[:, 5:182]), want)
-    assert (out[:, :5] == 7).all() and (out[:, 182:] == 7).all()
-    rest = wide[:, 180:].clone()
-    K.orthogonalize(x, out=x)
-    assert torch.equal(x, want) and torch.equal(wide[:, 180:], rest)
+    for rows in (300, 60):
+        x = wide[:rows, 3:180]               # rows of odd alignment
+        want = K.orthogonalize(x.contiguous())
+        out = torch.full((rows + 1, 200), 7.0, device="cuda", dtype=dtype)
+        assert torch.equal(K.orthogonalize(x, out=out[:rows, 5:182]), want)
+        assert (out[:, :5] == 7).all() and (out[:, 182:] == 7).all() and (out[rows] == 7).all()
+        rest = wide[:, 180:].clone()
+        K.orthogonalize(x, out=x)
+        assert torch.equal(x, want) and torch.equal(wide[:, 180:], rest)
+        wide = _gradient(2, 300, 500, dtype)
 
 
 @pytest.mark.parametrize("size", [1e-42, 1e-30, 1e-12, 1e12, 1e30])
-def test_scale_of_the_matrix_does_not_matter(size):
-    x = _gradient(1, 65, 40, size=1.0)
+@pytest.mark.parametrize("rows,cols", [(65, 40), (50, 700), (140, 200)])
+def test_scale_of_the_matrix_does_not_matter(size, rows, cols):
+    x = _gradient(1, rows, cols, size=1.0)
     x = (x.double() * size).float()
     ref = R.orthogonalize(_np(x), eps=0.0)    # (1e-42: denormals, the few bits that they have)
     _, tol = _tolerance(x, F32, FULL, eps=0.0)
@@ -153,22 +158,23 @@ def test_scale_of_the_matrix_does_not_matter(size):
 
 @pytest.mark.parametrize("math", [FULL, HALF])
 def test_zeros_and_what_is_not_finite_stay_where_they_are(math):
-    xs = [_gradient(i, 150, 70) for i in range(5)]
-    xs[1].zero_()
-    xs[2][149, 69] = float("nan")
-    xs[3][0, 1] = float("inf")
-    got = K.orthogonalize(xs, math=math)
-    assert (got[1] == 0).all() and torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
-    for i in (0, 4):
-        assert torch.equal(got[i], K.orthogonalize(xs[i], math=math))
-    assert (K.orthogonalize(xs[1], eps=0.0, math=math) == 0).all()
+    for rows, cols in ((150, 70), (150, 170), (60, 1000)):
+        xs = [_gradient(i, rows, cols) for i in range(5)]
+        xs[1].zero_()
+        xs[2][rows - 1, cols - 1] = float("nan")
+        xs[3][0, 1] = float("inf")
+        got = K.orthogonalize(xs, math=math)
+        assert (got[1] == 0).all() and torch.isnan(got[2]).all() and torch.isnan(got[3]).all()
+        for i in (0, 4):
+            assert torch.equal(got[i], K.orthogonalize(xs[i], math=math))
+        assert (K.orthogonalize(xs[1], eps=0.0, math=math) == 0).all()
 
 
 @pytest.mark.parametrize("nesterov", [True, False])
 @pytest.mark.parametrize("dtype,math", [(F32, None), (F32, HALF), (BF16, None)])
 def test_step(dtype, math, nesterov):
     """Two steps of several matrices; rows of any alignment."""
-    shapes = [(64, 64), (10, 300), (300, 33), (257, 256)]
+    shapes = [(64, 64), (10, 300), (300, 33), (257, 256), (90, 1100), (700, 120)]
     kw = dict(lr=0.05, momentum=0.9, weight_decay=0.1, nesterov=nesterov, update_scale=0.7)
     gs = [[_gradient(10 * k + i, *s, dtype) for i, s in enumerate(shapes)] for k in range(2)]
     ms = [_gradient(50 + i, *s) for i, s in enumerate(shapes)]
@@ -199,6 +205,9 @@ def test_step(dtype, math, nesterov):
 def test_streams_and_graphs():
     """On another stream; two captured calls with workspaces of their own, replayed in turn."""
     xs = [_gradient(i, 200, 300, BF16) for i in range(2)]
+    small = _gradient(5, 40, 900, BF16)
+    done = torch.empty_like(small)
+    once = K.orthogonalize(small)
     want = [K.orthogonalize(x) for x in xs]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -210,7 +219,7 @@ def test_streams_and_graphs():
         out = torch.empty_like(x)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            K.orthogonalize(x, out=out)
+            K.orthogonalize([x, small], out=[out, done])
         graphs.append((g, out))
     for _ in range(3):
         for g, out in graphs:
@@ -218,6 +227,7 @@ def test_streams_and_graphs():
             g.replay()
     for (_, out), w in zip(graphs, want):
         assert torch.equal(out, w)
+    assert torch.equal(done, once)
     xs[0].copy_(xs[1])       # a replay reads the present values
     graphs[0][0].replay()
     assert torch.equal(graphs[0][1], want[1])
@@ -236,4 +246,5 @@ def test_python_refusals():
     with pytest.raises(ValueError, match="2-D|rows, columns"):
         K.orthogonalize(x[0])
     with pytest.raises(K.KfacError, match="WORKSPACE"):
-        K.orthogonalize(x, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        K.orthogonalize(torch.zeros(150, 200, device="cuda"),
+                        workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -274,15 +274,18 @@ def test_orthogonalize_limits_and_workspace(lib):
     assert _ortho(lib, count=0) == 0 and _ortho(lib, step=True, count=0) == 0
     assert _ortho(lib, rows=(0, 5), cols=(3, 0), x=(None, None), ws=None) == 0   # nothing to do
     assert _ortho(lib, rows=(32769, 4)) == U
-    assert [_ortho(lib, ws=None), _ortho(lib, ws=P + 128), _ortho(lib, nb=512)] == [W] * 3
+    big = dict(rows=(200, 4), cols=(300, 4), ldx=(300, 4), ldo=(300, 4))
+    assert [_ortho(lib, ws=None, **big), _ortho(lib, ws=P + 128, **big), _ortho(lib, nb=512, **big)] == [W] * 3
     n = ctypes.c_size_t(0)
     one = (ctypes.c_int * 1)
     size = lambda math, r, c: (lib.LIB.kfac_orthogonalize_workspace_size(
         lib.ORTHO_DESC.pack(1, math, 5, 0.0, 0), 1, one(r), one(c), ctypes.byref(n)), n.value)
-    assert size(1, 100, 300)[0] == 0 and size(1, 100, 300)[1] % 256 == 0
-    assert size(1, 100, 300)[1] >= 4 * 100 * 300 + 4 * 100 * 100
-    assert size(0, 100, 300)[1] >= 2 * (4 * 100 * 300 + 4 * 100 * 100)
-    assert size(1, 0, 300) == (0, 0)
+    assert size(1, 200, 300)[0] == 0 and size(1, 200, 300)[1] % 256 == 0
+    assert size(1, 200, 300)[1] >= 4 * 200 * 300 + 4 * 200 * 200
+    assert size(0, 200, 300)[1] >= 2 * (4 * 200 * 300 + 4 * 200 * 200)
+    assert size(1, 1024, 4096)[1] >= 4 * 1024 * 4096 + 10 * 1024 * 1024   # steps in groups
+    assert size(1, 0, 300) == (0, 0) and size(1, 128, 300) == (0, 0)      # (in shared memory)
+    assert size(1, 128, 4097)[1] > 0 and size(0, 1537, 128)[1] > 0
     assert lib.LIB.kfac_orthogonalize_workspace_size(lib.ORTHO_DESC.pack(1, 0, 5, 0.0, 0), 1, one(1),
                                                      one(1), None) == A
 
