@@ -670,8 +670,8 @@ typedef struct {
 /* Bytes of workspace that kfac_orthogonalize and kfac_orthogonal_step need for `count`
  * matrices of these sizes (host arrays; a 256-byte multiple): about 4 bytes per element
  * and 4 per element of the square of the smaller side (10 where steps are taken in
- * groups), twice that in full arithmetic; none for a matrix whose smaller side is at most
- * 128 and whose larger one at most 4096 (full arithmetic: 1536).  It holds nothing between
+ * groups), twice that in full arithmetic; none if every matrix has a smaller side of at
+ * most 128 and a larger one of at most 4096 (full arithmetic: 1536).  It holds nothing between
  * calls; calls that share one must be ordered. */
 kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int count, const int* rows,
                                               const int* cols, size_t* bytes);
@@ -683,8 +683,9 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  * anywhere in x makes all of its out NaN.  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
  * count.  out may be x with the same leading dimension.  All matrices go through each
- * product together, up to 24 at a time (full arithmetic: 12); those that need no
- * workspace take all steps in one launch.  The coefficients have to keep the bound of the
+ * product together, up to 24 at a time (full arithmetic: 12); small ones take all steps in
+ * one launch, unless the others' launches have room for them (a matrix's last bits may differ
+ * between the two).  The same call on the same inputs gives the same bits.  The coefficients have to keep the bound of the
  * singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at each step (else
  * KFAC_ERR_INVALID_ARG). */
 kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int* rows,

@@ -453,14 +453,12 @@ __device__ __forceinline__ void put_columns(__half* out, int64_t pitch, bool row
   }
 }
 
-// A tile on the diagonal: the elements on and above it as they are, those above it transposed, so
-// that the matrix is symmetric to the last bit.  (A A^T
-// is by itself, in half arithmetic; in full arithmetic hi lo and lo hi are added in another order
-// on the two sides of the diagonal.  Rounding leaves the product of two matrices that
-// commute a little unsymmetric, and of that part the polynomial's next step sees b L without c L^2,
-// which for the symmetric part takes most of it back: three steps on the small side, then three
-// more, were 1.2e-2 off where 2e-3 is due.)  to: row gr (its column c0); mirror: row c0, column gr
-// rounded down to even.
+// A block on the diagonal of a product of two different matrices: the elements on and above it as
+// they are, those above it transposed, so that the matrix is symmetric to the last bit.  (Rounding
+// leaves the product of two matrices that commute a little unsymmetric, and of that part the
+// polynomial's next step sees b L without c L^2, which for the symmetric part takes most of it
+// back: three steps on the small side, then three more, were 1.2e-2 off where 2e-3 is due.)  to:
+// row gr (its column c0); mirror: row c0, column gr rounded down to even.
 __device__ __forceinline__ void put_diagonal(__half* to, __half* mirror, int64_t pitch, int gr, int c0, int n,
                                              const uint32_t (&w)[32]) {
   if (gr < n) {
@@ -854,7 +852,10 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
             for (int i = 0; i < 64; ++i)
               if (c0 + i == gr) v[i] += k.diag;
           }
-          // hi (and lo) values, each as they are and, off the diagonal, transposed
+          // hi (and lo) values, each as they are and, above the diagonal, transposed.  What lies above
+          // goes by blocks of 128 whatever the tile is: a pair's diagonal tile has one above the
+          // diagonal (1), one below it (-1) and two on it (0).
+          const int side = !k.upper ? 2 : ti != tj ? 1 : kPair ? h - (int)rank : 0;
           uint32_t w[32];
 #pragma unroll
           for (int part = 0; part < (kFull ? 2 : 1); ++part) {
@@ -869,7 +870,8 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
             }
             __half* const other = k.upper ? (part ? k.mirror_lo : k.mirror_hi) : nullptr;
             const int64_t pitch = k.mirror_pitch;
-            if (k.upper && ti == tj && (kFull || !k.same_ab)) {
+            if (side < 0) continue;
+            if (side == 0 && !k.same_ab) {
               if (c0 + 64 > r0 + 32 * qd)   // (all of the warp's are below it otherwise)
                 put_diagonal(other + gr * pitch + c0, other + c0 * pitch + (gr & ~1), pitch, gr, c0, kN, w);
               continue;
@@ -885,7 +887,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
               tma_store_2d(&g.maps[q][part * MAPS + MAP_STORE], buf, c0, r0);
               bulk_commit();
             }
-            if (k.upper && ti != tj) put_columns(other + c0 * pitch + (gr & ~1), pitch, gr < kM, min(64, kN - c0), w);
+            if (side == 1) put_columns(other + c0 * pitch + (gr & ~1), pitch, gr < kM, min(64, kN - c0), w);
           }
         }
       }
@@ -1078,6 +1080,9 @@ kfac_status check_sizes(const kfac_ortho_desc* d, int count, const int* rows, co
   return KFAC_OK;
 }
 
+// Matrices that a product launch takes: up to two tasks each.
+int per_launch(int halves) { return (halves == 2 ? Launch<true>::TASKS : Launch<false>::TASKS) / 2; }
+
 // Regions of the workspace; matrices without elements take none and are left out.
 size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* cols,
                std::vector<Matrix>* out) {
@@ -1088,6 +1093,18 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
     return here;
   };
   const int halves = d->math == KFAC_ORTHO_FULL ? 2 : 1;
+  auto cluster = [&](int s, int l) {
+    return s > kSide ? 0 : halves == 2 ? small_cluster<true>(l) : small_cluster<false>(l);
+  };
+  // Small matrices have a kernel of their own, unless the others' launches have room for them: there
+  // they cost next to nothing (the MLP set's 10 x 1024 beside three of 1024 x 1024 in full
+  // arithmetic: 85 us by itself).
+  int64_t small = 0, large = 0;
+  for (int i = 0; i < count; ++i) {
+    const int s = std::min(rows[i], cols[i]);
+    if (s > 0) ++(cluster(s, std::max(rows[i], cols[i])) ? small : large);
+  }
+  const int64_t room = cdiv(large, per_launch(halves)) * per_launch(halves) - large;
   for (int i = 0; i < count; ++i) {
     Matrix m{};
     m.rows = rows[i];
@@ -1096,7 +1113,7 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
     m.l = std::max(rows[i], cols[i]);
     m.tall = rows[i] > cols[i];
     m.group = d->steps > 1 && grouped(m.s, m.l);
-    if (m.s <= kSide) m.cluster = halves == 2 ? small_cluster<true>(m.l) : small_cluster<false>(m.l);
+    if (m.s > 0 && small > room) m.cluster = cluster(m.s, m.l);
     if (m.s > 0 && !m.cluster) {
       m.xp = (int)pitch_of(m.cols);
       m.sp = (int)pitch_of(m.s);
@@ -1425,7 +1442,7 @@ kfac_status run(const Call& c, int count, const int* rows, const int* cols, void
     return e;
   std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return ms[a].l > ms[b].l; });
   const bool full = c.d->math == KFAC_ORTHO_FULL;
-  const size_t most = (full ? Launch<true>::TASKS : Launch<false>::TASKS) / 2;   // two tasks each, at times
+  const size_t most = (size_t)per_launch(full ? 2 : 1);
   for (size_t at = 0; at < order.size(); at += most) {
     const std::vector<int> idx(order.begin() + at, order.begin() + std::min(order.size(), at + most));
     kfac_status e = full

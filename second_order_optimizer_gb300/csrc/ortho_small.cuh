@@ -13,7 +13,7 @@
 // large matrices' form) pays 6 to 8 us for each.
 
 constexpr int kSide = 128;
-constexpr int kSmallThreads = 256;
+constexpr int kSmallThreads = 512;                // 16 warps: four for each quarter of TMEM's lanes
 constexpr int kSmallTasks = 64;                  // matrices per launch
 constexpr int kTileBytes = kSide * 64 * 2;       // 128 rows x 64 columns
 
@@ -37,7 +37,8 @@ template <bool kFull> struct SmallCfg {
   // columns per block: what shared memory holds beside L (or M) and, in a cluster, the parts of L
   static constexpr int most_tiles(int cluster) { return kFull ? (cluster > 1 ? 3 : 4) : 8; }
   static constexpr size_t smem(int tiles, int cluster) {
-    return 1024 + (size_t)HALVES * (tiles + 2) * kTileBytes + (cluster > 1 ? kSide * kSide * 4 : 0);
+    const size_t bytes = (size_t)HALVES * (tiles + 2) * kTileBytes + (cluster > 1 ? kSide * kSide * 4 : 0);
+    return 1024 + (bytes < kSmallThreads * 128 ? kSmallThreads * 128 : bytes);   // (4 KB a warp at the end)
   }
   static_assert(smem(most_tiles(1), 1) <= 231424 && smem(most_tiles(8), 8) <= 231424, "shared memory");
 };
@@ -61,9 +62,8 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag;
   __shared__ float red[3][kSmallThreads / 32];
-  __shared__ float parts[8][3];
+  __shared__ float parts[8][3], factors[3];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const xs = smem;                                            // [halves][tiles]
   uint8_t* const ls = xs + (size_t)HALVES * g.tiles * kTileBytes;      // [halves][2]: L, then M
@@ -80,7 +80,6 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&done, 1);
-    abort_flag = 0;
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -109,7 +108,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     constexpr int N = decltype(n_)::value;
     const int per = ((tall ? s : width) + N - 1) / N;
     const int total = per * (tall ? width : s);
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = N == 1 ? 16 : 4;   // loads in flight
     for (int i = threadIdx.x; i < total; i += AHEAD * kSmallThreads) {
       Piece<TI, N, kStep> p[AHEAD];
       int row[AHEAD], c[AHEAD];
@@ -135,10 +134,38 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     if (t.vec) visit(std::integral_constant<int, 16 / (int)sizeof(TI)>(), fresh, f);
     else visit(std::integral_constant<int, 1>(), fresh, f);
   };
+  // The values are kept as they were read where a tile has the bits for them (bf16 in one half, fp32
+  // in two), and converted in place once the norm is known; fp32 in half arithmetic is read again.
+  constexpr bool kKeep = !kStep && (sizeof(TI) == 2 || kFull);
+  auto put = [&](int row, int c, auto& hi, auto& lo) {   // one or more 16-bit values from (row, c) on
+    constexpr int n = sizeof(hi) / 2;
+    if (!tall) {
+      *reinterpret_cast<Vec<uint16_t, n>*>(xs + tile_offset(row, c)) = hi;
+      if (kFull) *reinterpret_cast<Vec<uint16_t, n>*>(xs + x_lo + tile_offset(row, c)) = lo;
+    } else {
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        *reinterpret_cast<uint16_t*>(xs + tile_offset(c + i, row)) = hi.v[i];
+        if (kFull) *reinterpret_cast<uint16_t*>(xs + x_lo + tile_offset(c + i, row)) = lo.v[i];
+      }
+    }
+  };
   float up0, up1, r;
   {
     Squares sq;
-    visit_by(std::true_type(), [&](int, int, auto& u) { sq.add(u); });
+    visit_by(std::true_type(), [&](int row, int c, auto& u) {
+      sq.add(u);
+      if constexpr (kKeep) {
+        constexpr int n = sizeof(u) / sizeof(float);
+        Vec<uint16_t, n> hi, lo;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          hi.v[i] = (uint16_t)(__float_as_uint(u[i]) >> 16);
+          lo.v[i] = (uint16_t)__float_as_uint(u[i]);
+        }
+        put(row, c, hi, lo);
+      }
+    });
     if (sq.unsafe()) visit_by(std::false_type(), [&](int, int, auto& u) { sq.add_scaled(u); });
     float v[3];
     sq.finish(v);
@@ -156,39 +183,52 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
         tc::st_cluster_u32(tc::mapa(&parts[rank][threadIdx.x], (uint32_t)c), __float_as_uint(sum));
     }
     cluster_sync();
-    double sums[3] = {0.0, 0.0, 0.0};
-    for (int c = 0; c < cs; ++c)
-      for (int k = 0; k < 3; ++k) sums[k] += (double)parts[c][k];
-    float up[2];
-    scale_factors(sums, g.eps, up, &r);
-    up0 = up[0];
-    up1 = up[1];
+    if (threadIdx.x == 0) {   // (64-bit arithmetic is slow: 512 threads took 7 us over it)
+      double sums[3] = {0.0, 0.0, 0.0};
+      for (int c = 0; c < cs; ++c)
+        for (int k = 0; k < 3; ++k) sums[k] += (double)parts[c][k];
+      float up[2];
+      scale_factors(sums, g.eps, up, &factors[2]);
+      factors[0] = up[0];
+      factors[1] = up[1];
+    }
+    __syncthreads();
+    up0 = factors[0];
+    up1 = factors[1];
+    r = factors[2];
   }
-  visit_by(std::false_type(), [&](int row, int c, auto& u) {
-    constexpr int n = sizeof(u) / sizeof(float);
-    Vec<__half, n> hi, lo;
+  auto halves_of = [&](float x, uint16_t& hi, uint16_t& lo) {
+    const float v = x * up0 * up1;
+    const __half h = __float2half_rn(v);
+    hi = __half_as_ushort(h);
+    if (kFull) lo = __half_as_ushort(__float2half_rn(v - __half2float(h)));
+  };
+  if constexpr (kKeep) {
+    for (int i = threadIdx.x; i < used * kTileBytes / 16; i += kSmallThreads) {
+      Vec<uint16_t, 8>* at = reinterpret_cast<Vec<uint16_t, 8>*>(xs) + i;
+      Vec<uint16_t, 8>* at_lo = reinterpret_cast<Vec<uint16_t, 8>*>(xs + x_lo) + i;
+      Vec<uint16_t, 8> hi = *at, lo;
+      if (kFull) lo = *at_lo;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float v = u[i] * up0 * up1;
-      hi.v[i] = __float2half_rn(v);
-      if (kFull) lo.v[i] = __float2half_rn(v - __half2float(hi.v[i]));
+      for (int j = 0; j < 8; ++j)
+        halves_of(__uint_as_float((uint32_t)hi.v[j] << 16 | (kFull ? lo.v[j] : 0u)), hi.v[j], lo.v[j]);
+      *at = hi;
+      if (kFull) *at_lo = lo;
     }
-    if (!tall) {
-      *reinterpret_cast<Vec<__half, n>*>(xs + tile_offset(row, c)) = hi;
-      if (kFull) *reinterpret_cast<Vec<__half, n>*>(xs + x_lo + tile_offset(row, c)) = lo;
-    } else {
+  } else {
+    visit_by(std::false_type(), [&](int row, int c, auto& u) {
+      constexpr int n = sizeof(u) / sizeof(float);
+      Vec<uint16_t, n> hi, lo;
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        *reinterpret_cast<__half*>(xs + tile_offset(c + i, row)) = hi.v[i];
-        if (kFull) *reinterpret_cast<__half*>(xs + x_lo + tile_offset(c + i, row)) = lo.v[i];
-      }
-    }
-  });
+      for (int i = 0; i < n; ++i) halves_of(u[i], hi.v[i], lo.v[i]);
+      put(row, c, hi, lo);
+    });
+  }
 
   // --------------------------------------------------------------------- steps
   const uint32_t xa = tc::smem_u32(xs), la = tc::smem_u32(ls);
-  // what the threads wrote is visible to the tensor core, and what they read of TMEM may go;
-  // then `issue` by one lane of warp 0, and everyone waits for its products
+  // what the threads wrote is visible to the tensor core, and what they read of TMEM may go; then
+  // warp 0 issues (one lane) and waits for the products, the others at the block's barrier
   auto products = [&](auto issue) {
     tc::fence_proxy_async();
     tc::tc_fence_before();
@@ -199,11 +239,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       issue(leader);
       tc::umma_commit_by(leader, &done);
       __syncwarp();
-    }
-    if (ok && !tc::mbar_wait(&done, phase, &abort_flag)) {
-      ok = false;
-      report_error(&g_status, KFAC_ERR_TIMEOUT, -1, 46);
-      *(volatile int*)&abort_flag = 1;
+      volatile int never = 0;
+      if (ok && !tc::mbar_wait(&done, phase, &never)) {
+        ok = false;
+        if (leader) report_error(&g_status, KFAC_ERR_TIMEOUT, -1, 46);
+      }
+      ok = __all_sync(0xffffffffu, ok);
     }
     phase ^= 1;
     ok = __syncthreads_and(ok);   // one that gave up is joined by all: the barriers below stay whole
@@ -220,35 +261,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       tc::umma_f16_by(leader, d, a + (uint64_t)(a_lo >> 4), b, idesc, 1u);
     }
   };
-  const int qd = warp & 3, h = warp >> 2;                  // TMEM quarter, column half
+  const int qd = warp & 3, h = warp >> 2;                  // TMEM quarter, 32 columns of L and M
   const int row = 32 * qd + lane;                          // of X, L and M
   const uint32_t lane_tmem = tmem + ((uint32_t)(32 * qd) << 16);
-  auto load64 = [&](int col, float (&v)[64]) {
-    uint32_t w0[32], w1[32];
-    tc::tmem_ld32_issue(lane_tmem + (uint32_t)col, w0);
-    tc::tmem_ld32_issue(lane_tmem + (uint32_t)col + 32, w1);
-    tc::tmem_ld_wait();
-    tc::tmem_ld_use(w0);
-    tc::tmem_ld_use(w1);
+  // 32 values of this thread's row, columns from 32 piece on, to tiles as hi (and lo) halves
+  auto store32 = [&](uint8_t* tiles, int piece, int lo, const float (&v)[32]) {
+    uint8_t* at = tiles + (piece >> 1) * kTileBytes + row * 128;
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = __uint_as_float(w0[i]);
-      v[32 + i] = __uint_as_float(w1[i]);
-    }
-  };
-  // 64 values of this thread's row to a tile as hi (and lo) halves
-  auto store64 = [&](uint8_t* tile, int lo, const float (&v)[64]) {
-    uint32_t w[32];
+    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1]);
-    put_rows(tile, row, w);
-    if constexpr (kFull) {
+    for (int half = 0; half < HALVES; ++half) {
+      if (half) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float2 hi = unpack2(w[i]);
-        w[i] = pack2(v[2 * i] - hi.x, v[2 * i + 1] - hi.y);
+        for (int i = 0; i < 16; ++i) {
+          const float2 hi = unpack2(w[i]);
+          w[i] = pack2(v[2 * i] - hi.x, v[2 * i + 1] - hi.y);
+        }
       }
-      put_rows(tile + lo, row, w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(at + half * lo + ((((piece & 1) * 4 + j) ^ (row & 7)) << 4)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
   };
   const int k16 = (s + 15) / 16;                           // of the small side
@@ -266,22 +300,22 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
           }
     });
     const float gram = step == 0 ? p.gram * r * r : p.gram;
-    float v[64];
+    float v[32];
     if (used > 0) {
-      load64(64 * h, v);
+      tc::tmem_ld32(lane_tmem + (uint32_t)(32 * h), v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] = 0.f;
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
     }
     if (cs == 1) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] *= gram;
-      store64(ls + h * kTileBytes, l_lo, v);
+      for (int i = 0; i < 32; ++i) v[i] *= gram;
+      store32(ls, h, l_lo, v);
     } else {
       const int own = kSide / cs;                          // columns that a block adds up
 #pragma unroll
-      for (int i = 0; i < 64; i += 4) {
-        const int col = 64 * h + i, to = col / own, group = (col - to * own) / 4;
+      for (int i = 0; i < 32; i += 4) {
+        const int col = 32 * h + i, to = col / own, group = (col - to * own) / 4;
         const float* at = recv + (((rank * (own / 4) + group) * kSide) + row) * 4;
         st_cluster_f4(tc::mapa(at, (uint32_t)to), v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
@@ -318,14 +352,15 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
           mma(leader, tmem, a, a, l_lo, l_lo, kSquare, pass, k > 0 || (kFull && pass == 1));
         }
     });
-    load64(64 * h, v);
+    tc::tmem_ld32(lane_tmem + (uint32_t)(32 * h), v);
 #pragma unroll
-    for (int i = 0; i < 64; ++i) v[i] *= p.poly;
+    for (int i = 0; i < 32; ++i) v[i] *= p.poly;
+#pragma unroll
     for (int half = 0; half < HALVES; ++half) {
-      const uint8_t* from = ls + half * l_lo + h * kTileBytes;
+      const uint8_t* from = ls + half * l_lo + (h >> 1) * kTileBytes + row * 128;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint4 q = *reinterpret_cast<const uint4*>(from + row * 128 + ((j ^ (row & 7)) << 4));
+      for (int j = 0; j < 4; ++j) {
+        const uint4 q = *reinterpret_cast<const uint4*>(from + ((((h & 1) * 4 + j) ^ (row & 7)) << 4));
         const uint32_t e[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -336,9 +371,9 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       }
     }
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-      if (64 * h + i == row) v[i] += p.diag;
-    store64(ls + h * kTileBytes, l_lo, v);
+    for (int i = 0; i < 32; ++i)
+      if (32 * h + i == row) v[i] += p.diag;
+    store32(ls, h, l_lo, v);
     // ---- X
     products([&](uint32_t leader) {
       for (int pass = kFull ? 0 : 1; pass < 2; ++pass)
@@ -353,12 +388,12 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
         }
     });
     const float apply = step == 0 ? p.apply * r : p.apply;
-    for (int c = h; c < used; c += 2) {
-      load64(64 * c, v);
+    for (int piece = h; piece < 2 * used; piece += 4) {
+      tc::tmem_ld32(lane_tmem + (uint32_t)(32 * piece), v);
 #pragma unroll
-      for (int i = 0; i < 64; ++i) v[i] *= apply;
+      for (int i = 0; i < 32; ++i) v[i] *= apply;
       if (!last) {
-        store64(xs + c * kTileBytes, x_lo, v);
+        store32(xs, piece, x_lo, v);
         continue;
       }
       auto emit = [&](T* at, float x) {
@@ -369,32 +404,28 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
         }
       };
       if (tall) {                          // lanes along the rows of out
-        T* at = static_cast<T*>(task.out) + (int64_t)(l0 + 64 * c) * task.ldo + row;
-        const int n = min(64, width - 64 * c);
+        T* at = static_cast<T*>(task.out) + (int64_t)(l0 + 32 * piece) * task.ldo + row;
+        const int n = min(32, width - 32 * piece);
         if (row < s) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
+          for (int i = 0; i < 32; ++i)
             if (i < n) emit(at + (int64_t)i * task.ldo, v[i]);
         }
-      } else {                             // through the space of M: rows of out in whole pieces
-        float* mine = reinterpret_cast<float*>(ls) + warp * 1024;
+      } else {   // through the space of X and M, which the products have read: rows of out in whole pieces
+        float* mine = reinterpret_cast<float*>(smem) + warp * 1024;
+        __syncwarp();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          __syncwarp();
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<float4*>(mine + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+              make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        __syncwarp();
+        const int col = 32 * piece + lane, rows = min(32, s - 32 * qd);
+        T* at = static_cast<T*>(task.out) + (int64_t)(32 * qd) * task.ldo + l0 + col;
+        if (col < width) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(mine + lane * 32 + ((j ^ (lane & 7)) << 2)) =
-                make_float4(v[half * 32 + 4 * j], v[half * 32 + 4 * j + 1], v[half * 32 + 4 * j + 2],
-                            v[half * 32 + 4 * j + 3]);
-          __syncwarp();
-          const int col = 64 * c + half * 32 + lane, rows = min(32, s - 32 * qd);
-          T* at = static_cast<T*>(task.out) + (int64_t)(32 * qd) * task.ldo + l0 + col;
-          if (col < width) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i < rows)
-                emit(at + (int64_t)i * task.ldo, mine[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)]);
-          }
+          for (int i = 0; i < 32; ++i)
+            if (i < rows)
+              emit(at + (int64_t)i * task.ldo, mine[i * 32 + (((lane >> 2) ^ (i & 7)) << 2) + (lane & 3)]);
         }
       }
     }

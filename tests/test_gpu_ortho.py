@@ -102,16 +102,28 @@ def test_long_matrices_take_steps_in_groups(dtype, math, rows, cols):
 def test_many_matrices_at_once(dtype):
     """More than one launch takes, of all kinds, each as by itself; defaults by type."""
     rng = np.random.default_rng(0)
-    shapes = [tuple(rng.integers(1, 400, 2)) for _ in range(36)] + [(600, 90), (0, 5), (90, 700), (4, 0),
-                                                                     (1024, 1536)]
-    xs = [_gradient(i, *s, dtype) for i, s in enumerate(shapes)]
-    ws = K.orthogonalize_workspace(xs)
-    ws.fill_(255)         # whatever an earlier call left there: NaNs
-    got = K.orthogonalize(xs, workspace=ws)
-    for x, y in zip(xs, got):
-        assert y.shape == x.shape
-        if x.numel():
-            assert torch.equal(y, K.orthogonalize(x))
+    draws = [tuple(rng.integers(1, 400, 2)) for _ in range(60)]
+    empty = [(0, 5), (4, 0)]
+    small = [s for s in draws if min(s) <= 128] + [(600, 90), (90, 700)] + empty
+    large = [s for s in draws if min(s) > 128] + [(1024, 1536)] + empty
+    for shapes in (small, large, small + large):
+        xs = [_gradient(i, *s, dtype) for i, s in enumerate(shapes)]
+        ws = K.orthogonalize_workspace(xs)
+        ws.fill_(255)     # whatever an earlier call left there: NaNs
+        got = K.orthogonalize(xs, workspace=ws)
+        for x, y in zip(xs, got):
+            assert y.shape == x.shape
+            if x.numel():
+                assert torch.equal(y, K.orthogonalize(x))
+    # a few small ones beside a large one: the large one's launches take them
+    xs = [_gradient(i, *s, dtype) for i, s in enumerate([(300, 200), (10, 700), (33, 20), (600, 128), (0, 3)])]
+    got = K.orthogonalize(xs)
+    again = K.orthogonalize(xs)
+    assert torch.equal(got[0], K.orthogonalize(xs[0]))
+    for x, y, z in list(zip(xs, got, again))[:4]:
+        ref, tol = _tolerance(x, dtype, HALF if dtype is BF16 else FULL)
+        _check(y, ref, tol)
+        assert torch.equal(y, z)
     stacked = torch.stack([_gradient(i, 70, 130, dtype) for i in range(3)])
     got = K.orthogonalize(stacked)
     assert got.shape == stacked.shape
@@ -219,7 +231,8 @@ def test_streams_and_graphs():
         out = torch.empty_like(x)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            K.orthogonalize([x, small], out=[out, done])
+            K.orthogonalize(x, out=out)
+            K.orthogonalize(small, out=done)
         graphs.append((g, out))
     for _ in range(3):
         for g, out in graphs:
