@@ -35,6 +35,7 @@ struct SmallLaunch {
 template <bool kFull> struct SmallCfg {
   static constexpr int HALVES = kFull ? 2 : 1;
   // columns per block: what shared memory holds beside L (or M) and, in a cluster, the parts of L
+  // (full arithmetic: and TMEM, 128 columns for each tile's part of L)
   static constexpr int most_tiles(int cluster) { return kFull ? (cluster > 1 ? 3 : 4) : 8; }
   static constexpr size_t smem(int tiles, int cluster) {
     const size_t bytes = (size_t)HALVES * (tiles + 2) * kTileBytes + (cluster > 1 ? kSide * kSide * 4 : 0);
@@ -285,7 +286,27 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     }
   };
+  // 32 columns of this thread's row of an accumulator.  Full arithmetic has one for every 64 k
+  // (`parts` of them, `apart` columns), added here: in one for all of L's k it was 3.9e-6 off.
+  auto load32 = [&](int col, int apart, int parts, float (&v)[32]) {
+    if (parts == 0) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = 0.f;
+      return;
+    }
+    tc::tmem_ld32(lane_tmem + (uint32_t)col, v);
+    if constexpr (kFull) {
+      for (int k = 1; k < parts; ++k) {
+        float w[32];
+        tc::tmem_ld32(lane_tmem + (uint32_t)(col + k * apart), w);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] += w[i];
+      }
+    }
+  };
   const int k16 = (s + 15) / 16;                           // of the small side
+  // whether a product with M or L adds to what is in its accumulator
+  auto more = [&](int k, int pass) { return (uint32_t)((kFull ? k % 4 > 0 : k > 0) || (kFull && pass == 1)); };
   for (int step = 0; step < g.steps; ++step) {
     const SmallStep p = g.step[step];
     const bool last = step + 1 == g.steps;
@@ -296,17 +317,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             const uint64_t a = tc::sdesc_kmajor_sw128(xa + c * kTileBytes + kk * 32);
-            mma(leader, tmem, a, a, x_lo, x_lo, kSquare, pass, c > 0 || kk > 0 || (kFull && pass == 1));
+            mma(leader, tmem + (kFull ? 128u * c : 0u), a, a, x_lo, x_lo, kSquare, pass,
+                (!kFull && c > 0) || kk > 0 || (kFull && pass == 1));
           }
     });
     const float gram = step == 0 ? p.gram * r * r : p.gram;
     float v[32];
-    if (used > 0) {
-      tc::tmem_ld32(lane_tmem + (uint32_t)(32 * h), v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = 0.f;
-    }
+    load32(32 * h, 128, used, v);
     if (cs == 1) {
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= gram;
@@ -349,10 +366,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       for (int pass = kFull ? 0 : 1; pass < 2; ++pass)
         for (int k = 0; k < k16; ++k) {
           const uint64_t a = tc::sdesc_kmajor_sw128(la + (k / 4) * kTileBytes + (k % 4) * 32);
-          mma(leader, tmem, a, a, l_lo, l_lo, kSquare, pass, k > 0 || (kFull && pass == 1));
+          mma(leader, tmem + (kFull ? 128u * (k / 4) : 0u), a, a, l_lo, l_lo, kSquare, pass, more(k, pass));
         }
     });
-    tc::tmem_ld32(lane_tmem + (uint32_t)(32 * h), v);
+    load32(32 * h, 128, (k16 + 3) / 4, v);
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= p.poly;
 #pragma unroll
@@ -381,15 +398,14 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
           const uint64_t a = tc::sdesc_kmajor_sw128(la + (k / 4) * kTileBytes + (k % 4) * 32);
           for (int c = 0; c < used; c += 4) {
             const uint64_t b = tc::sdesc_mnmajor_sw128(xa + c * kTileBytes + k * 2048, kTileBytes);
-            mma(leader, tmem + (uint32_t)(64 * c), a, b, l_lo, x_lo,
-                tc::make_idesc(0, kSide, 64 * min(4, used - c)) | tc::kIdescMnB, pass,
-                k > 0 || (kFull && pass == 1));
+            mma(leader, tmem + (uint32_t)(64 * c) + (kFull ? 256u * (k / 4) : 0u), a, b, l_lo, x_lo,
+                tc::make_idesc(0, kSide, 64 * min(4, used - c)) | tc::kIdescMnB, pass, more(k, pass));
           }
         }
     });
     const float apply = step == 0 ? p.apply * r : p.apply;
     for (int piece = h; piece < 2 * used; piece += 4) {
-      tc::tmem_ld32(lane_tmem + (uint32_t)(32 * piece), v);
+      load32(32 * piece, 256, (k16 + 3) / 4, v);
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] *= apply;
       if (!last) {
