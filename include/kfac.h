@@ -682,7 +682,8 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  * b t^3 + c t^5, its singular vectors stay.  A matrix of zeros gives zeros; Inf or NaN
  * anywhere in x makes all of its out NaN.  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
- * count.  out may be x with the same leading dimension.  All matrices go through each
+ * count.  out may be x with the same leading dimension; no out may be given twice, and
+ * other overlaps are not allowed.  All matrices go through each
  * product together, up to 24 at a time (full arithmetic: 12); small ones take all steps in
  * one launch, unless the others' launches have room for them (a matrix's last bits may differ
  * between the two).  The same call on the same inputs gives the same bits.  The coefficients have to keep the bound of the

@@ -284,13 +284,13 @@ struct NormGradArgs {
 // STAGES - 1 rounds of R rows ahead), so that loads stay in flight through the sums and stores and no
 // barrier orders the ring.  Single bf16 elements are below cp.async's 4 bytes: they are loaded
 // when they are used.  Of 16384 x 2048 (bf16, 268 MB) loads of four rows at a time into registers
-// took 111 us.
+// took 111 us; rounds of two rows from the ring 58, of three 46.
 template <typename T, int N, int TPR, int V, int R, bool kDh> struct GradRing {
   static constexpr bool kOn = N * sizeof(T) >= 4;
   static constexpr int BLOCK = TPR > 256 ? TPR : 256, TENSORS = kDh ? 3 : 2;
   static constexpr size_t ROUND = (size_t)R * TENSORS * V * BLOCK * N * sizeof(T);
-  // two blocks an SM where two rounds allow it
-  static constexpr int STAGES = ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
+  // room for two blocks an SM (single elements: four, see backward_parts)
+  static constexpr int STAGES = N == 1 ? 2 : ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
   static constexpr size_t BYTES = kOn ? STAGES * ROUND : 0;
 };
 template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
@@ -545,9 +545,11 @@ __global__ void __launch_bounds__(1024) norm_parts_kernel(const __grid_constant_
   }
 }
 
-// Blocks of the backward pass: two per SM.
-int64_t backward_parts(int64_t rows) {
-  return std::max<int64_t>(1, std::min<int64_t>(rows, 2 * (int64_t)num_sms()));
+// Blocks of the backward pass: two per SM; four where single elements are loaded, whose blocks
+// have less in flight (4099 x 1025 in fp32, forward and backward: 27 us, with two 33; 16384 x 2048 in
+// bf16: 94 us with two, 102 with four).
+int64_t backward_parts(int64_t rows, bool vec) {
+  return std::max<int64_t>(1, std::min<int64_t>(rows, (vec ? 2 : 4) * (int64_t)num_sms()));
 }
 
 template <typename T, int N, int TPR, int V, int R, bool kDh>
@@ -579,7 +581,7 @@ template <typename T, int N> kfac_status launch_backward(const NormGradArgs& a, 
   const int64_t vecs = cdiv(a.cols, N);
   *done = true;
   if (vecs <= 32) return launch_backward_rows<T, N, 32, 1, 2>(a, st);
-  if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 2>(a, st);
+  if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 3>(a, st);
   if (vecs <= 512) return launch_backward_rows<T, N, 256, 2, 1>(a, st);
   if (vecs <= 1024) return launch_backward_rows<T, N, 256, 4, 1>(a, st);
   if constexpr (N == 1) {
@@ -666,7 +668,7 @@ extern "C" kfac_status kfac_rms_norm(const kfac_norm_desc* d, const void* x, con
 extern "C" kfac_status kfac_rms_norm_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
   if (!bytes || rows < 0 || cols < 0) return KFAC_ERR_INVALID_ARG;
   if (rows >= (int64_t(1) << 31) || cols > kMaxCols) return KFAC_ERR_UNSUPPORTED;
-  *bytes = align_up((size_t)(backward_parts(rows) * 2 * cols) * sizeof(float)) +
+  *bytes = align_up((size_t)(backward_parts(rows, false) * 2 * cols) * sizeof(float)) +
            align_up((size_t)rows * sizeof(float));
   return KFAC_OK;
 }
@@ -712,7 +714,6 @@ extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, cons
   a.lddh = d->lddh;
   a.lddx = d->lddx;
   a.cols = (int)d->cols;
-  a.parts = (int)backward_parts(d->rows);
   a.inv_cols = (float)(1.0 / (double)d->cols);
   a.inv_rows = d->rows > 0 ? (float)(1.0 / (double)d->rows) : 0.f;
   if (dgain || dgain_square) a.part = static_cast<float*>(workspace);
@@ -720,6 +721,7 @@ extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, cons
   const bool vec = d->cols % n == 0 && wide_ok(dy, d->lddy, d->rows, 16, es) &&
                    wide_ok(h, d->ldh, d->rows, 16, es) && wide_ok(dh, d->lddh, d->rows, 16, es) &&
                    wide_ok(dx, d->lddx, d->rows, 16, es) && (uintptr_t)gain % 16 == 0;
+  a.parts = (int)backward_parts(d->rows, vec);
   int launches = 1;
   bool done;
   const kfac_status e =

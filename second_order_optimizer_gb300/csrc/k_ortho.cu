@@ -604,9 +604,9 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
           }
         }
       }
-      // A CTA that gave up lets its memory go only after its copies have landed: they complete on
-      // the even CTA's barriers, which it waits for (bounded) before both leave.
-      if (*abort_flag && rank == 0) {
+      // The block's memory goes only after its copies have landed, whoever gave up: both CTAs' complete
+      // on the even CTA's barriers, which it waits for (bounded) before both leave.
+      if (rank == 0) {
         volatile int never = 0;
         for (int s = 0; s < STAGES; ++s)
           if (const int uses = ring_uses(issued, s, STAGES))
@@ -1144,6 +1144,18 @@ kfac_status launch_tiles(const Launch<kFull>& g, cudaStream_t st) {
   using C = Cfg<kFull, kPair>;
   static OncePerDevice once;
   if (kfac_status e = allow_smem(once, ortho_product_kernel<TO, T, kFull, kPair>, C::SMEM)) return e;
+  if constexpr (kFull && kPair) {   // a register split that the launch does not cover would wait for ever
+    cudaFuncAttributes at{};
+    static OncePerDevice covered;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !covered(dev, [&] {
+          return cudaFuncGetAttributes(&at, ortho_product_kernel<TO, T, kFull, kPair>) == cudaSuccess &&
+                 at.numRegs / 8 * 8 * C::THREADS >= 256 * kEpilogueRegs + 128 * kOtherRegs;
+        })) {
+      check_launch();
+      return KFAC_ERR_UNSUPPORTED;
+    }
+  }
   constexpr int CTAS = kPair ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(CTAS * std::max(1, std::min(g.tile_start[g.count], num_sms() / CTAS))));
@@ -1457,6 +1469,15 @@ bool bad_matrix(const void* p, int64_t ld, int rows, int cols, size_t es) {
   return !p || (uintptr_t)p % es || ld < 0 || ld > (int64_t(1) << 40) || (rows > 1 && ld < cols);
 }
 
+// Whether two matrices are the same one (their results would depend on which came last).
+bool any_twice(void* const* p, int count, const int* rows, const int* cols) {
+  std::vector<void*> at;
+  for (int i = 0; i < count; ++i)
+    if (rows[i] > 0 && cols[i] > 0) at.push_back(p[i]);
+  std::sort(at.begin(), at.end());
+  return std::adjacent_find(at.begin(), at.end()) != at.end();
+}
+
 // A C entry lets no exception out: what can be thrown here is a failed host allocation.
 template <typename F> kfac_status guarded(F f) {
   try {
@@ -1510,7 +1531,10 @@ extern "C" kfac_status kfac_orthogonalize(const kfac_ortho_desc* d, int count, c
   c.ldx = ldx;
   c.out = out;
   c.ldo = ldo;
-  return guarded([&] { return run(c, count, rows, cols, workspace, workspace_bytes, stream); });
+  return guarded([&] {
+    if (any_twice(out, count, rows, cols)) return KFAC_ERR_INVALID_ARG;
+    return run(c, count, rows, cols, workspace, workspace_bytes, stream);
+  });
 }
 
 extern "C" kfac_status kfac_orthogonal_step(const kfac_ortho_desc* d, const kfac_ortho_step* hp, int count,
@@ -1533,7 +1557,9 @@ extern "C" kfac_status kfac_orthogonal_step(const kfac_ortho_desc* d, const kfac
       return KFAC_ERR_INVALID_ARG;
   }
   return guarded([&] {
-    std::vector<void*> out(param, param + count);
+    std::vector<void*> out(param, param + count), m(momentum, momentum + count);
+    if (any_twice(out.data(), count, rows, cols) || any_twice(m.data(), count, rows, cols))
+      return KFAC_ERR_INVALID_ARG;
     Call c{};
     c.d = d;
     c.x = grad;

@@ -234,21 +234,21 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     tc::fence_proxy_async();
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (warp == 0 && ok) {
       tc::tc_fence_after();
       const uint32_t leader = tc::elect_leader();
       issue(leader);
       tc::umma_commit_by(leader, &done);
       __syncwarp();
       volatile int never = 0;
-      if (ok && !tc::mbar_wait(&done, phase, &never)) {
-        ok = false;
+      if (!tc::mbar_wait(&done, phase, &never)) {
         if (leader) report_error(&g_status, KFAC_ERR_TIMEOUT, -1, 46);
+        ok = tc::mbar_wait(&done, phase, &never) && false;   // (TMEM goes after the products, if they end)
       }
       ok = __all_sync(0xffffffffu, ok);
+      phase ^= 1;
     }
-    phase ^= 1;
-    ok = __syncthreads_and(ok);   // one that gave up is joined by all: the barriers below stay whole
+    ok = __syncthreads_and(ok);   // all give up together, and go on to the barriers without products
     tc::tc_fence_after();
   };
   constexpr uint32_t kSquare = tc::make_idesc(0, kSide, kSide);

@@ -76,7 +76,7 @@ def test_orthogonalize(dtype, math, rows, cols):
     assert torch.equal(got, K.orthogonalize(x, math=math))   # the same bits
 
 
-@pytest.mark.parametrize("dtype,math", [(BF16, HALF), (F32, FULL), (F32, HALF)])
+@pytest.mark.parametrize("dtype,math", [(BF16, HALF), (F32, FULL), (F32, HALF), (BF16, FULL)])
 @pytest.mark.parametrize("rows,cols", [(1024, 1600), (2100, 1030)])
 def test_long_matrices_take_steps_in_groups(dtype, math, rows, cols):
     x = _gradient(rows + cols, rows, cols, dtype)
@@ -258,6 +258,9 @@ def test_python_refusals():
         K.orthogonalize(x.t())
     with pytest.raises(ValueError, match="2-D|rows, columns"):
         K.orthogonalize(x[0])
+    with pytest.raises(K.KfacError, match="INVALID_ARG"):
+        K.orthogonalize([x, x + 1], out=[x, x])
+    assert K.orthogonalize([]) == [] and K.orthogonalize([x[:0], x[:, :0]])[0].shape == (0, 6)
     with pytest.raises(K.KfacError, match="WORKSPACE"):
         K.orthogonalize(torch.zeros(150, 200, device="cuda"),
                         workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -239,6 +239,19 @@ def test_embedding_backward(dtype, tokens, rows, width, kind):
            (terms * F * size + F * np.abs(ref + _np(base)))[~none])
 
 
+@pytest.mark.parametrize("tokens", [100, 17000])
+def test_embedding_backward_of_a_huge_table(tokens):
+    """Ids of more than 24 bits: four passes of the sort."""
+    rows = 2 ** 24 + 5
+    ids = torch.from_numpy(np.random.default_rng(1).integers(rows - 300, rows + 3, tokens)).cuda()
+    dout = _randn(2, tokens, 1)
+    got = K.embedding_backward(ids, dout, rows)
+    ref, _ = R.embedding_backward(ids.cpu().numpy() - (rows - 300), _np(dout), 300)
+    size, _ = R.embedding_backward(ids.cpu().numpy() - (rows - 300), np.abs(_np(dout)), 300)
+    assert (got[:-300] == 0).all()
+    _close(got[-300:], ref, 200 * F * size)
+
+
 def test_embedding_strides_and_shapes():
     rows, width = 50, 24
     wide = _randn(1, rows, 40, dtype=BF16)

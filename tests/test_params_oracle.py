@@ -240,7 +240,7 @@ def _ortho(lib, rows=(8, 4), cols=(4, 4), x=None, ldx=(4, 4), out=None, ldo=(4, 
     desc = lib.ORTHO_DESC.pack(*d.values(), 0 if co is None else ctypes.addressof(co))
     n = len(rows)
     ints = lambda v: (ctypes.c_int * n)(*v)
-    ptrs = lambda v, e: (ctypes.c_void_p * n)(*(v or (e,) * n))
+    ptrs = lambda v, e: (ctypes.c_void_p * n)(*(v or [e + 4096 * i for i in range(n)]))
     i64 = lambda v: (ctypes.c_int64 * n)(*v)
     count = n if count is None else count
     if step:
@@ -256,7 +256,7 @@ def _ortho(lib, rows=(8, 4), cols=(4, 4), x=None, ldx=(4, 4), out=None, ldo=(4, 
 @pytest.mark.parametrize("kw", [
     dict(dtype=2), dict(math=2), dict(steps=0), dict(steps=33), dict(eps=-1.0), dict(eps=float("nan")),
     dict(rows=(8, -1)), dict(cols=(-4, 4)), dict(count=-1), dict(x=(P, None)), dict(x=(P + 1, P)),
-    dict(out=(None, P)), dict(out=(P, P + 1)), dict(ldx=(3, 4)), dict(ldo=(4, -4)),
+    dict(out=(None, P)), dict(out=(P, P + 1)), dict(out=(5 * P, 5 * P)), dict(ldx=(3, 4)), dict(ldo=(4, -4)),
     dict(steps=1, coefficients=(float("nan"), 0, 0)), dict(steps=1, coefficients=(0.0, 0.0, 0.0)),
     dict(steps=2, coefficients=(1e5, 0, 0, 1e5, 0, 0)), dict(steps=1, coefficients=(1e9, 0, 0))])
 def test_orthogonalize_refuses(lib, kw, step):
@@ -268,6 +268,7 @@ def test_orthogonal_step_refuses(lib):
            dict(scale=float("inf")), dict(nesterov=2)]
     assert [_ortho(lib, step=True, hp=h) for h in bad] == [A] * len(bad)
     assert _ortho(lib, step=True, m=(P, None)) == A and _ortho(lib, step=True, m=(P, P + 2)) == A
+    assert _ortho(lib, step=True, m=(P, P)) == A
 
 
 def test_orthogonalize_limits_and_workspace(lib):
