@@ -620,7 +620,7 @@ typedef struct {
   int dtype;             /* kfac_dtype of table and out, or of dout                 */
   int id_bits;           /* 32 or 64: signed ids                                    */
   int64_t tokens, rows;  /* ids, rows of the table (< 2^31 - 1 each)                */
-  int64_t width;         /* channels of a row                                       */
+  int64_t width;         /* channels of a row, at most 2^20                         */
   double scale;          /* finite                                                  */
   int64_t ldt;           /* rows of table (forward) or of dtable (backward)         */
   int64_t ldo;           /* rows of out (forward) or of dout (backward)             */

@@ -36,6 +36,7 @@ struct NormArgs {
   float* scales;
   int64_t rows, ldx, ldr, ldh, ldy, ldq;
   int cols, group, groups;
+  int shift;               // channel >> shift: its group (31: one for the row)
   float inv_cols, eps;
 };
 
@@ -80,8 +81,26 @@ __device__ __forceinline__ void load_gain(const float* gain, int c, int cols, fl
 // |v| as an integer: ordered like the values, NaN above infinity.
 __device__ __forceinline__ int abs_bits(float v) { return __float_as_int(v) & 0x7fffffff; }
 
-__device__ __forceinline__ uint8_t e4m3_of(float v, float scale) {
-  return (uint8_t)__nv_cvt_float_to_fp8(scale == 0.f ? 0.f : v / scale, __NV_SATFINITE, __NV_E4M3);
+// N values over their group's scale as e4m3 (two per conversion).  The quotient is v (1 / scale), two
+// roundings from v / scale, except where 1 / scale is out of range.
+template <int N>
+__device__ __forceinline__ void e4m3_of(const float (&v)[N], float scale, Vec<uint8_t, N>& q) {
+  const float inv = 1.f / scale;
+  const bool far = isinf(inv);
+  float u[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = !far ? v[i] * inv : scale == 0.f ? 0.f : v[i] / scale;
+  if constexpr (N == 1) {
+    q.v[0] = (uint8_t)__nv_cvt_float_to_fp8(u[0], __NV_SATFINITE, __NV_E4M3);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const __nv_fp8x2_storage_t two =
+          __nv_cvt_float2_to_fp8x2(make_float2(u[i], u[i + 1]), __NV_SATFINITE, __NV_E4M3);
+      q.v[i] = (uint8_t)(two & 0xff);
+      q.v[i + 1] = (uint8_t)(two >> 8);
+    }
+  }
 }
 
 // A row per TPR threads, all of it in registers: thread t holds vectors t, t + TPR, ... of N
@@ -154,37 +173,44 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
     }
   }
   if constexpr (kQuant) {
+    // a group's channels lie beside each other: its maximum is that of some neighbouring lanes, or of
+    // whole warps
+    const int lanes = a.group == 0 ? 32 : min(32, a.group / N);
+    int top[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int c = (v * TPR + t) * N;
-      int top = 0;
-      if (live && c < a.cols) {
+      top[v] = 0;
+      if (live && (v * TPR + t) * N < a.cols) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) top = max(top, abs_bits(s[v][i]));
+        for (int i = 0; i < N; ++i) top[v] = max(top[v], abs_bits(s[v][i]));
       }
-      if (a.group == 0) {   // one maximum per warp
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (threadIdx.x % 32 == 0) atomicMax(&amax[sub * a.groups], top);
-      } else if (live && c < a.cols) {
-        atomicMax(&amax[sub * a.groups + c / a.group], top);   // N divides the group
-      }
+      for (int o = lanes / 2; o > 0; o >>= 1) top[v] = max(top[v], __shfl_xor_sync(0xffffffffu, top[v], o));
     }
-    __syncthreads();
-    if (live) {
-      for (int g = t; g < a.groups; g += TPR)
-        a.scales[row * a.groups + g] = __int_as_float(amax[sub * a.groups + g]) / kE4m3Max;
-      uint8_t* q = a.q + row * a.ldq;
+    if (a.group == 0 || a.group / N > 32) {   // the warps' maxima meet in shared memory
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = (v * TPR + t) * N;
-        if (c < a.cols) {
-          const float scale =
-              __int_as_float(amax[sub * a.groups + (a.group ? c / a.group : 0)]) / kE4m3Max;
-          Vec<uint8_t, N> pq;
+        if (threadIdx.x % 32 == 0 && live && c < a.cols)
+          atomicMax(&amax[sub * a.groups + (c >> a.shift)], top[v]);
+      }
+      __syncthreads();
 #pragma unroll
-          for (int i = 0; i < N; ++i) pq.v[i] = e4m3_of(s[v][i], scale);
-          *reinterpret_cast<Vec<uint8_t, N>*>(q + c) = pq;
-        }
+      for (int v = 0; v < V; ++v) {
+        const int c = (v * TPR + t) * N;
+        if (c < a.cols) top[v] = amax[sub * a.groups + (c >> a.shift)];
+      }
+    }
+    uint8_t* q = a.q + row * a.ldq;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * TPR + t) * N;
+      if (live && c < a.cols) {
+        const float scale = __int_as_float(top[v]) / kE4m3Max;
+        if (c == (c >> a.shift) << a.shift)   // the group's first channels
+          a.scales[row * a.groups + (c >> a.shift)] = scale;
+        Vec<uint8_t, N> pq;
+        e4m3_of<N>(s[v], scale, pq);
+        *reinterpret_cast<Vec<uint8_t, N>*>(q + c) = pq;
       }
     }
   }
@@ -217,7 +243,7 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const __grid_constant__
   auto norm = [&](int c, float s) { return s * rstd * (a.gain ? __ldg(a.gain + c) : 1.f); };
   if (a.q) {
     for (int c = threadIdx.x; c < a.cols; c += 1024)
-      atomicMax(&amax[a.group ? c / a.group : 0], abs_bits(norm(c, at(c))));
+      atomicMax(&amax[c >> a.shift], abs_bits(norm(c, at(c))));
     __syncthreads();
     for (int g = threadIdx.x; g < a.groups; g += 1024)
       a.scales[row * a.groups + g] = __int_as_float(amax[g]) / kE4m3Max;
@@ -226,8 +252,12 @@ __global__ void __launch_bounds__(1024) norm_wide_kernel(const __grid_constant__
     const float s = at(c), v = norm(c, s);
     if (h) h[c] = (T)s;
     if (y) y[c] = (T)v;
-    if (a.q)
-      a.q[row * a.ldq + c] = e4m3_of(v, __int_as_float(amax[a.group ? c / a.group : 0]) / kE4m3Max);
+    if (a.q) {
+      const float one[1] = {v};
+      Vec<uint8_t, 1> pq;
+      e4m3_of<1>(one, __int_as_float(amax[c >> a.shift]) / kE4m3Max, pq);
+      a.q[row * a.ldq + c] = pq.v[0];
+    }
   }
 }
 
@@ -245,12 +275,13 @@ void launch_norm_rows(const NormArgs& a, cudaStream_t st) {
   }
 }
 
-// Threads per row: 256 with as many vectors each as the row needs; a warp for narrow rows;
-// 1024 for wide ones.
+// Threads per row: 256 with as many vectors each as the row needs; a warp for narrow rows (single
+// elements too: 16384 x 199 in bf16 8.3 us, 256 threads 20.6); 1024 for wide ones.
 template <typename T, int N> bool launch_norm(const NormArgs& a, cudaStream_t st) {
   const int64_t vecs = cdiv(a.cols, N);
   if (vecs <= 32) launch_norm_rows<T, N, 32, 1>(a, st);
   else if (vecs <= 64) launch_norm_rows<T, N, 32, 2>(a, st);
+  else if (N == 1 && vecs <= 256) launch_norm_rows<T, 1, 32, 8>(a, st);
   else if (vecs <= 256) launch_norm_rows<T, N, 256, 1>(a, st);
   else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
   else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
@@ -291,6 +322,7 @@ template <typename T, int N, int TPR, int V, int R, bool kDh> struct GradRing {
   static constexpr size_t ROUND = (size_t)R * TENSORS * V * BLOCK * N * sizeof(T);
   // room for two blocks an SM (single elements: four, see backward_parts)
   static constexpr int STAGES = N == 1 ? 2 : ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
+  static_assert(STAGES * ROUND <= 220 * 1024, "shared memory");
   static constexpr size_t BYTES = kOn ? STAGES * ROUND : 0;
 };
 template <int BYTES> __device__ __forceinline__ void copy_async(void* dst, const void* src) {
@@ -576,14 +608,27 @@ kfac_status launch_backward_rows(const NormGradArgs& a, cudaStream_t st) {
               : launch_backward_kernel<T, N, TPR, V, R, false>(a, st);
 }
 
-// Threads per row as in the forward pass; *done false: too wide.
+// Threads per row: as in the forward pass a warp for narrow rows and 256 with as many vectors each as
+// the row needs, 512 where 256 would hold too much of it; *done false: too wide.  Measured at 4096
+// rows, of the copy rate: bf16 4096 wide 0.47 (two rows a round: 0.41), 8192 0.47 (256 threads: 0.43);
+// fp32 4096 0.79, 8192 0.76 (read twice by the kernels below: 0.42).
 template <typename T, int N> kfac_status launch_backward(const NormGradArgs& a, cudaStream_t st, bool* done) {
   const int64_t vecs = cdiv(a.cols, N);
   *done = true;
   if (vecs <= 32) return launch_backward_rows<T, N, 32, 1, 2>(a, st);
+  if (vecs <= 64) return launch_backward_rows<T, N, 32, 2, 2>(a, st);
+  if constexpr (N == 1) {
+    if (vecs <= 256) return launch_backward_rows<T, 1, 32, 8, 1>(a, st);
+  }
   if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 3>(a, st);
   if (vecs <= 512) return launch_backward_rows<T, N, 256, 2, 1>(a, st);
+  if constexpr (N == 8) {
+    if (vecs <= 1024) return launch_backward_rows<T, N, 512, 2, 1>(a, st);
+  }
   if (vecs <= 1024) return launch_backward_rows<T, N, 256, 4, 1>(a, st);
+  if constexpr (N == 4) {
+    if (vecs <= 2048) return launch_backward_rows<T, N, 512, 4, 1>(a, st);
+  }
   if constexpr (N == 1) {
     if (vecs <= 2048) return launch_backward_rows<T, N, 256, 8, 1>(a, st);
     if (vecs <= 8192) return launch_backward_rows<T, N, 1024, 8, 1>(a, st);
@@ -643,6 +688,7 @@ extern "C" kfac_status kfac_rms_norm(const kfac_norm_desc* d, const void* x, con
   a.cols = (int)d->cols;
   a.group = d->group;
   a.groups = d->group ? (int)cdiv(d->cols, d->group) : 1;
+  a.shift = d->group == 32 ? 5 : d->group == 64 ? 6 : d->group == 128 ? 7 : 31;
   a.inv_cols = (float)(1.0 / (double)d->cols);
   a.eps = (float)d->eps;
   const int n = 16 / (int)es;
