@@ -81,15 +81,12 @@ __device__ __forceinline__ void load_gain(const float* gain, int c, int cols, fl
 // |v| as an integer: ordered like the values, NaN above infinity.
 __device__ __forceinline__ int abs_bits(float v) { return __float_as_int(v) & 0x7fffffff; }
 
-// N values over their group's scale as e4m3 (two per conversion).  The quotient is v (1 / scale), two
-// roundings from v / scale, except where 1 / scale is out of range.
+// N values over their group's scale as e4m3 (two per conversion).
 template <int N>
 __device__ __forceinline__ void e4m3_of(const float (&v)[N], float scale, Vec<uint8_t, N>& q) {
-  const float inv = 1.f / scale;
-  const bool far = isinf(inv);
   float u[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) u[i] = !far ? v[i] * inv : scale == 0.f ? 0.f : v[i] / scale;
+  for (int i = 0; i < N; ++i) u[i] = scale == 0.f ? 0.f : v[i] / scale;
   if constexpr (N == 1) {
     q.v[0] = (uint8_t)__nv_cvt_float_to_fp8(u[0], __NV_SATFINITE, __NV_E4M3);
   } else {
