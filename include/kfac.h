@@ -631,8 +631,9 @@ typedef struct {
 kfac_status kfac_embedding(const kfac_embedding_desc* desc, const void* ids, const void* table,
                            void* out, cudaStream_t stream);
 
-/* Bytes of workspace that kfac_embedding_backward needs (a 256-byte multiple).  It holds
- * nothing between calls; calls that share one must be ordered. */
+/* Bytes of workspace that kfac_embedding_backward needs on the current device (a
+ * 256-byte multiple).  It holds nothing between calls; calls that share one must be
+ * ordered. */
 kfac_status kfac_embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width,
                                           size_t* bytes);
 

@@ -595,12 +595,13 @@ template <typename T, int N> kfac_status launch_sums(const EmbedArgs& a, cudaStr
   return cdiv(a.width, N) <= 64 ? launch_sums_by<T, N, 32>(a, st) : launch_sums_by<T, N, 256>(a, st);
 }
 
-// Sorted positions per chunk: two rounds of rows in flight, more where a row of one hot run would
-// add up thousands of parts.
-int chunk_of(int64_t tokens) {
-  int c = 16;
-  while (cdiv(tokens, c) > 4096) c *= 2;
-  return c;
+// Sorted positions per chunk: at least two stages of rows, else one wave of the chunks' blocks (three
+// per SM, of up to 2048 channels; narrow rows: eight chunks a block).  16384 x 2048 in bf16 in chunks
+// of 36: sums and joins 25 and 7 us, of 16 (2.2 waves) 29 and 12.
+int chunk_of(int64_t tokens, int64_t width) {
+  const int64_t blocks = std::max<int64_t>(1, 3 * (int64_t)num_sms() / cdiv(std::max<int64_t>(width, 1), 2048));
+  const int64_t wave = width <= 512 ? 8 * blocks : blocks;
+  return (int)std::max<int64_t>(2 * kStageRows, cdiv(tokens, wave));
 }
 
 struct Layout {
@@ -623,7 +624,7 @@ Layout layout_of(int64_t tokens, int64_t rows, int64_t width) {
   l.end = take((size_t)rows * 4);
   l.hist = take(small ? 0 : (size_t)cdiv(tokens, kTileItems) * kDigits * 4);
   l.total = take(small ? 0 : kDigits * 4);
-  const int chunk = chunk_of(tokens);
+  const int chunk = chunk_of(tokens, width);
   l.part = take(tokens > chunk ? (size_t)cdiv(tokens, chunk) * 2 * (size_t)width * 4 : 0);
   l.bytes = at;
   return l;
@@ -736,7 +737,7 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
   a.total = at(l.total);
   a.tiles = (int)cdiv(d->tokens, kTileItems);
   a.part = reinterpret_cast<float*>(at(l.part));
-  a.chunk = chunk_of(d->tokens);
+  a.chunk = chunk_of(d->tokens, d->width);
   int launches = 0;
   // blocks that clear: a few per SM, or what there is to clear
   const int64_t clears = std::min<int64_t>(
