@@ -652,7 +652,8 @@ kfac_status kfac_embedding_backward(const kfac_embedding_desc* desc, const void*
                                     size_t workspace_bytes, cudaStream_t stream);
 
 /* Arithmetic of the orthogonalised update.  FULL: operands as two fp16 values each (22
- * bits), three products, fp32 sums: results within about 1e-6 of exact ones in norm.
+ * bits), three products, fp32 sums: results within 3e-6 of exact ones in norm
+ * (elementary fp32 products: 1e-6 to 4e-6).
  * HALF: operands as one fp16 value, scaled by powers of two to their bounds: within 2e-3
  * to 3e-3 after five steps of a matrix with a few strong directions and noise, more where
  * nearly all singular values are tiny (1e-2 where they fall to 1e-4 of the largest). */
