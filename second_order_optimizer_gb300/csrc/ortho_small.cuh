@@ -78,6 +78,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   const int s = tall ? t.cols : t.rows, l = tall ? t.rows : t.cols;
   const int l0 = rank * g.tiles * 64, width = max(0, min(l - l0, g.tiles * 64));
   const int used = (width + 63) / 64;                                  // tiles with columns
+  auto cluster_sync = [&]() {
+    if (cs > 1) tc::cluster_sync();
+    else __syncthreads();
+  };
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&done, 1);
@@ -90,17 +94,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   for (int i = threadIdx.x; i < HALVES * g.tiles * kTileBytes / 16; i += kSmallThreads)
     reinterpret_cast<uint4*>(xs)[i] = make_uint4(0u, 0u, 0u, 0u);
   tc::tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // (a block's shared memory is written to by the others only once it has started)
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_wait();
   pdl_trigger();
   bool ok = true;
   uint32_t phase = 0;
-  auto cluster_sync = [&]() {
-    if (cs > 1) tc::cluster_sync();
-    else __syncthreads();
-  };
 
   // ------------------------------------------------------------------ norm, X_0
   // f(row of X, column of X in this block, values) for this block's part of the matrix; values run
