@@ -289,6 +289,9 @@ def embedding_backward(ids, dout, rows: int, scale: float = 1.0, padding_id: int
 
 # ----------------------------------------------------------------------- orthogonalised updates
 
+_INT_MAX = 2**31 - 1
+
+
 class _Matrices:
     """A list of 2-D tensors with contiguous rows (3-D ones: their entries) as the C call takes it."""
 
@@ -307,8 +310,9 @@ class _Matrices:
             self.dtype = ts[0].dtype if n else torch.float32
             self.dt = _dtype(ts[0], what) if n else 0
             self.shapes = [t.shape for t in ts]
-            self.rows = (ctypes.c_int * n)(*[s[0] for s in self.shapes])
-            self.cols = (ctypes.c_int * n)(*[s[1] for s in self.shapes])
+            # (a side that no int holds is refused by the library, not wrapped)
+            self.rows = (ctypes.c_int * n)(*[min(s[0], _INT_MAX) for s in self.shapes])
+            self.cols = (ctypes.c_int * n)(*[min(s[1], _INT_MAX) for s in self.shapes])
         else:
             self.dev, self.dtype, self.shapes = like.dev, dtype or like.dtype, like.shapes
             if n != like.count:

@@ -264,3 +264,14 @@ def test_python_refusals():
     with pytest.raises(K.KfacError, match="WORKSPACE"):
         K.orthogonalize(torch.zeros(150, 200, device="cuda"),
                         workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def test_sides_that_no_int_holds_are_refused():
+    """2^32 + 1 rows (of one stored row) are not taken for one row."""
+    x = torch.ones(8, device="cuda").as_strided((2**32 + 1, 8), (0, 1))
+    with pytest.raises(K.KfacError, match="UNSUPPORTED"):
+        K.orthogonalize(x, out=x)
+    with pytest.raises(K.KfacError, match="UNSUPPORTED"):
+        K.orthogonalize_workspace(x)
+    with pytest.raises(K.KfacError, match="UNSUPPORTED"):
+        K.orthogonal_step(x, x, x, lr=0.1)
