@@ -584,9 +584,10 @@ typedef struct {
  * NULL, not y and q both.  q: y in 8 bits (e4m3: 3 mantissa bits, largest value 448)
  * with fp32 scales [rows x ceil(cols / group)] contiguous: over each group of
  * channels scale = max |y| / 448 and q = e4m3(y / scale), nearest even (a group of
- * zeros: scale 0, q 0); at most 8192 groups.  Inf or NaN in a row makes that row's results NaN or, where
- * exact arithmetic gives it, zero or Inf.  Outputs may not overlap inputs, except that
- * h may be x or residual with the same leading dimension. */
+ * zeros: scale 0, q 0); at most 8192 groups.  Inf or NaN in a row makes that row's
+ * results NaN or, where exact arithmetic gives it, zero or Inf; squares whose sum passes
+ * 2^128 count as Inf (r = 0).  Outputs may not overlap inputs, except that h may be x or
+ * residual with the same leading dimension. */
 kfac_status kfac_rms_norm(const kfac_norm_desc* desc, const void* x, const void* residual,
                           const float* gain, void* h, void* y, float* rstd, void* q,
                           float* scales, cudaStream_t stream);
@@ -621,7 +622,7 @@ typedef struct {
   int id_bits;           /* 32 or 64: signed ids                                    */
   int64_t tokens, rows;  /* ids, rows of the table (< 2^31 - 1 each)                */
   int64_t width;         /* channels of a row, at most 2^20                         */
-  double scale;          /* finite                                                  */
+  double scale;          /* finite as fp32                                          */
   int64_t ldt;           /* rows of table (forward) or of dtable (backward)         */
   int64_t ldo;           /* rows of out (forward) or of dout (backward)             */
 } kfac_embedding_desc;
@@ -685,12 +686,12 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  * anywhere in x makes all of its out NaN.  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
  * count.  out may be x with the same leading dimension; no out may be given twice, and
- * other overlaps are not allowed.  All matrices go through each
- * product together, up to 24 at a time (full arithmetic: 12); small ones take all steps in
- * one launch, unless the others' launches have room for them (a matrix's last bits may differ
- * between the two).  The same call on the same inputs gives the same bits.  The coefficients have to keep the bound of the
- * singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at each step (else
- * KFAC_ERR_INVALID_ARG). */
+ * other overlaps are not allowed.  All matrices go through each product together, up to
+ * 24 at a time (full arithmetic: 12); small ones take all steps in one launch, unless the
+ * others' launches have room for them (a matrix's last bits may differ between the two).
+ * The same call on the same inputs gives the same bits.  The coefficients have to keep
+ * the bound of the singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at
+ * each step (else KFAC_ERR_INVALID_ARG). */
 kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int* rows,
                                const int* cols, const void* const* x, const int64_t* ldx,
                                void* const* out, const int64_t* ldo, void* workspace,

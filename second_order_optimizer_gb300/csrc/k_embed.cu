@@ -637,7 +637,7 @@ bool whole_vectors(const void* p, int64_t ld, int64_t rows, size_t es) {
 kfac_status check_desc(const kfac_embedding_desc* d, size_t* es) {
   if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16)) return KFAC_ERR_INVALID_ARG;
   if ((d->id_bits != 32 && d->id_bits != 64) || d->tokens < 0 || d->rows < 0 || d->width < 0 ||
-      !std::isfinite(d->scale))
+      !std::isfinite((float)d->scale))
     return KFAC_ERR_INVALID_ARG;
   if (d->tokens > kMaxIds || d->rows > kMaxIds || d->width > (int64_t(1) << 20))
     return KFAC_ERR_UNSUPPORTED;

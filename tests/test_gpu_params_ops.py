@@ -144,6 +144,15 @@ def test_norm_of_extreme_rows():
     assert torch.isnan(q[3].float()).all() and torch.isnan(scales[3:]).all() and (q[1].float() == 0).all()
 
 
+def test_norm_of_squares_beyond_fp32():
+    """A sum of squares past 2^128 is taken as infinite: zeros; just below it the norm is exact."""
+    x = torch.full((2, 64), 2.0**60, device="cuda")   # squares 2^120, their sum 2^126
+    x[1, 3] = 2.0**64
+    y, _, rstd = K.rms_norm(x, eps=0.0)
+    assert torch.allclose(y[0], torch.ones(64, device="cuda"), rtol=1e-6) and (y[1] == 0).all()
+    assert rstd[1] == 0
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("rows,cols", NORM_SIZES + [(5000, 64), (2500, 33)])
 def test_norm_backward(dtype, rows, cols):

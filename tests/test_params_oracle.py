@@ -187,6 +187,11 @@ def test_embedding_refuses(lib, kw):
     assert _embed(lib, **kw) == A
 
 
+def test_embedding_refuses_a_scale_beyond_fp32(lib):
+    assert _embed(lib, scale=1e39) == A and _embed_grad(lib, scale=-1e39) == A
+    assert _embed(lib, scale=3e38, tokens=0) == 0
+
+
 def test_embedding_limits(lib):
     assert _embed(lib, tokens=0, ids=None) == 0 and _embed(lib, width=0, ids=None) == 0
     assert _embed(lib, tokens=1 << 31) == U and _embed(lib, rows=1 << 31) == U
