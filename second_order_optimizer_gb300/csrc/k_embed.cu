@@ -8,7 +8,7 @@
 // of its tokens: no atomics, the same inputs give the same bits.  Up to 16384 tokens a cluster of
 // eight blocks sorts through distributed shared memory while the launch's other blocks clear
 // the table (one block alone took 42 us for 16384 tokens); beyond that, histogram, scan and scatter
-// launches per pass.
+// launches per pass, and what is cleared are the rows without tokens, beside the joins.
 // Text has hot ids (padding, articles), so the sums are divided by tokens, not by rows: a chunk of
 // the sorted order per block, each run inside it to its row; a second launch joins the parts of
 // runs that cross chunks, in order.
@@ -45,6 +45,7 @@ struct EmbedArgs {
   int tiles;
   float* part;             // [chunks][2][width]
   int chunk;
+  int late;                // rows without tokens are cleared after the sums, not all rows before them
 };
 
 template <typename T, int N> struct alignas(N * sizeof(T)) Vec { T v[N]; };
@@ -195,6 +196,33 @@ __device__ __forceinline__ void clear_table(const EmbedArgs& a, int64_t block, i
   }
   if (a.frequency)
     for (int64_t i = first; i < a.rows; i += step) a.frequency[i] = 0.f;
+}
+// Clears the rows that no token has, and their frequencies: kRestRows at a time by a warp.  A row v
+// has tokens where the sorted keys have v at start[v]; the other rows' start is whatever the
+// workspace held.
+constexpr int kRestRows = 8;
+template <int N> __device__ __forceinline__ void clear_rest(const EmbedArgs& a, int64_t block, int64_t blocks) {
+  const int lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  for (int64_t r0 = (block * warps + threadIdx.x / 32) * kRestRows; r0 < a.rows;
+       r0 += blocks * warps * kRestRows) {
+    const int64_t row = r0 + lane;
+    bool none = false;
+    if (lane < kRestRows && row < a.rows) {
+      const uint32_t at = __ldg(a.start + row);
+      none = at >= a.tokens || __ldg(a.keys + at) != (uint32_t)row;
+      if (none && a.frequency) a.frequency[row] = 0.f;
+    }
+    if (a.accumulate) continue;
+    for (uint32_t todo = __ballot_sync(0xffffffffu, none); todo; todo &= todo - 1) {
+      float* out = a.dtable + (r0 + __ffs(todo) - 1) * a.ld_out;
+      if constexpr (N > 1) {
+        for (int64_t c = lane * 4; c < a.width; c += 128)
+          *reinterpret_cast<float4*>(out + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        for (int64_t c = lane; c < a.width; c += 32) out[c] = 0.f;
+      }
+    }
+  }
 }
 __global__ void __launch_bounds__(kSortThreads) clear_kernel(const __grid_constant__ EmbedArgs a) {
   pdl_wait();
@@ -526,10 +554,16 @@ __global__ void __launch_bounds__(256) embedding_chunks_kernel(const __grid_cons
 }
 
 // The runs that cross chunks: the threads of the first border that one crosses add its parts in order.
+// The blocks from `joins` on clear the rows without tokens.
 template <typename T, int N, int TPR>
-__global__ void __launch_bounds__(256) embedding_join_kernel(const __grid_constant__ EmbedArgs a) {
+__global__ void __launch_bounds__(256) embedding_join_kernel(const __grid_constant__ EmbedArgs a, int joins) {
   pdl_wait();
   pdl_trigger();
+  if ((int)blockIdx.x >= joins) {
+    const int64_t each = gridDim.x - joins;
+    clear_rest<N>(a, blockIdx.x - joins + blockIdx.y * each, each * gridDim.y);
+    return;
+  }
   constexpr int RPB = 256 / TPR;
   const int t = threadIdx.x % TPR;
   const int64_t chunk = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR + 1;
@@ -586,9 +620,12 @@ template <typename T, int N, int TPR> kfac_status launch_sums_by(const EmbedArgs
   const unsigned columns = (unsigned)cdiv(a.width, TPR * N);
   launch_pdl(embedding_chunks_kernel<T, N, TPR>, dim3((unsigned)cdiv(chunks, 256 / TPR), columns), dim3(256),
              smem, st, a);
-  if (chunks > 1)
-    launch_pdl(embedding_join_kernel<T, N, TPR>, dim3((unsigned)cdiv(chunks - 1, 256 / TPR), columns),
-               dim3(256), 0, st, a);
+  const int joins = (int)cdiv(chunks - 1, 256 / TPR);
+  const int64_t rest = std::min<int64_t>(8 * (int64_t)num_sms(), cdiv(a.rows, 8 * kRestRows));
+  const int clears = a.late ? (int)cdiv(rest, columns) : 0;
+  if (joins + clears > 0)
+    launch_pdl(embedding_join_kernel<T, N, TPR>, dim3((unsigned)(joins + clears), columns), dim3(256), 0, st, a,
+               joins);
   return KFAC_OK;
 }
 template <typename T, int N> kfac_status launch_sums(const EmbedArgs& a, cudaStream_t st) {
@@ -738,6 +775,11 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
   a.tiles = (int)cdiv(d->tokens, kTileItems);
   a.part = reinterpret_cast<float*>(at(l.part));
   a.chunk = chunk_of(d->tokens, d->width);
+  // Beside the one cluster's sort the table is cleared whole: the memory is idle then, and rows that the
+  // sums write soon after are often still in L2 (16384 tokens, 50021 x 2048: 103 us, 108 with
+  // only the first 50 to 160 MB cleared there and the rest behind the sums).  Where the sort is
+  // launches of its own, only rows without tokens are, behind the sums (65536 tokens: 175 us for 225).
+  a.late = d->tokens > kSmallTokens && (!accumulate || frequency);
   int launches = 0;
   // blocks that clear: a few per SM, or what there is to clear
   const int64_t clears = std::min<int64_t>(
@@ -747,7 +789,7 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
     const dim3 grid((unsigned)(kCluster + cdiv(std::max<int64_t>(clears, accumulate && !frequency ? 0 : 1), kCluster) * kCluster));
     launch_pdl(sort_small_kernel, grid, dim3(kSortThreads), 0, stream, a);
     launches = 1;
-  } else if (!accumulate || frequency) {
+  } else if (d->tokens == 0 && (!accumulate || frequency)) {
     launch_pdl(clear_kernel, dim3((unsigned)std::max<int64_t>(1, clears)), dim3(kSortThreads), 0, stream, a);
     launches = 1;
   }

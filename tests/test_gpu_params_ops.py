@@ -248,6 +248,31 @@ def test_embedding_backward(dtype, tokens, rows, width, kind):
            (terms * F * size + F * np.abs(ref + _np(base)))[~none])
 
 
+@pytest.mark.parametrize("width", [5, 16])
+def test_embedding_backward_of_many_tokens_clears_the_other_rows(width):
+    """Beyond one cluster's sort, whatever an earlier call left in the workspace: other ids, or anything."""
+    tokens, rows = 16385, 40003
+    dout = _randn(1, tokens, width)
+    ws = None
+    for seed, fill in ((2, 0), (3, None), (4, 255), (5, 1)):
+        ids = _ids(seed, tokens, rows // seed, "any", torch.int64)
+        ws = K.embedding_workspace(ids, rows, width) if ws is None else ws
+        if fill is not None:
+            ws.fill_(fill)
+        store = torch.full((rows, width + 3), float("nan"), device="cuda")
+        freq = torch.full((rows,), float("nan"), device="cuda")
+        K.embedding_backward(ids, dout, rows, out=store[:, :width], frequency=freq, workspace=ws)
+        ref, want = R.embedding_backward(ids.cpu().numpy(), _np(dout), rows, 1.0, -1)
+        size, _ = R.embedding_backward(ids.cpu().numpy(), np.abs(_np(dout)), rows, 1.0, -1)
+        _close(store[:, :width], ref, (np.round(want * tokens)[:, None] + 4) * F * size)
+        _close(freq, want, 2 * F * want)
+        assert torch.isnan(store[:, width:]).all()
+        again = torch.full((rows,), float("nan"), device="cuda")   # frequencies alone are cleared
+        K.embedding_backward(ids, dout, rows, out=store[:, :width], accumulate=True, frequency=again,
+                             workspace=ws)
+        assert torch.equal(again, freq)
+
+
 @pytest.mark.parametrize("tokens", [100, 17000])
 def test_embedding_backward_of_a_huge_table(tokens):
     """Ids of more than 24 bits: four passes of the sort."""
