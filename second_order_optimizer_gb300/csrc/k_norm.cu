@@ -6,8 +6,8 @@
 //
 // Bound by memory: each tensor crosses it once.  A row stays in the registers of the threads
 // that share it (a warp, 256 or 1024 threads) between its sum and its use, in vectors of 16
-// bytes where rows and columns allow, else element by element; rows wider than that are read
-// again (from L2).  Statistics, sums and products in fp32, one rounding at each store.
+// bytes where rows and columns allow, else in pairs or element by element; rows wider than that
+// are read again (from L2).  Statistics, sums and products in fp32, one rounding at each store.
 //
 // The gradients of the gain sum over the rows.  A block walks rows a grid apart and keeps its
 // threads' columns in registers; its sums go to the workspace and a second launch adds the
@@ -63,7 +63,7 @@ template <int TPR> __device__ __forceinline__ float row_sum(float v, float* red)
   return v;
 }
 
-// gain[c .. c + N), ones where there is none (N > 1: 16-byte aligned).
+// gain[c .. c + N), ones where there is none (N > 1: 4 N bytes aligned, at most 16).
 template <int N>
 __device__ __forceinline__ void load_gain(const float* gain, int c, int cols, float (&g)[N]) {
   if (!gain || c >= cols) {
@@ -71,6 +71,8 @@ __device__ __forceinline__ void load_gain(const float* gain, int c, int cols, fl
     for (int i = 0; i < N; ++i) g[i] = 1.f;
   } else if constexpr (N == 1) {
     g[0] = __ldg(gain + c);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<float2*>(&g[0]) = __ldg(reinterpret_cast<const float2*>(gain + c));
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4)
@@ -273,22 +275,30 @@ void launch_norm_rows(const NormArgs& a, cudaStream_t st) {
 }
 
 // Threads per row: 256 with as many vectors each as the row needs; a warp for narrow rows (single
-// elements too: 16384 x 199 in bf16 8.3 us, 256 threads 20.6); 1024 for wide ones.
+// elements too: 16384 x 199 in bf16 8.3 us, 256 threads 20.6); 1024 for wide ones.  Pairs of elements
+// where rows are no whole vectors but even: 16384 x 1002, fp32 with the 8-bit output 53 us for 82, bf16
+// 55 for 82, without it 29 for 37.  (4096 x 8190 with the 8-bit output: fp32 256 threads 232 us,
+// 1024 134; bf16 without it 256 threads 49, 1024 83.)
 template <typename T, int N> bool launch_norm(const NormArgs& a, cudaStream_t st) {
+  constexpr bool kWhole = N * sizeof(T) == 16;
   const int64_t vecs = cdiv(a.cols, N);
   if (vecs <= 32) launch_norm_rows<T, N, 32, 1>(a, st);
   else if (vecs <= 64) launch_norm_rows<T, N, 32, 2>(a, st);
-  else if (N == 1 && vecs <= 256) launch_norm_rows<T, 1, 32, 8>(a, st);
-  else if (vecs <= 256) launch_norm_rows<T, N, 256, 1>(a, st);
-  else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
-  else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
-  else if constexpr (N == 1) {
-    if (vecs <= 2048) launch_norm_rows<T, N, 256, 8>(a, st);
-    else if (vecs <= 4096) launch_norm_rows<T, N, 256, 16>(a, st);
-    else if (vecs <= 8192) launch_norm_rows<T, N, 1024, 8>(a, st);
+  else if constexpr (kWhole) {
+    if (vecs <= 256) launch_norm_rows<T, N, 256, 1>(a, st);
+    else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
+    else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
+    else if (vecs <= 2048) launch_norm_rows<T, N, 1024, 2>(a, st);
     else return false;
   } else {
-    if (vecs <= 2048) launch_norm_rows<T, N, 1024, 2>(a, st);
+    if (N == 2 && vecs <= 128) launch_norm_rows<T, 2, 32, 4>(a, st);
+    else if (vecs <= 256) launch_norm_rows<T, N, 32, 8>(a, st);
+    else if (vecs <= 512) launch_norm_rows<T, N, 256, 2>(a, st);
+    else if (vecs <= 1024) launch_norm_rows<T, N, 256, 4>(a, st);
+    else if (vecs <= 2048) launch_norm_rows<T, N, 256, 8>(a, st);
+    else if (N == 2 && sizeof(T) == 4 && vecs <= 4096) launch_norm_rows<float, 2, 1024, 4>(a, st);
+    else if (vecs <= 4096) launch_norm_rows<T, N, 256, 16>(a, st);
+    else if (N == 1 && vecs <= 8192) launch_norm_rows<T, 1, 1024, 8>(a, st);
     else return false;
   }
   return true;
@@ -317,8 +327,8 @@ template <typename T, int N, int TPR, int V, int R, bool kDh> struct GradRing {
   static constexpr bool kOn = N * sizeof(T) >= 4;
   static constexpr int BLOCK = TPR > 256 ? TPR : 256, TENSORS = kDh ? 3 : 2;
   static constexpr size_t ROUND = (size_t)R * TENSORS * V * BLOCK * N * sizeof(T);
-  // room for two blocks an SM (single elements: four, see backward_parts)
-  static constexpr int STAGES = N == 1 ? 2 : ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
+  // room for two blocks an SM (less than whole vectors: four, see backward_parts)
+  static constexpr int STAGES = N * sizeof(T) < 16 ? 2 : ROUND * 4 <= 112 * 1024 ? 4 : ROUND * 3 <= 112 * 1024 ? 3 : 2;
   static_assert(STAGES * ROUND <= 220 * 1024, "shared memory");
   static constexpr size_t BYTES = kOn ? STAGES * ROUND : 0;
 };
@@ -610,25 +620,28 @@ kfac_status launch_backward_rows(const NormGradArgs& a, cudaStream_t st) {
 // rows, of the copy rate: bf16 4096 wide 0.47 (two rows a round: 0.41), 8192 0.47 (256 threads: 0.43);
 // fp32 4096 0.79, 8192 0.76 (read twice by the kernels below: 0.42).
 template <typename T, int N> kfac_status launch_backward(const NormGradArgs& a, cudaStream_t st, bool* done) {
+  constexpr bool kWhole = N * sizeof(T) == 16;
   const int64_t vecs = cdiv(a.cols, N);
   *done = true;
   if (vecs <= 32) return launch_backward_rows<T, N, 32, 1, 2>(a, st);
   if (vecs <= 64) return launch_backward_rows<T, N, 32, 2, 2>(a, st);
-  if constexpr (N == 1) {
-    if (vecs <= 256) return launch_backward_rows<T, 1, 32, 8, 1>(a, st);
+  if constexpr (!kWhole) {
+    if (vecs <= 256) return launch_backward_rows<T, N, 32, 8, 1>(a, st);
+  } else {
+    if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 3>(a, st);
   }
-  if (vecs <= 256) return launch_backward_rows<T, N, 256, 1, 3>(a, st);
   if (vecs <= 512) return launch_backward_rows<T, N, 256, 2, 1>(a, st);
   if constexpr (N == 8) {
     if (vecs <= 1024) return launch_backward_rows<T, N, 512, 2, 1>(a, st);
+  } else {
+    if (vecs <= 1024) return launch_backward_rows<T, N, 256, 4, 1>(a, st);
   }
-  if (vecs <= 1024) return launch_backward_rows<T, N, 256, 4, 1>(a, st);
   if constexpr (N == 4) {
     if (vecs <= 2048) return launch_backward_rows<T, N, 512, 4, 1>(a, st);
   }
-  if constexpr (N == 1) {
+  if constexpr (!kWhole) {
     if (vecs <= 2048) return launch_backward_rows<T, N, 256, 8, 1>(a, st);
-    if (vecs <= 8192) return launch_backward_rows<T, N, 1024, 8, 1>(a, st);
+    if (N == 1 && vecs <= 8192) return launch_backward_rows<T, 1, 1024, 8, 1>(a, st);
   }
   *done = false;
   return KFAC_OK;
@@ -688,16 +701,23 @@ extern "C" kfac_status kfac_rms_norm(const kfac_norm_desc* d, const void* x, con
   a.shift = d->group == 32 ? 5 : d->group == 64 ? 6 : d->group == 128 ? 7 : 31;
   a.inv_cols = (float)(1.0 / (double)d->cols);
   a.eps = (float)d->eps;
-  const int n = 16 / (int)es;
-  const bool vec = d->cols % n == 0 && wide_ok(x, d->ldx, d->rows, 16, es) &&
-                   wide_ok(residual, d->ldr, d->rows, 16, es) && wide_ok(h, d->ldh, d->rows, 16, es) &&
-                   wide_ok(y, d->ldy, d->rows, 16, es) && wide_ok(q, d->ldq, d->rows, n, 1) &&
-                   (uintptr_t)gain % 16 == 0;
+  auto whole = [&](int n) {   // rows of whole vectors of n elements
+    const int bytes = n * (int)es;
+    return d->cols % n == 0 && wide_ok(x, d->ldx, d->rows, bytes, es) &&
+           wide_ok(residual, d->ldr, d->rows, bytes, es) && wide_ok(h, d->ldh, d->rows, bytes, es) &&
+           wide_ok(y, d->ldy, d->rows, bytes, es) && wide_ok(q, d->ldq, d->rows, n, 1) &&
+           (uintptr_t)gain % std::min(4 * n, 16) == 0;
+  };
+  const bool vec = whole(16 / (int)es);
   bool done;
   if (d->dtype == KFAC_BF16)
-    done = vec ? launch_norm<__nv_bfloat16, 8>(a, stream) : launch_norm<__nv_bfloat16, 1>(a, stream);
+    done = vec        ? launch_norm<__nv_bfloat16, 8>(a, stream)
+           : whole(2) ? launch_norm<__nv_bfloat16, 2>(a, stream)
+                      : launch_norm<__nv_bfloat16, 1>(a, stream);
   else
-    done = vec ? launch_norm<float, 4>(a, stream) : launch_norm<float, 1>(a, stream);
+    done = vec        ? launch_norm<float, 4>(a, stream)
+           : whole(2) ? launch_norm<float, 2>(a, stream)
+                      : launch_norm<float, 1>(a, stream);
   if (!done) {
     const size_t smem = q ? (size_t)a.groups * sizeof(int) : 0;
     const dim3 grid((unsigned)a.rows), block(1024);
@@ -760,17 +780,23 @@ extern "C" kfac_status kfac_rms_norm_backward(const kfac_norm_grad_desc* d, cons
   a.inv_cols = (float)(1.0 / (double)d->cols);
   a.inv_rows = d->rows > 0 ? (float)(1.0 / (double)d->rows) : 0.f;
   if (dgain || dgain_square) a.part = static_cast<float*>(workspace);
-  const int n = 16 / (int)es;
-  const bool vec = d->cols % n == 0 && wide_ok(dy, d->lddy, d->rows, 16, es) &&
-                   wide_ok(h, d->ldh, d->rows, 16, es) && wide_ok(dh, d->lddh, d->rows, 16, es) &&
-                   wide_ok(dx, d->lddx, d->rows, 16, es) && (uintptr_t)gain % 16 == 0;
+  auto whole = [&](int n) {   // rows of whole vectors of n elements
+    const int bytes = n * (int)es;
+    return d->cols % n == 0 && wide_ok(dy, d->lddy, d->rows, bytes, es) &&
+           wide_ok(h, d->ldh, d->rows, bytes, es) && wide_ok(dh, d->lddh, d->rows, bytes, es) &&
+           wide_ok(dx, d->lddx, d->rows, bytes, es) && (uintptr_t)gain % std::min(4 * n, 16) == 0;
+  };
+  // (bf16 in pairs, 16384 x 2046: 68 us, in single elements 110; but 4096 x 8190 132 and 121, and fp32
+  // 16384 x 2046 119 and 115, x 130 23 and 16)
+  const bool vec = whole(16 / (int)es), pairs = es == 2 && d->cols <= 4096 && whole(2);
   a.parts = (int)backward_parts(d->rows, vec);
   int launches = 1;
   bool done;
   const kfac_status e =
       d->dtype == KFAC_BF16
-          ? (vec ? launch_backward<__nv_bfloat16, 8>(a, stream, &done)
-                 : launch_backward<__nv_bfloat16, 1>(a, stream, &done))
+          ? (vec     ? launch_backward<__nv_bfloat16, 8>(a, stream, &done)
+             : pairs ? launch_backward<__nv_bfloat16, 2>(a, stream, &done)
+                     : launch_backward<__nv_bfloat16, 1>(a, stream, &done))
           : (vec ? launch_backward<float, 4>(a, stream, &done) : launch_backward<float, 1>(a, stream, &done));
   if (e) return e;
   if (!done) {

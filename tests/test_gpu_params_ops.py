@@ -144,6 +144,34 @@ def test_norm_of_extreme_rows():
     assert torch.isnan(q[3].float()).all() and torch.isnan(scales[3:]).all() and (q[1].float() == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,cols", [(9, 2), (33, 62), (40, 126), (17, 254), (40, 258), (9, 510),
+                                       (5, 1022), (7, 2046), (3, 4094), (3, 4098), (2, 8190), (2, 8194)])
+def test_norm_of_even_rows(dtype, rows, cols):
+    """Rows of whole pairs, and the same rows where the pairs do not begin at whole words."""
+    x, res, dy = (_randn(s, rows, cols, dtype=dtype) for s in (1, 2, 3))
+    gain = 1 + 0.3 * _randn(4, cols)
+    y, h, rstd = K.rms_norm(x, gain, res)
+    _check_norm(x, gain, res, 1e-6, y, h, rstd)
+    q, scales, _ = K.rms_norm_e4m3(x, gain, res, group=64)
+    dx, dgain, square = K.rms_norm_backward(dy, h, gain, rstd, dresidual=res, square=True)
+    ref = R.rms_norm_backward(_np(dy), _np(h), _np(gain), _np(rstd), _np(res))
+    n, w = _np(h) * _np(rstd)[:, None], np.abs(_np(dy) * _np(gain))
+    size = _np(rstd)[:, None] * (w + np.abs(n) * (w * np.abs(n)).mean(axis=1, keepdims=True))
+    _close(dx, ref[0], 96 * F * (size + np.abs(_np(res))) + U[dtype] * np.abs(ref[0]))
+    _close(dgain, ref[1], (rows + 16) * F * np.abs(_np(dy) * n).sum(axis=0))
+    _close(square, ref[2], (rows + 20) * F * ref[2])
+    odd = torch.empty(rows, cols + 1, device="cuda", dtype=dtype)[:, 1:]   # single elements
+    odd.copy_(x)
+    y1, h1, rstd1 = K.rms_norm(odd, gain, res)
+    _check_norm(x, gain, res, 1e-6, y1, h1, rstd1)
+    assert torch.equal(h1, h)
+    q1, scales1, _ = K.rms_norm_e4m3(odd, gain, res, group=64)
+    # (r's last bits move a scale by as much, and a value over it by no more than a step)
+    _close(scales1, _np(scales), 128 * F * _np(scales))
+    assert (q1.float() - q.float()).abs().le(q.float().abs() / 8 + 2.0 ** -9).all()
+
+
 def test_norm_of_squares_beyond_fp32():
     """A sum of squares past 2^128 is taken as infinite: zeros; just below it the norm is exact."""
     x = torch.full((2, 64), 2.0**60, device="cuda")   # squares 2^120, their sum 2^126
@@ -194,7 +222,8 @@ def test_norm_backward_in_place_and_parts():
 # ---------------------------------------------------------------------------------- embedding
 
 EMBED_SIZES = [(1, 1, 1), (5, 10, 16), (1, 300, 40), (333, 7, 33), (1000, 5000, 520), (4097, 100, 65),
-               (16384, 1000, 24), (16385, 70000, 8), (50000, 300, 16), (130, 1, 48), (20000, 3, 9)]
+               (300, 40, 2), (17001, 700, 258), (260, 50, 1030), (16384, 1000, 24),
+               (16385, 70000, 8), (50000, 300, 16), (130, 1, 48), (20000, 3, 9)]
 
 
 def _ids(seed, tokens, rows, kind, dtype):
