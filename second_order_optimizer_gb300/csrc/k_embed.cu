@@ -7,7 +7,7 @@
 // radix sort (8 bits a pass, ranks from warp ballots), so that every row is summed in the order
 // of its tokens: no atomics, the same inputs give the same bits.  Up to 16384 tokens a cluster of
 // eight blocks sorts through distributed shared memory while the launch's other blocks clear
-// the table (one block alone took 42 us for 16384 tokens); beyond that, histogram, scan and scatter
+// the table (one block alone took 42 us for 16384 tokens; up to 2048 one does); beyond that, histogram, scan and scatter
 // launches per pass, and what is cleared are the rows without tokens, beside the joins.
 // Text has hot ids (padding, articles), so the sums are divided by tokens, not by rows: a chunk of
 // the sorted order per block, each run inside it to its row; a second launch joins the parts of
@@ -231,7 +231,8 @@ __global__ void __launch_bounds__(kSortThreads) clear_kernel(const __grid_consta
 }
 
 // Up to kSmallTokens tokens by the first cluster: block b holds items [b I, (b + 1) I) in every
-// pass, its warp w 32 at a time from w I / 16 on.  The other clusters clear the table.
+// pass, its warp w 32 at a time from w I / 16 on.  What one block can hold (kAlone, 2048 tokens) one
+// sorts without the barriers between blocks, 2 to 3 us sooner.  The other blocks clear the table.
 struct SmallSort {
   uint32_t keys[kSmallTokens / kCluster];
   uint32_t vals[kSmallTokens / kCluster];
@@ -243,20 +244,26 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
+template <bool kAlone>
+__global__ void __cluster_dims__(kAlone ? 1 : kCluster, 1, 1) __launch_bounds__(kSortThreads)
     sort_small_kernel(const __grid_constant__ EmbedArgs a) {
   __shared__ SmallSort s;
   constexpr int ROUNDS = kSmallTokens / kCluster / kSortThreads;
   pdl_wait();
   pdl_trigger();
-  if (blockIdx.x >= kCluster) {
-    clear_table(a, blockIdx.x - kCluster, gridDim.x - kCluster, kSortThreads);
+  constexpr int BLOCKS = kAlone ? 1 : kCluster;
+  if (blockIdx.x >= BLOCKS) {
+    clear_table(a, blockIdx.x - BLOCKS, gridDim.x - BLOCKS, kSortThreads);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank_in = tc::cluster_rank();
+  const uint32_t rank_in = kAlone ? 0 : tc::cluster_rank();
   const int n = (int)a.tokens;
-  const int rounds = (n + kCluster * kSortThreads - 1) / (kCluster * kSortThreads);
+  auto sync = [&]() {
+    if (kAlone) __syncthreads();
+    else tc::cluster_sync();
+  };
+  const int rounds = (n + BLOCKS * kSortThreads - 1) / (BLOCKS * kSortThreads);
   const int items = rounds * kSortThreads;          // of a block
   const int base_item = (int)rank_in * items;
   auto local = [&](int r) { return (warp * rounds + r) * 32 + lane; };
@@ -283,14 +290,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     if (d < kDigits)
       s.total[d] = (d + 1 < kDigits ? s.counts.scan[d + 1] : (uint32_t)max(0, min(items, n - base_item))) -
                    s.counts.scan[d];
-    tc::cluster_sync();
+    sync();
     uint32_t before = 0, all = 0;
     if (d < kDigits) {
+      if (kAlone) {
+        all = s.total[d];
+      } else {
 #pragma unroll
-      for (uint32_t c = 0; c < kCluster; ++c) {
-        const uint32_t v = ld_cluster_u32(tc::mapa(&s.total[d], c));
-        before += c < rank_in ? v : 0;
-        all += v;
+        for (uint32_t c = 0; c < kCluster; ++c) {
+          const uint32_t v = ld_cluster_u32(tc::mapa(&s.total[d], c));
+          before += c < rank_in ? v : 0;
+          all += v;
+        }
       }
       uint32_t incl = all;
 #pragma unroll
@@ -310,12 +321,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
       if (r < rounds && base_item + local(r) < n) {
         const uint32_t g = (key[r] >> (kBits * pass)) % kDigits;
         const uint32_t at = s.base[g] + s.counts.n[g][warp] + rank[r];
-        const uint32_t to = at / (uint32_t)items, off = at - to * (uint32_t)items;
-        tc::st_cluster_u32(tc::mapa(&s.keys[off], to), key[r]);
-        tc::st_cluster_u32(tc::mapa(&s.vals[off], to), val[r]);
+        if (kAlone) {
+          s.keys[at] = key[r];
+          s.vals[at] = val[r];
+        } else {
+          const uint32_t to = at / (uint32_t)items, off = at - to * (uint32_t)items;
+          tc::st_cluster_u32(tc::mapa(&s.keys[off], to), key[r]);
+          tc::st_cluster_u32(tc::mapa(&s.vals[off], to), val[r]);
+        }
       }
     }
-    tc::cluster_sync();
+    sync();
     if (pass + 1 < a.passes) {
 #pragma unroll
       for (int r = 0; r < ROUNDS; ++r) {
@@ -329,7 +345,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
   for (int j = threadIdx.x; j < items && base_item + j < n; j += kSortThreads) {
     const int i = base_item + j;
     auto neighbour = [&](int k) -> uint32_t {      // the key at item k, of this block or the next one
-      if (k < 0 || k >= n) return 0;
+      if (kAlone || k < 0 || k >= n) return 0;   // (one block's neighbours are its own)
       const int b = k / items;
       return ld_cluster_u32(tc::mapa(&s.keys[k - b * items], (uint32_t)b));
     };
@@ -339,7 +355,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSortThreads)
     mark_run(a, i, k, j > 0 ? s.keys[j - 1] : neighbour(i - 1),
              j + 1 < items && i + 1 < n ? s.keys[j + 1] : neighbour(i + 1));
   }
-  tc::cluster_sync();   // no block's shared memory goes while another reads it
+  sync();   // no block's shared memory goes while another reads it
 }
 
 // A tile's counts of each digit.
@@ -495,69 +511,88 @@ __global__ void __launch_bounds__(256) embedding_chunks_kernel(const __grid_cons
   const uint32_t before = lo > 0 ? __ldg(a.keys + lo - 1) : 0xffffffffu;   // (no key: see kMaxIds)
   const uint32_t after = hi < a.tokens ? __ldg(a.keys + hi) : 0xffffffffu;
   const int64_t c = ((int64_t)blockIdx.y * TPR + t) * N;
-  if (c < a.width) {
-    const T* src = static_cast<const T*>(a.src) + c;
-    auto fetch = [&](int64_t i, int stage) {
+  const int lane = threadIdx.x % 32;
+  if (c - lane * N >= a.width) return;   // a warp without columns
+  const bool on = c < a.width;
+  const T* src = static_cast<const T*>(a.src) + c;
+  // the next 64 positions' keys and tokens, two per lane (of a warp all positions are the same): read one
+  // by one where they are used they were a chain of loads (300 tokens of 2046 channels in bf16, 8000 rows:
+  // 26 us for 34)
+  uint32_t keys0, vals0, keys1, vals1;
+  auto window = [&](int64_t at, uint32_t& k, uint32_t& v) {
+    const bool in = at + lane < hi;
+    k = in ? __ldg(a.keys + at + lane) : 0xffffffffu;
+    v = in ? __ldg(a.vals + at + lane) : 0u;
+  };
+  window(lo, keys0, vals0);
+  window(lo + 32, keys1, vals1);
+  auto fetch = [&](int from, int stage) {   // position `from` of the windows
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        if (i + j < hi && __ldg(a.keys + i + j) < rows) {
-          const T* from = src + (int64_t)__ldg(a.vals + i + j) * a.ld_src;
-          Pack* to = slots + (stage * R + j) * 256;
-          if constexpr (sizeof(Pack) == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(from)
-                         : "memory");
-          else if constexpr (sizeof(Pack) == 4)
-            tc::cp_async4(to, from);
-          else if constexpr (sizeof(Pack) == 8)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(to)), "l"(from)
-                         : "memory");
-          else
-            *to = *reinterpret_cast<const Pack*>(from);
-        }
-      }
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    float sum[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) sum[i] = 0.f;
-    uint32_t run = __ldg(a.keys + lo);
-    int64_t begin = lo;                  // of the run, in this chunk
-    fetch(lo, 0);
-    fetch(lo + R, 1);
-    int stage = 0;
-    for (int64_t i = lo;;) {             // position i, the first behind the run included
-      const uint32_t key = i < hi ? __ldg(a.keys + i) : 0xffffffffu;
-      if (key != run) {
-        if (run < rows) {
-          const bool from_before = begin == lo && before == run, goes_on = i == hi && after == run;
-          if (from_before || goes_on) {
-            store_floats<N>(a.part + (chunk * 2 + (from_before ? 0 : 1)) * a.width + c, sum);
-          } else {
-            store_row<N>(a, run, c, sum);
-            if (c == 0 && a.frequency) a.frequency[run] = (float)(i - begin) * a.inv_tokens;
-          }
-        }
-        if (i >= hi) break;
-        run = key;
-        begin = i;
-#pragma unroll
-        for (int k = 0; k < N; ++k) sum[k] = 0.f;
-      }
-      const int j = (int)(i - lo) % R;
-      if (j == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
-      if (run < rows) {
-        const Pack p = slots[(stage * R + j) * 256];
-#pragma unroll
-        for (int k = 0; k < N; ++k) sum[k] += to_f32<T>(p.v[k]);
-      }
-      ++i;
-      if (j == R - 1) {
-        fetch(i + R, stage);             // the slots just read
-        stage ^= 1;
+    for (int j = 0; j < R; ++j) {
+      const int p = from + j;               // (R divides 32: a fetch lies in one window)
+      const uint32_t k = __shfl_sync(0xffffffffu, from < 32 ? keys0 : keys1, p % 32);
+      const uint32_t v = __shfl_sync(0xffffffffu, from < 32 ? vals0 : vals1, p % 32);
+      if (on && k < rows) {
+        const T* at = src + (int64_t)v * a.ld_src;
+        Pack* to = slots + (stage * R + j) * 256;
+        if constexpr (sizeof(Pack) == 16)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(to)), "l"(at) : "memory");
+        else if constexpr (sizeof(Pack) == 8)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(tc::smem_u32(to)), "l"(at) : "memory");
+        else if constexpr (sizeof(Pack) == 4)
+          tc::cp_async4(to, at);
+        else
+          *to = *reinterpret_cast<const Pack*>(at);
       }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float sum[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = 0.f;
+  uint32_t run = __shfl_sync(0xffffffffu, keys0, 0);
+  int64_t begin = lo, base = lo;       // of the run in this chunk; of the windows
+  fetch(0, 0);
+  fetch(R, 1);
+  int stage = 0;
+  for (int64_t i = lo;;) {             // position i, the first behind the run included
+    const uint32_t key = __shfl_sync(0xffffffffu, keys0, (int)(i - base));   // (none from hi on)
+    if (key != run) {
+      if (on && run < rows) {
+        const bool from_before = begin == lo && before == run, goes_on = i == hi && after == run;
+        if (from_before || goes_on) {
+          store_floats<N>(a.part + (chunk * 2 + (from_before ? 0 : 1)) * a.width + c, sum);
+        } else {
+          store_row<N>(a, run, c, sum);
+          if (c == 0 && a.frequency) a.frequency[run] = (float)(i - begin) * a.inv_tokens;
+        }
+      }
+      if (i >= hi) break;
+      run = key;
+      begin = i;
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum[k] = 0.f;
+    }
+    const int j = (int)(i - lo) % R;
+    if (j == 0) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    if (on && run < rows) {
+      const Pack p = slots[(stage * R + j) * 256];
+#pragma unroll
+      for (int k = 0; k < N; ++k) sum[k] += to_f32<T>(p.v[k]);
+    }
+    ++i;
+    if (j == R - 1) {
+      fetch((int)(i - base) + R, stage);   // the slots just read
+      stage ^= 1;
+      if (i - base == 32) {
+        base = i;
+        keys0 = keys1;
+        vals0 = vals1;
+        window(base + 32, keys1, vals1);
+      }
+    }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // The runs that cross chunks: the threads of the first border that one crosses add its parts in order.
@@ -791,19 +826,26 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
   // Beside the one cluster's sort the table is cleared whole: the memory is idle then, and rows that the
   // sums write soon after are often still in L2 (16384 tokens, 50021 x 2048: 103 us, 108 with
   // only the first 50 to 160 MB cleared there and the rest behind the sums).  Where the sort is
-  // launches of its own, only rows without tokens are, behind the sums (65536 tokens: 175 us for 225).
+  // launches of its own, only rows without tokens are, behind the sums (65536 tokens: 180 us for 225).
   a.late = d->tokens > kSmallTokens && (!accumulate || frequency);
   int launches = 0;
   // blocks that clear: a few per SM, or what there is to clear
-  const int64_t clears = std::min<int64_t>(
-      4 * (int64_t)num_sms(),
-      cdiv((accumulate ? 0 : d->rows * d->width / 4) + (frequency ? d->rows : 0), kSortThreads));
+  const int64_t clears =
+      accumulate && !frequency
+          ? 0
+          : std::min<int64_t>(4 * (int64_t)num_sms(),
+                              cdiv((accumulate ? 0 : cdiv(d->rows * d->width, 4)) + (frequency ? d->rows : 0),
+                                   kSortThreads));
   if (d->tokens > 0 && d->tokens <= kSmallTokens) {
-    const dim3 grid((unsigned)(kCluster + cdiv(std::max<int64_t>(clears, accumulate && !frequency ? 0 : 1), kCluster) * kCluster));
-    launch_pdl(sort_small_kernel, grid, dim3(kSortThreads), 0, stream, a);
+    if (d->tokens <= kSmallTokens / kCluster) {
+      launch_pdl(sort_small_kernel<true>, dim3((unsigned)(1 + clears)), dim3(kSortThreads), 0, stream, a);
+    } else {
+      const dim3 grid((unsigned)(kCluster + cdiv(clears, kCluster) * kCluster));
+      launch_pdl(sort_small_kernel<false>, grid, dim3(kSortThreads), 0, stream, a);
+    }
     launches = 1;
-  } else if (d->tokens == 0 && (!accumulate || frequency)) {
-    launch_pdl(clear_kernel, dim3((unsigned)std::max<int64_t>(1, clears)), dim3(kSortThreads), 0, stream, a);
+  } else if (d->tokens == 0 && clears > 0) {
+    launch_pdl(clear_kernel, dim3((unsigned)clears), dim3(kSortThreads), 0, stream, a);
     launches = 1;
   }
   if (d->tokens == 0) {

@@ -222,7 +222,8 @@ def test_norm_backward_in_place_and_parts():
 # ---------------------------------------------------------------------------------- embedding
 
 EMBED_SIZES = [(1, 1, 1), (5, 10, 16), (1, 300, 40), (333, 7, 33), (1000, 5000, 520), (4097, 100, 65),
-               (300, 40, 2), (17001, 700, 258), (260, 50, 1030), (16384, 1000, 24),
+               (300, 40, 2), (17001, 700, 258), (260, 50, 1030), (2048, 70000, 72),
+               (2049, 200, 72), (16384, 1000, 24),
                (16385, 70000, 8), (50000, 300, 16), (130, 1, 48), (20000, 3, 9)]
 
 
