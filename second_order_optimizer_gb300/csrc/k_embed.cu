@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(256) embedding_chunks_kernel(const __grid_cons
 
 // The runs that cross chunks: a warp per border, which adds the parts if it is the first that the run
 // crosses.  The parts of a run over more than kLong chunks (a hot id) are divided by the block's
-// warps and added in order.  (Parts added four at a time by one warp: the gradient of
-// 13810 tokens of one id, 224 channels, 130 us, so 35; of 16384 of 2048 channels 186 and 92.)  The blocks from `joins` on clear the rows without tokens.
+// warps and added in order (by one warp, four at a time, the gradient of 13810 tokens of one id and
+// 224 channels took 130 us, so 35; of 16384 of 2048 channels 186 and 92).  The blocks from `joins`
+// on clear the rows without tokens.
 constexpr int kLong = 32;
 template <int N>
 __global__ void __launch_bounds__(256) embedding_join_kernel(const __grid_constant__ EmbedArgs a, int joins) {
