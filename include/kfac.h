@@ -724,6 +724,13 @@ kfac_status kfac_orthogonal_step(const kfac_ortho_desc* desc, const kfac_ortho_s
  * (weights: keep their values).  KFAC_OK: none. */
 kfac_status kfac_operator_status(int* info);
 
+/* Failure-detection self-test of the orthogonalised updates: in this thread's next call of
+ * kfac_orthogonalize or kfac_orthogonal_step that passes its checks, one wait of product
+ * launch `launch` (counted from 0; -1: none) is taken for one that gave up: no fault and no
+ * endless wait, the call ends as kfac_operator_status describes.  Matrices whose smaller
+ * side is at most 128 have such launches beside larger ones only. */
+kfac_status kfac_selftest_orthogonal(int launch);
+
 /* Diagnostics: number of kernels this library has launched in this process. */
 unsigned long long kfac_launch_count(void);
 

@@ -123,6 +123,7 @@ SIGNATURES = [
     ("kfac_orthogonalize_workspace_size", _i, [_vp, _i, _vp, _vp, ctypes.POINTER(_sz)]),
     ("kfac_orthogonalize", _i, [_vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     ("kfac_orthogonal_step", _i, [_vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    ("kfac_selftest_orthogonal", _i, [_i]),
     ("kfac_operator_status", _i, [ctypes.POINTER(_i)]),
 ]
 

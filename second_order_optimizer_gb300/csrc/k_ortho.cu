@@ -331,6 +331,7 @@ struct Task {
 enum { MAP_A, MAP_B, MAP_STORE, MAPS };   // operands and result
 template <bool kFull> struct Launch {
   static constexpr int TASKS = kFull ? 24 : 48;   // a kernel's parameters end at 32764 bytes
+  int give_up;             // self-test: a warp's wait for the first tile is taken for one that ran out
   CUtensorMap maps[TASKS][MAPS * (kFull ? 2 : 1)];
   Task task[TASKS];
   int tile_start[TASKS + 1];
@@ -376,6 +377,12 @@ __device__ __forceinline__ void commit_pair_by(uint32_t leader, uint64_t* bar) {
       "h"((uint16_t)3), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+constexpr long long kLandCycles = 1 << 20;   // 0.5 ms: of copies and products in flight
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y,
                                             int z) {
   asm volatile(
@@ -504,6 +511,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* copies = tmem_slot + 2;   // loads of operands that the producer has issued
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int total = g.tile_start[g.count];
   const uint32_t rank = kPair ? tc::cluster_rank() : 0;
@@ -531,6 +539,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
     }
     tc::mbar_init(drained, 1);
     *abort_flag = 0;
+    *copies = 0;
     tc::fence_mbar_init();
   }
   if (warp == 1) {
@@ -604,14 +613,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
           }
         }
       }
-      // The block's memory goes only after its copies have landed, whoever gave up: both CTAs' complete
-      // on the even CTA's barriers, which it waits for (bounded) before both leave.
-      if (rank == 0) {
-        volatile int never = 0;
-        for (int s = 0; s < STAGES; ++s)
-          if (const int uses = ring_uses(issued, s, STAGES))
-            tc::mbar_wait(&full[s], ring_last_parity(uses), &never);
-      }
+      *copies = (uint32_t)issued;
     } else if (warp == 1 && rank == 0) {
       // ---------------------------------------------------------------- MMA issuer
       const uint32_t leader = tc::elect_leader();
@@ -678,11 +680,6 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
           if (ok) commit(&acc_full[buf]);
         }
       }
-      if (!ok || *abort_flag) {   // the products in flight end before TMEM and the tiles go
-        commit(drained);
-        volatile int never = 0;
-        tc::mbar_wait(drained, 0, &never);
-      }
     }
   } else {
     // -------------------------------------------------------------------- epilogue
@@ -708,6 +705,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
       int q, ti, tj;
       tile_of(g, t, &q, &ti, &tj);
       const Task& k = g.task[q];
+      const bool quit = g.give_up && t == 0 && rank == 0 && warp == C::EPI0;
       const int kM = k.M, kN = k.N;
       const int r0 = ti * TILE + (int)rank * 128, gr = r0 + row;
       const int cols0 = tj * TILE + h * CW;
@@ -747,7 +745,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
         const int nsub = (k.kblocks + C::SUB - 1) / C::SUB;
         for (int sub = 0; sub < nsub && ok; ++sub, ++gsub) {
           const int buf = gsub & 1, use = gsub >> 1;
-          if (!tc::mbar_wait(&acc_full[buf], use & 1, abort_flag)) {
+          if (quit || !tc::mbar_wait(&acc_full[buf], use & 1, abort_flag)) {
             if (lane == 0) give_up(44);
             ok = false;
             break;
@@ -763,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
           release(buf);
         }
       } else if (ok) {
-        if (!tc::mbar_wait(&acc_full[gsub & 1], (gsub >> 1) & 1, abort_flag)) {
+        if (quit || !tc::mbar_wait(&acc_full[gsub & 1], (gsub >> 1) & 1, abort_flag)) {
           if (lane == 0) give_up(45);
           ok = false;
         }
@@ -898,6 +896,26 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
   tc::tc_fence_before();
   __syncwarp();
   block_sync();   // every MMA has completed; no peer arrival is pending
+  if (*abort_flag) {   // (of both CTAs) unless a role gave up, whichever and whenever:
+    // memory goes only after the copies have landed and the products have ended.  Both CTAs' complete
+    // on the even one's barriers; where one CTA has issued more copies than the other a barrier does
+    // not turn, and the limit outlasts them.
+    volatile int never = 0;
+    if (rank == 0 && threadIdx.x == 0) {
+      const int issued = (int)(kPair ? max(*copies, ld_cluster_u32(tc::mapa(copies, 1))) : *copies);
+      for (int s = 0; s < STAGES; ++s)
+        if (const int uses = ring_uses(issued, s, STAGES))
+          tc::mbar_wait(&full[s], ring_last_parity(uses), &never, kLandCycles);
+    }
+    if (rank == 0 && warp == 1) {
+      const uint32_t leader = tc::elect_leader();   // the lane that issued them
+      if constexpr (kPair) commit_pair_by(leader, drained);
+      else tc::umma_commit_by(leader, drained);
+      tc::mbar_wait(drained, 0, &never, kLandCycles);
+    }
+    __syncwarp();
+    block_sync();
+  }
   if (warp == 1) {
     if constexpr (kPair) tc::tmem_dealloc_pair(tmem, C::TMEM);
     else tc::tmem_dealloc(tmem, C::TMEM);
@@ -1301,10 +1319,13 @@ kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>
   return KFAC_OK;
 }
 
+// The product launch whose first wait the thread's next call lets run out (kfac_selftest_orthogonal).
+thread_local int t_selftest = -1;
+
 // The matrices of `idx` (at most half of a launch's tasks, none empty), all launches.
 template <bool kFull>
 kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>& ms,
-                      const std::vector<int>& idx, char* ws, cudaStream_t st) {
+                      const std::vector<int>& idx, int give_up, char* ws, cudaStream_t st) {
   const int n = (int)idx.size();
   constexpr int halves = kFull ? 2 : 1;
   auto half_at = [&](size_t off) { return reinterpret_cast<__half*>(ws + off); };
@@ -1373,6 +1394,7 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
   std::unique_ptr<Launch<kFull>> g(new Launch<kFull>());
   for (size_t round = 0; round < rounds; ++round) {
     g->count = 0;
+    g->give_up = (int)round == give_up;
     const bool last = round + 1 == rounds;
     for (int i = 0; i < n; ++i) {
       if (round + ops[i].size() < rounds) continue;
@@ -1440,6 +1462,8 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
 
 kfac_status run(const Call& c, int count, const int* rows, const int* cols, void* workspace,
                 size_t bytes, cudaStream_t st) {
+  const int give_up = t_selftest;
+  t_selftest = -1;
   Plan plan;
   if (kfac_status e = make_plan(c.d, &plan)) return e;
   std::vector<Matrix> ms;
@@ -1458,8 +1482,8 @@ kfac_status run(const Call& c, int count, const int* rows, const int* cols, void
   for (size_t at = 0; at < order.size(); at += most) {
     const std::vector<int> idx(order.begin() + at, order.begin() + std::min(order.size(), at + most));
     kfac_status e = full
-                        ? run_group<true>(c, plan, ms, idx, static_cast<char*>(workspace), st)
-                        : run_group<false>(c, plan, ms, idx, static_cast<char*>(workspace), st);
+                        ? run_group<true>(c, plan, ms, idx, give_up, static_cast<char*>(workspace), st)
+                        : run_group<false>(c, plan, ms, idx, give_up, static_cast<char*>(workspace), st);
     if (e) return e;
   }
   return KFAC_OK;
@@ -1571,4 +1595,10 @@ extern "C" kfac_status kfac_orthogonal_step(const kfac_ortho_desc* d, const kfac
     c.hp = hp;
     return run(c, count, rows, cols, workspace, workspace_bytes, stream);
   });
+}
+
+extern "C" kfac_status kfac_selftest_orthogonal(int launch) {
+  if (launch < -1) return KFAC_ERR_INVALID_ARG;
+  t_selftest = launch;
+  return KFAC_OK;
 }

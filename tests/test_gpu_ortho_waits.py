@@ -1,0 +1,63 @@
+"""Orthogonalised updates whose waits give up: the self-test takes one wait of a product launch for one
+that ran out.  The call ends, says so once, and what runs behind it is not disturbed."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA GPU", allow_module_level=True)
+
+import second_order_optimizer_gb300 as K  # noqa: E402
+from second_order_optimizer_gb300._lib import LIB  # noqa: E402
+
+BF16, F32 = torch.bfloat16, torch.float32
+TIMEOUT = 5
+FORMS = [(BF16, K.KFAC_ORTHO_HALF), (F32, K.KFAC_ORTHO_FULL)]
+# single CTAs on 128 x 128 tiles; CTA pairs on 256 x 256 ones
+SIZES = [(300, 500), (2304, 2400)]
+
+
+def _matrix(rows, cols, dtype, seed=0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(rows, cols, generator=g, device="cuda").to(dtype)
+
+
+def _selftest(launch):
+    assert LIB.kfac_selftest_orthogonal(launch) == 0
+
+
+LAUNCHES = 15   # of five single steps: X X^T, M, M X each
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_last_product(rows, cols, dtype, math):
+    """The rows of the warp that gave up are NaN; then the same call on the same workspace is right."""
+    x = _matrix(rows, cols, dtype)
+    work = K.orthogonalize_workspace(x, math=math)
+    want = K.orthogonalize(x, math=math, workspace=work)
+    for _ in range(3):
+        _selftest(LAUNCHES - 1)
+        got = K.orthogonalize(x, math=math, workspace=work)
+        code, info = K.operator_status()
+        assert code == TIMEOUT and info in (44, 45)
+        assert torch.isnan(got[:32, :32]).all() and not torch.isnan(want).any()
+        kept = ~torch.isnan(got)
+        assert torch.equal(got[kept], want[kept])
+        assert K.operator_status() == (0, 0)
+        assert torch.equal(K.orthogonalize(x, math=math, workspace=work), want)
+        assert K.operator_status() == (0, 0)
+
+
+def test_selftest_is_of_one_call():
+    assert LIB.kfac_selftest_orthogonal(-2) == 1
+    x = _matrix(300, 500, BF16)
+    want = K.orthogonalize(x)
+    _selftest(3)
+    _selftest(-1)
+    assert torch.equal(K.orthogonalize(x), want) and K.operator_status() == (0, 0)
+    _selftest(LAUNCHES)   # none of this number
+    assert torch.equal(K.orthogonalize(x), want)
+    assert torch.equal(K.orthogonalize(x), want) and K.operator_status() == (0, 0)
