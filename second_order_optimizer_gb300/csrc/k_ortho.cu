@@ -406,6 +406,18 @@ __device__ __forceinline__ void group_sync(int id) {   // the 128 threads of an 
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
 }
 
+// Whether all 128 say yes.
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.and.pred q, %2, 128, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "r"(id)
+      : "memory");
+  return all != 0;
+}
+
 // Tile t of the launch: its task, row and column block.
 template <bool kFull>
 __device__ __forceinline__ void tile_of(const Launch<kFull>& g, int t, int* q, int* ti, int* tj) {
@@ -767,7 +779,10 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
         }
         tc::tc_fence_after();
       }
-      ok = __all_sync(0xffffffffu, ok);
+      // One warp may see the abort flag where another, a moment later, finds its products done: what
+      // stores by groups decides by groups, or some would wait in group_sync for ever.
+      __syncwarp();
+      ok = TO == TO_MATRIX ? group_all(1 + h, ok) : __all_sync(0xffffffffu, ok);
       if (!ok && TO != TO_OUT) break;        // TO_OUT: the tiles from here on become NaN
 #pragma unroll
       for (int ch = 0; ch < CW / 64; ++ch) {       // 64 columns at a time

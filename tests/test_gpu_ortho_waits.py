@@ -61,3 +61,21 @@ def test_selftest_is_of_one_call():
     _selftest(LAUNCHES)   # none of this number
     assert torch.equal(K.orthogonalize(x), want)
     assert torch.equal(K.orthogonalize(x), want) and K.operator_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("launch", [0, 1, 2, 13])
+def test_product_on_the_way(rows, cols, dtype, math, launch):
+    """One warp of four that store together gives up; the others, whose products are done, do not wait
+    for it."""
+    x = _matrix(rows, cols, dtype)
+    work = K.orthogonalize_workspace(x, math=math)
+    want = K.orthogonalize(x, math=math, workspace=work)
+    for _ in range(3):
+        _selftest(launch)
+        K.orthogonalize(x, math=math, workspace=work)
+        code, info = K.operator_status()
+        assert code == TIMEOUT and info in (44, 45) and K.operator_status() == (0, 0)
+        assert torch.equal(K.orthogonalize(x, math=math, workspace=work), want)
+        assert K.operator_status() == (0, 0)
