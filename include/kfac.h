@@ -720,8 +720,9 @@ kfac_status kfac_orthogonal_step(const kfac_ortho_desc* desc, const kfac_ortho_s
 /* Synchronise the current device and report the first device-side error of the
  * block operators, or of the orthogonalised updates, on it since the last call (then
  * clear it): a pipeline wait of their tensor-core kernels that gave up
- * (KFAC_ERR_TIMEOUT; info: which role).  The outputs of the blocks concerned hold NaN
- * (weights: keep their values).  KFAC_OK: none. */
+ * (KFAC_ERR_TIMEOUT; info: which role).  The outputs of the blocks concerned hold NaN.
+ * Of an orthogonalised update those are of the whole matrix, unless the wait was for its
+ * last product; weights keep their values, momenta have taken the step.  KFAC_OK: none. */
 kfac_status kfac_operator_status(int* info);
 
 /* Failure-detection self-test of the orthogonalised updates: in this thread's next call of

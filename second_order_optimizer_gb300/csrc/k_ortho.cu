@@ -70,7 +70,7 @@ struct PrepTask {
   int64_t ldx, ldm;
   __half *hi, *lo;         // X_0, rows of `pitch`
   float* part;             // [blocks][3]: squares by range
-  float* r;
+  float* r;                // the factor r; behind it the word of a lost product (see Task)
   int rows, cols, pitch;
   int tx;                  // threads per row (a power of two)
   int vec;                 // whole 16-byte vectors of x (and of m)
@@ -287,7 +287,10 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_
     scale_factors(all, g.eps, up, &r);
     factor[0] = up[0];
     factor[1] = up[1];
-    if (block == 0) *t.r = r;
+    if (block == 0) {
+      t.r[0] = r;
+      t.r[1] = 0.f;
+    }
   }
   __syncthreads();
   const float up0 = factor[0], up1 = factor[1];
@@ -319,7 +322,9 @@ struct Task {
   void* out;                    // TO_OUT: the direction; TO_WEIGHTS: the weights, fp32
   const __half *add_hi, *add_lo;   // or null
   __half *mirror_hi, *mirror_lo;   // upper: the result itself, whose other half is stored directly
-  const float* r;
+  float* r;                     // r, and a word that is not 0 once a product of this matrix is lost: a wait
+                                // gave up, so its tile was not stored, and what the last launch makes of it is
+                                // NaN (weights: left as they were)
   float alpha, beta, diag;
   float keep, rate;             // TO_WEIGHTS: W <- keep W - rate X
   int rpow, add_pitch, mirror_pitch;
@@ -783,7 +788,15 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
       // stores by groups decides by groups, or some would wait in group_sync for ever.
       __syncwarp();
       ok = TO == TO_MATRIX ? group_all(1 + h, ok) : __all_sync(0xffffffffu, ok);
+      if (!ok && TO == TO_MATRIX && issuer) {
+        for (int u = t; u < total; u += units) {
+          tile_of(g, u, &q, &ti, &tj);
+          g.task[q].r[1] = 1.f;
+        }
+      }
       if (!ok && TO != TO_OUT) break;        // TO_OUT: the tiles from here on become NaN
+      const bool lost = TO != TO_MATRIX && __ldcg(k.r + 1) != 0.f;
+      if (TO == TO_OUT && lost) alpha = __int_as_float(0x7fffffff);
 #pragma unroll
       for (int ch = 0; ch < CW / 64; ++ch) {       // 64 columns at a time
         const int c0 = cols0 + ch * 64;
@@ -825,7 +838,7 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
                               v[half * 32 + 4 * j + 3]);
             __syncwarp();
             const int c = c0 + half * 32 + lane;
-            const int rows = min(32, kM - (r0 + 32 * qd));
+            const int rows = TO == TO_WEIGHTS && lost ? 0 : min(32, kM - (r0 + 32 * qd));
             T* out = static_cast<T*>(k.out) + (int64_t)(r0 + 32 * qd) * k.out_ld + c;
             if (c < kN) {
               const int64_t ld = k.out_ld;
@@ -1154,7 +1167,7 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
         for (int h = 0; h < halves && has_buffer(m, d->steps, b); ++h)
           m.at[b][h] = take(b == X_0 || b == X_1 ? (size_t)m.rows * m.xp * 2 : (size_t)m.s * m.sp * 2);
       m.part = take(kPrepBlocks * 3 * sizeof(float));
-      m.r = take(sizeof(float));
+      m.r = take(2 * sizeof(float));
     }
     if (out) out->push_back(m);
   }
@@ -1418,7 +1431,7 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
         Task& t = g->task[g->count];
         CUtensorMap* to = g->maps[g->count++];
         t = Task{};
-        t.r = reinterpret_cast<const float*>(ws + m.r);
+        t.r = reinterpret_cast<float*>(ws + m.r);
         t.alpha = (float)op.alpha;
         t.beta = (float)op.beta;
         t.diag = (float)op.diag;

@@ -79,3 +79,45 @@ def test_product_on_the_way(rows, cols, dtype, math, launch):
         assert code == TIMEOUT and info in (44, 45) and K.operator_status() == (0, 0)
         assert torch.equal(K.orthogonalize(x, math=math, workspace=work), want)
         assert K.operator_status() == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("launch", [0, 1, 2, 7, 13])
+def test_a_lost_product_reaches_the_result(rows, cols, dtype, math, launch):
+    """All of the matrix's direction is NaN, whatever earlier calls left in the workspace; the matrices
+    beside it are right."""
+    xs = [_matrix(rows, cols, dtype), _matrix(200, 300, dtype), _matrix(260, 140, dtype)]
+    work = K.orthogonalize_workspace(xs, math=math)
+    want = K.orthogonalize(xs, math=math, workspace=work)
+    _selftest(launch)
+    got = K.orthogonalize(xs, math=math, workspace=work)
+    assert K.operator_status()[0] == TIMEOUT
+    # (with 128 x 128 tiles the block that gave up has none of the others' tiles behind its first)
+    assert torch.isnan(got[0]).all()
+    for x, y in zip(got[1:], want[1:]):
+        assert torch.equal(x, y) or torch.isnan(x).all()
+    assert sum(bool(torch.isnan(x).any()) for x in got) < 3
+    for x, y in zip(K.orthogonalize(xs, math=math, workspace=work), want):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols", SIZES)
+@pytest.mark.parametrize("launch", [0, 7, 13, 14])
+def test_weights_keep_their_values(rows, cols, dtype, math, launch):
+    g, m0, w0 = _matrix(rows, cols, dtype), _matrix(rows, cols, F32, 1), _matrix(rows, cols, F32, 2)
+    work = K.orthogonalize_workspace(g, math=math)
+    m, w = m0.clone(), w0.clone()
+    K.orthogonal_step(g, m, w, lr=0.1, weight_decay=0.1, math=math, workspace=work)
+    stepped, moved = m.clone(), w.clone()
+    m.copy_(m0)
+    w.copy_(w0)
+    _selftest(launch)
+    K.orthogonal_step(g, m, w, lr=0.1, weight_decay=0.1, math=math, workspace=work)
+    assert K.operator_status()[0] == TIMEOUT
+    assert torch.equal(m, stepped)
+    if launch < LAUNCHES - 1:
+        assert torch.equal(w, w0)
+    else:   # of the last product what gave up keeps its weights, the rest has moved
+        assert torch.equal(w[:32, :32], w0[:32, :32]) and ((w == w0) | (w == moved)).all()
