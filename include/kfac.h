@@ -721,15 +721,15 @@ kfac_status kfac_orthogonal_step(const kfac_ortho_desc* desc, const kfac_ortho_s
  * block operators, or of the orthogonalised updates, on it since the last call (then
  * clear it): a pipeline wait of their tensor-core kernels that gave up
  * (KFAC_ERR_TIMEOUT; info: which role).  The outputs of the blocks concerned hold NaN.
- * Of an orthogonalised update those are of the whole matrix, unless the wait was for its
- * last product; weights keep their values, momenta have taken the step.  KFAC_OK: none. */
+ * Of an orthogonalised update that is the whole matrix, or the part of it that its last
+ * products lost; weights keep their values, momenta have taken the step.  KFAC_OK: none. */
 kfac_status kfac_operator_status(int* info);
 
 /* Failure-detection self-test of the orthogonalised updates: in this thread's next call of
  * kfac_orthogonalize or kfac_orthogonal_step that passes its checks, one wait of product
- * launch `launch` (counted from 0; -1: none) is taken for one that gave up: no fault and no
- * endless wait, the call ends as kfac_operator_status describes.  Matrices whose smaller
- * side is at most 128 have such launches beside larger ones only. */
+ * launch `launch` (counted from 0; -1: none), or of that step of each matrix that takes all
+ * its steps in one launch, is taken for one that gave up: no fault and no endless wait, the
+ * call ends as kfac_operator_status describes. */
 kfac_status kfac_selftest_orthogonal(int launch);
 
 /* Diagnostics: number of kernels this library has launched in this process. */

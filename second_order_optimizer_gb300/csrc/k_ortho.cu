@@ -1274,6 +1274,10 @@ float rate_of(const Call& c, const Matrix& m) {
 }
 float keep_of(const Call& c) { return (float)(1.0 - c.hp->lr * c.hp->weight_decay); }
 
+// The product launch (small matrices: the step) whose first wait the thread's next call takes for one
+// that ran out (kfac_selftest_orthogonal).
+thread_local int t_selftest = -1;
+
 template <int TO, typename TI, typename T, bool kFull>
 kfac_status launch_small(const SmallLaunch& g, int count, cudaStream_t st) {
   static OncePerDevice once;
@@ -1302,7 +1306,8 @@ kfac_status launch_small(const SmallLaunch& g, int count, cudaStream_t st) {
 
 // The matrices with a side of at most kSide: a launch for each size of cluster.
 template <bool kFull>
-kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>& ms, cudaStream_t st) {
+kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>& ms, int give_up,
+                      cudaStream_t st) {
   std::unique_ptr<SmallLaunch> g;
   for (int cs = 1; cs <= 8; cs *= 2) {
     for (size_t at = 0; at < ms.size();) {
@@ -1320,6 +1325,7 @@ kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>
       }
       if (n == 0) continue;
       g->steps = plan.steps;
+      g->give_up = give_up;
       for (int k = 0; k < plan.steps; ++k) {   // ops_of, steps one by one
         const double sx = k == 0 ? 1.0 : scale_of(plan.u[k]), to = k + 1 == plan.steps ? 1.0 : scale_of(plan.u[k + 1]);
         const double sl = scale_of(plan.u[k] * plan.u[k]), sm = scale_of(plan.v[k]);
@@ -1346,9 +1352,6 @@ kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>
   }
   return KFAC_OK;
 }
-
-// The product launch whose first wait the thread's next call lets run out (kfac_selftest_orthogonal).
-thread_local int t_selftest = -1;
 
 // The matrices of `idx` (at most half of a launch's tasks, none empty), all launches.
 template <bool kFull>
@@ -1501,8 +1504,8 @@ kfac_status run(const Call& c, int count, const int* rows, const int* cols, void
   std::vector<int> order;
   for (int i = 0; i < count; ++i)
     if (ms[i].s > 0 && !ms[i].cluster) order.push_back(i);
-  if (kfac_status e = c.d->math == KFAC_ORTHO_FULL ? run_small<true>(c, plan, ms, st)
-                                                   : run_small<false>(c, plan, ms, st))
+  if (kfac_status e = c.d->math == KFAC_ORTHO_FULL ? run_small<true>(c, plan, ms, give_up, st)
+                                                   : run_small<false>(c, plan, ms, give_up, st))
     return e;
   std::stable_sort(order.begin(), order.end(), [&](int a, int b) { return ms[a].l > ms[b].l; });
   const bool full = c.d->math == KFAC_ORTHO_FULL;

@@ -29,6 +29,7 @@ struct SmallLaunch {
   SmallStep step[kMaxSteps];
   int steps, cluster, tiles;                     // tiles: of 64 columns per block
   int nesterov;
+  int give_up;                                   // self-test: a step whose first wait counts as one that ran out
   float mu, eps, keep;
 };
 
@@ -62,7 +63,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   constexpr int HALVES = kFull ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t done;
-  __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t tmem_slot, lost;   // lost: a block of the cluster gave up
   __shared__ float red[3][kSmallThreads / 32];
   __shared__ float parts[8][3], factors[3];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
 
   if (threadIdx.x == 0) {
     tc::mbar_init(&done, 1);
+    lost = 0;
     tc::fence_mbar_init();
   }
   if (warp == 0) {
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   const uint32_t xa = tc::smem_u32(xs), la = tc::smem_u32(ls);
   // what the threads wrote is visible to the tensor core, and what they read of TMEM may go; then
   // warp 0 issues (one lane) and waits for the products, the others at the block's barrier
-  auto products = [&](auto issue) {
+  auto products = [&](auto issue, bool quit = false) {
     tc::fence_proxy_async();
     tc::tc_fence_before();
     __syncthreads();
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       tc::umma_commit_by(leader, &done);
       __syncwarp();
       volatile int never = 0;
-      if (!tc::mbar_wait(&done, phase, &never)) {
+      if (quit || !tc::mbar_wait(&done, phase, &never)) {
         if (leader) report_error(&g_status, KFAC_ERR_TIMEOUT, -1, 46);
         ok = tc::mbar_wait(&done, phase, &never) && false;   // (TMEM goes after the products, if they end)
       }
@@ -320,7 +322,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
             mma(leader, tmem + (kFull ? 128u * c : 0u), a, a, x_lo, x_lo, kSquare, pass,
                 (!kFull && c > 0) || kk > 0 || (kFull && pass == 1));
           }
-    });
+    }, step == g.give_up && rank == 0);
     const float gram = step == 0 ? p.gram * r * r : p.gram;
     float v[32];
     load32(32 * h, 128, used, v);
@@ -336,7 +338,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
         const float* at = recv + (((rank * (own / 4) + group) * kSide) + row) * 4;
         st_cluster_f4(tc::mapa(at, (uint32_t)to), v[i], v[i + 1], v[i + 2], v[i + 3]);
       }
+      // (what a block sends after it gave up is no part of L: all give up with it)
+      if (!ok && threadIdx.x < cs) tc::st_cluster_u32(tc::mapa(&lost, threadIdx.x), 1u);
       tc::cluster_sync();
+      ok = ok && *static_cast<volatile uint32_t*>(&lost) == 0;
       const int mine = threadIdx.x % kSide;
       for (int group = threadIdx.x / kSide; group < own / 4; group += kSmallThreads / kSide) {
         float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);

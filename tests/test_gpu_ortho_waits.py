@@ -121,3 +121,28 @@ def test_weights_keep_their_values(rows, cols, dtype, math, launch):
         assert torch.equal(w, w0)
     else:   # of the last product what gave up keeps its weights, the rest has moved
         assert torch.equal(w[:32, :32], w0[:32, :32]) and ((w == w0) | (w == moved)).all()
+
+
+# one block; clusters of two to eight; both orientations
+SMALL = [(100, 90), (60, 1000), (1000, 128), (128, 1400), (1500, 30)]
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols", SMALL)
+@pytest.mark.parametrize("step", [0, 2, 4])
+def test_small_matrices_give_up_as_a_cluster(rows, cols, dtype, math, step):
+    x = _matrix(rows, cols, dtype)
+    want = K.orthogonalize(x, math=math)
+    _selftest(step)
+    got = K.orthogonalize(x, math=math)
+    code, info = K.operator_status()
+    assert (code, info) == (TIMEOUT, 46)
+    assert torch.isnan(got).all()
+    assert torch.equal(K.orthogonalize(x, math=math), want)
+    m, w0 = _matrix(rows, cols, F32, 1), _matrix(rows, cols, F32, 2)
+    w = w0.clone()
+    _selftest(step)
+    K.orthogonal_step(x, m, w, lr=0.1, weight_decay=0.1, math=math)
+    assert K.operator_status()[0] == TIMEOUT and torch.equal(w, w0)
+    K.orthogonal_step(x, m, w, lr=0.1, weight_decay=0.1, math=math)
+    assert K.operator_status() == (0, 0) and not torch.isnan(w).any() and (w != w0).any()
