@@ -683,7 +683,8 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  *   X = x / (|x|_F + eps);  per step: L = X X^T, X <- (a I + b L + c L^2) X;  out = X
  * (L = X^T X and X <- X (...) where rows > cols).  A singular value t of X becomes a t +
  * b t^3 + c t^5, its singular vectors stay.  A matrix of zeros gives zeros; Inf or NaN
- * anywhere in x makes all of its out NaN.  x, out: [rows x cols], sides up to 32768 (else
+ * anywhere in x makes all of its out NaN.  Small matrices are as exact as others, down to
+ * |x|_F of 2^-90 (|x|_F + eps).  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
  * count.  out may be x with the same leading dimension; no out may be given twice, and
  * other overlaps are not allowed.  All matrices go through each product together, up to

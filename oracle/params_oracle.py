@@ -100,13 +100,18 @@ def orthogonal_step(grad, m, w, lr, momentum=0.95, weight_decay=0.0, nesterov=Tr
     return m, w - lr * (scale * o + weight_decay * w)
 
 
-def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, groups=None):
+def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, groups=None, mirror=False):
     """The products with every matrix between them rounded to fp16's 11 bits (x too): the error that
     such operands cannot avoid.  groups: sizes of the groups of steps taken on the small side before x
-    is formed (None: single steps)."""
+    is formed (None: single steps).  mirror: of the products on the small side the upper half is stored
+    on both sides, so that their roundings are equal in pairs."""
     def near(v):
         m, e = np.frexp(v)
         return np.ldexp(np.rint(m * 2.0 ** 11), e - 11)
+
+    def both(v):
+        v = near(v)
+        return np.triu(v) + np.triu(v, 1).T if mirror else v
     x = np.asarray(x, np.float64)
     x = x.T if x.shape[0] > x.shape[1] else x
     x = near(x) / (np.sqrt((x * x).sum()) + eps)
@@ -117,9 +122,9 @@ def newton_schulz_fp16(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, groups=N
         g, p = near(x @ x.T), None
         for j in range(size):
             m = near(a * eye + b * g + c * g @ g)
-            p = m if p is None else near(m @ p)
+            p = m if p is None else both(m @ p)
             if j + 1 < size:
-                g = near(near(g @ m) @ m)
+                g = both(both(g @ m) @ m)
         k += size
         x = p @ x
         x = x if k == steps else near(x)

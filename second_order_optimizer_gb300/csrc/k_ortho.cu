@@ -70,7 +70,7 @@ struct PrepTask {
   int64_t ldx, ldm;
   __half *hi, *lo;         // X_0, rows of `pitch`
   float* part;             // [blocks][3]: squares by range
-  float* r;                // the factor r; behind it the word of a lost product (see Task)
+  float* r;                // the factor r, the word of a lost product (see Task) and the exponent j
   int rows, cols, pitch;
   int tx;                  // threads per row (a power of two)
   int vec;                 // whole 16-byte vectors of x (and of m)
@@ -79,7 +79,8 @@ struct PrepLaunch {
   PrepTask task[kMaxGroup];
   int block_start[kMaxGroup + 1];
   int count;
-  float mu, eps;
+  double eps;
+  float mu;
   int nesterov;
 };
 
@@ -244,23 +245,30 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const __grid_c
 }
 
 // From the squares by range (big, plain, small): 2^k (in two factors, each within fp32's range)
-// with |x 2^k|_F in (2^13, 2^14], and r with x / (|x| + eps) = r x 2^k.
-__device__ __forceinline__ void scale_factors(const double (&sums)[3], float eps, float (&up)[2], float* r_out) {
-  const double norm = sqrt(sums[0] * 0x1p168 + sums[1] + sums[2] * 0x1p-176) + (double)eps;
+// with |x 2^k|_F in [2^13, 2^14), and r and j with x / (|x| + eps) = r 2^-j x 2^k, where 2^-j is just
+// above |x| / (|x| + eps).  (j is 0 unless |x| < eps.  Then all of X is that small, and is kept times a
+// power of two through the steps, see Plan: scaled as if |X| were 1 it would fall out of fp16's range.  Of
+// 256 x 512 in full arithmetic, |x| = 1e-13 and eps = 1e-7 were 4.7e-4 off, 1e-15 4.7e-2.)
+__device__ __forceinline__ void scale_factors(const double (&sums)[3], double eps, float (&up)[2], float* r_out,
+                                              float* j_out) {
+  const double x = sqrt(sums[0] * 0x1p168 + sums[1] + sums[2] * 0x1p-176), norm = x + eps;
   float r = 0.f;
-  int k = 0;
-  if (norm > 0.0 && isfinite(norm)) {
+  int k = 0, j = 0;
+  if (x > 0.0 && isfinite(norm)) {
     int e = 0;
-    frexp(norm, &e);                         // norm < 2^e
+    frexp(x, &e);                            // x < 2^e
     k = 14 - e;
-    r = (float)ldexp(1.0 / norm, -k);
-  } else if (norm != 0.0) {                  // Inf and NaN reach everything through r
+    frexp(x / norm, &e);
+    j = max(0, -e);
+    r = (float)ldexp(1.0 / norm, j - k);
+  } else if (x != 0.0) {                     // Inf and NaN reach everything through r
     r = __int_as_float(0x7fffffff);
   }
   const int k0 = min(max(k, -126), 126);
   up[0] = ldexpf(1.f, k0);
   up[1] = ldexpf(1.f, k - k0);
   *r_out = r;
+  *j_out = (float)j;
 }
 
 template <typename T, bool kStep, bool kFull>
@@ -283,13 +291,14 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_
   __syncthreads();
   if (threadIdx.x == 0) {
     const double all[3] = {sums[0], sums[1], sums[2]};
-    float up[2], r;
-    scale_factors(all, g.eps, up, &r);
+    float up[2], r, j;
+    scale_factors(all, g.eps, up, &r, &j);
     factor[0] = up[0];
     factor[1] = up[1];
     if (block == 0) {
       t.r[0] = r;
       t.r[1] = 0.f;
+      t.r[2] = j;
     }
   }
   __syncthreads();
@@ -316,18 +325,20 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const __grid_
 // the weights.
 enum { TO_MATRIX, TO_OUT, TO_WEIGHTS };
 
-// out = alpha r^rpow A B^T [+ beta add + diag I], stored as fp16, or as it is below
+// out = alpha r^rpow 2^e A B^T [+ beta add + diag I], stored as fp16, or as it is below.  X before step k
+// is kept times 2^max(0, j + shift_k): of the product of an X, e takes that away (xpow times), and adds
+// what the X that it gives has.
 struct Task {
   int64_t out_ld;
   void* out;                    // TO_OUT: the direction; TO_WEIGHTS: the weights, fp32
   const __half *add_hi, *add_lo;   // or null
   __half *mirror_hi, *mirror_lo;   // upper: the result itself, whose other half is stored directly
-  float* r;                     // r, and a word that is not 0 once a product of this matrix is lost: a wait
+  float* r;                     // r, j behind it, and between them a word that is not 0 once a product of this matrix is lost: a wait
                                 // gave up, so its tile was not stored, and what the last launch makes of it is
                                 // NaN (weights: left as they were)
   float alpha, beta, diag;
   float keep, rate;             // TO_WEIGHTS: W <- keep W - rate X
-  int rpow, add_pitch, mirror_pitch;
+  int rpow, xpow, shift_in, shift_out, add_pitch, mirror_pitch;
   int M, N, kblocks;            // sizes of the product; k in blocks of 64
   int tiles_m, upper;           // upper: symmetric, tiles on and above the diagonal
   int mn_a, mn_b;               // operands read as MN-major tiles
@@ -752,9 +763,11 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
       };
       if (TO == TO_MATRIX && !kFull && k.add_hi) load_addend(k.add_hi, cols0);
       float alpha = k.alpha;
-      if (k.rpow) {
+      if (k.xpow) {
         const float r = __ldg(k.r);
-        alpha *= k.rpow == 2 ? r * r : r;
+        const int j = (int)__ldg(k.r + 2);
+        if (k.rpow) alpha *= k.rpow == 2 ? r * r : r;
+        if (j > 0) alpha = ldexpf(alpha, max(0, j + k.shift_out) - k.xpow * max(0, j + k.shift_in));
       }
       float sum[kFull ? CW : 1];
       if constexpr (kFull) {
@@ -951,6 +964,8 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
   }
 }
 
+constexpr int kNoShift = -(1 << 20);   // below any j
+
 // --------------------------------------------------------------------------- small matrices
 
 #include "ortho_small.cuh"
@@ -988,6 +1003,9 @@ struct Plan {
   int steps = 0;
   double a[kMaxSteps], b[kMaxSteps], c[kMaxSteps];
   double u[kMaxSteps + 1], v[kMaxSteps];   // of the singular values before step k, of |M|
+  // Where those of X_0 are at most 2^-j, step k's are at most 2^-j v_0 v_1 ... v_(k-1) too: X may be kept
+  // times 2^max(0, j + shift_k), below the bound u_k that it is scaled to
+  int shift[kMaxSteps + 1];
   std::vector<int> groups;
 };
 // The power of two that brings a matrix of this bound below 2^15.
@@ -995,6 +1013,7 @@ double scale_of(double bound) { return std::exp2(std::floor(std::log2(32000.0 / 
 constexpr double kMaxGrowth = 150.0;   // of L's rounding within a group
 kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
   p->steps = d->steps;
+  double all_v = 1.0;
   double u = 1.0;   // bound of the singular values, a little above what exact arithmetic gives
   for (int k = 0; k < d->steps; ++k) {
     const double a = d->coefficients ? d->coefficients[3 * k] : 3.4445;
@@ -1027,9 +1046,12 @@ kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
     p->c[k] = c;
     p->u[k] = u;
     p->v[k] = v;
+    p->shift[k] = std::min(0, (int)std::floor(std::log2(u / all_v)));
+    all_v *= v;
     u = next;
   }
   p->u[d->steps] = u;
+  p->shift[d->steps] = kNoShift;   // the result is what it is
   for (int k = 0; k < d->steps;) {
     int g = 1;
     double growth = p->v[k] * p->v[k];
@@ -1067,6 +1089,7 @@ struct Op {
   int a, b, out, add;           // add: buffer or -1
   double alpha, beta, diag;
   int rpow, upper;
+  int xpow, shift_in, shift_out;   // see Task
 };
 // A matrix's products, those of one entry at the same time.
 std::vector<std::vector<Op>> ops_of(const Plan& p, bool group) {
@@ -1077,13 +1100,14 @@ std::vector<std::vector<Op>> ops_of(const Plan& p, bool group) {
     const bool first = k == 0, last = k + g == p.steps;
     const double sx = first ? 1.0 : scale_of(p.u[k]);   // X_0's factor is r, on the device
     double sl = scale_of(p.u[k] * p.u[k]);
-    ops.push_back({{x, x, GRAM, -1, sl / (sx * sx), 0.0, 0.0, first ? 2 : 0, 1}});
+    const int shift_in = p.shift[k];
+    ops.push_back({{x, x, GRAM, -1, sl / (sx * sx), 0.0, 0.0, first ? 2 : 0, 1, 2, shift_in, kNoShift}});
     int prod = PROD_0;
     double sp = 1.0, bound = 1.0;
     for (int j = 0; j < g; ++j, ++k) {
       const double sm = scale_of(p.v[k]);
       const int poly = j == 0 ? PROD_0 : POLY;
-      ops.push_back({{GRAM, GRAM, poly, GRAM, sm * p.c[k] / (sl * sl), sm * p.b[k] / sl, sm * p.a[k], 0, 1}});
+      ops.push_back({{GRAM, GRAM, poly, GRAM, sm * p.c[k] / (sl * sl), sm * p.b[k] / sl, sm * p.a[k], 0, 1, 0, 0, 0}});
       std::vector<Op> both;
       bound *= p.v[k];
       if (j == 0) {
@@ -1091,15 +1115,15 @@ std::vector<std::vector<Op>> ops_of(const Plan& p, bool group) {
       } else {   // P <- M P
         const double to = scale_of(bound);
         const int next = prod == PROD_0 ? PROD_1 : PROD_0;
-        both.push_back({POLY, prod, next, -1, to / (sm * sp), 0.0, 0.0, 0, 1});
+        both.push_back({POLY, prod, next, -1, to / (sm * sp), 0.0, 0.0, 0, 1, 0, 0, 0});
         prod = next;
         sp = to;
       }
       if (j + 1 < g) {   // L <- (L M) M
         const double st = scale_of(p.u[k] * p.u[k] * p.v[k]), to = scale_of(p.u[k + 1] * p.u[k + 1]);
-        both.push_back({GRAM, poly, TEMP, -1, st / (sl * sm), 0.0, 0.0, 0, 1});
+        both.push_back({GRAM, poly, TEMP, -1, st / (sl * sm), 0.0, 0.0, 0, 1, 0, 0, 0});
         ops.push_back(both);
-        ops.push_back({{TEMP, poly, GRAM, -1, to / (st * sm), 0.0, 0.0, 0, 1}});
+        ops.push_back({{TEMP, poly, GRAM, -1, to / (st * sm), 0.0, 0.0, 0, 1, 0, 0, 0}});
         sl = to;
       } else if (!both.empty()) {
         ops.push_back(both);
@@ -1107,7 +1131,7 @@ std::vector<std::vector<Op>> ops_of(const Plan& p, bool group) {
     }
     const double to = last ? 1.0 : scale_of(p.u[k]);
     const int next = last ? BUFFERS : x == X_0 ? X_1 : X_0;
-    ops.push_back({{prod, x, next, -1, to / (sp * sx), 0.0, 0.0, first ? 1 : 0, 0}});
+    ops.push_back({{prod, x, next, -1, to / (sp * sx), 0.0, 0.0, first ? 1 : 0, 0, 1, shift_in, p.shift[k]}});
     x = next;
   }
   return ops;
@@ -1168,7 +1192,7 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
         for (int h = 0; h < halves && has_buffer(m, d->steps, b); ++h)
           m.at[b][h] = take(b == X_0 || b == X_1 ? (size_t)m.rows * m.xp * 2 : (size_t)m.s * m.sp * 2);
       m.part = take(kPrepBlocks * 3 * sizeof(float));
-      m.r = take(2 * sizeof(float));
+      m.r = take(3 * sizeof(float));
     }
     if (out) out->push_back(m);
   }
@@ -1331,14 +1355,15 @@ kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>
         const double sx = k == 0 ? 1.0 : scale_of(plan.u[k]), to = k + 1 == plan.steps ? 1.0 : scale_of(plan.u[k + 1]);
         const double sl = scale_of(plan.u[k] * plan.u[k]), sm = scale_of(plan.v[k]);
         g->step[k] = {(float)(sl / (sx * sx)), (float)(sm * plan.c[k] / (sl * sl)),
-                      (float)(sm * plan.b[k] / sl), (float)(sm * plan.a[k]), (float)(to / (sm * sx))};
+                      (float)(sm * plan.b[k] / sl), (float)(sm * plan.a[k]), (float)(to / (sm * sx)),
+                      plan.shift[k], plan.shift[k + 1]};
       }
       g->cluster = cs;
       // a matrix's columns are divided by its own length alone: the sums' order is the same in any company
       g->tiles = cs == 1 ? (int)cdiv(longest, 64) : SmallCfg<kFull>::most_tiles(cs);
       g->nesterov = c.hp ? c.hp->nesterov : 0;
       g->mu = c.hp ? (float)c.hp->momentum : 0.f;
-      g->eps = (float)c.d->eps;
+      g->eps = c.d->eps;
       g->keep = c.hp ? keep_of(c) : 1.f;
       kfac_status e;
       const bool bf16 = c.d->dtype == KFAC_BF16;
@@ -1386,7 +1411,7 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
     g->count = n;
     g->mu = c.hp ? (float)c.hp->momentum : 0.f;
     g->nesterov = c.hp ? c.hp->nesterov : 0;
-    g->eps = (float)c.d->eps;
+    g->eps = c.d->eps;
     const dim3 grid((unsigned)blocks), block(kPrepThreads);
     if (c.hp) {
       if (bf16) launch_pdl(ortho_norm_kernel<__nv_bfloat16, true>, grid, block, 0, st, *g);
@@ -1440,6 +1465,9 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
         t.beta = (float)op.beta;
         t.diag = (float)op.diag;
         t.rpow = op.rpow;
+        t.xpow = op.xpow;
+        t.shift_in = op.shift_in;
+        t.shift_out = op.shift_out;
         t.upper = op.upper;
         t.same_ab = op.a == op.b;
         int a = op.a, b = op.b;

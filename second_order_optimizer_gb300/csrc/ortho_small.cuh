@@ -23,14 +23,18 @@ struct SmallTask {
   int64_t ldo;
   float rate;
 };
-struct SmallStep { float gram, poly, beta, diag, apply; };
+struct SmallStep {
+  float gram, poly, beta, diag, apply;
+  int shift_in, shift_out;                       // of X before and after the step, see Plan
+};
 struct SmallLaunch {
   SmallTask task[kSmallTasks];
   SmallStep step[kMaxSteps];
   int steps, cluster, tiles;                     // tiles: of 64 columns per block
   int nesterov;
   int give_up;                                   // self-test: a step whose first wait counts as one that ran out
-  float mu, eps, keep;
+  float mu, keep;
+  double eps;
 };
 
 template <bool kFull> struct SmallCfg {
@@ -65,7 +69,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
   __shared__ uint64_t done;
   __shared__ uint32_t tmem_slot, lost;   // lost: a block of the cluster gave up
   __shared__ float red[3][kSmallThreads / 32];
-  __shared__ float parts[8][3], factors[3];
+  __shared__ float parts[8][3], factors[4];
   uint8_t* smem = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* const xs = smem;                                            // [halves][tiles]
   uint8_t* const ls = xs + (size_t)HALVES * g.tiles * kTileBytes;      // [halves][2]: L, then M
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       }
     }
   };
-  float up0, up1, r;
+  float up0, up1;
   {
     Squares sq;
     visit_by(std::true_type(), [&](int row, int c, auto& u) {
@@ -191,14 +195,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
       for (int c = 0; c < cs; ++c)
         for (int k = 0; k < 3; ++k) sums[k] += (double)parts[c][k];
       float up[2];
-      scale_factors(sums, g.eps, up, &factors[2]);
+      scale_factors(sums, g.eps, up, &factors[2], &factors[3]);
       factors[0] = up[0];
       factors[1] = up[1];
     }
     __syncthreads();
     up0 = factors[0];
     up1 = factors[1];
-    r = factors[2];
   }
   auto halves_of = [&](float x, uint16_t& hi, uint16_t& lo) {
     const float v = x * up0 * up1;
@@ -323,7 +326,13 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
                 (!kFull && c > 0) || kk > 0 || (kFull && pass == 1));
           }
     }, step == g.give_up && rank == 0);
-    const float gram = step == 0 ? p.gram * r * r : p.gram;
+    // X is kept times 2^max(0, j + shift): see Plan (factors: r, j)
+    auto scaled = [&](float by, int power, int shift_out) {
+      const int j = (int)factors[3];
+      if (step == 0) by *= power == 2 ? factors[2] * factors[2] : factors[2];
+      return j > 0 ? ldexpf(by, max(0, j + shift_out) - power * max(0, j + p.shift_in)) : by;
+    };
+    const float gram = scaled(p.gram, 2, kNoShift);
     float v[32];
     load32(32 * h, 128, used, v);
     if (cs == 1) {
@@ -408,7 +417,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
           }
         }
     });
-    const float apply = step == 0 ? p.apply * r : p.apply;
+    const float apply = scaled(p.apply, 1, p.shift_out);
     for (int piece = h; piece < 2 * used; piece += 4) {
       load32(32 * piece, 256, (k16 + 3) / 4, v);
 #pragma unroll
