@@ -390,7 +390,8 @@ def orthogonal_step(grads, momenta, params, lr: float, momentum: float = 0.95,
                     steps: int = 5, coefficients=None, eps: float = 1e-7, math=None, workspace=None,
                     stream=None):
     """kfac_orthogonal_step: one optimizer step of each matrix along its orthogonalised momentum.
-    grads: as orthogonalize's x; momenta, params: float32 of the same shapes, updated in place."""
+    grads: as orthogonalize's x; momenta, params: float32 of the same shapes, updated in place.  math:
+    as there, by the gradients' type: KFAC_ORTHO_HALF for bfloat16 ones, whatever the momenta are."""
     what = "orthogonal_step"
     g = _Matrices(what, "grads", grads)
     m = _Matrices(what, "momenta", momenta, torch.float32, like=g)

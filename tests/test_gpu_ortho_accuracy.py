@@ -72,3 +72,35 @@ def test_eps_beyond_fp32():
         assert (K.orthogonalize(x, eps=1e300) == 0).all()
         x[0, 0] = float("inf")
         assert torch.isnan(K.orthogonalize(x, eps=1e300)).all()
+
+
+def _low_rank(rows, cols, rank):
+    return _randn(rank, rows, rank) @ _randn(rank + 1, rank, cols)
+
+
+def _falling(rows, cols, least):
+    """Singular values from 1 to `least`, evenly in their logarithm."""
+    s = min(rows, cols)
+    u, v = np.linalg.qr(_randn(5, rows, s))[0], np.linalg.qr(_randn(6, cols, s))[0]
+    return (u * np.logspace(0, np.log10(least), s)) @ v.T
+
+
+SPECTRA = [(256, 512, None), (60, 1000, None), (700, 120, None), (1030, 1600, (3, 2))]
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols,groups", SPECTRA)
+def test_low_rank(rows, cols, groups, dtype, math):
+    """Gradients of fewer tokens than channels: the steps lift what rounding leaves in the empty
+    directions, by up to 3.4445^5."""
+    for rank in (1, 4, min(rows, cols) // 8):
+        off, tol = _off(_low_rank(rows, cols, rank), dtype, math, groups)
+        assert off <= tol, (rank, off, tol)
+
+
+@pytest.mark.parametrize("dtype,math", FORMS)
+@pytest.mark.parametrize("rows,cols,groups", SPECTRA)
+def test_falling_spectra(rows, cols, groups, dtype, math):
+    for least in (1e-2, 1e-4, 1e-6):
+        off, tol = _off(_falling(rows, cols, least), dtype, math, groups)
+        assert off <= tol, (least, off, tol)
