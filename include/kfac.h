@@ -633,8 +633,8 @@ kfac_status kfac_embedding(const kfac_embedding_desc* desc, const void* ids, con
                            void* out, cudaStream_t stream);
 
 /* Bytes of workspace that kfac_embedding_backward needs on the current device (a
- * 256-byte multiple).  It holds nothing between calls; calls that share one must be
- * ordered. */
+ * 256-byte multiple); enough for fewer tokens or rows of the same width too.  It holds
+ * nothing between calls; calls that share one must be ordered. */
 kfac_status kfac_embedding_workspace_size(int64_t tokens, int64_t rows, int64_t width,
                                           size_t* bytes);
 

@@ -252,7 +252,7 @@ def embedding(ids, table, scale: float = 1.0, out=None, stream=None):
 
 
 def embedding_workspace(ids, rows: int, width: int):
-    """A workspace tensor for embedding_backward of as many ids, to be kept and passed to it."""
+    """A workspace tensor for embedding_backward of as many ids or fewer, to be kept and passed to it."""
     dev = _device(ids, "embedding_workspace")
     return _kept(_sized(LIB.kfac_embedding_workspace_size, "kfac_embedding_workspace_size", dev,
                         ids.numel(), rows, width), dev)

@@ -726,10 +726,12 @@ template <typename T, int N> kfac_status launch_sums(const EmbedArgs& a, cudaStr
 // Sorted positions per chunk: at least two stages of rows, else one wave of the chunks' blocks (three
 // per SM, of up to 2048 channels; narrow rows: eight chunks a block).  16384 x 2048 in bf16 in chunks
 // of 36: sums and joins 25 and 7 us, of 16 (2.2 waves) 29 and 12.
-int chunk_of(int64_t tokens, int64_t width) {
+int64_t chunks_of_wave(int64_t width) {
   const int64_t blocks = std::max<int64_t>(1, 3 * (int64_t)num_sms() / cdiv(std::max<int64_t>(width, 1), 2048));
-  const int64_t wave = width <= 512 ? 8 * blocks : blocks;
-  return (int)std::max<int64_t>(2 * kStageRows, cdiv(tokens, wave));
+  return width <= 512 ? 8 * blocks : blocks;
+}
+int chunk_of(int64_t tokens, int64_t width) {
+  return (int)std::max<int64_t>(2 * kStageRows, cdiv(tokens, chunks_of_wave(width)));
 }
 
 struct Layout {
@@ -752,8 +754,9 @@ Layout layout_of(int64_t tokens, int64_t rows, int64_t width) {
   l.end = take((size_t)rows * 4);
   l.hist = take(small ? 0 : (size_t)cdiv(tokens, kTileItems) * kDigits * 4);
   l.total = take(small ? 0 : kDigits * 4);
-  const int chunk = chunk_of(tokens, width);
-  l.part = take(tokens > chunk ? (size_t)cdiv(tokens, chunk) * 2 * (size_t)width * 4 : 0);
+  // as many parts as any smaller number of tokens takes: a chunk more than this one's can be fewer chunks
+  const int64_t chunks = std::min(cdiv(tokens, 2 * kStageRows), chunks_of_wave(width));
+  l.part = take(chunks > 1 ? (size_t)chunks * 2 * (size_t)width * 4 : 0);
   l.bytes = at;
   return l;
 }

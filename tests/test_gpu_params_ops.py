@@ -364,3 +364,20 @@ def test_streams_and_graphs():
             g.replay()
     for _, out, gr in graphs:
         assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(gr, grads))
+
+
+@pytest.mark.parametrize("tokens", [7753, 16385])
+def test_embedding_workspace_kept_for_the_largest_batch(tokens):
+    """One token fewer may take more chunks: the kept workspace serves it all the same."""
+    rows, width = 50021, 2048
+    g = torch.Generator(device="cuda")
+    g.manual_seed(tokens)
+    ids = torch.randint(0, rows, (tokens,), generator=g, device="cuda")
+    dout = torch.randn(tokens, width, generator=g, device="cuda").bfloat16()
+    work = K.embedding_workspace(ids, rows, width)
+    for n in (tokens, tokens - 1, tokens - 2, 5000, 17, 1, 0):
+        got = K.embedding_backward(ids[:n], dout[:n], rows, workspace=work)
+        # at most a dozen tokens of one id: sums of 12 values, 2^-24 of each partial sum
+        want = torch.zeros(rows, width, device="cuda", dtype=torch.float64).index_add_(0, ids[:n], dout[:n].double())
+        size = torch.zeros(rows, width, device="cuda", dtype=torch.float64).index_add_(0, ids[:n], dout[:n].double().abs())
+        assert ((got - want).abs() <= 12 * 2.0 ** -24 * size).all(), n

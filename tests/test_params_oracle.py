@@ -309,3 +309,18 @@ def test_python_refuses_matrices_that_do_not_fit(lib):
         _params._ortho_desc("orthogonalize", 0, None, 3, 0.0, [(1, 2, 3), (1, 2, 3)])
     desc, flat = _params._ortho_desc("orthogonalize", 0, None, 2, 0.0, (1.5, -0.5, 0))
     assert list(flat) == [1.5, -0.5, 0, 1.5, -0.5, 0]
+
+
+@pytest.mark.parametrize("width", [1, 80, 512, 513, 2048, 8191, 1 << 20])
+def test_embedding_workspace_serves_smaller_calls(lib, width):
+    n = ctypes.c_size_t(0)
+
+    def size(tokens, rows=50021):
+        assert lib.LIB.kfac_embedding_workspace_size(tokens, rows, width, ctypes.byref(n)) == 0
+        return n.value
+
+    most = 0
+    for tokens in [*range(1, 40), *range(7600, 7800), *range(16000, 16500, 3), *range(50000, 50600, 7), 1 << 20]:
+        assert size(tokens) >= most, tokens
+        most = size(tokens)
+        assert size(tokens, 50020) <= most
