@@ -685,8 +685,9 @@ typedef struct {
  * matrices of these sizes (host arrays; a 256-byte multiple): about 4 bytes per element
  * and 4 per element of the square of the smaller side (10 where steps are taken in
  * groups), twice that in full arithmetic; none if every matrix has a smaller side of at
- * most 128 and a larger one of at most 4096 (full arithmetic: 1536).  It holds nothing between
- * calls; calls that share one must be ordered. */
+ * most 128 and a larger one of at most 4096 (full arithmetic: 1536).  Enough for any of these
+ * matrices by themselves too.  It holds nothing between calls; calls that share one must
+ * be ordered. */
 kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int count, const int* rows,
                                               const int* cols, size_t* bytes);
 

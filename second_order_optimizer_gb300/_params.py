@@ -348,8 +348,8 @@ def _ortho_desc(what, dt, math, steps, eps, coefficients):
 
 
 def orthogonalize_workspace(x, math=None):
-    """A workspace tensor for orthogonalize or orthogonal_step of matrices like x (tensor or list;
-    orthogonal_step: the gradients), to be kept and passed to the calls."""
+    """A workspace tensor for orthogonalize or orthogonal_step of matrices like x, or of some of them
+    (tensor or list; orthogonal_step: the gradients), to be kept and passed to the calls."""
     what = "orthogonalize_workspace"
     m = _Matrices(what, "x", x)
     # (any number of steps but one takes the same)

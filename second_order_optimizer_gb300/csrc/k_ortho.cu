@@ -1154,47 +1154,77 @@ kfac_status check_sizes(const kfac_ortho_desc* d, int count, const int* rows, co
 // Matrices that a product launch takes: up to two tasks each.
 int per_launch(int halves) { return (halves == 2 ? Launch<true>::TASKS : Launch<false>::TASKS) / 2; }
 
-// Regions of the workspace; matrices without elements take none and are left out.
-size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* cols,
-               std::vector<Matrix>* out) {
-  size_t at = 0;
+// Blocks of the small matrices' kernel for a matrix; 0: too large for it.
+int cluster_of(int s, int l, int halves) {
+  return s > kSide ? 0 : halves == 2 ? small_cluster<true>(l) : small_cluster<false>(l);
+}
+// A matrix's regions of the workspace, from `at` on; returns where they end.
+size_t lay_out_matrix(Matrix* m, int steps, int halves, size_t at) {
   auto take = [&](size_t bytes) {
     const size_t here = at;
     at += align_up(bytes);
     return here;
   };
+  m->xp = (int)pitch_of(m->cols);
+  m->sp = (int)pitch_of(m->s);
+  for (int b = 0; b < BUFFERS; ++b)
+    for (int h = 0; h < halves && has_buffer(*m, steps, b); ++h)
+      m->at[b][h] = take(b == X_0 || b == X_1 ? (size_t)m->rows * m->xp * 2 : (size_t)m->s * m->sp * 2);
+  m->part = take(kPrepBlocks * 3 * sizeof(float));
+  m->r = take(3 * sizeof(float));
+  return at;
+}
+Matrix matrix_of(int rows, int cols, int steps) {
+  Matrix m{};
+  m.rows = rows;
+  m.cols = cols;
+  m.s = std::min(rows, cols);
+  m.l = std::max(rows, cols);
+  m.tall = rows > cols;
+  m.group = steps > 1 && grouped(m.s, m.l);
+  return m;
+}
+// What any of the matrices need, together or not: all the large ones, and as many of the small ones,
+// the longest regions, as ever ride with them (lay_out).
+size_t workspace_bytes(const kfac_ortho_desc* d, int count, const int* rows, const int* cols) {
+  const int halves = d->math == KFAC_ORTHO_FULL ? 2 : 1, most = per_launch(halves) - 1;
+  size_t bytes = 0, riding[kMaxGroup] = {};   // in falling order
+  bool large = false;
+  for (int i = 0; i < count; ++i) {
+    Matrix m = matrix_of(rows[i], cols[i], d->steps);
+    if (m.s == 0) continue;
+    size_t n = lay_out_matrix(&m, d->steps, halves, 0);
+    if (!cluster_of(m.s, m.l, halves)) {
+      bytes += n;
+      large = true;
+      continue;
+    }
+    for (int k = 0; k < most; ++k)
+      if (n > riding[k]) std::swap(n, riding[k]);
+  }
+  for (int k = 0; k < most && large; ++k) bytes += riding[k];
+  return bytes;
+}
+
+// Regions of the workspace; matrices without elements take none and are left out.
+size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* cols,
+               std::vector<Matrix>* out) {
+  size_t at = 0;
   const int halves = d->math == KFAC_ORTHO_FULL ? 2 : 1;
-  auto cluster = [&](int s, int l) {
-    return s > kSide ? 0 : halves == 2 ? small_cluster<true>(l) : small_cluster<false>(l);
-  };
   // Small matrices have a kernel of their own, unless the others' launches have room for them: there
   // they cost next to nothing (the MLP set's 10 x 1024 beside three of 1024 x 1024 in full
   // arithmetic: 85 us by itself).
   int64_t small = 0, large = 0;
   for (int i = 0; i < count; ++i) {
     const int s = std::min(rows[i], cols[i]);
-    if (s > 0) ++(cluster(s, std::max(rows[i], cols[i])) ? small : large);
+    if (s > 0) ++(cluster_of(s, std::max(rows[i], cols[i]), halves) ? small : large);
   }
   const int64_t room = cdiv(large, per_launch(halves)) * per_launch(halves) - large;
   for (int i = 0; i < count; ++i) {
-    Matrix m{};
-    m.rows = rows[i];
-    m.cols = cols[i];
-    m.s = std::min(rows[i], cols[i]);
-    m.l = std::max(rows[i], cols[i]);
-    m.tall = rows[i] > cols[i];
-    m.group = d->steps > 1 && grouped(m.s, m.l);
-    if (m.s > 0 && small > room) m.cluster = cluster(m.s, m.l);
-    if (m.s > 0 && !m.cluster) {
-      m.xp = (int)pitch_of(m.cols);
-      m.sp = (int)pitch_of(m.s);
-      for (int b = 0; b < BUFFERS; ++b)
-        for (int h = 0; h < halves && has_buffer(m, d->steps, b); ++h)
-          m.at[b][h] = take(b == X_0 || b == X_1 ? (size_t)m.rows * m.xp * 2 : (size_t)m.s * m.sp * 2);
-      m.part = take(kPrepBlocks * 3 * sizeof(float));
-      m.r = take(3 * sizeof(float));
-    }
-    if (out) out->push_back(m);
+    Matrix m = matrix_of(rows[i], cols[i], d->steps);
+    if (m.s > 0 && small > room) m.cluster = cluster_of(m.s, m.l, halves);
+    if (m.s > 0 && !m.cluster) at = lay_out_matrix(&m, d->steps, halves, at);
+    out->push_back(m);
   }
   return at;
 }
@@ -1592,7 +1622,7 @@ extern "C" kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* 
                                                          size_t* bytes) {
   if (!bytes) return KFAC_ERR_INVALID_ARG;
   if (kfac_status e = check_sizes(d, count, rows, cols)) return e;
-  *bytes = lay_out(d, count, rows, cols, nullptr);
+  *bytes = workspace_bytes(d, count, rows, cols);
   return KFAC_OK;
 }
 

@@ -324,3 +324,30 @@ def test_embedding_workspace_serves_smaller_calls(lib, width):
         assert size(tokens) >= most, tokens
         most = size(tokens)
         assert size(tokens, 50020) <= most
+
+
+def test_orthogonalize_workspace_serves_any_of_its_matrices(lib):
+    """Small matrices need none in a launch of their own, but some beside large ones: what is kept for
+    all of a list is enough for a part of it."""
+    rng = np.random.default_rng(0)
+    n = ctypes.c_size_t(0)
+
+    def size(shapes, math, steps):
+        ints = lambda v: (ctypes.c_int * len(shapes))(*v)
+        assert lib.LIB.kfac_orthogonalize_workspace_size(
+            lib.ORTHO_DESC.pack(1, math, steps, 0.0, 0), len(shapes), ints([s[0] for s in shapes]),
+            ints([s[1] for s in shapes]), ctypes.byref(n)) == 0
+        return n.value
+
+    for math in (0, 1):
+        shapes = [(64, 64)] * 30 + [(300, 200)]
+        assert size(shapes, math, 5) >= size(shapes[20:], math, 5) > 0
+        for _ in range(200):
+            shapes = [tuple(int(v) for v in rng.integers(0, 200, 2)) for _ in range(rng.integers(1, 70))]
+            shapes += [(int(rng.integers(129, 2000)), 1600) for _ in range(rng.integers(0, 5))]
+            if rng.random() < 0.2:
+                shapes += [(140, 150)] * int(rng.integers(10, 60))
+            some = [s for s in shapes if rng.random() < rng.choice([0.2, 0.5, 0.9])]
+            assert size(some, math, 5) <= size(shapes, math, 5)
+            assert size(shapes, math, 1) <= size(shapes, math, 5)
+    assert size([(64, 64)] * 40, 1, 5) == 0    # nothing for them to ride with
