@@ -642,7 +642,7 @@ kfac_status kfac_embedding_workspace_size(int64_t tokens, int64_t rows, int64_t 
  * (fp32 [rows x width]), over the tokens whose id is not padding_id (-1: none is
  * padding); ids outside [0, rows) are left out.  accumulate = 0: every row is written,
  * zeros where no token is; 1: added to dtable, whose other rows are not touched.
- * frequency (fp32 [rows], NULL: not wanted, always written whole): the share of the
+ * frequency (fp32 [rows], NULL: not wanted, always written whole; width > 0 then): the share of the
  * tokens that dtable[v] sums, count / tokens.  It is the diagonal of the A factor of the
  * one-hot inputs: a KFAC_DIAG layer of d_out = rows, d_in = width takes it as g_new, with
  * the mean squares of dout as a_new.  Sums are fp32 in a fixed order, no atomics: the

@@ -839,6 +839,7 @@ extern "C" kfac_status kfac_embedding_backward(const kfac_embedding_desc* d, con
   if (kfac_status e = check_desc(d, &es)) return e;
   if ((accumulate != 0 && accumulate != 1) || padding_id < -1 || (uintptr_t)frequency % 4)
     return KFAC_ERR_INVALID_ARG;
+  if (d->rows > 0 && d->width == 0 && frequency) return KFAC_ERR_INVALID_ARG;   // (no launch would write it)
   if (d->rows == 0 || d->width == 0) return KFAC_OK;
   if (bad_rows(dtable, d->ldt, d->rows, d->width, 4)) return KFAC_ERR_INVALID_ARG;
   if (d->tokens > 0 && (!ids || (uintptr_t)ids % (d->id_bits / 8) ||

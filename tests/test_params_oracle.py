@@ -351,3 +351,9 @@ def test_orthogonalize_workspace_serves_any_of_its_matrices(lib):
             assert size(some, math, 5) <= size(shapes, math, 5)
             assert size(shapes, math, 1) <= size(shapes, math, 5)
     assert size([(64, 64)] * 40, 1, 5) == 0    # nothing for them to ride with
+
+
+def test_embedding_backward_refuses_frequencies_of_rows_without_channels(lib):
+    """(They would be left unwritten.)"""
+    assert _embed_grad(lib, width=0, dt=None, freq=P) == A
+    assert _embed_grad(lib, width=0, dt=None) == 0 and _embed_grad(lib, rows=0, width=0, dt=None, freq=P) == 0
