@@ -698,11 +698,11 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  * anywhere in x makes all of its out NaN.  Small matrices are as exact as others, down to
  * |x|_F of 2^-90 (|x|_F + eps).  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
- * count.  out may be x with the same leading dimension; no out may be given twice, and
- * other overlaps are not allowed.  All matrices go through each product together, up to
- * 24 at a time (full arithmetic: 12); small ones take all steps in one launch, unless the
- * others' launches have room for them (a matrix's last bits may differ between the two).
- * The same call on the same inputs gives the same bits.  The coefficients have to keep
+ * count.  out may be its own x with the same leading dimension; no out may be given twice
+ * or be another's x, and other overlaps are not allowed.  All matrices go through each
+ * product together, up to 24 at a time (full arithmetic: 12); small ones take all steps in
+ * one launch, unless the others' launches have room for them (a matrix's last bits may
+ * differ between the two).  The same call on the same inputs gives the same bits.  The coefficients have to keep
  * the bound of the singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at
  * each step (else KFAC_ERR_INVALID_ARG). */
 kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int* rows,

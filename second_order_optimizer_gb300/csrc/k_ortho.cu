@@ -46,6 +46,7 @@
 #include <cstring>
 #include <memory>
 #include <type_traits>
+#include <utility>
 #include <vector>
 
 namespace kfac {
@@ -1583,13 +1584,27 @@ bool bad_matrix(const void* p, int64_t ld, int rows, int cols, size_t es) {
   return !p || (uintptr_t)p % es || ld < 0 || ld > (int64_t(1) << 40) || (rows > 1 && ld < cols);
 }
 
-// Whether two matrices are the same one (their results would depend on which came last).
-bool any_twice(void* const* p, int count, const int* rows, const int* cols) {
-  std::vector<void*> at;
+// Addresses of the matrices with elements, sorted, with their indexes.
+using Places = std::vector<std::pair<const void*, int>>;
+template <typename Q> Places places(Q const* p, int count, const int* rows, const int* cols) {
+  Places at;
   for (int i = 0; i < count; ++i)
-    if (rows[i] > 0 && cols[i] > 0) at.push_back(p[i]);
+    if (rows[i] > 0 && cols[i] > 0) at.emplace_back(p[i], i);
   std::sort(at.begin(), at.end());
-  return std::adjacent_find(at.begin(), at.end()) != at.end();
+  return at;
+}
+// Whether two matrices are the same one (their results would depend on which came last).
+bool any_twice(const Places& p) {
+  return std::adjacent_find(p.begin(), p.end(), [](auto& a, auto& b) { return a.first == b.first; }) != p.end();
+}
+// Whether a result (no two the same) lies where something else is read, other than as may(i) allows: the
+// matrix's own.
+template <typename F> bool any_shared(const Places& results, const Places& others, F may) {
+  for (auto& o : others) {
+    auto r = std::lower_bound(results.begin(), results.end(), std::make_pair(o.first, -1));
+    if (r != results.end() && r->first == o.first && (r->second != o.second || !may(o.second))) return true;
+  }
+  return false;
 }
 
 // A C entry lets no exception out: what can be thrown here is a failed host allocation.
@@ -1646,7 +1661,10 @@ extern "C" kfac_status kfac_orthogonalize(const kfac_ortho_desc* d, int count, c
   c.out = out;
   c.ldo = ldo;
   return guarded([&] {
-    if (any_twice(out, count, rows, cols)) return KFAC_ERR_INVALID_ARG;
+    const Places results = places(out, count, rows, cols);
+    if (any_twice(results) || any_shared(results, places(x, count, rows, cols),
+                                         [&](int i) { return rows[i] == 1 || ldx[i] == ldo[i]; }))
+      return KFAC_ERR_INVALID_ARG;
     return run(c, count, rows, cols, workspace, workspace_bytes, stream);
   });
 }
@@ -1671,8 +1689,12 @@ extern "C" kfac_status kfac_orthogonal_step(const kfac_ortho_desc* d, const kfac
       return KFAC_ERR_INVALID_ARG;
   }
   return guarded([&] {
-    std::vector<void*> out(param, param + count), m(momentum, momentum + count);
-    if (any_twice(out.data(), count, rows, cols) || any_twice(m.data(), count, rows, cols))
+    std::vector<void*> out(param, param + count);
+    const Places g = places(grad, count, rows, cols), m = places(momentum, count, rows, cols),
+                 w = places(param, count, rows, cols);
+    auto never = [](int) { return false; };
+    if (any_twice(w) || any_twice(m) || any_shared(w, m, never) || any_shared(w, g, never) ||
+        any_shared(m, g, never))
       return KFAC_ERR_INVALID_ARG;
     Call c{};
     c.d = d;

@@ -357,3 +357,20 @@ def test_embedding_backward_refuses_frequencies_of_rows_without_channels(lib):
     """(They would be left unwritten.)"""
     assert _embed_grad(lib, width=0, dt=None, freq=P) == A
     assert _embed_grad(lib, width=0, dt=None) == 0 and _embed_grad(lib, rows=0, width=0, dt=None, freq=P) == 0
+
+
+def test_orthogonalize_refuses_results_over_other_inputs(lib):
+    """In place is the same matrix with the same leading dimension; anything else would be read while it
+    is written."""
+    assert _ortho(lib, x=(P, 2 * P), out=(P, 5 * P), ldx=(4, 4), ldo=(8, 4)) == A     # another layout
+    assert _ortho(lib, x=(P, 2 * P), out=(2 * P, P)) == A                             # each other's
+    assert _ortho(lib, x=(P, P), out=(P, 5 * P)) == A                                 # x of the second as well
+    step = lambda **kw: _ortho(lib, step=True, **kw)
+    assert step(x=(P, 2 * P), m=(P, 6 * P)) == A and step(x=(P, 2 * P), out=(7 * P, P)) == A
+    assert step(m=(7 * P, 8 * P), out=(8 * P, 9 * P)) == A and step(m=(7 * P, 8 * P), out=(7 * P, 9 * P)) == A
+    # (these pass the checks: the next one, of the workspace, refuses)
+    big = dict(rows=(200, 4), cols=(300, 4), ldx=(300, 4), ldo=(300, 4), ws=None)
+    assert _ortho(lib, x=(P, 2 * P), out=(P, 2 * P), **big) == W
+    assert _ortho(lib, x=(P, P), out=(5 * P, 6 * P), **big) == W
+    assert _ortho(lib, x=(P, 2 * P), out=(P, 2 * P), **(big | dict(rows=(1, 200), cols=(4, 300), ldx=(4, 300), ldo=(9, 300)))) == W
+    assert step(**big) == W
