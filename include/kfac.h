@@ -569,7 +569,7 @@ kfac_status kfac_cross_attention_backward(const kfac_attention_desc* desc,
 typedef struct {
   int dtype;            /* kfac_dtype of x, residual, h, y and their gradients            */
   int64_t rows, cols;   /* cols <= 2^20                                                   */
-  double eps;           /* >= 0                                                           */
+  double eps;           /* >= 0; neither infinite nor, unless it is 0, zero as fp32       */
   int64_t ldx, ldr;     /* rows of x and of residual                                      */
   int64_t ldh, ldy;     /* of h and of y                                                  */
   int64_t ldq;          /* of q (bytes)                                                   */
@@ -586,7 +586,8 @@ typedef struct {
  * channels scale = max |y| / 448 and q = e4m3(y / scale), nearest even (a group of
  * zeros: scale 0, q 0); at most 8192 groups.  Inf or NaN in a row makes that row's
  * results NaN or, where exact arithmetic gives it, zero or Inf; squares whose sum passes
- * 2^128 count as Inf (r = 0).  Outputs may not overlap inputs, except that h may be x or
+ * 2^128 count as Inf (r = 0), squares below 2^-149 as zero; eps 0 makes a row of zeros NaN.
+ * Without columns nothing is written.  Outputs may not overlap inputs, except that h may be x or
  * residual with the same leading dimension. */
 kfac_status kfac_rms_norm(const kfac_norm_desc* desc, const void* x, const void* residual,
                           const float* gain, void* h, void* y, float* rstd, void* q,
@@ -710,6 +711,8 @@ kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int
                                void* const* out, const int64_t* ldo, void* workspace,
                                size_t workspace_bytes, cudaStream_t stream);
 
+/* (What the step uses, mu, 1 - eta lambda and eta kappa sqrt(max(1, rows / cols)), is finite as
+ * fp32.) */
 typedef struct {
   double lr;            /* eta                                                         */
   double momentum;      /* mu                                                          */

@@ -661,7 +661,8 @@ extern "C" kfac_status kfac_rms_norm(const kfac_norm_desc* d, const void* x, con
                                      const float* gain, void* h, void* y, float* rstd, void* q,
                                      float* scales, cudaStream_t stream) {
   if (!d || (d->dtype != KFAC_F32 && d->dtype != KFAC_BF16)) return KFAC_ERR_INVALID_ARG;
-  if (d->rows < 0 || d->cols < 0 || !(d->eps >= 0.0) || !std::isfinite(d->eps))
+  if (d->rows < 0 || d->cols < 0 || !(d->eps >= 0.0) || !std::isfinite((float)d->eps) ||
+      (d->eps > 0.0 && (float)d->eps == 0.f))
     return KFAC_ERR_INVALID_ARG;
   if (d->group != 0 && d->group != 32 && d->group != 64 && d->group != 128)
     return KFAC_ERR_INVALID_ARG;

@@ -1325,8 +1325,8 @@ PrepTask prep_task(const Call& c, const Matrix& m, int i) {
   while (t.tx < pieces && t.tx < kPrepThreads) t.tx *= 2;
   return t;
 }
-float rate_of(const Call& c, const Matrix& m) {
-  return (float)(c.hp->lr * c.hp->update_scale * std::sqrt(std::max(1.0, (double)m.rows / (double)m.cols)));
+float rate_of(const kfac_ortho_step& hp, int rows, int cols) {
+  return (float)(hp.lr * hp.update_scale * std::sqrt(std::max(1.0, (double)rows / (double)cols)));
 }
 float keep_of(const Call& c) { return (float)(1.0 - c.hp->lr * c.hp->weight_decay); }
 
@@ -1376,7 +1376,7 @@ kfac_status run_small(const Call& c, const Plan& plan, const std::vector<Matrix>
         t.in = prep_task(c, m, (int)at);
         t.out = c.out[at];
         t.ldo = c.ldo[at];
-        t.rate = c.hp ? rate_of(c, m) : 0.f;
+        t.rate = c.hp ? rate_of(*c.hp, m.rows, m.cols) : 0.f;
         longest = std::max(longest, m.l);
       }
       if (n == 0) continue;
@@ -1536,7 +1536,7 @@ kfac_status run_group(const Call& c, const Plan& plan, const std::vector<Matrix>
           t.out_ld = c.ldo[idx[i]];
           if (c.hp) {
             t.keep = keep_of(c);
-            t.rate = rate_of(c, m);
+            t.rate = rate_of(*c.hp, m.rows, m.cols);
           }
         }
       }
@@ -1681,8 +1681,11 @@ extern "C" kfac_status kfac_orthogonal_step(const kfac_ortho_desc* d, const kfac
   if (count == 0) return KFAC_OK;
   if (!grad || !ldg || !momentum || !ldm || !param || !ldp) return KFAC_ERR_INVALID_ARG;
   const size_t es = d->dtype == KFAC_BF16 ? 2 : 4;
+  if (!std::isfinite((float)hp->momentum) || !std::isfinite((float)(1.0 - hp->lr * hp->weight_decay)))
+    return KFAC_ERR_INVALID_ARG;
   for (int i = 0; i < count; ++i) {
     if (rows[i] == 0 || cols[i] == 0) continue;
+    if (!std::isfinite(rate_of(*hp, rows[i], cols[i]))) return KFAC_ERR_INVALID_ARG;
     if (bad_matrix(grad[i], ldg[i], rows[i], cols[i], es) ||
         bad_matrix(momentum[i], ldm[i], rows[i], cols[i], 4) ||
         bad_matrix(param[i], ldp[i], rows[i], cols[i], 4))

@@ -374,3 +374,15 @@ def test_orthogonalize_refuses_results_over_other_inputs(lib):
     assert _ortho(lib, x=(P, P), out=(5 * P, 6 * P), **big) == W
     assert _ortho(lib, x=(P, 2 * P), out=(P, 2 * P), **(big | dict(rows=(1, 200), cols=(4, 300), ldx=(4, 300), ldo=(9, 300)))) == W
     assert step(**big) == W
+
+
+def test_what_fp32_does_not_hold_is_refused(lib):
+    """eps that becomes infinite (results of 0) or zero (rows of zeros become NaN) as fp32; rates and
+    decays of the step likewise."""
+    assert _norm(lib, eps=1e39) == A and _norm(lib, eps=1e-46) == A
+    assert [_norm(lib, eps=e, rows=0) for e in (0.0, 1e-45, 1e-12, 3e38)] == [0] * 4
+    big = dict(rows=(200, 4), cols=(300, 4), ldx=(300, 4), ldo=(300, 4), ws=None)
+    for hp in (dict(lr=1e39), dict(lr=1e30, scale=1e9), dict(momentum=1e39), dict(lr=1e20, decay=1e20),
+               dict(lr=3e37)):   # times sqrt(32000 / 140) = 15.1
+        assert _ortho(lib, step=True, hp=hp, **(big | dict(rows=(32000, 4), cols=(140, 4)))) == A
+    assert _ortho(lib, step=True, hp=dict(lr=1e36), **big) == W   # (the next check)
