@@ -372,6 +372,10 @@ def orthogonalize(x, out=None, steps: int = 5, coefficients=None, eps: float = 1
     float32) or KFAC_ORTHO_HALF (for bfloat16).  coefficients: (a, b, c) of x -> a x + b x^3 + c x^5
     for every step, or one triple per step."""
     what = "orthogonalize"
+    if not isinstance(x, torch.Tensor):
+        x = list(x)   # (an iterator gives its tensors once)
+    if out is not None and not isinstance(out, torch.Tensor):
+        out = list(out)
     m = _Matrices(what, "x", x)
     if out is None:
         one = isinstance(x, torch.Tensor)

@@ -301,3 +301,13 @@ def test_full_arithmetic_keeps_products_symmetric(s, cols):
         for part in parts:
             part = part[:, :small]
             assert part.abs().max() > 0 and torch.equal(part, part.t())
+
+
+def test_matrices_from_an_iterator():
+    xs = [_gradient(i, 30 + i, 40) for i in range(3)]
+    want = K.orthogonalize(xs)
+    got = K.orthogonalize(x for x in xs)
+    assert len(got) == 3 and all(torch.equal(a, b) for a, b in zip(got, want))
+    out = [torch.empty_like(x) for x in xs]
+    got = K.orthogonalize(iter(xs), out=iter(out))
+    assert len(got) == 3 and all(a is b and torch.equal(a, c) for a, b, c in zip(got, out, want))
