@@ -270,6 +270,8 @@ def embedding_backward(ids, dout, rows: int, scale: float = 1.0, padding_id: int
     bits = _ids(what, ids, dev)
     if dout.dim() < 1 or dout.shape[:-1] != ids.shape:
         raise ValueError(f"{what}: dout is [..., width] for ids [...], not {tuple(dout.shape)}")
+    if not -2**63 <= padding_id < 2**63:   # (ctypes would wrap it)
+        raise ValueError(f"{what}: padding_id is an id, or -1 for none, not {padding_id}")
     width, tokens = dout.shape[-1], ids.numel()
     ldo = _ld(what, "dout", dout, dout.shape, dout.dtype, dev)
     if out is None:

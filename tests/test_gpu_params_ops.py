@@ -381,3 +381,12 @@ def test_embedding_workspace_kept_for_the_largest_batch(tokens):
         want = torch.zeros(rows, width, device="cuda", dtype=torch.float64).index_add_(0, ids[:n], dout[:n].double())
         size = torch.zeros(rows, width, device="cuda", dtype=torch.float64).index_add_(0, ids[:n], dout[:n].double().abs())
         assert ((got - want).abs() <= 12 * 2.0 ** -24 * size).all(), n
+
+
+def test_padding_ids_no_c_type_holds_are_refused():
+    ids, dout = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.zeros(3, 8, device="cuda")
+    for padding in (2**64 - 1, 2**64 + 5):    # not -1, not 5
+        with pytest.raises(ValueError, match="padding_id"):
+            K.embedding_backward(ids, dout, 9, padding_id=padding)
+    with pytest.raises(K.KfacError, match="INVALID_ARG"):
+        K.embedding_backward(ids, dout, 9, padding_id=-2)
