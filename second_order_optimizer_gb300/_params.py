@@ -173,10 +173,8 @@ def rms_norm_e4m3(x, gain=None, residual=None, eps: float = 1e-6, group: int = 0
 
 def rms_norm_workspace(x):
     """A workspace tensor for rms_norm_backward of tensors like x, to be kept and passed to it."""
-    dev = _device(x, "rms_norm_workspace")
-    cols = x.shape[-1]
-    return _kept(_sized(LIB.kfac_rms_norm_workspace_size, "kfac_rms_norm_workspace_size", dev,
-                        x.numel() // cols if cols else 0, cols), dev)
+    _, dev, _, rows, cols = _channels("rms_norm_workspace", "x", x)
+    return _kept(_sized(LIB.kfac_rms_norm_workspace_size, "kfac_rms_norm_workspace_size", dev, rows, cols), dev)
 
 
 def rms_norm_backward(dout, x, gain, rstd, dresidual=None, dx=None, dgain=None, dgain_square=None,

@@ -390,3 +390,8 @@ def test_padding_ids_no_c_type_holds_are_refused():
             K.embedding_backward(ids, dout, 9, padding_id=padding)
     with pytest.raises(K.KfacError, match="INVALID_ARG"):
         K.embedding_backward(ids, dout, 9, padding_id=-2)
+
+
+def test_norm_workspace_of_a_scalar_is_refused():
+    with pytest.raises(ValueError, match="channels"):
+        K.rms_norm_workspace(torch.zeros((), device="cuda"))
