@@ -277,32 +277,6 @@ def test_sides_that_no_int_holds_are_refused():
         K.orthogonal_step(x, x, x, lr=0.1)
 
 
-def _halves(work, at, rows, pitch):
-    """The [hi, lo] parts of a matrix that a call left at this offset of its workspace."""
-    n = rows * pitch * 2
-    each = -(-n // 256) * 256
-    return [work[at + k * each:at + k * each + n].view(torch.float16).view(rows, pitch) for k in (0, 1)], 2 * each
-
-
-@pytest.mark.parametrize("s,cols", [(200, 300), (384, 384), (2304, 2400), (2400, 2304)])
-def test_full_arithmetic_keeps_products_symmetric(s, cols):
-    """L = X X^T and M = a I + b L + c L L are symmetric to the last bit: one step leaves X, L and M in
-    that order in the workspace (of tall matrices too; blocks of 128 on the diagonal, by themselves and
-    in tiles of 256)."""
-    rows, small = s, min(s, cols)
-    x = _gradient(s, rows, cols)
-    work = torch.zeros_like(K.orthogonalize_workspace(x))
-    K.orthogonalize(x, steps=1, workspace=work)
-    up = lambda n: -(-n // 64) * 64
-    at = _halves(work, 0, rows, up(cols))[1]
-    for _ in range(2):
-        parts, nbytes = _halves(work, at, small, up(small))
-        at += nbytes
-        for part in parts:
-            part = part[:, :small]
-            assert part.abs().max() > 0 and torch.equal(part, part.t())
-
-
 def test_matrices_from_an_iterator():
     xs = [_gradient(i, 30 + i, 40) for i in range(3)]
     want = K.orthogonalize(xs)
