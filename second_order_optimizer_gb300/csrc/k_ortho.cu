@@ -246,28 +246,27 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const __grid_c
 }
 
 // From the squares by range (big, plain, small): 2^k (in two factors, each within fp32's range)
-// with |x 2^k|_F in [2^13, 2^14), and r and j with x / (|x| + eps) = r 2^-j x 2^k, where 2^-j is just
-// above |x| / (|x| + eps).  (j is 0 unless |x| < eps.  Then all of X is that small, and is kept times a
-// power of two through the steps, see Plan: scaled as if |X| were 1 it would fall out of fp16's range.  Of
-// 256 x 512 in full arithmetic, |x| = 1e-13 and eps = 1e-7 were 4.7e-4 off, 1e-15 4.7e-2.)
+// with |x 2^k|_F in [2^13, 2^14), and r and j with x / (|x| + eps) = r 2^-j x 2^k, where 2^-j is the power
+// of two from |x| / (|x| + eps) up.  (j is 0 unless |x| < eps.  Then all of X is that small, and is kept
+// times a power of two through the steps, see Plan: scaled as if |X| were 1 it would fall out of fp16's
+// range.  Of 256 x 512 in full arithmetic, |x| = 1e-13 and eps = 1e-7 were 4.7e-4 off, 1e-15 4.7e-2.)
 __device__ __forceinline__ void scale_factors(const double (&sums)[3], double eps, float (&up)[2], float* r_out,
                                               float* j_out) {
   const double x = sqrt(sums[0] * 0x1p168 + sums[1] + sums[2] * 0x1p-176), norm = x + eps;
   float r = 0.f;
   int k = 0, j = 0;
   if (x > 0.0 && isfinite(norm)) {
-    int e = 0;
-    frexp(x, &e);                            // x < 2^e
-    k = 14 - e;
-    frexp(x / norm, &e);
-    j = max(0, -e);
-    r = (float)ldexp(1.0 / norm, j - k);
+    // by the bits of the doubles (both normal): 64-bit functions are slow, and all wait for this thread
+    const long long xb = __double_as_longlong(x), nb = __double_as_longlong(norm);
+    k = 14 - ((int)(xb >> 52) - 1022);       // x < 2^(14 - k)
+    j = (int)((nb - xb) >> 52);              // x / norm <= 2^-j < 2 x / norm
+    r = (float)(__longlong_as_double((long long)(1023 + j - k) << 52) / norm);
   } else if (x != 0.0) {                     // Inf and NaN reach everything through r
     r = __int_as_float(0x7fffffff);
   }
   const int k0 = min(max(k, -126), 126);
-  up[0] = ldexpf(1.f, k0);
-  up[1] = ldexpf(1.f, k - k0);
+  up[0] = __int_as_float((127 + k0) << 23);
+  up[1] = __int_as_float((127 + k - k0) << 23);
   *r_out = r;
   *j_out = (float)j;
 }

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     }
   };
   float up0, up1;
+  bool far;             // below eps: j > 0
   {
     Squares sq;
     visit_by(std::true_type(), [&](int row, int c, auto& u) {
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     __syncthreads();
     up0 = factors[0];
     up1 = factors[1];
+    far = factors[3] > 0.f;
   }
   auto halves_of = [&](float x, uint16_t& hi, uint16_t& lo) {
     const float v = x * up0 * up1;
@@ -328,9 +330,10 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(const __g
     }, step == g.give_up && rank == 0);
     // X is kept times 2^max(0, j + shift): see Plan (factors: r, j)
     auto scaled = [&](float by, int power, int shift_out) {
-      const int j = (int)factors[3];
       if (step == 0) by *= power == 2 ? factors[2] * factors[2] : factors[2];
-      return j > 0 ? ldexpf(by, max(0, j + shift_out) - power * max(0, j + p.shift_in)) : by;
+      if (!far) return by;
+      const int j = (int)factors[3];
+      return ldexpf(by, max(0, j + shift_out) - power * max(0, j + p.shift_in));
     };
     const float gram = scaled(p.gram, 2, kNoShift);
     float v[32];
