@@ -1067,7 +1067,13 @@ kfac_status make_plan(const kfac_ortho_desc* d, Plan* p) {
   return KFAC_OK;
 }
 
-// Steps are grouped where X is long enough for that to pay.
+// Steps are grouped where X is long enough for that to pay: by operations from l > s on, measured later,
+// since two launches more and products with fewer tiles come with it.  Single steps and groups, us, one
+// matrix and eight, bf16: 1024 x 1536 158 and 186, 406 and 448; 1024 x 2048 170 and 191, 462 and 467;
+// 2048 x 2560 301 and 313, 1274 and 1303; 2048 x 4096 336 and 329, 1744 and 1572; 4096 x 5120 1142 and
+// 1134; 4096 x 8192 1564 and 1348.  Full arithmetic: 1024 x 2048 322 and 357, 2048 x 4096 792 and 718,
+// 4096 x 8192 4816 and 3944.  So the border would better be near l = s + 1500 (512 x 4096 too: 189 and
+// 174); up to there a matrix that this rule groups takes up to 18% longer.
 bool grouped(int s, int l) { return s >= 1024 && l >= s + s / 2; }
 
 enum { X_0, X_1, GRAM, TEMP, POLY, PROD_0, PROD_1, BUFFERS };
@@ -1153,7 +1159,8 @@ kfac_status check_sizes(const kfac_ortho_desc* d, int count, const int* rows, co
   return KFAC_OK;
 }
 
-// Matrices that a product launch takes: up to two tasks each.
+// Matrices that a product launch takes: up to two tasks each.  One more is a chain of launches by itself
+// (512 x 512 in bf16: 24 take 223 us, 25 take 333; full arithmetic: 12 take 256, 13 take 446).
 int per_launch(int halves) { return (halves == 2 ? Launch<true>::TASKS : Launch<false>::TASKS) / 2; }
 
 // Blocks of the small matrices' kernel for a matrix; 0: too large for it.
@@ -1214,8 +1221,11 @@ size_t lay_out(const kfac_ortho_desc* d, int count, const int* rows, const int* 
   size_t at = 0;
   const int halves = d->math == KFAC_ORTHO_FULL ? 2 : 1;
   // Small matrices have a kernel of their own, unless the others' launches have room for them: there
-  // they cost next to nothing (the MLP set's 10 x 1024 beside three of 1024 x 1024 in full
-  // arithmetic: 85 us by itself).
+  // they cost less, in the worst case the same.  Beside a large one, their own kernel and riding, us, bf16:
+  // one 10 x 1024 beside 1024 x 1024 199 and 145; ten of 128 x 512 beside 300 x 300 148 and 109, beside
+  // 4096 x 4096 997 and 987; ten of 128 x 4096 beside 1024 x 1024 236 and 235, beside 4096 x 4096 1042 and
+  // 988; 23 of 64 x 64 beside 300 x 300 121 and 102.  Full arithmetic: one 10 x 1024 361 and 269, ten of
+  // 128 x 1536 beside 1024 x 1024 387 and 336, eleven of 64 x 64 beside 300 x 300 197 and 164.
   int64_t small = 0, large = 0;
   for (int i = 0; i < count; ++i) {
     const int s = std::min(rows[i], cols[i]);
@@ -1279,7 +1289,11 @@ kfac_status launch_tiles(const Launch<kFull>& g, cudaStream_t st) {
   return check_launch();
 }
 // Numbers the tasks' tiles and launches them: pairs on 256 x 256 tiles, or, where these would be
-// fewer than half a tile per pair, single CTAs on 128 x 128 ones.
+// fewer than half a tile per pair, single CTAs on 128 x 128 ones.  All launches of one matrix on singles and
+// on pairs, us, bf16: 1024 x 1024 (10 tiles of 256 in L, 16 in X) 143 and 195; 1536 (21, 36) 183 and 233;
+// 2048 (36, 64) 265 and 282, and 242 by this rule, L on singles and X on pairs; 2304 (45, 81) 449 and 357;
+// 2560 (55, 100) 486 and 384.  Full arithmetic: 1536 353 and 525, 2048 544 and 649 (508 by the rule), 2304
+// 999 and 901, 2560 1092 and 989.
 template <int TO, typename T, bool kFull> kfac_status launch_product(Launch<kFull>& g, cudaStream_t st) {
   auto number = [&](int tile) {
     int64_t tiles = 0;
