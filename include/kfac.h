@@ -643,8 +643,8 @@ kfac_status kfac_embedding_workspace_size(int64_t tokens, int64_t rows, int64_t 
  * (fp32 [rows x width]), over the tokens whose id is not padding_id (-1: none is
  * padding); ids outside [0, rows) are left out.  accumulate = 0: every row is written,
  * zeros where no token is; 1: added to dtable, whose other rows are not touched.
- * frequency (fp32 [rows], NULL: not wanted, always written whole; width > 0 then): the share of the
- * tokens that dtable[v] sums, count / tokens.  It is the diagonal of the A factor of the
+ * frequency (fp32 [rows], NULL: not wanted, always written whole; width > 0 then): the
+ * share of the tokens that dtable[v] sums, count / tokens.  It is the diagonal of the A factor of the
  * one-hot inputs: a KFAC_DIAG layer of d_out = rows, d_in = width takes it as g_new, with
  * the mean squares of dout as a_new.  Sums are fp32 in a fixed order, no atomics: the
  * same inputs give the same bits. */
@@ -696,16 +696,16 @@ kfac_status kfac_orthogonalize_workspace_size(const kfac_ortho_desc* desc, int c
  *   X = x / (|x|_F + eps);  per step: L = X X^T, X <- (a I + b L + c L^2) X;  out = X
  * (L = X^T X and X <- X (...) where rows > cols).  A singular value t of X becomes a t +
  * b t^3 + c t^5, its singular vectors stay.  A matrix of zeros gives zeros; Inf or NaN
- * anywhere in x makes all of its out NaN.  Small matrices are as exact as others, down to
- * |x|_F of 2^-90 (|x|_F + eps).  x, out: [rows x cols], sides up to 32768 (else
+ * anywhere in x makes all of its out NaN.  Matrices far below eps are as exact as others,
+ * down to |x|_F of 2^-90 (|x|_F + eps).  x, out: [rows x cols], sides up to 32768 (else
  * KFAC_ERR_UNSUPPORTED); matrices without elements are passed over.  Host arrays of length
  * count.  out may be its own x with the same leading dimension; no out may be given twice
  * or be another's x, and other overlaps are not allowed.  All matrices go through each
  * product together, up to 24 at a time (full arithmetic: 12); small ones take all steps in
  * one launch, unless the others' launches have room for them (a matrix's last bits may
- * differ between the two).  The same call on the same inputs gives the same bits.  The coefficients have to keep
- * the bound of the singular values, and of a + b t + c t^2, between 2^-20 and 2^20 at
- * each step (else KFAC_ERR_INVALID_ARG). */
+ * differ between the two).  The same call on the same inputs gives the same bits.  The
+ * coefficients have to keep the bound of the singular values, and of a + b t + c t^2,
+ * between 2^-20 and 2^20 at each step (else KFAC_ERR_INVALID_ARG). */
 kfac_status kfac_orthogonalize(const kfac_ortho_desc* desc, int count, const int* rows,
                                const int* cols, const void* const* x, const int64_t* ldx,
                                void* const* out, const int64_t* ldo, void* workspace,

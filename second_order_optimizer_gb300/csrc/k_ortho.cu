@@ -333,9 +333,9 @@ struct Task {
   void* out;                    // TO_OUT: the direction; TO_WEIGHTS: the weights, fp32
   const __half *add_hi, *add_lo;   // or null
   __half *mirror_hi, *mirror_lo;   // upper: the result itself, whose other half is stored directly
-  float* r;                     // r, j behind it, and between them a word that is not 0 once a product of this matrix is lost: a wait
-                                // gave up, so its tile was not stored, and what the last launch makes of it is
-                                // NaN (weights: left as they were)
+  float* r;                     // r; a word that is not 0 once a product of this matrix is lost (a wait gave
+                                // up, its tile was not stored: the last launch makes the matrix NaN, or
+                                // leaves its weights); j
   float alpha, beta, diag;
   float keep, rate;             // TO_WEIGHTS: W <- keep W - rate X
   int rpow, xpow, shift_in, shift_out, add_pitch, mirror_pitch;
@@ -940,10 +940,10 @@ __global__ void __launch_bounds__(Cfg<kFull, kPair>::THREADS, 1)
   tc::tc_fence_before();
   __syncwarp();
   block_sync();   // every MMA has completed; no peer arrival is pending
-  if (*abort_flag) {   // (of both CTAs) unless a role gave up, whichever and whenever:
-    // memory goes only after the copies have landed and the products have ended.  Both CTAs' complete
-    // on the even one's barriers; where one CTA has issued more copies than the other a barrier does
-    // not turn, and the limit outlasts them.
+  if (*abort_flag) {   // (both CTAs' are set)
+    // A role gave up, whichever and whenever: memory goes only after the copies have landed and the products
+    // have ended.  Both CTAs' complete on the even one's barriers; where one CTA has issued more copies
+    // than the other a barrier does not turn, and the limit outlasts them.
     volatile int never = 0;
     if (rank == 0 && threadIdx.x == 0) {
       const int issued = (int)(kPair ? max(*copies, ld_cluster_u32(tc::mapa(copies, 1))) : *copies);
